@@ -204,7 +204,11 @@ def prepare(case, seed):
             if c["op"] == "norm":
                 s["out"] = [torch.empty(o, dtype=BF16, device="cuda") for o in out]
             else:
-                s["out"] = [torch.empty(B, N, h, D, dtype=BF16, device="cuda") for h in (Hq, Hkv)] + [torch.empty(D, device="cuda") for _ in range(2)]
+                # the gradients lie as the inputs do: in one buffer where q and k are views of one
+                x = torch.empty(B, N, (Hq + 2 * Hkv) * D, dtype=BF16, device="cuda") if c["fused"] else None
+                s["out"] = [x[..., : Hq * D].view(B, N, Hq, D), x[..., Hq * D: (Hq + Hkv) * D].view(B, N, Hkv, D)] if c["fused"] else \
+                    [torch.empty(B, N, h, D, dtype=BF16, device="cuda") for h in (Hq, Hkv)]
+                s["out"] += [torch.empty(D, device="cuda") for _ in range(2)]
                 s["ws"] = mcs.empty_workspace(mcs.mcs_qk_norm_rope_backward_workspace(s["p"]))
         return s
     B, page = c["B"], c["page"]
