@@ -36,6 +36,9 @@
  *    creates and destroys (mcs_stager_*: a few CUDA events each) it holds no
  *    state between calls.
  *  - Supported: D in {64, 128}, C in {64, 128}, 1 <= K <= N, B*H <= 65535.
+ *  - The paged entry points (mcs_paged_*) and mcs_qk_norm_rope have parameter
+ *    structs, layouts and limits of their own, stated where they stand; the
+ *    rest of these conventions holds for them too.
  */
 #ifndef MCS_H_
 #define MCS_H_
@@ -407,6 +410,188 @@ mcs_status mcs_gather_mass(const mcs_params* p, const float* mass, int rows, con
  */
 mcs_status mcs_rel_l1(const mcs_params* p, const void* got, const void* want, const int32_t* rows,
                       int nrows, double* sums, cudaStream_t stream);
+
+/*
+ * Paged key-value cache: generation one token per sequence at a time.  No
+ * counterpart in the paper, whose method works on whole sequences; these entry
+ * points carry its pieces (attention, selection by a score, attention over
+ * the selected tokens, the E4M3 cache) to a cache that grows token by token.
+ *
+ *   k_cache, v_cache [num_pages, Hkv, page, D]  bf16, or E4M3 bytes standing
+ *                                               for k_scale * k8, v_scale * v8
+ *   k_mean           [num_pages, Hkv, D] bf16   mean of the page's keys
+ *   block_table      [B, max_pages] int32       page of each logical page of a
+ *                                               sequence; entries past its
+ *                                               last page are never read
+ *   lens             [B] int32                  tokens of each sequence in the
+ *                                               cache
+ * Query head h reads KV head h / (Hq / Hkv).  Token t of sequence b is row
+ * t % page of page block_table[b, t / page]; its slot is that page * page +
+ * t % page.  Rows of a page that hold no token may hold anything, NaN among
+ * it: they do not reach any result.  A page number outside [0, num_pages), a
+ * length that is negative or above max_pages * page, or a slot past the cache
+ * sets MCS_ERR_BOUNDS in the device status; what it names is skipped and
+ * nothing is read or written through it.
+ *
+ * Supported: D in {64, 128}, page in {16, 32, 64, 128}, Hq a multiple of Hkv,
+ * B <= 4096, B * Hq <= 2^20, num_pages * Hkv * page and max_pages * page below
+ * 2^31 (byte offsets are 64-bit).  Tensors are 16-byte aligned.
+ */
+typedef struct {
+  int B, Hq, Hkv, D;  /* sequences, query heads, KV heads, head dim */
+  int page;           /* tokens per page */
+  int num_pages;      /* pages of the cache */
+  int max_pages;      /* entries per row of block_table */
+  int kv;             /* MCS_KV_BF16 (0) or MCS_KV_E4M3 (1) */
+  float scale;        /* softmax scale; 0 selects 1/sqrt(D) */
+  float k_scale, v_scale; /* E4M3: scales of the two caches, > 0; ignored for bf16 */
+  int q_stride;       /* elements between the rows of consecutive tokens of q; 0: Hq * D */
+  int kv_stride;      /* the same of k and v given to mcs_paged_write; 0: Hkv * D */
+} mcs_paged;
+
+/* Element type of k_cache and v_cache. */
+enum { MCS_KV_BF16 = 0, MCS_KV_E4M3 = 1 };
+
+/*
+ * Pages and slots of a step's new tokens, from the lengths alone, without a
+ * visit to the host.  Sequence b holds lens[b] tokens and gets new_lens[b]
+ * (>= 0).  The pages that are missing come from free_pages [n_free] from
+ * position free_head[0] on, sequence by sequence, and enter block_table behind
+ * the pages the sequence has; lens_out[b] = lens[b] + new_lens[b]; head_out[0]
+ * = free_head[0] + the pages taken; cu_new [B+1] = exclusive sums of new_lens.
+ * The new tokens, sequence after sequence, are rows t < cu_new[B] of this
+ * step's tensors: slots[t] and positions[t] (nullable) receive the token's slot
+ * and its position in its sequence, and rows [cu_new[B], T) get -1.
+ * lens_out may be lens and head_out may be free_head (then each call advances
+ * the state); other outputs must not overlap inputs.  A request that cannot be
+ * met (more than T new tokens, more than n_free - free_head[0] missing pages, a
+ * sequence past max_pages * page, a negative length, a page outside the
+ * cache) sets MCS_ERR_BOUNDS in the device status and takes nothing: lens_out =
+ * lens, head_out = free_head, block_table stays, cu_new is 0, and slots and
+ * positions are -1.  T, n_free >= 0.
+ */
+mcs_status mcs_paged_plan(const mcs_paged* p, const int32_t* new_lens, const int32_t* lens,
+                          const int32_t* free_pages, int n_free, const int32_t* free_head,
+                          int32_t* block_table, int32_t* lens_out, int32_t* head_out,
+                          int32_t* cu_new, int32_t* slots, int32_t* positions, int T,
+                          cudaStream_t stream);
+
+/*
+ * Writes the rows k[t], v[t] [T, Hkv, D] bf16 of T new tokens to slots[t] of
+ * the two caches; a token whose slot is negative is skipped.  E4M3: each value
+ * as mcs_quantize_e4m3 rounds it.  k_mean (nullable): every page that gets a
+ * token receives the mean of the keys it holds after the call, the stored
+ * values of rows 0 .. its last new row, summed in fp32 and rounded once; the
+ * rows in front of the first new one are read from the cache.  The slots of
+ * one call are distinct, and the tokens of one page stand one behind another
+ * in ascending order, as mcs_paged_plan lays them out.
+ */
+mcs_status mcs_paged_write(const mcs_paged* p, int T, const void* k, const void* v,
+                           const int32_t* slots, void* k_cache, void* v_cache, void* k_mean,
+                           cudaStream_t stream);
+
+/*
+ * Attention of one token per sequence over its cache: out[b, h] = softmax(scale
+ * * q[b, h] . k) v over the lens[b] tokens of sequence b, q [B, Hq, D] (rows
+ * q_stride apart), out [B, Hq, D] bf16; lse [B, Hq] fp32 (natural log,
+ * nullable).  lens counts the new token itself, once mcs_paged_write has stored
+ * it.  A sequence of no tokens gets zeros, and -inf as its lse.
+ * E4M3: q is converted to f16 as in mcs_sparse_attn_e4m3.
+ * ws: at least mcs_paged_decode_workspace(p) bytes, used until the call's work
+ * on the stream is done; its contents do not matter.  Calls that may overlap
+ * on the GPU need one each.  mcs_paged_decode_workspace returns 0 for
+ * unsupported params.
+ */
+size_t mcs_paged_decode_workspace(const mcs_paged* p);
+mcs_status mcs_paged_decode(const mcs_paged* p, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* block_table, const int32_t* lens,
+                            void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The pages each token attends to, by a cheap score (the one-token form of
+ * mcs_pooled_block_select: the query heads that share a KV head are the
+ * group).  For sequence b, KV head h and each of the n = ceil(lens[b] / page)
+ * pages: score = (sum of the group's queries) . k_mean, summed without visible
+ * rounding and rounded to fp32 once.  Keeps the first `sink` pages, the last
+ * `recent` pages and the best others, `select` in all (ties to the lower page;
+ * every page when n <= select).  sel [B, Hkv, select]: logical page numbers,
+ * ascending, -1 behind them.  1 <= select, sink + recent <= select, sink and
+ * recent >= 0.  ws: at least mcs_paged_select_workspace(p) bytes, as above.
+ */
+size_t mcs_paged_select_workspace(const mcs_paged* p);
+mcs_status mcs_paged_select(const mcs_paged* p, const void* q, const void* k_mean,
+                            const int32_t* block_table, const int32_t* lens, int select, int sink,
+                            int recent, int32_t* sel, void* ws, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/*
+ * mcs_paged_decode over the pages sel [B, Hkv, select] alone (the softmax is
+ * renormalised over their tokens).  The first min(select, n) entries of a row
+ * are read; -1 entries are skipped, and an entry outside [-1, n) sets
+ * MCS_ERR_BOUNDS and is skipped.  A page listed twice counts twice.  A row of
+ * nothing gives zeros and -inf.
+ */
+mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_table,
+                                   const int32_t* lens, const int32_t* sel, int select, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * What stands between a block's projections and its attention: RMS norm of
+ * each head of q and k, then the rotation of its first `rot` values by the
+ * token's angles, in one pass (for mcs_group, mcs_dense_attn and the sparse
+ * entry points in either layout, or for mcs_paged_write and mcs_paged_decode).
+ *   r = 1 / sqrt(mean(x^2) + eps), y = x r w,
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for the pairs (a, b) = (2i, 2i + 1) when interleaved, (i, i + rot/2)
+ * otherwise, i < rot/2; all in fp32, rounded to bf16 once.
+ * q [B, N, Hq, D], k [B, N, Hkv, D] bf16, tokens q_stride / k_stride elements
+ * apart (views into a fused projection); wq, wk [D] fp32 (nullable: ones);
+ * cos_table, sin_table [table_rows, rot/2] fp32; positions [B, N] int32
+ * (nullable: position n; then N <= table_rows).  A token whose position is
+ * negative is padding: its rows of the outputs stay as they were.  A position
+ * >= table_rows sets MCS_ERR_BOUNDS in the device status and is treated the
+ * same.  q_out, k_out: contiguous, [B, H, N, D] or [B, N, H, D] by layout;
+ * in place is possible where the layouts are equal (MCS_LAYOUT_BNHD, stride 0
+ * or H * D).  Hkv = 0: no k (its pointers are ignored).
+ * Supported: D in {64, 128}, rot a multiple of 16 in [0, D], strides multiples
+ * of 8, B * N * (Hq + Hkv) below 2^31.
+ */
+typedef struct {
+  int B, N, Hq, Hkv, D;
+  int rot;            /* rotated values per head; 0: norm alone (the tables are ignored) */
+  int interleaved;    /* pairs (2i, 2i+1) when 1, (i, i + rot/2) when 0 */
+  int table_rows;     /* positions the tables hold */
+  int layout;         /* of q_out and k_out: MCS_LAYOUT_BHND or MCS_LAYOUT_BNHD */
+  float eps;          /* >= 0 */
+  int q_stride, k_stride; /* elements between consecutive tokens; 0: Hq * D, Hkv * D */
+} mcs_rope;
+
+mcs_status mcs_qk_norm_rope(const mcs_rope* p, const void* q, const void* k, const float* wq,
+                            const float* wk, const float* cos_table, const float* sin_table,
+                            const int32_t* positions, void* q_out, void* k_out,
+                            cudaStream_t stream);
+
+/*
+ * Its gradients: from dq_out, dk_out (shape and layout of q_out, k_out) and the
+ * forward pass's inputs, dq [B, N, Hq, D], dk [B, N, Hkv, D] (bf16, tokens
+ * q_stride / k_stride apart like q and k) and dwq, dwk [D] fp32 (both nullable;
+ * overwritten).  With g = dq_out rotated back and xh = x r:
+ *   dw = sum over tokens and heads of g xh,
+ *   dx = r (w g - xh mean(w g xh)).
+ * Padding tokens (see above) add nothing, and their rows of dq, dk stay as
+ * they were.  dq may be dq_out where the layouts are equal.  The sums are taken
+ * in an order that does not change from call to call.
+ * ws: at least mcs_qk_norm_rope_backward_workspace(p) bytes, used until the
+ * call's work on the stream is done.
+ */
+size_t mcs_qk_norm_rope_backward_workspace(const mcs_rope* p);
+mcs_status mcs_qk_norm_rope_backward(const mcs_rope* p, const void* dq_out, const void* dk_out,
+                                     const void* q, const void* k, const float* wq,
+                                     const float* wk, const float* cos_table,
+                                     const float* sin_table, const int32_t* positions, void* dq,
+                                     void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream);
 
 #ifdef __cplusplus
 }

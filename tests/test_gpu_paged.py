@@ -1,0 +1,610 @@
+"""GPU parity of the paged-cache entry points against the fp64 oracle.
+
+Tolerances, taken before the first run (u = 2^-24, half a step of fp32):
+
+* attention output: rounding to bf16 is off by at most 2^-8 |out|.  A score is
+  a sum of D products in fp32, off by at most delta = (D + 8) u S with S the
+  largest sum of |q k| scale of the row, and its exponential by 2 delta and
+  2^-21 (the hardware's base-2 exponential and the argument's rounding); both
+  change the weights, so the output by at most that times A = sum p |v|,
+  numerator and denominator.  The weights enter the second product as two bf16
+  parts (off by 2^-16) or one f16 (2^-11), again times A; sums of the products
+  add (number of keys) u A.
+* lse: delta + 2^-20 + 2^-23 |lse| + (number of keys) u.
+* page means: 2^-8 |mean| for bf16, and (page + 2) u times the mean of |k|.
+* codes, copied rows, slots, tables and selections: equal.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import mcs_oracle as orc
+from oracle import paged_oracle as po
+from token_sparse_attention_gb300 import build as mcs_build
+from token_sparse_attention_gb300 import mcs
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+KS, VS = 3 / 256, 45 / 4096
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    mcs_build.build()
+    mcs.lib()
+    assert torch.cuda.is_available()
+    yield
+    assert mcs.mcs_device_status() == 0
+
+
+def _i32(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+
+def _f64(t):
+    if t.dtype == torch.uint8:
+        return orc.e4m3_decode(t.cpu().numpy()).astype(np.float64)
+    return t.cpu().double().numpy()
+
+
+class Cache:
+    """A paged cache of given lengths; rows without a token, spare pages and table entries
+    past a sequence's end hold NaN or numbers outside the cache."""
+
+    def __init__(self, lens, Hq, Hkv, D, page, e4m3=False, seed=0, level=0.8, extra=2, scale=0.0,
+                 q_stride=0, q_size=1.0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = np.random.default_rng(seed)
+        B, n = len(lens), [-(-x // page) for x in lens]
+        total, P = sum(n) + 3, max(n) + extra
+        self.lens, self.page, self.B, self.D, self.e4m3 = lens, page, B, D, e4m3
+        self.table = np.full((B, P), 2 ** 31 - 1)
+        order, at = r.permutation(total), 0
+        shape = (total, Hkv, page, D)
+        rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+        k = level * rand(total, Hkv, 1, D) + 0.7 * rand(*shape)
+        v = rand(*shape)
+        hole = torch.ones(total, page, dtype=torch.bool, device="cuda")
+        for b in range(B):
+            for j in range(n[b]):
+                self.table[b, j] = order[at]
+                hole[order[at], :min(page, lens[b] - j * page)] = False
+                at += 1
+        self.scales = (KS, VS) if e4m3 else (1.0, 1.0)
+        if e4m3:
+            enc = lambda x, s: (x / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            k, v, nan = enc(k, KS), enc(v, VS), 0x7F
+        else:
+            k, v, nan = k.to(torch.bfloat16), v.to(torch.bfloat16), float("nan")
+        self.k, self.v = (x.masked_fill(hole[:, None, :, None], nan) for x in (k, v))
+        rows = rand(B, q_stride or Hq * D).to(torch.bfloat16) * q_size
+        self.q = rows[:, :Hq * D].view(B, Hq, D)
+        self.p = mcs.paged(B, Hq, Hkv, D, page, total, P, kv=int(e4m3), scale=scale,
+                           k_scale=self.scales[0], v_scale=self.scales[1], q_stride=q_stride)
+        self.scale = scale or D ** -0.5
+        self.dtable, self.dlens = _i32(self.table), _i32(lens)
+        self.ws = mcs.empty_workspace(mcs.mcs_paged_decode_workspace(self.p))
+
+    def means(self):
+        """bf16 means of the tokens in each page, NaN where there are none."""
+        k = torch.from_numpy(_f64(self.k)) * self.scales[0]
+        return torch.nanmean(k, 2).to(torch.bfloat16).cuda()
+
+    def run(self, sel=None, lse=True, stream=None):
+        # everything is written over, and one row behind the last sequence stays
+        B, Hq, D = self.q.shape
+        out = torch.full((B + 1, Hq, D), 77.0, dtype=torch.bfloat16, device="cuda")
+        ls = torch.full((B + 1, Hq), 77.0, device="cuda")
+        a = (self.dtable, self.dlens) if sel is None else (self.dtable, self.dlens, sel)
+        f = mcs.mcs_paged_decode if sel is None else mcs.mcs_paged_decode_sparse
+        f(self.p, self.q, self.k, self.v, *a, out[:B], self.ws, lse=ls[:B] if lse else None,
+          stream=stream)
+        return out, ls
+
+    def check(self, out, ls, sel=None):
+        B, Hq, D = self.q.shape
+        k, v = (_f64(x) * s for x, s in zip((self.k, self.v), self.scales))
+        q = self.q
+        want, lse, absv, size = po.decode(_f64(q), k, v, self.table, self.lens, self.scale, sel)
+        assert (_f64(out[B]) == 77).all() and (_f64(ls[B]) == 77).all()
+        out, ls = _f64(out[:B]), _f64(ls[:B])
+        n = max(self.lens)
+        delta = (D + 8) * U * size
+        tol = 2.0 ** -8 * np.abs(want) + absv * (
+            2 * (2 * delta + 2.0 ** -21) + (2.0 ** -11 if self.e4m3 else 2.0 ** -16) + n * U)[..., None]
+        bad = ~(np.abs(out - want) <= tol)
+        assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5], want[bad][:5])
+        live = np.isfinite(lse)
+        assert (ls[~live] == -np.inf).all()
+        off = np.abs(ls[live] - lse[live])
+        assert (off <= (delta + 2.0 ** -20 + n * U)[live] + 2.0 ** -23 * np.abs(lse[live])).all(), off.max()
+
+
+SHAPES = [  # lens, Hq, Hkv, D, page
+    ([1], 1, 1, 128, 16), ([1], 8, 1, 64, 128), ([16], 4, 4, 128, 16), ([17], 16, 2, 128, 16),
+    ([0, 1, 15, 16, 33], 8, 2, 128, 16), ([129, 128, 0, 127], 5, 1, 64, 64),
+    ([700, 3, 64], 20, 1, 128, 64), ([255, 1000], 34, 2, 64, 32), ([0, 0], 4, 2, 128, 128),
+    ([513, 31, 2, 0, 260, 77, 1, 128], 6, 3, 128, 128), ([3001], 32, 8, 128, 16),
+    ([1501, 40], 16, 16, 64, 32), ([2100], 40, 40, 128, 32)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page", SHAPES)
+def test_decode_matches_oracle(lens, Hq, Hkv, D, page, e4m3):
+    c = Cache(lens, Hq, Hkv, D, page, e4m3, seed=sum(lens) + Hq)
+    c.check(*c.run())
+    assert mcs.mcs_device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_decode_strided_queries_own_scale_and_peaks(e4m3):
+    # q inside a fused projection; scores spread over about +-100, so that the running
+    # maximum moves and most weights vanish
+    c = Cache([400, 33, 0, 90], 8, 2, 128, 16, e4m3, seed=5, scale=0.25, q_stride=12 * 128, q_size=8.0)
+    c.check(*c.run())
+    # without lse
+    out, ls = c.run(lse=False)
+    assert torch.equal(out, c.run()[0]) and (ls == 77).all()
+
+
+def test_decode_many_sequences_and_long_ones():
+    c = Cache([int(x) for x in np.random.default_rng(0).integers(0, 90, 300)], 4, 2, 64, 16, seed=8)
+    c.check(*c.run())
+    c = Cache([20011, 5], 4, 1, 128, 64, seed=9)
+    c.check(*c.run())
+
+
+def _sel(c, select, seed, holes=False):
+    r = np.random.default_rng(seed)
+    Hkv = c.k.shape[1]
+    sel = np.full((c.B, Hkv, select), -1)
+    for b, x in enumerate(c.lens):
+        n = -(-x // c.page)
+        for h in range(Hkv):
+            kept = np.sort(r.permutation(n)[:min(n, select)])
+            sel[b, h, :len(kept)] = kept
+            if holes and len(kept) > 1:
+                sel[b, h, r.integers(0, len(kept))] = -1
+    return sel
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,select", [
+    ([1], 1, 1, 128, 16, 1), ([100, 0, 17], 8, 2, 128, 16, 3), ([1000, 33], 20, 1, 64, 32, 7),
+    ([700, 64, 1], 16, 4, 128, 64, 5), ([3000, 2999], 8, 8, 128, 16, 40), ([500], 6, 2, 64, 128, 9)])
+def test_sparse_decode_matches_oracle(lens, Hq, Hkv, D, page, select, e4m3):
+    c = Cache(lens, Hq, Hkv, D, page, e4m3, seed=select)
+    for holes in (False, True):
+        sel = _sel(c, select, select, holes)
+        c.check(*c.run(_i32(sel)), sel)
+    # every page listed: the dense result up to summation order
+    if select >= max(-(-x // page) for x in lens):
+        c.check(*c.run(_i32(_sel(c, select, 0))))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,select,sink,recent", [
+    ([1], 1, 1, 128, 16, 1, 0, 0), ([100, 0, 17, 16], 8, 2, 128, 16, 3, 1, 1),
+    ([4000, 33], 20, 1, 64, 16, 100, 0, 2), ([2500, 64], 16, 4, 128, 32, 2, 2, 0),
+    ([900, 800, 5], 32, 2, 64, 16, 30, 0, 0), ([20000], 2, 1, 128, 16, 333, 1, 3)])
+def test_select_matches_oracle(lens, Hq, Hkv, D, page, select, sink, recent):
+    c = Cache(lens, Hq, Hkv, D, page, seed=select)
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(c.p))
+    mean = c.means()
+    sel = torch.full((c.B, Hkv, select), -7, dtype=torch.int32, device="cuda")
+    mcs.mcs_paged_select(c.p, c.q, mean, c.dtable, c.dlens, sel, ws, sink=sink, recent=recent)
+    want = po.select(_f64(c.q), _f64(mean), c.table, lens, page, select, sink, recent)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n,select", [(5000, 1), (5000, 1234), (37, 36), (1025, 1024)])
+def test_select_ties_go_to_the_lower_page(n, select):
+    # three distinct scores, -0 among them, and whole rows of equal ones
+    r = np.random.default_rng(n)
+    page, D = 16, 64
+    p = mcs.paged(2, 2, 1, D, page, n, n)
+    mean = np.zeros((n, 1, D))
+    mean[:, 0, 0] = r.integers(-1, 2, n)
+    mean[::7, 0, 0] = -0.0
+    table = np.stack([r.permutation(n), np.arange(n)])
+    q = np.zeros((2, 2, D))
+    q[0, :, 0] = 0.5
+    lens = [n * page - 3, n * page]
+    md, qd = (torch.from_numpy(x).cuda().to(torch.bfloat16) for x in (mean, q))
+    sel = torch.empty(2, 1, select, dtype=torch.int32, device="cuda")
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(p))
+    mcs.mcs_paged_select(p, qd, md, _i32(table), _i32(lens), sel, ws, sink=0, recent=0)
+    want = po.select(q, mean, table, lens, page, select, 0, 0)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
+def test_select_near_ties_follow_the_exact_sum():
+    # scores that cancel: large parts of both signs leave differences at fp32's last bits
+    r = np.random.default_rng(4)
+    n, page, D, select = 600, 16, 128, 77
+    p = mcs.paged(1, 4, 1, D, page, n, n)
+    mean = np.zeros((n, 1, D))
+    mean[:, 0, :63] = r.standard_normal((n, 63)) * 1000
+    mean[:, 0, 64:127] = -mean[:, 0, :63]
+    mean[:, 0, 127] = r.standard_normal(n) * 0.01
+    md = torch.from_numpy(mean).cuda().to(torch.bfloat16)
+    qd = torch.ones(1, 4, D, device="cuda", dtype=torch.bfloat16)
+    qd[:, 1] = 2.0 ** -9
+    sel = torch.empty(1, 1, select, dtype=torch.int32, device="cuda")
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(p))
+    table = r.permutation(n)[None]
+    mcs.mcs_paged_select(p, qd, md, _i32(table), _i32([n * page]), sel, ws, sink=0, recent=0)
+    want = po.select(_f64(qd), _f64(md), table, [n * page], page, select, 0, 0)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ plan and write
+
+def _plan(p, new, lens, free, head, table, T, in_place=False):
+    d = dict(lens=_i32(lens), head=_i32([head]), table=_i32(table))
+    lo, ho = (d["lens"], d["head"]) if in_place else (_i32(lens) * 0 - 9, _i32([0]))
+    cu = torch.full((p.B + 1,), -9, dtype=torch.int32, device="cuda")
+    slots, pos = (torch.full((T,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    mcs.mcs_paged_plan(p, _i32(new), d["lens"], _i32(free), d["head"], d["table"], lo, ho, cu, slots, pos)
+    return [x.cpu().numpy() for x in (lo, ho, d["table"], cu, slots, pos)]
+
+
+@pytest.mark.parametrize("B,page,most,T_over,in_place", [
+    (1, 16, 1, 0, False), (3, 16, 40, 5, True), (7, 64, 500, 0, False), (1500, 16, 9, 100, True),
+    (4096, 32, 3, 0, False), (33, 128, 2000, 1, True)])
+def test_plan_matches_oracle(B, page, most, T_over, in_place):
+    r = np.random.default_rng(B + most)
+    lens, new = r.integers(0, 300, B), r.integers(0, most + 1, B)
+    lens[0] = 0
+    new[-1] = most
+    P = -(-(300 + most) // page) + 1
+    num = 2 * int(sum(-(-(lens + new) // page))) + 7
+    order = r.permutation(num)
+    table, at = np.full((B, P), -1), 0
+    for b in range(B):
+        n = -(-lens[b] // page)
+        table[b, :n] = order[at:at + n]
+        at += n
+    free, head, T = order[at:], 2, int(new.sum()) + T_over
+    want = po.plan(new, lens, free, head, table, page, T, num)
+    got = _plan(mcs.paged(B, 1, 1, 64, page, num, P), new, lens, free, head, table, T, in_place)
+    for x, y in zip(got, want):
+        np.testing.assert_array_equal(x, y)
+    assert mcs.mcs_device_status() == 0
+
+
+@pytest.mark.parametrize("what", ["tokens", "pages", "table", "negative", "free", "started", "head"])
+def test_plan_refuses_and_takes_nothing(what):
+    lens, new, free, head, T = [20, 0, 5], [3, 40, 12], [7, 8, 9, 4, 5], 1, 60
+    table = np.array([[1, 2, -1, -1], [-1] * 4, [3, -1, -1, -1]])
+    if what == "tokens":
+        T = 54
+    elif what == "pages":
+        head = 2
+    elif what == "table":
+        new[1] = 65
+    elif what == "negative":
+        new[0] = -1
+    elif what == "free":
+        free[2] = 10
+    elif what == "started":
+        table[0, 1] = -1
+    elif what == "head":
+        head = -1
+    p = mcs.paged(3, 1, 1, 64, 16, 10, 4)
+    lo, ho, tab, cu, slots, pos = _plan(p, new, lens, free, head, table, T)
+    assert mcs.mcs_device_status() == 6
+    assert lo.tolist() == lens and ho.tolist() == [head] and (tab == table).all()
+    assert not cu.any() and (slots == -1).all() and (pos == -1).all()
+
+
+def test_plan_of_a_good_request_after_a_refused_one():
+    lens, new, free = [20, 0, 5], [3, 40, 12], [7, 8, 9, 4, 5]
+    table = np.array([[1, 2, -1, -1], [-1] * 4, [3, -1, -1, -1]])
+    p = mcs.paged(3, 1, 1, 64, 16, 10, 4)
+    got = _plan(p, new, lens, free, 1, table, 55)
+    for x, y in zip(got, po.plan(new, lens, free, 1, table, 16, 55, 10)):
+        np.testing.assert_array_equal(x, y)
+    assert mcs.mcs_device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,new,Hkv,D,page,stride", [
+    ([0], [1], 1, 128, 16, 0), ([15, 16, 17, 0], [1, 1, 0, 40], 2, 64, 16, 0),
+    ([100, 3], [29, 300], 3, 128, 128, 8 * 128), ([31, 0, 64], [1, 7, 64], 8, 128, 32, 0)])
+def test_write_matches_oracle(lens, new, Hkv, D, page, stride, e4m3):
+    after = [a + n for a, n in zip(lens, new)]
+    c = Cache(after, Hkv, Hkv, D, page, e4m3, seed=sum(after))
+    c.p.kv_stride = stride
+    free = np.concatenate([c.table[b, -(-a // page):-(-z // page)] for b, (a, z) in enumerate(zip(lens, after))])
+    T = sum(new) + 3
+    planned = po.plan(new, lens, free, 0, c.table, page, T, c.p.num_pages)
+    slots = planned[4]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(T, stride or Hkv * D, generator=g, device="cuda").to(torch.bfloat16)[:, :Hkv * D]
+            .view(T, Hkv, D) for _ in range(2))
+    mean = c.means()
+    before = [x.clone() for x in (c.k, c.v, mean)]
+    mcs.mcs_paged_write(c.p, k, v, _i32(slots), c.k, c.v, mean)
+    if e4m3:
+        enc = lambda x, s: orc.e4m3_encode(x.float().cpu().numpy(), s)
+        kn, vn, held = enc(k, KS), enc(v, VS), [x.cpu().numpy() for x in before[:2]]
+        values = lambda x: orc.e4m3_decode(x).astype(np.float64) * KS
+    else:
+        bits = lambda x: x.contiguous().view(torch.int16).cpu().numpy()
+        kn, vn, held = bits(k), bits(v), [bits(x) for x in before[:2]]
+        values = lambda x: torch.from_numpy(np.ascontiguousarray(x)).view(torch.bfloat16).double().numpy()
+    want_mean = _f64(before[2])
+    touched = po.write(kn, vn, slots, *held, want_mean, values)
+    for got, want in zip((c.k, c.v), held):
+        got = got.cpu().numpy() if e4m3 else got.view(torch.int16).cpu().numpy()
+        np.testing.assert_array_equal(got, want)
+    got = _f64(mean)
+    for pg in range(c.p.num_pages):
+        if pg not in touched:
+            np.testing.assert_array_equal(got[pg], _f64(before[2])[pg])
+            continue
+        size = np.abs(values(held[0][pg, :, :touched[pg]])).mean(1)
+        assert (np.abs(got[pg] - want_mean[pg]) <= 2.0 ** -8 * np.abs(want_mean[pg]) + (page + 2) * U * size).all()
+    # without means nothing else changes
+    k2, v2 = before[0], before[1]
+    mcs.mcs_paged_write(c.p, k, v, _i32(slots), k2, v2)
+    eq = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert eq(k2, c.k) and eq(v2, c.v)
+
+
+def test_write_skips_padding_and_slots_past_the_cache():
+    p = mcs.paged(1, 1, 1, 64, 16, 4, 4)
+    cache, mean = torch.zeros(2, 4, 1, 16, 64, device="cuda").to(torch.bfloat16), None
+    k = torch.ones(4, 1, 64, device="cuda", dtype=torch.bfloat16)
+    mcs.mcs_paged_write(p, k, k, _i32([-1, 64, -5, 2 ** 31 - 1]), cache[0], cache[1], mean)
+    assert mcs.mcs_device_status() == 6
+    assert not cache.any()
+    mcs.mcs_paged_write(p, k[:0], k[:0], _i32([]), cache[0], cache[1])
+    assert mcs.mcs_device_status() == 0
+
+
+# ------------------------------------------------------------------ what the arrays may get wrong
+
+def test_decode_reports_and_skips_what_lies_outside():
+    """A page outside the cache is skipped as if its tokens were not there; a length past the
+    table counts as no tokens.  The checks stand in the kernels in front of each access."""
+    c = Cache([40, 100, 33], 4, 2, 128, 16, seed=3)
+    table = c.table.copy()
+    table[1, 2], table[1, 4] = -1, c.p.num_pages
+    c.dtable = _i32(table)
+    out, ls = c.run()
+    assert mcs.mcs_device_status() == 6
+    sel = np.full((3, 2, 9), -1)
+    for b, n in enumerate([3, 7, 3]):
+        sel[b, :, :n] = np.arange(n)
+    sel[1, :, 2] = sel[1, :, 4] = -1
+    c.check(out, ls, sel)
+    # the sparse form with logical pages outside the sequence
+    bad = sel.copy()
+    bad[0, 0, 1], bad[2, 1, 0] = 3, -2
+    c.dtable = _i32(c.table)
+    out, ls = c.run(_i32(bad))
+    assert mcs.mcs_device_status() == 6
+    sel[0, 0, 1] = sel[2, 1, 0] = -1
+    c.check(out, ls, sel)
+    # lengths outside the table
+    c.dlens, c.lens = _i32([40, c.p.max_pages * 16 + 1, -3]), [40, 0, 0]
+    out, ls = c.run()
+    assert mcs.mcs_device_status() == 6
+    c.check(out, ls)
+
+
+def test_select_reports_and_ranks_bad_pages_last():
+    c = Cache([100, 64], 4, 2, 64, 16, seed=3)
+    mean, table = c.means(), c.table.copy()
+    table[0, 3], table[1, 1] = -1, c.p.num_pages
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(c.p))
+    sel = torch.empty(2, 2, 3, dtype=torch.int32, device="cuda")
+    mcs.mcs_paged_select(c.p, c.q, mean, _i32(table), _i32([100, 64]), sel, ws, sink=0, recent=0)
+    assert mcs.mcs_device_status() == 6
+    got = sel.cpu().numpy()
+    assert (got >= 0).all() and not (got[0] == 3).any() and not (got[1] == 1).any()
+    mcs.mcs_paged_select(c.p, c.q, mean, _i32(c.table), _i32([-1, 10 ** 6]), sel, ws)
+    assert mcs.mcs_device_status() == 6
+    assert (sel == -1).all()
+
+
+# ------------------------------------------------------------------ together, as they are used
+
+@pytest.mark.parametrize("e4m3,Hq,Hkv,D,page", [(False, 8, 2, 128, 16), (True, 4, 4, 64, 32)])
+def test_generation_steps_together(e4m3, Hq, Hkv, D, page):
+    """Prompts, then tokens one at a time: normalise and rotate, plan, write, select, attend;
+    the batch has an idle request.  Against the oracle over the whole sequences."""
+    r = np.random.default_rng(D)
+    B, rot, P, num, select = 3, D // 2, 12, 30, 3
+    kv = mcs.KV_E4M3 if e4m3 else mcs.KV_BF16
+    fused = (Hq + 2 * Hkv) * D
+    g = torch.Generator(device="cuda").manual_seed(D)
+    angle = np.arange(256)[:, None] * 100.0 ** -np.linspace(0, 1, rot // 2)
+    cos, sin = (torch.from_numpy(f(angle)).float().cuda() for f in (np.cos, np.sin))
+    w = [(1 + 0.1 * torch.randn(D, generator=g, device="cuda")) for _ in range(2)]
+    p = mcs.paged(B, Hq, Hkv, D, page, num, P, kv=kv, k_scale=2.0 ** -6, v_scale=2.0 ** -6, kv_stride=0)
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    kc, vc = (torch.zeros(num, Hkv, page, D, dtype=dt, device="cuda") for _ in range(2))
+    mean = torch.zeros(num, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    free, head = _i32(r.permutation(num)), _i32([0])
+    lens, table = _i32([0] * B), _i32(np.full((B, P), -1))
+    ws = mcs.empty_workspace(mcs.mcs_paged_decode_workspace(p))
+    ws2 = mcs.empty_workspace(mcs.mcs_paged_select_workspace(p))
+    seq_k, seq_v = [[] for _ in range(B)], [[] for _ in range(B)]
+    for step, new in enumerate([[50, 0, 97], [1, 1, 1], [1, 0, 1], [1, 1, 1]]):
+        T = sum(new) + 2
+        x = torch.randn(T, fused, generator=g, device="cuda").to(torch.bfloat16)
+        cu = torch.empty(B + 1, dtype=torch.int32, device="cuda")
+        slots, pos = (torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2))
+        mcs.mcs_paged_plan(p, _i32(new), lens, free, head, table, lens, head, cu, slots, pos)
+        rp = mcs.rope_params(T, 1, Hq, Hkv, D, rot, 256, interleaved=e4m3, layout=mcs.LAYOUT_BNHD,
+                             q_stride=fused, k_stride=fused)
+        q, k = (torch.full((T, 1, h, D), 5.0, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv))
+        mcs.mcs_qk_norm_rope(rp, x[:, :Hq * D].view(T, 1, Hq, D), x[:, Hq * D:(Hq + Hkv) * D].view(T, 1, Hkv, D),
+                             w[0], w[1], cos, sin, pos.view(T, 1), q, k)
+        v = x[:, (Hq + Hkv) * D:].view(T, Hkv, D)
+        mcs.mcs_paged_write(p, k.view(T, Hkv, D), v.contiguous(), slots, kc, vc, mean)
+        # padding rows stay as they were
+        assert (q[-2:] == 5).all() and (k[-2:] == 5).all()
+        # the stored keys are the oracle's rotated ones
+        c = cu.cpu().numpy()
+        pn = pos.cpu().numpy()
+        live = slice(0, c[-1])
+        for h0, w0, got in ((0, w[0], q), (Hq, w[1], k)):
+            n = Hq if h0 == 0 else Hkv
+            xs = _f64(x[:, h0 * D:(h0 + n) * D]).reshape(T, 1, n, D)[live]
+            want = po.norm_rope(xs, _f64(w0), _f64(cos), _f64(sin), pn[live, None], rot, e4m3, 1e-6)
+            # bf16 rounding, and fp32 arithmetic on values below 2 max |y|
+            assert (np.abs(_f64(got)[live] - want) <= 2.0 ** -8 * np.abs(want) + 2 * (D / 2 + 8) * U * np.abs(want).max()).all()
+        for b in range(B):
+            seq_k[b] += list(_f64(k)[c[b]:c[b + 1], 0])
+            seq_v[b] += list(_f64(v)[c[b]:c[b + 1]])
+        if step == 0:
+            continue
+        # one query per sequence, in batch order; the idle request asks nothing new
+        # but still attends to what it has
+        last = [max(c[b + 1] - 1, 0) for b in range(B)]
+        qd = q[last, 0].contiguous()
+        sel = torch.empty(B, Hkv, select, dtype=torch.int32, device="cuda")
+        out, outs = (torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        mcs.mcs_paged_decode(p, qd, kc, vc, table, lens, out, ws)
+        mcs.mcs_paged_select(p, qd, mean, table, lens, sel, ws2, sink=1, recent=1)
+        mcs.mcs_paged_decode_sparse(p, qd, kc, vc, table, lens, sel, outs, ws)
+        assert mcs.mcs_device_status() == 0
+        ln, tb = lens.cpu().numpy(), table.cpu().numpy()
+        assert ln.tolist() == [len(x) for x in seq_k]
+        np.testing.assert_array_equal(sel.cpu().numpy(), po.select(_f64(qd), _f64(mean), tb, ln, page, select, 1, 1))
+        kd, vd = (_f64(x) * (2.0 ** -6 if e4m3 else 1) for x in (kc, vc))
+        for b in range(B):  # the cache is the sequence
+            for t in range(ln[b]):
+                row = kd[tb[b, t // page], :, t % page]
+                # E4M3: half a step, 2^-4 of the value or half the smallest step 2^-10 * scale
+                assert (np.abs(row - seq_k[b][t]) <= (2.0 ** -4 * np.abs(seq_k[b][t]) + 2.0 ** -16 if e4m3 else 0)).all()
+        for got, s in ((out, None), (outs, sel.cpu().numpy())):
+            want, _, absv, size = po.decode(_f64(qd), kd, vd, tb, ln, D ** -0.5, s)
+            tol = 2.0 ** -8 * np.abs(want) + absv * (4 * (D + 8) * U * size + 2.0 ** -20 + (2.0 ** -11 if e4m3 else 2.0 ** -16) + 100 * U)[..., None]
+            assert (np.abs(_f64(got) - want) <= tol).all()
+
+
+# ------------------------------------------------------------------ streams, graphs, repeats
+
+def test_repeated_calls_give_the_same_bits():
+    c = Cache([3000, 17, 900, 0], 16, 2, 128, 16, seed=1)
+    a = c.run()
+    for _ in range(5):
+        b = c.run()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    cs = [Cache([5000, 300], 8, 2, 128, 32, e, seed=i) for i, e in enumerate((False, True))]
+    want = [c.run() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = []
+    for _ in range(10):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                got.append(c.run())
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_captured_step_follows_lengths_and_pages():
+    """plan, write, select and both attentions in one graph, replayed while the state advances
+    in place; a second graph shares the workspace on the same stream."""
+    B, Hq, Hkv, D, page, P, num = 2, 8, 2, 128, 16, 8, 16
+    p = mcs.paged(B, Hq, Hkv, D, page, num, P)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    kc, vc, mean = rand(num, Hkv, page, D), rand(num, Hkv, page, D), rand(num, Hkv, D)
+    lens, head, table = _i32([30, 0]), _i32([2]), _i32([[3, 9] + [-1] * 6, [-1] * 8])
+    free = _i32([9, 3, 1, 0, 15, 7, 8, 2])
+    new, cu = _i32([1, 1]), _i32([0] * 3)
+    slots, pos = _i32([0, 0]), _i32([0, 0])
+    q, k, v = rand(B, Hq, D), rand(B, Hkv, D), rand(B, Hkv, D)
+    out, outs = (torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    sel = torch.empty(B, Hkv, 2, dtype=torch.int32, device="cuda")
+    ws = mcs.empty_workspace(mcs.mcs_paged_decode_workspace(p))
+    ws2 = mcs.empty_workspace(mcs.mcs_paged_select_workspace(p))
+
+    def attend(o):
+        mcs.mcs_paged_decode(p, q, kc, vc, table, lens, o, ws)
+
+    def step():
+        mcs.mcs_paged_plan(p, new, lens, free, head, table, lens, head, cu, slots, pos)
+        mcs.mcs_paged_write(p, k, v, slots, kc, vc, mean)
+        mcs.mcs_paged_select(p, q, mean, table, lens, sel, ws2, sink=0, recent=1)
+        mcs.mcs_paged_decode_sparse(p, q, kc, vc, table, lens, sel, outs, ws)
+        attend(out)
+
+    state = [x.clone() for x in (kc, vc, mean, lens, head, table)]
+    step()  # first calls outside the capture
+    for x, y in zip((kc, vc, mean, lens, head, table), state):
+        x.copy_(y)
+    s = torch.cuda.Stream()
+    graph, other, out2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph(), torch.empty_like(out)
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    with torch.cuda.graph(other, stream=s):
+        attend(out2)
+    for x, y in zip((kc, vc, mean, lens, head, table), state):
+        x.copy_(y)
+    for i in range(4):
+        k.copy_(rand(B, Hkv, D))
+        graph.replay()
+        other.replay()
+        torch.cuda.synchronize()
+        assert lens.tolist() == [31 + i, 1 + i]
+        assert head.tolist() == [2 + 1 + (i >= 2)]
+        assert torch.equal(out, out2)
+        tb, ln = table.cpu().numpy(), lens.cpu().numpy()
+        for o, sl in ((out, None), (outs, sel.cpu().numpy())):
+            want, _, absv, size = po.decode(_f64(q), _f64(kc), _f64(vc), tb, ln, D ** -0.5, sl)
+            tol = 2.0 ** -8 * np.abs(want) + absv * (4 * (D + 8) * U * size + 2.0 ** -15)[..., None]
+            assert (np.abs(_f64(o) - want) <= tol).all()
+    assert mcs.mcs_device_status() == 0
+
+
+def test_rows_past_two_gib_of_cache():
+    """Pages whose byte offsets pass 32 bits: a 4.3 GB cache, the sequence's pages at its end."""
+    page, Hkv, D, num = 64, 8, 128, 33000
+    p = mcs.paged(1, 8, Hkv, D, page, num, 4)
+    kc = torch.empty(num, Hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    last = num - 1
+    tab = np.array([[last, last - 2, last - 1, 0]])
+    k = torch.randn(150, Hkv, D, device="cuda").to(torch.bfloat16)
+    slots = [tab[0, t // page] * page + t % page for t in range(150)]
+    mcs.mcs_paged_write(p, k, -k, _i32(slots), kc, vc)
+    q = torch.randn(1, 8, D, device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    ws = mcs.empty_workspace(mcs.mcs_paged_decode_workspace(p))
+    mcs.mcs_paged_decode(p, q, kc, vc, _i32(tab), _i32([150]), out, ws)
+    z = torch.einsum("hd,thd->ht", q[0].double(), k.double()) * D ** -0.5
+    want = -torch.einsum("ht,thd->hd", torch.softmax(z, 1), k.double())
+    absv = torch.einsum("ht,thd->hd", torch.softmax(z, 1), k.double().abs())
+    # scores below about 10 in size: 2 (D + 8) u * 10 * 2 < 2^-13
+    assert ((out[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -13 * absv).all()
+
+
+def test_binding_refuses_what_does_not_fit():
+    c = Cache([40], 4, 2, 128, 16, seed=0)
+    out = torch.empty(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ok = (c.p, c.q, c.k, c.v, c.dtable, c.dlens, out, c.ws)
+    for i, bad in [(1, c.q.float()), (2, c.k[:, :, :8]), (2, c.k.transpose(2, 3).contiguous().transpose(2, 3)),
+                   (4, c.dtable[:, :2]), (5, c.dlens.long()), (6, out[:, :2]), (1, c.q.cpu())]:
+        with pytest.raises(ValueError):
+            mcs.mcs_paged_decode(*ok[:i], bad, *ok[i + 1:])
+    with pytest.raises(ValueError, match="strides"):
+        wide = torch.zeros(1, 4, 256, dtype=torch.bfloat16, device="cuda")[:, :, :128]
+        mcs.mcs_paged_decode(ok[0], wide, *ok[2:])
+    with pytest.raises(mcs.McsError, match="WORKSPACE"):
+        mcs.mcs_paged_decode(*ok[:7], c.ws[:16])
+    if torch.cuda.device_count() > 1:
+        with pytest.raises(ValueError, match="cuda:1"):
+            mcs.mcs_paged_decode(*ok[:1], c.q.to("cuda:1"), *ok[2:])

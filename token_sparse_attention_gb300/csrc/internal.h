@@ -153,4 +153,107 @@ cudaError_t launch_pddp(const __nv_bfloat16* q, int layout, int H, int head0, in
                         int D, int C, int iters, int32_t* perm_out, void* ws, size_t ws_bytes,
                         unsigned* status, cudaStream_t stream);
 
+// ---------------------------------------------------------------- paged cache
+
+// New tokens' pages and slots (see mcs_paged_plan).
+struct PlanArgs {
+  int B, page, num_pages, max_pages, n_free, T;
+  const int32_t* new_lens;   // [B]
+  const int32_t* lens;       // [B]
+  const int32_t* free_pages; // [n_free]
+  const int32_t* free_head;  // [1]
+  int32_t* table;            // [B, max_pages]
+  int32_t* lens_out;         // [B], may be lens
+  int32_t* head_out;         // [1], may be free_head
+  int32_t* cu_new;           // [B + 1]
+  int32_t* slots;            // [T]
+  int32_t* positions;        // [T], nullable
+  unsigned* status;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct WriteArgs {
+  int T, Hkv, D, page;
+  long long slots_total;     // num_pages * page
+  long long stride;          // elements between tokens of k and v
+  float k_scale, v_scale;    // E4M3
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const int32_t* slots;      // [T]
+  void* k_cache;
+  void* v_cache;
+  __nv_bfloat16* k_mean;     // [num_pages, Hkv, D], nullable
+  unsigned* status;
+};
+cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t stream);
+
+struct SelectArgs {
+  int B, Hq, Hkv, D, page, num_pages, max_pages;
+  int select, sink, recent;
+  long long q_stride;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_mean;
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t* sel;              // [B, Hkv, select]
+  uint32_t* keys;            // [B * Hkv, max_pages] order-preserving score keys
+  unsigned* status;
+};
+cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream);
+size_t paged_select_workspace_bytes(int B, int Hkv, int max_pages);
+
+struct DecodeArgs {
+  int B, Hq, Hkv, D, page, num_pages, max_pages;
+  long long q_stride;
+  float scale_log2;          // softmax scale * log2(e) (* k_scale for E4M3)
+  float v_scale;             // 1 for bf16
+  const __nv_bfloat16* q;
+  const void* k;             // [num_pages, Hkv, page, D]
+  const void* v;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* sel;        // [B, Hkv, select]; null: every page
+  int select;
+  __nv_bfloat16* out;        // [B, Hq, D]
+  float* lse;                // [B, Hq], nullable
+  void* ws;
+  unsigned* status;
+};
+cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream);
+size_t paged_decode_workspace_bytes(int D);
+
+// ---------------------------------------------------------------- norm and rotation
+
+struct RopeArgs {
+  int B, N, Hq, Hkv, D, rot, interleaved, table_rows, layout;
+  float eps;
+  long long q_stride, k_stride;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const float* wq;
+  const float* wk;
+  const float* cos_table;
+  const float* sin_table;
+  const int32_t* positions;
+  __nv_bfloat16* q_out;      // backward: dq, dk (strided like q, k)
+  __nv_bfloat16* k_out;
+  const __nv_bfloat16* dq_out;  // backward
+  const __nv_bfloat16* dk_out;
+  float* dwq;
+  float* dwk;
+  float* ws;
+  unsigned* status;
+};
+cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_rope_backward(const RopeArgs& a, cudaStream_t stream);
+size_t norm_rope_backward_workspace_bytes(int D);
+
+// Order-preserving map of floats to unsigned keys (a larger score has a larger
+// key; -0 and +0 the same key, NaN above every number).
+__host__ __device__ __forceinline__ uint32_t score_key_bits(uint32_t bits) {
+  if ((bits & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFC00000u;
+  if ((bits & 0x7FFFFFFFu) == 0u) return 0x80000000u;
+  return (bits & 0x80000000u) ? ~bits : (bits | 0x80000000u);
+}
+
 }  // namespace mcs

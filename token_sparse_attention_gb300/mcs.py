@@ -25,7 +25,11 @@ __all__ = [
     "meta_views", "mcs_meta_pack", "mcs_meta_unpack", "Stager", "mcs_block_workspace", "mcs_block_topk", "mcs_pooled_block_select",
     "mcs_gather_mass", "mcs_rel_l1", "mcs_pair_bytes", "empty_pairs", "mcs_pair_lists",
     "mcs_sparse_attn_pairs", "mcs_sparse_attn_pairs_record", "mcs_quantize_e4m3",
-    "mcs_sparse_attn_e4m3",
+    "mcs_sparse_attn_e4m3", "Paged", "paged", "KV_BF16", "KV_E4M3", "mcs_paged_plan",
+    "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
+    "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse", "Rope",
+    "rope_params", "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace",
+    "mcs_qk_norm_rope_backward",
 ]
 
 # Every symbol include/mcs.h declares.
@@ -39,6 +43,9 @@ EXPORTED = (
     "mcs_stager_prefetch", "mcs_stager_offload", "mcs_stager_wait", "mcs_block_workspace",
     "mcs_block_topk", "mcs_pooled_block_select", "mcs_gather_mass", "mcs_rel_l1",
     "mcs_quantize_e4m3", "mcs_sparse_attn_e4m3",
+    "mcs_paged_plan", "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
+    "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
+    "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace", "mcs_qk_norm_rope_backward",
 )
 
 STATUS_NAMES = {0: "MCS_OK", 1: "MCS_ERR_INVALID_ARG", 2: "MCS_ERR_UNSUPPORTED",
@@ -73,6 +80,44 @@ def params(B, H, N, D, C=128, K=None, scale=0.0, pddp_iters=0, layout=LAYOUT_BHN
     return Params(B, H, N, D, C, N if K is None else K, scale, pddp_iters, layout)
 
 
+class Paged(ctypes.Structure):
+    """mcs_paged: B, Hq, Hkv, D, page, num_pages, max_pages, kv (KV_BF16 or KV_E4M3),
+    scale (0 -> 1/sqrt(D)), k_scale, v_scale, q_stride, kv_stride (elements between
+    consecutive tokens' rows; 0: contiguous)."""
+
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("D", ctypes.c_int), ("page", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("kv", ctypes.c_int), ("scale", ctypes.c_float),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int), ("kv_stride", ctypes.c_int)]
+
+
+KV_BF16, KV_E4M3 = 0, 1
+
+
+def paged(B, Hq, Hkv, D, page, num_pages, max_pages, kv=KV_BF16, scale=0.0, k_scale=1.0,
+          v_scale=1.0, q_stride=0, kv_stride=0) -> Paged:
+    return Paged(B, Hq, Hkv, D, page, num_pages, max_pages, kv, scale, k_scale, v_scale,
+                 q_stride, kv_stride)
+
+
+class Rope(ctypes.Structure):
+    """mcs_rope: B, N, Hq, Hkv, D, rot, interleaved, table_rows, layout, eps, q_stride,
+    k_stride (elements between consecutive tokens' rows; 0: contiguous)."""
+
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("table_rows", ctypes.c_int),
+                ("layout", ctypes.c_int), ("eps", ctypes.c_float), ("q_stride", ctypes.c_int),
+                ("k_stride", ctypes.c_int)]
+
+
+def rope_params(B, N, Hq, Hkv, D, rot, table_rows, interleaved=False, layout=LAYOUT_BHND,
+                eps=1e-6, q_stride=0, k_stride=0) -> Rope:
+    return Rope(B, N, Hq, Hkv, D, rot, int(interleaved), table_rows, layout, eps, q_stride,
+                k_stride)
+
+
 def library_path() -> str:
     return os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmcs.so")
 
@@ -80,6 +125,7 @@ def library_path() -> str:
 _LIB = None
 _vp, _sz, _i, _st = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int
 _pp = ctypes.POINTER(Params)
+_gp, _rp = ctypes.POINTER(Paged), ctypes.POINTER(Rope)
 
 _SIGS = {
     "mcs_status_string": ([_st], ctypes.c_char_p),
@@ -117,6 +163,17 @@ _SIGS = {
     "mcs_quantize_e4m3": ([_vp, _sz, ctypes.c_float, _vp, _vp], _st),
     "mcs_sparse_attn_e4m3": ([_pp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp,
                               _vp, _vp, _vp], _st),
+    "mcs_paged_plan": ([_gp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp], _st),
+    "mcs_paged_write": ([_gp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _st),
+    "mcs_paged_decode_workspace": ([_gp], _sz),
+    "mcs_paged_decode": ([_gp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _st),
+    "mcs_paged_select_workspace": ([_gp], _sz),
+    "mcs_paged_select": ([_gp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp], _st),
+    "mcs_paged_decode_sparse": ([_gp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp],
+                                _st),
+    "mcs_qk_norm_rope": ([_rp] + [_vp] * 10, _st),
+    "mcs_qk_norm_rope_backward_workspace": ([_rp], _sz),
+    "mcs_qk_norm_rope_backward": ([_rp] + [_vp] * 14 + [_sz, _vp], _st),
 }
 
 
@@ -485,6 +542,176 @@ def mcs_rel_l1(p: Params, got, want, rows=None, stream=None) -> tuple:
                             sums.data_ptr(), _stream(stream)), "mcs_rel_l1")
     v = sums.cpu()
     return float(v[0]), float(v[1])
+
+
+# ---------------------------------------------------------------- paged cache
+
+def _device(stream) -> int:
+    """The device a call runs on: the stream's, or the current one."""
+    current = torch.cuda.current_device()
+    if getattr(stream, "device_index", current) != current:
+        raise ValueError("stream belongs to another device than the current one")
+    return current
+
+
+def _at(dev, t, dtype, shape, name, optional=False):
+    """As _ptr, and on device `dev`."""
+    p = _ptr(t, dtype, shape, name, optional)
+    if t is not None and t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
+    return p
+
+
+def _rows_at(dev, t, dtype, shape, stride, name):
+    """Rows [..., H, D] whose consecutive tokens stand `stride` elements apart (0: H * D)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
+    want, n = [1, shape[-1]], stride or shape[-1] * shape[-2]
+    for size in reversed(shape[:-2]):
+        want.append(n)
+        n *= size
+    if any(size > 1 and have != w for size, have, w in zip(shape, t.stride(), reversed(want))):
+        raise ValueError(f"{name} must have strides {tuple(reversed(want))}, got {t.stride()}")
+    return t.data_ptr()
+
+
+def _cache_at(dev, t, p: Paged, name):
+    if p.kv == KV_E4M3 and isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+        t = t.view(torch.uint8)
+    return _at(dev, t, torch.uint8 if p.kv == KV_E4M3 else torch.bfloat16,
+               (p.num_pages, p.Hkv, p.page, p.D), name)
+
+
+def mcs_paged_plan(p: Paged, new_lens, lens, free_pages, free_head, block_table, lens_out,
+                   head_out, cu_new, slots, positions=None, stream=None):
+    dev, i32, T = _device(stream), torch.int32, slots.numel()
+    _check(lib().mcs_paged_plan(
+        ctypes.byref(p), _at(dev, new_lens, i32, (p.B,), "new_lens"),
+        _at(dev, lens, i32, (p.B,), "lens"), _at(dev, free_pages, i32, None, "free_pages"),
+        free_pages.numel(), _at(dev, free_head, i32, (1,), "free_head"),
+        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
+        _at(dev, lens_out, i32, (p.B,), "lens_out"), _at(dev, head_out, i32, (1,), "head_out"),
+        _at(dev, cu_new, i32, (p.B + 1,), "cu_new"), _at(dev, slots, i32, (T,), "slots"),
+        _at(dev, positions, i32, (T,), "positions", optional=True), T, _stream(stream)),
+        "mcs_paged_plan")
+
+
+def mcs_paged_write(p: Paged, k, v, slots, k_cache, v_cache, k_mean=None, stream=None):
+    dev, bf, T = _device(stream), torch.bfloat16, slots.numel()
+    _check(lib().mcs_paged_write(
+        ctypes.byref(p), T, _rows_at(dev, k, bf, (T, p.Hkv, p.D), p.kv_stride, "k"),
+        _rows_at(dev, v, bf, (T, p.Hkv, p.D), p.kv_stride, "v"),
+        _at(dev, slots, torch.int32, (T,), "slots"), _cache_at(dev, k_cache, p, "k_cache"),
+        _cache_at(dev, v_cache, p, "v_cache"),
+        _at(dev, k_mean, bf, (p.num_pages, p.Hkv, p.D), "k_mean", optional=True),
+        _stream(stream)), "mcs_paged_write")
+
+
+def mcs_paged_decode_workspace(p: Paged) -> int:
+    return lib().mcs_paged_decode_workspace(ctypes.byref(p))
+
+
+def mcs_paged_decode(p: Paged, q, k_cache, v_cache, block_table, lens, out, ws, lse=None,
+                     stream=None):
+    dev, bf, i32 = _device(stream), torch.bfloat16, torch.int32
+    _check(lib().mcs_paged_decode(
+        ctypes.byref(p), _rows_at(dev, q, bf, (p.B, p.Hq, p.D), p.q_stride, "q"),
+        _cache_at(dev, k_cache, p, "k_cache"), _cache_at(dev, v_cache, p, "v_cache"),
+        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
+        _at(dev, lens, i32, (p.B,), "lens"), _at(dev, out, bf, (p.B, p.Hq, p.D), "out"),
+        _at(dev, lse, torch.float32, (p.B, p.Hq), "lse", optional=True),
+        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)), "mcs_paged_decode")
+
+
+def mcs_paged_select_workspace(p: Paged) -> int:
+    return lib().mcs_paged_select_workspace(ctypes.byref(p))
+
+
+def _sel_at(dev, sel, p: Paged):
+    if not isinstance(sel, torch.Tensor) or sel.dim() != 3:
+        raise ValueError("sel must be a [B, Hkv, select] tensor")
+    return _at(dev, sel, torch.int32, (p.B, p.Hkv, sel.shape[2]), "sel")
+
+
+def mcs_paged_select(p: Paged, q, k_mean, block_table, lens, sel, ws, sink=1, recent=1,
+                     stream=None):
+    """sel [B, Hkv, select]: the last dimension says how many pages are kept."""
+    dev, bf, i32 = _device(stream), torch.bfloat16, torch.int32
+    ps = _sel_at(dev, sel, p)
+    _check(lib().mcs_paged_select(
+        ctypes.byref(p), _rows_at(dev, q, bf, (p.B, p.Hq, p.D), p.q_stride, "q"),
+        _at(dev, k_mean, bf, (p.num_pages, p.Hkv, p.D), "k_mean"),
+        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
+        _at(dev, lens, i32, (p.B,), "lens"), sel.shape[2], int(sink), int(recent), ps,
+        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)), "mcs_paged_select")
+
+
+def mcs_paged_decode_sparse(p: Paged, q, k_cache, v_cache, block_table, lens, sel, out, ws,
+                            lse=None, stream=None):
+    dev, bf, i32 = _device(stream), torch.bfloat16, torch.int32
+    ps = _sel_at(dev, sel, p)
+    _check(lib().mcs_paged_decode_sparse(
+        ctypes.byref(p), _rows_at(dev, q, bf, (p.B, p.Hq, p.D), p.q_stride, "q"),
+        _cache_at(dev, k_cache, p, "k_cache"), _cache_at(dev, v_cache, p, "v_cache"),
+        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
+        _at(dev, lens, i32, (p.B,), "lens"), ps, sel.shape[2],
+        _at(dev, out, bf, (p.B, p.Hq, p.D), "out"),
+        _at(dev, lse, torch.float32, (p.B, p.Hq), "lse", optional=True),
+        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)),
+        "mcs_paged_decode_sparse")
+
+
+# ---------------------------------------------------------------- norm and rotation
+
+def _rope_out_shape(p: Rope, H):
+    return (p.B, p.N, H, p.D) if p.layout == LAYOUT_BNHD else (p.B, H, p.N, p.D)
+
+
+def _rope_inputs(dev, p: Rope, q, k, wq, wk, cos, sin, positions):
+    """Pointers of q, k, wq, wk, cos, sin, positions (k and wk null when Hkv = 0)."""
+    bf, f32, table = torch.bfloat16, torch.float32, (p.table_rows, p.rot // 2)
+    some = p.Hkv > 0
+    return (_rows_at(dev, q, bf, (p.B, p.N, p.Hq, p.D), p.q_stride, "q"),
+            _rows_at(dev, k, bf, (p.B, p.N, p.Hkv, p.D), p.k_stride, "k") if some else None,
+            _at(dev, wq, f32, (p.D,), "wq", optional=True),
+            _at(dev, wk, f32, (p.D,), "wk", optional=True) if some else None,
+            _at(dev, cos, f32, table, "cos") if p.rot else None,
+            _at(dev, sin, f32, table, "sin") if p.rot else None,
+            _at(dev, positions, torch.int32, (p.B, p.N), "positions", optional=True))
+
+
+def mcs_qk_norm_rope(p: Rope, q, k, wq, wk, cos, sin, positions, q_out, k_out, stream=None):
+    dev, bf = _device(stream), torch.bfloat16
+    _check(lib().mcs_qk_norm_rope(
+        ctypes.byref(p), *_rope_inputs(dev, p, q, k, wq, wk, cos, sin, positions),
+        _at(dev, q_out, bf, _rope_out_shape(p, p.Hq), "q_out"),
+        _at(dev, k_out, bf, _rope_out_shape(p, p.Hkv), "k_out") if p.Hkv else None,
+        _stream(stream)), "mcs_qk_norm_rope")
+
+
+def mcs_qk_norm_rope_backward_workspace(p: Rope) -> int:
+    return lib().mcs_qk_norm_rope_backward_workspace(ctypes.byref(p))
+
+
+def mcs_qk_norm_rope_backward(p: Rope, dq_out, dk_out, q, k, wq, wk, cos, sin, positions, dq, dk,
+                              dwq, dwk, ws, stream=None):
+    dev, bf, f32, some = _device(stream), torch.bfloat16, torch.float32, p.Hkv > 0
+    _check(lib().mcs_qk_norm_rope_backward(
+        ctypes.byref(p), _at(dev, dq_out, bf, _rope_out_shape(p, p.Hq), "dq_out"),
+        _at(dev, dk_out, bf, _rope_out_shape(p, p.Hkv), "dk_out") if some else None,
+        *_rope_inputs(dev, p, q, k, wq, wk, cos, sin, positions),
+        _rows_at(dev, dq, bf, (p.B, p.N, p.Hq, p.D), p.q_stride, "dq"),
+        _rows_at(dev, dk, bf, (p.B, p.N, p.Hkv, p.D), p.k_stride, "dk") if some else None,
+        _at(dev, dwq, f32, (p.D,), "dwq", optional=True),
+        _at(dev, dwk, f32, (p.D,), "dwk", optional=True) if some else None,
+        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)),
+        "mcs_qk_norm_rope_backward")
 
 
 def empty_workspace(nbytes: int, device="cuda") -> torch.Tensor:
