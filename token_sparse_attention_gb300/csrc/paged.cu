@@ -259,114 +259,277 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteA
 }
 
 // ------------------------------------------------------------------ select
+//
+// score(page) = (sum of the group's queries) . mean, and the pages of the
+// largest scores.  Which page is kept must not depend on the order of a sum,
+// so the products are summed in two fp32 words per sum (error-free sums and
+// products of pairs: about 48 bits) and rounded to fp32 once; ties then go to
+// the lower page.  fp64 would give the same but runs at 1/60 of the fp32 rate here.
+// Bound: the means are read once, 2 D bytes per page and KV head.
 
-constexpr int kSelectThreads = 1024;
+constexpr int kScoreThreads = 256;
+constexpr int kTopkKeys = 8;  // consecutive keys per thread and step
 
-// One warp per page: the score in 64 bits, rounded to fp32 once.
-__global__ void __launch_bounds__(256) paged_score_kernel(const SelectArgs a) {
-  const int bh = blockIdx.y, b = bh / a.Hkv, h = bh % a.Hkv;
+// Two independent sums (x and y halves of the pairs), each as hi + lo.
+struct Sum2 {
+  uint64_t hi, lo;
+};
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+  return f2_fma(b, f2_pack(-1.f, -1.f), a);
+}
+// s + x: hi takes the rounded sum, lo what it lost (Knuth's two-sum).
+__device__ __forceinline__ void two_add(Sum2& s, uint64_t x) {
+  const uint64_t sum = f2_add(s.hi, x), bb = f2_sub(sum, s.hi);
+  const uint64_t err = f2_add(f2_sub(s.hi, f2_sub(sum, bb)), f2_sub(x, bb));
+  s.hi = sum;
+  s.lo = f2_add(s.lo, err);
+}
+__device__ __forceinline__ void two_add(float& hi, float& lo, float x, float xl) {
+  const float sum = __fadd_rn(hi, x), bb = __fsub_rn(sum, hi);
+  const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, bb)), __fsub_rn(x, bb));
+  hi = sum;
+  lo = __fadd_rn(__fadd_rn(lo, xl), err);
+}
+
+// A block takes ROWS = 256 / D KV heads of one sequence and 8 * per_warp of its
+// pages.  D/8 lanes hold a head, 8 values each; a warp sums four pages at a
+// time and folds them over the lanes, so that each fold halves what is left.
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads)
+    paged_score_kernel(const SelectArgs a, int head_blocks, int page_blocks, int per_warp, int stride) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES;
+  __shared__ float s_hi[ROWS * D], s_lo[ROWS * D];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int xp = blockIdx.x % page_blocks, hb = blockIdx.x / page_blocks % head_blocks;
+  const int b = blockIdx.x / page_blocks / head_blocks;
   const int len = a.lens[b];
-  if (len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_pages) * a.page) return;
-  const int n = (len + a.page - 1) / a.page;
-  const int group = a.Hq / a.Hkv, lane = lane_id();
-  for (int j = blockIdx.x * 8 + warp_id(); j < n; j += gridDim.x * 8) {
-    uint32_t key;
-    const int pid = a.table[static_cast<size_t>(b) * a.max_pages + j];
-    if (pid < 0 || pid >= a.num_pages) {
-      if (lane == 0) atomicOr(a.status, DEV_BOUNDS);
-      key = 0;  // last of all; the attention skips it too
-    } else if (j < a.sink || j >= n - a.recent) {
-      key = 0xFFFFFFFFu;
-    } else {
-      double s = 0;
-      for (int d = lane; d < a.D; d += 32) {
-        double qs = 0;
-        for (int g = 0; g < group; ++g)
-          qs += static_cast<double>(__bfloat162float(
-              a.q[static_cast<size_t>(b) * a.q_stride + static_cast<size_t>(h * group + g) * a.D + d]));
-        s += qs * static_cast<double>(
-                      __bfloat162float(a.k_mean[(static_cast<size_t>(pid) * a.Hkv + h) * a.D + d]));
+  if (len <= 0 || static_cast<long long>(len) > static_cast<long long>(a.max_pages) * a.page) return;
+  const int n = (len - 1) / a.page + 1;
+  const int j0 = (xp * (kScoreThreads / 32) + warp_id()) * per_warp;
+  if (xp * (kScoreThreads / 32) * per_warp >= n) return;
+  const int group = a.Hq / a.Hkv;
+  {  // the group's summed query, one value per thread
+    const int r = threadIdx.x / D, d = threadIdx.x % D, h = min(hb * ROWS + r, a.Hkv - 1);
+    const __nv_bfloat16* q = a.q + b * a.q_stride + static_cast<size_t>(h) * group * D + d;
+    float hi = 0.f, lo = 0.f;
+    for (int i = 0; i < group; ++i) two_add(hi, lo, __bfloat162float(q[i * D]), 0.f);
+    const float sum = __fadd_rn(hi, lo);
+    s_hi[threadIdx.x] = sum;
+    s_lo[threadIdx.x] = __fsub_rn(lo, __fsub_rn(sum, hi));
+  }
+  __syncthreads();
+  const int lane = lane_id(), l = lane % LANES, h = hb * ROWS + lane / LANES;
+  uint64_t qh[4], ql[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = lane / LANES * D + 8 * l + 2 * i;
+    qh[i] = f2_pack(s_hi[at], s_hi[at + 1]);
+    ql[i] = f2_pack(s_lo[at], s_lo[at + 1]);
+  }
+  const __nv_bfloat16* mean = a.k_mean + static_cast<size_t>(min(h, a.Hkv - 1)) * D + 8 * l;
+  const size_t page_step = static_cast<size_t>(a.Hkv) * D;
+  uint32_t* keys = a.keys + (static_cast<size_t>(b) * a.Hkv + h) * stride;
+  const int j1 = min(n, j0 + per_warp);
+  if (j0 >= j1) return;
+  // per_warp <= 32: a page number per lane
+  int pid = 0;
+  bool outside = false;
+  if (j0 + lane < j1) {
+    pid = a.table[static_cast<size_t>(b) * a.max_pages + j0 + lane];
+    outside = pid < 0 || pid >= a.num_pages;
+    if (outside) {
+      atomicOr(a.status, DEV_BOUNDS);
+      pid = 0;
+    }
+  }
+  const uint32_t bad = __ballot_sync(0xffffffffu, outside);
+  for (int j = j0; j < j1; j += 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - j0 + i) * page_step);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {x[4 * half + i].x, x[4 * half + i].y, x[4 * half + i].z,
+                               x[4 * half + i].w};
+        Sum2 s = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint64_t m = f2_pack(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xFFFF0000u));
+          const uint64_t p = f2_fma(qh[c], m, 0);
+          // what the product lost, and the low word's product
+          const uint64_t e = f2_fma(qh[c], m, p ^ 0x8000000080000000ull);
+          two_add(s, p);
+          s.lo = f2_add(s.lo, f2_fma(ql[c], m, e));
+        }
+        float h0, h1, l0, l1;
+        f2_unpack(s.hi, h0, h1);
+        f2_unpack(s.lo, l0, l1);
+        two_add(h0, l0, h1, l1);
+        hi[i] = h0;
+        lo[i] = l0;
+      }
+      // fold over the lanes: the upper half of each group of lanes keeps the
+      // upper half of the pages
+      int o = LANES / 2;
+#pragma unroll
+      for (int keep = 2; keep >= 1; keep /= 2, o /= 2) {
+        const bool upper = l & o;
+#pragma unroll
+        for (int i = 0; i < keep; ++i) {
+          const float sh = upper ? hi[i] : hi[i + keep], sl = upper ? lo[i] : lo[i + keep];
+          hi[i] = upper ? hi[i + keep] : hi[i];
+          lo[i] = upper ? lo[i + keep] : lo[i];
+          const float rh = __shfl_xor_sync(0xffffffffu, sh, o), rl = __shfl_xor_sync(0xffffffffu, sl, o);
+          two_add(hi[i], lo[i], rh, rl);
+        }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      key = score_key_bits(__float_as_uint(static_cast<float>(s)));
+      for (; o > 0; o /= 2) {
+        const float rh = __shfl_xor_sync(0xffffffffu, hi[0], o), rl = __shfl_xor_sync(0xffffffffu, lo[0], o);
+        two_add(hi[0], lo[0], rh, rl);
+      }
+      // lane bits LANES/2 and LANES/4 name the page
+      const int mine = 4 * half + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
+      const int page = j + mine;
+      const int from = __shfl_sync(0xffffffffu, pid, page - j0);
+      if (l % (LANES / 4) == 0 && page < j1 && h < a.Hkv) {
+        float score = __fadd_rn(hi[0], lo[0]);
+        if (!(fabsf(score) <= 3.0e38f)) {
+          // infinities or an overflow in between, where the two-word sum does
+          // not hold: in fp64
+          double sum = 0;
+          for (int d = 0; d < D; ++d) {
+            const int at = lane / LANES * D + d;
+            sum += (static_cast<double>(s_hi[at]) + static_cast<double>(s_lo[at])) *
+                   static_cast<double>(__bfloat162float(a.k_mean[from * page_step + static_cast<size_t>(h) * D + d]));
+          }
+          score = static_cast<float>(sum);
+        }
+        uint32_t key = score_key_bits(__float_as_uint(score));
+        if (page < a.sink || page >= n - a.recent) key = 0xFFFFFFFFu;
+        if ((bad >> (page - j0)) & 1u) key = 0;  // last of all; the attention skips it too
+        keys[page] = key;
+      }
     }
-    if (lane == 0) a.keys[static_cast<size_t>(bh) * a.max_pages + j] = key;
   }
 }
 
-// One block per (sequence, KV head): the select-th largest key by four 8-bit
-// digits, then the kept pages in order.
-__global__ void __launch_bounds__(kSelectThreads) paged_topk_kernel(const SelectArgs a) {
-  const int bh = blockIdx.x, b = bh / a.Hkv, tid = threadIdx.x;
+// One block per (sequence, KV head).  The select-th largest key by four 8-bit
+// digits, counted in a histogram per warp (scores share their leading bits, and
+// one histogram for all would queue every warp at a few counters); then the
+// kept pages in order, each thread with 8 consecutive ones.
+__global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, int stride) {
+  extern __shared__ uint32_t hist[];  // [warps][256]
+  __shared__ uint32_t s_prefix, s_left;
+  __shared__ int s_warp[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int bh = blockIdx.x, b = bh / a.Hkv, tid = threadIdx.x, w = warp_id(), lane = lane_id();
+  const int warps = blockDim.x / 32, step = blockDim.x * kTopkKeys;
   const int len = a.lens[b];
   const bool bad = len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_pages) * a.page;
   if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
-  const int n = bad ? 0 : (len + a.page - 1) / a.page;
+  const int n = bad || len == 0 ? 0 : (len - 1) / a.page + 1;
   const int keep = min(n, a.select);
-  const uint32_t* keys = a.keys + static_cast<size_t>(bh) * a.max_pages;
+  const uint32_t* keys = a.keys + static_cast<size_t>(bh) * stride;
   int32_t* sel = a.sel + static_cast<size_t>(bh) * a.select;
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_digit, s_left;
-  __shared__ int s_warp[2][32], s_out[2];
-  uint32_t prefix = 0, left = keep;
-  if (n > keep) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int j = tid; j < n; j += kSelectThreads) {
-        const uint32_t key = keys[j];
-        if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t above = 0;
-        int d = 255;
-        while (above + hist[d] < left) above += hist[d--];
-        s_digit = d;
-        s_left = left - above;
-      }
-      __syncthreads();
-      prefix = (prefix << 8) | s_digit;
-      left = s_left;
-      __syncthreads();
-    }
+  for (int i = keep + tid; i < a.select; i += blockDim.x) sel[i] = -1;
+  if (n <= keep) {
+    for (int i = tid; i < n; i += blockDim.x) sel[i] = i;
+    return;
   }
-  // keys above `prefix` are kept, and the first `left` that equal it
-  if (tid < 2) s_out[tid] = 0;
-  __syncthreads();
-  for (int j0 = 0; j0 < n; j0 += kSelectThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < n ? keys[j] : 0;
-    const bool all = n <= keep;
-    const bool more = j < n && (all || key > prefix), same = j < n && !all && key == prefix;
-    const uint32_t mb = __ballot_sync(0xffffffffu, more), sb = __ballot_sync(0xffffffffu, same);
-    if (lane_id() == 0) {
-      s_warp[0][warp_id()] = __popc(mb);
-      s_warp[1][warp_id()] = __popc(sb);
+  uint32_t prefix = 0, left = keep;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < warps * 256; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    for (int j = tid * kTopkKeys; j < n; j += step) {
+      uint32_t x[kTopkKeys];
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(keys + j);
+      *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(keys + j + 4);
+#pragma unroll
+      for (int i = 0; i < kTopkKeys; ++i)
+        if (j + i < n && (shift == 24 || (x[i] >> (shift + 8)) == prefix))
+          atomicAdd(&hist[w * 256 + ((x[i] >> shift) & 255u)], 1u);
     }
     __syncthreads();
-    if (warp_id() < 2) {
-      int x = s_warp[warp_id()][lane_id()];
-      const int own = x;
+    for (int d = tid; d < 256; d += blockDim.x) {
+      uint32_t c = 0;
+      for (int i = 0; i < warps; ++i) c += hist[i * 256 + d];
+      hist[d] = c;  // row 0; each column is one thread's
+    }
+    __syncthreads();
+    if (w == 0) {  // lane i: digits 255 - 8 i down to 248 - 8 i
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+      uint32_t upto = sum;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane_id() >= d) x += y;
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
       }
-      s_warp[warp_id()][lane_id()] = x - own + s_out[warp_id()];
-      __syncwarp();
-      if (lane_id() == 31) s_out[warp_id()] += x;
+      uint32_t above = upto - sum;
+      if (above < left && left <= upto) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (above < left && left <= above + c[i]) {
+            s_prefix = (prefix << 8) | (255 - 8 * lane - i);
+            s_left = left - above;
+          }
+          above += c[i];
+        }
+      }
     }
     __syncthreads();
-    const uint32_t below = (1u << lane_id()) - 1u;
-    const int nm = s_warp[0][warp_id()] + __popc(mb & below);
-    const int ns = s_warp[1][warp_id()] + __popc(sb & below);
-    const int taken = min(ns, static_cast<int>(left));
-    if (more || (same && ns < static_cast<int>(left))) sel[nm + (all ? 0 : taken)] = j;
-    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
   }
-  for (int i = keep + tid; i < a.select; i += kSelectThreads) sel[i] = -1;
+  // keys above `prefix` are kept, and the first `left` that equal it
+  int more0 = 0, same0 = 0;
+  for (int base = 0; base < n; base += step) {
+    const int j = base + tid * kTopkKeys;
+    uint32_t x[kTopkKeys] = {};
+    if (j < n) {
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(keys + j);
+      *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(keys + j + 4);
+    }
+    int own = 0;  // kept above in the low half, equal in the high half
+#pragma unroll
+    for (int i = 0; i < kTopkKeys; ++i)
+      if (j + i < n) own += x[i] > prefix ? 1 : (x[i] == prefix ? 0x10000 : 0);
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[w] = upto;
+    __syncthreads();
+    int before = upto - own, all = 0;
+    for (int i = 0; i < warps; ++i) {
+      const int y = s_warp[i];
+      if (i < w) before += y;
+      all += y;
+    }
+    int more = more0 + (before & 0xFFFF), same = same0 + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < kTopkKeys; ++i) {
+      if (j + i >= n) break;
+      if (x[i] > prefix) {
+        sel[more + min(same, static_cast<int>(left))] = j + i;
+        ++more;
+      } else if (x[i] == prefix) {
+        if (same < static_cast<int>(left)) sel[more + same] = j + i;
+        ++same;
+      }
+    }
+    more0 += all & 0xFFFF;
+    same0 += all >> 16;
+  }
 }
 
 }  // namespace
@@ -403,26 +566,41 @@ cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t strea
   return cudaGetLastError();
 }
 
+// Keys of a row: whole 16-byte words for every thread's eight.
+static int key_stride(int max_pages) { return (max_pages + kTopkKeys - 1) / kTopkKeys * kTopkKeys; }
+
 size_t paged_select_workspace_bytes(int B, int Hkv, int max_pages) {
-  return static_cast<size_t>(B) * Hkv * max_pages * sizeof(uint32_t);
+  return static_cast<size_t>(B) * Hkv * key_stride(max_pages) * sizeof(uint32_t);
 }
 
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
-  const int bh = a.B * a.Hkv;
-  const unsigned x = static_cast<unsigned>(std::min((a.max_pages + 63) / 64, 256));
-  // rows of the grid's y axis are limited to 65535
-  for (int b0 = 0; b0 < a.B;) {
-    const int nb = std::min(a.B - b0, std::max(1, 65535 / a.Hkv));
-    SelectArgs c = a;
-    c.q = a.q + static_cast<size_t>(b0) * a.q_stride;
-    c.table = a.table + static_cast<size_t>(b0) * a.max_pages;
-    c.lens = a.lens + b0;
-    c.keys = a.keys + static_cast<size_t>(b0) * a.Hkv * a.max_pages;
-    paged_score_kernel<<<dim3(x, nb * a.Hkv), 256, 0, stream>>>(c);
-    b0 += nb;
-  }
-  paged_topk_kernel<<<bh, kSelectThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int rows = 256 / a.D, head_blocks = (a.Hkv + rows - 1) / rows;
+  const int stride = key_stride(a.max_pages);
+  // 32 pages per warp; fewer where that would leave SMs idle
+  int per_warp = 32;
+  while (per_warp > 8 && static_cast<long long>(a.B) * head_blocks *
+                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 304)
+    per_warp /= 2;
+  const int page_blocks = (a.max_pages + 8 * per_warp - 1) / (8 * per_warp);
+  const unsigned blocks = static_cast<unsigned>(static_cast<long long>(a.B) * head_blocks * page_blocks);
+  if (a.D == 128)
+    paged_score_kernel<128><<<blocks, kScoreThreads, 0, stream>>>(a, head_blocks, page_blocks, per_warp, stride);
+  else
+    paged_score_kernel<64><<<blocks, kScoreThreads, 0, stream>>>(a, head_blocks, page_blocks, per_warp, stride);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int threads = a.max_pages > 4096 ? 1024 : (a.max_pages > 1024 ? 512 : 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.B * a.Hkv);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = threads / 32 * 256 * sizeof(uint32_t);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_topk_kernel, a, stride);
 }
 
 }  // namespace mcs
