@@ -13,13 +13,14 @@
 // scores and weights in registers.
 //
 // Split: the keys of all (sequence, KV head) pairs, in tiles of 8 KB (K and V
-// together), form one list; each of the SMs' CTAs takes an equal share, whatever the
-// lengths are.  Inside a CTA each of the 8 warps takes every eighth tile and
-// has a ring of its own of 3 tiles, filled by 16-byte cp.async: 192 KB per SM
-// in flight, no barrier in the main loop.  At the end of a pair's part the
-// warps join through shared memory; a pair that lies in one CTA is written
-// at once, the parts of the others go to the workspace and a second,
-// programmatically dependent launch joins them in a fixed order.
+// together), form one list, and each warp of the machine takes an equal piece
+// of it whatever the lengths are.  A warp works alone: a ring of 3 tiles of its
+// own, filled by 16-byte cp.async (8 warps per SM: 192 KB in flight), no barrier
+// after the shares are known, so that the latencies of one warp's new sequence
+// (page numbers, queries) hide behind the other warps' loads.  What a warp holds
+// whole it writes at once.  Neighbouring warps' pieces of one segment are joined in
+// shared memory when the CTA is done, what crosses CTAs goes to the workspace, and a
+// second, programmatically dependent launch joins that in the order of the tiles.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -35,8 +36,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kHalfStage = 4096;              // bytes of K (and of V) in a tile
 constexpr int kStageBytes = 2 * kHalfStage;
-constexpr int kMaxCtas = 256;                 // parts in the workspace: two per CTA
-constexpr int kMinTiles = 8;                  // tiles a CTA takes at least: one per warp
+constexpr int kMaxCtas = 192;                 // parts in the workspace: two per warp
+constexpr int kSegCost = 1;                   // what starting a segment costs, in tiles
 constexpr int kHeads = 16;                    // query heads per pass over a KV head
 constexpr int kPidBits = 27;                  // num_pages * page < 2^31, page >= 16
 
@@ -83,10 +84,11 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Workspace: exclusive sums of the sequences' tiles [B + 1], then the parts:
-// (log2 maximum, sum) of 16 rows and 16 rows of D sums each.
-__host__ __device__ constexpr size_t parts_offset() { return ((4096 + 1) * 8 + 255) / 256 * 256; }
-__host__ __device__ constexpr size_t part_floats(int D) { return kHeads * (2 + D); }
+// Workspace: exclusive sums of the sequences' tiles and of the sequences that
+// have any [2 (B + 1)], then the parts: (log2 maximum, sum) of each row and the
+// rows' D sums.
+__host__ __device__ constexpr size_t parts_offset() { return ((4096 + 1) * 16 + 255) / 256 * 256; }
+__host__ __device__ constexpr size_t part_floats(int D, bool wide) { return (wide ? 16 : 8) * (2 + D); }
 
 // Pages are powers of two.
 __device__ __forceinline__ int page_log2(const DecodeArgs& a) { return 31 - __clz(a.page); }
@@ -107,23 +109,25 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
   return (list_rows(a, a.lens[b]) + TK - 1) / TK;
 }
 
-// CTAs that share `total` tiles, and the first tile of CTA c among them.
-__device__ __forceinline__ long long active_ctas(long long total, int ctas) {
-  const long long want = (total + kMinTiles - 1) / kMinTiles;
-  return want < 1 ? 1 : (want < ctas ? want : ctas);
+// The list of all segments (a segment: one sequence, one KV head, up to 16
+// query heads) has tiles + kSegCost positions for each; warp i of `warps` takes
+// positions [i * all / warps, (i + 1) * all / warps) and the tiles that begin there.
+__device__ __forceinline__ long long active_warps(long long all, int ctas) {
+  return min(all, static_cast<long long>(ctas) * kWarps);
 }
 
-// A walk over this CTA's tiles, segment by segment (a segment: one sequence,
-// one KV head, up to 16 query heads).
+// A walk over a warp's share, segment by segment.
 struct Walk {
-  int b, seg;        // sequence, segment inside it
-  int tb;            // tiles of each segment of the sequence
-  int t0, count;     // this CTA's tiles of the current segment: [t0, t0 + count)
-  long long left;    // tiles behind the current segment
+  int b, seg;       // sequence, segment inside it
+  int tb;           // tiles of each segment of the sequence
+  int t0, count;    // the warp's tiles of this segment: [t0, t0 + count)
+  long long left;   // positions from t0 to the end of the share
 };
+// To the next segment; false at the end of the share.
 template <int TK>
 __device__ __forceinline__ bool next_segment(Walk& w, const DecodeArgs& a, int segs) {
-  if (w.left == 0) return false;
+  w.left -= w.tb + kSegCost - w.t0;
+  if (w.left <= 0) return false;
   if (++w.seg == segs) {
     w.seg = 0;
     do {
@@ -132,8 +136,23 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DecodeArgs& a, int s
   }
   w.t0 = 0;
   w.count = static_cast<int>(min(static_cast<long long>(w.tb), w.left));
-  w.left -= w.count;
   return true;
+}
+
+// A thread's values of row r (0: g, 1: g + 8), times f, to their columns.
+template <int D, bool E4M3>
+__device__ __forceinline__ void store_rows(float* to, const float (*o)[4], int r, float f, int t) {
+#pragma unroll
+  for (int c = 0; c < D / 8; c += 2) {
+    if (E4M3) {
+      *reinterpret_cast<float4*>(to + 8 * c + 4 * t) =
+          make_float4(o[c][2 * r] * f, o[c + 1][2 * r] * f, o[c][2 * r + 1] * f, o[c + 1][2 * r + 1] * f);
+    } else {
+      *reinterpret_cast<float2*>(to + 8 * c + 2 * t) = make_float2(o[c][2 * r] * f, o[c][2 * r + 1] * f);
+      *reinterpret_cast<float2*>(to + 8 * c + 8 + 2 * t) =
+          make_float2(o[c + 1][2 * r] * f, o[c + 1][2 * r + 1] * f);
+    }
+  }
 }
 
 // WIDE: more than 8 query heads in a segment.
@@ -142,14 +161,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const DecodeArgs a, int chunks) {
   using G = Geo<D, E4M3>;
   constexpr int RB = G::RB, TK = G::TK, NS = G::NS, CPR = G::CPR, RPI = G::RPI;
-  constexpr int OS = D + 4;                     // row stride of the join buffer
   constexpr float kShift = E4M3 ? 12.f : 0.f;   // weights carry 2^12 so that f16 holds small ones
   extern __shared__ __align__(128) uint8_t smem[];
-  float* s_o = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
-  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
   __shared__ int s_cnt[kWarps][kStages];
-  __shared__ long long s_sum[kWarps], s_off;
-  __shared__ int s_b;
+  __shared__ long long s_sum[kWarps][2], s_off[kWarps], s_share[kWarps][2];
+  __shared__ int s_b[kWarps], s_seg[kWarps];
+  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
 
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
   const int g = lane >> 2, t = lane & 3;
@@ -160,77 +177,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the dependent launch may be set up; it waits for this one to finish
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's share
-  long long total = 0;
-  for (int b = tid; b < a.B; b += kThreads) {
-    const int len = a.lens[b];
-    if (blockIdx.x == 0 && len != 0 && list_rows(a, len) == 0) atomicOr(a.status, DEV_BOUNDS);
-    total += tiles_of<TK>(a, b);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) s_sum[w] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += s_sum[i];
-  __syncthreads();
-  const long long all = total * segs;
-  const long long ctas = active_ctas(all, gridDim.x);
-  if (blockIdx.x > 0 && (blockIdx.x >= ctas || all == 0)) return;
-  const long long lo = blockIdx.x * all / ctas, hi = (blockIdx.x + 1) * all / ctas;
-  long long carry = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const long long own = b < a.B ? tiles_of<TK>(a, b) : 0;
-    long long x = own;
+  // ---- the shares: sums over the sequences' tiles, 256 sequences at a time
+  // (inclusive in x and y; a batch of up to 256 needs one round)
+  long long x = 0, y = 0, own = 0, all_t = 0, all_s = 0;
+  auto scan = [&](int b) {
+    own = b < a.B ? tiles_of<TK>(a, b) : 0;
+    x = own;
+    y = own > 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
+      const long long u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) x += u, y += v;
     }
-    if (lane == 31) s_sum[w] = x;
     __syncthreads();
-    long long chunk = 0;
+    if (lane == 31) s_sum[w][0] = x, s_sum[w][1] = y;
+    __syncthreads();
+    long long sum_t = 0, sum_s = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      if (i < w) x += s_sum[i];
-      chunk += s_sum[i];
+      if (i < w) x += s_sum[i][0], y += s_sum[i][1];
+      sum_t += s_sum[i][0];
+      sum_s += s_sum[i][1];
     }
-    const long long first = (carry + x - own) * segs, end = (carry + x) * segs;
-    if (own > 0 && first <= lo && lo < end) {
-      s_b = b;
-      s_off = lo - first;
+    x += all_t;
+    y += all_s;
+    all_t += sum_t;
+    all_s += sum_s;
+  };
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    scan(b0 + tid);
+    if (blockIdx.x == 0 && b0 + tid < a.B) {
+      prefix[2 * (b0 + tid)] = x - own;
+      prefix[2 * (b0 + tid) + 1] = y - (own > 0);
+      if (own == 0 && a.lens[b0 + tid] != 0) atomicOr(a.status, DEV_BOUNDS);
     }
-    if (blockIdx.x == 0 && b < a.B) prefix[b] = carry + x - own;
-    carry += chunk;
-    __syncthreads();
   }
-  if (blockIdx.x == 0 && tid == 0) prefix[a.B] = total;
-  if (all == 0) return;
+  const long long all = (all_t + all_s * kSegCost) * segs;
+  const long long warps = active_warps(all, gridDim.x);
+  const long long me = static_cast<long long>(blockIdx.x) * kWarps + w;
+  if (tid < 2 * kWarps) {  // starts and ends; an empty share for the warps that are not needed
+    const long long i = static_cast<long long>(blockIdx.x) * kWarps + tid % kWarps;
+    s_share[tid % kWarps][tid / kWarps] = i < warps ? (i + tid / kWarps) * all / warps : -1;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) prefix[2 * a.B] = all_t, prefix[2 * a.B + 1] = all_s;
+  if (a.B > kThreads) all_t = all_s = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    if (a.B > kThreads) scan(b0 + tid);
+    const long long end = (x + y * kSegCost) * segs;
+    const long long first = end - (own + (own > 0) * kSegCost) * segs;
+    if (own > 0) {
+      // each warp's start that falls into this sequence
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const long long at = s_share[i][0];
+        if (first <= at && at < end) {
+          s_b[i] = b0 + tid;
+          s_off[i] = at - first;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (s_share[0][0] < 0 || all == 0) return;  // a CTA without a share
+  const long long lo = s_share[w][0], hi = s_share[w][1];
 
-  Walk here;
-  here.b = s_b;
-  here.tb = tiles_of<TK>(a, here.b);
-  here.seg = static_cast<int>(s_off / here.tb);
-  here.t0 = static_cast<int>(s_off % here.tb);
-  here.count = static_cast<int>(min(static_cast<long long>(here.tb - here.t0), hi - lo));
-  here.left = hi - lo - here.count;
+  Walk here = {};
+  bool busy = lo < hi;  // from here on each warp is alone
+  if (busy) {
+    here.b = s_b[w];
+    here.tb = tiles_of<TK>(a, here.b);
+    here.seg = static_cast<int>(s_off[w] / (here.tb + kSegCost));
+    here.t0 = static_cast<int>(s_off[w] % (here.tb + kSegCost));
+    here.left = hi - lo;
+    here.count = static_cast<int>(min(static_cast<long long>(here.tb - here.t0), here.left));
+    if (here.count <= 0) busy = next_segment<TK>(here, a, segs);
+  }
 
-  // ---- the warp's ring: its tiles of every segment, three ahead
+  // ---- the warp's ring: its tiles, three ahead
   uint8_t* ring = smem + w * (kStages * kStageBytes);
   const uint32_t ring_s = smem_u32(ring);
   Walk ahead = here;
-  int k_next = 0;          // next tile of `ahead` to load: t0 + w + 8 k_next
-  uint32_t found = 0;      // lane i: page and rows of slab i % NS of tile k0 + i / NS
-  bool more = true;
+  int k_next = 0;          // next tile of `ahead` to load: t0 + k_next
+  uint32_t found = 0;      // lane i: page and rows of the i-th 16-key slab from a window's start
+  bool more = busy;
   const int l_row = lane / CPR, l_chunk = lane % CPR;
 
   auto look_up = [&](int k) {
-    const int kk = k + lane / NS;
-    const long long row0 = static_cast<long long>(ahead.t0 + w + kWarps * kk) * TK + lane % NS * 16;
+    const long long row0 = static_cast<long long>(ahead.t0 + k) * TK + lane * 16;
     found = 0;
-    if (w + kWarps * kk >= ahead.count) return;
+    if (k + lane / NS >= ahead.count) return;
     const int len = a.lens[ahead.b];
     if (row0 >= list_rows(a, len)) return;
     const int h = ahead.seg / chunks;
@@ -254,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   auto load_next = [&](int stage) {
-    while (more && w + kWarps * k_next >= ahead.count) {
+    if (more && k_next >= ahead.count) {
       more = next_segment<TK>(ahead, a, segs);
       k_next = 0;
     }
@@ -262,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kWindow = 32 / NS;
       if (k_next % kWindow == 0) look_up(k_next);
       const int h = ahead.seg / chunks;
-      const int row0 = (ahead.t0 + w + kWarps * k_next) * TK & (a.page - 1);
+      const int row0 = (ahead.t0 + k_next) * TK & (a.page - 1);
       const uint32_t dst = ring_s + stage * kStageBytes;
       uint32_t counts = 0;
 #pragma unroll
@@ -302,7 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int NT = D / 8;          // 8-column tiles of the output
   constexpr uint32_t kFull = NS == 1 ? 16u : NS == 2 ? 0x1010u : 0x10101010u;
 
-  while (true) {
+  float o[NT][4];
+  float m[2], l[2];
+  bool goes_on = false;  // the last segment continues in the next warp's share
+
+  while (busy) {
     const int h = here.seg / chunks, q0 = here.seg % chunks * kHeads;
     const int heads = min(kHeads, group - q0);
     const __nv_bfloat16* q = a.q + here.b * a.q_stride + static_cast<size_t>(h * group + q0) * D;
@@ -329,10 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         qa[i][r + 2] = y;
       }
     }
-    float o[NT][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
 
-    for (int k = w; k < here.count; k += kWarps) {
+    for (int k = 0; k < here.count; ++k) {
       cp_async_wait_group<kStages - 1>();
       __syncwarp();
       const uint32_t ks = ring_s + stage * kStageBytes, vs = ks + kHalfStage;
@@ -459,170 +501,244 @@ __global__ void __launch_bounds__(kThreads, 1)
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
-    // ---- join the warps
 #pragma unroll
     for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       m[r] *= a.scale_log2;
-      if (t == 0) {
-        s_m[w][g + 8 * r] = m[r];
-        s_l[w][g + 8 * r] = l[r];
+    }
+    goes_on = here.t0 + here.count < here.tb;
+    if (goes_on) break;
+    // ---- the segment ends here: its rows, or the last part of them
+    float* part = parts + 2 * me * part_floats(D, WIDE);
+#pragma unroll
+    for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
+      const int head = g + 8 * r;
+      if (head >= heads) continue;
+      if (here.t0 == 0) {
+        const float inv = l[r] > 0.f || l[r] != l[r] ? a.v_scale / l[r] : 0.f;
+        const size_t at = static_cast<size_t>(here.b) * a.Hq + h * group + q0 + head;
+        __nv_bfloat16* to = a.out + at * D;
+#pragma unroll
+        for (int c = 0; c < NT; c += 2) {
+          const float x0 = o[c][2 * r] * inv, x1 = o[c][2 * r + 1] * inv;
+          const float y0 = o[c + 1][2 * r] * inv, y1 = o[c + 1][2 * r + 1] * inv;
+          if (E4M3) {
+            *reinterpret_cast<uint2*>(to + 8 * c + 4 * t) = make_uint2(pack_bf16(x0, y0), pack_bf16(x1, y1));
+          } else {
+            *reinterpret_cast<uint32_t*>(to + 8 * c + 2 * t) = pack_bf16(x0, x1);
+            *reinterpret_cast<uint32_t*>(to + 8 * c + 8 + 2 * t) = pack_bf16(y0, y1);
+          }
+        }
+        if (a.lse != nullptr && t == 0)
+          a.lse[at] = l[r] == 0.f ? -INFINITY : (m[r] + (log2f(l[r]) - kShift)) * 0.6931471805599453f;
+      } else {
+        if (t == 0) *reinterpret_cast<float2*>(part + 2 * head) = make_float2(m[r], l[r]);
+        store_rows<D, E4M3>(part + 2 * (WIDE ? 16 : 8) + head * D, o, r, 1.f, t);
       }
     }
-    __syncthreads();
-    const bool whole = here.t0 == 0 && here.count == here.tb;
-    float* part = parts + (2 * static_cast<size_t>(blockIdx.x) + (here.t0 == 0 ? 1 : 0)) * part_floats(D);
+    busy = next_segment<TK>(here, a, segs);
+  }
+
+  // ---- join the warps whose last segment is the same and goes on
+  cp_async_wait_group<0>();
+  if (lane == 0) s_seg[w] = goes_on ? here.b * segs + here.seg : -1;
+  if (goes_on && t == 0) {
+    s_m[w][g] = m[0];
+    s_l[w][g] = l[0];
+    if (WIDE) {
+      s_m[w][g + 8] = m[1];
+      s_l[w][g + 8] = l[1];
+    }
+  }
+  __syncthreads();  // also: every ring is idle, and is the join's buffer from here
+  constexpr int ROWS = WIDE ? 16 : 8, OS = D + 4;
+  float* s_o = reinterpret_cast<float*>(smem);  // [warp][row][OS]
+  if (goes_on) {
 #pragma unroll
     for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
       float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, s_m[i][g + 8 * r]);
-      const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - top);
-      float* to = s_o + (w * 8 + g) * OS;
-      if (f != 0.f) {
-#pragma unroll
-        for (int c = 0; c < NT; c += 2) {
-          if (E4M3) {
-            *reinterpret_cast<float4*>(to + 8 * c + 4 * t) =
-                make_float4(o[c][2 * r] * f, o[c + 1][2 * r] * f, o[c][2 * r + 1] * f,
-                            o[c + 1][2 * r + 1] * f);
-          } else {
-            *reinterpret_cast<float2*>(to + 8 * c + 2 * t) =
-                make_float2(o[c][2 * r] * f, o[c][2 * r + 1] * f);
-            *reinterpret_cast<float2*>(to + 8 * c + 8 + 2 * t) =
-                make_float2(o[c + 1][2 * r] * f, o[c + 1][2 * r + 1] * f);
-          }
-        }
-      }
-      __syncthreads();
-      const int row = tid / (D / 4), col = tid % (D / 4) * 4;  // 8 rows, four columns per thread
-      const int head = row + 8 * r;
-      if (row < 8 && head < heads) {
-        float best = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) best = fmaxf(best, s_m[i][head]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float mi = s_m[i][head];
-          const float fi = mi == -INFINITY ? 0.f : ex2(mi - best);
-          if (fi != 0.f) {  // a warp of no weight has written nothing
-            sum += s_l[i][head] * fi;
-            const float4 x = *reinterpret_cast<const float4*>(s_o + (i * 8 + row) * OS + col);
-            acc.x += x.x;
-            acc.y += x.y;
-            acc.z += x.z;
-            acc.w += x.w;
-          }
-        }
-        if (whole) {
-          const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-          const size_t at = static_cast<size_t>(here.b) * a.Hq + h * group + q0 + head;
-          *reinterpret_cast<uint2*>(a.out + at * D + col) =
-              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-          if (a.lse != nullptr && col == 0)
-            a.lse[at] = sum == 0.f ? -INFINITY : (best + (log2f(sum) - kShift)) * 0.6931471805599453f;
-        } else {
-          if (col == 0) {
-            part[2 * head] = best;
-            part[2 * head + 1] = sum;
-          }
-          *reinterpret_cast<float4*>(part + 2 * kHeads + head * D + col) = acc;
-        }
-      }
-      __syncthreads();
+      for (int i = 0; i < kWarps; ++i)
+        if (s_seg[i] == s_seg[w]) top = fmaxf(top, s_m[i][g + 8 * r]);
+      store_rows<D, E4M3>(s_o + (w * ROWS + g + 8 * r) * OS, o, r, m[r] == -INFINITY ? 0.f : ex2(m[r] - top), t);
     }
-    if (!next_segment<TK>(here, a, segs)) break;
-  }
-  cp_async_wait_group<0>();
-}
-
-// One block per query head: joins the parts of a segment that several CTAs
-// share, in the order of their tiles, and writes the rows of sequences that
-// hold nothing.
-template <int D, int TK>
-__global__ void __launch_bounds__(2 * D) paged_join_kernel(const DecodeArgs a, int chunks, int grid,
-                                                           float shift) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, group = a.Hq / a.Hkv;
-  const int h = hq / group, row = hq % group % kHeads;
-  const int seg = h * chunks + hq % group / kHeads, segs = a.Hkv * chunks;
-  const long long* prefix = static_cast<const long long*>(a.ws);
-  const float* parts =
-      reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
-  const long long p0 = prefix[b], tb = prefix[b + 1] - p0, all = prefix[a.B] * segs;
-  const int col = threadIdx.x % D, side = threadIdx.x / D;
-  if (tb == 0) {
-    if (side == 0) a.out[static_cast<size_t>(blockIdx.x) * D + col] = __float2bfloat16(0.f);
-    if (a.lse != nullptr && threadIdx.x == 0) a.lse[blockIdx.x] = -INFINITY;
-    return;
-  }
-  const long long ctas = active_ctas(all, grid), first = p0 * segs + seg * tb;
-  const int c0 = static_cast<int>(((first + 1) * ctas - 1) / all);
-  const int c1 = static_cast<int>(((first + tb) * ctas - 1) / all);
-  if (c0 == c1) return;
-  // CTA c0 holds the segment's first tile (its second part), the others go on
-  // with it (their first parts); two threads per column take every other part
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
-  for (int c = c0; c <= c1; ++c)
-    top = fmaxf(top, parts[(2 * static_cast<size_t>(c) + (c == c0)) * part_floats(D) + 2 * row]);
-  for (int c = c0 + side; c <= c1; c += 2) {
-    const float* part = parts + (2 * static_cast<size_t>(c) + (c == c0)) * part_floats(D);
-    const float m = part[2 * row];
-    if (m == -INFINITY) continue;
-    const float f = ex2(m - top);
-    sum += part[2 * row + 1] * f;
-    acc += part[2 * kHeads + row * D + col] * f;
-  }
-  __shared__ float s_sum, s_acc[D];
-  if (side == 1) {
-    s_acc[col] = acc;
-    if (col == 0) s_sum = sum;
   }
   __syncthreads();
-  if (side == 0) {
-    sum += s_sum;
-    acc += s_acc[col];
+  for (int first = 0; first < kWarps; ++first) {
+    const int id = s_seg[first];
+    if (id < 0 || (first > 0 && s_seg[first - 1] == id)) continue;
+    float* part = parts + (2 * (static_cast<long long>(blockIdx.x) * kWarps + first) + 1) * part_floats(D, WIDE);
+    for (int e = tid; e < ROWS * D / 4; e += kThreads) {
+      const int row = e / (D / 4), col = e % (D / 4) * 4;
+      float top = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i)
+        if (s_seg[i] == id) top = fmaxf(top, s_m[i][row]);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (s_seg[i] != id) continue;
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (i * ROWS + row) * OS + col);
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        sum += s_m[i][row] == -INFINITY ? 0.f : s_l[i][row] * ex2(s_m[i][row] - top);
+      }
+      if (col == 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(top, sum);
+      *reinterpret_cast<float4*>(part + 2 * ROWS + row * D + col) = acc;
+    }
+  }
+}
+
+constexpr int kJoinThreads = 256;
+static_assert(kMaxCtas + 1 <= kJoinThreads, "a thread takes one part's maximum and sum");
+
+// The share that holds position x: the largest i with i * all < (x + 1) * warps.
+__device__ __forceinline__ int share_of(long long x, long long all, long long warps) {
+  const long long y = (x + 1) * warps;
+  // an estimate that is off by one at most, then exact products
+  int i = static_cast<int>(static_cast<float>(x) * (static_cast<float>(warps) / static_cast<float>(all)));
+  while (i > 0 && i * all >= y) --i;
+  while ((i + 1) * all < y) ++i;
+  return i;
+}
+
+// One block per query head and 1/splits of its columns: joins the parts of a
+// segment that reaches over several CTAs, in the order of its tiles, and
+// writes the rows of sequences that hold nothing.  Latency: the sums, then maxima,
+// sums and values in one go (a thread's first four parts are on their way while
+// the weights are found).
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const DecodeArgs a, int chunks, int grid, bool wide, int splits) {
+  __shared__ float s_f[kJoinThreads];  // weight of each part
+  __shared__ float s_top[kJoinThreads / 32], s_sum[kJoinThreads / 32];
+  __shared__ float4 s_acc[kJoinThreads / 32][32];
+  constexpr float kShift = E4M3 ? 12.f : 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
+  const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * (D / splits);
+  const int b = head / a.Hq, hq = head % a.Hq, group = a.Hq / a.Hkv;
+  const int row = hq % group % kHeads;
+  const int seg = hq / group * chunks + hq % group / kHeads, segs = a.Hkv * chunks;
+  const longlong2* prefix = static_cast<const longlong2*>(a.ws);
+  const float* parts =
+      reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
+  const longlong2 p0 = prefix[b], p1 = prefix[b + 1], end = prefix[a.B];
+  const long long tb = p1.x - p0.x, all = (end.x + end.y * kSegCost) * segs;
+  const int cols = D / splits / 4;  // columns in fours
+  if (tb == 0) {
+    if (tid < cols)
+      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(head) * D + col0 + 4 * tid) = make_uint2(0, 0);
+    if (a.lse != nullptr && col0 == 0 && tid == 0) a.lse[head] = -INFINITY;
+    return;
+  }
+  const long long warps = active_warps(all, grid);
+  const long long first = (p0.x + p0.y * kSegCost) * segs + seg * (tb + kSegCost);
+  const int c0 = share_of(first, all, warps), c1 = share_of(first + tb - 1, all, warps);
+  if (c0 == c1) return;
+  // shares c0 to c1 - 1 go on to the next one and are joined per CTA (the second
+  // part of the CTA's first such warp); share c1 ends the segment (its first part)
+  const size_t size = part_floats(D, wide);
+  const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
+  auto part = [&](int i) {
+    const int warp = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
+    return parts + (2 * static_cast<size_t>(warp) + (i < n - 1)) * size;
+  };
+  // `cols` neighbouring threads take a part, the block 256 / cols parts at a time
+  const int col = tid % cols, side = tid / cols, sides = kJoinThreads / cols;
+  const int at = 2 * (wide ? 16 : 8) + row * D + col0 + 4 * col;
+  float4 x[4];
+  const float2 ml = tid < n ? *reinterpret_cast<const float2*>(part(tid) + 2 * row) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = side + k * sides;
+    if (i < n) x[k] = *reinterpret_cast<const float4*>(part(i) + at);
+  }
+  float top = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_top[w] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, s_top[i]);
+  const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+  s_f[tid] = f;
+  float sum = tid < n ? ml.y * f : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[w] = sum;
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& v, float f) {
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  };
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (side + k * sides < n) add(x[k], s_f[side + k * sides]);
+#pragma unroll 4
+  for (int i = side + 4 * sides; i < n; i += sides) add(*reinterpret_cast<const float4*>(part(i) + at), s_f[i]);
+  for (int o = 16; o >= cols; o >>= 1) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+  }
+  if (lane < cols) s_acc[w][lane] = acc;
+  __syncthreads();
+  if (tid < cols) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) {
+      sum += s_sum[i];
+      if (i > 0) add(s_acc[i][tid], 1.f);
+    }
     const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-    a.out[static_cast<size_t>(blockIdx.x) * D + col] = __float2bfloat16(acc * inv);
-    if (a.lse != nullptr && col == 0)
-      a.lse[blockIdx.x] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - shift)) * 0.6931471805599453f;
+    *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(head) * D + col0 + 4 * tid) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (a.lse != nullptr && col0 == 0 && tid == 0)
+      a.lse[head] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
   }
 }
 
 template <int D, bool E4M3, bool WIDE>
 cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream) {
-  using G = Geo<D, E4M3>;
-  constexpr int kSmem = kWarps * kStages * kStageBytes + kWarps * 8 * (D + 4) * 4;
+  constexpr int kSmem = kWarps * kStages * kStageBytes;
   auto kernel = paged_decode_kernel<D, E4M3, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  // no more CTAs than the longest lists could fill
+  // one CTA per SM, no more than the longest lists could give a tile to
   const long long rows = a.sel != nullptr
                              ? static_cast<long long>(std::min(a.select, a.max_pages)) * a.page
                              : static_cast<long long>(a.max_pages) * a.page;
-  const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + G::TK - 1) / G::TK);
-  const int grid = static_cast<int>(
-      std::min<long long>(std::min(sms, kMaxCtas), (most + kMinTiles - 1) / kMinTiles));
+  constexpr int TK = Geo<D, E4M3>::TK;
+  const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + TK - 1) / TK + kSegCost);
+  const int grid = static_cast<int>(std::min<long long>(std::min(sms, kMaxCtas), most));
   kernel<<<grid, kThreads, kSmem, stream>>>(a, chunks);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // few heads have many parts each: their columns go to several blocks
+  const int splits = a.B * a.Hq <= sms / 4 ? 8 : a.B * a.Hq <= sms ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.B * a.Hq);
-  cfg.blockDim = dim3(2 * D);
+  cfg.gridDim = dim3(a.B * a.Hq * splits);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, G::TK>, a, chunks, grid, E4M3 ? 12.f : 0.f);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, E4M3>, a, chunks, grid, WIDE, splits);
 }
 
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int D) {
-  return parts_offset() + 2 * kMaxCtas * part_floats(D) * sizeof(float);
+size_t paged_decode_workspace_bytes(int D, int group) {
+  return parts_offset() + 2 * kMaxCtas * kWarps * part_floats(D, group > 8) * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream) {

@@ -220,7 +220,7 @@ struct DecodeArgs {
   unsigned* status;
 };
 cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream);
-size_t paged_decode_workspace_bytes(int D);
+size_t paged_decode_workspace_bytes(int D, int group);
 
 // ---------------------------------------------------------------- norm and rotation
 

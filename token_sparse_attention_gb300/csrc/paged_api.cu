@@ -207,7 +207,7 @@ mcs_status mcs_paged_write(const mcs_paged* p, int T, const void* k, const void*
 }
 
 size_t mcs_paged_decode_workspace(const mcs_paged* p) {
-  return check_paged(p) == MCS_OK ? mcs::paged_decode_workspace_bytes(p->D) : 0;
+  return check_paged(p) == MCS_OK ? mcs::paged_decode_workspace_bytes(p->D, p->Hq / p->Hkv) : 0;
 }
 
 mcs_status mcs_paged_decode(const mcs_paged* p, const void* q, const void* k_cache,
