@@ -546,71 +546,106 @@ def mcs_rel_l1(p: Params, got, want, rows=None, stream=None) -> tuple:
 
 # ---------------------------------------------------------------- paged cache
 
+# A decoding step makes these calls for every layer, and their checks stand
+# beside kernels of a few microseconds: each tensor is looked at once, by the
+# cheapest expression that says whether it fits, and only one that does not is
+# taken apart for the message.
+
 def _device(stream) -> int:
-    """The device a call runs on: the stream's, or the current one."""
+    """The device a call runs on: the current one, which the stream must belong to."""
     current = torch.cuda.current_device()
-    if getattr(stream, "device_index", current) != current:
+    if stream is not None and getattr(stream, "device_index", current) != current:
         raise ValueError("stream belongs to another device than the current one")
     return current
 
 
-def _at(dev, t, dtype, shape, name, optional=False):
+def _queue(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _refuse(dev, t, dtype, shape, name):
+    _ptr(t, dtype, shape, name)
+    raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
+
+
+def _at(dev, t, dtype, shape, name):
     """As _ptr, and on device `dev`."""
-    p = _ptr(t, dtype, shape, name, optional)
-    if t is not None and t.device.index != dev:
-        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
-    return p
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and \
+            t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(dev, t, dtype, shape, name)
+
+
+def _maybe_at(dev, t, dtype, shape, name):
+    return None if t is None else _at(dev, t, dtype, shape, name)
+
+
+def _bytes_at(dev, t, name):
+    """(pointer, size) of a workspace."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    return _at(dev, t, torch.uint8, t.shape, name), t.numel()
 
 
 def _rows_at(dev, t, dtype, shape, stride, name):
     """Rows [..., H, D] whose consecutive tokens stand `stride` elements apart (0: H * D)."""
+    if stride == 0 and isinstance(t, torch.Tensor) and t.dtype is dtype and \
+            t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device.index != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
-    want, n = [1, shape[-1]], stride or shape[-1] * shape[-2]
-    for size in reversed(shape[:-2]):
-        want.append(n)
+    want, n = (shape[-1], 1), stride or shape[-1] * shape[-2]
+    for size in shape[-3::-1]:
+        want = (n,) + want
         n *= size
-    if any(size > 1 and have != w for size, have, w in zip(shape, t.stride(), reversed(want))):
-        raise ValueError(f"{name} must have strides {tuple(reversed(want))}, got {t.stride()}")
+    have = t.stride()
+    if have != want and any(x > 1 and h != w for x, h, w in zip(shape, have, want)):
+        raise ValueError(f"{name} must have strides {want}, got {have}")
     return t.data_ptr()
 
 
-def _cache_at(dev, t, p: Paged, name):
-    if p.kv == KV_E4M3 and isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    return _at(dev, t, torch.uint8 if p.kv == KV_E4M3 else torch.bfloat16,
-               (p.num_pages, p.Hkv, p.page, p.D), name)
+def _cache_at(dev, t, kv, shape, name):
+    if kv == KV_E4M3:
+        if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
+            t = t.view(torch.uint8)
+        return _at(dev, t, torch.uint8, shape, name)
+    return _at(dev, t, torch.bfloat16, shape, name)
+
+
+_BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def mcs_paged_plan(p: Paged, new_lens, lens, free_pages, free_head, block_table, lens_out,
                    head_out, cu_new, slots, positions=None, stream=None):
-    dev, i32, T = _device(stream), torch.int32, slots.numel()
+    dev, B, T = _device(stream), (p.B,), slots.numel()
+    one, n_free = (1,), free_pages.numel()
     _check(lib().mcs_paged_plan(
-        ctypes.byref(p), _at(dev, new_lens, i32, (p.B,), "new_lens"),
-        _at(dev, lens, i32, (p.B,), "lens"), _at(dev, free_pages, i32, None, "free_pages"),
-        free_pages.numel(), _at(dev, free_head, i32, (1,), "free_head"),
-        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
-        _at(dev, lens_out, i32, (p.B,), "lens_out"), _at(dev, head_out, i32, (1,), "head_out"),
-        _at(dev, cu_new, i32, (p.B + 1,), "cu_new"), _at(dev, slots, i32, (T,), "slots"),
-        _at(dev, positions, i32, (T,), "positions", optional=True), T, _stream(stream)),
+        ctypes.byref(p), _at(dev, new_lens, _I32, B, "new_lens"), _at(dev, lens, _I32, B, "lens"),
+        _at(dev, free_pages, _I32, (n_free,), "free_pages"), n_free,
+        _at(dev, free_head, _I32, one, "free_head"),
+        _at(dev, block_table, _I32, (p.B, p.max_pages), "block_table"),
+        _at(dev, lens_out, _I32, B, "lens_out"), _at(dev, head_out, _I32, one, "head_out"),
+        _at(dev, cu_new, _I32, (p.B + 1,), "cu_new"), _at(dev, slots, _I32, (T,), "slots"),
+        _maybe_at(dev, positions, _I32, (T,), "positions"), T, _queue(stream, dev)),
         "mcs_paged_plan")
 
 
 def mcs_paged_write(p: Paged, k, v, slots, k_cache, v_cache, k_mean=None, stream=None):
-    dev, bf, T = _device(stream), torch.bfloat16, slots.numel()
+    dev, T, Hkv, D, pages, kv = _device(stream), slots.numel(), p.Hkv, p.D, p.num_pages, p.kv
+    rows, cache, stride = (T, Hkv, D), (pages, Hkv, p.page, D), p.kv_stride
     _check(lib().mcs_paged_write(
-        ctypes.byref(p), T, _rows_at(dev, k, bf, (T, p.Hkv, p.D), p.kv_stride, "k"),
-        _rows_at(dev, v, bf, (T, p.Hkv, p.D), p.kv_stride, "v"),
-        _at(dev, slots, torch.int32, (T,), "slots"), _cache_at(dev, k_cache, p, "k_cache"),
-        _cache_at(dev, v_cache, p, "v_cache"),
-        _at(dev, k_mean, bf, (p.num_pages, p.Hkv, p.D), "k_mean", optional=True),
-        _stream(stream)), "mcs_paged_write")
+        ctypes.byref(p), T, _rows_at(dev, k, _BF, rows, stride, "k"),
+        _rows_at(dev, v, _BF, rows, stride, "v"), _at(dev, slots, _I32, (T,), "slots"),
+        _cache_at(dev, k_cache, kv, cache, "k_cache"),
+        _cache_at(dev, v_cache, kv, cache, "v_cache"),
+        _maybe_at(dev, k_mean, _BF, (pages, Hkv, D), "k_mean"), _queue(stream, dev)),
+        "mcs_paged_write")
 
 
 def mcs_paged_decode_workspace(p: Paged) -> int:
@@ -619,80 +654,85 @@ def mcs_paged_decode_workspace(p: Paged) -> int:
 
 def mcs_paged_decode(p: Paged, q, k_cache, v_cache, block_table, lens, out, ws, lse=None,
                      stream=None):
-    dev, bf, i32 = _device(stream), torch.bfloat16, torch.int32
+    dev, B, Hq, D, kv = _device(stream), p.B, p.Hq, p.D, p.kv
+    cache, rows = (p.num_pages, p.Hkv, p.page, D), (B, Hq, D)
     _check(lib().mcs_paged_decode(
-        ctypes.byref(p), _rows_at(dev, q, bf, (p.B, p.Hq, p.D), p.q_stride, "q"),
-        _cache_at(dev, k_cache, p, "k_cache"), _cache_at(dev, v_cache, p, "v_cache"),
-        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
-        _at(dev, lens, i32, (p.B,), "lens"), _at(dev, out, bf, (p.B, p.Hq, p.D), "out"),
-        _at(dev, lse, torch.float32, (p.B, p.Hq), "lse", optional=True),
-        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)), "mcs_paged_decode")
+        ctypes.byref(p), _rows_at(dev, q, _BF, rows, p.q_stride, "q"),
+        _cache_at(dev, k_cache, kv, cache, "k_cache"),
+        _cache_at(dev, v_cache, kv, cache, "v_cache"),
+        _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
+        _at(dev, lens, _I32, (B,), "lens"), _at(dev, out, _BF, rows, "out"),
+        _maybe_at(dev, lse, _F32, (B, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
+        _queue(stream, dev)), "mcs_paged_decode")
 
 
 def mcs_paged_select_workspace(p: Paged) -> int:
     return lib().mcs_paged_select_workspace(ctypes.byref(p))
 
 
-def _sel_at(dev, sel, p: Paged):
+def _select_of(sel) -> int:
     if not isinstance(sel, torch.Tensor) or sel.dim() != 3:
         raise ValueError("sel must be a [B, Hkv, select] tensor")
-    return _at(dev, sel, torch.int32, (p.B, p.Hkv, sel.shape[2]), "sel")
+    return sel.shape[2]
 
 
 def mcs_paged_select(p: Paged, q, k_mean, block_table, lens, sel, ws, sink=1, recent=1,
                      stream=None):
     """sel [B, Hkv, select]: the last dimension says how many pages are kept."""
-    dev, bf, i32 = _device(stream), torch.bfloat16, torch.int32
-    ps = _sel_at(dev, sel, p)
+    dev, B, Hkv, D, keep = _device(stream), p.B, p.Hkv, p.D, _select_of(sel)
     _check(lib().mcs_paged_select(
-        ctypes.byref(p), _rows_at(dev, q, bf, (p.B, p.Hq, p.D), p.q_stride, "q"),
-        _at(dev, k_mean, bf, (p.num_pages, p.Hkv, p.D), "k_mean"),
-        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
-        _at(dev, lens, i32, (p.B,), "lens"), sel.shape[2], int(sink), int(recent), ps,
-        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)), "mcs_paged_select")
+        ctypes.byref(p), _rows_at(dev, q, _BF, (B, p.Hq, D), p.q_stride, "q"),
+        _at(dev, k_mean, _BF, (p.num_pages, Hkv, D), "k_mean"),
+        _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
+        _at(dev, lens, _I32, (B,), "lens"), keep, sink, recent,
+        _at(dev, sel, _I32, (B, Hkv, keep), "sel"), *_bytes_at(dev, ws, "ws"),
+        _queue(stream, dev)), "mcs_paged_select")
 
 
 def mcs_paged_decode_sparse(p: Paged, q, k_cache, v_cache, block_table, lens, sel, out, ws,
                             lse=None, stream=None):
-    dev, bf, i32 = _device(stream), torch.bfloat16, torch.int32
-    ps = _sel_at(dev, sel, p)
+    dev, B, Hq, Hkv, D, kv = _device(stream), p.B, p.Hq, p.Hkv, p.D, p.kv
+    cache, rows, keep = (p.num_pages, Hkv, p.page, D), (B, Hq, D), _select_of(sel)
     _check(lib().mcs_paged_decode_sparse(
-        ctypes.byref(p), _rows_at(dev, q, bf, (p.B, p.Hq, p.D), p.q_stride, "q"),
-        _cache_at(dev, k_cache, p, "k_cache"), _cache_at(dev, v_cache, p, "v_cache"),
-        _at(dev, block_table, i32, (p.B, p.max_pages), "block_table"),
-        _at(dev, lens, i32, (p.B,), "lens"), ps, sel.shape[2],
-        _at(dev, out, bf, (p.B, p.Hq, p.D), "out"),
-        _at(dev, lse, torch.float32, (p.B, p.Hq), "lse", optional=True),
-        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)),
-        "mcs_paged_decode_sparse")
+        ctypes.byref(p), _rows_at(dev, q, _BF, rows, p.q_stride, "q"),
+        _cache_at(dev, k_cache, kv, cache, "k_cache"),
+        _cache_at(dev, v_cache, kv, cache, "v_cache"),
+        _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
+        _at(dev, lens, _I32, (B,), "lens"), _at(dev, sel, _I32, (B, Hkv, keep), "sel"), keep,
+        _at(dev, out, _BF, rows, "out"), _maybe_at(dev, lse, _F32, (B, Hq), "lse"),
+        *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_paged_decode_sparse")
 
 
 # ---------------------------------------------------------------- norm and rotation
 
-def _rope_out_shape(p: Rope, H):
-    return (p.B, p.N, H, p.D) if p.layout == LAYOUT_BNHD else (p.B, H, p.N, p.D)
-
-
 def _rope_inputs(dev, p: Rope, q, k, wq, wk, cos, sin, positions):
     """Pointers of q, k, wq, wk, cos, sin, positions (k and wk null when Hkv = 0)."""
-    bf, f32, table = torch.bfloat16, torch.float32, (p.table_rows, p.rot // 2)
-    some = p.Hkv > 0
-    return (_rows_at(dev, q, bf, (p.B, p.N, p.Hq, p.D), p.q_stride, "q"),
-            _rows_at(dev, k, bf, (p.B, p.N, p.Hkv, p.D), p.k_stride, "k") if some else None,
-            _at(dev, wq, f32, (p.D,), "wq", optional=True),
-            _at(dev, wk, f32, (p.D,), "wk", optional=True) if some else None,
-            _at(dev, cos, f32, table, "cos") if p.rot else None,
-            _at(dev, sin, f32, table, "sin") if p.rot else None,
-            _at(dev, positions, torch.int32, (p.B, p.N), "positions", optional=True))
+    B, N, Hkv, D, rot = p.B, p.N, p.Hkv, p.D, p.rot
+    table = (p.table_rows, rot // 2)
+    return (_rows_at(dev, q, _BF, (B, N, p.Hq, D), p.q_stride, "q"),
+            _rows_at(dev, k, _BF, (B, N, Hkv, D), p.k_stride, "k") if Hkv else None,
+            _maybe_at(dev, wq, _F32, (D,), "wq"),
+            _maybe_at(dev, wk, _F32, (D,), "wk") if Hkv else None,
+            _at(dev, cos, _F32, table, "cos") if rot else None,
+            _at(dev, sin, _F32, table, "sin") if rot else None,
+            _maybe_at(dev, positions, _I32, (B, N), "positions"))
+
+
+def _rope_outs(dev, p: Rope, q, k, names):
+    """Pointers of the two tensors in the layout of q_out and k_out."""
+    B, N, Hq, Hkv, D = p.B, p.N, p.Hq, p.Hkv, p.D
+    by_token = p.layout == LAYOUT_BNHD
+    return (_at(dev, q, _BF, (B, N, Hq, D) if by_token else (B, Hq, N, D), names[0]),
+            _at(dev, k, _BF, (B, N, Hkv, D) if by_token else (B, Hkv, N, D), names[1])
+            if Hkv else None)
 
 
 def mcs_qk_norm_rope(p: Rope, q, k, wq, wk, cos, sin, positions, q_out, k_out, stream=None):
-    dev, bf = _device(stream), torch.bfloat16
+    dev = _device(stream)
     _check(lib().mcs_qk_norm_rope(
         ctypes.byref(p), *_rope_inputs(dev, p, q, k, wq, wk, cos, sin, positions),
-        _at(dev, q_out, bf, _rope_out_shape(p, p.Hq), "q_out"),
-        _at(dev, k_out, bf, _rope_out_shape(p, p.Hkv), "k_out") if p.Hkv else None,
-        _stream(stream)), "mcs_qk_norm_rope")
+        *_rope_outs(dev, p, q_out, k_out, ("q_out", "k_out")), _queue(stream, dev)),
+        "mcs_qk_norm_rope")
 
 
 def mcs_qk_norm_rope_backward_workspace(p: Rope) -> int:
@@ -701,17 +741,15 @@ def mcs_qk_norm_rope_backward_workspace(p: Rope) -> int:
 
 def mcs_qk_norm_rope_backward(p: Rope, dq_out, dk_out, q, k, wq, wk, cos, sin, positions, dq, dk,
                               dwq, dwk, ws, stream=None):
-    dev, bf, f32, some = _device(stream), torch.bfloat16, torch.float32, p.Hkv > 0
+    dev, Hkv = _device(stream), p.Hkv
     _check(lib().mcs_qk_norm_rope_backward(
-        ctypes.byref(p), _at(dev, dq_out, bf, _rope_out_shape(p, p.Hq), "dq_out"),
-        _at(dev, dk_out, bf, _rope_out_shape(p, p.Hkv), "dk_out") if some else None,
+        ctypes.byref(p), *_rope_outs(dev, p, dq_out, dk_out, ("dq_out", "dk_out")),
         *_rope_inputs(dev, p, q, k, wq, wk, cos, sin, positions),
-        _rows_at(dev, dq, bf, (p.B, p.N, p.Hq, p.D), p.q_stride, "dq"),
-        _rows_at(dev, dk, bf, (p.B, p.N, p.Hkv, p.D), p.k_stride, "dk") if some else None,
-        _at(dev, dwq, f32, (p.D,), "dwq", optional=True),
-        _at(dev, dwk, f32, (p.D,), "dwk", optional=True) if some else None,
-        _at(dev, ws, torch.uint8, None, "ws"), ws.numel(), _stream(stream)),
-        "mcs_qk_norm_rope_backward")
+        _rows_at(dev, dq, _BF, (p.B, p.N, p.Hq, p.D), p.q_stride, "dq"),
+        _rows_at(dev, dk, _BF, (p.B, p.N, Hkv, p.D), p.k_stride, "dk") if Hkv else None,
+        _maybe_at(dev, dwq, _F32, (p.D,), "dwq"),
+        _maybe_at(dev, dwk, _F32, (p.D,), "dwk") if Hkv else None,
+        *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_qk_norm_rope_backward")
 
 
 def empty_workspace(nbytes: int, device="cuda") -> torch.Tensor:
