@@ -468,7 +468,7 @@ enum { MCS_KV_BF16 = 0, MCS_KV_E4M3 = 1 };
  * sequence past max_pages * page, a negative length, a page outside the
  * cache) sets MCS_ERR_BOUNDS in the device status and takes nothing: lens_out =
  * lens, head_out = free_head, block_table stays, cu_new is 0, and slots and
- * positions are -1.  T, n_free >= 0.
+ * positions are -1.  0 <= T, n_free <= 2^30.
  */
 mcs_status mcs_paged_plan(const mcs_paged* p, const int32_t* new_lens, const int32_t* lens,
                           const int32_t* free_pages, int n_free, const int32_t* free_head,

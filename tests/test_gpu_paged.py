@@ -354,6 +354,21 @@ def test_write_matches_oracle(lens, new, Hkv, D, page, stride, e4m3):
     assert eq(k2, c.k) and eq(v2, c.v)
 
 
+@pytest.mark.parametrize("ks,vs", [(KS, VS), (1.0, 3.0), (0.7131, 2.0 ** -20), (2.0 ** -90, 2.0 ** 70),
+                                   (2.0 ** -60, 1.9999999), (1e-38, 3e38)])
+def test_write_rounds_every_value_as_the_quantiser(ks, vs):
+    """All 65536 bf16 patterns, infinities, NaN, zeros of both signs and denormals among them."""
+    x = torch.arange(-32768, 32768, device="cuda", dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    p = mcs.paged(1, 4, 4, 128, 16, 8, 8, kv=mcs.KV_E4M3, k_scale=ks, v_scale=vs)
+    rows = x.view(128, 4, 128)
+    cache = torch.zeros(2, 8, 4, 16, 128, dtype=torch.uint8, device="cuda")
+    mcs.mcs_paged_write(p, rows, rows, _i32(np.arange(128)), cache[0], cache[1])
+    want = torch.empty(65536, dtype=torch.uint8, device="cuda")
+    for got, scale in zip(cache, (ks, vs)):
+        mcs.mcs_quantize_e4m3(x, scale, want)
+        assert torch.equal(got.transpose(1, 2).reshape(-1), want)
+
+
 def test_write_skips_padding_and_slots_past_the_cache():
     p = mcs.paged(1, 1, 1, 64, 16, 4, 4)
     cache, mean = torch.zeros(2, 4, 1, 16, 64, device="cuda").to(torch.bfloat16), None

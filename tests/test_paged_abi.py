@@ -75,6 +75,8 @@ def test_paged_pointers_are_checked(L):
     assert L.mcs_paged_plan(r, *plan[:10], 18, 4, None) == INVALID
     assert L.mcs_paged_plan(r, *plan[:11], -1, None) == INVALID
     assert L.mcs_paged_plan(r, *plan[:3], -1, *plan[4:], None) == INVALID
+    assert L.mcs_paged_plan(r, *plan[:11], (1 << 30) + 1, None) == UNSUPPORTED
+    assert L.mcs_paged_plan(r, *plan[:3], (1 << 30) + 1, *plan[4:], None) == UNSUPPORTED
     assert L.mcs_paged_plan(None, *plan, None) == INVALID
     # write
     write = [16, 16, 16, 16, 16, None]

@@ -177,6 +177,7 @@ struct WriteArgs {
   long long slots_total;     // num_pages * page
   long long stride;          // elements between tokens of k and v
   float k_scale, v_scale;    // E4M3
+  float k_inv, v_inv;        // their reciprocals (set by the launcher)
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
   const int32_t* slots;      // [T]

@@ -1,6 +1,7 @@
 // Paged key-value cache: pages and slots of new tokens, writes into the pages
 // with the pages' mean keys, and the choice of pages by a cheap score.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -14,68 +15,47 @@ namespace {
 //
 // have_b = ceil(len_b / page), need_b = ceil((len_b + new_b) / page) - have_b;
 // with the exclusive sums of new and need every token and every fresh page
-// finds its sequence by a binary search.  A few microseconds of latency and
-// nothing else, so it is one launch: every CTA of one cluster takes the sums
-// over all sequences for itself (B <= 4096: at most four rounds of one block
-// scan, 32 KB from L2), checks everything that can be wrong, and
-// only behind the cluster barrier, when all have read the state, writes its
-// share.  The state can so be updated in place and a request that cannot be
-// met takes nothing.
+// finds its sequence by a binary search.  Latency and nothing else, so it is
+// one launch: every CTA of one cluster takes the sums over all sequences for
+// itself (B <= 4096: at most four rounds of one block scan, 32 KB from L2),
+// checks everything that can be wrong, and only behind the cluster barrier,
+// when all have read the state, writes its share.  The state can so be updated
+// in place, and a request that cannot be met takes nothing.
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxThreads = 1024;
 constexpr int kPlanMaxCluster = 8;
+constexpr int kPlanAtOnce = 4;  // tokens a thread searches side by side
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Inclusive sum over the block of x (all threads call); `sums` holds 32 values.
-__device__ __forceinline__ long long block_scan(long long x, long long* sums) {
-  const int lane = lane_id(), w = warp_id();
+// For each x[k] the last i in [0, n) with first[i] <= x[k] (first ascending, first[0] <= x[k]).
+template <int K>
+__device__ __forceinline__ void owners(const int32_t* first, int n, const int (&x)[K], int (&at)[K]) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) sums[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    long long t = sums[lane];
+  for (int k = 0; k < K; ++k) at[k] = 0;
+  for (int d = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; d > 0; d >>= 1) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, t, d);
-      if (lane >= d) t += y;
-    }
-    sums[lane] = t;
+    for (int k = 0; k < K; ++k)
+      if (at[k] + d < n && first[at[k] + d] <= x[k]) at[k] += d;
   }
-  __syncthreads();
-  if (w > 0) x += sums[w - 1];
-  __syncthreads();
-  return x;
 }
 
-// The last i in [0, n) with first[i] <= x, for ascending first with first[0] <= x.
-__device__ __forceinline__ int owner(const int32_t* first, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a, int ctas) {
+__global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanArgs a, int ctas) {
   extern __shared__ int32_t sm[];
-  int32_t* s_cu = sm;                // [B + 1] exclusive sums of new tokens
-  int32_t* s_base = s_cu + a.B + 1;  // [B + 1] exclusive sums of missing pages
-  int32_t* s_len = s_base + a.B + 1; // [B]
-  __shared__ long long sums[32];
-  const int tid = threadIdx.x;
-  const long long room = static_cast<long long>(a.max_pages) * a.page;
+  int32_t* s_cu = sm;                 // [B + 1] exclusive sums of new tokens
+  int32_t* s_base = s_cu + a.B + 1;   // [B + 1] exclusive sums of missing pages
+  int32_t* s_len = s_base + a.B + 1;  // [B]
+  __shared__ long long sums[32][2];
+  const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
+  const int threads = blockDim.x, warps = threads / 32;
+  const int shift = 31 - __clz(a.page), mask = a.page - 1;
+  const long long room = static_cast<long long>(a.max_pages) << shift;
+  const int head = a.free_head[0];
   long long tokens = 0, pages = 0;
   bool bad = false;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
     long long nw = 0, need = 0;
     if (b < a.B) {
@@ -85,46 +65,53 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
         bad = true;
         nw = 0;
       } else {
-        const int have = (len + a.page - 1) / a.page;
-        need = (len + nw + a.page - 1) / a.page - have;
-        if (nw > 0 && len % a.page != 0) {  // continues in its last page
-          const int pid = a.table[static_cast<size_t>(b) * a.max_pages + len / a.page];
+        need = ((len + nw + mask) >> shift) - ((static_cast<long long>(len) + mask) >> shift);
+        if (nw > 0 && (len & mask) != 0) {  // continues in its last page
+          const int pid = a.table[static_cast<size_t>(b) * a.max_pages + (len >> shift)];
           bad = bad || pid < 0 || pid >= a.num_pages;
         }
       }
       s_len[b] = len;
     }
-    const long long t = block_scan(nw, sums), g = block_scan(need, sums);
+    long long x = nw, y = need;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) x += u, y += v;
+    }
+    if (lane == 31) sums[w][0] = x, sums[w][1] = y;
+    __syncthreads();
+    long long all_x = 0, all_y = 0;
+    for (int i = 0; i < warps; ++i) {
+      if (i < w) x += sums[i][0], y += sums[i][1];
+      all_x += sums[i][0];
+      all_y += sums[i][1];
+    }
     if (b < a.B) {
       // sums beyond T or n_free are refused below, before they are used
-      s_cu[b] = static_cast<int32_t>(tokens + t - nw);
-      s_base[b] = static_cast<int32_t>(pages + g - need);
+      s_cu[b] = static_cast<int32_t>(tokens + x - nw);
+      s_base[b] = static_cast<int32_t>(pages + y - need);
     }
-    if (tid == kPlanThreads - 1) sums[0] = t, sums[1] = g;
-    __syncthreads();
-    tokens += sums[0];
-    pages += sums[1];
+    tokens += all_x;
+    pages += all_y;
     __syncthreads();
   }
-  const int head = a.free_head[0];
   bad = bad || tokens > a.T || head < 0 || head > a.n_free || pages > a.n_free - head;
-  bad = __syncthreads_or(bad);
   if (!bad) {
-    for (int j = tid; j < pages; j += kPlanThreads) {
+    for (int j = tid; j < pages; j += threads) {
       const int pid = a.free_pages[head + j];
       bad = bad || pid < 0 || pid >= a.num_pages;
     }
-    bad = __syncthreads_or(bad);
   }
   if (tid == 0) {
     s_cu[a.B] = static_cast<int32_t>(tokens);
     s_base[a.B] = static_cast<int32_t>(pages);
   }
+  bad = __syncthreads_or(bad);
   // every CTA has read what any CTA is about to write
   if (ctas > 1) cluster_sync();
-  else __syncthreads();
 
-  const int at = blockIdx.x * kPlanThreads + tid, step = ctas * kPlanThreads;
+  const int at = blockIdx.x * threads + tid, step = ctas * threads;
   if (bad) {
     if (at == 0) {
       atomicOr(a.status, DEV_BOUNDS);
@@ -146,40 +133,77 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     if (b < a.B) a.lens_out[b] = s_len[b] + (s_cu[b + 1] - s_cu[b]);
   }
   for (int j = at; j < pages; j += step) {
-    const int b = owner(s_base, a.B, j);
-    const int have = (s_len[b] + a.page - 1) / a.page;
-    a.table[static_cast<size_t>(b) * a.max_pages + have + (j - s_base[b])] = a.free_pages[head + j];
+    const int x[1] = {j};
+    int b[1];
+    owners(s_base, a.B, x, b);
+    const int have = (s_len[b[0]] + mask) >> shift;
+    a.table[static_cast<size_t>(b[0]) * a.max_pages + have + (j - s_base[b[0]])] = a.free_pages[head + j];
   }
-  for (int t = at; t < a.T; t += step) {
-    int slot = -1, pos = -1;
-    if (t < tokens) {
-      const int b = owner(s_cu, a.B, t);
-      pos = s_len[b] + (t - s_cu[b]);
-      const int have = (s_len[b] + a.page - 1) / a.page, j = pos / a.page;
-      const int pid = j < have ? a.table[static_cast<size_t>(b) * a.max_pages + j]
-                               : a.free_pages[head + s_base[b] + (j - have)];
-      slot = pid * a.page + pos % a.page;
+  for (long long t0 = at; t0 < a.T; t0 += static_cast<long long>(kPlanAtOnce) * step) {
+    int t[kPlanAtOnce], b[kPlanAtOnce], pid[kPlanAtOnce], pos[kPlanAtOnce];
+#pragma unroll
+    for (int k = 0; k < kPlanAtOnce; ++k)
+      t[k] = static_cast<int>(min(t0 + static_cast<long long>(k) * step, static_cast<long long>(a.T)));
+    owners(s_cu, a.B, t, b);
+#pragma unroll
+    for (int k = 0; k < kPlanAtOnce; ++k) {
+      pos[k] = pid[k] = -1;
+      if (t[k] >= tokens) continue;
+      pos[k] = s_len[b[k]] + (t[k] - s_cu[b[k]]);
+      // pages the sequence had (its last one, read above), or fresh ones
+      const int have = (s_len[b[k]] + mask) >> shift, j = pos[k] >> shift;
+      pid[k] = j < have ? a.table[static_cast<size_t>(b[k]) * a.max_pages + j]
+                        : a.free_pages[head + s_base[b[k]] + (j - have)];
     }
-    a.slots[t] = slot;
-    if (a.positions) a.positions[t] = pos;
+#pragma unroll
+    for (int k = 0; k < kPlanAtOnce; ++k) {
+      if (t[k] >= a.T) continue;
+      a.slots[t[k]] = pos[k] < 0 ? -1 : (pid[k] << shift) + (pos[k] & mask);
+      if (a.positions) a.positions[t[k]] = pos[k];
+    }
   }
 }
 
 // ------------------------------------------------------------------ write
 
+// x / scale, correctly rounded, from inv = 1 / scale (itself correctly rounded): the
+// product and one exact remainder (Markstein 1990).  For every mantissa of a
+// bf16 x and of the scale this is the fp32 quotient (all 2^30 pairs compared);
+// scales outside [2^-60, 2^60], where remainders could underflow, divide instead.
+// Infinities (and what overflows) and the sign of zero are put back.
+struct Scale {
+  float s, inv;
+  bool fast;
+};
+__device__ __forceinline__ uint64_t quotient2(uint32_t lo, uint32_t hi, const Scale& c) {
+  const float x0 = __uint_as_float(lo), x1 = __uint_as_float(hi);
+  if (!c.fast) return f2_pack(__fdiv_rn(x0, c.s), __fdiv_rn(x1, c.s));
+  const uint64_t x = f2_pack(x0, x1), inv = f2_pack(c.inv, c.inv);
+  const uint64_t q = f2_fma(x, inv, 0x8000000080000000ull);
+  const uint64_t rem = f2_fma(q ^ 0x8000000080000000ull, f2_pack(c.s, c.s), x);
+  float q0, q1, r0, r1;
+  f2_unpack(q, q0, q1);
+  f2_unpack(f2_fma(rem, inv, q), r0, r1);
+  r0 = fabsf(q0) <= 1e30f ? copysignf(r0, x0) : q0;
+  r1 = fabsf(q1) <= 1e30f ? copysignf(r1, x1) : q1;
+  return f2_pack(r0, r1);
+}
+
 // 8 bf16 values (a 16-byte word) -> 8 E4M3 codes of x / scale.
-__device__ __forceinline__ uint2 encode8(uint4 x, float scale) {
+__device__ __forceinline__ uint2 encode8(uint4 x, const Scale& scale) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = f32x2_to_e4m3x2(__fdiv_rn(__uint_as_float(w[i] << 16), scale),
-                           __fdiv_rn(__uint_as_float(w[i] & 0xFFFF0000u), scale));
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(quotient2(w[i] << 16, w[i] & 0xFFFF0000u, scale), lo, hi);
+    c[i] = f32x2_to_e4m3x2(lo, hi);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // sum += the stored values: 8 bf16, or scale * 8 E4M3 codes.
-__device__ __forceinline__ void add8(float* sum, uint4 x) {
+__device__ __forceinline__ void add8(float* sum, uint4 x, float) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -206,56 +230,83 @@ constexpr int kWriteThreads = 256;
 
 // D/8 threads per (token, head) copy its k and v rows.  The threads of the
 // first token of each page's run also take the page's mean: the rows in front
-// of it from the cache, the run's own from k, so that nothing is read that
-// another thread of this launch writes.
-template <bool kE4M3Cache>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteArgs a) {
-  const int lanes = a.D / 8;
-  const long long item =
-      (static_cast<long long>(blockIdx.x) * kWriteThreads + threadIdx.x) / lanes;
-  const int l = threadIdx.x % lanes;
-  if (item >= static_cast<long long>(a.T) * a.Hkv) return;
-  const int t = static_cast<int>(item / a.Hkv), h = static_cast<int>(item % a.Hkv);
+// of it from the cache, the run's own from k (now in L2), so that nothing is
+// read that another thread of this launch writes; eight rows at a time, since
+// one thread's loads are all that hides their latency.
+template <int D, bool kE4M3Cache>
+__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteArgs a, bool fast) {
+  constexpr int LANES = D / 8;
+  const unsigned item = blockIdx.x * (kWriteThreads / LANES) + threadIdx.x / LANES;
+  const int l = threadIdx.x % LANES;
+  const unsigned t = item / static_cast<unsigned>(a.Hkv), h = item - t * a.Hkv;
+  if (t >= static_cast<unsigned>(a.T)) return;
   const int slot = a.slots[t];
   if (slot < 0) return;
   if (slot >= a.slots_total) {
     if (h == 0 && l == 0) atomicOr(a.status, DEV_BOUNDS);
     return;
   }
-  const int page_id = slot / a.page, off = slot % a.page;
+  const Scale ks = {a.k_scale, a.k_inv, fast}, vs = {a.v_scale, a.v_inv, fast};
+  const int off = slot & (a.page - 1), page_id = slot >> (31 - __clz(a.page));
   const size_t page_row = (static_cast<size_t>(page_id) * a.Hkv + h) * a.page;
-  const size_t src = static_cast<size_t>(t) * a.stride + static_cast<size_t>(h) * a.D + 8 * l;
-  const size_t dst = (page_row + off) * a.D + 8 * l;
+  const size_t src = t * a.stride + static_cast<size_t>(h) * D + 8 * l;
+  const size_t dst = (page_row + off) * D + 8 * l;
   const uint4 k = ld_global_nc16(a.k + src), v = ld_global_nc16(a.v + src);
+  const bool mean = a.k_mean != nullptr && (t == 0 || off == 0 || a.slots[t - 1] != slot - 1);
   if (kE4M3Cache) {
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_cache) + dst) = encode8(k, a.k_scale);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_cache) + dst) = encode8(v, a.v_scale);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_cache) + dst) = encode8(k, ks);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_cache) + dst) = encode8(v, vs);
   } else {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_cache) + dst) = k;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + dst) = v;
   }
-  if (a.k_mean == nullptr || (t > 0 && off > 0 && a.slots[t - 1] == slot - 1)) return;
+  if (!mean) return;
+  // the run: how many tokens behind t continue in the page, LANES of them looked at a time
+  const int lane0 = lane_id() / LANES * LANES;
+  const uint32_t mates = ((1u << LANES) - 1u) << lane0;
+  int run = 1;
+  for (const int most = min(a.page - off, a.T - static_cast<int>(t)); run < most;) {
+    const bool next = run + l < most && a.slots[t + run + l] == slot + run + l;
+    const uint32_t no = ~__ballot_sync(mates, next) & mates;
+    const int more = no == 0 ? LANES : __ffs(no) - 1 - lane0;
+    run += more;
+    if (more < LANES) break;
+  }
   float sum[8] = {};
-  for (int r = 0; r < off; ++r) {
-    const size_t row = (page_row + r) * a.D + 8 * l;
-    if (kE4M3Cache)
-      add8(sum, *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k_cache) + row), a.k_scale);
-    else
-      add8(sum, *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k_cache) + row));
+  using Word = typename std::conditional<kE4M3Cache, uint2, uint4>::type;  // 8 stored values
+  const Word* old = reinterpret_cast<const Word*>(
+      static_cast<const uint8_t*>(a.k_cache) + (page_row * D + 8 * l) * (kE4M3Cache ? 1 : 2));
+  for (int r = 0; r < off; r += 8) {
+    Word x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = Word{};
+      if (r + i < off) x[i] = old[(r + i) * LANES];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) add8(sum, x[i], a.k_scale);
   }
-  int n = off;
-  for (int u = t; u < a.T && n < a.page && a.slots[u] == slot + (u - t); ++u, ++n) {
-    const uint4 x = ld_global_nc16(a.k + src + static_cast<size_t>(u - t) * a.stride);
-    if (kE4M3Cache) add8(sum, encode8(x, a.k_scale), a.k_scale);
-    else add8(sum, x);
+  for (int r = 0; r < run; r += 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r + i < run) x[i] = ld_global_nc16(a.k + src + static_cast<size_t>(r + i) * a.stride);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r + i >= run) break;
+      if (kE4M3Cache) add8(sum, encode8(x[i], ks), a.k_scale);
+      else add8(sum, x[i], 1.f);
+    }
   }
-  const float inv = static_cast<float>(n);
+  const float n = static_cast<float>(off + run);
   uint4 m;
-  m.x = pack_bf16(sum[0] / inv, sum[1] / inv);
-  m.y = pack_bf16(sum[2] / inv, sum[3] / inv);
-  m.z = pack_bf16(sum[4] / inv, sum[5] / inv);
-  m.w = pack_bf16(sum[6] / inv, sum[7] / inv);
-  *reinterpret_cast<uint4*>(a.k_mean + (static_cast<size_t>(page_id) * a.Hkv + h) * a.D + 8 * l) = m;
+  m.x = pack_bf16(sum[0] / n, sum[1] / n);
+  m.y = pack_bf16(sum[2] / n, sum[3] / n);
+  m.z = pack_bf16(sum[4] / n, sum[5] / n);
+  m.w = pack_bf16(sum[6] / n, sum[7] / n);
+  *reinterpret_cast<uint4*>(a.k_mean + (static_cast<size_t>(page_id) * a.Hkv + h) * D + 8 * l) = m;
 }
 
 // ------------------------------------------------------------------ select
@@ -536,13 +587,14 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int32_t);
-  // one CTA per 4096 tokens or sequences, up to one cluster
+  // a thread per item up to one CTA of 1024, then a CTA per 4096 up to one cluster
   const long long items = std::max<long long>(a.T, a.B);
+  const int threads = items > 512 ? kPlanMaxThreads : items > 256 ? 512 : 256;
   int ctas = 1;
   while (ctas < kPlanMaxCluster && items > 4096LL * ctas) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -551,18 +603,30 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 49168);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, ctas);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const long long threads = static_cast<long long>(a.T) * a.Hkv * (a.D / 8);
-  const unsigned blocks = static_cast<unsigned>((threads + kWriteThreads - 1) / kWriteThreads);
-  if (e4m3) paged_write_kernel<true><<<blocks, kWriteThreads, 0, stream>>>(a);
-  else paged_write_kernel<false><<<blocks, kWriteThreads, 0, stream>>>(a);
+  const long long items = static_cast<long long>(a.T) * a.Hkv;
+  const int per_block = kWriteThreads / (a.D / 8);
+  const unsigned blocks = static_cast<unsigned>((items + per_block - 1) / per_block);
+  WriteArgs c = a;
+  c.k_inv = e4m3 ? 1.f / a.k_scale : 1.f;
+  c.v_inv = e4m3 ? 1.f / a.v_scale : 1.f;
+  auto middle = [](float s) { return s >= 0x1p-60f && s <= 0x1p60f; };
+  const bool fast = middle(a.k_scale) && middle(a.v_scale);
+  if (a.D == 128) {
+    if (e4m3) paged_write_kernel<128, true><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
+    else paged_write_kernel<128, false><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
+  } else {
+    if (e4m3) paged_write_kernel<64, true><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
+    else paged_write_kernel<64, false><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
+  }
   return cudaGetLastError();
 }
 

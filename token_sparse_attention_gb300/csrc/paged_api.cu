@@ -150,6 +150,7 @@ mcs_status mcs_paged_plan(const mcs_paged* p, const int32_t* new_lens, const int
   mcs_status s = check_paged(p);
   if (s != MCS_OK) return s;
   if (T < 0 || n_free < 0) return MCS_ERR_INVALID_ARG;
+  if (T > (1 << 30) || n_free > (1 << 30)) return MCS_ERR_UNSUPPORTED;
   if (!good_ints(new_lens) || !good_ints(lens) || (n_free > 0 && !good_ints(free_pages)) ||
       !good_ints(free_head) || !good_ints(block_table) || !good_ints(lens_out) ||
       !good_ints(head_out) || !good_ints(cu_new) || (T > 0 && !good_ints(slots)) ||

@@ -4,12 +4,18 @@
 //   r = 1 / sqrt(mean(x^2) + eps), y = x r w,
 //   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
 //
-// D/8 threads hold a row (one head of one token), 8 values each: the mean is a
-// shuffle sum over them, the rotation's partner is in the same thread
-// (interleaved pairs) or rot/16 threads away (split pairs).  A warp keeps one
-// token, so that its angles are loaded once for a chunk of heads, and the warps
-// of a block take consecutive tokens, so that a head's rows of a
-// [B, H, N, D] output are written next to each other.
+// D/8 threads hold a row (one head of one token), 8 values each, as four pairs
+// (a, b) of the rotation: neighbours in memory when interleaved, else four
+// values of each half, so that no value crosses threads and only the mean is a
+// shuffle sum.  Values that are not rotated are pairs of angle 0.  The weights
+// are multiplied into a token's cosines and sines once for the heads a warp
+// takes (8, or 16 at D = 64): y_a' = r (x_a (w_a cos) - x_b (w_b sin)).  Pairs of values go through
+// the packed fp32 instructions.
+//
+// Bound: HBM, 4 bytes per value (6 for the gradients), at about 45 (85)
+// instructions per 512 bytes of a row pair.  The warps of a block take
+// consecutive tokens, so that a head's rows of a [B, H, N, D] output are
+// written next to each other.
 #include <algorithm>
 
 #include "internal.h"
@@ -20,82 +26,129 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = 32 * kRopeWarps;
-constexpr int kRopeHeads = 8;   // heads of one token a warp takes
-constexpr int kGradBlocks = 1024;  // partial sums of the weight gradients
+// Loads in flight per thread and blocks per SM, measured: forward 4 at D = 128 and 8 at
+// D = 64, whose rows are half as long (75600 tokens, 64 heads of D = 64: 84 -> 90 % of
+// copy bandwidth); backward 2 rows of x and dy (32760 tokens, 24 heads of D = 128: 116 us
+// with 4 rows and 3 blocks, 112 with 2 and 3, 109 with 2 and 4; 80 heads of D = 64: 195 us
+// with 2 and 3, 238 with 2 and 4, whose spills cost more than the blocks bring).
+template <int D> struct Tune {
+  static constexpr int STEPS = 512 / D, BLOCKS = D == 128 ? 4 : 3;
+  static constexpr int GRAD_STEPS = 2, GRAD_BLOCKS = D == 128 ? 4 : 3;
+};
+constexpr int kGradBlocks = 1024;  // most partial sums of the weight gradients
 
-// 16 bytes that may be overwritten later by this thread (in-place calls).
-__device__ __forceinline__ uint4 ld_row16(const __nv_bfloat16* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void unpack8(uint4 x, float* f) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                    pack_bf16(f[6], f[7]));
-}
+// Heads of one token a warp takes.
+__host__ __device__ constexpr int heads_per_warp(int D, int steps) { return steps * (256 / D); }
 
-// A thread's angles: cs[i], sn[i] for its values 8l + i (split pairs), or
-// for its pairs i < 4 (interleaved).
-struct Angles {
-  float cs[8], sn[8];
+struct Row {  // 8 bf16 values as loaded: pairs' first and second members
+  uint32_t w[4];
 };
 
-__device__ __forceinline__ void load_angles(Angles& g, const RopeArgs& a, int pos, int l) {
-  if (8 * l >= a.rot) return;
-  const size_t row = static_cast<size_t>(pos) * (a.rot / 2);
-  if (a.interleaved) {
-    *reinterpret_cast<float4*>(g.cs) = *reinterpret_cast<const float4*>(a.cos_table + row + 4 * l);
-    *reinterpret_cast<float4*>(g.sn) = *reinterpret_cast<const float4*>(a.sin_table + row + 4 * l);
+// Where a thread's values lie in a row: 8 consecutive ones (interleaved), or
+// four at `a` and four at `b` (split: thread l < rot/8 holds 4l.. of both
+// halves, the others 8 of the values behind the rotated ones).
+struct Place {
+  int a, b;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Place place_of(int rot, int l) {
+  if (!SPLIT) return {8 * l, 8 * l + 4};
+  const int lanes = rot / 8;
+  if (l < lanes) return {4 * l, rot / 2 + 4 * l};
+  return {8 * l, 8 * l + 4};
+}
+
+// Rows may be overwritten later by the thread that reads them (in-place calls).
+template <bool SPLIT>
+__device__ __forceinline__ Row load_row(const __nv_bfloat16* p, Place at) {
+  Row r;
+  if (SPLIT) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p + at.a) : "memory");
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(r.w[2]), "=r"(r.w[3]) : "l"(p + at.b) : "memory");
   } else {
-    const int i = 8 * l < a.rot / 2 ? 8 * l : 8 * l - a.rot / 2;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(p + at.a)
+                 : "memory");
+  }
+  return r;
+}
+__device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
+  return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+}
+// a[0], a[1]: the pairs' first members, b: the second ones.
+template <bool SPLIT>
+__device__ __forceinline__ void unpack(const Row& r, uint64_t* a, uint64_t* b) {
+  constexpr uint32_t kHi = 0xFFFF0000u;
 #pragma unroll
-    for (int k = 0; k < 8; k += 4) {
-      *reinterpret_cast<float4*>(g.cs + k) =
-          *reinterpret_cast<const float4*>(a.cos_table + row + i + k);
-      *reinterpret_cast<float4*>(g.sn + k) =
-          *reinterpret_cast<const float4*>(a.sin_table + row + i + k);
+  for (int i = 0; i < 2; ++i) {
+    if (SPLIT) {
+      a[i] = two(r.w[i] << 16, r.w[i] & kHi);
+      b[i] = two(r.w[i + 2] << 16, r.w[i + 2] & kHi);
+    } else {
+      a[i] = two(r.w[2 * i] << 16, r.w[2 * i + 1] << 16);
+      b[i] = two(r.w[2 * i] & kHi, r.w[2 * i + 1] & kHi);
     }
   }
 }
-
-// Rotates the row's values (sign = 1) or rotates them back (sign = -1).  All
-// lanes of the warp call.
-template <int LANES>
-__device__ __forceinline__ void rotate(float* y, const Angles& g, const RopeArgs& a, int l,
-                                       float sign) {
-  if (a.rot == 0) return;
-  if (a.interleaved) {
-    if (8 * l < a.rot) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = y[2 * i], q = y[2 * i + 1], s = sign * g.sn[i];
-        y[2 * i] = p * g.cs[i] - q * s;
-        y[2 * i + 1] = q * g.cs[i] + p * s;
-      }
-    }
-    return;
+template <bool SPLIT>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, Place at, const uint64_t* a,
+                                          const uint64_t* b) {
+  float a0, a1, a2, a3, b0, b1, b2, b3;
+  f2_unpack(a[0], a0, a1);
+  f2_unpack(a[1], a2, a3);
+  f2_unpack(b[0], b0, b1);
+  f2_unpack(b[1], b2, b3);
+  if (SPLIT) {
+    *reinterpret_cast<uint2*>(p + at.a) = make_uint2(pack_bf16(a0, a1), pack_bf16(a2, a3));
+    *reinterpret_cast<uint2*>(p + at.b) = make_uint2(pack_bf16(b0, b1), pack_bf16(b2, b3));
+  } else {
+    *reinterpret_cast<uint4*>(p + at.a) =
+        make_uint4(pack_bf16(a0, b0), pack_bf16(a1, b1), pack_bf16(a2, b2), pack_bf16(a3, b3));
   }
-  const int half = a.rot / 16;  // threads that hold the first halves
-  const bool first = l < half;
-  const int from = l < half ? l + half : (l < 2 * half ? l - half : l);
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float f2_sum(uint64_t a) {
+  float x, y;
+  f2_unpack(a, x, y);
+  return x + y;
+}
+
+// Cosines and sines of the thread's pairs (1 and 0 where nothing is rotated).
+__device__ __forceinline__ void load_angles(const RopeArgs& a, int pos, int l, uint64_t* cs,
+                                            uint64_t* sn) {
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (8 * l < a.rot) {
+    const size_t at = static_cast<size_t>(pos) * (a.rot / 2) + 4 * l;
+    c = *reinterpret_cast<const float4*>(a.cos_table + at);
+    s = *reinterpret_cast<const float4*>(a.sin_table + at);
+  }
+  cs[0] = f2_pack(c.x, c.y);
+  cs[1] = f2_pack(c.z, c.w);
+  sn[0] = f2_pack(s.x, s.y);
+  sn[1] = f2_pack(s.z, s.w);
+}
+// The thread's weights, as the pairs' members.
+template <bool SPLIT>
+__device__ __forceinline__ void load_weights(const float* w, Place at, uint64_t* a, uint64_t* b) {
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float other = __shfl_sync(0xffffffffu, y[i], from, LANES);
-    if (8 * l < a.rot) {
-      const float s = sign * g.sn[i];
-      y[i] = y[i] * g.cs[i] + (first ? -other : other) * s;
-    }
+  for (int i = 0; i < 4; ++i) {
+    x[i] = w ? w[at.a + i] : 1.f;
+    x[i + 4] = w ? w[at.b + i] : 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a[i] = SPLIT ? f2_pack(x[2 * i], x[2 * i + 1]) : f2_pack(x[4 * i], x[4 * i + 2]);
+    b[i] = SPLIT ? f2_pack(x[4 + 2 * i], x[5 + 2 * i]) : f2_pack(x[4 * i + 1], x[4 * i + 3]);
   }
 }
 
@@ -106,153 +159,256 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The token's position, or -1 where its rows stay as they are.
-__device__ __forceinline__ int position_of(const RopeArgs& a, long long token) {
-  const int pos = a.positions ? a.positions[token] : static_cast<int>(token % a.N);
-  if (a.rot > 0 && pos >= a.table_rows) {
+// A token (below 2^31): its batch entry and place in it, and its position, or
+// -1 where its rows stay as they are.
+struct Token {
+  int b, n, pos;
+};
+__device__ __forceinline__ Token token_of(const RopeArgs& a, unsigned token) {
+  Token t;
+  t.b = static_cast<int>(token / static_cast<unsigned>(a.N));
+  t.n = static_cast<int>(token - static_cast<unsigned>(t.b) * a.N);
+  t.pos = a.positions ? a.positions[token] : t.n;
+  if (a.rot > 0 && t.pos >= a.table_rows) {
     atomicOr(a.status, DEV_BOUNDS);
-    return -1;
+    t.pos = -1;
   }
-  return pos;
+  return t;
+}
+// Head 0 of the token in the [B, H, N, D] or [B, N, H, D] tensors, and the step to the next head.
+__device__ __forceinline__ size_t out_base(const RopeArgs& a, const Token& t, int H, size_t* step) {
+  const bool by_token = a.layout == MCS_LAYOUT_BNHD;
+  *step = by_token ? a.D : static_cast<size_t>(a.N) * a.D;
+  return by_token ? (static_cast<size_t>(t.b) * a.N + t.n) * H * a.D
+                  : (static_cast<size_t>(t.b) * H * a.N + t.n) * a.D;
 }
 
-// Offset of (token, head h of H) in the [B, H, N, D] or [B, N, H, D] tensors.
-__device__ __forceinline__ size_t out_row(const RopeArgs& a, long long token, int h, int H) {
-  if (a.layout == MCS_LAYOUT_BNHD) return (static_cast<size_t>(token) * H + h) * a.D;
-  const long long b = token / a.N, n = token % a.N;
-  return ((static_cast<size_t>(b) * H + h) * a.N + n) * a.D;
-}
-
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs a, int chunks_q,
-                                                                 int chunks) {
-  constexpr int LANES = D / 8, ROWS = 32 / LANES;  // rows a warp holds at a time
-  const int chunk = blockIdx.x % chunks;
-  const long long token =
-      static_cast<long long>(blockIdx.x / chunks) * kRopeWarps + warp_id();
-  if (token >= static_cast<long long>(a.B) * a.N) return;
-  const int pos = position_of(a, token);
-  if (pos < 0) return;
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kRopeThreads, Tune<D>::BLOCKS)
+    norm_rope_kernel(const RopeArgs a, int chunks_q, int chunks) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::STEPS;  // ROWS: rows per load
+  const unsigned tile = blockIdx.x / static_cast<unsigned>(chunks);
+  const int chunk = static_cast<int>(blockIdx.x - tile * chunks);
+  const unsigned token = tile * kRopeWarps + warp_id();
+  if (token >= static_cast<unsigned>(a.B) * a.N) return;
+  const Token t = token_of(a, token);
+  if (t.pos < 0) return;
   const bool is_q = chunk < chunks_q;
-  const int H = is_q ? a.Hq : a.Hkv, h0 = (is_q ? chunk : chunk - chunks_q) * kRopeHeads;
-  const int l = lane_id() % LANES, r = lane_id() / LANES;
-  const __nv_bfloat16* src = (is_q ? a.q : a.k) + token * (is_q ? a.q_stride : a.k_stride);
-  __nv_bfloat16* dst = is_q ? a.q_out : a.k_out;
-  const float* wp = is_q ? a.wq : a.wk;
-  uint4 x[kRopeHeads / ROWS];
+  const int H = is_q ? a.Hq : a.Hkv;
+  const int l = lane_id() % LANES, h0 = (is_q ? chunk : chunk - chunks_q) * heads_per_warp(D, Tune<D>::STEPS) + lane_id() / LANES;
+  const Place at = place_of<SPLIT>(a.rot, l);
+  const __nv_bfloat16* src = (is_q ? a.q : a.k) + token * (is_q ? a.q_stride : a.k_stride) + h0 * D;
+  Row x[STEPS];
 #pragma unroll
-  for (int i = 0; i < kRopeHeads / ROWS; ++i) {
-    const int h = h0 + i * ROWS + r;
-    x[i] = h < H ? ld_row16(src + h * D + 8 * l) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < STEPS; ++i) {
+    x[i] = Row{{0, 0, 0, 0}};
+    if (h0 + i * ROWS < H) x[i] = load_row<SPLIT>(src + i * ROWS * D, at);
   }
-  Angles g;
-  load_angles(g, a, pos, l);
-  float w[8];
+  uint64_t ac[2], as[2], bc[2], bs[2];
+  {
+    uint64_t cs[2], sn[2], wa[2], wb[2];
+    load_angles(a, t.pos, l, cs, sn);
+    load_weights<SPLIT>(is_q ? a.wq : a.wk, at, wa, wb);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = wp ? wp[8 * l + i] : 1.f;
+    for (int i = 0; i < 2; ++i) {
+      ac[i] = f2_mul(wa[i], cs[i]);
+      as[i] = f2_mul(wa[i], sn[i]);
+      bc[i] = f2_mul(wb[i], cs[i]);
+      bs[i] = f2_neg(f2_mul(wb[i], sn[i]));
+    }
+  }
+  size_t step;
+  __nv_bfloat16* dst = (is_q ? a.q_out : a.k_out) + out_base(a, t, H, &step);
 #pragma unroll
-  for (int i = 0; i < kRopeHeads / ROWS; ++i) {
-    float y[8], ss = 0;
-    unpack8(x[i], y);
+  for (int i = 0; i < STEPS; ++i) {
+    uint64_t p[2], q[2], u[2], v[2];
+    unpack<SPLIT>(x[i], p, q);
+    uint64_t ss = f2_mul(p[0], p[0]);
+    ss = f2_fma(p[1], p[1], ss);
+    ss = f2_fma(q[0], q[0], ss);
+    ss = f2_fma(q[1], q[1], ss);
+    const float r = rsqrtf(row_sum<LANES>(f2_sum(ss)) * (1.f / D) + a.eps);
+    const uint64_t rr = f2_pack(r, r);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(y[k], y[k], ss);
-    const float rr = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = y[k] * rr * w[k];
-    rotate<LANES>(y, g, a, l, 1.f);
-    const int h = h0 + i * ROWS + r;
-    if (h < H) *reinterpret_cast<uint4*>(dst + out_row(a, token, h, H) + 8 * l) = pack8(y);
+    for (int k = 0; k < 2; ++k) {
+      u[k] = f2_mul(f2_fma(p[k], ac[k], f2_mul(q[k], bs[k])), rr);
+      v[k] = f2_mul(f2_fma(q[k], bc[k], f2_mul(p[k], as[k])), rr);
+    }
+    const int h = h0 + i * ROWS;
+    if (h < H) store_row<SPLIT>(dst + h * step, at, u, v);
   }
 }
 
-// Backward: units of (8 tokens, 8 heads) as above; a block takes every
-// gridDim-th unit of q (blocks below blocks_q) or of k and keeps the weight
-// gradient of its units in registers, one partial row per block at the end.
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads)
+// Backward: units of 8 tokens and a warp's heads as above; a block takes every
+// blocks_q-th unit of q (or blocks_k-th of k) and keeps the weight gradient of
+// its units in registers, one partial row per block at the end.
+//   g = dy rotated back, dx = r (w g - x r^2 mean(w g x)), dw += g x r
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
     norm_rope_backward_kernel(const RopeArgs a, int blocks_q, int blocks_k) {
-  constexpr int LANES = D / 8, ROWS = 32 / LANES;
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::GRAD_STEPS;
   const bool is_q = static_cast<int>(blockIdx.x) < blocks_q;
-  const int H = is_q ? a.Hq : a.Hkv, chunks = (H + kRopeHeads - 1) / kRopeHeads;
-  const int block = is_q ? blockIdx.x : blockIdx.x - blocks_q, blocks = is_q ? blocks_q : blocks_k;
-  const long long tokens = static_cast<long long>(a.B) * a.N;
-  const long long units = (tokens + kRopeWarps - 1) / kRopeWarps * chunks;
-  const int l = lane_id() % LANES, r = lane_id() / LANES;
-  const __nv_bfloat16* xs = is_q ? a.q : a.k;
+  const int H = is_q ? a.Hq : a.Hkv;
+  const unsigned chunks = (H + heads_per_warp(D, Tune<D>::GRAD_STEPS) - 1) / heads_per_warp(D, Tune<D>::GRAD_STEPS);
+  const unsigned block = is_q ? blockIdx.x : blockIdx.x - blocks_q, blocks = is_q ? blocks_q : blocks_k;
+  const unsigned tokens = static_cast<unsigned>(a.B) * a.N;
+  const unsigned units = (tokens + kRopeWarps - 1) / kRopeWarps * chunks;
+  const int l = lane_id() % LANES, r0 = lane_id() / LANES;
+  const Place at = place_of<SPLIT>(a.rot, l);
   const __nv_bfloat16* dys = is_q ? a.dq_out : a.dk_out;
-  __nv_bfloat16* dxs = is_q ? a.q_out : a.k_out;
   const long long stride = is_q ? a.q_stride : a.k_stride;
-  const float* wp = is_q ? a.wq : a.wk;
-  float w[8], dw[8] = {};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = wp ? wp[8 * l + i] : 1.f;
-  for (long long u = block; u < units; u += blocks) {
-    const long long token = u / chunks * kRopeWarps + warp_id();
-    const int h0 = static_cast<int>(u % chunks) * kRopeHeads;
+  uint64_t wa[2], wb[2], da[2] = {0, 0}, db[2] = {0, 0};
+  load_weights<SPLIT>(is_q ? a.wq : a.wk, at, wa, wb);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (unsigned u = block; u < units; u += blocks) {
+    const unsigned tile = u / chunks, token = tile * kRopeWarps + warp_id();
     if (token >= tokens) continue;  // whole warps
-    const int pos = position_of(a, token);
-    if (pos < 0) continue;
-    uint4 x[kRopeHeads / ROWS], dy[kRopeHeads / ROWS];
+    const Token t = token_of(a, token);
+    if (t.pos < 0) continue;
+    const int h0 = static_cast<int>(u - tile * chunks) * heads_per_warp(D, Tune<D>::GRAD_STEPS) + r0;
+    const size_t row = token * stride + h0 * D;
+    const __nv_bfloat16* xs = (is_q ? a.q : a.k) + row;
+    __nv_bfloat16* dxs = (is_q ? a.q_out : a.k_out) + row;
+    size_t step;
+    const __nv_bfloat16* dy = dys + out_base(a, t, H, &step);
+    Row x[STEPS], y[STEPS];
 #pragma unroll
-    for (int i = 0; i < kRopeHeads / ROWS; ++i) {
-      const int h = h0 + i * ROWS + r;
-      x[i] = h < H ? ld_row16(xs + token * stride + h * D + 8 * l) : make_uint4(0, 0, 0, 0);
-      dy[i] = h < H ? ld_row16(dys + out_row(a, token, h, H) + 8 * l) : make_uint4(0, 0, 0, 0);
-    }
-    Angles ang;
-    load_angles(ang, a, pos, l);
-#pragma unroll
-    for (int i = 0; i < kRopeHeads / ROWS; ++i) {
-      float xh[8], g[8], ss = 0, dot = 0;
-      unpack8(x[i], xh);
-      unpack8(dy[i], g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(xh[k], xh[k], ss);
-      const float rr = rsqrtf(row_sum<LANES>(ss) * (1.f / D) + a.eps);
-      rotate<LANES>(g, ang, a, l, -1.f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        xh[k] *= rr;
-        dw[k] = fmaf(g[k], xh[k], dw[k]);
-        g[k] *= w[k];
-        dot = fmaf(g[k], xh[k], dot);
+    for (int i = 0; i < STEPS; ++i) {
+      const int h = h0 + i * ROWS;
+      x[i] = y[i] = Row{{0, 0, 0, 0}};
+      if (h < H) {
+        x[i] = load_row<SPLIT>(xs + i * ROWS * D, at);
+        y[i] = load_row<SPLIT>(dy + h * step, at);
       }
-      dot = row_sum<LANES>(dot) * (1.f / D);
+    }
+    uint64_t cs[2], sn[2];
+    load_angles(a, t.pos, l, cs, sn);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = rr * (g[k] - xh[k] * dot);
-      const int h = h0 + i * ROWS + r;
-      if (h < H) *reinterpret_cast<uint4*>(dxs + token * stride + h * D + 8 * l) = pack8(g);
+    for (int i = 0; i < STEPS; ++i) {
+      uint64_t p[2], q[2], c[2], d[2], g[2], f[2];
+      unpack<SPLIT>(x[i], p, q);
+      unpack<SPLIT>(y[i], c, d);
+      uint64_t ss = 0, dot = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
+        g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
+        f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
+        c[k] = f2_mul(g[k], wa[k]);
+        d[k] = f2_mul(f[k], wb[k]);
+        dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
+      }
+      float s1 = f2_sum(ss), s2 = f2_sum(dot);
+      s1 = row_sum<LANES>(s1);
+      s2 = row_sum<LANES>(s2);
+      const float r = rsqrtf(s1 * (1.f / D) + a.eps), m = -(s2 * (1.f / D)) * r * r;
+      const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
+        db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
+        c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
+        d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
+      }
+      if (h0 + i * ROWS < H) store_row<SPLIT>(dxs + i * ROWS * D, at, c, d);
     }
   }
   __shared__ float part[kRopeWarps * ROWS][D];
+  float s[8];
+  f2_unpack(da[0], s[0], s[1]);
+  f2_unpack(da[1], s[2], s[3]);
+  f2_unpack(db[0], s[4], s[5]);
+  f2_unpack(db[1], s[6], s[7]);
+  float* to = part[warp_id() * ROWS + r0];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) part[warp_id() * ROWS + r][8 * l + k] = dw[k];
+  for (int k = 0; k < 4; ++k) {
+    to[SPLIT ? at.a + k : at.a + 2 * k] = s[k];
+    to[SPLIT ? at.b + k : at.a + 2 * k + 1] = s[4 + k];
+  }
   __syncthreads();
   if (threadIdx.x < D) {
-    float s = 0;
-    for (int i = 0; i < kRopeWarps * ROWS; ++i) s += part[i][threadIdx.x];
-    a.ws[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = s;
+    float sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRopeWarps * ROWS; ++i) sum += part[i][threadIdx.x];
+    a.ws[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = sum;
   }
 }
 
-// dw = sum of the partial rows [first, first + n), block 0 for q, 1 for k.
+// dw = sum of the partial rows in a fixed order, block 0 for q, 1 for k.
 template <int D>
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int blocks_q,
                                                            int blocks_k) {
+  constexpr int COLS = D / 4, SIDES = 1024 / COLS;
+  __shared__ float4 sums[SIDES][COLS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool is_q = blockIdx.x == 0;
   float* out = is_q ? a.dwq : a.dwk;
   if (out == nullptr) return;
   const int first = is_q ? 0 : blocks_q, n = is_q ? blocks_q : blocks_k;
-  const int d = threadIdx.x % D, part = threadIdx.x / D, parts = 1024 / D;
-  float s = 0;
-  for (int i = part; i < n; i += parts) s += a.ws[static_cast<size_t>(first + i) * D + d];
-  __shared__ float sums[1024];
-  sums[threadIdx.x] = s;
+  const int col = threadIdx.x % COLS, side = threadIdx.x / COLS;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& x) {
+    s.x += x.x;
+    s.y += x.y;
+    s.z += x.z;
+    s.w += x.w;
+  };
+#pragma unroll 8
+  for (int i = side; i < n; i += SIDES)
+    add(*reinterpret_cast<const float4*>(a.ws + static_cast<size_t>(first + i) * D + 4 * col));
+  sums[side][col] = s;
   __syncthreads();
-  if (part == 0) {
-    for (int i = 1; i < parts; ++i) s += sums[i * D + d];
-    out[d] = s;
+  for (int half = SIDES / 2; half > 0; half /= 2) {
+    if (side < half) {
+      add(sums[side + half][col]);
+      sums[side][col] = s;
+    }
+    __syncthreads();
   }
+  if (side == 0) {
+    out[4 * col] = s.x;
+    out[4 * col + 1] = s.y;
+    out[4 * col + 2] = s.z;
+    out[4 * col + 3] = s.w;
+  }
+}
+
+template <int D>
+cudaError_t forward(const RopeArgs& a, cudaStream_t stream) {
+  constexpr int heads = heads_per_warp(D, Tune<D>::STEPS);
+  const int cq = (a.Hq + heads - 1) / heads, ck = (a.Hkv + heads - 1) / heads;
+  const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
+  const unsigned blocks = static_cast<unsigned>(tiles * (cq + ck));
+  if (a.interleaved) norm_rope_kernel<D, false><<<blocks, kRopeThreads, 0, stream>>>(a, cq, cq + ck);
+  else norm_rope_kernel<D, true><<<blocks, kRopeThreads, 0, stream>>>(a, cq, cq + ck);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
+  constexpr int heads = heads_per_warp(D, Tune<D>::GRAD_STEPS);
+  const int cq = (a.Hq + heads - 1) / heads, ck = (a.Hkv + heads - 1) / heads;
+  const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
+  // the blocks that are resident at a time, shared between q and k by their work
+  const int limit = std::min(Tune<D>::GRAD_BLOCKS * sms, kGradBlocks);
+  const long long share = (static_cast<long long>(limit) * cq + (cq + ck) / 2) / (cq + ck);
+  const int limit_q = ck ? static_cast<int>(std::max<long long>(1, std::min<long long>(share, limit - 1))) : limit;
+  const int bq = static_cast<int>(std::min<long long>(tiles * cq, limit_q));
+  const int bk = static_cast<int>(std::min<long long>(tiles * ck, limit - limit_q));
+  if (a.interleaved) norm_rope_backward_kernel<D, false><<<bq + bk, kRopeThreads, 0, stream>>>(a, bq, bk);
+  else norm_rope_backward_kernel<D, true><<<bq + bk, kRopeThreads, 0, stream>>>(a, bq, bk);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.Hkv ? 2 : 1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weight_grad_kernel<D>, a, bq, bk);
 }
 
 }  // namespace
@@ -262,29 +418,15 @@ size_t norm_rope_backward_workspace_bytes(int D) {
 }
 
 cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream) {
-  const int cq = (a.Hq + kRopeHeads - 1) / kRopeHeads, ck = (a.Hkv + kRopeHeads - 1) / kRopeHeads;
-  const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
-  const unsigned blocks = static_cast<unsigned>(tiles * (cq + ck));
-  if (a.D == 128) norm_rope_kernel<128><<<blocks, kRopeThreads, 0, stream>>>(a, cq, cq + ck);
-  else norm_rope_kernel<64><<<blocks, kRopeThreads, 0, stream>>>(a, cq, cq + ck);
-  return cudaGetLastError();
+  return a.D == 128 ? forward<128>(a, stream) : forward<64>(a, stream);
 }
 
 cudaError_t launch_norm_rope_backward(const RopeArgs& a, cudaStream_t stream) {
-  const int cq = (a.Hq + kRopeHeads - 1) / kRopeHeads, ck = (a.Hkv + kRopeHeads - 1) / kRopeHeads;
-  const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
-  // the partial rows are shared between q and k by their work
-  const long long share = static_cast<long long>(kGradBlocks) * cq / (cq + ck);
-  const int limit_q = static_cast<int>(std::max<long long>(1, ck ? std::min<long long>(share, kGradBlocks - 1) : kGradBlocks));
-  const int bq = static_cast<int>(std::min<long long>(tiles * cq, limit_q));
-  const int bk = static_cast<int>(std::min<long long>(tiles * ck, kGradBlocks - limit_q));
-  if (a.D == 128) norm_rope_backward_kernel<128><<<bq + bk, kRopeThreads, 0, stream>>>(a, bq, bk);
-  else norm_rope_backward_kernel<64><<<bq + bk, kRopeThreads, 0, stream>>>(a, bq, bk);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
-  if (a.D == 128) weight_grad_kernel<128><<<a.Hkv ? 2 : 1, 1024, 0, stream>>>(a, bq, bk);
-  else weight_grad_kernel<64><<<a.Hkv ? 2 : 1, 1024, 0, stream>>>(a, bq, bk);
-  return cudaGetLastError();
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  return a.D == 128 ? backward<128>(a, sms, stream) : backward<64>(a, sms, stream);
 }
 
 }  // namespace mcs
