@@ -177,7 +177,8 @@ struct WriteArgs {
   long long slots_total;     // num_pages * page
   long long stride;          // elements between tokens of k and v
   float k_scale, v_scale;    // E4M3
-  float k_inv, v_inv;        // their reciprocals (set by the launcher)
+  float k_inv, v_inv;        // set by the launcher: their reciprocals,
+  uint32_t k_most, v_most;   // and where values may be cut off (bf16 twice; 0: divide)
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
   const int32_t* slots;      // [T]

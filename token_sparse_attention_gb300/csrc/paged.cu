@@ -1,5 +1,7 @@
 // Paged key-value cache: pages and slots of new tokens, writes into the pages
 // with the pages' mean keys, and the choice of pages by a cheap score.
+#include <string.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -15,20 +17,18 @@ namespace {
 //
 // have_b = ceil(len_b / page), need_b = ceil((len_b + new_b) / page) - have_b;
 // with the exclusive sums of new and need every token and every fresh page
-// finds its sequence by a binary search.  Latency and nothing else, so it is
-// one launch: every CTA of one cluster takes the sums over all sequences for
-// itself (B <= 4096: at most four rounds of one block scan, 32 KB from L2),
-// checks everything that can be wrong, and only behind the cluster barrier,
-// when all have read the state, writes its share.  The state can so be updated
-// in place, and a request that cannot be met takes nothing.
+// finds its sequence by a binary search.  Latency and nothing else: one CTA
+// takes the sums and checks everything that can be wrong before it writes
+// anything, so the state can be updated in place and a request that cannot be
+// met takes nothing.  The tokens of a small step it places itself; for many, a
+// second launch (programmatically dependent) places them over all SMs from what
+// the first one wrote: cu_new, lens_out and the table say everything.
+// 9 sequences, 108 000 tokens: 12.3 us with all in one cluster of 8 CTAs (bound by
+// their instruction issue), PLAN_TWO us in two launches; 256 single tokens PLAN_ONE us.
 
 constexpr int kPlanMaxThreads = 1024;
-constexpr int kPlanMaxCluster = 8;
-constexpr int kPlanAtOnce = 4;  // tokens a thread searches side by side
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
+constexpr int kPlanAtOnce = 4;      // tokens a thread searches side by side
+constexpr int kPlanTokens = 8192;   // as many tokens the first launch places itself
 
 // For each x[k] the last i in [0, n) with first[i] <= x[k] (first ascending, first[0] <= x[k]).
 template <int K>
@@ -42,14 +42,42 @@ __device__ __forceinline__ void owners(const int32_t* first, int n, const int (&
   }
 }
 
-__global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanArgs a, int ctas) {
+// Slots and positions of the tokens at, at + step, ...: cu (shared), the
+// lengths before the step and the complete table.
+template <typename Len>
+__device__ __forceinline__ void place_tokens(const PlanArgs& a, const int32_t* cu, Len old, int at,
+                                             int step) {
+  const int shift = 31 - __clz(a.page), mask = a.page - 1, tokens = cu[a.B];
+  for (long long t0 = at; t0 < a.T; t0 += static_cast<long long>(kPlanAtOnce) * step) {
+    int t[kPlanAtOnce], b[kPlanAtOnce], pid[kPlanAtOnce], pos[kPlanAtOnce];
+#pragma unroll
+    for (int k = 0; k < kPlanAtOnce; ++k)
+      t[k] = static_cast<int>(min(t0 + static_cast<long long>(k) * step, static_cast<long long>(a.T)));
+    owners(cu, a.B, t, b);
+#pragma unroll
+    for (int k = 0; k < kPlanAtOnce; ++k) {
+      pos[k] = pid[k] = -1;
+      if (t[k] >= tokens) continue;
+      pos[k] = old(b[k]) + (t[k] - cu[b[k]]);
+      pid[k] = a.table[static_cast<size_t>(b[k]) * a.max_pages + (pos[k] >> shift)];
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanAtOnce; ++k) {
+      if (t[k] >= a.T) continue;
+      a.slots[t[k]] = pos[k] < 0 ? -1 : (pid[k] << shift) + (pos[k] & mask);
+      if (a.positions) a.positions[t[k]] = pos[k];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanArgs a, bool place) {
   extern __shared__ int32_t sm[];
   int32_t* s_cu = sm;                 // [B + 1] exclusive sums of new tokens
   int32_t* s_base = s_cu + a.B + 1;   // [B + 1] exclusive sums of missing pages
   int32_t* s_len = s_base + a.B + 1;  // [B]
-  __shared__ long long sums[32][2];
-  const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
-  const int threads = blockDim.x, warps = threads / 32;
+  __shared__ long long sums[33][2];   // of the warps in front of each; in 32 the block's
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = lane_id(), w = warp_id(), threads = blockDim.x;
   const int shift = 31 - __clz(a.page), mask = a.page - 1;
   const long long room = static_cast<long long>(a.max_pages) << shift;
   const int head = a.free_head[0];
@@ -73,27 +101,34 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanA
       }
       s_len[b] = len;
     }
-    long long x = nw, y = need;
+    auto scan = [&](long long& x, long long& y) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
-      if (lane >= d) x += u, y += v;
-    }
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+        if (lane >= d) x += u, y += v;
+      }
+    };
+    long long x = nw, y = need;
+    scan(x, y);
     if (lane == 31) sums[w][0] = x, sums[w][1] = y;
     __syncthreads();
-    long long all_x = 0, all_y = 0;
-    for (int i = 0; i < warps; ++i) {
-      if (i < w) x += sums[i][0], y += sums[i][1];
-      all_x += sums[i][0];
-      all_y += sums[i][1];
+    if (w == 0) {
+      const bool in = lane < threads / 32;
+      const long long p = in ? sums[lane][0] : 0, q = in ? sums[lane][1] : 0;
+      long long u = p, v = q;
+      scan(u, v);
+      sums[lane][0] = u - p;
+      sums[lane][1] = v - q;
+      if (lane == 31) sums[32][0] = u, sums[32][1] = v;
     }
+    __syncthreads();
     if (b < a.B) {
       // sums beyond T or n_free are refused below, before they are used
-      s_cu[b] = static_cast<int32_t>(tokens + x - nw);
-      s_base[b] = static_cast<int32_t>(pages + y - need);
+      s_cu[b] = static_cast<int32_t>(tokens + sums[w][0] + x - nw);
+      s_base[b] = static_cast<int32_t>(pages + sums[w][1] + y - need);
     }
-    tokens += all_x;
-    pages += all_y;
+    tokens += sums[32][0];
+    pages += sums[32][1];
     __syncthreads();
   }
   bad = bad || tokens > a.T || head < 0 || head > a.n_free || pages > a.n_free - head;
@@ -103,90 +138,73 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanA
       bad = bad || pid < 0 || pid >= a.num_pages;
     }
   }
-  if (tid == 0) {
-    s_cu[a.B] = static_cast<int32_t>(tokens);
-    s_base[a.B] = static_cast<int32_t>(pages);
-  }
-  bad = __syncthreads_or(bad);
-  // every CTA has read what any CTA is about to write
-  if (ctas > 1) cluster_sync();
-
-  const int at = blockIdx.x * threads + tid, step = ctas * threads;
+  bad = __syncthreads_or(bad);  // from here on everything has been read that is written below
   if (bad) {
-    if (at == 0) {
+    if (tid == 0) {
       atomicOr(a.status, DEV_BOUNDS);
       a.head_out[0] = head;
     }
-    for (int b = at; b <= a.B; b += step) {
+    for (int b = tid; b <= a.B; b += threads) {
       if (b < a.B) a.lens_out[b] = s_len[b];
       a.cu_new[b] = 0;
+      s_cu[b] = 0;
     }
-    for (int t = at; t < a.T; t += step) {
-      a.slots[t] = -1;
-      if (a.positions) a.positions[t] = -1;
+  } else {
+    if (tid == 0) {
+      a.head_out[0] = head + static_cast<int>(pages);
+      a.cu_new[a.B] = s_cu[a.B] = static_cast<int32_t>(tokens);
+      s_base[a.B] = static_cast<int32_t>(pages);
     }
-    return;
-  }
-  if (at == 0) a.head_out[0] = head + static_cast<int>(pages);
-  for (int b = at; b <= a.B; b += step) {
-    a.cu_new[b] = s_cu[b];
-    if (b < a.B) a.lens_out[b] = s_len[b] + (s_cu[b + 1] - s_cu[b]);
-  }
-  for (int j = at; j < pages; j += step) {
-    const int x[1] = {j};
-    int b[1];
-    owners(s_base, a.B, x, b);
-    const int have = (s_len[b[0]] + mask) >> shift;
-    a.table[static_cast<size_t>(b[0]) * a.max_pages + have + (j - s_base[b[0]])] = a.free_pages[head + j];
-  }
-  for (long long t0 = at; t0 < a.T; t0 += static_cast<long long>(kPlanAtOnce) * step) {
-    int t[kPlanAtOnce], b[kPlanAtOnce], pid[kPlanAtOnce], pos[kPlanAtOnce];
-#pragma unroll
-    for (int k = 0; k < kPlanAtOnce; ++k)
-      t[k] = static_cast<int>(min(t0 + static_cast<long long>(k) * step, static_cast<long long>(a.T)));
-    owners(s_cu, a.B, t, b);
-#pragma unroll
-    for (int k = 0; k < kPlanAtOnce; ++k) {
-      pos[k] = pid[k] = -1;
-      if (t[k] >= tokens) continue;
-      pos[k] = s_len[b[k]] + (t[k] - s_cu[b[k]]);
-      // pages the sequence had (its last one, read above), or fresh ones
-      const int have = (s_len[b[k]] + mask) >> shift, j = pos[k] >> shift;
-      pid[k] = j < have ? a.table[static_cast<size_t>(b[k]) * a.max_pages + j]
-                        : a.free_pages[head + s_base[b[k]] + (j - have)];
+    __syncthreads();
+    for (int b = tid; b < a.B; b += threads) {
+      a.cu_new[b] = s_cu[b];
+      a.lens_out[b] = s_len[b] + (s_cu[b + 1] - s_cu[b]);
     }
-#pragma unroll
-    for (int k = 0; k < kPlanAtOnce; ++k) {
-      if (t[k] >= a.T) continue;
-      a.slots[t[k]] = pos[k] < 0 ? -1 : (pid[k] << shift) + (pos[k] & mask);
-      if (a.positions) a.positions[t[k]] = pos[k];
+    for (int j = tid; j < pages; j += threads) {
+      const int x[1] = {j};
+      int b[1];
+      owners(s_base, a.B, x, b);
+      const int have = (s_len[b[0]] + mask) >> shift;
+      a.table[static_cast<size_t>(b[0]) * a.max_pages + have + (j - s_base[b[0]])] = a.free_pages[head + j];
     }
   }
+  if (!place) return;
+  __syncthreads();  // the table's new entries, too
+  place_tokens(a, s_cu, [&](int b) { return s_len[b]; }, tid, threads);
+}
+
+__global__ void __launch_bounds__(256) paged_place_kernel(const PlanArgs a) {
+  extern __shared__ int32_t s_cu[];  // [B + 1]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int b = threadIdx.x; b <= a.B; b += blockDim.x) s_cu[b] = a.cu_new[b];
+  __syncthreads();
+  place_tokens(a, s_cu, [&](int b) { return a.lens_out[b] - (s_cu[b + 1] - s_cu[b]); },
+               blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 // ------------------------------------------------------------------ write
 
 // x / scale, correctly rounded, from inv = 1 / scale (itself correctly rounded): the
 // product and one exact remainder (Markstein 1990).  For every mantissa of a
-// bf16 x and of the scale this is the fp32 quotient (all 2^30 pairs compared);
-// scales outside [2^-60, 2^60], where remainders could underflow, divide instead.
-// Infinities (and what overflows) and the sign of zero are put back.
+// bf16 x and of the scale this is the fp32 quotient (all 2^30 pairs compared).
+// |x| is first limited to `most`, at least 1024 scale, which changes no code and
+// keeps infinities out of the remainder; NaN stays, and so does the sign of zero.
+// Scales outside [2^-60, 2^60], where remainders could underflow, divide instead.
 struct Scale {
   float s, inv;
-  bool fast;
+  uint32_t most;  // bf16 twice; 0: divide
 };
-__device__ __forceinline__ uint64_t quotient2(uint32_t lo, uint32_t hi, const Scale& c) {
-  const float x0 = __uint_as_float(lo), x1 = __uint_as_float(hi);
-  if (!c.fast) return f2_pack(__fdiv_rn(x0, c.s), __fdiv_rn(x1, c.s));
-  const uint64_t x = f2_pack(x0, x1), inv = f2_pack(c.inv, c.inv);
-  const uint64_t q = f2_fma(x, inv, 0x8000000080000000ull);
-  const uint64_t rem = f2_fma(q ^ 0x8000000080000000ull, f2_pack(c.s, c.s), x);
-  float q0, q1, r0, r1;
-  f2_unpack(q, q0, q1);
-  f2_unpack(f2_fma(rem, inv, q), r0, r1);
-  r0 = fabsf(q0) <= 1e30f ? copysignf(r0, x0) : q0;
-  r1 = fabsf(q1) <= 1e30f ? copysignf(r1, x1) : q1;
-  return f2_pack(r0, r1);
+__device__ __forceinline__ uint64_t quotient2(uint32_t w, const Scale& c) {
+  if (c.most == 0)
+    return f2_pack(__fdiv_rn(__uint_as_float(w << 16), c.s), __fdiv_rn(__uint_as_float(w & 0xFFFF0000u), c.s));
+  uint32_t y;
+  asm("{\n\t.reg .b32 a;\n\tmin.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 %0, a, %3;\n\t}"
+      : "=r"(y)
+      : "r"(w), "r"(c.most), "r"(c.most ^ 0x80008000u));
+  const uint64_t x = f2_pack(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u));
+  const uint64_t q = f2_fma(x, f2_pack(c.inv, c.inv), 0x8000000080000000ull);
+  const uint64_t rem = f2_fma(q, f2_pack(c.s, c.s), x ^ 0x8000000080000000ull);
+  return f2_fma(rem, f2_pack(-c.inv, -c.inv), q);
 }
 
 // 8 bf16 values (a 16-byte word) -> 8 E4M3 codes of x / scale.
@@ -196,7 +214,7 @@ __device__ __forceinline__ uint2 encode8(uint4 x, const Scale& scale) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float lo, hi;
-    f2_unpack(quotient2(w[i] << 16, w[i] & 0xFFFF0000u, scale), lo, hi);
+    f2_unpack(quotient2(w[i], scale), lo, hi);
     c[i] = f32x2_to_e4m3x2(lo, hi);
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
@@ -228,85 +246,156 @@ __device__ __forceinline__ void add8(float* sum, uint2 c, float scale) {
 
 constexpr int kWriteThreads = 256;
 
-// D/8 threads per (token, head) copy its k and v rows.  The threads of the
-// first token of each page's run also take the page's mean: the rows in front
-// of it from the cache, the run's own from k (now in L2), so that nothing is
-// read that another thread of this launch writes; eight rows at a time, since
-// one thread's loads are all that hides their latency.
+// A block takes one KV head and a window of consecutive tokens, D/8 threads per
+// row and ROWS rows per thread, all loaded before the first slot is needed: the
+// stores of a window then lie next to each other in its pages.  The block that
+// holds the first token of a page's run also takes the page's mean: the rows in
+// front of it from the cache, the run's own from k (now in L2), so that nothing
+// is read that another block of this launch writes.  With few runs (prompts) the
+// whole block sums one, up to 128 rows in one round of loads; with many (a
+// decoding step) every D/8 threads take one.
 template <int D, bool kE4M3Cache>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteArgs a, bool fast) {
-  constexpr int LANES = D / 8;
-  const unsigned item = blockIdx.x * (kWriteThreads / LANES) + threadIdx.x / LANES;
-  const int l = threadIdx.x % LANES;
-  const unsigned t = item / static_cast<unsigned>(a.Hkv), h = item - t * a.Hkv;
-  if (t >= static_cast<unsigned>(a.T)) return;
-  const int slot = a.slots[t];
-  if (slot < 0) return;
-  if (slot >= a.slots_total) {
-    if (h == 0 && l == 0) atomicOr(a.status, DEV_BOUNDS);
-    return;
-  }
-  const Scale ks = {a.k_scale, a.k_inv, fast}, vs = {a.v_scale, a.v_inv, fast};
-  const int off = slot & (a.page - 1), page_id = slot >> (31 - __clz(a.page));
-  const size_t page_row = (static_cast<size_t>(page_id) * a.Hkv + h) * a.page;
-  const size_t src = t * a.stride + static_cast<size_t>(h) * D + 8 * l;
-  const size_t dst = (page_row + off) * D + 8 * l;
-  const uint4 k = ld_global_nc16(a.k + src), v = ld_global_nc16(a.v + src);
-  const bool mean = a.k_mean != nullptr && (t == 0 || off == 0 || a.slots[t - 1] != slot - 1);
-  if (kE4M3Cache) {
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_cache) + dst) = encode8(k, ks);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_cache) + dst) = encode8(v, vs);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_cache) + dst) = k;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + dst) = v;
-  }
-  if (!mean) return;
-  // the run: how many tokens behind t continue in the page, LANES of them looked at a time
-  const int lane0 = lane_id() / LANES * LANES;
-  const uint32_t mates = ((1u << LANES) - 1u) << lane0;
-  int run = 1;
-  for (const int most = min(a.page - off, a.T - static_cast<int>(t)); run < most;) {
-    const bool next = run + l < most && a.slots[t + run + l] == slot + run + l;
-    const uint32_t no = ~__ballot_sync(mates, next) & mates;
-    const int more = no == 0 ? LANES : __ffs(no) - 1 - lane0;
-    run += more;
-    if (more < LANES) break;
-  }
-  float sum[8] = {};
+__device__ __forceinline__ void sum_run(const WriteArgs& a, const Scale& ks, size_t page_row, size_t src, int off,
+                                        int run, int first, int step, int l, float* sum) {
   using Word = typename std::conditional<kE4M3Cache, uint2, uint4>::type;  // 8 stored values
   const Word* old = reinterpret_cast<const Word*>(
       static_cast<const uint8_t*>(a.k_cache) + (page_row * D + 8 * l) * (kE4M3Cache ? 1 : 2));
-  for (int r = 0; r < off; r += 8) {
+  for (int r = first; r < off; r += 8 * step) {
     Word x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[i] = Word{};
-      if (r + i < off) x[i] = old[(r + i) * LANES];
+      if (r + i * step < off) x[i] = old[(r + i * step) * (D / 8)];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) add8(sum, x[i], a.k_scale);
   }
-  for (int r = 0; r < run; r += 8) {
+  for (int r = first; r < run; r += 8 * step) {
     uint4 x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[i] = make_uint4(0, 0, 0, 0);
-      if (r + i < run) x[i] = ld_global_nc16(a.k + src + static_cast<size_t>(r + i) * a.stride);
+      if (r + i * step < run) x[i] = ld_global_nc16(a.k + src + static_cast<size_t>(r + i * step) * a.stride);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (r + i >= run) break;
+      if (r + i * step >= run) break;
       if (kE4M3Cache) add8(sum, encode8(x[i], ks), a.k_scale);
       else add8(sum, x[i], 1.f);
     }
   }
-  const float n = static_cast<float>(off + run);
-  uint4 m;
-  m.x = pack_bf16(sum[0] / n, sum[1] / n);
-  m.y = pack_bf16(sum[2] / n, sum[3] / n);
-  m.z = pack_bf16(sum[4] / n, sum[5] / n);
-  m.w = pack_bf16(sum[6] / n, sum[7] / n);
-  *reinterpret_cast<uint4*>(a.k_mean + (static_cast<size_t>(page_id) * a.Hkv + h) * D + 8 * l) = m;
+}
+
+template <int D, bool kE4M3Cache, int ROWS>
+__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteArgs a) {
+  constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES;
+  constexpr int WINDOW = GROUPS * ROWS;
+  __shared__ int s_first[WINDOW], s_slot[WINDOW];
+  __shared__ uint32_t s_break[kWriteThreads / 32], s_lead[kWriteThreads / 32];
+  __shared__ float s_sum[GROUPS][D];
+  const unsigned window = blockIdx.x / static_cast<unsigned>(a.Hkv);
+  const int h = static_cast<int>(blockIdx.x - window * a.Hkv), g = threadIdx.x / LANES, l = threadIdx.x % LANES;
+  const long long start = static_cast<long long>(window) * WINDOW, t0 = start + g;
+  const size_t col = static_cast<size_t>(h) * D + 8 * l;
+  const int shift = 31 - __clz(a.page), mask = a.page - 1;
+  uint4 k[ROWS], v[ROWS];
+  int slot[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const long long t = t0 + i * GROUPS;
+    slot[i] = -1;
+    if (t < a.T) {
+      k[i] = ld_global_nc16(a.k + t * a.stride + col);
+      v[i] = ld_global_nc16(a.v + t * a.stride + col);
+      slot[i] = a.slots[t];
+    }
+  }
+  // where runs begin, while the rows are on their way: a thread looks at one
+  // token of the window or of the 128 behind it (a run ends with its page)
+  int count = 0;
+  if (a.k_mean != nullptr) {
+    static_assert(WINDOW + 128 <= kWriteThreads, "a thread per token");
+    const long long t = start + threadIdx.x;
+    const int mine = t < a.T ? a.slots[t] : -1, before = t > 0 && t <= a.T ? a.slots[t - 1] : -1;
+    const bool begins = mine < 0 || (mine & mask) == 0 || before != mine - 1;
+    const bool leads = begins && mine >= 0 && mine < a.slots_total && threadIdx.x < WINDOW;
+    const uint32_t bb = __ballot_sync(0xffffffffu, begins), lb = __ballot_sync(0xffffffffu, leads);
+    if (lane_id() == 0) {
+      s_break[warp_id()] = bb;
+      s_lead[warp_id()] = lb;
+    }
+    __syncthreads();
+    int rank = __popc(lb & ((1u << lane_id()) - 1u));
+#pragma unroll
+    for (int i = 0; i < kWriteThreads / 32; ++i) {
+      if (i < warp_id()) rank += __popc(s_lead[i]);
+      count += __popc(s_lead[i]);
+    }
+    if (leads) {
+      s_first[rank] = static_cast<int>(threadIdx.x);
+      s_slot[rank] = mine;
+    }
+  }
+  const Scale ks = {a.k_scale, a.k_inv, a.k_most}, vs = {a.v_scale, a.v_inv, a.v_most};
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (slot[i] < 0) continue;
+    if (slot[i] >= a.slots_total) {
+      if (h == 0 && l == 0) atomicOr(a.status, DEV_BOUNDS);
+      continue;
+    }
+    const size_t row = ((static_cast<size_t>(slot[i] >> shift) * a.Hkv + h) << shift) + (slot[i] & mask);
+    const size_t dst = row * D + 8 * l;
+    if (kE4M3Cache) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_cache) + dst) = encode8(k[i], ks);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_cache) + dst) = encode8(v[i], vs);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_cache) + dst) = k[i];
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + dst) = v[i];
+    }
+  }
+  if (a.k_mean == nullptr) return;
+  __syncthreads();
+  // teams of `size` times D/8 threads, one run each
+  int size = GROUPS;
+  while (size > 1 && size * count > GROUPS) size /= 2;
+  const int member = g % size;
+  for (int n0 = 0; n0 < count; n0 += GROUPS / size) {
+    const int n = n0 + g / size;
+    float sum[8] = {};
+    int rows = 0, page_id = 0;
+    if (n < count) {
+      const int at = s_first[n], first_slot = s_slot[n], off = first_slot & mask;
+      page_id = first_slot >> shift;
+      // the run reaches to the next beginning behind it
+      int word = (at + 1) / 32;
+      uint32_t bits = s_break[word] >> ((at + 1) % 32) << ((at + 1) % 32);
+      while (bits == 0) bits = s_break[++word];
+      const int run = 32 * word + __ffs(bits) - 1 - at;
+      rows = off + run;
+      sum_run<D, kE4M3Cache>(a, ks, (static_cast<size_t>(page_id) * a.Hkv + h) << shift,
+                             static_cast<size_t>(start + at) * a.stride + col, off, run, member, size, l, sum);
+    }
+    if (size > 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s_sum[g][8 * l + i] = sum[i];
+      __syncthreads();
+      if (member == 0)
+        for (int o = 1; o < size; ++o)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] += s_sum[g + o][8 * l + i];
+      __syncthreads();
+    }
+    if (rows > 0 && member == 0) {
+      const float n_rows = static_cast<float>(rows);
+      uint4 m;
+      m.x = pack_bf16(sum[0] / n_rows, sum[1] / n_rows);
+      m.y = pack_bf16(sum[2] / n_rows, sum[3] / n_rows);
+      m.z = pack_bf16(sum[4] / n_rows, sum[5] / n_rows);
+      m.w = pack_bf16(sum[6] / n_rows, sum[7] / n_rows);
+      *reinterpret_cast<uint4*>(a.k_mean + (static_cast<size_t>(page_id) * a.Hkv + h) * D + 8 * l) = m;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ select
@@ -587,46 +676,57 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int32_t);
-  // a thread per item up to one CTA of 1024, then a CTA per 4096 up to one cluster
-  const long long items = std::max<long long>(a.T, a.B);
-  const int threads = items > 512 ? kPlanMaxThreads : items > 256 ? 512 : 256;
-  int ctas = 1;
-  while (ctas < kPlanMaxCluster && items > 4096LL * ctas) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const bool place = a.T <= kPlanTokens;
+  const int items = std::max(a.B, place ? a.T : 0);
+  const int threads = items > 512 || !place ? kPlanMaxThreads : items > 256 ? 512 : 256;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a, ctas);
+  paged_plan_kernel<<<1, threads, smem, stream>>>(a, place);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || place) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min((a.T + 256 * kPlanAtOnce - 1) / (256 * kPlanAtOnce), 1024));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = (static_cast<size_t>(a.B) + 1) * sizeof(int32_t);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_place_kernel, a);
+}
+
+template <int D, bool E4M3>
+static void write_launch(const WriteArgs& a, cudaStream_t stream) {
+  constexpr int GROUPS = kWriteThreads / (D / 8);
+  // four rows per thread once that leaves every SM (152) eight blocks
+  const bool many = static_cast<long long>(a.T) * a.Hkv >= 152LL * 8 * 4 * GROUPS;
+  const int window = GROUPS * (many ? 4 : 1);
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.T) + window - 1) / window * a.Hkv);
+  if (many) paged_write_kernel<D, E4M3, 4><<<blocks, kWriteThreads, 0, stream>>>(a);
+  else paged_write_kernel<D, E4M3, 1><<<blocks, kWriteThreads, 0, stream>>>(a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const long long items = static_cast<long long>(a.T) * a.Hkv;
-  const int per_block = kWriteThreads / (a.D / 8);
-  const unsigned blocks = static_cast<unsigned>((items + per_block - 1) / per_block);
   WriteArgs c = a;
   c.k_inv = e4m3 ? 1.f / a.k_scale : 1.f;
   c.v_inv = e4m3 ? 1.f / a.v_scale : 1.f;
-  auto middle = [](float s) { return s >= 0x1p-60f && s <= 0x1p60f; };
-  const bool fast = middle(a.k_scale) && middle(a.v_scale);
-  if (a.D == 128) {
-    if (e4m3) paged_write_kernel<128, true><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
-    else paged_write_kernel<128, false><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
-  } else {
-    if (e4m3) paged_write_kernel<64, true><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
-    else paged_write_kernel<64, false><<<blocks, kWriteThreads, 0, stream>>>(c, fast);
-  }
+  // 2048 scale cut to its upper half: a bf16 number, twice
+  auto most = [](float s) {
+    if (!(s >= 0x1p-60f && s <= 0x1p60f)) return 0u;
+    const float x = 2048.f * s;
+    uint32_t w;
+    memcpy(&w, &x, sizeof(w));
+    return (w & 0xFFFF0000u) | (w >> 16);
+  };
+  c.k_most = most(a.k_scale);
+  c.v_most = most(a.v_scale);
+  if (a.D == 128) e4m3 ? write_launch<128, true>(c, stream) : write_launch<128, false>(c, stream);
+  else e4m3 ? write_launch<64, true>(c, stream) : write_launch<64, false>(c, stream);
   return cudaGetLastError();
 }
 
