@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace mcs {
@@ -174,8 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long* prefix = static_cast<long long*>(a.ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + parts_offset());
 
-  // the dependent launch may be set up; it waits for this one to finish
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_begin();
 
   // ---- the shares: sums over the sequences' tiles, 256 sequences at a time
   // (inclusive in x and y; a batch of up to 256 needs one round)
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float s_top[kJoinThreads / 32], s_sum[kJoinThreads / 32];
   __shared__ float4 s_acc[kJoinThreads / 32][32];
   constexpr float kShift = E4M3 ? 12.f : 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_begin();
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
   const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * (D / splits);
   const int b = head / a.Hq, hq = head % a.Hq, group = a.Hq / a.Hkv;
@@ -719,20 +719,11 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   constexpr int TK = Geo<D, E4M3>::TK;
   const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + TK - 1) / TK + kSegCost);
   const int grid = static_cast<int>(std::min<long long>(std::min(sms, kMaxCtas), most));
-  kernel<<<grid, kThreads, kSmem, stream>>>(a, chunks);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks)) != cudaSuccess) return e;
   // few heads have many parts each: their columns go to several blocks
   const int splits = a.B * a.Hq <= sms / 4 ? 8 : a.B * a.Hq <= sms ? 2 : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.B * a.Hq * splits);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, E4M3>, a, chunks, grid, WIDE, splits);
+  return launch_dependent(paged_join_kernel<D, E4M3>, a.B * a.Hq * splits, kJoinThreads, 0, stream, a, chunks,
+                          grid, WIDE, splits);
 }
 
 }  // namespace

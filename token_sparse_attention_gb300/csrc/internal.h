@@ -198,7 +198,7 @@ struct SelectArgs {
   const int32_t* table;
   const int32_t* lens;
   int32_t* sel;              // [B, Hkv, select]
-  uint32_t* keys;            // [B * Hkv, max_pages rounded up to 8] order-preserving score keys
+  uint32_t* keys;            // [B * Hkv, 2, max_pages rounded up to 8] score keys, error bounds
   unsigned* status;
 };
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream);

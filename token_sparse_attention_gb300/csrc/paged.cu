@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace mcs {
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanA
   int32_t* s_base = s_cu + a.B + 1;   // [B + 1] exclusive sums of missing pages
   int32_t* s_len = s_base + a.B + 1;  // [B]
   __shared__ long long sums[33][2];   // of the warps in front of each; in 32 the block's
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_begin();
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id(), threads = blockDim.x;
   const int shift = 31 - __clz(a.page), mask = a.page - 1;
   const long long room = static_cast<long long>(a.max_pages) << shift;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanA
 
 __global__ void __launch_bounds__(256) paged_place_kernel(const PlanArgs a) {
   extern __shared__ int32_t s_cu[];  // [B + 1]
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_begin();
   for (int b = threadIdx.x; b <= a.B; b += blockDim.x) s_cu[b] = a.cu_new[b];
   __syncthreads();
   place_tokens(a, s_cu, [&](int b) { return a.lens_out[b] - (s_cu[b + 1] - s_cu[b]); },
@@ -287,12 +288,13 @@ __device__ __forceinline__ void sum_run(const WriteArgs& a, const Scale& ks, siz
 }
 
 template <int D, bool kE4M3Cache, int ROWS>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const WriteArgs a) {
   constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES;
   constexpr int WINDOW = GROUPS * ROWS;
   __shared__ int s_first[WINDOW], s_slot[WINDOW];
   __shared__ uint32_t s_break[kWriteThreads / 32], s_lead[kWriteThreads / 32];
   __shared__ float s_sum[GROUPS][D];
+  pdl_begin();
   const unsigned window = blockIdx.x / static_cast<unsigned>(a.Hkv);
   const int h = static_cast<int>(blockIdx.x - window * a.Hkv), g = threadIdx.x / LANES, l = threadIdx.x % LANES;
   const long long start = static_cast<long long>(window) * WINDOW, t0 = start + g;
@@ -401,34 +403,38 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const WriteA
 // ------------------------------------------------------------------ select
 //
 // score(page) = (sum of the group's queries) . mean, and the pages of the
-// largest scores.  Which page is kept must not depend on the order of a sum,
-// so the products are summed in two fp32 words per sum (error-free sums and
-// products of pairs: about 48 bits) and rounded to fp32 once; ties then go to
-// the lower page.  fp64 would give the same but runs at 1/60 of the fp32 rate here.
-// Bound: the means are read once, 2 D bytes per page and KV head.
+// largest scores.  Which page is kept must not depend on the order of a sum:
+// the score is the exact sum, rounded to fp32 once.  A first kernel takes plain
+// fp32 sums and a bound of their error, E = 2^-20 |q| |mean| (16 half steps of
+// the largest the sum can be; rounding the query, the products, 8 additions and
+// the final rounding are 11).  With T the select-th largest of these, pages
+// above T + 2E belong to the result and pages below T - 2E do not, whatever
+// the exact scores are; where more pages than needed lie between (ties, or
+// neighbours closer than 2^-19 of their size), those are computed in fp64 and
+// ranked again.  Bound: the means are read once, 2 D bytes per page and KV head;
+// 4725 pages of 40 heads (48 MB) take SCORE_US us, in two-word fp32 arithmetic 20.
 
 constexpr int kScoreThreads = 256;
 constexpr int kTopkKeys = 8;  // consecutive keys per thread and step
 
-// Two independent sums (x and y halves of the pairs), each as hi + lo.
-struct Sum2 {
-  uint64_t hi, lo;
-};
-__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
-  return f2_fma(b, f2_pack(-1.f, -1.f), a);
+// Keys of pages that are always kept, and of pages outside the cache (last of
+// all; the attention skips them too).
+constexpr uint32_t kKeyForced = 0xFFFFFFFFu, kKeyBad = 0u;
+
+__device__ __forceinline__ bool bad_length(const SelectArgs& a, int len) {
+  return len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_pages) * a.page;
 }
-// s + x: hi takes the rounded sum, lo what it lost (Knuth's two-sum).
-__device__ __forceinline__ void two_add(Sum2& s, uint64_t x) {
-  const uint64_t sum = f2_add(s.hi, x), bb = f2_sub(sum, s.hi);
-  const uint64_t err = f2_add(f2_sub(s.hi, f2_sub(sum, bb)), f2_sub(x, bb));
-  s.hi = sum;
-  s.lo = f2_add(s.lo, err);
-}
-__device__ __forceinline__ void two_add(float& hi, float& lo, float x, float xl) {
-  const float sum = __fadd_rn(hi, x), bb = __fsub_rn(sum, hi);
-  const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, bb)), __fsub_rn(x, bb));
-  hi = sum;
-  lo = __fadd_rn(__fadd_rn(lo, xl), err);
+
+// Sum of `group` bf16 values `step` apart, rounded to fp32 once (two words, Knuth's two-sum).
+__device__ __forceinline__ float sum_of_group(const __nv_bfloat16* q, int group, int step) {
+  float hi = 0.f, lo = 0.f;
+  for (int i = 0; i < group; ++i) {
+    const float x = __bfloat162float(q[static_cast<size_t>(i) * step]);
+    const float sum = __fadd_rn(hi, x), bb = __fsub_rn(sum, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, bb)), __fsub_rn(x, bb)));
+    hi = sum;
+  }
+  return __fadd_rn(hi, lo);
 }
 
 // A block takes ROWS = 256 / D KV heads of one sequence and 8 * per_warp of its
@@ -438,51 +444,46 @@ template <int D>
 __global__ void __launch_bounds__(kScoreThreads)
     paged_score_kernel(const SelectArgs a, int head_blocks, int page_blocks, int per_warp, int stride) {
   constexpr int LANES = D / 8, ROWS = 32 / LANES;
-  __shared__ float s_hi[ROWS * D], s_lo[ROWS * D];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float s_q[ROWS * D];
+  pdl_begin();
   const int xp = blockIdx.x % page_blocks, hb = blockIdx.x / page_blocks % head_blocks;
   const int b = blockIdx.x / page_blocks / head_blocks;
   const int len = a.lens[b];
-  if (len <= 0 || static_cast<long long>(len) > static_cast<long long>(a.max_pages) * a.page) return;
+  if (len == 0 || bad_length(a, len)) return;
   const int n = (len - 1) / a.page + 1;
-  const int j0 = (xp * (kScoreThreads / 32) + warp_id()) * per_warp;
+  const int j0 = (xp * (kScoreThreads / 32) + warp_id()) * per_warp, j1 = min(n, j0 + per_warp);
   if (xp * (kScoreThreads / 32) * per_warp >= n) return;
+  // per_warp <= 32: a page number per lane, on its way while the queries are summed
+  int pid = -1;
+  const bool mine = j0 + lane_id() < j1;
+  if (mine) pid = a.table[static_cast<size_t>(b) * a.max_pages + j0 + lane_id()];
   const int group = a.Hq / a.Hkv;
   {  // the group's summed query, one value per thread
     const int r = threadIdx.x / D, d = threadIdx.x % D, h = min(hb * ROWS + r, a.Hkv - 1);
     const __nv_bfloat16* q = a.q + b * a.q_stride + static_cast<size_t>(h) * group * D + d;
-    float hi = 0.f, lo = 0.f;
-    for (int i = 0; i < group; ++i) two_add(hi, lo, __bfloat162float(q[i * D]), 0.f);
-    const float sum = __fadd_rn(hi, lo);
-    s_hi[threadIdx.x] = sum;
-    s_lo[threadIdx.x] = __fsub_rn(lo, __fsub_rn(sum, hi));
+    s_q[threadIdx.x] = sum_of_group(q, group, D);
   }
   __syncthreads();
+  if (j0 >= j1) return;
+  const bool outside = mine && (pid < 0 || pid >= a.num_pages);
+  if (outside) atomicOr(a.status, DEV_BOUNDS);
+  if (outside || !mine) pid = 0;
+  const uint32_t bad = __ballot_sync(0xffffffffu, outside);
   const int lane = lane_id(), l = lane % LANES, h = hb * ROWS + lane / LANES;
-  uint64_t qh[4], ql[4];
+  uint64_t q[4];
+  float qq = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = lane / LANES * D + 8 * l + 2 * i;
-    qh[i] = f2_pack(s_hi[at], s_hi[at + 1]);
-    ql[i] = f2_pack(s_lo[at], s_lo[at + 1]);
+    q[i] = f2_pack(s_q[at], s_q[at + 1]);
+    qq = fmaf(s_q[at], s_q[at], fmaf(s_q[at + 1], s_q[at + 1], qq));
   }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) qq += __shfl_xor_sync(0xffffffffu, qq, o);
+  const float bound = 0x1p-20f * sqrtf(qq);
   const __nv_bfloat16* mean = a.k_mean + static_cast<size_t>(min(h, a.Hkv - 1)) * D + 8 * l;
   const size_t page_step = static_cast<size_t>(a.Hkv) * D;
-  uint32_t* keys = a.keys + (static_cast<size_t>(b) * a.Hkv + h) * stride;
-  const int j1 = min(n, j0 + per_warp);
-  if (j0 >= j1) return;
-  // per_warp <= 32: a page number per lane
-  int pid = 0;
-  bool outside = false;
-  if (j0 + lane < j1) {
-    pid = a.table[static_cast<size_t>(b) * a.max_pages + j0 + lane];
-    outside = pid < 0 || pid >= a.num_pages;
-    if (outside) {
-      atomicOr(a.status, DEV_BOUNDS);
-      pid = 0;
-    }
-  }
-  const uint32_t bad = __ballot_sync(0xffffffffu, outside);
+  uint32_t* keys = a.keys + 2 * (static_cast<size_t>(b) * a.Hkv + h) * stride;
   for (int j = j0; j < j1; j += 8) {
     uint4 x[8];
 #pragma unroll
@@ -490,27 +491,22 @@ __global__ void __launch_bounds__(kScoreThreads)
       x[i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - j0 + i) * page_step);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      float hi[4], lo[4];
+      float dot[4], mm[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {x[4 * half + i].x, x[4 * half + i].y, x[4 * half + i].z,
-                               x[4 * half + i].w};
-        Sum2 s = {0, 0};
+        const uint32_t w[4] = {x[4 * half + i].x, x[4 * half + i].y, x[4 * half + i].z, x[4 * half + i].w};
+        uint64_t s = 0, t = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint64_t m = f2_pack(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xFFFF0000u));
-          const uint64_t p = f2_fma(qh[c], m, 0);
-          // what the product lost, and the low word's product
-          const uint64_t e = f2_fma(qh[c], m, p ^ 0x8000000080000000ull);
-          two_add(s, p);
-          s.lo = f2_add(s.lo, f2_fma(ql[c], m, e));
+          s = f2_fma(q[c], m, s);
+          t = f2_fma(m, m, t);
         }
-        float h0, h1, l0, l1;
-        f2_unpack(s.hi, h0, h1);
-        f2_unpack(s.lo, l0, l1);
-        two_add(h0, l0, h1, l1);
-        hi[i] = h0;
-        lo[i] = l0;
+        float u, v;
+        f2_unpack(s, u, v);
+        dot[i] = u + v;
+        f2_unpack(t, u, v);
+        mm[i] = u + v;
       }
       // fold over the lanes: the upper half of each group of lanes keeps the
       // upper half of the pages
@@ -520,126 +516,239 @@ __global__ void __launch_bounds__(kScoreThreads)
         const bool upper = l & o;
 #pragma unroll
         for (int i = 0; i < keep; ++i) {
-          const float sh = upper ? hi[i] : hi[i + keep], sl = upper ? lo[i] : lo[i + keep];
-          hi[i] = upper ? hi[i + keep] : hi[i];
-          lo[i] = upper ? lo[i + keep] : lo[i];
-          const float rh = __shfl_xor_sync(0xffffffffu, sh, o), rl = __shfl_xor_sync(0xffffffffu, sl, o);
-          two_add(hi[i], lo[i], rh, rl);
+          const float sd = upper ? dot[i] : dot[i + keep], sm = upper ? mm[i] : mm[i + keep];
+          dot[i] = (upper ? dot[i + keep] : dot[i]) + __shfl_xor_sync(0xffffffffu, sd, o);
+          mm[i] = (upper ? mm[i + keep] : mm[i]) + __shfl_xor_sync(0xffffffffu, sm, o);
         }
       }
 #pragma unroll
       for (; o > 0; o /= 2) {
-        const float rh = __shfl_xor_sync(0xffffffffu, hi[0], o), rl = __shfl_xor_sync(0xffffffffu, lo[0], o);
-        two_add(hi[0], lo[0], rh, rl);
+        dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+        mm[0] += __shfl_xor_sync(0xffffffffu, mm[0], o);
       }
       // lane bits LANES/2 and LANES/4 name the page
-      const int mine = 4 * half + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
-      const int page = j + mine;
-      const int from = __shfl_sync(0xffffffffu, pid, page - j0);
+      const int page = j + 4 * half + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
       if (l % (LANES / 4) == 0 && page < j1 && h < a.Hkv) {
-        float score = __fadd_rn(hi[0], lo[0]);
-        if (!(fabsf(score) <= 3.0e38f)) {
-          // infinities or an overflow in between, where the two-word sum does
-          // not hold: in fp64
-          double sum = 0;
-          for (int d = 0; d < D; ++d) {
-            const int at = lane / LANES * D + d;
-            sum += (static_cast<double>(s_hi[at]) + static_cast<double>(s_lo[at])) *
-                   static_cast<double>(__bfloat162float(a.k_mean[from * page_step + static_cast<size_t>(h) * D + d]));
-          }
-          score = static_cast<float>(sum);
-        }
-        uint32_t key = score_key_bits(__float_as_uint(score));
-        if (page < a.sink || page >= n - a.recent) key = 0xFFFFFFFFu;
-        if ((bad >> (page - j0)) & 1u) key = 0;  // last of all; the attention skips it too
+        uint32_t key = score_key_bits(__float_as_uint(dot[0]));
+        float off = bound * sqrtf(mm[0]);
+        if (page < a.sink || page >= n - a.recent) key = kKeyForced, off = 0.f;
+        if ((bad >> (page - j0)) & 1u) key = kKeyBad, off = 0.f;
         keys[page] = key;
+        keys[stride + page] = __float_as_uint(off);
       }
     }
   }
 }
 
-// One block per (sequence, KV head).  The select-th largest key by four 8-bit
-// digits, counted in a histogram per warp (scores share their leading bits, and
-// one histogram for all would queue every warp at a few counters); then the
-// kept pages in order, each thread with 8 consecutive ones.
-__global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, int stride) {
-  extern __shared__ uint32_t hist[];  // [warps][256]
-  __shared__ uint32_t s_prefix, s_left;
-  __shared__ int s_warp[32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int bh = blockIdx.x, b = bh / a.Hkv, tid = threadIdx.x, w = warp_id(), lane = lane_id();
+// The largest key k with (number of keys >= k) >= keep among keys[0, n), and
+// how many of the keys equal to it belong to the first `keep`: by digits of
+// `bits` bits, counted in kTopkCopies histograms (scores share their leading
+// bits, and in one histogram all warps would queue at a few counters).
+constexpr int kTopkCopies = 4;
+constexpr int kTopkOpen = 512;  // pages whose exact rank is found one by one
+struct TopkShared {
+  uint32_t prefix, left;
+  int warp[32];
+};
+__device__ __forceinline__ void load_keys(const uint32_t* keys, int j, uint32_t* x) {
+  *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(keys + j);
+  *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(keys + j + 4);
+}
+__device__ __forceinline__ void nth_key(const uint32_t* keys, int n, int keep, int bits, uint32_t* hist,
+                                        TopkShared& sh, uint32_t* key, int* equal) {
+  const int tid = threadIdx.x, w = warp_id(), lane = lane_id(), warps = blockDim.x / 32;
+  const int bins = 1 << bits, per = bins / blockDim.x;  // 2 or 4 neighbouring bins per thread
+  uint32_t prefix = 0, left = keep;
+  for (int rest = 32; rest > 0;) {
+    const int width = min(bits, rest), shift = rest - width;
+    for (int i = tid; i < kTopkCopies * bins / 4; i += blockDim.x)
+      reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    uint32_t* mine = hist + (w % kTopkCopies) * bins;
+    for (int j = tid * kTopkKeys; j < n; j += blockDim.x * kTopkKeys) {
+      uint32_t x[kTopkKeys];
+      load_keys(keys, j, x);
+#pragma unroll
+      for (int i = 0; i < kTopkKeys; ++i)
+        if (j + i < n && (rest == 32 || x[i] >> rest == prefix))
+          atomicAdd(&mine[(x[i] >> shift) & ((1u << width) - 1u)], 1u);
+    }
+    __syncthreads();
+    // counts from the top bin down
+    uint32_t own = 0;
+    for (int i = 0; i < per; ++i) {
+      const int d = bins - 1 - tid * per - i;
+      uint32_t c = 0;
+#pragma unroll
+      for (int k = 0; k < kTopkCopies; ++k) c += hist[k * bins + d];
+      hist[d] = c;  // in copy 0: the bin is this thread's
+      own += c;
+    }
+    uint32_t upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    if (lane == 31) sh.warp[w] = static_cast<int>(upto);
+    __syncthreads();
+    uint32_t above = __reduce_add_sync(0xffffffffu, lane < w && lane < warps ? sh.warp[lane] : 0) + upto - own;
+    if (above < left && left <= above + own) {
+      for (int i = 0; i < per; ++i) {
+        const int d = bins - 1 - tid * per - i;
+        const uint32_t c = hist[d];
+        if (left <= above + c) {
+          sh.prefix = (prefix << width) | static_cast<uint32_t>(d);
+          sh.left = left - above;
+          break;
+        }
+        above += c;
+      }
+    }
+    __syncthreads();
+    prefix = sh.prefix;
+    left = sh.left;
+    rest = shift;
+  }
+  *key = prefix;
+  *equal = static_cast<int>(left);
+}
+
+__device__ __forceinline__ float key_score(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
+// One block per (sequence, KV head): the threshold, the pages around it again
+// where their order is not certain, then the kept pages in order.
+__global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, int stride, int bits) {
+  extern __shared__ uint32_t hist[];  // [kTopkCopies][2^bits]
+  __shared__ TopkShared sh;
+  __shared__ double s_q[128];
+  __shared__ uint32_t s_key[kTopkOpen];
+  __shared__ int s_page[kTopkOpen], s_open;
+  pdl_begin();
+  const int bh = blockIdx.x, b = bh / a.Hkv, h = bh % a.Hkv, tid = threadIdx.x, w = warp_id(), lane = lane_id();
   const int warps = blockDim.x / 32, step = blockDim.x * kTopkKeys;
   const int len = a.lens[b];
-  const bool bad = len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_pages) * a.page;
+  const bool bad = bad_length(a, len);
   if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
   const int n = bad || len == 0 ? 0 : (len - 1) / a.page + 1;
   const int keep = min(n, a.select);
-  const uint32_t* keys = a.keys + static_cast<size_t>(bh) * stride;
+  uint32_t* keys = a.keys + 2 * static_cast<size_t>(bh) * stride;
+  const float* offs = reinterpret_cast<const float*>(keys + stride);
   int32_t* sel = a.sel + static_cast<size_t>(bh) * a.select;
   for (int i = keep + tid; i < a.select; i += blockDim.x) sel[i] = -1;
   if (n <= keep) {
     for (int i = tid; i < n; i += blockDim.x) sel[i] = i;
     return;
   }
-  uint32_t prefix = 0, left = keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < warps * 256; i += blockDim.x) hist[i] = 0;
+  uint32_t least;  // kept: keys above it, and the first `equal` that equal it
+  int equal;
+  nth_key(keys, n, keep, bits, hist, sh, &least, &equal);
+  if (least != kKeyForced && least != kKeyBad) {
+    // the largest error bound of the sequence
+    float off = 0.f;
+    for (int j = tid; j < n; j += blockDim.x) off = fmaxf(off, offs[j]);
+    off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(off)));  // >= 0: ordered as integers
+    if (lane == 0) sh.warp[w] = __float_as_int(off);
     __syncthreads();
-    for (int j = tid * kTopkKeys; j < n; j += step) {
-      uint32_t x[kTopkKeys];
-      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(keys + j);
-      *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(keys + j + 4);
-#pragma unroll
-      for (int i = 0; i < kTopkKeys; ++i)
-        if (j + i < n && (shift == 24 || (x[i] >> (shift + 8)) == prefix))
-          atomicAdd(&hist[w * 256 + ((x[i] >> shift) & 255u)], 1u);
+    off = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? static_cast<uint32_t>(sh.warp[lane]) : 0u));
+    const float t = key_score(least);
+    uint32_t lo = kKeyBad + 1, hi = kKeyForced - 1;  // infinities or NaN around: every page again
+    if (fabsf(t) < INFINITY && off < INFINITY) {
+      lo = score_key_bits(__float_as_uint(t - 2.f * off));
+      hi = score_key_bits(__float_as_uint(t + 2.f * off));
     }
+    int upper = 0;  // pages from lo on
+    for (int j = tid; j < n; j += blockDim.x) upper += keys[j] >= lo;
+    upper = __reduce_add_sync(0xffffffffu, upper);
     __syncthreads();
-    for (int d = tid; d < 256; d += blockDim.x) {
-      uint32_t c = 0;
-      for (int i = 0; i < warps; ++i) c += hist[i * 256 + d];
-      hist[d] = c;  // row 0; each column is one thread's
-    }
+    if (lane == 0) sh.warp[w] = upper;
     __syncthreads();
-    if (w == 0) {  // lane i: digits 255 - 8 i down to 248 - 8 i
-      uint32_t c[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
-      uint32_t upto = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += y;
+    upper = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
+    if (upper == keep) {
+      least = lo - 1;  // all of them, none equal
+      equal = 0;
+    } else {
+      // the exact scores of the pages in [lo, hi]
+      const int group = a.Hq / a.Hkv;
+      for (int d = tid; d < a.D; d += blockDim.x) {
+        const __nv_bfloat16* q = a.q + b * a.q_stride + static_cast<size_t>(h) * group * a.D + d;
+        double s = 0;
+        for (int i = 0; i < group; ++i) s += static_cast<double>(__bfloat162float(q[static_cast<size_t>(i) * a.D]));
+        s_q[d] = s;
       }
-      uint32_t above = upto - sum;
-      if (above < left && left <= upto) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < left && left <= above + c[i]) {
-            s_prefix = (prefix << 8) | (255 - 8 * lane - i);
-            s_left = left - above;
-          }
-          above += c[i];
+      if (tid == 0) s_open = 0;
+      __syncthreads();
+      int above = 0;
+      for (int j = tid; j < n; j += blockDim.x) {
+        const uint32_t key = keys[j];
+        above += key > hi;
+        if (key >= lo && key <= hi) {
+          const int i = atomicAdd(&s_open, 1);  // (their order says nothing about the result)
+          if (i < kTopkOpen) s_page[i] = j;
         }
       }
+      above = __reduce_add_sync(0xffffffffu, above);
+      if (lane == 0) sh.warp[w] = above;
+      __syncthreads();
+      above = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
+      auto exact_key = [&](int j) {
+        // (a page number that the score kernel found inside the cache)
+        const __nv_bfloat16* mean =
+            a.k_mean + (static_cast<size_t>(a.table[static_cast<size_t>(b) * a.max_pages + j]) * a.Hkv + h) * a.D;
+        double s = 0;
+        for (int d = lane; d < a.D; d += 32) s += s_q[d] * static_cast<double>(__bfloat162float(mean[d]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return score_key_bits(__float_as_uint(static_cast<float>(s)));
+      };
+      const int open = s_open;
+      if (open <= kTopkOpen) {
+        // few: each one's rank among them, the best become forced, the others bad
+        for (int i = w; i < open; i += warps) {
+          const uint32_t key = exact_key(s_page[i]);
+          if (lane == 0) s_key[i] = key;
+        }
+        __syncthreads();
+        for (int i = tid; i < open; i += blockDim.x) {
+          int rank = 0;
+          for (int k = 0; k < open; ++k)
+            rank += s_key[k] > s_key[i] || (s_key[k] == s_key[i] && s_page[k] < s_page[i]);
+          keys[s_page[i]] = rank < keep - above ? kKeyForced : kKeyBad;
+        }
+        least = hi;
+        equal = 0;
+        __syncthreads();
+      } else {
+        // ties en masse: exact keys for all of them, forced and bad ones for the rest,
+        // and the threshold again
+        for (int j0 = w * 32; j0 < n; j0 += warps * 32) {
+          uint32_t key = j0 + lane < n ? keys[j0 + lane] : kKeyBad;
+          uint32_t todo = __ballot_sync(0xffffffffu, key >= lo && key <= hi);
+          key = key > hi ? kKeyForced : kKeyBad;
+          while (todo != 0) {
+            const int k = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const uint32_t x = exact_key(j0 + k);
+            if (lane == k) key = x;
+          }
+          if (j0 + lane < n) keys[j0 + lane] = key;
+        }
+        __syncthreads();
+        nth_key(keys, n, keep, bits, hist, sh, &least, &equal);
+      }
     }
-    __syncthreads();
-    prefix = s_prefix;
-    left = s_left;
   }
-  // keys above `prefix` are kept, and the first `left` that equal it
   int more0 = 0, same0 = 0;
   for (int base = 0; base < n; base += step) {
     const int j = base + tid * kTopkKeys;
     uint32_t x[kTopkKeys] = {};
-    if (j < n) {
-      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(keys + j);
-      *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(keys + j + 4);
-    }
+    if (j < n) load_keys(keys, j, x);
     int own = 0;  // kept above in the low half, equal in the high half
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i)
-      if (j + i < n) own += x[i] > prefix ? 1 : (x[i] == prefix ? 0x10000 : 0);
+      if (j + i < n) own += x[i] > least ? 1 : (x[i] == least ? 0x10000 : 0);
     int upto = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -647,23 +756,20 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
       if (lane >= d) upto += y;
     }
     __syncthreads();
-    if (lane == 31) s_warp[w] = upto;
+    if (lane == 31) sh.warp[w] = upto;
     __syncthreads();
-    int before = upto - own, all = 0;
-    for (int i = 0; i < warps; ++i) {
-      const int y = s_warp[i];
-      if (i < w) before += y;
-      all += y;
-    }
+    const int there = lane < warps ? sh.warp[lane] : 0;
+    const int before = upto - own + __reduce_add_sync(0xffffffffu, lane < w ? there : 0);
+    const int all = __reduce_add_sync(0xffffffffu, there);
     int more = more0 + (before & 0xFFFF), same = same0 + (before >> 16);
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i) {
       if (j + i >= n) break;
-      if (x[i] > prefix) {
-        sel[more + min(same, static_cast<int>(left))] = j + i;
+      if (x[i] > least) {
+        sel[more + min(same, equal)] = j + i;
         ++more;
-      } else if (x[i] == prefix) {
-        if (same < static_cast<int>(left)) sel[more + same] = j + i;
+      } else if (x[i] == least) {
+        if (same < equal) sel[more + same] = j + i;
         ++same;
       }
     }
@@ -683,31 +789,21 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  paged_plan_kernel<<<1, threads, smem, stream>>>(a, place);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(paged_plan_kernel, 1, threads, smem, stream, a, place);
   if (e != cudaSuccess || place) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min((a.T + 256 * kPlanAtOnce - 1) / (256 * kPlanAtOnce), 1024));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = (static_cast<size_t>(a.B) + 1) * sizeof(int32_t);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_place_kernel, a);
+  return launch_dependent(paged_place_kernel, std::min((a.T + 256 * kPlanAtOnce - 1) / (256 * kPlanAtOnce), 1024), 256,
+                          (static_cast<size_t>(a.B) + 1) * sizeof(int32_t), stream, a);
 }
 
 template <int D, bool E4M3>
-static void write_launch(const WriteArgs& a, cudaStream_t stream) {
+static cudaError_t write_launch(const WriteArgs& a, cudaStream_t stream) {
   constexpr int GROUPS = kWriteThreads / (D / 8);
   // four rows per thread once that leaves every SM (152) eight blocks
   const bool many = static_cast<long long>(a.T) * a.Hkv >= 152LL * 8 * 4 * GROUPS;
   const int window = GROUPS * (many ? 4 : 1);
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.T) + window - 1) / window * a.Hkv);
-  if (many) paged_write_kernel<D, E4M3, 4><<<blocks, kWriteThreads, 0, stream>>>(a);
-  else paged_write_kernel<D, E4M3, 1><<<blocks, kWriteThreads, 0, stream>>>(a);
+  return many ? launch_dependent(paged_write_kernel<D, E4M3, 4>, blocks, kWriteThreads, 0, stream, a)
+              : launch_dependent(paged_write_kernel<D, E4M3, 1>, blocks, kWriteThreads, 0, stream, a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t stream) {
@@ -725,16 +821,15 @@ cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t strea
   };
   c.k_most = most(a.k_scale);
   c.v_most = most(a.v_scale);
-  if (a.D == 128) e4m3 ? write_launch<128, true>(c, stream) : write_launch<128, false>(c, stream);
-  else e4m3 ? write_launch<64, true>(c, stream) : write_launch<64, false>(c, stream);
-  return cudaGetLastError();
+  if (a.D == 128) return e4m3 ? write_launch<128, true>(c, stream) : write_launch<128, false>(c, stream);
+  return e4m3 ? write_launch<64, true>(c, stream) : write_launch<64, false>(c, stream);
 }
 
 // Keys of a row: whole 16-byte words for every thread's eight.
 static int key_stride(int max_pages) { return (max_pages + kTopkKeys - 1) / kTopkKeys * kTopkKeys; }
 
 size_t paged_select_workspace_bytes(int B, int Hkv, int max_pages) {
-  return static_cast<size_t>(B) * Hkv * key_stride(max_pages) * sizeof(uint32_t);
+  return 2 * static_cast<size_t>(B) * Hkv * key_stride(max_pages) * sizeof(uint32_t);
 }
 
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
@@ -743,28 +838,19 @@ cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
   // 32 pages per warp; fewer where that would leave SMs idle
   int per_warp = 32;
   while (per_warp > 8 && static_cast<long long>(a.B) * head_blocks *
-                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 304)
+                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 152 * 4)
     per_warp /= 2;
   const int page_blocks = (a.max_pages + 8 * per_warp - 1) / (8 * per_warp);
   const unsigned blocks = static_cast<unsigned>(static_cast<long long>(a.B) * head_blocks * page_blocks);
-  if (a.D == 128)
-    paged_score_kernel<128><<<blocks, kScoreThreads, 0, stream>>>(a, head_blocks, page_blocks, per_warp, stride);
-  else
-    paged_score_kernel<64><<<blocks, kScoreThreads, 0, stream>>>(a, head_blocks, page_blocks, per_warp, stride);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(a.D == 128 ? paged_score_kernel<128> : paged_score_kernel<64>, blocks,
+                                   kScoreThreads, 0, stream, a, head_blocks, page_blocks, per_warp, stride);
   if (e != cudaSuccess) return e;
+  // three digits over 2048 counters for long lists, four over 256 for short ones, whose
+  // counters would cost more than their keys (512 lists of up to 512 pages: 38 us and TOPK_US)
   const int threads = a.max_pages > 4096 ? 1024 : (a.max_pages > 1024 ? 512 : 128);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.B * a.Hkv);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = threads / 32 * 256 * sizeof(uint32_t);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_topk_kernel, a, stride);
+  const int bits = threads == 128 ? 8 : 11;
+  return launch_dependent(paged_topk_kernel, a.B * a.Hkv, threads, (kTopkCopies << bits) * sizeof(uint32_t), stream, a,
+                          stride, bits);
 }
 
 }  // namespace mcs

@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace mcs {
@@ -187,6 +188,7 @@ template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kRopeThreads, Tune<D>::BLOCKS)
     norm_rope_kernel(const RopeArgs a, int chunks_q, int chunks) {
   constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::STEPS;  // ROWS: rows per load
+  pdl_begin();
   const unsigned tile = blockIdx.x / static_cast<unsigned>(chunks);
   const int chunk = static_cast<int>(blockIdx.x - tile * chunks);
   const unsigned token = tile * kRopeWarps + warp_id();
@@ -247,6 +249,7 @@ template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
     norm_rope_backward_kernel(const RopeArgs a, int blocks_q, int blocks_k) {
   constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::GRAD_STEPS;
+  pdl_begin();
   const bool is_q = static_cast<int>(blockIdx.x) < blocks_q;
   const int H = is_q ? a.Hq : a.Hkv;
   const unsigned chunks = (H + heads_per_warp(D, Tune<D>::GRAD_STEPS) - 1) / heads_per_warp(D, Tune<D>::GRAD_STEPS);
@@ -259,7 +262,6 @@ __global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
   const long long stride = is_q ? a.q_stride : a.k_stride;
   uint64_t wa[2], wb[2], da[2] = {0, 0}, db[2] = {0, 0};
   load_weights<SPLIT>(is_q ? a.wq : a.wk, at, wa, wb);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (unsigned u = block; u < units; u += blocks) {
     const unsigned tile = u / chunks, token = tile * kRopeWarps + warp_id();
     if (token >= tokens) continue;  // whole warps
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int
                                                            int blocks_k) {
   constexpr int COLS = D / 4, SIDES = 1024 / COLS;
   __shared__ float4 sums[SIDES][COLS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_begin();
   const bool is_q = blockIdx.x == 0;
   float* out = is_q ? a.dwq : a.dwk;
   if (out == nullptr) return;
@@ -379,9 +381,8 @@ cudaError_t forward(const RopeArgs& a, cudaStream_t stream) {
   const int cq = (a.Hq + heads - 1) / heads, ck = (a.Hkv + heads - 1) / heads;
   const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
   const unsigned blocks = static_cast<unsigned>(tiles * (cq + ck));
-  if (a.interleaved) norm_rope_kernel<D, false><<<blocks, kRopeThreads, 0, stream>>>(a, cq, cq + ck);
-  else norm_rope_kernel<D, true><<<blocks, kRopeThreads, 0, stream>>>(a, cq, cq + ck);
-  return cudaGetLastError();
+  return launch_dependent(a.interleaved ? norm_rope_kernel<D, false> : norm_rope_kernel<D, true>, blocks,
+                          kRopeThreads, 0, stream, a, cq, cq + ck);
 }
 
 template <int D>
@@ -395,20 +396,11 @@ cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
   const int limit_q = ck ? static_cast<int>(std::max<long long>(1, std::min<long long>(share, limit - 1))) : limit;
   const int bq = static_cast<int>(std::min<long long>(tiles * cq, limit_q));
   const int bk = static_cast<int>(std::min<long long>(tiles * ck, limit - limit_q));
-  if (a.interleaved) norm_rope_backward_kernel<D, false><<<bq + bk, kRopeThreads, 0, stream>>>(a, bq, bk);
-  else norm_rope_backward_kernel<D, true><<<bq + bk, kRopeThreads, 0, stream>>>(a, bq, bk);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(
+      a.interleaved ? norm_rope_backward_kernel<D, false> : norm_rope_backward_kernel<D, true>, bq + bk, kRopeThreads,
+      0, stream, a, bq, bk);
   if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.Hkv ? 2 : 1);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weight_grad_kernel<D>, a, bq, bk);
+  return launch_dependent(weight_grad_kernel<D>, a.Hkv ? 2 : 1, 1024, 0, stream, a, bq, bk);
 }
 
 }  // namespace
