@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "launch.cuh"
@@ -85,10 +86,9 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Workspace: exclusive sums of the sequences' tiles and of the sequences that
-// have any [2 (B + 1)], then the parts: (log2 maximum, sum) of each row and the
-// rows' D sums.
-__host__ __device__ constexpr size_t parts_offset() { return ((4096 + 1) * 16 + 255) / 256 * 256; }
+// Workspace: exclusive sums of the sequences' positions [B + 1] (see below), then
+// the parts: (log2 maximum, sum) of each row and the rows' D sums.
+__host__ __device__ constexpr size_t parts_offset() { return ((4096 + 1) * 8 + 255) / 256 * 256; }
 __host__ __device__ constexpr size_t part_floats(int D, bool wide) { return (wide ? 16 : 8) * (2 + D); }
 
 // Pages are powers of two.
@@ -111,8 +111,17 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
 }
 
 // The list of all segments (a segment: one sequence, one KV head, up to 16
-// query heads) has tiles + kSegCost positions for each; warp i of `warps` takes
-// positions [i * all / warps, (i + 1) * all / warps) and the tiles that begin there.
+// query heads) has tiles + kSegCost positions for each that has tiles; warp i of
+// `warps` takes positions [i * all / warps, (i + 1) * all / warps) and the tiles
+// that begin there.
+template <int TK>
+__device__ __forceinline__ int positions_of(const DecodeArgs& a, int b) {
+  const int tiles = tiles_of<TK>(a, b);
+  return tiles > 0 ? tiles + kSegCost : 0;
+}
+__device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
+  return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
+}
 __device__ __forceinline__ long long active_warps(long long all, int ctas) {
   return min(all, static_cast<long long>(ctas) * kWarps);
 }
@@ -165,8 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr float kShift = E4M3 ? 12.f : 0.f;   // weights carry 2^12 so that f16 holds small ones
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_cnt[kWarps][kStages];
-  __shared__ long long s_sum[kWarps][2], s_off[kWarps], s_share[kWarps][2];
-  __shared__ int s_b[kWarps], s_seg[kWarps];
+  __shared__ int s_seg[kWarps];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
 
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
@@ -177,78 +185,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   pdl_begin();
 
-  // ---- the shares: sums over the sequences' tiles, 256 sequences at a time
-  // (inclusive in x and y; a batch of up to 256 needs one round)
-  long long x = 0, y = 0, own = 0, all_t = 0, all_s = 0;
-  auto scan = [&](int b) {
-    own = b < a.B ? tiles_of<TK>(a, b) : 0;
-    x = own;
-    y = own > 0;
+  // ---- this warp's share, found by itself: lane i sums sequences [i * per, (i + 1) * per),
+  // one scan over the lanes, and one over the sequences of the lane that holds the start
+  const int per = (a.B + 31) / 32, b_lane = lane * per;
+  long long own = 0;
+#pragma unroll 4
+  for (int i = 0; i < per; ++i)
+    if (b_lane + i < a.B) own += positions_of<TK>(a, b_lane + i);
+  auto scan = [&](long long x) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
-      if (lane >= d) x += u, y += v;
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
     }
-    __syncthreads();
-    if (lane == 31) s_sum[w][0] = x, s_sum[w][1] = y;
-    __syncthreads();
-    long long sum_t = 0, sum_s = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < w) x += s_sum[i][0], y += s_sum[i][1];
-      sum_t += s_sum[i][0];
-      sum_s += s_sum[i][1];
-    }
-    x += all_t;
-    y += all_s;
-    all_t += sum_t;
-    all_s += sum_s;
+    return x;
   };
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    scan(b0 + tid);
-    if (blockIdx.x == 0 && b0 + tid < a.B) {
-      prefix[2 * (b0 + tid)] = x - own;
-      prefix[2 * (b0 + tid) + 1] = y - (own > 0);
-      if (own == 0 && a.lens[b0 + tid] != 0) atomicOr(a.status, DEV_BOUNDS);
+  const long long upto = scan(own), all = __shfl_sync(0xffffffffu, upto, 31) * segs;
+  if (blockIdx.x == 0 && w == 0) {
+    long long sum = upto - own;
+    for (int b = b_lane; b < min(a.B, b_lane + per); ++b) {
+      const int x = positions_of<TK>(a, b);
+      if (x == 0 && a.lens[b] != 0) atomicOr(a.status, DEV_BOUNDS);
+      prefix[b] = sum;
+      sum += x;
     }
+    if (lane == 31) prefix[a.B] = upto;
   }
-  const long long all = (all_t + all_s * kSegCost) * segs;
   const long long warps = active_warps(all, gridDim.x);
   const long long me = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (tid < 2 * kWarps) {  // starts and ends; an empty share for the warps that are not needed
-    const long long i = static_cast<long long>(blockIdx.x) * kWarps + tid % kWarps;
-    s_share[tid % kWarps][tid / kWarps] = i < warps ? (i + tid / kWarps) * all / warps : -1;
-  }
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0) prefix[2 * a.B] = all_t, prefix[2 * a.B + 1] = all_s;
-  if (a.B > kThreads) all_t = all_s = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    if (a.B > kThreads) scan(b0 + tid);
-    const long long end = (x + y * kSegCost) * segs;
-    const long long first = end - (own + (own > 0) * kSegCost) * segs;
-    if (own > 0) {
-      // each warp's start that falls into this sequence
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const long long at = s_share[i][0];
-        if (first <= at && at < end) {
-          s_b[i] = b0 + tid;
-          s_off[i] = at - first;
-        }
-      }
-    }
-  }
-  __syncthreads();
-  if (s_share[0][0] < 0 || all == 0) return;  // a CTA without a share
-  const long long lo = s_share[w][0], hi = s_share[w][1];
-
+  if (static_cast<long long>(blockIdx.x) * kWarps >= warps) return;  // a CTA without a share
   Walk here = {};
-  bool busy = lo < hi;  // from here on each warp is alone
+  bool busy = me < warps;
   if (busy) {
-    here.b = s_b[w];
-    here.tb = tiles_of<TK>(a, here.b);
-    here.seg = static_cast<int>(s_off[w] / (here.tb + kSegCost));
-    here.t0 = static_cast<int>(s_off[w] % (here.tb + kSegCost));
+    const long long lo = divide(me * all, warps), hi = divide((me + 1) * all, warps);
+    // (all > 0: some lane's sequences hold position lo)
+    const int from = __ffs(__ballot_sync(0xffffffffu, lo < upto * segs)) - 1;
+    long long base = __shfl_sync(0xffffffffu, upto - own, from);
+    for (int b0 = from * per;; b0 += 32) {
+      const int b = b0 + lane;
+      const long long x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, b) : 0;
+      const long long y = scan(x);
+      const uint32_t hit = __ballot_sync(0xffffffffu, lo < (base + y) * segs);
+      if (hit != 0) {
+        const int at = __ffs(hit) - 1;
+        const long long first = (base + __shfl_sync(0xffffffffu, y - x, at)) * segs;
+        const long long size = __shfl_sync(0xffffffffu, x, at);
+        here.b = b0 + at;
+        here.tb = static_cast<int>(size) - kSegCost;
+        here.seg = static_cast<int>(divide(lo - first, size));
+        here.t0 = static_cast<int>(lo - first - here.seg * size);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, y, 31);
+    }
     here.left = hi - lo;
     here.count = static_cast<int>(min(static_cast<long long>(here.tb - here.t0), here.left));
     if (here.count <= 0) busy = next_segment<TK>(here, a, segs);
@@ -593,7 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kJoinThreads = 256;
-static_assert(kMaxCtas + 1 <= kJoinThreads, "a thread takes one part's maximum and sum");
 
 // The share that holds position x: the largest i with i * all < (x + 1) * warps.
 __device__ __forceinline__ int share_of(long long x, long long all, long long warps) {
@@ -605,104 +593,142 @@ __device__ __forceinline__ int share_of(long long x, long long all, long long wa
   return i;
 }
 
-// One block per query head and 1/splits of its columns: joins the parts of a
-// segment that reaches over several CTAs, in the order of its tiles, and
-// writes the rows of sequences that hold nothing.  Latency: the sums, then maxima,
-// sums and values in one go (a thread's first four parts are on their way while
-// the weights are found).
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kJoinThreads)
-    paged_join_kernel(const DecodeArgs a, int chunks, int grid, bool wide, int splits) {
-  __shared__ float s_f[kJoinThreads];  // weight of each part
-  __shared__ float s_top[kJoinThreads / 32], s_sum[kJoinThreads / 32];
-  __shared__ float4 s_acc[kJoinThreads / 32][32];
-  constexpr float kShift = E4M3 ? 12.f : 0.f;
-  pdl_begin();
-  const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
-  const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * (D / splits);
-  const int b = head / a.Hq, hq = head % a.Hq, group = a.Hq / a.Hkv;
-  const int row = hq % group % kHeads;
-  const int seg = hq / group * chunks + hq % group / kHeads, segs = a.Hkv * chunks;
-  const longlong2* prefix = static_cast<const longlong2*>(a.ws);
-  const float* parts =
-      reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
-  const longlong2 p0 = prefix[b], p1 = prefix[b + 1], end = prefix[a.B];
-  const long long tb = p1.x - p0.x, all = (end.x + end.y * kSegCost) * segs;
-  const int cols = D / splits / 4;  // columns in fours
-  if (tb == 0) {
-    if (tid < cols)
-      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(head) * D + col0 + 4 * tid) = make_uint2(0, 0);
-    if (a.lse != nullptr && col0 == 0 && tid == 0) a.lse[head] = -INFINITY;
-    return;
-  }
-  const long long warps = active_warps(all, grid);
-  const long long first = (p0.x + p0.y * kSegCost) * segs + seg * (tb + kSegCost);
-  const int c0 = share_of(first, all, warps), c1 = share_of(first + tb - 1, all, warps);
-  if (c0 == c1) return;
+// The parts of a query head whose segment reaches over several shares.
+struct Parts {
+  int c0, c1;      // first and last share
+  int k0, n;       // first CTA, number of parts (0: the row is complete)
+  bool empty;      // the sequence holds nothing
+};
+__device__ __forceinline__ Parts parts_of(const DecodeArgs& a, int head, int chunks, int grid) {
+  const int b = head / a.Hq, hq = head - b * a.Hq, group = a.Hq / a.Hkv, h = hq / group;
+  const int segs = a.Hkv * chunks, seg = h * chunks + (hq - h * group) / kHeads;
+  const long long* prefix = static_cast<const long long*>(a.ws);
+  const long long p0 = prefix[b], size = prefix[b + 1] - p0, all = prefix[a.B] * segs;
+  Parts p = {};
+  p.empty = size == 0;
+  if (p.empty) return p;
+  const long long warps = active_warps(all, grid), first = p0 * segs + seg * size;
+  p.c0 = share_of(first, all, warps);
+  p.c1 = share_of(first + size - kSegCost - 1, all, warps);
   // shares c0 to c1 - 1 go on to the next one and are joined per CTA (the second
   // part of the CTA's first such warp); share c1 ends the segment (its first part)
+  p.k0 = p.c0 / kWarps;
+  if (p.c0 != p.c1) p.n = (p.c1 - 1) / kWarps - p.k0 + 2;
+  return p;
+}
+
+// Joins the parts of segments that several warps share, in the order of their
+// tiles, and writes the rows of sequences that hold nothing.  A warp takes a
+// query head; one with many parts is taken by the whole block, as is every head
+// when there are few (HPB = 1).  Latency: the sums, then maxima, sums and values
+// of up to 32 parts at a time.
+template <int D, bool E4M3, int HPB>
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const DecodeArgs a, int chunks, int grid, bool wide) {
+  constexpr int JW = kJoinThreads / 32, V = D / 32;  // a lane holds V columns
+  constexpr float kShift = E4M3 ? 12.f : 0.f;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  __shared__ float s_sum[JW];
+  __shared__ float s_acc[JW][D];
+  __shared__ uint32_t s_many[JW];
+  pdl_begin();
+  const int lane = lane_id(), w = warp_id();
   const size_t size = part_floats(D, wide);
-  const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
-  auto part = [&](int i) {
-    const int warp = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
-    return parts + (2 * static_cast<size_t>(warp) + (i < n - 1)) * size;
-  };
-  // `cols` neighbouring threads take a part, the block 256 / cols parts at a time
-  const int col = tid % cols, side = tid / cols, sides = kJoinThreads / cols;
-  const int at = 2 * (wide ? 16 : 8) + row * D + col0 + 4 * col;
-  float4 x[4];
-  const float2 ml = tid < n ? *reinterpret_cast<const float2*>(part(tid) + 2 * row) : make_float2(-INFINITY, 0.f);
+  const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
+  const int heads = a.B * a.Hq, group = a.Hq / a.Hkv;
+
+  // sums of the head's parts first, first + step, ... in units of 2^top
+  float top, sum, acc[V];
+  auto join = [&](int head, const Parts& p, int first, int step) {
+    const int row = head % a.Hq % group % kHeads;
+    auto part = [&](int i) {
+      const int warp = i == p.n - 1 ? p.c1 : max(p.c0, (p.k0 + i) * kWarps);
+      return parts + (2 * static_cast<size_t>(warp) + (i < p.n - 1)) * size;
+    };
+    top = -INFINITY;
+    for (int i = lane; i < p.n; i += 32) top = fmaxf(top, part(i)[2 * row]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = side + k * sides;
-    if (i < n) x[k] = *reinterpret_cast<const float4*>(part(i) + at);
-  }
-  float top = ml.x;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_top[w] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, s_top[i]);
-  const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-  s_f[tid] = f;
-  float sum = tid < n ? ml.y * f : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[w] = sum;
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float4& v, float f) {
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
-  };
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (side + k * sides < n) add(x[k], s_f[side + k * sides]);
-#pragma unroll 4
-  for (int i = side + 4 * sides; i < n; i += sides) add(*reinterpret_cast<const float4*>(part(i) + at), s_f[i]);
-  for (int o = 16; o >= cols; o >>= 1) {
-    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
-    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-  }
-  if (lane < cols) s_acc[w][lane] = acc;
-  __syncthreads();
-  if (tid < cols) {
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) {
-      sum += s_sum[i];
-      if (i > 0) add(s_acc[i][tid], 1.f);
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+    const float* rows = nullptr;
+    for (int i0 = first; i0 < p.n; i0 += 32 * step) {
+      const int i = i0 + lane * step;
+      float f = 0.f;
+      if (i < p.n) {
+        const float2 ml = *reinterpret_cast<const float2*>(part(i) + 2 * row);
+        f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+        sum += ml.y * f;
+      }
+      const int here = min(32, (p.n - i0 + step - 1) / step);
+      for (int k0 = 0; k0 < here; k0 += 8) {
+        Vec x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (k0 + k < here) {
+            rows = part(i0 + (k0 + k) * step) + 2 * (wide ? 16 : 8) + row * D;
+            x[k] = reinterpret_cast<const Vec*>(rows)[lane];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+          if (k0 + k < here) {
+            const float* v = reinterpret_cast<const float*>(&x[k]);
+#pragma unroll
+            for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], fk, acc[c]);
+          }
+        }
+      }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  };
+  auto write = [&](int head) {
     const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-    *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(head) * D + col0 + 4 * tid) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (a.lse != nullptr && col0 == 0 && tid == 0)
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.out + static_cast<size_t>(head) * D) + lane * (V / 2);
+#pragma unroll
+    for (int c = 0; c < V; c += 2) to[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+    if (a.lse != nullptr && lane == 0)
       a.lse[head] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
+  };
+
+  const int mine = blockIdx.x * HPB + (HPB == 1 ? 0 : w);
+  Parts p = {};
+  if (mine < heads) p = parts_of(a, mine, chunks, grid);
+  if (p.empty && (HPB > 1 || w == 0)) {
+    top = sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+    write(mine);
+  }
+  const bool many = p.n > (HPB == 1 ? 0 : 16);
+  if (!many && p.n > 0) {
+    join(mine, p, 0, 1);
+    write(mine);
+  }
+  if (lane == 0) s_many[w] = many;
+  __syncthreads();
+  for (int k = 0; k < HPB; ++k) {
+    if (!s_many[k]) continue;
+    const int head = blockIdx.x * HPB + k;
+    const Parts q = parts_of(a, head, chunks, grid);
+    join(head, q, w, JW);
+    if (lane == 0) s_sum[w] = sum;
+#pragma unroll
+    for (int c = 0; c < V; ++c) s_acc[w][lane * V + c] = acc[c];
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+      for (int i = 1; i < JW; ++i) {
+        sum += s_sum[i];
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] += s_acc[i][lane * V + c];
+      }
+      write(head);
+    }
+    __syncthreads();
   }
 }
 
@@ -720,10 +746,11 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + TK - 1) / TK + kSegCost);
   const int grid = static_cast<int>(std::min<long long>(std::min(sms, kMaxCtas), most));
   if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks)) != cudaSuccess) return e;
-  // few heads have many parts each: their columns go to several blocks
-  const int splits = a.B * a.Hq <= sms / 4 ? 8 : a.B * a.Hq <= sms ? 2 : 1;
-  return launch_dependent(paged_join_kernel<D, E4M3>, a.B * a.Hq * splits, kJoinThreads, 0, stream, a, chunks,
-                          grid, WIDE, splits);
+  const int heads = a.B * a.Hq;
+  if (heads <= 4 * sms)
+    return launch_dependent(paged_join_kernel<D, E4M3, 1>, heads, kJoinThreads, 0, stream, a, chunks, grid, WIDE);
+  return launch_dependent(paged_join_kernel<D, E4M3, 8>, (heads + 7) / 8, kJoinThreads, 0, stream, a, chunks, grid,
+                          WIDE);
 }
 
 }  // namespace

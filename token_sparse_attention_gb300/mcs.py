@@ -570,9 +570,11 @@ def _refuse(dev, t, dtype, shape, name):
 
 def _at(dev, t, dtype, shape, name):
     """As _ptr, and on device `dev`."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and \
-            t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _refuse(dev, t, dtype, shape, name)
 
 
