@@ -21,10 +21,17 @@
 // whole it writes at once.  Neighbouring warps' pieces of one segment are joined in
 // shared memory when the CTA is done, what crosses CTAs goes to the workspace, and a
 // second, programmatically dependent launch joins that in the order of the tiles.
+//
+// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) LONG_US us;
+// 64 x 1000 tokens of 8 KV heads, bf16 (262 MB) SHORT_US us; 1 x 1023 (4.2 MB) ONE_US us, most of
+// it latency (shares 1.5 us, page numbers and first loads 3 us, join 3 us).  What
+// bounds the long ones: SMs do not get equal parts of the bandwidth, equal shares
+// end up to 15 % apart, while the total runs above a copy's rate.  Handing the last fifth
+// out by a counter evened that (290 -> 270 us), but its sums, its counter and the
+// join of three times the parts cost as much, and ragged batches more.
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "internal.h"
 #include "launch.cuh"
@@ -38,7 +45,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kHalfStage = 4096;              // bytes of K (and of V) in a tile
 constexpr int kStageBytes = 2 * kHalfStage;
-constexpr int kMaxCtas = 192;                 // parts in the workspace: two per warp
+constexpr int kMaxCtas = 160;                 // parts in the workspace: two per warp
 constexpr int kSegCost = 1;                   // what starting a segment costs, in tiles
 constexpr int kHeads = 16;                    // query heads per pass over a KV head
 constexpr int kPidBits = 27;                  // num_pages * page < 2^31, page >= 16
@@ -581,8 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-constexpr int kJoinThreads = 256;
-
 // The share that holds position x: the largest i with i * all < (x + 1) * warps.
 __device__ __forceinline__ int share_of(long long x, long long all, long long warps) {
   const long long y = (x + 1) * warps;
@@ -593,142 +598,147 @@ __device__ __forceinline__ int share_of(long long x, long long all, long long wa
   return i;
 }
 
-// The parts of a query head whose segment reaches over several shares.
-struct Parts {
-  int c0, c1;      // first and last share
-  int k0, n;       // first CTA, number of parts (0: the row is complete)
-  bool empty;      // the sequence holds nothing
-};
-__device__ __forceinline__ Parts parts_of(const DecodeArgs& a, int head, int chunks, int grid) {
-  const int b = head / a.Hq, hq = head - b * a.Hq, group = a.Hq / a.Hkv, h = hq / group;
-  const int segs = a.Hkv * chunks, seg = h * chunks + (hq - h * group) / kHeads;
+// One block per segment: joins its parts if several shares hold tiles of it, in
+// the order of the tiles, and writes the rows of sequences that hold nothing.
+// All rows of a part are read together, SIDES parts at a time; a thread's first
+// four parts are on their way while the maxima and weights are found.
+template <int D, bool E4M3, bool WIDE, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    paged_join_kernel(const DecodeArgs a, int chunks, int grid) {
+  constexpr int ROWS = WIDE ? 16 : 8, E = ROWS * D / 4;               // fours of a part
+  constexpr int EPT = E > THREADS ? E / THREADS : 1, SIDES = E > THREADS ? 1 : THREADS / E;
+  constexpr int CHUNK = THREADS / ROWS, WARPS = THREADS / 32;         // parts weighed at a time
+  constexpr float kShift = E4M3 ? 12.f : 0.f;
+  __shared__ float s_red[WARPS][ROWS], s_top[ROWS], s_f[CHUNK][ROWS];
+  __shared__ float4 s_acc[SIDES][SIDES > 1 ? E : 1];
+  pdl_begin();
+  const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
+  const int group = a.Hq / a.Hkv, segs = a.Hkv * chunks, b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
+  const int h = seg / chunks, q0 = (seg - h * chunks) * kHeads, heads = min(kHeads, group - q0);
   const long long* prefix = static_cast<const long long*>(a.ws);
+  const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
   const long long p0 = prefix[b], size = prefix[b + 1] - p0, all = prefix[a.B] * segs;
-  Parts p = {};
-  p.empty = size == 0;
-  if (p.empty) return p;
+  const size_t out_row = static_cast<size_t>(b) * a.Hq + h * group + q0;
+  if (size == 0) {
+    uint2* out = reinterpret_cast<uint2*>(a.out + out_row * D);
+    for (int i = tid; i < heads * D / 4; i += THREADS) out[i] = make_uint2(0, 0);
+    if (a.lse != nullptr && tid < heads) a.lse[out_row + tid] = -INFINITY;
+    return;
+  }
   const long long warps = active_warps(all, grid), first = p0 * segs + seg * size;
-  p.c0 = share_of(first, all, warps);
-  p.c1 = share_of(first + size - kSegCost - 1, all, warps);
+  const int c0 = share_of(first, all, warps), c1 = share_of(first + size - kSegCost - 1, all, warps);
+  if (c0 == c1) return;
   // shares c0 to c1 - 1 go on to the next one and are joined per CTA (the second
   // part of the CTA's first such warp); share c1 ends the segment (its first part)
-  p.k0 = p.c0 / kWarps;
-  if (p.c0 != p.c1) p.n = (p.c1 - 1) / kWarps - p.k0 + 2;
-  return p;
-}
-
-// Joins the parts of segments that several warps share, in the order of their
-// tiles, and writes the rows of sequences that hold nothing.  A warp takes a
-// query head; one with many parts is taken by the whole block, as is every head
-// when there are few (HPB = 1).  Latency: the sums, then maxima, sums and values
-// of up to 32 parts at a time.
-template <int D, bool E4M3, int HPB>
-__global__ void __launch_bounds__(kJoinThreads)
-    paged_join_kernel(const DecodeArgs a, int chunks, int grid, bool wide) {
-  constexpr int JW = kJoinThreads / 32, V = D / 32;  // a lane holds V columns
-  constexpr float kShift = E4M3 ? 12.f : 0.f;
-  using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  __shared__ float s_sum[JW];
-  __shared__ float s_acc[JW][D];
-  __shared__ uint32_t s_many[JW];
-  pdl_begin();
-  const int lane = lane_id(), w = warp_id();
-  const size_t size = part_floats(D, wide);
-  const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
-  const int heads = a.B * a.Hq, group = a.Hq / a.Hkv;
-
-  // sums of the head's parts first, first + step, ... in units of 2^top
-  float top, sum, acc[V];
-  auto join = [&](int head, const Parts& p, int first, int step) {
-    const int row = head % a.Hq % group % kHeads;
-    auto part = [&](int i) {
-      const int warp = i == p.n - 1 ? p.c1 : max(p.c0, (p.k0 + i) * kWarps);
-      return parts + (2 * static_cast<size_t>(warp) + (i < p.n - 1)) * size;
-    };
-    top = -INFINITY;
-    for (int i = lane; i < p.n; i += 32) top = fmaxf(top, part(i)[2 * row]);
+  const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
+  auto part = [&](int i) {
+    const int c = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
+    return parts + (2 * static_cast<size_t>(c) + (i < n - 1)) * part_floats(D, WIDE);
+  };
+  const int side = tid / E, e0 = SIDES > 1 ? tid % E : tid;
+  auto values = [&](int i, int k) {
+    return *reinterpret_cast<const float4*>(part(i) + 2 * ROWS + 4 * (e0 + k * THREADS));
+  };
+  auto row_of = [&](int k) { return (e0 + k * THREADS) / (D / 4); };
+  float4 x[4][EPT];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    sum = 0.f;
+  for (int u = 0; u < 4; ++u) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] = 0.f;
-    const float* rows = nullptr;
-    for (int i0 = first; i0 < p.n; i0 += 32 * step) {
-      const int i = i0 + lane * step;
-      float f = 0.f;
-      if (i < p.n) {
-        const float2 ml = *reinterpret_cast<const float2*>(part(i) + 2 * row);
-        f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-        sum += ml.y * f;
+    for (int k = 0; k < EPT; ++k) {
+      x[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (side + u * SIDES < n && row_of(k) < heads) x[u][k] = values(side + u * SIDES, k);
+    }
+  }
+  // maxima and weights: thread (part, row r)
+  const int r = tid % ROWS, i_ml = tid / ROWS;
+  auto over_rows = [&](float v, bool max) {
+#pragma unroll
+    for (int o = 16; o >= ROWS; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, v, o);
+      v = max ? fmaxf(v, y) : v + y;
+    }
+    if (lane < ROWS) s_red[w][lane] = v;
+    __syncthreads();
+    for (int row = w; row < ROWS; row += WARPS) {  // a warp per row
+      v = lane < WARPS ? s_red[lane][row] : (max ? -INFINITY : 0.f);
+#pragma unroll
+      for (int o = WARPS / 2; o > 0; o >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, v, o);
+        v = max ? fmaxf(v, y) : v + y;
       }
-      const int here = min(32, (p.n - i0 + step - 1) / step);
-      for (int k0 = 0; k0 < here; k0 += 8) {
-        Vec x[8];
+      if (lane == 0) s_top[row] = v;
+    }
+    __syncthreads();
+  };
+  float top = -INFINITY;
+  if (r < heads)
+    for (int i = i_ml; i < n; i += CHUNK) top = fmaxf(top, part(i)[2 * r]);
+  over_rows(top, true);
+  top = s_top[r];
+  float sum = 0.f;
+  float4 acc[EPT];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (k0 + k < here) {
-            rows = part(i0 + (k0 + k) * step) + 2 * (wide ? 16 : 8) + row * D;
-            x[k] = reinterpret_cast<const Vec*>(rows)[lane];
-          }
-        }
+  for (int k = 0; k < EPT; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& v, float f, int k) {
+    acc[k].x = fmaf(v.x, f, acc[k].x);
+    acc[k].y = fmaf(v.y, f, acc[k].y);
+    acc[k].z = fmaf(v.z, f, acc[k].z);
+    acc[k].w = fmaf(v.w, f, acc[k].w);
+  };
+  for (int i0 = 0; i0 < n; i0 += CHUNK) {
+    float f = 0.f;
+    if (r < heads && i0 + i_ml < n) {
+      const float2 ml = *reinterpret_cast<const float2*>(part(i0 + i_ml) + 2 * r);
+      f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      sum += ml.y * f;
+    }
+    s_f[i_ml][r] = f;
+    __syncthreads();
+    const int end = min(n, i0 + CHUNK);
+    int i = i0 + side;
+    if (i0 == 0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
-          if (k0 + k < here) {
-            const float* v = reinterpret_cast<const float*>(&x[k]);
+      for (int u = 0; u < 4; ++u, i += SIDES) {
 #pragma unroll
-            for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], fk, acc[c]);
-          }
-        }
+        for (int k = 0; k < EPT; ++k)
+          if (i < end) add(x[u][k], s_f[i][row_of(k)], k);
       }
     }
+    for (; i < end; i += 4 * SIDES) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  };
-  auto write = [&](int head) {
-    const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-    uint32_t* to = reinterpret_cast<uint32_t*>(a.out + static_cast<size_t>(head) * D) + lane * (V / 2);
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-    for (int c = 0; c < V; c += 2) to[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
-    if (a.lse != nullptr && lane == 0)
-      a.lse[head] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kShift)) * 0.6931471805599453f;
-  };
-
-  const int mine = blockIdx.x * HPB + (HPB == 1 ? 0 : w);
-  Parts p = {};
-  if (mine < heads) p = parts_of(a, mine, chunks, grid);
-  if (p.empty && (HPB > 1 || w == 0)) {
-    top = sum = 0.f;
+        for (int k = 0; k < EPT; ++k)
+          if (i + u * SIDES < end && row_of(k) < heads) x[u][k] = values(i + u * SIDES, k);
 #pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] = 0.f;
-    write(mine);
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < EPT; ++k)
+          if (i + u * SIDES < end) add(x[u][k], s_f[i + u * SIDES - i0][row_of(k)], k);
+    }
+    __syncthreads();
   }
-  const bool many = p.n > (HPB == 1 ? 0 : 16);
-  if (!many && p.n > 0) {
-    join(mine, p, 0, 1);
-    write(mine);
-  }
-  if (lane == 0) s_many[w] = many;
+  if (SIDES > 1) s_acc[side][e0] = acc[0];
+  float tops[EPT];  // (before the sums take their place)
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) tops[k] = s_top[row_of(k)];
   __syncthreads();
-  for (int k = 0; k < HPB; ++k) {
-    if (!s_many[k]) continue;
-    const int head = blockIdx.x * HPB + k;
-    const Parts q = parts_of(a, head, chunks, grid);
-    join(head, q, w, JW);
-    if (lane == 0) s_sum[w] = sum;
+  over_rows(sum, false);
+  if (side > 0) return;
 #pragma unroll
-    for (int c = 0; c < V; ++c) s_acc[w][lane * V + c] = acc[c];
-    __syncthreads();
-    if (w == 0) {
+  for (int k = 0; k < EPT; ++k) {
+    const int row = row_of(k), col = (e0 + k * THREADS) % (D / 4) * 4;
+    if (row >= heads) continue;
+    if (SIDES > 1) {
 #pragma unroll
-      for (int i = 1; i < JW; ++i) {
-        sum += s_sum[i];
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] += s_acc[i][lane * V + c];
-      }
-      write(head);
+      for (int i = 1; i < SIDES; ++i) add(s_acc[i][e0], 1.f, k);
     }
-    __syncthreads();
+    const float total = s_top[row], inv = total > 0.f || total != total ? a.v_scale / total : 0.f;
+    *reinterpret_cast<uint2*>(a.out + (out_row + row) * D + col) =
+        make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
+    if (a.lse != nullptr && col == 0)
+      a.lse[out_row + row] =
+          total == 0.f ? -INFINITY : (tops[k] + (log2f(total) - kShift)) * 0.6931471805599453f;
   }
 }
 
@@ -746,11 +756,11 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + TK - 1) / TK + kSegCost);
   const int grid = static_cast<int>(std::min<long long>(std::min(sms, kMaxCtas), most));
   if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks)) != cudaSuccess) return e;
-  const int heads = a.B * a.Hq;
-  if (heads <= 4 * sms)
-    return launch_dependent(paged_join_kernel<D, E4M3, 1>, heads, kJoinThreads, 0, stream, a, chunks, grid, WIDE);
-  return launch_dependent(paged_join_kernel<D, E4M3, 8>, (heads + 7) / 8, kJoinThreads, 0, stream, a, chunks, grid,
-                          WIDE);
+  // few segments have many parts each, and an SM for each of them
+  const int segments = a.B * a.Hkv * chunks;
+  if (segments <= sms)
+    return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 1024>, segments, 1024, 0, stream, a, chunks, grid);
+  return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 256>, segments, 256, 0, stream, a, chunks, grid);
 }
 
 }  // namespace
