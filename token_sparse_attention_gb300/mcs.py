@@ -578,10 +578,6 @@ def _at(dev, t, dtype, shape, name):
     return _refuse(dev, t, dtype, shape, name)
 
 
-def _maybe_at(dev, t, dtype, shape, name):
-    return None if t is None else _at(dev, t, dtype, shape, name)
-
-
 def _bytes_at(dev, t, name):
     """(pointer, size) of a workspace."""
     if not isinstance(t, torch.Tensor):
@@ -591,9 +587,17 @@ def _bytes_at(dev, t, name):
 
 def _rows_at(dev, t, dtype, shape, stride, name):
     """Rows [..., H, D] whose consecutive tokens stand `stride` elements apart (0: H * D)."""
-    if stride == 0 and isinstance(t, torch.Tensor) and t.dtype is dtype and \
-            t.get_device() == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    D = shape[-1]
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+            if stride == 0:
+                if t.is_contiguous():
+                    return t.data_ptr()
+            elif t.stride() == ((stride, D, 1) if len(shape) == 3 else
+                                (shape[1] * stride, stride, D, 1)):
+                return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype is not dtype:
@@ -602,13 +606,13 @@ def _rows_at(dev, t, dtype, shape, stride, name):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{dev}")
-    want, n = (shape[-1], 1), stride or shape[-1] * shape[-2]
+    want, n = (D, 1), stride or D * shape[-2]
     for size in shape[-3::-1]:
         want = (n,) + want
         n *= size
-    have = t.stride()
-    if have != want and any(x > 1 and h != w for x, h, w in zip(shape, have, want)):
-        raise ValueError(f"{name} must have strides {want}, got {have}")
+    # (a dimension of one element may have any stride)
+    if any(x > 1 and h != w for x, h, w in zip(shape, t.stride(), want)):
+        raise ValueError(f"{name} must have strides {want}, got {t.stride()}")
     return t.data_ptr()
 
 
@@ -634,7 +638,7 @@ def mcs_paged_plan(p: Paged, new_lens, lens, free_pages, free_head, block_table,
         _at(dev, block_table, _I32, (p.B, p.max_pages), "block_table"),
         _at(dev, lens_out, _I32, B, "lens_out"), _at(dev, head_out, _I32, one, "head_out"),
         _at(dev, cu_new, _I32, (p.B + 1,), "cu_new"), _at(dev, slots, _I32, (T,), "slots"),
-        _maybe_at(dev, positions, _I32, (T,), "positions"), T, _queue(stream, dev)),
+        None if positions is None else _at(dev, positions, _I32, (T,), "positions"), T, _queue(stream, dev)),
         "mcs_paged_plan")
 
 
@@ -646,7 +650,7 @@ def mcs_paged_write(p: Paged, k, v, slots, k_cache, v_cache, k_mean=None, stream
         _rows_at(dev, v, _BF, rows, stride, "v"), _at(dev, slots, _I32, (T,), "slots"),
         _cache_at(dev, k_cache, kv, cache, "k_cache"),
         _cache_at(dev, v_cache, kv, cache, "v_cache"),
-        _maybe_at(dev, k_mean, _BF, (pages, Hkv, D), "k_mean"), _queue(stream, dev)),
+        None if k_mean is None else _at(dev, k_mean, _BF, (pages, Hkv, D), "k_mean"), _queue(stream, dev)),
         "mcs_paged_write")
 
 
@@ -664,7 +668,7 @@ def mcs_paged_decode(p: Paged, q, k_cache, v_cache, block_table, lens, out, ws, 
         _cache_at(dev, v_cache, kv, cache, "v_cache"),
         _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
         _at(dev, lens, _I32, (B,), "lens"), _at(dev, out, _BF, rows, "out"),
-        _maybe_at(dev, lse, _F32, (B, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
+        None if lse is None else _at(dev, lse, _F32, (B, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
         _queue(stream, dev)), "mcs_paged_decode")
 
 
@@ -701,40 +705,38 @@ def mcs_paged_decode_sparse(p: Paged, q, k_cache, v_cache, block_table, lens, se
         _cache_at(dev, v_cache, kv, cache, "v_cache"),
         _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
         _at(dev, lens, _I32, (B,), "lens"), _at(dev, sel, _I32, (B, Hkv, keep), "sel"), keep,
-        _at(dev, out, _BF, rows, "out"), _maybe_at(dev, lse, _F32, (B, Hq), "lse"),
+        _at(dev, out, _BF, rows, "out"), None if lse is None else _at(dev, lse, _F32, (B, Hq), "lse"),
         *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_paged_decode_sparse")
 
 
 # ---------------------------------------------------------------- norm and rotation
 
-def _rope_inputs(dev, p: Rope, q, k, wq, wk, cos, sin, positions):
-    """Pointers of q, k, wq, wk, cos, sin, positions (k and wk null when Hkv = 0)."""
-    B, N, Hkv, D, rot = p.B, p.N, p.Hkv, p.D, p.rot
-    table = (p.table_rows, rot // 2)
-    return (_rows_at(dev, q, _BF, (B, N, p.Hq, D), p.q_stride, "q"),
-            _rows_at(dev, k, _BF, (B, N, Hkv, D), p.k_stride, "k") if Hkv else None,
-            _maybe_at(dev, wq, _F32, (D,), "wq"),
-            _maybe_at(dev, wk, _F32, (D,), "wk") if Hkv else None,
-            _at(dev, cos, _F32, table, "cos") if rot else None,
-            _at(dev, sin, _F32, table, "sin") if rot else None,
-            _maybe_at(dev, positions, _I32, (B, N), "positions"))
-
-
-def _rope_outs(dev, p: Rope, q, k, names):
-    """Pointers of the two tensors in the layout of q_out and k_out."""
-    B, N, Hq, Hkv, D = p.B, p.N, p.Hq, p.Hkv, p.D
-    by_token = p.layout == LAYOUT_BNHD
-    return (_at(dev, q, _BF, (B, N, Hq, D) if by_token else (B, Hq, N, D), names[0]),
-            _at(dev, k, _BF, (B, N, Hkv, D) if by_token else (B, Hkv, N, D), names[1])
-            if Hkv else None)
+def _rope_args(dev, p: Rope, q, k, wq, wk, cos, sin, positions, q_out, k_out, names):
+    """(pointers of q, k, wq, wk, cos, sin, positions, pointers of the two tensors in the layout of
+    q_out and k_out); k's are null when Hkv = 0."""
+    B, N, Hq, Hkv, D, rot = p.B, p.N, p.Hq, p.Hkv, p.D, p.rot
+    by_token, vector = p.layout == LAYOUT_BNHD, (D,)
+    pk = pwk = pko = pc = ps = None
+    pq = _rows_at(dev, q, _BF, (B, N, Hq, D), p.q_stride, "q")
+    pwq = None if wq is None else _at(dev, wq, _F32, vector, "wq")
+    pqo = _at(dev, q_out, _BF, (B, N, Hq, D) if by_token else (B, Hq, N, D), names[0])
+    if Hkv:
+        pk = _rows_at(dev, k, _BF, (B, N, Hkv, D), p.k_stride, "k")
+        pwk = None if wk is None else _at(dev, wk, _F32, vector, "wk")
+        pko = _at(dev, k_out, _BF, (B, N, Hkv, D) if by_token else (B, Hkv, N, D), names[1])
+    if rot:
+        table = (p.table_rows, rot // 2)
+        pc, ps = _at(dev, cos, _F32, table, "cos"), _at(dev, sin, _F32, table, "sin")
+    pp = None if positions is None else _at(dev, positions, _I32, (B, N), "positions")
+    return (pq, pk, pwq, pwk, pc, ps, pp), (pqo, pko)
 
 
 def mcs_qk_norm_rope(p: Rope, q, k, wq, wk, cos, sin, positions, q_out, k_out, stream=None):
     dev = _device(stream)
-    _check(lib().mcs_qk_norm_rope(
-        ctypes.byref(p), *_rope_inputs(dev, p, q, k, wq, wk, cos, sin, positions),
-        *_rope_outs(dev, p, q_out, k_out, ("q_out", "k_out")), _queue(stream, dev)),
-        "mcs_qk_norm_rope")
+    ins, outs = _rope_args(dev, p, q, k, wq, wk, cos, sin, positions, q_out, k_out,
+                           ("q_out", "k_out"))
+    _check(lib().mcs_qk_norm_rope(ctypes.byref(p), *ins, *outs, _queue(stream, dev)),
+           "mcs_qk_norm_rope")
 
 
 def mcs_qk_norm_rope_backward_workspace(p: Rope) -> int:
@@ -744,13 +746,14 @@ def mcs_qk_norm_rope_backward_workspace(p: Rope) -> int:
 def mcs_qk_norm_rope_backward(p: Rope, dq_out, dk_out, q, k, wq, wk, cos, sin, positions, dq, dk,
                               dwq, dwk, ws, stream=None):
     dev, Hkv = _device(stream), p.Hkv
+    ins, grads = _rope_args(dev, p, q, k, wq, wk, cos, sin, positions, dq_out, dk_out,
+                            ("dq_out", "dk_out"))
     _check(lib().mcs_qk_norm_rope_backward(
-        ctypes.byref(p), *_rope_outs(dev, p, dq_out, dk_out, ("dq_out", "dk_out")),
-        *_rope_inputs(dev, p, q, k, wq, wk, cos, sin, positions),
+        ctypes.byref(p), *grads, *ins,
         _rows_at(dev, dq, _BF, (p.B, p.N, p.Hq, p.D), p.q_stride, "dq"),
         _rows_at(dev, dk, _BF, (p.B, p.N, Hkv, p.D), p.k_stride, "dk") if Hkv else None,
-        _maybe_at(dev, dwq, _F32, (p.D,), "dwq"),
-        _maybe_at(dev, dwk, _F32, (p.D,), "dwk") if Hkv else None,
+        None if dwq is None else _at(dev, dwq, _F32, (p.D,), "dwq"),
+        None if dwk is None or not Hkv else _at(dev, dwk, _F32, (p.D,), "dwk"),
         *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_qk_norm_rope_backward")
 
 
