@@ -150,6 +150,39 @@ def test_backward_matches_oracle(case):
     assert all(torch.equal(a, b) for a, b in zip(dx, again))
 
 
+@pytest.mark.parametrize("case", [
+    (2, 5003, 2, 1, 64, 64, False, 0, True, True, True), (1, 9801, 20, 1, 128, 32, True, 1, False, False, True),
+    (3, 3301, 1, 0, 128, 128, False, 1, False, True, False), (1, 10007, 3, 4, 64, 48, True, 0, False, True, True),
+    (1, 9999, 1, 12, 128, 128, True, 0, True, True, True)], ids=lambda c: "-".join(str(int(x)) for x in c))
+def test_many_tokens_of_few_heads(case):
+    """Warps that take several tokens (one, both or no tensors of such a call), with padding among them."""
+    c = Case(*case)
+    skip = torch.zeros(c.B, c.N, dtype=torch.bool, device="cuda")
+    if c.pos is not None:
+        skip = torch.rand(c.B, c.N, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) < 0.2
+        c.pos[skip] = -1
+    live = ~skip.cpu().numpy()
+    outs, (dx, dw) = c.forward(), c.backward()
+    assert mcs.mcs_device_status() == 0
+    for i in range(2):
+        if c.H[i] == 0:
+            continue
+        x, w, cos, sin, pos, *rest = c.oracle(i)
+        pos = np.maximum(pos, 0)
+        want = po.norm_rope(x, w, cos, sin, pos, *rest)
+        tol = 2.0 ** -8 * np.abs(want) + (c.D / 2 + 10) * U * _mix(want, c.rot, c.inter) * 2 ** 0.5
+        got = c.token_major(outs[i])
+        assert (np.abs(got - want) <= tol)[live].all() and (got[~live] == 9).all()
+        dy = c.token_major(c.dy[i]) * live[..., None, None]
+        want, want_w, _ = po.norm_rope_backward(dy, x, w, cos, sin, pos, *rest)
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + c.eps)
+        g, xh = _mix(dy, c.rot, c.inter), np.abs(x * r)
+        tol = 2.0 ** -8 * np.abs(want) + (c.D + 20) * U * r * (g * np.abs(w) + xh * (g * np.abs(w) * xh).mean(-1, keepdims=True))
+        got = _f64(dx[i])
+        assert (np.abs(got - want) <= tol)[live].all() and (got[~live] == 9).all()
+        assert (np.abs(_f64(dw[i]) - want_w) <= (c.D / 2 + 410) * U * (g * xh).sum((0, 1, 2))).all()
+
+
 def test_gradients_match_differences_of_the_kernel():
     """dx . e against (f(x + h e) - f(x - h e)) / 2h of the kernel's own forward pass, f = y . dy.
     bf16 outputs round by 2^-8 of each value, so f is off by about sqrt(n) 2^-9 |y dy|; a step of

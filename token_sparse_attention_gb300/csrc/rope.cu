@@ -36,7 +36,7 @@ template <int D> struct Tune {
   static constexpr int STEPS = 512 / D, BLOCKS = D == 128 ? 4 : 3;
   static constexpr int GRAD_STEPS = 2, GRAD_BLOCKS = D == 128 ? 4 : 3;
 };
-constexpr int kGradBlocks = 1024;  // most partial sums of the weight gradients
+constexpr int kGradBlocks = 2048;  // most partial sums of the weight gradients, half of them of k
 
 // Heads of one token a warp takes.
 __host__ __device__ constexpr int heads_per_warp(int D, int steps) { return steps * (256 / D); }
@@ -241,6 +241,115 @@ __global__ void __launch_bounds__(kRopeThreads, Tune<D>::BLOCKS)
   }
 }
 
+// x / rms(x), as the pairs' members.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void normed(const Row& x, float eps, uint64_t* u, uint64_t* v) {
+  unpack<SPLIT>(x, u, v);
+  uint64_t ss = f2_mul(u[0], u[0]);
+  ss = f2_fma(u[1], u[1], ss);
+  ss = f2_fma(v[0], v[0], ss);
+  ss = f2_fma(v[1], v[1], ss);
+  const float r = rsqrtf(row_sum<D / 8>(f2_sum(ss)) * (1.f / D) + eps);
+  const uint64_t rr = f2_pack(r, r);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    u[k] = f2_mul(u[k], rr);
+    v[k] = f2_mul(v[k], rr);
+  }
+}
+
+// A tensor with fewer heads than half of what a warp takes of one token: the warp
+// takes the heads of several consecutive tokens, with angles for each row.  One
+// tensor per launch.
+struct One {
+  int H, tokens;  // heads; tokens per warp
+  long long stride;
+  const __nv_bfloat16* x;
+  __nv_bfloat16* out;           // q_out / k_out; backward: dq / dk
+  const __nv_bfloat16* dy;      // backward
+  const float* w;
+  float* partial;               // backward: the blocks' sums
+};
+// Row r of a warp's rows: where it lies in x and in the output-shaped tensors, and its
+// position (-1: none, or a row that stays as it is).
+struct RowAt {
+  size_t x, y;
+  int pos;
+};
+__device__ __forceinline__ RowAt row_at(const RopeArgs& a, const One& one, unsigned warp, int r) {
+  RowAt p = {0, 0, -1};
+  const int k = r / one.H, h = r - k * one.H;
+  const unsigned token = warp * one.tokens + k;
+  if (k >= one.tokens || token >= static_cast<unsigned>(a.B) * a.N) return p;
+  const Token t = token_of(a, token);
+  size_t step;
+  p.y = out_base(a, t, one.H, &step);
+  p.y += h * step;
+  p.x = token * one.stride + h * a.D;
+  p.pos = t.pos;
+  return p;
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kRopeThreads, Tune<D>::BLOCKS)
+    norm_rope_few_kernel(const RopeArgs a, const One one) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::STEPS;
+  pdl_begin();
+  const int l = lane_id() % LANES;
+  const Place at = place_of<SPLIT>(a.rot, l);
+  const unsigned warp = blockIdx.x * kRopeWarps + warp_id();
+  RowAt p[STEPS];
+  Row x[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    p[i] = row_at(a, one, warp, i * ROWS + lane_id() / LANES);
+    x[i] = Row{{0, 0, 0, 0}};
+    if (p[i].pos >= 0) x[i] = load_row<SPLIT>(one.x + p[i].x, at);
+  }
+  uint64_t wa[2], wb[2];
+  load_weights<SPLIT>(one.w, at, wa, wb);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    uint64_t cs[2], sn[2], u[2], v[2];
+    load_angles(a, max(p[i].pos, 0), l, cs, sn);
+    normed<D, SPLIT>(x[i], a.eps, u, v);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      u[k] = f2_mul(u[k], wa[k]);
+      v[k] = f2_mul(v[k], wb[k]);
+      const uint64_t s = f2_mul(v[k], f2_neg(sn[k]));
+      v[k] = f2_fma(v[k], cs[k], f2_mul(u[k], sn[k]));
+      u[k] = f2_fma(u[k], cs[k], s);
+    }
+    if (p[i].pos >= 0) store_row<SPLIT>(one.out + p[i].y, at, u, v);
+  }
+}
+
+// The block's sum of its threads' weight gradients.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void block_weight_sum(const uint64_t* da, const uint64_t* db, Place at, int r0, float* out) {
+  constexpr int ROWS = 256 / D;
+  __shared__ float part[kRopeWarps * ROWS][D];
+  float s[8];
+  f2_unpack(da[0], s[0], s[1]);
+  f2_unpack(da[1], s[2], s[3]);
+  f2_unpack(db[0], s[4], s[5]);
+  f2_unpack(db[1], s[6], s[7]);
+  float* to = part[warp_id() * ROWS + r0];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    to[SPLIT ? at.a + k : at.a + 2 * k] = s[k];
+    to[SPLIT ? at.b + k : at.a + 2 * k + 1] = s[4 + k];
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0;
+#pragma unroll
+    for (int i = 0; i < kRopeWarps * ROWS; ++i) sum += part[i][threadIdx.x];
+    out[threadIdx.x] = sum;
+  }
+}
+
 // Backward: units of 8 tokens and a warp's heads as above; a block takes every
 // blocks_q-th unit of q (or blocks_k-th of k) and keeps the weight gradient of
 // its units in registers, one partial row per block at the end.
@@ -315,25 +424,65 @@ __global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
       if (h0 + i * ROWS < H) store_row<SPLIT>(dxs + i * ROWS * D, at, c, d);
     }
   }
-  __shared__ float part[kRopeWarps * ROWS][D];
-  float s[8];
-  f2_unpack(da[0], s[0], s[1]);
-  f2_unpack(da[1], s[2], s[3]);
-  f2_unpack(db[0], s[4], s[5]);
-  f2_unpack(db[1], s[6], s[7]);
-  float* to = part[warp_id() * ROWS + r0];
+  block_weight_sum<D, SPLIT>(da, db, at, r0, a.ws + static_cast<size_t>(blockIdx.x) * D);
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
+    norm_rope_few_backward_kernel(const RopeArgs a, const One one) {
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::GRAD_STEPS;
+  pdl_begin();
+  const int l = lane_id() % LANES, r0 = lane_id() / LANES;
+  const Place at = place_of<SPLIT>(a.rot, l);
+  const unsigned per = static_cast<unsigned>(kRopeWarps) * one.tokens;  // tokens of a block's step
+  const unsigned units = (static_cast<unsigned>(a.B) * a.N + per - 1) / per;
+  uint64_t wa[2], wb[2], da[2] = {0, 0}, db[2] = {0, 0};
+  load_weights<SPLIT>(one.w, at, wa, wb);
+  for (unsigned n = blockIdx.x; n < units; n += gridDim.x) {
+    RowAt pl[STEPS];
+    Row x[STEPS], y[STEPS];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    to[SPLIT ? at.a + k : at.a + 2 * k] = s[k];
-    to[SPLIT ? at.b + k : at.a + 2 * k + 1] = s[4 + k];
-  }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float sum = 0;
+    for (int i = 0; i < STEPS; ++i) {
+      pl[i] = row_at(a, one, n * kRopeWarps + warp_id(), i * ROWS + r0);
+      x[i] = y[i] = Row{{0, 0, 0, 0}};
+      if (pl[i].pos >= 0) {
+        x[i] = load_row<SPLIT>(one.x + pl[i].x, at);
+        y[i] = load_row<SPLIT>(one.dy + pl[i].y, at);
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < kRopeWarps * ROWS; ++i) sum += part[i][threadIdx.x];
-    a.ws[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = sum;
+    for (int i = 0; i < STEPS; ++i) {
+      uint64_t cs[2], sn[2];
+      load_angles(a, max(pl[i].pos, 0), l, cs, sn);
+      uint64_t p[2], q[2], c[2], d[2], g[2], f[2];
+      unpack<SPLIT>(x[i], p, q);
+      unpack<SPLIT>(y[i], c, d);
+      uint64_t ss = 0, dot = 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
+        g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
+        f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
+        c[k] = f2_mul(g[k], wa[k]);
+        d[k] = f2_mul(f[k], wb[k]);
+        dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
+      }
+      float s1 = f2_sum(ss), s2 = f2_sum(dot);
+      s1 = row_sum<LANES>(s1);
+      s2 = row_sum<LANES>(s2);
+      const float r = rsqrtf(s1 * (1.f / D) + a.eps), m = -(s2 * (1.f / D)) * r * r;
+      const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
+        db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
+        c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
+        d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
+      }
+      if (pl[i].pos >= 0) store_row<SPLIT>(one.out + pl[i].x, at, c, d);
+    }
   }
+  block_weight_sum<D, SPLIT>(da, db, at, r0, one.partial + static_cast<size_t>(blockIdx.x) * D);
 }
 
 // dw = sum of the partial rows in a fixed order, block 0 for q, 1 for k.
@@ -375,11 +524,40 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const RopeArgs a, int
   }
 }
 
+One one_of(const RopeArgs& a, bool q, int heads) {
+  One o = {};
+  o.H = q ? a.Hq : a.Hkv;
+  o.tokens = o.H > 0 ? heads / o.H : 0;
+  o.stride = q ? a.q_stride : a.k_stride;
+  o.x = q ? a.q : a.k;
+  o.out = q ? a.q_out : a.k_out;
+  o.dy = q ? a.dq_out : a.dk_out;
+  o.w = q ? a.wq : a.wk;
+  return o;
+}
+// Whether a tensor gets a launch of its own with several tokens per warp: below half of
+// the heads a warp takes, and enough tokens to fill the SMs several times, where the
+// second launch pays (62598 tokens of 2 + 1 heads, D = 128: 61 us in one, 32 in two).
+bool few_heads(int H, int heads, long long tokens, int sms) {
+  return H > 0 && 2 * H <= heads && tokens >= 64LL * sms;
+}
+
 template <int D>
-cudaError_t forward(const RopeArgs& a, cudaStream_t stream) {
+cudaError_t forward(const RopeArgs& a, int sms, cudaStream_t stream) {
   constexpr int heads = heads_per_warp(D, Tune<D>::STEPS);
-  const int cq = (a.Hq + heads - 1) / heads, ck = (a.Hkv + heads - 1) / heads;
-  const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  const bool few_q = few_heads(a.Hq, heads, tokens, sms), few_k = few_heads(a.Hkv, heads, tokens, sms);
+  for (int t = 0; t < 2; ++t) {
+    if (!(t == 0 ? few_q : few_k)) continue;
+    const One one = one_of(a, t == 0, heads);
+    const long long per = static_cast<long long>(kRopeWarps) * one.tokens;
+    const cudaError_t e = launch_dependent(a.interleaved ? norm_rope_few_kernel<D, false> : norm_rope_few_kernel<D, true>,
+                                           static_cast<unsigned>((tokens + per - 1) / per), kRopeThreads, 0, stream, a, one);
+    if (e != cudaSuccess) return e;
+  }
+  const int cq = few_q ? 0 : (a.Hq + heads - 1) / heads, ck = few_k ? 0 : (a.Hkv + heads - 1) / heads;
+  if (cq + ck == 0) return cudaSuccess;
+  const long long tiles = (tokens + kRopeWarps - 1) / kRopeWarps;
   const unsigned blocks = static_cast<unsigned>(tiles * (cq + ck));
   return launch_dependent(a.interleaved ? norm_rope_kernel<D, false> : norm_rope_kernel<D, true>, blocks,
                           kRopeThreads, 0, stream, a, cq, cq + ck);
@@ -388,18 +566,38 @@ cudaError_t forward(const RopeArgs& a, cudaStream_t stream) {
 template <int D>
 cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
   constexpr int heads = heads_per_warp(D, Tune<D>::GRAD_STEPS);
+  const long long tokens = static_cast<long long>(a.B) * a.N, tiles = (tokens + kRopeWarps - 1) / kRopeWarps;
+  const bool few_q = few_heads(a.Hq, heads, tokens, sms), few_k = few_heads(a.Hkv, heads, tokens, sms);
   const int cq = (a.Hq + heads - 1) / heads, ck = (a.Hkv + heads - 1) / heads;
-  const long long tiles = (static_cast<long long>(a.B) * a.N + kRopeWarps - 1) / kRopeWarps;
-  // the blocks that are resident at a time, shared between q and k by their work
-  const int limit = std::min(Tune<D>::GRAD_BLOCKS * sms, kGradBlocks);
+  // the blocks that are resident at a time, shared between q and k by their work where
+  // they run together
+  const int limit = std::min(Tune<D>::GRAD_BLOCKS * sms, kGradBlocks / 2);
+  const bool together = !few_q && !few_k && ck > 0;
   const long long share = (static_cast<long long>(limit) * cq + (cq + ck) / 2) / (cq + ck);
-  const int limit_q = ck ? static_cast<int>(std::max<long long>(1, std::min<long long>(share, limit - 1))) : limit;
-  const int bq = static_cast<int>(std::min<long long>(tiles * cq, limit_q));
-  const int bk = static_cast<int>(std::min<long long>(tiles * ck, limit - limit_q));
-  cudaError_t e = launch_dependent(
-      a.interleaved ? norm_rope_backward_kernel<D, false> : norm_rope_backward_kernel<D, true>, bq + bk, kRopeThreads,
-      0, stream, a, bq, bk);
-  if (e != cudaSuccess || (a.dwq == nullptr && a.dwk == nullptr)) return e;
+  const int limit_q = together ? static_cast<int>(std::max<long long>(1, std::min<long long>(share, limit - 1))) : limit;
+  auto blocks_of = [&](bool few, int H, int chunks, int most) {
+    const long long per = static_cast<long long>(kRopeWarps) * (few ? heads / H : 1);
+    return static_cast<int>(std::min<long long>(few ? (tokens + per - 1) / per : tiles * chunks, most));
+  };
+  const int bq = blocks_of(few_q, a.Hq, cq, limit_q), bk = ck ? blocks_of(few_k, a.Hkv, ck, together ? limit - limit_q : limit) : 0;
+  cudaError_t e = cudaSuccess;
+  for (int t = 0; t < 2; ++t) {
+    if (!(t == 0 ? few_q : few_k)) continue;
+    One one = one_of(a, t == 0, heads);
+    one.partial = a.ws + static_cast<size_t>(t == 0 ? 0 : bq) * D;
+    e = launch_dependent(a.interleaved ? norm_rope_few_backward_kernel<D, false> : norm_rope_few_backward_kernel<D, true>,
+                         t == 0 ? bq : bk, kRopeThreads, 0, stream, a, one);
+    if (e != cudaSuccess) return e;
+  }
+  const int rest_q = few_q ? 0 : bq, rest_k = few_k ? 0 : bk;
+  if (rest_q + rest_k > 0) {
+    RopeArgs c = a;
+    c.ws = a.ws + static_cast<size_t>(few_q ? bq : 0) * D;  // k's rows follow q's
+    e = launch_dependent(a.interleaved ? norm_rope_backward_kernel<D, false> : norm_rope_backward_kernel<D, true>,
+                         rest_q + rest_k, kRopeThreads, 0, stream, c, rest_q, rest_k);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dwq == nullptr && a.dwk == nullptr) return e;
   return launch_dependent(weight_grad_kernel<D>, a.Hkv ? 2 : 1, 1024, 0, stream, a, bq, bk);
 }
 
@@ -410,7 +608,11 @@ size_t norm_rope_backward_workspace_bytes(int D) {
 }
 
 cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream) {
-  return a.D == 128 ? forward<128>(a, stream) : forward<64>(a, stream);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  return a.D == 128 ? forward<128>(a, sms, stream) : forward<64>(a, sms, stream);
 }
 
 cudaError_t launch_norm_rope_backward(const RopeArgs& a, cudaStream_t stream) {
