@@ -239,6 +239,65 @@ def test_select_near_ties_follow_the_exact_sum():
     np.testing.assert_array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -80, 2.0 ** 100])
+def test_select_follows_the_exact_sum_at_any_size(scale):
+    """Means whose squares vanish or overflow in fp32, and infinite ones."""
+    r = np.random.default_rng(6)
+    n, page, D, select = 400, 16, 64, 60
+    p = mcs.paged(1, 2, 2, D, page, n, n)
+    md = torch.from_numpy(r.standard_normal((n, 2, D)) * scale).cuda().to(torch.bfloat16)
+    if scale > 1:
+        md[5, 0] = 0
+        md[5, 0, 0], md[9, 1] = float("inf"), 0
+        md[9, 1, 3] = float("-inf")
+    qd = torch.from_numpy(r.standard_normal((1, 2, D)) + 0.01).cuda().to(torch.bfloat16)
+    sel = torch.empty(1, 2, select, dtype=torch.int32, device="cuda")
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(p))
+    table = r.permutation(n)[None]
+    mcs.mcs_paged_select(p, qd, md, _i32(table), _i32([n * page]), sel, ws, sink=0, recent=0)
+    m = _f64(md)
+    with np.errstate(invalid="ignore", over="ignore"):
+        q = _f64(qd)
+        # (the infinite rows hold one value and zeros, and no query is zero: their sums are infinite)
+        score = np.stack([np.where(m[:, h] == 0, 0.0, m[:, h] * q[0, h]).sum(1) for h in range(2)]).astype(np.float32)
+    for h in range(2):
+        s = score[h][table[0]]
+        want = np.sort(np.lexsort((np.arange(n), -s))[:select])
+        np.testing.assert_array_equal(sel[0, h].cpu().numpy(), want)
+
+
+def test_tables_far_longer_than_their_sequences():
+    c = Cache([500, 17, 0, 4000], 8, 2, 128, 16, seed=2, extra=60000)
+    c.check(*c.run())
+    mean, select = c.means(), 9
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(c.p))
+    sel = torch.empty(4, 2, select, dtype=torch.int32, device="cuda")
+    mcs.mcs_paged_select(c.p, c.q, mean, c.dtable, c.dlens, sel, ws, sink=1, recent=1)
+    want = po.select(_f64(c.q), _f64(mean), c.table, c.lens, 16, select, 1, 1)
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+    c.check(*c.run(sel), want)
+
+
+def test_selection_of_a_long_sequence_takes_several_rounds():
+    # more pages than all blocks of the score kernel look at in one round, for many pairs
+    c = Cache([9000] * 40, 128, 64, 64, 16, seed=4)
+    mean, select = c.means(), 5
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(c.p))
+    sel = torch.empty(40, 64, select, dtype=torch.int32, device="cuda")
+    mcs.mcs_paged_select(c.p, c.q, mean, c.dtable, c.dlens, sel, ws, sink=0, recent=1)
+    q = c.q.double().view(40, 64, 2, 64).sum(2)
+    score = torch.einsum("bhd,bphd->bhp", q, mean[c.dtable[:, :563].long()].double()).float()
+    score[..., 562] = float("inf")
+    want = torch.sort(score, dim=-1, descending=True, stable=True).indices[..., :select].sort(-1).values
+    assert torch.equal(sel.long(), want)
+
+
+def test_batches_of_the_largest_count():
+    r = np.random.default_rng(1)
+    c = Cache([int(x) for x in r.integers(0, 20, 4096)], 2, 1, 64, 16, seed=3, extra=0)
+    c.check(*c.run())
+
+
 # ------------------------------------------------------------------ plan and write
 
 def _plan(p, new, lens, free, head, table, T, in_place=False):

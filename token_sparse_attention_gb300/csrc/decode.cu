@@ -147,8 +147,9 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DecodeArgs& a, int s
   if (w.left <= 0) return false;
   if (++w.seg == segs) {
     w.seg = 0;
-    do {
-      w.tb = tiles_of<TK>(a, ++w.b);
+    do {  // (there is one, unless the lengths change under the kernel)
+      if (++w.b >= a.B) return false;
+      w.tb = tiles_of<TK>(a, w.b);
     } while (w.tb == 0);
   }
   w.t0 = 0;
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (all > 0: some lane's sequences hold position lo)
     const int from = __ffs(__ballot_sync(0xffffffffu, lo < upto * segs)) - 1;
     long long base = __shfl_sync(0xffffffffu, upto - own, from);
-    for (int b0 = from * per;; b0 += 32) {
+    busy = false;
+    for (int b0 = from * per; from >= 0 && b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       const long long x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, b) : 0;
       const long long y = scan(x);
@@ -241,13 +243,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         here.tb = static_cast<int>(size) - kSegCost;
         here.seg = static_cast<int>(divide(lo - first, size));
         here.t0 = static_cast<int>(lo - first - here.seg * size);
+        busy = true;
         break;
       }
       base += __shfl_sync(0xffffffffu, y, 31);
     }
     here.left = hi - lo;
     here.count = static_cast<int>(min(static_cast<long long>(here.tb - here.t0), here.left));
-    if (here.count <= 0) busy = next_segment<TK>(here, a, segs);
+    if (busy && here.count <= 0) busy = next_segment<TK>(here, a, segs);
   }
 
   // ---- the warp's ring: its tiles, three ahead

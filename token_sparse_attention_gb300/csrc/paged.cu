@@ -446,17 +446,19 @@ __global__ void __launch_bounds__(kScoreThreads)
   constexpr int LANES = D / 8, ROWS = 32 / LANES;
   __shared__ float s_q[ROWS * D];
   pdl_begin();
-  const int xp = blockIdx.x % page_blocks, hb = blockIdx.x / page_blocks % head_blocks;
-  const int b = blockIdx.x / page_blocks / head_blocks;
+  const int hb = blockIdx.x / page_blocks % head_blocks, b = blockIdx.x / page_blocks / head_blocks;
   const int len = a.lens[b];
   if (len == 0 || bad_length(a, len)) return;
-  const int n = (len - 1) / a.page + 1;
-  const int j0 = (xp * (kScoreThreads / 32) + warp_id()) * per_warp, j1 = min(n, j0 + per_warp);
-  if (xp * (kScoreThreads / 32) * per_warp >= n) return;
-  // per_warp <= 32: a page number per lane, on its way while the queries are summed
-  int pid = -1;
-  const bool mine = j0 + lane_id() < j1;
-  if (mine) pid = a.table[static_cast<size_t>(b) * a.max_pages + j0 + lane_id()];
+  const int n = (len - 1) / a.page + 1, chunk = kScoreThreads / 32 * per_warp;
+  long long j0 = static_cast<long long>(blockIdx.x % page_blocks) * chunk;
+  if (j0 >= n) return;
+  j0 += warp_id() * per_warp;
+  // per_warp <= 32: a page number per lane, the first ones on their way while the queries are summed
+  auto page_number = [&](long long j) {
+    return j + lane_id() < min(static_cast<long long>(n), j + per_warp)
+               ? a.table[static_cast<size_t>(b) * a.max_pages + j + lane_id()] : -1;
+  };
+  int first = page_number(j0);
   const int group = a.Hq / a.Hkv;
   {  // the group's summed query, one value per thread
     const int r = threadIdx.x / D, d = threadIdx.x % D, h = min(hb * ROWS + r, a.Hkv - 1);
@@ -464,11 +466,6 @@ __global__ void __launch_bounds__(kScoreThreads)
     s_q[threadIdx.x] = sum_of_group(q, group, D);
   }
   __syncthreads();
-  if (j0 >= j1) return;
-  const bool outside = mine && (pid < 0 || pid >= a.num_pages);
-  if (outside) atomicOr(a.status, DEV_BOUNDS);
-  if (outside || !mine) pid = 0;
-  const uint32_t bad = __ballot_sync(0xffffffffu, outside);
   const int lane = lane_id(), l = lane % LANES, h = hb * ROWS + lane / LANES;
   uint64_t q[4];
   float qq = 0.f;
@@ -480,61 +477,68 @@ __global__ void __launch_bounds__(kScoreThreads)
   }
 #pragma unroll
   for (int o = LANES / 2; o > 0; o /= 2) qq += __shfl_xor_sync(0xffffffffu, qq, o);
-  const float bound = 0x1p-20f * sqrtf(qq);
+  const float bound = 0x1p-20f * sqrtf(qq + 0x1p-120f);  // (squares of tiny values vanish)
   const __nv_bfloat16* mean = a.k_mean + static_cast<size_t>(min(h, a.Hkv - 1)) * D + 8 * l;
   const size_t page_step = static_cast<size_t>(a.Hkv) * D;
   uint32_t* keys = a.keys + 2 * (static_cast<size_t>(b) * a.Hkv + h) * stride;
-  for (int j = j0; j < j1; j += 8) {
-    uint4 x[8];
+  for (; j0 < n; j0 += static_cast<long long>(page_blocks) * chunk, first = page_number(j0)) {
+    const int start = static_cast<int>(j0), j1 = static_cast<int>(min(static_cast<long long>(n), j0 + per_warp));
+    const bool mine = start + lane < j1, outside = mine && (first < 0 || first >= a.num_pages);
+    if (outside) atomicOr(a.status, DEV_BOUNDS);
+    const int pid = outside || !mine ? 0 : first;
+    const uint32_t bad = __ballot_sync(0xffffffffu, outside);
+    for (int j = start; j < j1; j += 8) {
+      uint4 x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - j0 + i) * page_step);
+      for (int i = 0; i < 8; ++i)
+        x[i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - start + i) * page_step);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float dot[4], mm[4];
+      for (int half = 0; half < 2; ++half) {
+        float dot[4], mm[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {x[4 * half + i].x, x[4 * half + i].y, x[4 * half + i].z, x[4 * half + i].w};
-        uint64_t s = 0, t = 0;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {x[4 * half + i].x, x[4 * half + i].y, x[4 * half + i].z, x[4 * half + i].w};
+          uint64_t s = 0, t = 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint64_t m = f2_pack(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xFFFF0000u));
-          s = f2_fma(q[c], m, s);
-          t = f2_fma(m, m, t);
+          for (int c = 0; c < 4; ++c) {
+            const uint64_t m = f2_pack(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xFFFF0000u));
+            s = f2_fma(q[c], m, s);
+            t = f2_fma(m, m, t);
+          }
+          float u, v;
+          f2_unpack(s, u, v);
+          dot[i] = u + v;
+          f2_unpack(t, u, v);
+          mm[i] = u + v;
         }
-        float u, v;
-        f2_unpack(s, u, v);
-        dot[i] = u + v;
-        f2_unpack(t, u, v);
-        mm[i] = u + v;
-      }
-      // fold over the lanes: the upper half of each group of lanes keeps the
-      // upper half of the pages
-      int o = LANES / 2;
+        // fold over the lanes: the upper half of each group of lanes keeps the
+        // upper half of the pages
+        int o = LANES / 2;
 #pragma unroll
-      for (int keep = 2; keep >= 1; keep /= 2, o /= 2) {
-        const bool upper = l & o;
+        for (int keep = 2; keep >= 1; keep /= 2, o /= 2) {
+          const bool upper = l & o;
 #pragma unroll
-        for (int i = 0; i < keep; ++i) {
-          const float sd = upper ? dot[i] : dot[i + keep], sm = upper ? mm[i] : mm[i + keep];
-          dot[i] = (upper ? dot[i + keep] : dot[i]) + __shfl_xor_sync(0xffffffffu, sd, o);
-          mm[i] = (upper ? mm[i + keep] : mm[i]) + __shfl_xor_sync(0xffffffffu, sm, o);
+          for (int i = 0; i < keep; ++i) {
+            const float sd = upper ? dot[i] : dot[i + keep], sm = upper ? mm[i] : mm[i + keep];
+            dot[i] = (upper ? dot[i + keep] : dot[i]) + __shfl_xor_sync(0xffffffffu, sd, o);
+            mm[i] = (upper ? mm[i + keep] : mm[i]) + __shfl_xor_sync(0xffffffffu, sm, o);
+          }
         }
-      }
 #pragma unroll
-      for (; o > 0; o /= 2) {
-        dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
-        mm[0] += __shfl_xor_sync(0xffffffffu, mm[0], o);
-      }
-      // lane bits LANES/2 and LANES/4 name the page
-      const int page = j + 4 * half + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
-      if (l % (LANES / 4) == 0 && page < j1 && h < a.Hkv) {
-        uint32_t key = score_key_bits(__float_as_uint(dot[0]));
-        float off = bound * sqrtf(mm[0]);
-        if (page < a.sink || page >= n - a.recent) key = kKeyForced, off = 0.f;
-        if ((bad >> (page - j0)) & 1u) key = kKeyBad, off = 0.f;
-        keys[page] = key;
-        keys[stride + page] = __float_as_uint(off);
+        for (; o > 0; o /= 2) {
+          dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+          mm[0] += __shfl_xor_sync(0xffffffffu, mm[0], o);
+        }
+        // lane bits LANES/2 and LANES/4 name the page
+        const int page = j + 4 * half + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
+        if (l % (LANES / 4) == 0 && page < j1 && h < a.Hkv) {
+          uint32_t key = score_key_bits(__float_as_uint(dot[0]));
+          float off = bound * sqrtf(mm[0] + 0x1p-120f);
+          if (page < a.sink || page >= n - a.recent) key = kKeyForced, off = 0.f;
+          if ((bad >> (page - start)) & 1u) key = kKeyBad, off = 0.f;
+          keys[page] = key;
+          keys[stride + page] = __float_as_uint(off);
+        }
       }
     }
   }
@@ -694,9 +698,9 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
       __syncthreads();
       above = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
       auto exact_key = [&](int j) {
-        // (a page number that the score kernel found inside the cache)
-        const __nv_bfloat16* mean =
-            a.k_mean + (static_cast<size_t>(a.table[static_cast<size_t>(b) * a.max_pages + j]) * a.Hkv + h) * a.D;
+        // (the score kernel has found the page number inside the cache)
+        const int pid = min(max(a.table[static_cast<size_t>(b) * a.max_pages + j], 0), a.num_pages - 1);
+        const __nv_bfloat16* mean = a.k_mean + (static_cast<size_t>(pid) * a.Hkv + h) * a.D;
         double s = 0;
         for (int d = lane; d < a.D; d += 32) s += s_q[d] * static_cast<double>(__bfloat162float(mean[d]));
 #pragma unroll
@@ -840,7 +844,10 @@ cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
   while (per_warp > 8 && static_cast<long long>(a.B) * head_blocks *
                                  ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 152 * 4)
     per_warp /= 2;
-  const int page_blocks = (a.max_pages + 8 * per_warp - 1) / (8 * per_warp);
+  // and no more blocks than a few rounds of all SMs: a table is often far longer than its sequences
+  const long long pairs = static_cast<long long>(a.B) * head_blocks;
+  const int page_blocks = static_cast<int>(
+      std::min<long long>((a.max_pages + 8 * per_warp - 1) / (8 * per_warp), std::max<long long>(1, 152 * 16 / pairs)));
   const unsigned blocks = static_cast<unsigned>(static_cast<long long>(a.B) * head_blocks * page_blocks);
   cudaError_t e = launch_dependent(a.D == 128 ? paged_score_kernel<128> : paged_score_kernel<64>, blocks,
                                    kScoreThreads, 0, stream, a, head_blocks, page_blocks, per_warp, stride);
