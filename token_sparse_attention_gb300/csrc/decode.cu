@@ -759,9 +759,9 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + TK - 1) / TK + kSegCost);
   const int grid = static_cast<int>(std::min<long long>(std::min(sms, kMaxCtas), most));
   if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks)) != cudaSuccess) return e;
-  // few segments have many parts each, and an SM for each of them
+  // few segments have many parts each (8 per thread of a large block and more)
   const int segments = a.B * a.Hkv * chunks;
-  if (segments <= sms)
+  if (segments <= sms / 8)
     return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 1024>, segments, 1024, 0, stream, a, chunks, grid);
   return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 256>, segments, 256, 0, stream, a, chunks, grid);
 }

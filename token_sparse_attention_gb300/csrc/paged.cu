@@ -544,49 +544,68 @@ __global__ void __launch_bounds__(kScoreThreads)
   }
 }
 
-// The largest key k with (number of keys >= k) >= keep among keys[0, n), and
-// how many of the keys equal to it belong to the first `keep`: by digits of
-// `bits` bits, counted in kTopkCopies histograms (scores share their leading
-// bits, and in one histogram all warps would queue at a few counters).
+// The keys of a list, 8 consecutive ones per thread and step of the block; a list of one
+// step (8192 pages with 1024 threads) stays in registers.
+struct Keys {
+  uint32_t* at;
+  int n, step;
+  bool fits;
+  uint32_t x[kTopkKeys];
+  __device__ __forceinline__ void load(int j) {
+    *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(at + j);
+    *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(at + j + 4);
+  }
+  // visit(page, key) for every key, in the thread's order
+  template <typename F>
+  __device__ __forceinline__ void each(F visit) {
+    for (int j = threadIdx.x * kTopkKeys; j < n; j += step) {
+      if (!fits) load(j);
+#pragma unroll
+      for (int i = 0; i < kTopkKeys; ++i)
+        if (j + i < n) visit(j + i, x[i]);
+    }
+  }
+};
+
+// The largest key k with (number of keys >= k) >= keep, and how many of the keys
+// equal to it belong to the first `keep`: by digits of `bits` bits, counted in
+// kTopkCopies histograms (scores share their leading bits, and in one histogram all
+// warps would queue at a few counters), which are zero before and after.
 constexpr int kTopkCopies = 4;
 constexpr int kTopkOpen = 512;  // pages whose exact rank is found one by one
 struct TopkShared {
   uint32_t prefix, left;
-  int warp[32];
+  int warp[32], open;
+  uint32_t off[32];
+  uint32_t key[kTopkOpen];
+  int page[kTopkOpen];
+  double q[128];
 };
-__device__ __forceinline__ void load_keys(const uint32_t* keys, int j, uint32_t* x) {
-  *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(keys + j);
-  *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(keys + j + 4);
-}
-__device__ __forceinline__ void nth_key(const uint32_t* keys, int n, int keep, int bits, uint32_t* hist,
-                                        TopkShared& sh, uint32_t* key, int* equal) {
+__device__ __forceinline__ void nth_key(Keys& keys, int keep, int bits, uint32_t* hist, TopkShared& sh, uint32_t* key,
+                                        int* equal) {
   const int tid = threadIdx.x, w = warp_id(), lane = lane_id(), warps = blockDim.x / 32;
   const int bins = 1 << bits, per = bins / blockDim.x;  // 2 or 4 neighbouring bins per thread
   uint32_t prefix = 0, left = keep;
   for (int rest = 32; rest > 0;) {
     const int width = min(bits, rest), shift = rest - width;
-    for (int i = tid; i < kTopkCopies * bins / 4; i += blockDim.x)
-      reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
     uint32_t* mine = hist + (w % kTopkCopies) * bins;
-    for (int j = tid * kTopkKeys; j < n; j += blockDim.x * kTopkKeys) {
-      uint32_t x[kTopkKeys];
-      load_keys(keys, j, x);
-#pragma unroll
-      for (int i = 0; i < kTopkKeys; ++i)
-        if (j + i < n && (rest == 32 || x[i] >> rest == prefix))
-          atomicAdd(&mine[(x[i] >> shift) & ((1u << width) - 1u)], 1u);
-    }
+    keys.each([&](int, uint32_t x) {
+      if (rest == 32 || x >> rest == prefix) atomicAdd(&mine[(x >> shift) & ((1u << width) - 1u)], 1u);
+    });
     __syncthreads();
     // counts from the top bin down
-    uint32_t own = 0;
-    for (int i = 0; i < per; ++i) {
-      const int d = bins - 1 - tid * per - i;
-      uint32_t c = 0;
+    uint32_t c[4], own = 0;
 #pragma unroll
-      for (int k = 0; k < kTopkCopies; ++k) c += hist[k * bins + d];
-      hist[d] = c;  // in copy 0: the bin is this thread's
-      own += c;
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 0;
+      if (i >= per) continue;
+      const int d = bins - 1 - tid * per - i;
+#pragma unroll
+      for (int k = 0; k < kTopkCopies; ++k) {
+        c[i] += hist[k * bins + d];
+        hist[k * bins + d] = 0;
+      }
+      own += c[i];
     }
     uint32_t upto = own;
 #pragma unroll
@@ -598,15 +617,13 @@ __device__ __forceinline__ void nth_key(const uint32_t* keys, int n, int keep, i
     __syncthreads();
     uint32_t above = __reduce_add_sync(0xffffffffu, lane < w && lane < warps ? sh.warp[lane] : 0) + upto - own;
     if (above < left && left <= above + own) {
-      for (int i = 0; i < per; ++i) {
-        const int d = bins - 1 - tid * per - i;
-        const uint32_t c = hist[d];
-        if (left <= above + c) {
-          sh.prefix = (prefix << width) | static_cast<uint32_t>(d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < per && above < left && left <= above + c[i]) {
+          sh.prefix = (prefix << width) | static_cast<uint32_t>(bins - 1 - tid * per - i);
           sh.left = left - above;
-          break;
         }
-        above += c;
+        above += c[i];
       }
     }
     __syncthreads();
@@ -627,108 +644,112 @@ __device__ __forceinline__ float key_score(uint32_t key) {
 __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, int stride, int bits) {
   extern __shared__ uint32_t hist[];  // [kTopkCopies][2^bits]
   __shared__ TopkShared sh;
-  __shared__ double s_q[128];
-  __shared__ uint32_t s_key[kTopkOpen];
-  __shared__ int s_page[kTopkOpen], s_open;
-  pdl_begin();
   const int bh = blockIdx.x, b = bh / a.Hkv, h = bh % a.Hkv, tid = threadIdx.x, w = warp_id(), lane = lane_id();
-  const int warps = blockDim.x / 32, step = blockDim.x * kTopkKeys;
+  const int warps = blockDim.x / 32;
+  for (int i = tid; i < kTopkCopies << bits >> 2; i += blockDim.x)
+    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) sh.open = 0;
+  pdl_begin();
   const int len = a.lens[b];
   const bool bad = bad_length(a, len);
   if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
   const int n = bad || len == 0 ? 0 : (len - 1) / a.page + 1;
   const int keep = min(n, a.select);
-  uint32_t* keys = a.keys + 2 * static_cast<size_t>(bh) * stride;
-  const float* offs = reinterpret_cast<const float*>(keys + stride);
   int32_t* sel = a.sel + static_cast<size_t>(bh) * a.select;
   for (int i = keep + tid; i < a.select; i += blockDim.x) sel[i] = -1;
   if (n <= keep) {
     for (int i = tid; i < n; i += blockDim.x) sel[i] = i;
     return;
   }
+  Keys keys;
+  keys.at = a.keys + 2 * static_cast<size_t>(bh) * stride;
+  keys.n = n;
+  keys.step = blockDim.x * kTopkKeys;
+  keys.fits = n <= keys.step;
+  // the keys, and the largest error bound of the list (bounds are >= 0: ordered as integers)
+  uint32_t off_bits = 0;
+  for (int j = tid * kTopkKeys; j < n; j += keys.step) {
+    Keys o;
+    o.at = keys.at + stride;
+    o.load(j);
+    keys.load(j);
+#pragma unroll
+    for (int i = 0; i < kTopkKeys; ++i)
+      if (j + i < n) off_bits = max(off_bits, o.x[i]);
+  }
+  off_bits = __reduce_max_sync(0xffffffffu, off_bits);
+  if (lane == 0) sh.off[w] = off_bits;
+  __syncthreads();
   uint32_t least;  // kept: keys above it, and the first `equal` that equal it
   int equal;
-  nth_key(keys, n, keep, bits, hist, sh, &least, &equal);
+  nth_key(keys, keep, bits, hist, sh, &least, &equal);
   if (least != kKeyForced && least != kKeyBad) {
-    // the largest error bound of the sequence
-    float off = 0.f;
-    for (int j = tid; j < n; j += blockDim.x) off = fmaxf(off, offs[j]);
-    off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(off)));  // >= 0: ordered as integers
-    if (lane == 0) sh.warp[w] = __float_as_int(off);
-    __syncthreads();
-    off = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? static_cast<uint32_t>(sh.warp[lane]) : 0u));
+    const float off = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? sh.off[lane] : 0u));
     const float t = key_score(least);
     uint32_t lo = kKeyBad + 1, hi = kKeyForced - 1;  // infinities or NaN around: every page again
     if (fabsf(t) < INFINITY && off < INFINITY) {
       lo = score_key_bits(__float_as_uint(t - 2.f * off));
       hi = score_key_bits(__float_as_uint(t + 2.f * off));
     }
-    int upper = 0;  // pages from lo on
-    for (int j = tid; j < n; j += blockDim.x) upper += keys[j] >= lo;
-    upper = __reduce_add_sync(0xffffffffu, upper);
+    // pages above, and those in between
+    int above = 0;
+    keys.each([&](int page, uint32_t x) {
+      above += x > hi;
+      if (x >= lo && x <= hi) {
+        const int i = atomicAdd(&sh.open, 1);  // (their order says nothing about the result)
+        if (i < kTopkOpen) sh.page[i] = page;
+      }
+    });
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 0) sh.warp[w] = above;
     __syncthreads();
-    if (lane == 0) sh.warp[w] = upper;
-    __syncthreads();
-    upper = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
-    if (upper == keep) {
+    above = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
+    const int open = sh.open;
+    if (above + open == keep) {
       least = lo - 1;  // all of them, none equal
       equal = 0;
     } else {
-      // the exact scores of the pages in [lo, hi]
+      // the exact scores of those in between
       const int group = a.Hq / a.Hkv;
       for (int d = tid; d < a.D; d += blockDim.x) {
         const __nv_bfloat16* q = a.q + b * a.q_stride + static_cast<size_t>(h) * group * a.D + d;
         double s = 0;
         for (int i = 0; i < group; ++i) s += static_cast<double>(__bfloat162float(q[static_cast<size_t>(i) * a.D]));
-        s_q[d] = s;
+        sh.q[d] = s;
       }
-      if (tid == 0) s_open = 0;
-      __syncthreads();
-      int above = 0;
-      for (int j = tid; j < n; j += blockDim.x) {
-        const uint32_t key = keys[j];
-        above += key > hi;
-        if (key >= lo && key <= hi) {
-          const int i = atomicAdd(&s_open, 1);  // (their order says nothing about the result)
-          if (i < kTopkOpen) s_page[i] = j;
-        }
-      }
-      above = __reduce_add_sync(0xffffffffu, above);
-      if (lane == 0) sh.warp[w] = above;
-      __syncthreads();
-      above = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
       auto exact_key = [&](int j) {
         // (the score kernel has found the page number inside the cache)
         const int pid = min(max(a.table[static_cast<size_t>(b) * a.max_pages + j], 0), a.num_pages - 1);
         const __nv_bfloat16* mean = a.k_mean + (static_cast<size_t>(pid) * a.Hkv + h) * a.D;
         double s = 0;
-        for (int d = lane; d < a.D; d += 32) s += s_q[d] * static_cast<double>(__bfloat162float(mean[d]));
+        for (int d = lane; d < a.D; d += 32) s += sh.q[d] * static_cast<double>(__bfloat162float(mean[d]));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return score_key_bits(__float_as_uint(static_cast<float>(s)));
       };
-      const int open = s_open;
+      __syncthreads();
       if (open <= kTopkOpen) {
         // few: each one's rank among them, the best become forced, the others bad
         for (int i = w; i < open; i += warps) {
-          const uint32_t key = exact_key(s_page[i]);
-          if (lane == 0) s_key[i] = key;
+          const uint32_t key = exact_key(sh.page[i]);
+          if (lane == 0) sh.key[i] = key;
         }
         __syncthreads();
         for (int i = tid; i < open; i += blockDim.x) {
           int rank = 0;
           for (int k = 0; k < open; ++k)
-            rank += s_key[k] > s_key[i] || (s_key[k] == s_key[i] && s_page[k] < s_page[i]);
-          keys[s_page[i]] = rank < keep - above ? kKeyForced : kKeyBad;
+            rank += sh.key[k] > sh.key[i] || (sh.key[k] == sh.key[i] && sh.page[k] < sh.page[i]);
+          keys.at[sh.page[i]] = rank < keep - above ? kKeyForced : kKeyBad;
         }
         least = hi;
         equal = 0;
         __syncthreads();
+        if (keys.fits && tid * kTopkKeys < n) keys.load(tid * kTopkKeys);
       } else {
         // ties en masse: exact keys for all of them, forced and bad ones for the rest,
         // and the threshold again
         for (int j0 = w * 32; j0 < n; j0 += warps * 32) {
-          uint32_t key = j0 + lane < n ? keys[j0 + lane] : kKeyBad;
+          uint32_t key = j0 + lane < n ? keys.at[j0 + lane] : kKeyBad;
           uint32_t todo = __ballot_sync(0xffffffffu, key >= lo && key <= hi);
           key = key > hi ? kKeyForced : kKeyBad;
           while (todo != 0) {
@@ -737,22 +758,22 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
             const uint32_t x = exact_key(j0 + k);
             if (lane == k) key = x;
           }
-          if (j0 + lane < n) keys[j0 + lane] = key;
+          if (j0 + lane < n) keys.at[j0 + lane] = key;
         }
         __syncthreads();
-        nth_key(keys, n, keep, bits, hist, sh, &least, &equal);
+        if (keys.fits && tid * kTopkKeys < n) keys.load(tid * kTopkKeys);
+        nth_key(keys, keep, bits, hist, sh, &least, &equal);
       }
     }
   }
   int more0 = 0, same0 = 0;
-  for (int base = 0; base < n; base += step) {
+  for (int base = 0; base < n; base += keys.step) {
     const int j = base + tid * kTopkKeys;
-    uint32_t x[kTopkKeys] = {};
-    if (j < n) load_keys(keys, j, x);
+    if (!keys.fits && j < n) keys.load(j);
     int own = 0;  // kept above in the low half, equal in the high half
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i)
-      if (j + i < n) own += x[i] > least ? 1 : (x[i] == least ? 0x10000 : 0);
+      if (j + i < n) own += keys.x[i] > least ? 1 : (keys.x[i] == least ? 0x10000 : 0);
     int upto = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -769,10 +790,10 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i) {
       if (j + i >= n) break;
-      if (x[i] > least) {
+      if (keys.x[i] > least) {
         sel[more + min(same, equal)] = j + i;
         ++more;
-      } else if (x[i] == least) {
+      } else if (keys.x[i] == least) {
         if (same < equal) sel[more + same] = j + i;
         ++same;
       }
