@@ -22,8 +22,8 @@
 // shared memory when the CTA is done, what crosses CTAs goes to the workspace, and a
 // second, programmatically dependent launch joins that in the order of the tiles.
 //
-// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) LONG_US us;
-// 64 x 1000 tokens of 8 KV heads, bf16 (262 MB) SHORT_US us; 1 x 1023 (4.2 MB) ONE_US us, most of
+// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 290 us;
+// 64 x 1000 tokens of 8 KV heads, bf16 (262 MB) 53 us; 1 x 1023 (4.2 MB) 10.7 us, most of
 // it latency (shares 1.5 us, page numbers and first loads 3 us, join 3 us).  What
 // bounds the long ones: SMs do not get equal parts of the bandwidth, equal shares
 // end up to 15 % apart, while the total runs above a copy's rate.  Handing the last fifth

@@ -25,7 +25,7 @@ namespace {
 // second launch (programmatically dependent) places them over all SMs from what
 // the first one wrote: cu_new, lens_out and the table say everything.
 // 9 sequences, 108 000 tokens: 12.3 us with all in one cluster of 8 CTAs (bound by
-// their instruction issue), PLAN_TWO us in two launches; 256 single tokens PLAN_ONE us.
+// their instruction issue), 6.2 us in two launches; 256 single tokens 3.9 us.
 
 constexpr int kPlanMaxThreads = 1024;
 constexpr int kPlanAtOnce = 4;      // tokens a thread searches side by side
@@ -247,14 +247,8 @@ __device__ __forceinline__ void add8(float* sum, uint2 c, float scale) {
 
 constexpr int kWriteThreads = 256;
 
-// A block takes one KV head and a window of consecutive tokens, D/8 threads per
-// row and ROWS rows per thread, all loaded before the first slot is needed: the
-// stores of a window then lie next to each other in its pages.  The block that
-// holds the first token of a page's run also takes the page's mean: the rows in
-// front of it from the cache, the run's own from k (now in L2), so that nothing
-// is read that another block of this launch writes.  With few runs (prompts) the
-// whole block sums one, up to 128 rows in one round of loads; with many (a
-// decoding step) every D/8 threads take one.
+// sum += rows first, first + step, ... of a page's off old rows, then of the run's rows of
+// k; eight loads at a time, which are all that hides their latency.
 template <int D, bool kE4M3Cache>
 __device__ __forceinline__ void sum_run(const WriteArgs& a, const Scale& ks, size_t page_row, size_t src, int off,
                                         int run, int first, int step, int l, float* sum) {
@@ -287,6 +281,16 @@ __device__ __forceinline__ void sum_run(const WriteArgs& a, const Scale& ks, siz
   }
 }
 
+// A block takes one KV head and a window of consecutive tokens, D/8 threads per
+// row and ROWS rows per thread, all loaded before the first slot is needed: the
+// stores of a window then lie next to each other in its pages.  The block that
+// holds the first token of a page's run also takes the page's mean: the rows in
+// front of it from the cache, the run's own from k (now in L2), so that nothing
+// is read that another block of this launch writes.  The block's threads are
+// shared between the runs that begin in its window: all of them on one (a prompt:
+// up to 128 rows in one round of loads), or D/8 on each (a decoding step).
+// Bound: HBM for prompts (28 005 tokens of 8 heads, bf16: 50 us, 5.1 TB/s; 41 us without
+// means, whose second look at k comes after the first), latency for a step (4.7 us).
 template <int D, bool kE4M3Cache, int ROWS>
 __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const WriteArgs a) {
   constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES;
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const Wri
 // the exact scores are; where more pages than needed lie between (ties, or
 // neighbours closer than 2^-19 of their size), those are computed in fp64 and
 // ranked again.  Bound: the means are read once, 2 D bytes per page and KV head;
-// 4725 pages of 40 heads (48 MB) take SCORE_US us, in two-word fp32 arithmetic 20.
+// 4725 pages of 40 heads (48 MB) take 15 us, in two-word fp32 arithmetic 20.
 
 constexpr int kScoreThreads = 256;
 constexpr int kTopkKeys = 8;  // consecutive keys per thread and step
@@ -863,7 +867,7 @@ cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
   // 32 pages per warp; fewer where that would leave SMs idle
   int per_warp = 32;
   while (per_warp > 8 && static_cast<long long>(a.B) * head_blocks *
-                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 152 * 4)
+                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 152 * 2)
     per_warp /= 2;
   // and no more blocks than a few rounds of all SMs: a table is often far longer than its sequences
   const long long pairs = static_cast<long long>(a.B) * head_blocks;
@@ -874,7 +878,7 @@ cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
                                    kScoreThreads, 0, stream, a, head_blocks, page_blocks, per_warp, stride);
   if (e != cudaSuccess) return e;
   // three digits over 2048 counters for long lists, four over 256 for short ones, whose
-  // counters would cost more than their keys (512 lists of up to 512 pages: 38 us and TOPK_US)
+  // counters would cost more than their keys (512 lists of up to 512 pages: 38 us and 9)
   const int threads = a.max_pages > 4096 ? 1024 : (a.max_pages > 1024 ? 512 : 128);
   const int bits = threads == 128 ? 8 : 11;
   return launch_dependent(paged_topk_kernel, a.B * a.Hkv, threads, (kTopkCopies << bits) * sizeof(uint32_t), stream, a,
