@@ -247,63 +247,35 @@ __device__ __forceinline__ void add8(float* sum, uint2 c, float scale) {
 
 constexpr int kWriteThreads = 256;
 
-// sum += rows first, first + step, ... of a page's off old rows, then of the run's rows of
-// k; eight loads at a time, which are all that hides their latency.
-template <int D, bool kE4M3Cache>
-__device__ __forceinline__ void sum_run(const WriteArgs& a, const Scale& ks, size_t page_row, size_t src, int off,
-                                        int run, int first, int step, int l, float* sum) {
-  using Word = typename std::conditional<kE4M3Cache, uint2, uint4>::type;  // 8 stored values
-  const Word* old = reinterpret_cast<const Word*>(
-      static_cast<const uint8_t*>(a.k_cache) + (page_row * D + 8 * l) * (kE4M3Cache ? 1 : 2));
-  for (int r = first; r < off; r += 8 * step) {
-    Word x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = Word{};
-      if (r + i * step < off) x[i] = old[(r + i * step) * (D / 8)];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) add8(sum, x[i], a.k_scale);
-  }
-  for (int r = first; r < run; r += 8 * step) {
-    uint4 x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (r + i * step < run) x[i] = ld_global_nc16(a.k + src + static_cast<size_t>(r + i * step) * a.stride);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (r + i * step >= run) break;
-      if (kE4M3Cache) add8(sum, encode8(x[i], ks), a.k_scale);
-      else add8(sum, x[i], 1.f);
-    }
+// Stores one row's 8 values of k and v at `dst` (elements) of the caches; what k's stand for
+// afterwards is added to sum.
+template <bool kE4M3Cache, bool kSum>
+__device__ __forceinline__ void store8(const WriteArgs& a, const Scale& ks, const Scale& vs, size_t dst, uint4 k,
+                                       uint4 v, float* sum) {
+  if (kE4M3Cache) {
+    const uint2 c = encode8(k, ks);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_cache) + dst) = c;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_cache) + dst) = encode8(v, vs);
+    if (kSum) add8(sum, c, a.k_scale);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_cache) + dst) = k;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + dst) = v;
+    if (kSum) add8(sum, k, 1.f);
   }
 }
 
-// A block takes one KV head and a window of consecutive tokens, D/8 threads per
-// row and ROWS rows per thread, all loaded before the first slot is needed: the
-// stores of a window then lie next to each other in its pages.  The block that
-// holds the first token of a page's run also takes the page's mean: the rows in
-// front of it from the cache, the run's own from k (now in L2), so that nothing
-// is read that another block of this launch writes.  The block's threads are
-// shared between the runs that begin in its window: all of them on one (a prompt:
-// up to 128 rows in one round of loads), or D/8 on each (a decoding step).
-// Bound: HBM for prompts (28 005 tokens of 8 heads, bf16: 50 us, 5.1 TB/s; 41 us without
-// means, whose second look at k comes after the first), latency for a step (4.7 us).
+// Without means.  A block takes one KV head and a window of consecutive tokens, D/8
+// threads per row and ROWS rows per thread, all loaded before the first slot is needed.
 template <int D, bool kE4M3Cache, int ROWS>
-__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const WriteArgs a) {
-  constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES;
-  constexpr int WINDOW = GROUPS * ROWS;
-  __shared__ int s_first[WINDOW], s_slot[WINDOW];
-  __shared__ uint32_t s_break[kWriteThreads / 32], s_lead[kWriteThreads / 32];
-  __shared__ float s_sum[GROUPS][D];
+__global__ void __launch_bounds__(kWriteThreads) paged_copy_kernel(const WriteArgs a) {
+  constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES, WINDOW = GROUPS * ROWS;
   pdl_begin();
   const unsigned window = blockIdx.x / static_cast<unsigned>(a.Hkv);
   const int h = static_cast<int>(blockIdx.x - window * a.Hkv), g = threadIdx.x / LANES, l = threadIdx.x % LANES;
-  const long long start = static_cast<long long>(window) * WINDOW, t0 = start + g;
+  const long long t0 = static_cast<long long>(window) * WINDOW + g;
   const size_t col = static_cast<size_t>(h) * D + 8 * l;
   const int shift = 31 - __clz(a.page), mask = a.page - 1;
+  const Scale ks = {a.k_scale, a.k_inv, a.k_most}, vs = {a.v_scale, a.v_inv, a.v_most};
   uint4 k[ROWS], v[ROWS];
   int slot[ROWS];
 #pragma unroll
@@ -316,15 +288,56 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const Wri
       slot[i] = a.slots[t];
     }
   }
-  // where runs begin, while the rows are on their way: a thread looks at one
-  // token of the window or of the 128 behind it (a run ends with its page)
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (slot[i] < 0) continue;
+    if (slot[i] >= a.slots_total) {
+      if (h == 0 && l == 0) atomicOr(a.status, DEV_BOUNDS);
+      continue;
+    }
+    const size_t row = ((static_cast<size_t>(slot[i] >> shift) * a.Hkv + h) << shift) + (slot[i] & mask);
+    store8<kE4M3Cache, false>(a, ks, vs, row * D + 8 * l, k[i], v[i], nullptr);
+  }
+}
+
+// With means.  A block takes one KV head and the runs (tokens of one page, one behind
+// another) that begin in its window of tokens, wherever they end; every row is so
+// read once, stored and added to its page's sum.  The rows in front of a run
+// come from the cache: no block writes what another reads.  The block's threads are
+// shared between its runs: all of them on one (a prompt), or D/8 on each (a decoding step).
+// Bound: HBM for prompts (28 005 tokens of 8 heads, bf16: 43 us; 50 when rows were copied
+// by token and each page summed afterwards, since L2 had lost a part of k by then, and
+// 55 without the requests to L2 ahead), the conversions for E4M3 prompts (47 us), latency
+// for a step (4.5 us).
+template <int D, bool kE4M3Cache, int WINDOW>
+__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const WriteArgs a) {
+  constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES, AHEAD = 2;
+  __shared__ int s_first[WINDOW], s_slot[WINDOW];
+  __shared__ uint32_t s_break[kWriteThreads / 32], s_lead[kWriteThreads / 32];
+  __shared__ float s_sum[GROUPS][D];
+  pdl_begin();
+  const unsigned window = blockIdx.x / static_cast<unsigned>(a.Hkv);
+  const int h = static_cast<int>(blockIdx.x - window * a.Hkv), g = threadIdx.x / LANES, l = threadIdx.x % LANES;
+  const long long start = static_cast<long long>(window) * WINDOW;
+  const size_t col = static_cast<size_t>(h) * D + 8 * l;
+  const int shift = 31 - __clz(a.page), mask = a.page - 1;
+  // the window's rows, 128 bytes per request, set out before the first slot is known
+  constexpr int LINES = D / 64;
+  for (int i = g; i < WINDOW; i += GROUPS) {
+    if (start + i >= a.T || l >= 2 * LINES) continue;
+    const __nv_bfloat16* row = (l < LINES ? a.k : a.v) + (start + i) * a.stride + static_cast<size_t>(h) * D;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + l % LINES * 64));
+  }
+  // where runs begin: a thread looks at one token of the window or of the 128
+  // behind it (a run ends with its page)
   int count = 0;
-  if (a.k_mean != nullptr) {
+  {
     static_assert(WINDOW + 128 <= kWriteThreads, "a thread per token");
     const long long t = start + threadIdx.x;
     const int mine = t < a.T ? a.slots[t] : -1, before = t > 0 && t <= a.T ? a.slots[t - 1] : -1;
     const bool begins = mine < 0 || (mine & mask) == 0 || before != mine - 1;
     const bool leads = begins && mine >= 0 && mine < a.slots_total && threadIdx.x < WINDOW;
+    if (mine >= a.slots_total && threadIdx.x < WINDOW && h == 0) atomicOr(a.status, DEV_BOUNDS);
     const uint32_t bb = __ballot_sync(0xffffffffu, begins), lb = __ballot_sync(0xffffffffu, leads);
     if (lane_id() == 0) {
       s_break[warp_id()] = bb;
@@ -341,27 +354,9 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const Wri
       s_first[rank] = static_cast<int>(threadIdx.x);
       s_slot[rank] = mine;
     }
+    __syncthreads();
   }
   const Scale ks = {a.k_scale, a.k_inv, a.k_most}, vs = {a.v_scale, a.v_inv, a.v_most};
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (slot[i] < 0) continue;
-    if (slot[i] >= a.slots_total) {
-      if (h == 0 && l == 0) atomicOr(a.status, DEV_BOUNDS);
-      continue;
-    }
-    const size_t row = ((static_cast<size_t>(slot[i] >> shift) * a.Hkv + h) << shift) + (slot[i] & mask);
-    const size_t dst = row * D + 8 * l;
-    if (kE4M3Cache) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_cache) + dst) = encode8(k[i], ks);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_cache) + dst) = encode8(v[i], vs);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_cache) + dst) = k[i];
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + dst) = v[i];
-    }
-  }
-  if (a.k_mean == nullptr) return;
-  __syncthreads();
   // teams of `size` times D/8 threads, one run each
   int size = GROUPS;
   while (size > 1 && size * count > GROUPS) size /= 2;
@@ -379,8 +374,37 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const Wri
       while (bits == 0) bits = s_break[++word];
       const int run = 32 * word + __ffs(bits) - 1 - at;
       rows = off + run;
-      sum_run<D, kE4M3Cache>(a, ks, (static_cast<size_t>(page_id) * a.Hkv + h) << shift,
-                             static_cast<size_t>(start + at) * a.stride + col, off, run, member, size, l, sum);
+      const size_t page_row = (static_cast<size_t>(page_id) * a.Hkv + h) << shift;
+      const __nv_bfloat16* src_k = a.k + static_cast<size_t>(start + at) * a.stride + col;
+      const __nv_bfloat16* src_v = a.v + static_cast<size_t>(start + at) * a.stride + col;
+      using Word = typename std::conditional<kE4M3Cache, uint2, uint4>::type;  // 8 stored values
+      const Word* old = reinterpret_cast<const Word*>(
+          static_cast<const uint8_t*>(a.k_cache) + (page_row * D + 8 * l) * (kE4M3Cache ? 1 : 2));
+      for (int r = member; r < off; r += 8 * size) {
+        Word x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = Word{};
+          if (r + i * size < off) x[i] = old[(r + i * size) * LANES];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) add8(sum, x[i], a.k_scale);
+      }
+      for (int r = member; r < run; r += AHEAD * size) {
+        uint4 k[AHEAD], v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          if (r + i * size < run) {
+            k[i] = ld_global_nc16(src_k + static_cast<size_t>(r + i * size) * a.stride);
+            v[i] = ld_global_nc16(src_v + static_cast<size_t>(r + i * size) * a.stride);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          if (r + i * size < run)
+            store8<kE4M3Cache, true>(a, ks, vs, (page_row + off + r + i * size) * D + 8 * l, k[i], v[i], sum);
+        }
+      }
     }
     if (size > 1) {
 #pragma unroll
@@ -831,8 +855,9 @@ static cudaError_t write_launch(const WriteArgs& a, cudaStream_t stream) {
   const bool many = static_cast<long long>(a.T) * a.Hkv >= 152LL * 8 * 4 * GROUPS;
   const int window = GROUPS * (many ? 4 : 1);
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.T) + window - 1) / window * a.Hkv);
-  return many ? launch_dependent(paged_write_kernel<D, E4M3, 4>, blocks, kWriteThreads, 0, stream, a)
-              : launch_dependent(paged_write_kernel<D, E4M3, 1>, blocks, kWriteThreads, 0, stream, a);
+  auto kernel = a.k_mean ? (many ? paged_write_kernel<D, E4M3, 4 * GROUPS> : paged_write_kernel<D, E4M3, GROUPS>)
+                         : (many ? paged_copy_kernel<D, E4M3, 4> : paged_copy_kernel<D, E4M3, 1>);
+  return launch_dependent(kernel, blocks, kWriteThreads, 0, stream, a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t stream) {
