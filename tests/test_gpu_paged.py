@@ -413,6 +413,58 @@ def test_write_matches_oracle(lens, new, Hkv, D, page, stride, e4m3):
     assert eq(k2, c.k) and eq(v2, c.v)
 
 
+@pytest.mark.parametrize("D,Hkv,page,e4m3,means", [(128, 8, 64, False, True), (64, 5, 128, True, True),
+                                                 (128, 7, 16, True, True), (64, 8, 32, False, False)])
+def test_write_of_long_prompts(D, Hkv, page, e4m3, means):
+    """Enough tokens for the widest windows; runs that begin in one block's window and end in the next's."""
+    r = np.random.default_rng(page)
+    B, P = 6, 100_000 // page
+    lens = r.integers(0, 3 * page, B)
+    new = r.integers(1, 2 * 152 * 8 * 4 * (256 // (D // 8)) // Hkv // B, B)
+    new[-1] += max(0, 152 * 8 * 4 * (256 // (D // 8)) // Hkv + 1 - int(new.sum()))
+    need = -(-(lens + new) // page)
+    num = int(need.sum()) + 5
+    order, table, at = r.permutation(num), np.full((B, P), -1), 0
+    for b in range(B):
+        table[b, :-(-lens[b] // page)] = order[at:at + -(-lens[b] // page)]
+        at += -(-lens[b] // page)
+    T = int(new.sum()) + 9
+    slots = po.plan(new, lens, order[at:], 0, table, page, T, num)[4]
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    k, v, s = rand(T, Hkv, D), rand(T, Hkv, D), _i32(slots)
+    if e4m3:
+        c = torch.randint(0, 0x78, (2, num, Hkv, page, D), generator=g, device="cuda").to(torch.uint8)
+        codes = [torch.empty(x.shape, dtype=torch.uint8, device="cuda") for x in (k, v)]
+        for x, y, f in zip((k, v), codes, (KS, VS)):
+            mcs.mcs_quantize_e4m3(x, f, y)
+        values = lambda x: x.view(torch.float8_e4m3fn).double() * KS
+    else:
+        c, codes, values = rand(2, num, Hkv, page, D), [k, v], lambda x: x.double()
+    want = c.clone()
+    live = s >= 0
+    for i in range(2):
+        want[i][s[live] // page, :, s[live] % page] = codes[i][live]
+    p = mcs.paged(B, Hkv, Hkv, D, page, num, P, kv=int(e4m3), k_scale=KS, v_scale=VS)
+    mean = rand(num, Hkv, D)
+    before = mean.clone()
+    mcs.mcs_paged_write(p, k, v, s, c[0], c[1], mean if means else None)
+    assert mcs.mcs_device_status() == 0
+    assert torch.equal(c.view(torch.uint8), want.view(torch.uint8))
+    fill = torch.zeros(num, dtype=torch.int64, device="cuda")
+    fill.scatter_reduce_(0, (s[live] // page).long(), (s[live] % page + 1).long(), "amax")
+    touched = fill > 0
+    assert torch.equal(mean[~touched], before[~touched])
+    if not means:
+        assert torch.equal(mean, before)
+        return
+    rows = torch.arange(page, device="cuda")[None] < fill[touched][:, None]
+    x = torch.where(rows[:, None, :, None], values(want[0][touched]), 0.0)
+    n = fill[touched][:, None, None]
+    exact, size = x.sum(2) / n, x.abs().sum(2) / n
+    assert ((mean[touched].double() - exact).abs() <= 2.0 ** -8 * exact.abs() + (page + 2) * U * size).all()
+
+
 @pytest.mark.parametrize("ks,vs", [(KS, VS), (1.0, 3.0), (0.7131, 2.0 ** -20), (2.0 ** -90, 2.0 ** 70),
                                    (2.0 ** -60, 1.9999999), (1e-38, 3e38)])
 def test_write_rounds_every_value_as_the_quantiser(ks, vs):
