@@ -443,7 +443,7 @@ typedef struct {
   int num_pages;      /* pages of the cache */
   int max_pages;      /* entries per row of block_table */
   int kv;             /* MCS_KV_BF16 (0) or MCS_KV_E4M3 (1) */
-  float scale;        /* softmax scale; 0 selects 1/sqrt(D) */
+  float scale;        /* softmax scale; 0 selects 1/sqrt(D).  scale * k_scale (E4M3) * log2(e) is finite */
   float k_scale, v_scale; /* E4M3: scales of the two caches, > 0; ignored for bf16 */
   int q_stride;       /* elements between the rows of consecutive tokens of q; 0: Hq * D */
   int kv_stride;      /* the same of k and v given to mcs_paged_write; 0: Hkv * D */
@@ -555,7 +555,7 @@ mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void
  * in place is possible where the layouts are equal (MCS_LAYOUT_BNHD, stride 0
  * or H * D).  Hkv = 0: no k (its pointers are ignored).
  * Supported: D in {64, 128}, rot a multiple of 16 in [0, D], strides multiples
- * of 8, B * N * (Hq + Hkv) below 2^31.
+ * of 8, B * N * (Hq + Hkv) and D * (Hq + Hkv) below 2^31.
  */
 typedef struct {
   int B, N, Hq, Hkv, D;

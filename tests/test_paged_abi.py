@@ -30,6 +30,7 @@ BAD_PAGED = [
     (dict(kv=1, k_scale=0.0), INVALID), (dict(kv=1, v_scale=float("inf")), INVALID),
     (dict(kv=1, k_scale=float("nan")), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(q_stride=1016), INVALID),
+    (dict(kv=1, scale=1e10, k_scale=1e30), INVALID), (dict(scale=3e38), INVALID),
     (dict(q_stride=1028), INVALID), (dict(kv_stride=248), INVALID), (dict(kv_stride=-256), INVALID),
 ]
 
@@ -121,7 +122,8 @@ BAD_ROPE = [
     (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID), (dict(q_stride=504), INVALID),
     (dict(q_stride=516), INVALID), (dict(k_stride=8), INVALID), (dict(table_rows=4), INVALID),
     (dict(table_rows=-1), INVALID), (dict(B=1 << 20, N=1 << 11), UNSUPPORTED),
-    (dict(B=1 << 15, N=1 << 14), UNSUPPORTED),
+    (dict(B=1 << 15, N=1 << 14), UNSUPPORTED), (dict(B=1, Hq=1 << 24), UNSUPPORTED),
+    (dict(B=1, Hkv=1 << 25, D=64), UNSUPPORTED),
 ]
 
 
@@ -170,6 +172,18 @@ def test_binding_refuses_host_tensors(monkeypatch):
         mcs.mcs_paged_plan(p, i(2), i(2), i(4), i(1), i(2, 4), i(2), i(1), i(3), i(3))
     with pytest.raises(ValueError, match="sel must be"):
         mcs.mcs_paged_select(p, f(2, 8, 128), f(9, 2, 128), i(2, 4), i(2), i(2, 4), f(256))
+    # sizes that a C int cannot hold are refused, not cut
+    big = lambda *s: torch.empty(*s, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="slots"):
+        mcs.mcs_paged_write(p, f(3, 2, 128), f(3, 2, 128), big((1 << 32) + 3), cache, cache)
+    with pytest.raises(ValueError, match="slots"):
+        mcs.mcs_paged_plan(p, i(2), i(2), i(4), i(1), i(2, 4), i(2), i(1), i(3), big((1 << 32) + 3))
+    with pytest.raises(ValueError, match="free_pages"):
+        mcs.mcs_paged_plan(p, i(2), i(2), big(1 << 31), i(1), i(2, 4), i(2), i(1), i(3), i(3))
+    with pytest.raises(ValueError, match="sel"):
+        mcs.mcs_paged_select(p, f(2, 8, 128), f(9, 2, 128), i(2, 4), i(2), big(2, 2, (1 << 32) + 2), f(256))
+    with pytest.raises(ValueError, match="sink"):
+        mcs.mcs_paged_select(p, f(2, 8, 128), f(9, 2, 128), i(2, 4), i(2), i(2, 2, 2), f(256), sink=1 << 32)
     r = mcs.rope_params(**ROPE)
     with pytest.raises(ValueError, match="CUDA"):
         mcs.mcs_qk_norm_rope(r, f(2, 5, 4, 128), f(2, 5, 2, 128), None, None, None, None, None,

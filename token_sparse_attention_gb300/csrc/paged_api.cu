@@ -19,6 +19,12 @@ bool good_stride(int s, long long row) { return s == 0 || (s >= row && s % 8 == 
 constexpr long long kIntMax = 0x7fffffffLL;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// What a product of stored q and k is multiplied by, for powers of two.
+float scale_log2_of(const mcs_paged* p) {
+  const float scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf(static_cast<float>(p->D));
+  return scale * (p->kv == MCS_KV_E4M3 ? p->k_scale : 1.f) * kLog2e;
+}
+
 mcs_status check_paged(const mcs_paged* p) {
   if (p == nullptr) return MCS_ERR_INVALID_ARG;
   if (p->B < 1 || p->Hkv < 1 || p->Hq < 1 || p->Hq % p->Hkv != 0 || p->num_pages < 1 ||
@@ -32,7 +38,8 @@ mcs_status check_paged(const mcs_paged* p) {
   if (p->kv != MCS_KV_BF16 && p->kv != MCS_KV_E4M3) return MCS_ERR_INVALID_ARG;
   if (p->kv == MCS_KV_E4M3 && (!good_scale(p->k_scale) || !good_scale(p->v_scale)))
     return MCS_ERR_INVALID_ARG;
-  if (!(p->scale >= 0.f) || !isfinite(p->scale)) return MCS_ERR_INVALID_ARG;
+  if (!(p->scale >= 0.f) || !isfinite(p->scale) || !isfinite(scale_log2_of(p)))
+    return MCS_ERR_INVALID_ARG;
   if (!good_stride(p->q_stride, static_cast<long long>(p->Hq) * p->D) ||
       !good_stride(p->kv_stride, static_cast<long long>(p->Hkv) * p->D))
     return MCS_ERR_INVALID_ARG;
@@ -70,8 +77,7 @@ mcs_status run_decode(const mcs_paged* p, const void* q, const void* k_cache, co
   a.num_pages = p->num_pages;
   a.max_pages = p->max_pages;
   a.q_stride = q_stride_of(p);
-  const float scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf(static_cast<float>(p->D));
-  a.scale_log2 = scale * (e4m3 ? p->k_scale : 1.f) * kLog2e;
+  a.scale_log2 = scale_log2_of(p);
   a.v_scale = e4m3 ? p->v_scale : 1.f;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = k_cache;
@@ -97,7 +103,8 @@ mcs_status check_rope(const mcs_rope* p) {
     return MCS_ERR_INVALID_ARG;
   if (p->layout != MCS_LAYOUT_BHND && p->layout != MCS_LAYOUT_BNHD) return MCS_ERR_INVALID_ARG;
   const long long tokens = static_cast<long long>(p->B) * p->N;
-  if (tokens > kIntMax || static_cast<long long>(p->Hq) + p->Hkv > kIntMax / tokens)
+  const long long heads = static_cast<long long>(p->Hq) + p->Hkv;
+  if (tokens > kIntMax || heads > kIntMax / tokens || heads > kIntMax / p->D)
     return MCS_ERR_UNSUPPORTED;
   if (!good_stride(p->q_stride, static_cast<long long>(p->Hq) * p->D) ||
       !good_stride(p->k_stride, static_cast<long long>(p->Hkv) * p->D))

@@ -616,6 +616,13 @@ def _rows_at(dev, t, dtype, shape, stride, name):
     return t.data_ptr()
 
 
+def _count(n, name):
+    """A size the library takes as an int (ctypes would cut it to 32 bits without a word)."""
+    if n > 0x7FFFFFFF:
+        raise ValueError(f"{name}: {n} elements are more than a call takes")
+    return n
+
+
 def _cache_at(dev, t, kv, shape, name):
     if kv == KV_E4M3:
         if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
@@ -629,8 +636,8 @@ _BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 def mcs_paged_plan(p: Paged, new_lens, lens, free_pages, free_head, block_table, lens_out,
                    head_out, cu_new, slots, positions=None, stream=None):
-    dev, B, T = _device(stream), (p.B,), slots.numel()
-    one, n_free = (1,), free_pages.numel()
+    T, n_free = _count(slots.numel(), "slots"), _count(free_pages.numel(), "free_pages")
+    dev, B, one = _device(stream), (p.B,), (1,)
     _check(lib().mcs_paged_plan(
         ctypes.byref(p), _at(dev, new_lens, _I32, B, "new_lens"), _at(dev, lens, _I32, B, "lens"),
         _at(dev, free_pages, _I32, (n_free,), "free_pages"), n_free,
@@ -643,7 +650,8 @@ def mcs_paged_plan(p: Paged, new_lens, lens, free_pages, free_head, block_table,
 
 
 def mcs_paged_write(p: Paged, k, v, slots, k_cache, v_cache, k_mean=None, stream=None):
-    dev, T, Hkv, D, pages, kv = _device(stream), slots.numel(), p.Hkv, p.D, p.num_pages, p.kv
+    T = _count(slots.numel(), "slots")
+    dev, Hkv, D, pages, kv = _device(stream), p.Hkv, p.D, p.num_pages, p.kv
     rows, cache, stride = (T, Hkv, D), (pages, Hkv, p.page, D), p.kv_stride
     _check(lib().mcs_paged_write(
         ctypes.byref(p), T, _rows_at(dev, k, _BF, rows, stride, "k"),
@@ -679,13 +687,14 @@ def mcs_paged_select_workspace(p: Paged) -> int:
 def _select_of(sel) -> int:
     if not isinstance(sel, torch.Tensor) or sel.dim() != 3:
         raise ValueError("sel must be a [B, Hkv, select] tensor")
-    return sel.shape[2]
+    return _count(sel.shape[2], "sel")
 
 
 def mcs_paged_select(p: Paged, q, k_mean, block_table, lens, sel, ws, sink=1, recent=1,
                      stream=None):
     """sel [B, Hkv, select]: the last dimension says how many pages are kept."""
-    dev, B, Hkv, D, keep = _device(stream), p.B, p.Hkv, p.D, _select_of(sel)
+    keep, sink, recent = _select_of(sel), _count(sink, "sink"), _count(recent, "recent")
+    dev, B, Hkv, D = _device(stream), p.B, p.Hkv, p.D
     _check(lib().mcs_paged_select(
         ctypes.byref(p), _rows_at(dev, q, _BF, (B, p.Hq, D), p.q_stride, "q"),
         _at(dev, k_mean, _BF, (p.num_pages, Hkv, D), "k_mean"),
@@ -697,8 +706,9 @@ def mcs_paged_select(p: Paged, q, k_mean, block_table, lens, sel, ws, sink=1, re
 
 def mcs_paged_decode_sparse(p: Paged, q, k_cache, v_cache, block_table, lens, sel, out, ws,
                             lse=None, stream=None):
+    keep = _select_of(sel)
     dev, B, Hq, Hkv, D, kv = _device(stream), p.B, p.Hq, p.Hkv, p.D, p.kv
-    cache, rows, keep = (p.num_pages, Hkv, p.page, D), (B, Hq, D), _select_of(sel)
+    cache, rows = (p.num_pages, Hkv, p.page, D), (B, Hq, D)
     _check(lib().mcs_paged_decode_sparse(
         ctypes.byref(p), _rows_at(dev, q, _BF, rows, p.q_stride, "q"),
         _cache_at(dev, k_cache, kv, cache, "k_cache"),
