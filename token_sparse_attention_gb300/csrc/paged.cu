@@ -371,8 +371,9 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const Wri
       // the run reaches to the next beginning behind it
       int word = (at + 1) / 32;
       uint32_t bits = s_break[word] >> ((at + 1) % 32) << ((at + 1) % 32);
-      while (bits == 0) bits = s_break[++word];
-      const int run = 32 * word + __ffs(bits) - 1 - at;
+      while (bits == 0 && word < kWriteThreads / 32 - 1) bits = s_break[++word];
+      // (slots that change under the call cannot lead out of the page)
+      const int run = min(32 * word + (bits != 0 ? __ffs(bits) - 1 : 32) - at, a.page - off);
       rows = off + run;
       const size_t page_row = (static_cast<size_t>(page_id) * a.Hkv + h) << shift;
       const __nv_bfloat16* src_k = a.k + static_cast<size_t>(start + at) * a.stride + col;
@@ -818,11 +819,13 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i) {
       if (j + i >= n) break;
+      // (keys that another call overwrites cannot lead out of the list)
+      const int at = more + min(same, equal);
       if (keys.x[i] > least) {
-        sel[more + min(same, equal)] = j + i;
+        if (at < keep) sel[at] = j + i;
         ++more;
       } else if (keys.x[i] == least) {
-        if (same < equal) sel[more + same] = j + i;
+        if (same < equal && at < keep) sel[at] = j + i;
         ++same;
       }
     }
