@@ -470,7 +470,7 @@ __device__ __forceinline__ float sum_of_group(const __nv_bfloat16* q, int group,
 // pages.  D/8 lanes hold a head, 8 values each; a warp sums four pages at a
 // time and folds them over the lanes, so that each fold halves what is left.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads)
+__global__ void __launch_bounds__(kScoreThreads, 3)
     paged_score_kernel(const SelectArgs a, int head_blocks, int page_blocks, int per_warp, int stride) {
   constexpr int LANES = D / 8, ROWS = 32 / LANES;
   __shared__ float s_q[ROWS * D];
@@ -516,17 +516,22 @@ __global__ void __launch_bounds__(kScoreThreads)
     if (outside) atomicOr(a.status, DEV_BOUNDS);
     const int pid = outside || !mine ? 0 : first;
     const uint32_t bad = __ballot_sync(0xffffffffu, outside);
+    // two sets of four means: each is asked for again as soon as its values are used
+    uint4 x[2][4];
+    auto fetch = [&](int set, int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[set][i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - start + i) * page_step);
+    };
+    fetch(0, start);
+    fetch(1, start + 4);
     for (int j = start; j < j1; j += 8) {
-      uint4 x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - start + i) * page_step);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int set = 0; set < 2; ++set) {
         float dot[4], mm[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t w[4] = {x[4 * half + i].x, x[4 * half + i].y, x[4 * half + i].z, x[4 * half + i].w};
+          const uint32_t w[4] = {x[set][i].x, x[set][i].y, x[set][i].z, x[set][i].w};
           uint64_t s = 0, t = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -540,6 +545,7 @@ __global__ void __launch_bounds__(kScoreThreads)
           f2_unpack(t, u, v);
           mm[i] = u + v;
         }
+        if (j + 4 * set + 8 < j1) fetch(set, j + 4 * set + 8);
         // fold over the lanes: the upper half of each group of lanes keeps the
         // upper half of the pages
         int o = LANES / 2;
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kScoreThreads)
           mm[0] += __shfl_xor_sync(0xffffffffu, mm[0], o);
         }
         // lane bits LANES/2 and LANES/4 name the page
-        const int page = j + 4 * half + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
+        const int page = j + 4 * set + ((l & (LANES / 2)) ? 2 : 0) + ((l & (LANES / 4)) ? 1 : 0);
         if (l % (LANES / 4) == 0 && page < j1 && h < a.Hkv) {
           uint32_t key = score_key_bits(__float_as_uint(dot[0]));
           float off = bound * sqrtf(mm[0] + 0x1p-120f);
