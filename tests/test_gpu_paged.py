@@ -103,14 +103,14 @@ class Cache:
           stream=stream)
         return out, ls
 
-    def check(self, out, ls, sel=None):
+    def check(self, out, ls, sel=None, terms=2 ** 31):
         B, Hq, D = self.q.shape
         k, v = (_f64(x) * s for x, s in zip((self.k, self.v), self.scales))
         q = self.q
         want, lse, absv, size = po.decode(_f64(q), k, v, self.table, self.lens, self.scale, sel)
         assert (_f64(out[B]) == 77).all() and (_f64(ls[B]) == 77).all()
         out, ls = _f64(out[:B]), _f64(ls[:B])
-        n = max(self.lens)
+        n = min(max(self.lens), terms)
         delta = (D + 8) * U * size
         tol = 2.0 ** -8 * np.abs(want) + absv * (
             2 * (2 * delta + 2.0 ** -21) + (2.0 ** -11 if self.e4m3 else 2.0 ** -16) + n * U)[..., None]
@@ -154,6 +154,28 @@ def test_decode_many_sequences_and_long_ones():
     c.check(*c.run())
     c = Cache([20011, 5], 4, 1, 128, 64, seed=9)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,e4m3,most", [(26, 8, 8, 128, False, 9000), (84, 16, 16, 64, True, 4600),
+                                                  (1, 10, 5, 128, False, 290000), (1, 18, 2, 128, False, 700000)])
+def test_decode_of_lists_long_enough_for_the_last_blocks(B, Hq, Hkv, D, e4m3, most):
+    # sequences of shared pages (a page may stand in many tables): lists so long that the
+    # last part of them goes to blocks of its own, with empty and short sequences in it
+    r = np.random.default_rng(most)
+    c = Cache([30 * 128] + [0] * (B - 1), Hq, Hkv, D, 128, e4m3, seed=B, extra=-(-most // 128) - 30)
+    live = c.table[0, :30].copy()
+    c.lens = [int(x) for x in r.integers(most * 9 // 10, most, B)]
+    for i, x in ((2, 0), (B // 2, 1), (B - 6, 0), (B - 4, 17), (B - 1, 128)):
+        if B > 1:
+            c.lens[i] = x
+    c.table = live[r.integers(0, 30, c.table.shape)]
+    c.dtable, c.dlens = _i32(c.table), _i32(c.lens)
+    first = c.run()
+    # no sum has more terms behind one another than a thread's of 80 tiles, 16 a tile, and
+    # one per part of a segment, at most 608 blocks: below 2048
+    c.check(*first, terms=2048)
+    again = c.run()
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
 def _sel(c, select, seed, holes=False):

@@ -15,20 +15,26 @@
 // Split: the keys of all (sequence, KV head) pairs, in tiles of 8 KB (K and V
 // together), form one list, and each warp of the machine takes an equal piece
 // of it whatever the lengths are.  A warp works alone: a ring of 3 tiles of its
-// own, filled by 16-byte cp.async (8 warps per SM: 192 KB in flight), no barrier
-// after the shares are known, so that the latencies of one warp's new sequence
+// own, filled by 16-byte cp.async (8 warps per SM, two CTAs: 192 KB in flight), no
+// barrier after the shares are known, so that the latencies of one warp's new sequence
 // (page numbers, queries) hide behind the other warps' loads.  What a warp holds
 // whole it writes at once.  Neighbouring warps' pieces of one segment are joined in
 // shared memory when the CTA is done, what crosses CTAs goes to the workspace, and a
 // second, programmatically dependent launch joins that in the order of the tiles.
 //
-// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 290 us;
-// 64 x 1000 tokens of 8 KV heads, bf16 (262 MB) 53 us; 1 x 1023 (4.2 MB) 10.7 us, most of
-// it latency (shares 1.5 us, page numbers and first loads 3 us, join 3 us).  What
-// bounds the long ones: SMs do not get equal parts of the bandwidth, equal shares
-// end up to 15 % apart, while the total runs above a copy's rate.  Handing the last fifth
-// out by a counter evened that (290 -> 270 us), but its sums, its counter and the
-// join of three times the parts cost as much, and ragged batches more.
+// SMs do not get equal parts of the bandwidth: with equal shares the same ones always
+// ended up to 15 % later.  So the last eighth of a long list is cut into shares of
+// 16 tiles or more for CTAs behind the resident ones, which go to the SMs that are
+// done first: 12 x 75600 tokens of 8 KV heads, E4M3 289 -> 283 us, 32 x 30000, bf16 565 ->
+// 552 us, 48 sequences up to 16001 120.5 -> 118.5 us.  From 64 tiles per warp on: at 43
+// it was 76.5 us against 74.3, at 55 even, since a share costs 4 us until its first tile
+// is there, and finer cuts cost parts (a quarter of the list in shares of 12: 123 us).
+// Which CTA does a share changes no result.  Handing shares out by a counter (a launch to
+// clear it, three times the parts) had given all of this back.
+//
+// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 283 us;
+// 1 x 1023 (4.2 MB) 9.3 us, all of it latency (shares 1.5 us, page numbers and first
+// tile 1.5, joins 2 and 4).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -40,12 +46,17 @@
 namespace mcs {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kHalfStage = 4096;              // bytes of K (and of V) in a tile
 constexpr int kStageBytes = 2 * kHalfStage;
-constexpr int kMaxCtas = 160;                 // parts in the workspace: two per warp
+constexpr int kMaxSms = 160;
+constexpr int kTailCut = 8;                   // CTAs behind the resident ones: a part of the list,
+constexpr int kTailMin = 64;                  // from so many positions per resident warp on,
+constexpr int kTailShare = 16;                // so many per warp and more,
+constexpr int kTailPerSm = 2;                 // and so many CTAs per SM at most
+constexpr int kMaxCtas = (2 + kTailPerSm) * kMaxSms;  // parts in the workspace: two per warp
 constexpr int kSegCost = 1;                   // what starting a segment costs, in tiles
 constexpr int kHeads = 16;                    // query heads per pass over a KV head
 constexpr int kPidBits = 27;                  // num_pages * page < 2^31, page >= 16
@@ -118,9 +129,9 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
 }
 
 // The list of all segments (a segment: one sequence, one KV head, up to 16
-// query heads) has tiles + kSegCost positions for each that has tiles; warp i of
-// `warps` takes positions [i * all / warps, (i + 1) * all / warps) and the tiles
-// that begin there.
+// query heads) has tiles + kSegCost positions for each that has tiles.  It is
+// cut into one share per warp, and a warp takes the tiles that begin in its
+// share: the first `big` warps equal parts of [0, cut), the others of [cut, all).
 template <int TK>
 __device__ __forceinline__ int positions_of(const DecodeArgs& a, int b) {
   const int tiles = tiles_of<TK>(a, b);
@@ -129,8 +140,38 @@ __device__ __forceinline__ int positions_of(const DecodeArgs& a, int b) {
 __device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
   return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
 }
-__device__ __forceinline__ long long active_warps(long long all, int ctas) {
-  return min(all, static_cast<long long>(ctas) * kWarps);
+struct Shares {
+  long long all, cut;
+  int big, small;  // warps
+  // the first position of share i: floor(i * cut / big), and so on (i, big, small < 2^15)
+  __device__ __forceinline__ long long begin(int i) const {
+    const bool first = i <= big;
+    const long long x = first ? cut : all - cut;
+    const unsigned n = first ? big : small, k = first ? i : i - big;
+    const long long q = divide(x, n);
+    return (first ? 0 : cut) + k * q + k * static_cast<unsigned>(x - q * n) / n;
+  }
+  // the share that holds position x
+  __device__ __forceinline__ int of(long long x) const {
+    const bool first = x < cut;
+    const long long size = first ? cut : all - cut, n = first ? big : small;
+    if (!first) x -= cut;
+    // the largest i with i * size < (x + 1) * n: an estimate that is off by one at most, then
+    // exact products
+    const long long y = (x + 1) * n;
+    int i = static_cast<int>(static_cast<float>(x) * (static_cast<float>(n) / static_cast<float>(size)));
+    while (i > 0 && i * size >= y) --i;
+    while ((i + 1) * size < y) ++i;
+    return first ? i : i + big;
+  }
+};
+// `tail` of the grid's `ctas` CTAs are the last ones.
+__device__ __forceinline__ Shares shares_of(long long all, int ctas, int tail) {
+  const int warps = (ctas - tail) * kWarps;
+  if (tail == 0 || all < static_cast<long long>(warps) * kTailMin)
+    return {all, all, static_cast<int>(min(all, static_cast<long long>(warps))), 0};
+  const long long last = divide(all, kTailCut);
+  return {all, all - last, warps, static_cast<int>(min(divide(last, kTailShare), static_cast<uint64_t>(tail * kWarps)))};
 }
 
 // A walk over a warp's share, segment by segment.
@@ -175,8 +216,8 @@ __device__ __forceinline__ void store_rows(float* to, const float (*o)[4], int r
 
 // WIDE: more than 8 query heads in a segment.
 template <int D, bool E4M3, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1)
-    paged_decode_kernel(const DecodeArgs a, int chunks) {
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_decode_kernel(const DecodeArgs a, int chunks, int tail) {
   using G = Geo<D, E4M3>;
   constexpr int RB = G::RB, TK = G::TK, NS = G::NS, CPR = G::CPR, RPI = G::RPI;
   constexpr float kShift = E4M3 ? 12.f : 0.f;   // weights carry 2^12 so that f16 holds small ones
@@ -219,13 +260,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) prefix[a.B] = upto;
   }
-  const long long warps = active_warps(all, gridDim.x);
-  const long long me = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (static_cast<long long>(blockIdx.x) * kWarps >= warps) return;  // a CTA without a share
+  const Shares shares = shares_of(all, gridDim.x, tail);
+  const int warps = shares.big + shares.small, me = blockIdx.x * kWarps + w;
+  if (static_cast<int>(blockIdx.x) * kWarps >= warps) return;  // a CTA without a share
   Walk here = {};
   bool busy = me < warps;
   if (busy) {
-    const long long lo = divide(me * all, warps), hi = divide((me + 1) * all, warps);
+    const long long lo = shares.begin(me), hi = shares.begin(me + 1);
     // (all > 0: some lane's sequences hold position lo)
     const int from = __ffs(__ballot_sync(0xffffffffu, lo < upto * segs)) - 1;
     long long base = __shfl_sync(0xffffffffu, upto - own, from);
@@ -509,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     goes_on = here.t0 + here.count < here.tb;
     if (goes_on) break;
     // ---- the segment ends here: its rows, or the last part of them
-    float* part = parts + 2 * me * part_floats(D, WIDE);
+    float* part = parts + 2 * static_cast<size_t>(me) * part_floats(D, WIDE);
 #pragma unroll
     for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
       const int head = g + 8 * r;
@@ -591,36 +632,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The share that holds position x: the largest i with i * all < (x + 1) * warps.
-__device__ __forceinline__ int share_of(long long x, long long all, long long warps) {
-  const long long y = (x + 1) * warps;
-  // an estimate that is off by one at most, then exact products
-  int i = static_cast<int>(static_cast<float>(x) * (static_cast<float>(warps) / static_cast<float>(all)));
-  while (i > 0 && i * all >= y) --i;
-  while ((i + 1) * all < y) ++i;
-  return i;
-}
-
 // One block per segment: joins its parts if several shares hold tiles of it, in
 // the order of the tiles, and writes the rows of sequences that hold nothing.
 // All rows of a part are read together, SIDES parts at a time; a thread's first
 // four parts are on their way while the maxima and weights are found.
 template <int D, bool E4M3, bool WIDE, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-    paged_join_kernel(const DecodeArgs a, int chunks, int grid) {
+    paged_join_kernel(const DecodeArgs a, int chunks, int grid, int tail) {
   constexpr int ROWS = WIDE ? 16 : 8, E = ROWS * D / 4;               // fours of a part
   constexpr int EPT = E > THREADS ? E / THREADS : 1, SIDES = E > THREADS ? 1 : THREADS / E;
   constexpr int CHUNK = THREADS / ROWS, WARPS = THREADS / 32;         // parts weighed at a time
+  constexpr int TK = Geo<D, E4M3>::TK;
   constexpr float kShift = E4M3 ? 12.f : 0.f;
   __shared__ float s_red[WARPS][ROWS], s_top[ROWS], s_f[CHUNK][ROWS];
   __shared__ float4 s_acc[SIDES][SIDES > 1 ? E : 1];
-  pdl_begin();
+  __shared__ long long s_sum[WARPS][2];
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
   const int group = a.Hq / a.Hkv, segs = a.Hkv * chunks, b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
   const int h = seg / chunks, q0 = (seg - h * chunks) * kHeads, heads = min(kHeads, group - q0);
-  const long long* prefix = static_cast<const long long*>(a.ws);
   const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
-  const long long p0 = prefix[b], size = prefix[b + 1] - p0, all = prefix[a.B] * segs;
+  // Where the segment lies follows from the lengths.  The attention kernel neither writes
+  // them nor begins before what does has ended, so they are read before it ends (1.5 us of
+  // sums and divisions off the chain); of many sequences it has left the sums.
+  long long p0 = 0, size, all = 0;
+  if (a.B <= THREADS) {
+    const long long x = tid < a.B ? positions_of<TK>(a, tid) : 0;
+    long long before = tid < b ? x : 0, total = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) s_sum[w][0] = before, s_sum[w][1] = total;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) p0 += s_sum[i][0], all += s_sum[i][1];
+    size = positions_of<TK>(a, b);
+  } else {
+    pdl_begin();
+    const long long* prefix = static_cast<const long long*>(a.ws);
+    p0 = prefix[b], size = prefix[b + 1] - p0, all = prefix[a.B];
+  }
+  all *= segs;
+  const Shares shares = shares_of(all, grid, tail);
+  const long long first = p0 * segs + seg * size;
+  const int c0 = size == 0 ? 0 : shares.of(first), c1 = size == 0 ? 0 : shares.of(first + size - kSegCost - 1);
+  if (a.B <= THREADS) pdl_begin();
   const size_t out_row = static_cast<size_t>(b) * a.Hq + h * group + q0;
   if (size == 0) {
     uint2* out = reinterpret_cast<uint2*>(a.out + out_row * D);
@@ -628,8 +685,6 @@ __global__ void __launch_bounds__(THREADS)
     if (a.lse != nullptr && tid < heads) a.lse[out_row + tid] = -INFINITY;
     return;
   }
-  const long long warps = active_warps(all, grid), first = p0 * segs + seg * size;
-  const int c0 = share_of(first, all, warps), c1 = share_of(first + size - kSegCost - 1, all, warps);
   if (c0 == c1) return;
   // shares c0 to c1 - 1 go on to the next one and are joined per CTA (the second
   // part of the CTA's first such warp); share c1 ends the segment (its first part)
@@ -751,19 +806,22 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   auto kernel = paged_decode_kernel<D, E4M3, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  // one CTA per SM, no more than the longest lists could give a tile to
+  // two CTAs per SM, no more than the longest lists could give a tile to, and the last
+  // ones (see the shares)
   const long long rows = a.sel != nullptr
                              ? static_cast<long long>(std::min(a.select, a.max_pages)) * a.page
                              : static_cast<long long>(a.max_pages) * a.page;
   constexpr int TK = Geo<D, E4M3>::TK;
   const long long most = static_cast<long long>(a.B) * a.Hkv * chunks * ((rows + TK - 1) / TK + kSegCost);
-  const int grid = static_cast<int>(std::min<long long>(std::min(sms, kMaxCtas), most));
-  if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks)) != cudaSuccess) return e;
+  const int n = std::min(sms, kMaxSms);
+  const int tail = most >= 2LL * n * kWarps * kTailMin ? kTailPerSm * n : 0;
+  const int grid = static_cast<int>(std::min<long long>(2 * n, most)) + tail;
+  if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks, tail)) != cudaSuccess) return e;
   // few segments have many parts each (8 per thread of a large block and more)
   const int segments = a.B * a.Hkv * chunks;
   if (segments <= sms / 8)
-    return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 1024>, segments, 1024, 0, stream, a, chunks, grid);
-  return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 256>, segments, 256, 0, stream, a, chunks, grid);
+    return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 1024>, segments, 1024, 0, stream, a, chunks, grid, tail);
+  return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 256>, segments, 256, 0, stream, a, chunks, grid, tail);
 }
 
 }  // namespace
