@@ -170,7 +170,7 @@ __device__ __forceinline__ Shares shares_of(long long all, int ctas, int tail) {
   const int warps = (ctas - tail) * kWarps;
   if (tail == 0 || all < static_cast<long long>(warps) * kTailMin)
     return {all, all, static_cast<int>(min(all, static_cast<long long>(warps))), 0};
-  const long long last = divide(all, kTailCut);
+  const long long last = all / kTailCut;
   return {all, all - last, warps, static_cast<int>(min(divide(last, kTailShare), static_cast<uint64_t>(tail * kWarps)))};
 }
 
@@ -266,15 +266,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   Walk here = {};
   bool busy = me < warps;
   if (busy) {
-    const long long lo = shares.begin(me), hi = shares.begin(me + 1);
+    const long long ends = shares.begin(me + (lane & 1));
+    const long long lo = __shfl_sync(0xffffffffu, ends, 0), hi = __shfl_sync(0xffffffffu, ends, 1);
     // (all > 0: some lane's sequences hold position lo)
-    const int from = __ffs(__ballot_sync(0xffffffffu, lo < upto * segs)) - 1;
-    long long base = __shfl_sync(0xffffffffu, upto - own, from);
+    const int from = per == 1 ? 0 : __ffs(__ballot_sync(0xffffffffu, lo < upto * segs)) - 1;
+    long long base = per == 1 ? 0 : __shfl_sync(0xffffffffu, upto - own, from);
     busy = false;
     for (int b0 = from * per; from >= 0 && b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
-      const long long x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, b) : 0;
-      const long long y = scan(x);
+      long long x = own, y = upto;  // (a sequence per lane: known already)
+      if (per > 1) {
+        x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, b) : 0;
+        y = scan(x);
+      }
       const uint32_t hit = __ballot_sync(0xffffffffu, lo < (base + y) * segs);
       if (hit != 0) {
         const int at = __ffs(hit) - 1;
@@ -644,9 +648,11 @@ __global__ void __launch_bounds__(THREADS)
   constexpr int CHUNK = THREADS / ROWS, WARPS = THREADS / 32;         // parts weighed at a time
   constexpr int TK = Geo<D, E4M3>::TK;
   constexpr float kShift = E4M3 ? 12.f : 0.f;
-  __shared__ float s_red[WARPS][ROWS], s_top[ROWS], s_f[CHUNK][ROWS];
+  __shared__ float s_red[WARPS][ROWS], s_top[ROWS];
+  __shared__ float2 s_f[CHUNK][ROWS];  // a part's weight, and its sum times that
   __shared__ float4 s_acc[SIDES][SIDES > 1 ? E : 1];
-  __shared__ long long s_sum[WARPS][2];
+  __shared__ float s_sums[SIDES][SIDES > 1 ? E : 1];
+  __shared__ long long s_before[WARPS][2];
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
   const int group = a.Hq / a.Hkv, segs = a.Hkv * chunks, b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
   const int h = seg / chunks, q0 = (seg - h * chunks) * kHeads, heads = min(kHeads, group - q0);
@@ -663,10 +669,10 @@ __global__ void __launch_bounds__(THREADS)
       before += __shfl_xor_sync(0xffffffffu, before, o);
       total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    if (lane == 0) s_sum[w][0] = before, s_sum[w][1] = total;
+    if (lane == 0) s_before[w][0] = before, s_before[w][1] = total;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) p0 += s_sum[i][0], all += s_sum[i][1];
+    for (int i = 0; i < WARPS; ++i) p0 += s_before[i][0], all += s_before[i][1];
     size = positions_of<TK>(a, b);
   } else {
     pdl_begin();
@@ -709,48 +715,42 @@ __global__ void __launch_bounds__(THREADS)
   }
   // maxima and weights: thread (part, row r)
   const int r = tid % ROWS, i_ml = tid / ROWS;
-  auto over_rows = [&](float v, bool max) {
-#pragma unroll
-    for (int o = 16; o >= ROWS; o >>= 1) {
-      const float y = __shfl_xor_sync(0xffffffffu, v, o);
-      v = max ? fmaxf(v, y) : v + y;
-    }
-    if (lane < ROWS) s_red[w][lane] = v;
-    __syncthreads();
-    for (int row = w; row < ROWS; row += WARPS) {  // a warp per row
-      v = lane < WARPS ? s_red[lane][row] : (max ? -INFINITY : 0.f);
-#pragma unroll
-      for (int o = WARPS / 2; o > 0; o >>= 1) {
-        const float y = __shfl_xor_sync(0xffffffffu, v, o);
-        v = max ? fmaxf(v, y) : v + y;
-      }
-      if (lane == 0) s_top[row] = v;
-    }
-    __syncthreads();
+  auto max_and_sum = [&](int i) {
+    return r < heads && i < n ? *reinterpret_cast<const float2*>(part(i) + 2 * r) : make_float2(-INFINITY, 0.f);
   };
-  float top = -INFINITY;
-  if (r < heads)
-    for (int i = i_ml; i < n; i += CHUNK) top = fmaxf(top, part(i)[2 * r]);
-  over_rows(top, true);
-  top = s_top[r];
-  float sum = 0.f;
-  float4 acc[EPT];
+  const float2 mine = max_and_sum(i_ml);
+  float top = mine.x;
+  for (int i = i_ml + CHUNK; i < n; i += CHUNK) top = fmaxf(top, max_and_sum(i).x);
 #pragma unroll
-  for (int k = 0; k < EPT; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float4& v, float f, int k) {
-    acc[k].x = fmaf(v.x, f, acc[k].x);
-    acc[k].y = fmaf(v.y, f, acc[k].y);
-    acc[k].z = fmaf(v.z, f, acc[k].z);
-    acc[k].w = fmaf(v.w, f, acc[k].w);
+  for (int o = 16; o >= ROWS; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane < ROWS) s_red[w][lane] = top;
+  __syncthreads();
+  for (int row = w; row < ROWS; row += WARPS) {  // a warp per row
+    float v = lane < WARPS ? s_red[lane][row] : -INFINITY;
+#pragma unroll
+    for (int o = WARPS / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (lane == 0) s_top[row] = v;
+  }
+  __syncthreads();
+  top = s_top[r];
+  float4 acc[EPT];
+  float sum[EPT];
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) {
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum[k] = 0.f;
+  }
+  auto add = [&](const float4& v, float2 f, int k) {
+    acc[k].x = fmaf(v.x, f.x, acc[k].x);
+    acc[k].y = fmaf(v.y, f.x, acc[k].y);
+    acc[k].z = fmaf(v.z, f.x, acc[k].z);
+    acc[k].w = fmaf(v.w, f.x, acc[k].w);
+    sum[k] += f.y;
   };
   for (int i0 = 0; i0 < n; i0 += CHUNK) {
-    float f = 0.f;
-    if (r < heads && i0 + i_ml < n) {
-      const float2 ml = *reinterpret_cast<const float2*>(part(i0 + i_ml) + 2 * r);
-      f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      sum += ml.y * f;
-    }
-    s_f[i_ml][r] = f;
+    const float2 ml = i0 == 0 ? mine : max_and_sum(i0 + i_ml);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    s_f[i_ml][r] = make_float2(f, ml.y * f);
     __syncthreads();
     const int end = min(n, i0 + CHUNK);
     int i = i0 + side;
@@ -776,27 +776,26 @@ __global__ void __launch_bounds__(THREADS)
     }
     __syncthreads();
   }
-  if (SIDES > 1) s_acc[side][e0] = acc[0];
-  float tops[EPT];  // (before the sums take their place)
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) tops[k] = s_top[row_of(k)];
-  __syncthreads();
-  over_rows(sum, false);
-  if (side > 0) return;
+  if (SIDES > 1) {
+    s_acc[side][e0] = acc[0];
+    s_sums[side][e0] = sum[0];
+    __syncthreads();
+    if (side > 0) return;
+  }
 #pragma unroll
   for (int k = 0; k < EPT; ++k) {
     const int row = row_of(k), col = (e0 + k * THREADS) % (D / 4) * 4;
     if (row >= heads) continue;
     if (SIDES > 1) {
 #pragma unroll
-      for (int i = 1; i < SIDES; ++i) add(s_acc[i][e0], 1.f, k);
+      for (int i = 1; i < SIDES; ++i) add(s_acc[i][e0], make_float2(1.f, s_sums[i][e0]), k);
     }
-    const float total = s_top[row], inv = total > 0.f || total != total ? a.v_scale / total : 0.f;
+    const float total = sum[k], inv = total > 0.f || total != total ? a.v_scale / total : 0.f;
     *reinterpret_cast<uint2*>(a.out + (out_row + row) * D + col) =
         make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
     if (a.lse != nullptr && col == 0)
       a.lse[out_row + row] =
-          total == 0.f ? -INFINITY : (tops[k] + (log2f(total) - kShift)) * 0.6931471805599453f;
+          total == 0.f ? -INFINITY : (s_top[row] + (log2f(total) - kShift)) * 0.6931471805599453f;
   }
 }
 
