@@ -261,6 +261,37 @@ def test_select_near_ties_follow_the_exact_sum():
     np.testing.assert_array_equal(sel.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("n,m", [(600, 3), (600, 40), (5000, 200), (5000, 300), (9000, 7), (9000, 400)])
+def test_select_inside_a_cluster_of_near_ties(n, m):
+    # scores of any size, and m of them that agree to about fp32's last bits (some fully) at the
+    # threshold; pages that are always kept, and one outside the cache
+    r = np.random.default_rng(n + m)
+    page, D = 32, 128
+    mean = r.standard_normal((n, 1, D))
+    mean[:, 0, 127] = 0
+    cluster = r.permutation(n)[:m]
+    mean[cluster] = mean[cluster[0]]
+    mean[cluster, 0, 127] = r.integers(-3, 4, m) * 2.0 ** -7
+    md = torch.from_numpy(mean).cuda().to(torch.bfloat16)
+    q = r.standard_normal((1, 2, D))
+    q[:, :, 127] = 2.0 ** -13
+    qd = torch.from_numpy(q).cuda().to(torch.bfloat16)
+    table = r.permutation(n)[None]
+    score = (_f64(md)[table[0], 0] @ _f64(qd)[0].sum(0)).astype(np.float32)
+    above = int((score > score[table[0] == cluster[0]].max() + 1e-3).sum())
+    for select in (above + m // 2, above + m, above + 1):
+        select = min(max(select, 5), n - 1)
+        bad = table.copy()
+        bad[0, np.argmin(score)] = n  # not among the kept ones
+        p = mcs.paged(1, 2, 1, D, page, n, n)
+        sel = torch.empty(1, 1, select, dtype=torch.int32, device="cuda")
+        ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(p))
+        mcs.mcs_paged_select(p, qd, md, _i32(bad), _i32([n * page]), sel, ws, sink=2, recent=3)
+        assert mcs.mcs_device_status() != 0  # the page outside
+        want = po.select(_f64(qd), _f64(md), table, [n * page], page, select, 2, 3)
+        np.testing.assert_array_equal(sel.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("scale", [1.0, 2.0 ** -80, 2.0 ** 100])
 def test_select_follows_the_exact_sum_at_any_size(scale):
     """Means whose squares vanish or overflow in fp32, and infinite ones."""

@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(THREADS)
   constexpr int ROWS = WIDE ? 16 : 8, E = ROWS * D / 4;               // fours of a part
   constexpr int EPT = E > THREADS ? E / THREADS : 1, SIDES = E > THREADS ? 1 : THREADS / E;
   constexpr int CHUNK = THREADS / ROWS, WARPS = THREADS / 32;         // parts weighed at a time
-  constexpr int TK = Geo<D, E4M3>::TK;
+  constexpr int TK = Geo<D, E4M3>::TK, kAtOnce = 6;  // parts a thread loads side by side
   constexpr float kShift = E4M3 ? 12.f : 0.f;
   __shared__ float s_red[WARPS][ROWS], s_top[ROWS];
   __shared__ float2 s_f[CHUNK][ROWS];  // a part's weight, and its sum times that
@@ -704,9 +704,9 @@ __global__ void __launch_bounds__(THREADS)
     return *reinterpret_cast<const float4*>(part(i) + 2 * ROWS + 4 * (e0 + k * THREADS));
   };
   auto row_of = [&](int k) { return (e0 + k * THREADS) / (D / 4); };
-  float4 x[4][EPT];
+  float4 x[kAtOnce][EPT];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < kAtOnce; ++u) {
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {
       x[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -756,20 +756,20 @@ __global__ void __launch_bounds__(THREADS)
     int i = i0 + side;
     if (i0 == 0) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u, i += SIDES) {
+      for (int u = 0; u < kAtOnce; ++u, i += SIDES) {
 #pragma unroll
         for (int k = 0; k < EPT; ++k)
           if (i < end) add(x[u][k], s_f[i][row_of(k)], k);
       }
     }
-    for (; i < end; i += 4 * SIDES) {
+    for (; i < end; i += kAtOnce * SIDES) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
         for (int k = 0; k < EPT; ++k)
           if (i + u * SIDES < end && row_of(k) < heads) x[u][k] = values(i + u * SIDES, k);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
         for (int k = 0; k < EPT; ++k)
           if (i + u * SIDES < end) add(x[u][k], s_f[i + u * SIDES - i0][row_of(k)], k);

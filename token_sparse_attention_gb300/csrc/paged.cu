@@ -441,10 +441,11 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const Wri
 // the exact scores are; where more pages than needed lie between (ties, or
 // neighbours closer than 2^-19 of their size), those are computed in fp64 and
 // ranked again.  Bound: the means are read once, 2 D bytes per page and KV head;
-// 4725 pages of 40 heads (48 MB) take 15 us, in two-word fp32 arithmetic 20.
+// 4725 pages of 40 heads (48 MB) take 12 us (15 before the next means were asked for
+// while the last ones are summed, 20 in two-word fp32 arithmetic), and the choice 8 us,
+// of which 3 are the exact scores of the lists that need some.
 
 constexpr int kScoreThreads = 256;
-constexpr int kTopkKeys = 8;  // consecutive keys per thread and step
 
 // Keys of pages that are always kept, and of pages outside the cache (last of
 // all; the attention skips them too).
@@ -579,90 +580,83 @@ __global__ void __launch_bounds__(kScoreThreads, 3)
   }
 }
 
-// The keys of a list, 8 consecutive ones per thread and step of the block; a list of one
-// step (8192 pages with 1024 threads) stays in registers.
-struct Keys {
-  uint32_t* at;
-  int n, step;
-  bool fits;
-  uint32_t x[kTopkKeys];
-  __device__ __forceinline__ void load(int j) {
-    *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(at + j);
-    *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(at + j + 4);
-  }
-  // visit(page, key) for every key, in the thread's order
-  template <typename F>
-  __device__ __forceinline__ void each(F visit) {
-    for (int j = threadIdx.x * kTopkKeys; j < n; j += step) {
-      if (!fits) load(j);
-#pragma unroll
-      for (int i = 0; i < kTopkKeys; ++i)
-        if (j + i < n) visit(j + i, x[i]);
-    }
-  }
-};
-
-// The largest key k with (number of keys >= k) >= keep, and how many of the keys
-// equal to it belong to the first `keep`: by digits of `bits` bits, counted in
-// kTopkCopies histograms (scores share their leading bits, and in one histogram all
-// warps would queue at a few counters), which are zero before and after.
-constexpr int kTopkCopies = 4;
-constexpr int kTopkOpen = 512;  // pages whose exact rank is found one by one
+constexpr int kTopkKeys = 8;    // consecutive keys per thread and pass of the block
+constexpr int kTopkCap = 8192;  // places of a list in shared memory; those of longer lists stay in L2
+constexpr int kTopkOpen = 256;  // pages whose rank is found one by one
 struct TopkShared {
-  uint32_t prefix, left;
-  int warp[32], open;
-  uint32_t off[32];
-  uint32_t key[kTopkOpen];
-  int page[kTopkOpen];
+  uint32_t digit, left, least;
+  int warp[32], near, open, above;
+  uint32_t off[32], low[32], high[32];
+  uint32_t key[kTopkOpen], exact[kTopkOpen];
+  int page[kTopkOpen], rank[kTopkOpen], open_page[kTopkOpen];
   double q[128];
 };
-__device__ __forceinline__ void nth_key(Keys& keys, int keep, int bits, uint32_t* hist, TopkShared& sh, uint32_t* key,
-                                        int* equal) {
+// 8 consecutive words (a list's rows are padded to 16 bytes).
+__device__ __forceinline__ void load8(const uint32_t* p, uint32_t* x) {
+  *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
+  *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(p + 4);
+}
+// visit(page, word) for every word of a list, 8 consecutive ones per thread and pass.
+template <typename F>
+__device__ __forceinline__ void each(const uint32_t* at, int n, F visit) {
+#pragma unroll 1
+  for (int j = threadIdx.x * kTopkKeys; j < n; j += blockDim.x * kTopkKeys) {
+    uint32_t x[kTopkKeys];
+    load8(at + j, x);
+#pragma unroll
+    for (int i = 0; i < kTopkKeys; ++i)
+      if (j + i < n) visit(j + i, x[i]);
+  }
+}
+// The counter from the top that holds the `left`-th, and how many of it are among them.
+template <bool CLEAR>
+__device__ __forceinline__ void count_from_top(uint32_t* hist, int bins, uint32_t left, TopkShared& sh) {
   const int tid = threadIdx.x, w = warp_id(), lane = lane_id(), warps = blockDim.x / 32;
-  const int bins = 1 << bits, per = bins / blockDim.x;  // 2 or 4 neighbouring bins per thread
-  uint32_t prefix = 0, left = keep;
-  for (int rest = 32; rest > 0;) {
-    const int width = min(bits, rest), shift = rest - width;
-    uint32_t* mine = hist + (w % kTopkCopies) * bins;
-    keys.each([&](int, uint32_t x) {
-      if (rest == 32 || x >> rest == prefix) atomicAdd(&mine[(x >> shift) & ((1u << width) - 1u)], 1u);
-    });
-    __syncthreads();
-    // counts from the top bin down
-    uint32_t c[4], own = 0;
+  const int top = bins - 1 - 4 * tid;  // four neighbouring ones per thread
+  uint32_t c[4], own = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = 0;
+    if (top < i) continue;
+    c[i] = hist[top - i];
+    if (CLEAR) hist[top - i] = 0;
+    own += c[i];
+  }
+  uint32_t upto = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
+  }
+  if (lane == 31) sh.warp[w] = static_cast<int>(upto);
+  __syncthreads();
+  uint32_t above = __reduce_add_sync(0xffffffffu, lane < w && lane < warps ? sh.warp[lane] : 0) + upto - own;
+  if (above < left && left <= above + own) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      c[i] = 0;
-      if (i >= per) continue;
-      const int d = bins - 1 - tid * per - i;
-#pragma unroll
-      for (int k = 0; k < kTopkCopies; ++k) {
-        c[i] += hist[k * bins + d];
-        hist[k * bins + d] = 0;
+      if (above < left && left <= above + c[i]) {
+        sh.digit = static_cast<uint32_t>(top - i);
+        sh.left = left - above;
       }
-      own += c[i];
+      above += c[i];
     }
-    uint32_t upto = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
-    }
-    if (lane == 31) sh.warp[w] = static_cast<int>(upto);
+  }
+  __syncthreads();
+}
+// The largest key k with (number of keys >= k) >= keep, and how many of the keys
+// equal to it belong to the first `keep`: by digits of log2(bins) bits, counted in hist, which is
+// zero before and after.
+__device__ __forceinline__ void nth_key(const uint32_t* keys, int n, int keep, int bins, uint32_t* hist, TopkShared& sh, uint32_t* key,
+                                        int* equal) {
+  uint32_t prefix = 0, left = keep;
+  for (int rest = 32; rest > 0;) {
+    const int width = min(31 - __clz(bins), rest), shift = rest - width;
+    each(keys, n, [&](int, uint32_t x) {
+      if (rest == 32 || x >> rest == prefix) atomicAdd(&hist[(x >> shift) & ((1u << width) - 1u)], 1u);
+    });
     __syncthreads();
-    uint32_t above = __reduce_add_sync(0xffffffffu, lane < w && lane < warps ? sh.warp[lane] : 0) + upto - own;
-    if (above < left && left <= above + own) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < per && above < left && left <= above + c[i]) {
-          sh.prefix = (prefix << width) | static_cast<uint32_t>(bins - 1 - tid * per - i);
-          sh.left = left - above;
-        }
-        above += c[i];
-      }
-    }
-    __syncthreads();
-    prefix = sh.prefix;
+    count_from_top<true>(hist, bins, left, sh);
+    prefix = (prefix << width) | sh.digit;
     left = sh.left;
     rest = shift;
   }
@@ -674,141 +668,258 @@ __device__ __forceinline__ float key_score(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
-// One block per (sequence, KV head): the threshold, the pages around it again
-// where their order is not certain, then the kept pages in order.
-__global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, int stride, int bits) {
-  extern __shared__ uint32_t hist[];  // [kTopkCopies][2^bits]
+// Which scores lie within 2E of a key's: all of them where infinities or NaN are around.
+__device__ __forceinline__ uint2 around(uint32_t key, float off) {
+  const float t = key_score(key);
+  if (!(fabsf(t) < INFINITY && off < INFINITY)) return make_uint2(kKeyBad + 1, kKeyForced - 1);
+  return make_uint2(score_key_bits(__float_as_uint(t - 2.f * off)), score_key_bits(__float_as_uint(t + 2.f * off)));
+}
+__device__ __forceinline__ void is_open(TopkShared& sh, int page) {
+  const int i = atomicAdd(&sh.open, 1);  // (their order says nothing about the result)
+  if (i < kTopkOpen) sh.open_page[i] = page;
+}
+// The rare ways are functions of their own: every block fetches the kernel's instructions once,
+// and with these in between a list took 0.7 us more.
+//
+// A lane's values of a page's mean, and the exact score from the queries summed in sh.q.
+struct Mean {
+  float x[4];
+};
+__device__ __forceinline__ Mean load_mean(const SelectArgs& a, int b, int h, int page) {
+  // (the score kernel has found the page number inside the cache)
+  const int pid = min(max(a.table[static_cast<size_t>(b) * a.max_pages + page], 0), a.num_pages - 1);
+  const __nv_bfloat16* mean = a.k_mean + (static_cast<size_t>(pid) * a.Hkv + h) * a.D;
+  Mean m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m.x[i] = 32 * i < a.D ? __bfloat162float(mean[32 * i + lane_id()]) : 0.f;
+  return m;
+}
+__device__ __forceinline__ uint32_t exact_key(const SelectArgs& a, const TopkShared& sh, const Mean& m) {
+  double s = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (32 * i < a.D) s += sh.q[32 * i + lane_id()] * static_cast<double>(m.x[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return score_key_bits(__float_as_uint(static_cast<float>(s)));
+}
+__device__ __forceinline__ void sum_queries(const SelectArgs& a, TopkShared& sh, int b, int h) {
+  const int group = a.Hq / a.Hkv;
+  for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
+    const __nv_bfloat16* q = a.q + b * a.q_stride + static_cast<size_t>(h) * group * a.D + d;
+    double s = 0;
+    for (int i = 0; i < group; ++i) s += static_cast<double>(__bfloat162float(q[static_cast<size_t>(i) * a.D]));
+    sh.q[d] = s;
+  }
+  __syncthreads();
+}
+// The words of the open pages become `yes` for the best `room` of them, `no` for the others.
+__device__ __noinline__ void settle(const SelectArgs& a, TopkShared& sh, int b, int h, int room, uint32_t* words,
+                                    uint32_t yes, uint32_t no) {
+  const int open = sh.open, w = warp_id(), warps = blockDim.x / 32;
+  Mean m = {};
+  if (w < open) m = load_mean(a, b, h, sh.open_page[w]);
+  sum_queries(a, sh, b, h);
+  for (int i = w; i < open; i += warps) {
+    if (i != w) m = load_mean(a, b, h, sh.open_page[i]);
+    const uint32_t key = exact_key(a, sh, m);
+    if (lane_id() == 0) sh.exact[i] = key;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < open; i += blockDim.x) {
+    int rank = 0;
+    for (int k = 0; k < open; ++k)
+      rank += sh.exact[k] > sh.exact[i] || (sh.exact[k] == sh.exact[i] && sh.open_page[k] < sh.open_page[i]);
+    words[sh.open_page[i]] = rank < room ? yes : no;
+  }
+  __syncthreads();
+}
+// Without steps: the threshold digit by digit.  Returned are the key above which pages are kept,
+// and how many of those that equal it.
+__device__ __noinline__ uint2 by_digits(const SelectArgs& a, TopkShared& sh, int b, int h, uint32_t* hist, uint32_t* keys,
+                                        int n, int keep, int bins, float off) {
+  uint32_t last;
+  int equal;
+  nth_key(keys, n, keep, bins, hist, sh, &last, &equal);
+  if (last == kKeyForced || last == kKeyBad) return make_uint2(last, equal);
+  const uint2 open = around(last, off);
+  each(keys, n, [&](int page, uint32_t x) {
+    if (x > open.y) atomicAdd(&sh.above, 1);
+    if (x >= open.x && x <= open.y) is_open(sh, page);
+  });
+  __syncthreads();
+  if (sh.open <= kTopkOpen) {
+    settle(a, sh, b, h, keep - sh.above, keys, kKeyForced, kKeyBad);
+    return make_uint2(open.y, 0);
+  }
+  // ties en masse: exact keys for all of them, forced and bad ones for the rest, and the
+  // threshold again
+  sum_queries(a, sh, b, h);
+  const int lane = lane_id();
+  for (int j0 = warp_id() * 32; j0 < n; j0 += blockDim.x) {
+    uint32_t key = j0 + lane < n ? keys[j0 + lane] : kKeyBad;
+    uint32_t todo = __ballot_sync(0xffffffffu, key >= open.x && key <= open.y);
+    key = key > open.y ? kKeyForced : kKeyBad;
+    while (todo != 0) {
+      const int k = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const uint32_t x = exact_key(a, sh, load_mean(a, b, h, j0 + k));
+      if (lane == k) key = x;
+    }
+    if (j0 + lane < n) keys[j0 + lane] = key;
+  }
+  __syncthreads();
+  nth_key(keys, n, keep, bins, hist, sh, &last, &equal);
+  return make_uint2(last, equal);
+}
+
+// One block per (sequence, KV head).  The scores are counted in equal steps from the least to
+// the largest.  Pages above the neighbours of the step that holds the select-th are kept, those
+// below them are not (a step is wider than 2E); of the few in between the select-th is found by
+// rank, and what lies within 2E of it is ranked by the exact scores.  Where that does not
+// separate few pages (infinite scores, a range as narrow as the bound, ties en masse), the
+// threshold is found digit by digit (which for all lists took 1 to 2 us more than steps).
+__global__ void __launch_bounds__(1024) paged_topk_kernel(const __grid_constant__ SelectArgs a, int stride, int bins) {
+  extern __shared__ __align__(16) uint32_t hist[];  // [bins], then the places of a list that fits
   __shared__ TopkShared sh;
   const int bh = blockIdx.x, b = bh / a.Hkv, h = bh % a.Hkv, tid = threadIdx.x, w = warp_id(), lane = lane_id();
-  const int warps = blockDim.x / 32;
-  for (int i = tid; i < kTopkCopies << bits >> 2; i += blockDim.x)
-    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) sh.open = 0;
-  pdl_begin();
+  const int threads = blockDim.x, warps = threads / 32;
+  for (int i = tid; i < bins; i += threads) hist[i] = 0;
+  if (tid == 0) sh.near = sh.open = sh.above = 0;
+  // (the score kernel, which has begun, neither writes the lengths nor begins before what does has ended)
   const int len = a.lens[b];
+  pdl_begin();
   const bool bad = bad_length(a, len);
   if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
   const int n = bad || len == 0 ? 0 : (len - 1) / a.page + 1;
   const int keep = min(n, a.select);
   int32_t* sel = a.sel + static_cast<size_t>(bh) * a.select;
-  for (int i = keep + tid; i < a.select; i += blockDim.x) sel[i] = -1;
+  for (int i = keep + tid; i < a.select; i += threads) sel[i] = -1;
   if (n <= keep) {
-    for (int i = tid; i < n; i += blockDim.x) sel[i] = i;
+    for (int i = tid; i < n; i += threads) sel[i] = i;
     return;
   }
-  Keys keys;
-  keys.at = a.keys + 2 * static_cast<size_t>(bh) * stride;
-  keys.n = n;
-  keys.step = blockDim.x * kTopkKeys;
-  keys.fits = n <= keys.step;
-  // the keys, and the largest error bound of the list (bounds are >= 0: ordered as integers)
-  uint32_t off_bits = 0;
-  for (int j = tid * kTopkKeys; j < n; j += keys.step) {
-    Keys o;
-    o.at = keys.at + stride;
-    o.load(j);
-    keys.load(j);
+  uint32_t* keys = a.keys + 2 * static_cast<size_t>(bh) * stride;
+  // places: 0 for pages outside the cache, bins - 1 for pages always kept, steps of the scores between
+  uint32_t* places = n <= kTopkCap ? hist + bins : keys + stride;
+  const int pass = threads * kTopkKeys, mine = tid * kTopkKeys;
+  // the keys, their range, and the largest error bound (bounds are >= 0: ordered as integers)
+  uint32_t x[kTopkKeys], off_bits = 0, low = kKeyForced, high = kKeyBad;
+  for (int j = mine; j < n; j += pass) {
+    uint32_t e[kTopkKeys];
+    load8(keys + j, x);
+    load8(keys + stride + j, e);
 #pragma unroll
-    for (int i = 0; i < kTopkKeys; ++i)
-      if (j + i < n) off_bits = max(off_bits, o.x[i]);
+    for (int i = 0; i < kTopkKeys; ++i) {
+      if (j + i >= n) continue;
+      off_bits = max(off_bits, e[i]);
+      if (x[i] == kKeyForced || x[i] == kKeyBad) continue;
+      low = min(low, x[i]);
+      high = max(high, x[i]);
+    }
   }
   off_bits = __reduce_max_sync(0xffffffffu, off_bits);
-  if (lane == 0) sh.off[w] = off_bits;
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) sh.off[w] = off_bits, sh.low[w] = low, sh.high[w] = high;
   __syncthreads();
-  uint32_t least;  // kept: keys above it, and the first `equal` that equal it
-  int equal;
-  nth_key(keys, keep, bits, hist, sh, &least, &equal);
-  if (least != kKeyForced && least != kKeyBad) {
-    const float off = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? sh.off[lane] : 0u));
-    const float t = key_score(least);
-    uint32_t lo = kKeyBad + 1, hi = kKeyForced - 1;  // infinities or NaN around: every page again
-    if (fabsf(t) < INFINITY && off < INFINITY) {
-      lo = score_key_bits(__float_as_uint(t - 2.f * off));
-      hi = score_key_bits(__float_as_uint(t + 2.f * off));
-    }
-    // pages above, and those in between
-    int above = 0;
-    keys.each([&](int page, uint32_t x) {
-      above += x > hi;
-      if (x >= lo && x <= hi) {
-        const int i = atomicAdd(&sh.open, 1);  // (their order says nothing about the result)
-        if (i < kTopkOpen) sh.page[i] = page;
-      }
-    });
-    above = __reduce_add_sync(0xffffffffu, above);
-    if (lane == 0) sh.warp[w] = above;
-    __syncthreads();
-    above = __reduce_add_sync(0xffffffffu, lane < warps ? sh.warp[lane] : 0);
-    const int open = sh.open;
-    if (above + open == keep) {
-      least = lo - 1;  // all of them, none equal
-      equal = 0;
-    } else {
-      // the exact scores of those in between
-      const int group = a.Hq / a.Hkv;
-      for (int d = tid; d < a.D; d += blockDim.x) {
-        const __nv_bfloat16* q = a.q + b * a.q_stride + static_cast<size_t>(h) * group * a.D + d;
-        double s = 0;
-        for (int i = 0; i < group; ++i) s += static_cast<double>(__bfloat162float(q[static_cast<size_t>(i) * a.D]));
-        sh.q[d] = s;
-      }
-      auto exact_key = [&](int j) {
-        // (the score kernel has found the page number inside the cache)
-        const int pid = min(max(a.table[static_cast<size_t>(b) * a.max_pages + j], 0), a.num_pages - 1);
-        const __nv_bfloat16* mean = a.k_mean + (static_cast<size_t>(pid) * a.Hkv + h) * a.D;
-        double s = 0;
-        for (int d = lane; d < a.D; d += 32) s += sh.q[d] * static_cast<double>(__bfloat162float(mean[d]));
+  const float off = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? sh.off[lane] : 0u));
+  low = __reduce_min_sync(0xffffffffu, lane < warps ? sh.low[lane] : kKeyForced);
+  high = __reduce_max_sync(0xffffffffu, lane < warps ? sh.high[lane] : kKeyBad);
+
+  const float base = key_score(low), range = key_score(high) - base, per_unit = static_cast<float>(bins - 2) / range;
+  bool by_step = low < high && range < INFINITY && per_unit < INFINITY && 2.f * off * per_unit < 0.9f;
+  uint32_t last = 0;  // kept: pages whose place (or key) is above `last`, and the first `equal` of those at it
+  int equal = 0;
+  if (by_step) {
+    uint32_t place[kTopkKeys];
+    auto places_of = [&]() {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        return score_key_bits(__float_as_uint(static_cast<float>(s)));
-      };
-      __syncthreads();
-      if (open <= kTopkOpen) {
-        // few: each one's rank among them, the best become forced, the others bad
-        for (int i = w; i < open; i += warps) {
-          const uint32_t key = exact_key(sh.page[i]);
-          if (lane == 0) sh.key[i] = key;
-        }
-        __syncthreads();
-        for (int i = tid; i < open; i += blockDim.x) {
-          int rank = 0;
-          for (int k = 0; k < open; ++k)
-            rank += sh.key[k] > sh.key[i] || (sh.key[k] == sh.key[i] && sh.page[k] < sh.page[i]);
-          keys.at[sh.page[i]] = rank < keep - above ? kKeyForced : kKeyBad;
-        }
-        least = hi;
-        equal = 0;
-        __syncthreads();
-        if (keys.fits && tid * kTopkKeys < n) keys.load(tid * kTopkKeys);
-      } else {
-        // ties en masse: exact keys for all of them, forced and bad ones for the rest,
-        // and the threshold again
-        for (int j0 = w * 32; j0 < n; j0 += warps * 32) {
-          uint32_t key = j0 + lane < n ? keys.at[j0 + lane] : kKeyBad;
-          uint32_t todo = __ballot_sync(0xffffffffu, key >= lo && key <= hi);
-          key = key > hi ? kKeyForced : kKeyBad;
-          while (todo != 0) {
-            const int k = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const uint32_t x = exact_key(j0 + k);
-            if (lane == k) key = x;
+      for (int i = 0; i < kTopkKeys; ++i) {
+        const int step = 1 + min(static_cast<int>((key_score(x[i]) - base) * per_unit), bins - 3);
+        place[i] = x[i] == kKeyForced ? bins - 1 : x[i] == kKeyBad ? 0 : step;
+      }
+    };
+#pragma unroll 1
+    for (int j = mine; j < n; j += pass) {
+      if (n > pass) load8(keys + j, x);
+      places_of();
+#pragma unroll
+      for (int i = 0; i < kTopkKeys; ++i) {
+        if (j + i >= n) break;
+        atomicAdd(&hist[place[i]], 1u);
+        places[j + i] = place[i];
+      }
+    }
+    __syncthreads();
+    count_from_top<false>(hist, bins, keep, sh);
+    const uint32_t at = sh.digit;
+    last = at;
+    if (at == 0 || at == static_cast<uint32_t>(bins - 1)) {
+      equal = static_cast<int>(sh.left);
+    } else {
+      const uint32_t first = max(at - 1, 1u);
+      last = min(at + 1, static_cast<uint32_t>(bins - 2));
+      const int over = last > at ? static_cast<int>(hist[last]) : 0, room = static_cast<int>(sh.left) + over;
+      const int near = over + static_cast<int>(hist[at]) + (first < at ? static_cast<int>(hist[first]) : 0);
+      if (near <= kTopkOpen) {
+#pragma unroll 1
+        for (int j = mine; j < n; j += pass) {
+          if (n > pass) {
+            load8(keys + j, x);
+            places_of();
           }
-          if (j0 + lane < n) keys.at[j0 + lane] = key;
+#pragma unroll
+          for (int i = 0; i < kTopkKeys; ++i) {
+            if (j + i >= n || place[i] < first || place[i] > last) continue;
+            const int k = atomicAdd(&sh.near, 1);
+            sh.page[k] = j + i;
+            sh.key[k] = x[i];
+          }
         }
         __syncthreads();
-        if (keys.fits && tid * kTopkKeys < n) keys.load(tid * kTopkKeys);
-        nth_key(keys, keep, bits, hist, sh, &least, &equal);
+        for (int i = tid; i < near; i += threads) {
+          int rank = 0;
+#pragma unroll 4
+          for (int k = 0; k < near; ++k)
+            rank += sh.key[k] > sh.key[i] || (sh.key[k] == sh.key[i] && sh.page[k] < sh.page[i]);
+          sh.rank[i] = rank;
+          if (rank == room - 1) sh.least = sh.key[i];
+        }
+        __syncthreads();
+        const uint2 open = around(sh.least, off);
+        for (int i = tid; i < near; i += threads) {
+          // (kept by rank, unless the exact scores are asked below)
+          places[sh.page[i]] = sh.rank[i] < room ? bins - 1 : 0;
+          if (sh.key[i] > open.y) atomicAdd(&sh.above, 1);
+          if (sh.key[i] >= open.x && sh.key[i] <= open.y) is_open(sh, sh.page[i]);
+        }
+        __syncthreads();
+        if (sh.open > room - sh.above) settle(a, sh, b, h, room - sh.above, places, bins - 1, 0);
+      } else {
+        by_step = false;
+        __syncthreads();
+        for (int i = tid; i < bins; i += threads) hist[i] = 0;
+        __syncthreads();
       }
     }
   }
+  if (!by_step) {
+    const uint2 cut = by_digits(a, sh, b, h, hist, keys, n, keep, bins, off);
+    last = cut.x;
+    equal = static_cast<int>(cut.y);
+  }
+  // in order
+  const uint32_t* words = by_step ? places : keys;
   int more0 = 0, same0 = 0;
-  for (int base = 0; base < n; base += keys.step) {
-    const int j = base + tid * kTopkKeys;
-    if (!keys.fits && j < n) keys.load(j);
+#pragma unroll 1
+  for (int base_page = 0; base_page < n; base_page += pass) {
+    const int j = base_page + mine;
+    if (j < n) load8(words + j, x);
     int own = 0;  // kept above in the low half, equal in the high half
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i)
-      if (j + i < n) own += keys.x[i] > least ? 1 : (keys.x[i] == least ? 0x10000 : 0);
+      if (j + i < n) own += x[i] > last ? 1 : (x[i] == last ? 0x10000 : 0);
     int upto = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -825,15 +936,12 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const SelectArgs a, in
 #pragma unroll
     for (int i = 0; i < kTopkKeys; ++i) {
       if (j + i >= n) break;
+      const bool tie = x[i] == last;
+      const int to = more + min(same, equal);
       // (keys that another call overwrites cannot lead out of the list)
-      const int at = more + min(same, equal);
-      if (keys.x[i] > least) {
-        if (at < keep) sel[at] = j + i;
-        ++more;
-      } else if (keys.x[i] == least) {
-        if (same < equal && at < keep) sel[at] = j + i;
-        ++same;
-      }
+      if ((x[i] > last || (tie && same < equal)) && to < keep) sel[to] = j + i;
+      more += x[i] > last;
+      same += tie;
     }
     more0 += all & 0xFFFF;
     same0 += all >> 16;
@@ -911,12 +1019,10 @@ cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
   cudaError_t e = launch_dependent(a.D == 128 ? paged_score_kernel<128> : paged_score_kernel<64>, blocks,
                                    kScoreThreads, 0, stream, a, head_blocks, page_blocks, per_warp, stride);
   if (e != cudaSuccess) return e;
-  // three digits over 2048 counters for long lists, four over 256 for short ones, whose
-  // counters would cost more than their keys (512 lists of up to 512 pages: 38 us and 9)
-  const int threads = a.max_pages > 4096 ? 1024 : (a.max_pages > 1024 ? 512 : 128);
-  const int bits = threads == 128 ? 8 : 11;
-  return launch_dependent(paged_topk_kernel, a.B * a.Hkv, threads, (kTopkCopies << bits) * sizeof(uint32_t), stream, a,
-                          stride, bits);
+  // as many threads as the longest list keeps busy; of the counters, four per thread
+  const int threads = std::min((stride / kTopkKeys + 127) / 128 * 128, 1024), bins = std::min(4 * threads, 2048);
+  return launch_dependent(paged_topk_kernel, a.B * a.Hkv, threads, (bins + std::min(stride, kTopkCap)) * sizeof(uint32_t),
+                          stream, a, stride, bins);
 }
 
 }  // namespace mcs
