@@ -749,6 +749,56 @@ def test_captured_step_follows_lengths_and_pages():
     assert mcs.mcs_device_status() == 0
 
 
+@pytest.mark.parametrize("B,page,D", [(5, 16, 128), (40, 32, 64)])
+def test_steps_one_behind_another_see_their_own_lengths(B, page, D):
+    # lengths that change from step to step, many steps in one graph with nothing between the
+    # launches, against the same steps one at a time
+    r = np.random.default_rng(B)
+    steps, Hkv, Hq, P = 24, 2, 4, 24 * 40 // page + 2
+    num = B * P
+    p = mcs.paged(B, Hq, Hkv, D, page, num, P)
+    g = torch.Generator(device="cuda").manual_seed(B)
+    kc, vc, q = (torch.randn(*x, generator=g, device="cuda").to(torch.bfloat16)
+                 for x in ((num, Hkv, page, D), (num, Hkv, page, D), (B, Hq, D)))
+    mean = kc.float().mean(2).to(torch.bfloat16)
+    new = _i32(r.integers(0, 40, (steps, B)) * (r.random((steps, B)) < 0.7))
+    slots, cu, free = _i32(np.zeros(40 * B)), _i32(np.zeros(B + 1)), _i32(r.permutation(num))
+    ws = mcs.empty_workspace(max(mcs.mcs_paged_decode_workspace(p), mcs.mcs_paged_select_workspace(p)))
+
+    def run(between):
+        lens, head, table = _i32(np.zeros(B)), _i32([0]), _i32(np.zeros((B, P)))
+        outs = torch.zeros(steps, 2, B, Hq, D, dtype=torch.bfloat16, device="cuda")
+        sels = torch.zeros(steps, B, Hkv, 5, dtype=torch.int32, device="cuda")
+        def go():
+            lens.zero_(), head.zero_()
+            for i in range(steps):
+                mcs.mcs_paged_plan(p, new[i], lens, free, head, table, lens, head, cu, slots)
+                between()
+                mcs.mcs_paged_decode(p, q, kc, vc, table, lens, outs[i, 0], ws)
+                between()
+                mcs.mcs_paged_select(p, q, mean, table, lens, sels[i], ws)
+                between()
+                mcs.mcs_paged_decode_sparse(p, q, kc, vc, table, lens, sels[i], outs[i, 1], ws)
+                between()
+        return go, outs, sels
+
+    go, want, want_sel = run(torch.cuda.synchronize)
+    go()
+    go, outs, sels = run(lambda: None)
+    go()
+    torch.cuda.synchronize()
+    assert torch.equal(outs, want) and torch.equal(sels, want_sel)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for _ in range(3):
+        outs.zero_(), sels.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs, want) and torch.equal(sels, want_sel)
+    assert mcs.mcs_device_status() == 0
+
+
 def test_rows_past_two_gib_of_cache():
     """Pages whose byte offsets pass 32 bits: a 4.3 GB cache, the sequence's pages at its end."""
     page, Hkv, D, num = 64, 8, 128, 33000

@@ -124,8 +124,8 @@ __device__ __forceinline__ int list_rows(const DecodeArgs& a, int len) {
   return min(pages_of(a, len), a.select) * a.page;
 }
 template <int TK>
-__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
-  return (list_rows(a, a.lens[b]) + TK - 1) / TK;
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int len) {
+  return (list_rows(a, len) + TK - 1) / TK;
 }
 
 // The list of all segments (a segment: one sequence, one KV head, up to 16
@@ -133,8 +133,8 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
 // cut into one share per warp, and a warp takes the tiles that begin in its
 // share: the first `big` warps equal parts of [0, cut), the others of [cut, all).
 template <int TK>
-__device__ __forceinline__ int positions_of(const DecodeArgs& a, int b) {
-  const int tiles = tiles_of<TK>(a, b);
+__device__ __forceinline__ int positions_of(const DecodeArgs& a, int len) {
+  const int tiles = tiles_of<TK>(a, len);
   return tiles > 0 ? tiles + kSegCost : 0;
 }
 __device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
@@ -190,7 +190,7 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DecodeArgs& a, int s
     w.seg = 0;
     do {  // (there is one, unless the lengths change under the kernel)
       if (++w.b >= a.B) return false;
-      w.tb = tiles_of<TK>(a, w.b);
+      w.tb = tiles_of<TK>(a, a.lens[w.b]);
     } while (w.tb == 0);
   }
   w.t0 = 0;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   long long own = 0;
 #pragma unroll 4
   for (int i = 0; i < per; ++i)
-    if (b_lane + i < a.B) own += positions_of<TK>(a, b_lane + i);
+    if (b_lane + i < a.B) own += positions_of<TK>(a, a.lens[b_lane + i]);
   auto scan = [&](long long x) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (blockIdx.x == 0 && w == 0) {
     long long sum = upto - own;
     for (int b = b_lane; b < min(a.B, b_lane + per); ++b) {
-      const int x = positions_of<TK>(a, b);
+      const int x = positions_of<TK>(a, a.lens[b]);
       if (x == 0 && a.lens[b] != 0) atomicOr(a.status, DEV_BOUNDS);
       prefix[b] = sum;
       sum += x;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int b = b0 + lane;
       long long x = own, y = upto;  // (a sequence per lane: known already)
       if (per > 1) {
-        x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, b) : 0;
+        x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, a.lens[b]) : 0;
         y = scan(x);
       }
       const uint32_t hit = __ballot_sync(0xffffffffu, lo < (base + y) * segs);
@@ -659,10 +659,11 @@ __global__ void __launch_bounds__(THREADS)
   const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
   // Where the segment lies follows from the lengths.  The attention kernel neither writes
   // them nor begins before what does has ended, so they are read before it ends (1.5 us of
-  // sums and divisions off the chain); of many sequences it has left the sums.
+  // sums and divisions off the chain), from L2, since an L1 may hold older ones until the
+  // wait; of many sequences it has left the sums.
   long long p0 = 0, size, all = 0;
   if (a.B <= THREADS) {
-    const long long x = tid < a.B ? positions_of<TK>(a, tid) : 0;
+    const long long x = tid < a.B ? positions_of<TK>(a, __ldcg(a.lens + tid)) : 0;
     long long before = tid < b ? x : 0, total = x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(THREADS)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) p0 += s_before[i][0], all += s_before[i][1];
-    size = positions_of<TK>(a, b);
+    size = positions_of<TK>(a, __ldcg(a.lens + b));
   } else {
     pdl_begin();
     const long long* prefix = static_cast<const long long*>(a.ws);

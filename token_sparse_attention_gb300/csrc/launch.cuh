@@ -4,6 +4,9 @@
 // visible, and only then lets its own successor be set up; so the order of
 // reads and writes between kernels is that of plain launches, and what is
 // saved is the launch latency (1 to 2 us per kernel in a chain of short ones).
+// What a call's first kernel found finished when it began, and does not write itself, its
+// second kernel may read before pdl_begin(): it is set up when all blocks of the first
+// have begun.  Nothing is written before pdl_begin().
 #pragma once
 
 #include <cuda_runtime_api.h>

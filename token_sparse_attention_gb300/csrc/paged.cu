@@ -786,8 +786,9 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const __grid_constant_
   const int threads = blockDim.x, warps = threads / 32;
   for (int i = tid; i < bins; i += threads) hist[i] = 0;
   if (tid == 0) sh.near = sh.open = sh.above = 0;
-  // (the score kernel, which has begun, neither writes the lengths nor begins before what does has ended)
-  const int len = a.lens[b];
+  // (the score kernel neither writes the lengths nor begins before what does has ended; an L1
+  // may hold older ones until the wait)
+  const int len = __ldcg(a.lens + b);
   pdl_begin();
   const bool bad = bad_length(a, len);
   if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
