@@ -580,9 +580,12 @@ def _at(dev, t, dtype, shape, name):
 
 def _bytes_at(dev, t, name):
     """(pointer, size) of a workspace."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    return _at(dev, t, torch.uint8, t.shape, name), t.numel()
+    try:
+        if t.dtype is _U8 and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
+    return _refuse(dev, t, _U8, None, name)
 
 
 def _rows_at(dev, t, dtype, shape, stride, name):
@@ -624,14 +627,14 @@ def _count(n, name):
 
 
 def _cache_at(dev, t, kv, shape, name):
-    if kv == KV_E4M3:
-        if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
-            t = t.view(torch.uint8)
-        return _at(dev, t, torch.uint8, shape, name)
-    return _at(dev, t, torch.bfloat16, shape, name)
+    dtype = _BF
+    if kv == KV_E4M3:  # codes as bytes or as what they stand for
+        dtype = _F8 if getattr(t, "dtype", None) is _F8 else _U8
+    return _at(dev, t, dtype, shape, name)
 
 
 _BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_U8, _F8 = torch.uint8, torch.float8_e4m3fn
 
 
 def mcs_paged_plan(p: Paged, new_lens, lens, free_pages, free_head, block_table, lens_out,
