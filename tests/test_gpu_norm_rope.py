@@ -153,7 +153,10 @@ def test_backward_matches_oracle(case):
 @pytest.mark.parametrize("case", [
     (2, 5003, 2, 1, 64, 64, False, 0, True, True, True), (1, 9801, 20, 1, 128, 32, True, 1, False, False, True),
     (3, 3301, 1, 0, 128, 128, False, 1, False, True, False), (1, 10007, 3, 4, 64, 48, True, 0, False, True, True),
-    (1, 9999, 1, 12, 128, 128, True, 0, True, True, True)], ids=lambda c: "-".join(str(int(x)) for x in c))
+    (1, 9999, 1, 12, 128, 128, True, 0, True, True, True),
+    # and many of more heads: blocks that take several units, two and four rows per thread
+    (1, 4999, 8, 16, 128, 96, False, 0, True, True, True), (2, 1501, 40, 10, 128, 128, True, 1, False, True, True),
+    (1, 6007, 16, 9, 64, 64, False, 1, False, True, True)], ids=lambda c: "-".join(str(int(x)) for x in c))
 def test_many_tokens_of_few_heads(case):
     """Warps that take several tokens (one, both or no tensors of such a call), with padding among them."""
     c = Case(*case)

@@ -29,13 +29,15 @@ constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = 32 * kRopeWarps;
 // Loads in flight per thread and blocks per SM, measured: forward 4 at D = 128 and 8 at
 // D = 64, whose rows are half as long (75600 tokens, 64 heads of D = 64: 84 -> 90 % of
-// copy bandwidth); backward 2 rows of x and dy (32760 tokens, 24 heads of D = 128: 116 us
-// with 4 rows and 3 blocks, 112 with 2 and 3, 109 with 2 and 4; 80 heads of D = 64: 195 us
-// with 2 and 3, 238 with 2 and 4, whose spills cost more than the blocks bring).
+// copy bandwidth).  The gradients have two forms, 2 rows of x and dy per thread and 3 blocks, or
+// 4 and 2, which has less to find out per row, but takes twice the heads at a time: 32760 tokens,
+// 12 + 12 heads of D = 128: 97 us and 103; 40000 tokens, 40 + 8 heads: 244 and 214; 75600 tokens,
+// 32 + 32 heads of D = 64: 300 and 325 (D = 128, 2 rows and 4 blocks: spills, 40 + 8 heads 410).
 template <int D> struct Tune {
   static constexpr int STEPS = 512 / D, BLOCKS = D == 128 ? 4 : 3;
-  static constexpr int GRAD_STEPS = 2, GRAD_BLOCKS = D == 128 ? 4 : 3;
+  static constexpr int FEW_STEPS = 2, FEW_BLOCKS = D == 128 ? 4 : 3;  // gradients of few heads
 };
+__host__ __device__ constexpr int grad_blocks(int steps) { return steps == 2 ? 3 : 2; }
 constexpr int kGradBlocks = 2048;  // most partial sums of the weight gradients, half of them of k
 
 // Heads of one token a warp takes.
@@ -354,83 +356,151 @@ __device__ __forceinline__ void block_weight_sum(const uint64_t* da, const uint6
 // blocks_q-th unit of q (or blocks_k-th of k) and keeps the weight gradient of
 // its units in registers, one partial row per block at the end.
 //   g = dy rotated back, dx = r (w g - x r^2 mean(w g x)), dw += g x r
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
+// A warp's next unit (rows of x and dy, angles) is on its way to shared memory while it
+// computes one, and the position after that to a register (with loads to registers, one unit
+// after the other, 32760 tokens of 12 + 12 heads took 109 us).
+__host__ __device__ constexpr int kGradStage(int steps) { return 2 * steps * 512 + 512; }  // bytes of x and dy, then the angles
+constexpr int kGradStages = 2;
+
+template <int D, bool SPLIT, int STEPS>
+__global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
     norm_rope_backward_kernel(const RopeArgs a, int blocks_q, int blocks_k) {
-  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::GRAD_STEPS;
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, HEADS = heads_per_warp(D, STEPS);
+  constexpr int STAGE = kGradStage(STEPS), ANGLES = 2 * STEPS * 512;
+  extern __shared__ __align__(16) uint8_t grad_smem[];
   pdl_begin();
   const bool is_q = static_cast<int>(blockIdx.x) < blocks_q;
   const int H = is_q ? a.Hq : a.Hkv;
-  const unsigned chunks = (H + heads_per_warp(D, Tune<D>::GRAD_STEPS) - 1) / heads_per_warp(D, Tune<D>::GRAD_STEPS);
+  const unsigned chunks = (H + HEADS - 1) / HEADS;
   const unsigned block = is_q ? blockIdx.x : blockIdx.x - blocks_q, blocks = is_q ? blocks_q : blocks_k;
   const unsigned tokens = static_cast<unsigned>(a.B) * a.N;
-  const unsigned units = (tokens + kRopeWarps - 1) / kRopeWarps * chunks;
-  const int l = lane_id() % LANES, r0 = lane_id() / LANES;
+  const int lane = lane_id(), l = lane % LANES, r0 = lane / LANES;
   const Place at = place_of<SPLIT>(a.rot, l);
+  const __nv_bfloat16* xs = is_q ? a.q : a.k;
   const __nv_bfloat16* dys = is_q ? a.dq_out : a.dk_out;
+  __nv_bfloat16* dxs = is_q ? a.q_out : a.k_out;
   const long long stride = is_q ? a.q_stride : a.k_stride;
+  uint8_t* ring = grad_smem + warp_id() * (kGradStages * STAGE);
   uint64_t wa[2], wb[2], da[2] = {0, 0}, db[2] = {0, 0};
   load_weights<SPLIT>(is_q ? a.wq : a.wk, at, wa, wb);
-  for (unsigned u = block; u < units; u += blocks) {
-    const unsigned tile = u / chunks, token = tile * kRopeWarps + warp_id();
-    if (token >= tokens) continue;  // whole warps
-    const Token t = token_of(a, token);
-    if (t.pos < 0) continue;
-    const int h0 = static_cast<int>(u - tile * chunks) * heads_per_warp(D, Tune<D>::GRAD_STEPS) + r0;
-    const size_t row = token * stride + h0 * D;
-    const __nv_bfloat16* xs = (is_q ? a.q : a.k) + row;
-    __nv_bfloat16* dxs = (is_q ? a.q_out : a.k_out) + row;
-    size_t step;
-    const __nv_bfloat16* dy = dys + out_base(a, t, H, &step);
-    Row x[STEPS], y[STEPS];
+
+  // a warp's unit: its token and chunk of heads (pos < 0: no token, or rows that stay as they are)
+  struct Unit {
+    unsigned token, chunk;
+    Token t;
+  };
+  auto find = [&](Unit& u) {
+    u.t.pos = -1;
+    if (u.token < tokens) u.t = token_of(a, u.token);
+  };
+  const unsigned tile_step = blocks / chunks, chunk_step = blocks - tile_step * chunks;
+  auto after = [&](const Unit& u) {
+    Unit v = u;
+    v.chunk += chunk_step;
+    const bool over = v.chunk >= chunks;
+    if (over) v.chunk -= chunks;
+    v.token += kRopeWarps * (tile_step + over);
+    find(v);
+    return v;
+  };
+  auto copy = [&](uint8_t* to, const void* from, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(live ? 16 : 0) : "memory");
+  };
+  auto fetch = [&](const Unit& u, uint8_t* stage) {
+    if (u.t.pos >= 0) {
+      const int h0 = static_cast<int>(u.chunk) * HEADS + r0;
+      size_t step;
+      const size_t y0 = out_base(a, u.t, H, &step) + 8 * l;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int h = h0 + i * ROWS;
-      x[i] = y[i] = Row{{0, 0, 0, 0}};
-      if (h < H) {
-        x[i] = load_row<SPLIT>(xs + i * ROWS * D, at);
-        y[i] = load_row<SPLIT>(dy + h * step, at);
+      for (int i = 0; i < STEPS; ++i) {
+        // (heads past the last one become zeros)
+        const int h = h0 + i * ROWS, hc = min(h, H - 1);
+        copy(stage + i * 512 + lane * 16, xs + u.token * stride + hc * D + 8 * l, h < H);
+        copy(stage + (STEPS + i) * 512 + lane * 16, dys + y0 + hc * step, h < H);
+      }
+      if (r0 < 2 && 8 * l < a.rot) {
+        const float* table = r0 == 0 ? a.cos_table : a.sin_table;
+        copy(stage + ANGLES + r0 * 256 + l * 16, table + static_cast<size_t>(u.t.pos) * (a.rot / 2) + 4 * l, true);
       }
     }
-    uint64_t cs[2], sn[2];
-    load_angles(a, t.pos, l, cs, sn);
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      uint64_t p[2], q[2], c[2], d[2], g[2], f[2];
-      unpack<SPLIT>(x[i], p, q);
-      unpack<SPLIT>(y[i], c, d);
-      uint64_t ss = 0, dot = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
-        g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
-        f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
-        c[k] = f2_mul(g[k], wa[k]);
-        d[k] = f2_mul(f[k], wb[k]);
-        dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
-      }
-      float s1 = f2_sum(ss), s2 = f2_sum(dot);
-      s1 = row_sum<LANES>(s1);
-      s2 = row_sum<LANES>(s2);
-      const float r = rsqrtf(s1 * (1.f / D) + a.eps), m = -(s2 * (1.f / D)) * r * r;
-      const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
-        db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
-        c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
-        d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
-      }
-      if (h0 + i * ROWS < H) store_row<SPLIT>(dxs + i * ROWS * D, at, c, d);
+    cp_async_commit();
+  };
+  auto row_in = [&](const uint8_t* p) {
+    Row r;
+    const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(p) + r0 * D;
+    if (SPLIT) {
+      const uint2 x = *reinterpret_cast<const uint2*>(row + at.a), y = *reinterpret_cast<const uint2*>(row + at.b);
+      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = y.x, r.w[3] = y.y;
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + at.a);
+      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
     }
+    return r;
+  };
+
+  Unit now = {block / chunks * kRopeWarps + warp_id(), block % chunks, {}};
+  find(now);
+  Unit next = after(now);
+  int turn = 0;
+  fetch(now, ring);
+  while (now.token < tokens) {
+    fetch(next, ring + (turn ^ 1) * STAGE);
+    const Unit later = after(next);
+    cp_async_wait_group<1>();
+    __syncwarp();
+    if (now.t.pos >= 0) {
+      const uint8_t* stage = ring + turn * STAGE;
+      const int h0 = static_cast<int>(now.chunk) * HEADS + r0;
+      __nv_bfloat16* dx = dxs + now.token * stride + h0 * D;
+      float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (8 * l < a.rot) {
+        c4 = *reinterpret_cast<const float4*>(stage + ANGLES + l * 16);
+        s4 = *reinterpret_cast<const float4*>(stage + ANGLES + 256 + l * 16);
+      }
+      const uint64_t cs[2] = {f2_pack(c4.x, c4.y), f2_pack(c4.z, c4.w)}, sn[2] = {f2_pack(s4.x, s4.y), f2_pack(s4.z, s4.w)};
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        uint64_t p[2], q[2], c[2], d[2], g[2], f[2];
+        unpack<SPLIT>(row_in(stage + i * 512), p, q);
+        unpack<SPLIT>(row_in(stage + (STEPS + i) * 512), c, d);
+        uint64_t ss = 0, dot = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
+          g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
+          f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
+          c[k] = f2_mul(g[k], wa[k]);
+          d[k] = f2_mul(f[k], wb[k]);
+          dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
+        }
+        float s1 = f2_sum(ss), s2 = f2_sum(dot);
+        s1 = row_sum<LANES>(s1);
+        s2 = row_sum<LANES>(s2);
+        const float r = rsqrtf(s1 * (1.f / D) + a.eps), m = -(s2 * (1.f / D)) * r * r;
+        const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
+          db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
+          c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
+          d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
+        }
+        if (h0 + i * ROWS < H) store_row<SPLIT>(dx + i * ROWS * D, at, c, d);
+      }
+    }
+    __syncwarp();
+    turn ^= 1;
+    now = next;
+    next = later;
   }
+  cp_async_wait_group<0>();
   block_weight_sum<D, SPLIT>(da, db, at, r0, a.ws + static_cast<size_t>(blockIdx.x) * D);
 }
 
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kRopeThreads, Tune<D>::GRAD_BLOCKS)
+__global__ void __launch_bounds__(kRopeThreads, Tune<D>::FEW_BLOCKS)
     norm_rope_few_backward_kernel(const RopeArgs a, const One one) {
-  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::GRAD_STEPS;
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::FEW_STEPS;
   pdl_begin();
   const int l = lane_id() % LANES, r0 = lane_id() / LANES;
   const Place at = place_of<SPLIT>(a.rot, l);
@@ -563,27 +633,44 @@ cudaError_t forward(const RopeArgs& a, int sms, cudaStream_t stream) {
                           kRopeThreads, 0, stream, a, cq, cq + ck);
 }
 
+template <int D, int STEPS>
+cudaError_t backward_rows(const RopeArgs& a, int blocks_q, int blocks_k, cudaStream_t stream) {
+  constexpr int kSmem = kRopeWarps * kGradStages * kGradStage(STEPS);
+  auto kernel = a.interleaved ? norm_rope_backward_kernel<D, false, STEPS> : norm_rope_backward_kernel<D, true, STEPS>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, blocks_q + blocks_k, kRopeThreads, kSmem, stream, a, blocks_q, blocks_k);
+}
+
 template <int D>
 cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
-  constexpr int heads = heads_per_warp(D, Tune<D>::GRAD_STEPS);
+  constexpr int few = heads_per_warp(D, Tune<D>::FEW_STEPS);
   const long long tokens = static_cast<long long>(a.B) * a.N, tiles = (tokens + kRopeWarps - 1) / kRopeWarps;
-  const bool few_q = few_heads(a.Hq, heads, tokens, sms), few_k = few_heads(a.Hkv, heads, tokens, sms);
-  const int cq = (a.Hq + heads - 1) / heads, ck = (a.Hkv + heads - 1) / heads;
+  const bool few_q = few_heads(a.Hq, few, tokens, sms), few_k = few_heads(a.Hkv, few, tokens, sms);
+  // four rows per thread at D = 128 where that leaves few lanes without a head
+  const int hq = few_q ? 0 : a.Hq, hk = few_k ? 0 : a.Hkv;
+  auto chunks = [](int H, int steps) { return (H + heads_per_warp(D, steps) - 1) / heads_per_warp(D, steps); };
+  const int steps = 20LL * (chunks(hq, 4) + chunks(hk, 4)) * heads_per_warp(D, 4) <= 23LL * (hq + hk) && D == 128 ? 4 : 2;
+  const int cq = chunks(hq, steps), ck = chunks(hk, steps);
   // the blocks that are resident at a time, shared between q and k by their work where
   // they run together
-  const int limit = std::min(Tune<D>::GRAD_BLOCKS * sms, kGradBlocks / 2);
-  const bool together = !few_q && !few_k && ck > 0;
-  const long long share = (static_cast<long long>(limit) * cq + (cq + ck) / 2) / (cq + ck);
-  const int limit_q = together ? static_cast<int>(std::max<long long>(1, std::min<long long>(share, limit - 1))) : limit;
-  auto blocks_of = [&](bool few, int H, int chunks, int most) {
-    const long long per = static_cast<long long>(kRopeWarps) * (few ? heads / H : 1);
-    return static_cast<int>(std::min<long long>(few ? (tokens + per - 1) / per : tiles * chunks, most));
+  const int most = std::min(grad_blocks(steps) * sms, kGradBlocks / 2), most_few = std::min(Tune<D>::FEW_BLOCKS * sms, kGradBlocks / 2);
+  auto few_blocks = [&](int H) {
+    const long long per = static_cast<long long>(kRopeWarps) * (few / H);
+    return static_cast<int>(std::min<long long>((tokens + per - 1) / per, most_few));
   };
-  const int bq = blocks_of(few_q, a.Hq, cq, limit_q), bk = ck ? blocks_of(few_k, a.Hkv, ck, together ? limit - limit_q : limit) : 0;
+  int limit_q = most, limit_k = most;
+  if (cq > 0 && ck > 0) {
+    const long long share = (static_cast<long long>(most) * cq + (cq + ck) / 2) / (cq + ck);
+    limit_q = static_cast<int>(std::max<long long>(1, std::min<long long>(share, most - 1)));
+    limit_k = most - limit_q;
+  }
+  const int bq = few_q ? few_blocks(a.Hq) : static_cast<int>(std::min<long long>(tiles * cq, limit_q));
+  const int bk = few_k ? few_blocks(a.Hkv) : static_cast<int>(std::min<long long>(tiles * ck, limit_k));
   cudaError_t e = cudaSuccess;
   for (int t = 0; t < 2; ++t) {
     if (!(t == 0 ? few_q : few_k)) continue;
-    One one = one_of(a, t == 0, heads);
+    One one = one_of(a, t == 0, few);
     one.partial = a.ws + static_cast<size_t>(t == 0 ? 0 : bq) * D;
     e = launch_dependent(a.interleaved ? norm_rope_few_backward_kernel<D, false> : norm_rope_few_backward_kernel<D, true>,
                          t == 0 ? bq : bk, kRopeThreads, 0, stream, a, one);
@@ -593,8 +680,7 @@ cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
   if (rest_q + rest_k > 0) {
     RopeArgs c = a;
     c.ws = a.ws + static_cast<size_t>(few_q ? bq : 0) * D;  // k's rows follow q's
-    e = launch_dependent(a.interleaved ? norm_rope_backward_kernel<D, false> : norm_rope_backward_kernel<D, true>,
-                         rest_q + rest_k, kRopeThreads, 0, stream, c, rest_q, rest_k);
+    e = steps == 4 ? backward_rows<D, 4>(c, rest_q, rest_k, stream) : backward_rows<D, 2>(c, rest_q, rest_k, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.dwq == nullptr && a.dwk == nullptr) return e;
