@@ -34,9 +34,9 @@ constexpr int kRopeThreads = 32 * kRopeWarps;
 // 12 + 12 heads of D = 128: 97 us and 103; 40000 tokens, 40 + 8 heads: 244 and 214; 75600 tokens,
 // 32 + 32 heads of D = 64: 300 and 325 (D = 128, 2 rows and 4 blocks: spills, 40 + 8 heads 410).
 template <int D> struct Tune {
-  static constexpr int STEPS = 512 / D, BLOCKS = D == 128 ? 4 : 3;
-  static constexpr int FEW_STEPS = 2, FEW_BLOCKS = D == 128 ? 4 : 3;  // gradients of few heads
+  static constexpr int STEPS = 512 / D, BLOCKS = D == 128 ? 4 : 3, FEW_BLOCKS = BLOCKS;
 };
+constexpr int kFewSteps = 2;  // gradients of few heads (and FEW_BLOCKS)
 __host__ __device__ constexpr int grad_blocks(int steps) { return steps == 2 ? 3 : 2; }
 constexpr int kGradBlocks = 2048;  // most partial sums of the weight gradients, half of them of k
 
@@ -356,6 +356,62 @@ __device__ __forceinline__ void block_weight_sum(const uint64_t* da, const uint6
 // blocks_q-th unit of q (or blocks_k-th of k) and keeps the weight gradient of
 // its units in registers, one partial row per block at the end.
 //   g = dy rotated back, dx = r (w g - x r^2 mean(w g x)), dw += g x r
+// 16 bytes on their way to shared memory, zeros unless `live`.
+__device__ __forceinline__ void copy16(uint8_t* to, const void* from, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+// A thread's values of a row in shared memory.
+template <bool SPLIT>
+__device__ __forceinline__ Row row_in(const uint8_t* p, Place at) {
+  Row r;
+  const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(p);
+  if (SPLIT) {
+    const uint2 x = *reinterpret_cast<const uint2*>(row + at.a), y = *reinterpret_cast<const uint2*>(row + at.b);
+    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = y.x, r.w[3] = y.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + at.a);
+    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+  }
+  return r;
+}
+__device__ __forceinline__ void angles_in(const uint8_t* cos4, const uint8_t* sin4, bool rotated, uint64_t* cs, uint64_t* sn) {
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 c = rotated ? *reinterpret_cast<const float4*>(cos4) : one;
+  const float4 s = rotated ? *reinterpret_cast<const float4*>(sin4) : zero;
+  cs[0] = f2_pack(c.x, c.y), cs[1] = f2_pack(c.z, c.w);
+  sn[0] = f2_pack(s.x, s.y), sn[1] = f2_pack(s.z, s.w);
+}
+// dx of a row (its pairs' members to c and d), and its part of the weight gradients added to da, db.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void row_gradient(const Row& x, const Row& y, float eps, const uint64_t* cs, const uint64_t* sn,
+                                             const uint64_t* wa, const uint64_t* wb, uint64_t* c, uint64_t* d, uint64_t* da,
+                                             uint64_t* db) {
+  uint64_t p[2], q[2], g[2], f[2], ss = 0, dot = 0;
+  unpack<SPLIT>(x, p, q);
+  unpack<SPLIT>(y, c, d);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
+    g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
+    f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
+    c[k] = f2_mul(g[k], wa[k]);
+    d[k] = f2_mul(f[k], wb[k]);
+    dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
+  }
+  float s1 = f2_sum(ss), s2 = f2_sum(dot);
+  s1 = row_sum<D / 8>(s1);
+  s2 = row_sum<D / 8>(s2);
+  const float r = rsqrtf(s1 * (1.f / D) + eps), m = -(s2 * (1.f / D)) * r * r;
+  const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
+    db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
+    c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
+    d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
+  }
+}
+
 // A warp's next unit (rows of x and dy, angles) is on its way to shared memory while it
 // computes one, and the position after that to a register (with loads to registers, one unit
 // after the other, 32760 tokens of 12 + 12 heads took 109 us).
@@ -403,9 +459,6 @@ __global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
     find(v);
     return v;
   };
-  auto copy = [&](uint8_t* to, const void* from, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(live ? 16 : 0) : "memory");
-  };
   auto fetch = [&](const Unit& u, uint8_t* stage) {
     if (u.t.pos >= 0) {
       const int h0 = static_cast<int>(u.chunk) * HEADS + r0;
@@ -415,29 +468,16 @@ __global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
       for (int i = 0; i < STEPS; ++i) {
         // (heads past the last one become zeros)
         const int h = h0 + i * ROWS, hc = min(h, H - 1);
-        copy(stage + i * 512 + lane * 16, xs + u.token * stride + hc * D + 8 * l, h < H);
-        copy(stage + (STEPS + i) * 512 + lane * 16, dys + y0 + hc * step, h < H);
+        copy16(stage + i * 512 + lane * 16, xs + u.token * stride + hc * D + 8 * l, h < H);
+        copy16(stage + (STEPS + i) * 512 + lane * 16, dys + y0 + hc * step, h < H);
       }
       if (r0 < 2 && 8 * l < a.rot) {
         const float* table = r0 == 0 ? a.cos_table : a.sin_table;
-        copy(stage + ANGLES + r0 * 256 + l * 16, table + static_cast<size_t>(u.t.pos) * (a.rot / 2) + 4 * l, true);
+        copy16(stage + ANGLES + r0 * 256 + l * 16, table + static_cast<size_t>(u.t.pos) * (a.rot / 2) + 4 * l, true);
       }
     }
     cp_async_commit();
   };
-  auto row_in = [&](const uint8_t* p) {
-    Row r;
-    const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(p) + r0 * D;
-    if (SPLIT) {
-      const uint2 x = *reinterpret_cast<const uint2*>(row + at.a), y = *reinterpret_cast<const uint2*>(row + at.b);
-      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = y.x, r.w[3] = y.y;
-    } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + at.a);
-      r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-    }
-    return r;
-  };
-
   Unit now = {block / chunks * kRopeWarps + warp_id(), block % chunks, {}};
   find(now);
   Unit next = after(now);
@@ -452,39 +492,13 @@ __global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
       const uint8_t* stage = ring + turn * STAGE;
       const int h0 = static_cast<int>(now.chunk) * HEADS + r0;
       __nv_bfloat16* dx = dxs + now.token * stride + h0 * D;
-      float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (8 * l < a.rot) {
-        c4 = *reinterpret_cast<const float4*>(stage + ANGLES + l * 16);
-        s4 = *reinterpret_cast<const float4*>(stage + ANGLES + 256 + l * 16);
-      }
-      const uint64_t cs[2] = {f2_pack(c4.x, c4.y), f2_pack(c4.z, c4.w)}, sn[2] = {f2_pack(s4.x, s4.y), f2_pack(s4.z, s4.w)};
+      uint64_t cs[2], sn[2];
+      angles_in(stage + ANGLES + l * 16, stage + ANGLES + 256 + l * 16, 8 * l < a.rot, cs, sn);
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        uint64_t p[2], q[2], c[2], d[2], g[2], f[2];
-        unpack<SPLIT>(row_in(stage + i * 512), p, q);
-        unpack<SPLIT>(row_in(stage + (STEPS + i) * 512), c, d);
-        uint64_t ss = 0, dot = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
-          g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
-          f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
-          c[k] = f2_mul(g[k], wa[k]);
-          d[k] = f2_mul(f[k], wb[k]);
-          dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
-        }
-        float s1 = f2_sum(ss), s2 = f2_sum(dot);
-        s1 = row_sum<LANES>(s1);
-        s2 = row_sum<LANES>(s2);
-        const float r = rsqrtf(s1 * (1.f / D) + a.eps), m = -(s2 * (1.f / D)) * r * r;
-        const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
-          db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
-          c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
-          d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
-        }
+        uint64_t c[2], d[2];
+        row_gradient<D, SPLIT>(row_in<SPLIT>(stage + i * 512 + r0 * 2 * D, at),
+                               row_in<SPLIT>(stage + (STEPS + i) * 512 + r0 * 2 * D, at), a.eps, cs, sn, wa, wb, c, d, da, db);
         if (h0 + i * ROWS < H) store_row<SPLIT>(dx + i * ROWS * D, at, c, d);
       }
     }
@@ -497,10 +511,12 @@ __global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
   block_weight_sum<D, SPLIT>(da, db, at, r0, a.ws + static_cast<size_t>(blockIdx.x) * D);
 }
 
+// (The same ring made it slower, 39 -> 42 us for 62598 tokens of 2 + 1 heads: every row has angles of
+// its own here, and the copies of those are what it spends its time on.)
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kRopeThreads, Tune<D>::FEW_BLOCKS)
     norm_rope_few_backward_kernel(const RopeArgs a, const One one) {
-  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = Tune<D>::FEW_STEPS;
+  constexpr int LANES = D / 8, ROWS = 32 / LANES, STEPS = kFewSteps;
   pdl_begin();
   const int l = lane_id() % LANES, r0 = lane_id() / LANES;
   const Place at = place_of<SPLIT>(a.rot, l);
@@ -522,33 +538,9 @@ __global__ void __launch_bounds__(kRopeThreads, Tune<D>::FEW_BLOCKS)
     }
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      uint64_t cs[2], sn[2];
+      uint64_t cs[2], sn[2], c[2], d[2];
       load_angles(a, max(pl[i].pos, 0), l, cs, sn);
-      uint64_t p[2], q[2], c[2], d[2], g[2], f[2];
-      unpack<SPLIT>(x[i], p, q);
-      unpack<SPLIT>(y[i], c, d);
-      uint64_t ss = 0, dot = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        ss = f2_fma(q[k], q[k], f2_fma(p[k], p[k], ss));
-        g[k] = f2_fma(c[k], cs[k], f2_mul(d[k], sn[k]));
-        f[k] = f2_fma(d[k], cs[k], f2_neg(f2_mul(c[k], sn[k])));
-        c[k] = f2_mul(g[k], wa[k]);
-        d[k] = f2_mul(f[k], wb[k]);
-        dot = f2_fma(d[k], q[k], f2_fma(c[k], p[k], dot));
-      }
-      float s1 = f2_sum(ss), s2 = f2_sum(dot);
-      s1 = row_sum<LANES>(s1);
-      s2 = row_sum<LANES>(s2);
-      const float r = rsqrtf(s1 * (1.f / D) + a.eps), m = -(s2 * (1.f / D)) * r * r;
-      const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        da[k] = f2_fma(f2_mul(g[k], rr), p[k], da[k]);
-        db[k] = f2_fma(f2_mul(f[k], rr), q[k], db[k]);
-        c[k] = f2_mul(f2_fma(p[k], mm, c[k]), rr);
-        d[k] = f2_mul(f2_fma(q[k], mm, d[k]), rr);
-      }
+      row_gradient<D, SPLIT>(x[i], y[i], a.eps, cs, sn, wa, wb, c, d, da, db);
       if (pl[i].pos >= 0) store_row<SPLIT>(one.out + pl[i].x, at, c, d);
     }
   }
@@ -644,7 +636,7 @@ cudaError_t backward_rows(const RopeArgs& a, int blocks_q, int blocks_k, cudaStr
 
 template <int D>
 cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
-  constexpr int few = heads_per_warp(D, Tune<D>::FEW_STEPS);
+  constexpr int few = heads_per_warp(D, kFewSteps);
   const long long tokens = static_cast<long long>(a.B) * a.N, tiles = (tokens + kRopeWarps - 1) / kRopeWarps;
   const bool few_q = few_heads(a.Hq, few, tokens, sms), few_k = few_heads(a.Hkv, few, tokens, sms);
   // four rows per thread at D = 128 where that leaves few lanes without a head
