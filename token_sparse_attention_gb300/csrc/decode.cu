@@ -636,14 +636,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// One block per segment: joins its parts if several shares hold tiles of it, in
+// Joins the parts of a segment if several shares hold tiles of it, in
 // the order of the tiles, and writes the rows of sequences that hold nothing.
 // All rows of a part are read together, SIDES parts at a time; a thread's first
-// four parts are on their way while the maxima and weights are found.
+// six parts are on their way while the maxima and weights are found.  Few segments, which
+// may have a part of every CTA each, take blocks of two rows and 512 threads (one
+// sequence of 131072 tokens and one KV head: 36 us with one block for its 8 rows, 24 so).
+// Many segments, of which most are whole, share blocks.
+constexpr int kJoinFew = 512;
+constexpr int kJoinMost = 32;  // segments a block looks at
+__host__ __device__ constexpr int join_rows(bool wide, int threads) { return threads == kJoinFew ? 2 : wide ? 16 : 8; }
 template <int D, bool E4M3, bool WIDE, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-    paged_join_kernel(const DecodeArgs a, int chunks, int grid, int tail) {
-  constexpr int ROWS = WIDE ? 16 : 8, E = ROWS * D / 4;               // fours of a part
+__global__ void __launch_bounds__(THREADS, THREADS == kJoinFew ? 2 : WIDE && D == 128 ? 3 : 4)
+    paged_join_kernel(const DecodeArgs a, int chunks, int grid, int tail, int count, bool early) {
+  constexpr int ALL = WIDE ? 16 : 8, ROWS = join_rows(WIDE, THREADS);  // rows of a part, and of those the block's
+  constexpr int E = ROWS * D / 4;                                     // fours of these
   constexpr int EPT = E > THREADS ? E / THREADS : 1, SIDES = E > THREADS ? 1 : THREADS / E;
   constexpr int CHUNK = THREADS / ROWS, WARPS = THREADS / 32;         // parts weighed at a time
   constexpr int TK = Geo<D, E4M3>::TK, kAtOnce = 6;  // parts a thread loads side by side
@@ -653,150 +660,183 @@ __global__ void __launch_bounds__(THREADS)
   __shared__ float4 s_acc[SIDES][SIDES > 1 ? E : 1];
   __shared__ float s_sums[SIDES][SIDES > 1 ? E : 1];
   __shared__ long long s_before[WARPS][2];
+  struct Segment {
+    int b, seg, c0, c1;  // the shares of its first and last tile (no tiles: c1 < 0)
+  };
+  __shared__ Segment s_todo[kJoinMost];
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
-  const int group = a.Hq / a.Hkv, segs = a.Hkv * chunks, b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
-  const int h = seg / chunks, q0 = (seg - h * chunks) * kHeads, heads = min(kHeads, group - q0);
+  const int group = a.Hq / a.Hkv, segs = a.Hkv * chunks;
+  const int at = static_cast<int>(blockIdx.x / (ALL / ROWS)) * count, row0 = static_cast<int>(blockIdx.x % (ALL / ROWS)) * ROWS;
   const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
-  // Where the segment lies follows from the lengths.  The attention kernel neither writes
+  // Where the segments lie follows from the lengths.  The attention kernel neither writes
   // them nor begins before what does has ended, so they are read before it ends (1.5 us of
   // sums and divisions off the chain), from L2, since an L1 may hold older ones until the
-  // wait; of many sequences it has left the sums.
-  long long p0 = 0, size, all = 0;
-  if (a.B <= THREADS) {
-    const long long x = tid < a.B ? positions_of<TK>(a, __ldcg(a.lens + tid)) : 0;
-    long long before = tid < b ? x : 0, total = x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    if (lane == 0) s_before[w][0] = before, s_before[w][1] = total;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < WARPS; ++i) p0 += s_before[i][0], all += s_before[i][1];
-    size = positions_of<TK>(a, __ldcg(a.lens + b));
-  } else {
-    pdl_begin();
+  // wait; where there are more blocks than can wait for it, from the sums that it has left.
+  {
+    int b = at / segs, seg = at - b * segs + tid;
+    long long p0 = 0, all = 0;
     const long long* prefix = static_cast<const long long*>(a.ws);
-    p0 = prefix[b], size = prefix[b + 1] - p0, all = prefix[a.B];
-  }
-  all *= segs;
-  const Shares shares = shares_of(all, grid, tail);
-  const long long first = p0 * segs + seg * size;
-  const int c0 = size == 0 ? 0 : shares.of(first), c1 = size == 0 ? 0 : shares.of(first + size - kSegCost - 1);
-  if (a.B <= THREADS) pdl_begin();
-  const size_t out_row = static_cast<size_t>(b) * a.Hq + h * group + q0;
-  if (size == 0) {
-    uint2* out = reinterpret_cast<uint2*>(a.out + out_row * D);
-    for (int i = tid; i < heads * D / 4; i += THREADS) out[i] = make_uint2(0, 0);
-    if (a.lse != nullptr && tid < heads) a.lse[out_row + tid] = -INFINITY;
-    return;
-  }
-  if (c0 == c1) return;
-  // shares c0 to c1 - 1 go on to the next one and are joined per CTA (the second
-  // part of the CTA's first such warp); share c1 ends the segment (its first part)
-  const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
-  auto part = [&](int i) {
-    const int c = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
-    return parts + (2 * static_cast<size_t>(c) + (i < n - 1)) * part_floats(D, WIDE);
-  };
-  const int side = tid / E, e0 = SIDES > 1 ? tid % E : tid;
-  auto values = [&](int i, int k) {
-    return *reinterpret_cast<const float4*>(part(i) + 2 * ROWS + 4 * (e0 + k * THREADS));
-  };
-  auto row_of = [&](int k) { return (e0 + k * THREADS) / (D / 4); };
-  float4 x[kAtOnce][EPT];
+    if (early) {
+      const long long x = tid < a.B ? positions_of<TK>(a, __ldcg(a.lens + tid)) : 0;
+      long long before = tid < b ? x : 0, total = x;
 #pragma unroll
-  for (int u = 0; u < kAtOnce; ++u) {
+      for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+      }
+      if (lane == 0) s_before[w][0] = before, s_before[w][1] = total;
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      x[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (side + u * SIDES < n && row_of(k) < heads) x[u][k] = values(side + u * SIDES, k);
+      for (int i = 0; i < WARPS; ++i) p0 += s_before[i][0], all += s_before[i][1];
+    } else {
+      pdl_begin();
+      p0 = prefix[b];
+      all = prefix[a.B];
     }
-  }
-  // maxima and weights: thread (part, row r)
-  const int r = tid % ROWS, i_ml = tid / ROWS;
-  auto max_and_sum = [&](int i) {
-    return r < heads && i < n ? *reinterpret_cast<const float2*>(part(i) + 2 * r) : make_float2(-INFINITY, 0.f);
-  };
-  const float2 mine = max_and_sum(i_ml);
-  float top = mine.x;
-  for (int i = i_ml + CHUNK; i < n; i += CHUNK) top = fmaxf(top, max_and_sum(i).x);
-#pragma unroll
-  for (int o = 16; o >= ROWS; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane < ROWS) s_red[w][lane] = top;
-  __syncthreads();
-  for (int row = w; row < ROWS; row += WARPS) {  // a warp per row
-    float v = lane < WARPS ? s_red[lane][row] : -INFINITY;
-#pragma unroll
-    for (int o = WARPS / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (lane == 0) s_top[row] = v;
-  }
-  __syncthreads();
-  top = s_top[r];
-  float4 acc[EPT];
-  float sum[EPT];
-#pragma unroll
-  for (int k = 0; k < EPT; ++k) {
-    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    sum[k] = 0.f;
-  }
-  auto add = [&](const float4& v, float2 f, int k) {
-    acc[k].x = fmaf(v.x, f.x, acc[k].x);
-    acc[k].y = fmaf(v.y, f.x, acc[k].y);
-    acc[k].z = fmaf(v.z, f.x, acc[k].z);
-    acc[k].w = fmaf(v.w, f.x, acc[k].w);
-    sum[k] += f.y;
-  };
-  for (int i0 = 0; i0 < n; i0 += CHUNK) {
-    const float2 ml = i0 == 0 ? mine : max_and_sum(i0 + i_ml);
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    s_f[i_ml][r] = make_float2(f, ml.y * f);
+    all *= segs;
+    // thread i: the block's i-th segment
+    if (tid < count) {
+      Segment todo = {a.B, 0, 0, 0};
+      auto size_of = [&](int i) {
+        return early ? static_cast<long long>(positions_of<TK>(a, __ldcg(a.lens + i))) : prefix[i + 1] - prefix[i];
+      };
+      long long size = b < a.B ? size_of(b) : 0;
+      for (; seg >= segs && b < a.B; seg -= segs) {
+        p0 += size;
+        size = ++b < a.B ? size_of(b) : 0;
+      }
+      if (b < a.B) {
+        todo = {b, seg, 0, -1};
+        if (size > 0) {
+          const Shares shares = shares_of(all, grid, tail);
+          const long long first = p0 * segs + seg * size;
+          todo.c0 = shares.of(first);
+          todo.c1 = shares.of(first + size - kSegCost - 1);
+        }
+      }
+      s_todo[tid] = todo;
+    }
+    if (early) pdl_begin();
     __syncthreads();
-    const int end = min(n, i0 + CHUNK);
-    int i = i0 + side;
-    if (i0 == 0) {
+  }
+#pragma unroll 1
+  for (int j = 0; j < count; ++j) {
+    const Segment todo = s_todo[j];
+    const int b = todo.b, h = todo.seg / chunks, q0 = (todo.seg - h * chunks) * kHeads + row0, heads = min(ROWS, group - q0);
+    if (b >= a.B || heads <= 0 || todo.c0 == todo.c1) continue;
+    const int c0 = todo.c0, c1 = todo.c1;
+    const size_t out_row = static_cast<size_t>(b) * a.Hq + h * group + q0;
+    if (c1 < 0) {
+      uint2* out = reinterpret_cast<uint2*>(a.out + out_row * D);
+      for (int i = tid; i < heads * D / 4; i += THREADS) out[i] = make_uint2(0, 0);
+      if (a.lse != nullptr && tid < heads) a.lse[out_row + tid] = -INFINITY;
+      continue;
+    }
+    // shares c0 to c1 - 1 go on to the next one and are joined per CTA (the second
+    // part of the CTA's first such warp); share c1 ends the segment (its first part)
+    const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
+    auto part = [&](int i) {
+      const int c = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
+      return parts + (2 * static_cast<size_t>(c) + (i < n - 1)) * part_floats(D, WIDE);
+    };
+    const int side = tid / E, e0 = SIDES > 1 ? tid % E : tid;
+    auto values = [&](int i, int k) {
+      return *reinterpret_cast<const float4*>(part(i) + 2 * ALL + row0 * D + 4 * (e0 + k * THREADS));
+    };
+    auto row_of = [&](int k) { return (e0 + k * THREADS) / (D / 4); };
+    float4 x[kAtOnce][EPT];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u, i += SIDES) {
+    for (int u = 0; u < kAtOnce; ++u) {
 #pragma unroll
-        for (int k = 0; k < EPT; ++k)
-          if (i < end) add(x[u][k], s_f[i][row_of(k)], k);
+      for (int k = 0; k < EPT; ++k) {
+        x[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (side + u * SIDES < n && row_of(k) < heads) x[u][k] = values(side + u * SIDES, k);
       }
     }
-    for (; i < end; i += kAtOnce * SIDES) {
+    // maxima and weights: thread (part, row r)
+    const int r = tid % ROWS, i_ml = tid / ROWS;
+    auto max_and_sum = [&](int i) {
+      return r < heads && i < n ? *reinterpret_cast<const float2*>(part(i) + 2 * (row0 + r)) : make_float2(-INFINITY, 0.f);
+    };
+    const float2 mine = max_and_sum(i_ml);
+    float top = mine.x;
+    for (int i = i_ml + CHUNK; i < n; i += CHUNK) top = fmaxf(top, max_and_sum(i).x);
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
+    for (int o = 16; o >= ROWS; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane < ROWS) s_red[w][lane] = top;
+    __syncthreads();
+    for (int row = w; row < ROWS; row += WARPS) {  // a warp per row
+      float v = lane < WARPS ? s_red[lane][row] : -INFINITY;
 #pragma unroll
-        for (int k = 0; k < EPT; ++k)
-          if (i + u * SIDES < end && row_of(k) < heads) x[u][k] = values(i + u * SIDES, k);
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-        for (int k = 0; k < EPT; ++k)
-          if (i + u * SIDES < end) add(x[u][k], s_f[i + u * SIDES - i0][row_of(k)], k);
+      for (int o = WARPS / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      if (lane == 0) s_top[row] = v;
     }
     __syncthreads();
-  }
-  if (SIDES > 1) {
-    s_acc[side][e0] = acc[0];
-    s_sums[side][e0] = sum[0];
-    __syncthreads();
-    if (side > 0) return;
-  }
+    top = s_top[r];
+    float4 acc[EPT];
+    float sum[EPT];
 #pragma unroll
-  for (int k = 0; k < EPT; ++k) {
-    const int row = row_of(k), col = (e0 + k * THREADS) % (D / 4) * 4;
-    if (row >= heads) continue;
+    for (int k = 0; k < EPT; ++k) {
+      acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum[k] = 0.f;
+    }
+    auto add = [&](const float4& v, float2 f, int k) {
+      acc[k].x = fmaf(v.x, f.x, acc[k].x);
+      acc[k].y = fmaf(v.y, f.x, acc[k].y);
+      acc[k].z = fmaf(v.z, f.x, acc[k].z);
+      acc[k].w = fmaf(v.w, f.x, acc[k].w);
+      sum[k] += f.y;
+    };
+    for (int i0 = 0; i0 < n; i0 += CHUNK) {
+      const float2 ml = i0 == 0 ? mine : max_and_sum(i0 + i_ml);
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      s_f[i_ml][r] = make_float2(f, ml.y * f);
+      __syncthreads();
+      const int end = min(n, i0 + CHUNK);
+      int i = i0 + side;
+      if (i0 == 0) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u, i += SIDES) {
+#pragma unroll
+          for (int k = 0; k < EPT; ++k)
+            if (i < end) add(x[u][k], s_f[i][row_of(k)], k);
+        }
+      }
+      for (; i < end; i += kAtOnce * SIDES) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+          for (int k = 0; k < EPT; ++k)
+            if (i + u * SIDES < end && row_of(k) < heads) x[u][k] = values(i + u * SIDES, k);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+          for (int k = 0; k < EPT; ++k)
+            if (i + u * SIDES < end) add(x[u][k], s_f[i + u * SIDES - i0][row_of(k)], k);
+      }
+      __syncthreads();
+    }
     if (SIDES > 1) {
-#pragma unroll
-      for (int i = 1; i < SIDES; ++i) add(s_acc[i][e0], make_float2(1.f, s_sums[i][e0]), k);
+      s_acc[side][e0] = acc[0];
+      s_sums[side][e0] = sum[0];
+      __syncthreads();
     }
-    const float total = sum[k], inv = total > 0.f || total != total ? a.v_scale / total : 0.f;
-    *reinterpret_cast<uint2*>(a.out + (out_row + row) * D + col) =
-        make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
-    if (a.lse != nullptr && col == 0)
-      a.lse[out_row + row] =
-          total == 0.f ? -INFINITY : (s_top[row] + (log2f(total) - kShift)) * 0.6931471805599453f;
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int row = row_of(k), col = (e0 + k * THREADS) % (D / 4) * 4;
+      if (row >= heads || side > 0) continue;
+      if (SIDES > 1) {
+#pragma unroll
+        for (int i = 1; i < SIDES; ++i) add(s_acc[i][e0], make_float2(1.f, s_sums[i][e0]), k);
+      }
+      const float total = sum[k], inv = total > 0.f || total != total ? a.v_scale / total : 0.f;
+      *reinterpret_cast<uint2*>(a.out + (out_row + row) * D + col) =
+          make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
+      if (a.lse != nullptr && col == 0)
+        a.lse[out_row + row] =
+            total == 0.f ? -INFINITY : (s_top[row] + (log2f(total) - kShift)) * 0.6931471805599453f;
+    }
+    __syncthreads();  // s_top, s_acc and s_f are the next one's
   }
 }
 
@@ -817,11 +857,15 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   const int tail = most >= 2LL * n * kWarps * kTailMin ? kTailPerSm * n : 0;
   const int grid = static_cast<int>(std::min<long long>(2 * n, most)) + tail;
   if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks, tail)) != cudaSuccess) return e;
-  // few segments have many parts each (8 per thread of a large block and more)
   const int segments = a.B * a.Hkv * chunks;
-  if (segments <= sms / 8)
-    return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 1024>, segments, 1024, 0, stream, a, chunks, grid, tail);
-  return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 256>, segments, 256, 0, stream, a, chunks, grid, tail);
+  if (segments <= sms / 8) {
+    constexpr int kBlocks = (WIDE ? 16 : 8) / join_rows(WIDE, kJoinFew);
+    return launch_dependent(paged_join_kernel<D, E4M3, WIDE, kJoinFew>, segments * kBlocks, kJoinFew, 0, stream, a, chunks,
+                            grid, tail, 1, true);
+  }
+  const int room = 4 * sms, count = std::min((segments + room - 1) / room, kJoinMost), blocks = (segments + count - 1) / count;
+  return launch_dependent(paged_join_kernel<D, E4M3, WIDE, 256>, blocks, 256, 0, stream, a, chunks, grid, tail, count,
+                          a.B <= 256 && blocks <= room);
 }
 
 }  // namespace
