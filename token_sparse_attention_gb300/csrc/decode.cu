@@ -26,15 +26,15 @@
 // ended up to 15 % later.  So the last eighth of a long list is cut into shares of
 // 16 tiles or more for CTAs behind the resident ones, which go to the SMs that are
 // done first: 12 x 75600 tokens of 8 KV heads, E4M3 289 -> 283 us, 32 x 30000, bf16 565 ->
-// 552 us, 48 sequences up to 16001 120.5 -> 118.5 us.  From 64 tiles per warp on: at 43
+// 552 us, 48 sequences up to 16001 120.5 -> 117 us.  From 64 tiles per warp on: at 43
 // it was 76.5 us against 74.3, at 55 even, since a share costs 4 us until its first tile
 // is there, and finer cuts cost parts (a quarter of the list in shares of 12: 123 us).
 // Which CTA does a share changes no result.  Handing shares out by a counter (a launch to
 // clear it, three times the parts) had given all of this back.
 //
 // Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 283 us;
-// 1 x 1023 (4.2 MB) 9.3 us, all of it latency (shares 1.5 us, page numbers and first
-// tile 1.5, joins 2 and 4).
+// 1 x 1023 (4.2 MB) 8.3 us, all of it latency (shares 1.3 us, page numbers and first
+// tile 1.2, its products and the CTA's join 1.9, the launch behind it 0.7 and its join 2).
 #include <cuda_fp16.h>
 
 #include <algorithm>
