@@ -837,3 +837,24 @@ def test_binding_refuses_what_does_not_fit():
     if torch.cuda.device_count() > 1:
         with pytest.raises(ValueError, match="cuda:1"):
             mcs.mcs_paged_decode(*ok[:1], c.q.to("cuda:1"), *ok[2:])
+
+
+def test_caches_of_codes_come_as_bytes_or_as_what_they_stand_for():
+    c = Cache([200, 33], 4, 2, 128, 16, True, seed=1)
+    want = c.run()
+    mean = torch.zeros(c.k.shape[0], 2, 128, dtype=torch.bfloat16, device="cuda")
+    rows, slots = torch.ones(3, 2, 128, dtype=torch.bfloat16, device="cuda"), _i32([16, 17, 40])
+    other = [x.clone() for x in (c.k, c.v, mean)]
+    mcs.mcs_paged_write(c.p, rows, rows, slots, *other)
+    c.k, c.v = c.k.view(torch.float8_e4m3fn), c.v.view(torch.float8_e4m3fn)
+    assert all(torch.equal(a, b) for a, b in zip(c.run(), want))
+    mcs.mcs_paged_write(c.p, rows, rows, slots, c.k, c.v, mean)
+    assert all(torch.equal(a.view(b.dtype), b) for a, b in zip((c.k, c.v, mean), other))
+    b = Cache([40], 4, 2, 128, 16, seed=0)
+    out = torch.empty(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    codes = b.k.to(torch.float8_e4m3fn)
+    for bad in (codes, codes.view(torch.uint8)):
+        with pytest.raises(ValueError, match="k_cache"):
+            mcs.mcs_paged_decode(b.p, b.q, bad, b.v, b.dtable, b.dlens, out, b.ws)
+    with pytest.raises(ValueError, match="ws"):
+        mcs.mcs_paged_decode(b.p, b.q, b.k, b.v, b.dtable, b.dlens, out, b.ws.view(torch.float32))

@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const __grid_constant_
     auto places_of = [&]() {
 #pragma unroll
       for (int i = 0; i < kTopkKeys; ++i) {
-        const int step = 1 + min(static_cast<int>((key_score(x[i]) - base) * per_unit), bins - 3);
+        const int step = 1 + min(max(static_cast<int>((key_score(x[i]) - base) * per_unit), 0), bins - 3);
         place[i] = x[i] == kKeyForced ? bins - 1 : x[i] == kKeyBad ? 0 : step;
       }
     };
@@ -874,6 +874,7 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const __grid_constant_
           for (int i = 0; i < kTopkKeys; ++i) {
             if (j + i >= n || place[i] < first || place[i] > last) continue;
             const int k = atomicAdd(&sh.near, 1);
+            if (k >= kTopkOpen) continue;  // (as for the list below: keys that change under the call)
             sh.page[k] = j + i;
             sh.key[k] = x[i];
           }
