@@ -199,9 +199,7 @@ __device__ __forceinline__ uint64_t quotient2(uint32_t w, const Scale& c) {
   if (c.most == 0)
     return f2_pack(__fdiv_rn(__uint_as_float(w << 16), c.s), __fdiv_rn(__uint_as_float(w & 0xFFFF0000u), c.s));
   uint32_t y;
-  asm("{\n\t.reg .b32 a;\n\tmin.NaN.bf16x2 a, %1, %2;\n\tmax.NaN.bf16x2 %0, a, %3;\n\t}"
-      : "=r"(y)
-      : "r"(w), "r"(c.most), "r"(c.most ^ 0x80008000u));
+  asm("min.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w), "r"(c.most));
   const uint64_t x = f2_pack(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u));
   const uint64_t q = f2_fma(x, f2_pack(c.inv, c.inv), 0x8000000080000000ull);
   const uint64_t rem = f2_fma(q, f2_pack(c.s, c.s), x ^ 0x8000000080000000ull);
