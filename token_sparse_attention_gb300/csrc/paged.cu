@@ -306,11 +306,15 @@ __global__ void __launch_bounds__(kWriteThreads) paged_copy_kernel(const WriteAr
 // shared between its runs: all of them on one (a prompt), or D/8 on each (a decoding step).
 // Bound: HBM for prompts (28 005 tokens of 8 heads, bf16: 43 us; 50 when rows were copied
 // by token and each page summed afterwards, since L2 had lost a part of k by then, and
-// 55 without the requests to L2 ahead), the conversions for E4M3 prompts (42 us), latency
+// 55 without the requests to L2 ahead), the conversions for E4M3 prompts (38 us), latency
 // for a step (4.5 us).
+// E4M3 prompts want more warps for their conversions, bf16 ones and steps more loads per thread
+// (5 blocks of 1 row ahead against 4 of 2: 38 us and 42, bf16 43 and 42.7, steps 4.8 and 4.5).
+constexpr bool write_by_warps(int D, bool e4m3, int window) { return e4m3 && window > kWriteThreads / (D / 8); }
 template <int D, bool kE4M3Cache, int WINDOW>
-__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_kernel(const WriteArgs a) {
-  constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES, AHEAD = 2;
+__global__ void __launch_bounds__(kWriteThreads, write_by_warps(D, kE4M3Cache, WINDOW) ? 5 : 4)
+    paged_write_kernel(const WriteArgs a) {
+  constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES, AHEAD = write_by_warps(D, kE4M3Cache, WINDOW) ? 1 : 2;
   __shared__ int s_first[WINDOW], s_slot[WINDOW];
   __shared__ uint32_t s_break[kWriteThreads / 32], s_lead[kWriteThreads / 32];
   __shared__ float s_sum[GROUPS][D];
