@@ -496,7 +496,10 @@ mcs_status mcs_paged_write(const mcs_paged* p, int T, const void* k, const void*
  * q_stride apart), out [B, Hq, D] bf16; lse [B, Hq] fp32 (natural log,
  * nullable).  lens counts the new token itself, once mcs_paged_write has stored
  * it.  A sequence of no tokens gets zeros, and -inf as its lse.
- * E4M3: q is converted to f16 as in mcs_sparse_attn_e4m3.
+ * E4M3: q is converted to f16 as in mcs_sparse_attn_e4m3 (values below 2^-14
+ * to multiples of 2^-24).  The weights enter the product with v as two parts,
+ * off by 2^-16 of a weight (bf16 cache) or 2^-22 (E4M3, and 2^-37 of the
+ * row's largest); scores, maxima and sums are fp32.
  * ws: at least mcs_paged_decode_workspace(p) bytes, used until the call's work
  * on the stream is done; its contents do not matter.  Calls that may overlap
  * on the GPU need one each.  mcs_paged_decode_workspace returns 0 for

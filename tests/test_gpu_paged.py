@@ -858,3 +858,30 @@ def test_caches_of_codes_come_as_bytes_or_as_what_they_stand_for():
             mcs.mcs_paged_decode(b.p, b.q, bad, b.v, b.dtable, b.dlens, out, b.ws)
     with pytest.raises(ValueError, match="ws"):
         mcs.mcs_paged_decode(b.p, b.q, b.k, b.v, b.dtable, b.dlens, out, b.ws.view(torch.float32))
+
+
+@pytest.mark.parametrize("n,Hq,Hkv,D,page", [(48, 1, 1, 64, 16), (200, 12, 1, 128, 32), (200, 8, 8, 64, 16),
+                                             (160, 6, 2, 128, 128)])
+@pytest.mark.parametrize("off", [2.0 ** -13, -2.0 ** -14, 2.0 ** -12 * 0.7])
+def test_e4m3_weights_keep_their_low_bits(n, Hq, Hkv, D, page, off):
+    """Half of the keys have weight 1 and value -3/4, the others weight 3/4 (1 + off) and value 1, so
+    that the output is 3/7 off and a bit: all of it lies below one f16's half step of the weight (2^-11).
+    Two f16 parts are off by 2^-22, below the 2^-21 that is allowed here; the rest as above."""
+    scale = -np.log(0.75 * (1 + off))
+    c = Cache([n], Hq, Hkv, D, page, True, seed=1, scale=float(np.float32(scale)))
+    c.scale = float(np.float32(scale))
+    c.scales, c.p.k_scale, c.p.v_scale = (1.0, 1.0), 1.0, 1.0
+    odd = torch.arange(page, device="cuda") % 2 == 1
+    code = lambda x: int(torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8))
+    c.k.zero_()
+    c.k[:, :, odd, 0] = code(-1.0)
+    c.v[:, :, odd] = code(1.0)
+    c.v[:, :, ~odd] = code(-0.75)
+    c.q.zero_()
+    c.q[:, :, 0] = 1
+    out, ls = c.run()
+    want, lse, absv, size = po.decode(_f64(c.q), _f64(c.k), _f64(c.v), c.table, c.lens, c.scale)
+    tol = 2.0 ** -8 * np.abs(want) + absv * (2 * (2 * (D + 8) * U * size + 2.0 ** -21) + 2.0 ** -21 + n * U)[..., None]
+    assert (tol < np.abs(want)).all()  # (that it would show)
+    assert (np.abs(_f64(out[:1]) - want) <= tol).all(), (_f64(out[0, 0, 0]), want[0, 0, 0])
+    c.check(out, ls)

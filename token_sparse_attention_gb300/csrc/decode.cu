@@ -32,7 +32,8 @@
 // Which CTA does a share changes no result.  Handing shares out by a counter (a launch to
 // clear it, three times the parts) had given all of this back.
 //
-// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 283 us;
+// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 284 us (282 with weights in
+// one part and one running sum in the tensor cores);
 // 1 x 1023 (4.2 MB) 8.3 us, all of it latency (shares 1.3 us, page numbers and first
 // tile 1.2, its products and the CTA's join 1.9, the launch behind it 0.7 and its join 2).
 #include <cuda_fp16.h>
@@ -487,56 +488,79 @@ __global__ void __launch_bounds__(kThreads, 2)
           m[r] = mx[r];
         }
       }
-      // weights (bf16: two parts, 2^-16 off; f16: one, 2^-11 off, the values exact)
+      // weights in two parts (bf16: 2^-16 off; f16: 2^-22, and 2^-37 of the largest weight), so that
+      // their rounding stays below fp32 sums' or the output's; one f16 part, 2^-11 off, showed
+      // wherever values cancel
       const float off0 = kShift - (m[0] == -INFINITY ? 0.f : m[0] * a.scale_log2);
       const float off1 = kShift - (m[1] == -INFINITY ? 0.f : m[1] * a.scale_log2);
+      constexpr int GS = E4M3 ? 2 : 1;  // slabs at a time
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        uint32_t p[4], pl[4];
+      for (int i0 = 0; i0 < NS; i0 += GS) {
+        uint32_t p[GS][4], pl[GS][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float* x = s[2 * i + j];
+        for (int i = 0; i < GS; ++i) {
 #pragma unroll
-          for (int e = 0; e < (WIDE ? 4 : 2); ++e) {
-            x[e] = ex2(fmaf(x[e], a.scale_log2, e < 2 ? off0 : off1));
-            l[e >> 1] += x[e];
-          }
+          for (int j = 0; j < 2; ++j) {
+            float* x = s[2 * (i0 + i) + j];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (r == 1 && !WIDE) {
-              p[2 * j + 1] = pl[2 * j + 1] = 0;
-            } else if (E4M3) {
-              p[2 * j + r] = pack_f16(x[2 * r], x[2 * r + 1]);
-            } else {
-              const uint32_t hb = pack_bf16(x[2 * r], x[2 * r + 1]);
-              p[2 * j + r] = hb;
-              pl[2 * j + r] = pack_bf16(x[2 * r] - __uint_as_float(hb << 16),
-                                        x[2 * r + 1] - __uint_as_float(hb & 0xFFFF0000u));
+            for (int e = 0; e < (WIDE ? 4 : 2); ++e) {
+              x[e] = ex2(fmaf(x[e], a.scale_log2, e < 2 ? off0 : off1));
+              l[e >> 1] += x[e];
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if (r == 1 && !WIDE) {
+                p[i][2 * j + 1] = pl[i][2 * j + 1] = 0;
+              } else if (E4M3) {
+                uint32_t hw = pack_f16(x[2 * r], x[2 * r + 1]);
+                const float2 hf = __half22float2(*reinterpret_cast<__half2*>(&hw));
+                p[i][2 * j + r] = hw;
+                pl[i][2 * j + r] = pack_f16(x[2 * r] - hf.x, x[2 * r + 1] - hf.y);
+              } else {
+                const uint32_t hb = pack_bf16(x[2 * r], x[2 * r + 1]);
+                p[i][2 * j + r] = hb;
+                pl[i][2 * j + r] = pack_bf16(x[2 * r] - __uint_as_float(hb << 16),
+                                             x[2 * r + 1] - __uint_as_float(hb & 0xFFFF0000u));
+              }
             }
           }
         }
-        const int r = 16 * i + (lane & 15);
 #pragma unroll
         for (int c = 0; c < CPR; c += 2) {
-          uint32_t f[4];
-          ldm4t(vs + swz<RB>(r, c + (lane >> 4)), f);
-          if (E4M3) {
-            // bytes (key 2t, values 2g and 2g + 1), (key 2t + 1, the same): even
-            // and odd values become two 8-column tiles
+          // E4M3: the slabs' sums by themselves, added to the running ones afterwards: the tensor
+          // cores cut their sums off, and 700 products behind one another came out 2^-16 too small
+          float sums[4][4] = {};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t a0, a1, b0, b1;
-              e4m3x4_to_f16x4(f[2 * u], a0, a1);
-              e4m3x4_to_f16x4(f[2 * u + 1], b0, b1);
-              mma<true>(o[2 * (c + u)], p, __byte_perm(a0, a1, 0x5410), __byte_perm(b0, b1, 0x5410));
-              mma<true>(o[2 * (c + u) + 1], p, __byte_perm(a0, a1, 0x7632),
-                        __byte_perm(b0, b1, 0x7632));
+          for (int i = 0; i < GS; ++i) {
+            uint32_t f[4];
+            ldm4t(vs + swz<RB>(16 * (i0 + i) + (lane & 15), c + (lane >> 4)), f);
+            if (E4M3) {
+              // bytes (key 2t, values 2g and 2g + 1), (key 2t + 1, the same): even
+              // and odd values become two 8-column tiles
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                uint32_t a0, a1, b0, b1;
+                e4m3x4_to_f16x4(f[2 * u], a0, a1);
+                e4m3x4_to_f16x4(f[2 * u + 1], b0, b1);
+                const uint32_t even0 = __byte_perm(a0, a1, 0x5410), even1 = __byte_perm(b0, b1, 0x5410);
+                const uint32_t odd0 = __byte_perm(a0, a1, 0x7632), odd1 = __byte_perm(b0, b1, 0x7632);
+                mma<true>(sums[2 * u], p[i], even0, even1);
+                mma<true>(sums[2 * u + 1], p[i], odd0, odd1);
+                mma<true>(sums[2 * u], pl[i], even0, even1);
+                mma<true>(sums[2 * u + 1], pl[i], odd0, odd1);
+              }
+            } else {
+              mma<false>(o[c], p[i], f[0], f[1]);
+              mma<false>(o[c + 1], p[i], f[2], f[3]);
+              mma<false>(o[c], pl[i], f[0], f[1]);
+              mma<false>(o[c + 1], pl[i], f[2], f[3]);
             }
-          } else {
-            mma<false>(o[c], p, f[0], f[1]);
-            mma<false>(o[c + 1], p, f[2], f[3]);
-            mma<false>(o[c], pl, f[0], f[1]);
-            mma<false>(o[c + 1], pl, f[2], f[3]);
+          }
+          if (E4M3) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int e = 0; e < (WIDE ? 4 : 2); ++e) o[2 * c + u][e] += sums[u][e];
           }
         }
       }
