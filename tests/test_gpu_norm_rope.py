@@ -269,3 +269,43 @@ def test_weight_gradients_repeat_bit_for_bit_also_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, dw))
+
+
+@pytest.mark.parametrize("case", [
+    # heads that do not fill a warp's 4, 8 or 16, two and four rows per thread
+    (1, 9, 5, 3, 128, 128, True, 0, False, False, True), (2, 17, 9, 1, 64, 16, False, 0, True, False, True),
+    (1, 50, 40, 10, 128, 64, False, 1, True, True, True), (1, 2500, 9, 10, 128, 0, False, 1, False, True, True),
+    # several tokens per warp, with rows left over
+    (2, 5003, 2, 1, 64, 64, False, 0, True, True, True), (1, 9999, 1, 12, 128, 128, True, 0, True, True, True),
+    (3, 3301, 1, 0, 128, 128, False, 1, False, True, False), (1, 10007, 3, 4, 64, 48, True, 0, False, False, True)],
+    ids=lambda c: "-".join(str(int(x)) for x in c))
+def test_gradients_without_eps(case):
+    """eps = 0 and no row of zeros: rows that do not exist and padding add nothing to the weights'
+    gradients.  Tolerances as above."""
+    c = Case(*case, eps=0.0)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for t in (c.q, c.k):
+        t[:, -1] = torch.randn(t[:, -1].shape, generator=g, device="cuda").to(BF)
+    skip = torch.zeros(c.B, c.N, dtype=torch.bool, device="cuda")
+    if c.pos is not None:
+        skip = torch.rand(c.B, c.N, device="cuda", generator=g) < 0.2
+        c.pos[skip] = -1
+    live = ~skip.cpu().numpy()
+    outs, (dx, dw) = c.forward(), c.backward()
+    for i in range(2):
+        if c.H[i] == 0:
+            continue
+        x, w, cos, sin, pos, *rest = c.oracle(i)
+        pos = np.maximum(pos, 0)
+        want = po.norm_rope(x, w, cos, sin, pos, *rest)
+        tol = 2.0 ** -8 * np.abs(want) + (c.D / 2 + 10) * U * _mix(want, c.rot, c.inter) * 2 ** 0.5
+        got = c.token_major(outs[i])
+        assert (np.abs(got - want) <= tol)[live].all() and (got[~live] == 9).all()
+        dy = c.token_major(c.dy[i]) * live[..., None, None]
+        want, want_w, _ = po.norm_rope_backward(dy, x, w, cos, sin, pos, *rest)
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True))
+        g_, xh = _mix(dy, c.rot, c.inter), np.abs(x * r)
+        tol = 2.0 ** -8 * np.abs(want) + (c.D + 20) * U * r * (g_ * np.abs(w) + xh * (g_ * np.abs(w) * xh).mean(-1, keepdims=True))
+        got = _f64(dx[i])
+        assert (np.abs(got - want) <= tol)[live].all() and (got[~live] == 9).all()
+        assert (np.abs(_f64(dw[i]) - want_w) <= (c.D / 2 + 410) * U * (g_ * xh).sum((0, 1, 2))).all()

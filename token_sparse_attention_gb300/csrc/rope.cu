@@ -125,11 +125,11 @@ __device__ __forceinline__ float f2_sum(uint64_t a) {
   return x + y;
 }
 
-// Cosines and sines of the thread's pairs (1 and 0 where nothing is rotated).
+// Cosines and sines of the thread's pairs (1 and 0 where nothing is rotated, and for a row that is none).
 __device__ __forceinline__ void load_angles(const RopeArgs& a, int pos, int l, uint64_t* cs,
                                             uint64_t* sn) {
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (8 * l < a.rot) {
+  if (8 * l < a.rot && pos >= 0) {
     const size_t at = static_cast<size_t>(pos) * (a.rot / 2) + 4 * l;
     c = *reinterpret_cast<const float4*>(a.cos_table + at);
     s = *reinterpret_cast<const float4*>(a.sin_table + at);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kRopeThreads, Tune<D>::BLOCKS)
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
     uint64_t cs[2], sn[2], u[2], v[2];
-    load_angles(a, max(p[i].pos, 0), l, cs, sn);
+    load_angles(a, p[i].pos, l, cs, sn);
     normed<D, SPLIT>(x[i], a.eps, u, v);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -382,8 +382,10 @@ __device__ __forceinline__ void angles_in(const uint8_t* cos4, const uint8_t* si
   sn[0] = f2_pack(s.x, s.y), sn[1] = f2_pack(s.z, s.w);
 }
 // dx of a row (its pairs' members to c and d), and its part of the weight gradients added to da, db.
+// A row that is not `live` (no such row, or padding) holds zeros, whose 1 / rms is infinite at
+// eps = 0, and adds nothing.
 template <int D, bool SPLIT>
-__device__ __forceinline__ void row_gradient(const Row& x, const Row& y, float eps, const uint64_t* cs, const uint64_t* sn,
+__device__ __forceinline__ void row_gradient(const Row& x, const Row& y, bool live, float eps, const uint64_t* cs, const uint64_t* sn,
                                              const uint64_t* wa, const uint64_t* wb, uint64_t* c, uint64_t* d, uint64_t* da,
                                              uint64_t* db) {
   uint64_t p[2], q[2], g[2], f[2], ss = 0, dot = 0;
@@ -401,7 +403,7 @@ __device__ __forceinline__ void row_gradient(const Row& x, const Row& y, float e
   float s1 = f2_sum(ss), s2 = f2_sum(dot);
   s1 = row_sum<D / 8>(s1);
   s2 = row_sum<D / 8>(s2);
-  const float r = rsqrtf(s1 * (1.f / D) + eps), m = -(s2 * (1.f / D)) * r * r;
+  const float r = live ? rsqrtf(s1 * (1.f / D) + eps) : 0.f, m = -(s2 * (1.f / D)) * r * r;
   const uint64_t rr = f2_pack(r, r), mm = f2_pack(m, m);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -466,9 +468,9 @@ __global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
       const size_t y0 = out_base(a, u.t, H, &step) + 8 * l;
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        // (heads past the last one become zeros)
+        // (heads past the last one: its x, so that 1 / rms is a number whatever eps is, and zeros as dy)
         const int h = h0 + i * ROWS, hc = min(h, H - 1);
-        copy16(stage + i * 512 + lane * 16, xs + u.token * stride + hc * D + 8 * l, h < H);
+        copy16(stage + i * 512 + lane * 16, xs + u.token * stride + hc * D + 8 * l, true);
         copy16(stage + (STEPS + i) * 512 + lane * 16, dys + y0 + hc * step, h < H);
       }
       if (r0 < 2 && 8 * l < a.rot) {
@@ -498,7 +500,8 @@ __global__ void __launch_bounds__(kRopeThreads, grad_blocks(STEPS))
       for (int i = 0; i < STEPS; ++i) {
         uint64_t c[2], d[2];
         row_gradient<D, SPLIT>(row_in<SPLIT>(stage + i * 512 + r0 * 2 * D, at),
-                               row_in<SPLIT>(stage + (STEPS + i) * 512 + r0 * 2 * D, at), a.eps, cs, sn, wa, wb, c, d, da, db);
+                               row_in<SPLIT>(stage + (STEPS + i) * 512 + r0 * 2 * D, at), true, a.eps, cs, sn, wa, wb, c, d,
+                               da, db);
         if (h0 + i * ROWS < H) store_row<SPLIT>(dx + i * ROWS * D, at, c, d);
       }
     }
@@ -539,8 +542,8 @@ __global__ void __launch_bounds__(kRopeThreads, Tune<D>::FEW_BLOCKS)
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
       uint64_t cs[2], sn[2], c[2], d[2];
-      load_angles(a, max(pl[i].pos, 0), l, cs, sn);
-      row_gradient<D, SPLIT>(x[i], y[i], a.eps, cs, sn, wa, wb, c, d, da, db);
+      load_angles(a, pl[i].pos, l, cs, sn);
+      row_gradient<D, SPLIT>(x[i], y[i], pl[i].pos >= 0, a.eps, cs, sn, wa, wb, c, d, da, db);
       if (pl[i].pos >= 0) store_row<SPLIT>(one.out + pl[i].x, at, c, d);
     }
   }
