@@ -15,6 +15,10 @@ Tolerances, taken before the first run (u = 2^-24, half a step of fp32):
 * codes, copied rows, slots, tables and selections: equal.
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -885,3 +889,30 @@ def test_e4m3_weights_keep_their_low_bits(n, Hq, Hkv, D, page, off):
     assert (tol < np.abs(want)).all()  # (that it would show)
     assert (np.abs(_f64(out[:1]) - want) <= tol).all(), (_f64(out[0, 0, 0]), want[0, 0, 0])
     c.check(out, ls)
+
+
+def _plan_of_many(B):
+    """A step of B sequences against the oracle."""
+    r = np.random.default_rng(B)
+    lens, new, page = r.integers(0, 40, B), r.integers(0, 3, B), 16
+    need = int((-(-(lens + new) // page)).sum())
+    order, table, at = r.permutation(need + 3), np.full((B, 3), -1), 0
+    for b in range(B):
+        n = -(-lens[b] // page)
+        table[b, :n] = order[at:at + n]
+        at += n
+    p, T = mcs.paged(B, 1, 1, 64, page, need + 3, 3), int(new.sum()) + 1
+    want = po.plan(new, lens, order[at:], 0, table, page, T, need + 3)
+    for x, y in zip(_plan(p, new, lens, order[at:], 0, table, T), want):
+        np.testing.assert_array_equal(x, y)
+    assert mcs.mcs_device_status() == 0
+
+
+def test_plan_of_every_count_that_is_documented():
+    """Counts around the shared memory that a launch has without asking, in a process of its own: asking
+    for one count holds for the process."""
+    code = ("import sys; sys.path.insert(0, sys.argv[1]); from tests import test_gpu_paged as t; "
+            "[t._plan_of_many(b) for b in (4051, 4052, 4060, 4095, 4096, 1)]")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

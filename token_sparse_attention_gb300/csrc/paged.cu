@@ -28,6 +28,7 @@ namespace {
 // their instruction issue), 6.2 us in two launches; 256 single tokens 3.9 us.
 
 constexpr int kPlanMaxThreads = 1024;
+constexpr int kPlanSums = 33;
 constexpr int kPlanAtOnce = 4;      // tokens a thread searches side by side
 constexpr int kPlanTokens = 8192;   // as many tokens the first launch places itself
 
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kPlanMaxThreads) paged_plan_kernel(const PlanA
   int32_t* s_cu = sm;                 // [B + 1] exclusive sums of new tokens
   int32_t* s_base = s_cu + a.B + 1;   // [B + 1] exclusive sums of missing pages
   int32_t* s_len = s_base + a.B + 1;  // [B]
-  __shared__ long long sums[33][2];   // of the warps in front of each; in 32 the block's
+  __shared__ long long sums[kPlanSums][2];  // of the warps in front of each; in the last the block's
   pdl_begin();
   const int tid = threadIdx.x, lane = lane_id(), w = warp_id(), threads = blockDim.x;
   const int shift = 31 - __clz(a.page), mask = a.page - 1;
@@ -960,7 +961,8 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   const bool place = a.T <= kPlanTokens;
   const int items = std::max(a.B, place ? a.T : 0);
   const int threads = items > 512 || !place ? kPlanMaxThreads : items > 256 ? 512 : 256;
-  if (smem > 48 * 1024) {
+  // (48 KB without asking, the kernel's own sums among them: from 4052 sequences on)
+  if (smem + kPlanSums * 2 * sizeof(long long) > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
