@@ -443,7 +443,8 @@ typedef struct {
   int num_pages;      /* pages of the cache */
   int max_pages;      /* entries per row of block_table */
   int kv;             /* MCS_KV_BF16 (0) or MCS_KV_E4M3 (1) */
-  float scale;        /* softmax scale; 0 selects 1/sqrt(D).  scale * k_scale (E4M3) * log2(e) is finite */
+  float scale;        /* softmax scale; 0 selects 1/sqrt(D).  scale * k_scale (E4M3) * log2(e) is finite;
+                         where it is too small for a float all weights are equal */
   float k_scale, v_scale; /* E4M3: scales of the two caches, > 0; ignored for bf16 */
   int q_stride;       /* elements between the rows of consecutive tokens of q; 0: Hq * D */
   int kv_stride;      /* the same of k and v given to mcs_paged_write; 0: Hkv * D */

@@ -916,3 +916,16 @@ def test_plan_of_every_count_that_is_documented():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code, root], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("e4m3,scale,k_scale", [(True, 1e-30, 1e-20), (True, 1e-45, 1e-45), (True, 0.0, 1e-45),
+                                                (False, 1e-45, 1.0), (False, 1e-30, 1.0)])
+def test_decode_of_scales_that_vanish_is_the_mean(e4m3, scale, k_scale):
+    """Scales whose product is too small for a float, each of them accepted: all weights are equal."""
+    c = Cache([700, 33, 0, 1, 16], 8, 2, 64, 16, e4m3, seed=2, scale=scale)
+    if e4m3:
+        c.p.k_scale = k_scale
+        c.scales = (k_scale, VS)
+    c.check(*c.run())
+    sel = _sel(c, 3, 3)
+    c.check(*c.run(_i32(sel)), sel)

@@ -19,10 +19,12 @@ bool good_stride(int s, long long row) { return s == 0 || (s >= row && s % 8 == 
 constexpr long long kIntMax = 0x7fffffffLL;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// What a product of stored q and k is multiplied by, for powers of two.
+// What a product of stored q and k is multiplied by, for powers of two.  Scales whose product
+// vanishes stay above zero: the kernels multiply the -inf of masked scores by it, and with the
+// smallest float any weight is within 2^-21 of 1.
 float scale_log2_of(const mcs_paged* p) {
   const float scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf(static_cast<float>(p->D));
-  return scale * (p->kv == MCS_KV_E4M3 ? p->k_scale : 1.f) * kLog2e;
+  return fmaxf(scale * (p->kv == MCS_KV_E4M3 ? p->k_scale : 1.f) * kLog2e, 0x1p-149f);
 }
 
 mcs_status check_paged(const mcs_paged* p) {
