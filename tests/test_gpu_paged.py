@@ -929,3 +929,18 @@ def test_decode_of_scales_that_vanish_is_the_mean(e4m3, scale, k_scale):
     c.check(*c.run())
     sel = _sel(c, 3, 3)
     c.check(*c.run(_i32(sel)), sel)
+
+
+@pytest.mark.parametrize("v_scale", [2.0 ** -122, 1.7 * 2.0 ** -126, 2.0 ** 100])
+@pytest.mark.parametrize("lens", [[3000], [30, 2900, 0, 17]])
+def test_value_scales_of_any_size(v_scale, lens):
+    """The quotient of a small value scale and a sum of weights is far below the smallest normal
+    float; the outputs are not.  (Half of bf16's smallest step is 2^-134.)"""
+    c = Cache(lens, 4, 2, 128, 16, True, seed=7)
+    c.p.v_scale = v_scale
+    c.scales = (KS, v_scale)
+    out, _ = c.run()
+    want, _, absv, size = po.decode(_f64(c.q), _f64(c.k) * KS, _f64(c.v) * v_scale, c.table, lens, c.scale)
+    tol = 2.0 ** -134 + 2.0 ** -8 * np.abs(want) + absv * (
+        2 * (2 * (128 + 8) * U * size + 2.0 ** -21) + 2.0 ** -21 + max(lens) * U)[..., None]
+    assert (np.abs(_f64(out[:len(lens)]) - want) <= tol).all()

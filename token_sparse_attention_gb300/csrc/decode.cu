@@ -584,13 +584,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int head = g + 8 * r;
       if (head >= heads) continue;
       if (here.t0 == 0) {
-        const float inv = l[r] > 0.f || l[r] != l[r] ? a.v_scale / l[r] : 0.f;
+        // (the value scale by itself: its quotient by l may be too small for a normal float)
+        const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
         const size_t at = static_cast<size_t>(here.b) * a.Hq + h * group + q0 + head;
         __nv_bfloat16* to = a.out + at * D;
 #pragma unroll
         for (int c = 0; c < NT; c += 2) {
-          const float x0 = o[c][2 * r] * inv, x1 = o[c][2 * r + 1] * inv;
-          const float y0 = o[c + 1][2 * r] * inv, y1 = o[c + 1][2 * r + 1] * inv;
+          float x0 = o[c][2 * r] * inv, x1 = o[c][2 * r + 1] * inv;
+          float y0 = o[c + 1][2 * r] * inv, y1 = o[c + 1][2 * r + 1] * inv;
+          if (E4M3) x0 *= a.v_scale, x1 *= a.v_scale, y0 *= a.v_scale, y1 *= a.v_scale;
           if (E4M3) {
             *reinterpret_cast<uint2*>(to + 8 * c + 4 * t) = make_uint2(pack_bf16(x0, y0), pack_bf16(x1, y1));
           } else {
@@ -853,9 +855,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kJoinFew ? 2 : WIDE && D =
 #pragma unroll
         for (int i = 1; i < SIDES; ++i) add(s_acc[i][e0], make_float2(1.f, s_sums[i][e0]), k);
       }
-      const float total = sum[k], inv = total > 0.f || total != total ? a.v_scale / total : 0.f;
-      *reinterpret_cast<uint2*>(a.out + (out_row + row) * D + col) =
-          make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
+      const float total = sum[k], inv = total > 0.f || total != total ? 1.f / total : 0.f;
+      float4 y = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+      if (E4M3) y.x *= a.v_scale, y.y *= a.v_scale, y.z *= a.v_scale, y.w *= a.v_scale;
+      *reinterpret_cast<uint2*>(a.out + (out_row + row) * D + col) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
       if (a.lse != nullptr && col == 0)
         a.lse[out_row + row] =
             total == 0.f ? -INFINITY : (s_top[row] + (log2f(total) - kShift)) * 0.6931471805599453f;
