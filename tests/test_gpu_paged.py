@@ -944,3 +944,15 @@ def test_value_scales_of_any_size(v_scale, lens):
     tol = 2.0 ** -134 + 2.0 ** -8 * np.abs(want) + absv * (
         2 * (2 * (128 + 8) * U * size + 2.0 ** -21) + 2.0 ** -21 + max(lens) * U)[..., None]
     assert (np.abs(_f64(out[:len(lens)]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("select", [2 ** 31 - 1, 2 ** 31 - 1000])
+def test_select_rows_as_long_as_a_call_takes(select):
+    """Far more places than pages: the rest of the row is -1 up to its end, and nothing else is written."""
+    c = Cache([100], 2, 1, 64, 16, seed=1)
+    row = torch.full((select + 1024,), 7, dtype=torch.int32, device="cuda")
+    ws = mcs.empty_workspace(mcs.mcs_paged_select_workspace(c.p))
+    mcs.mcs_paged_select(c.p, c.q, c.means(), c.dtable, c.dlens, row[:select].view(1, 1, select), ws)
+    assert row[:7].tolist() == list(range(7)) and (row[select:] == 7).all()
+    assert int(row[7:select].max()) == -1 and int(row[7:select].min()) == -1
+    c.check(*c.run(row[:select].view(1, 1, select)))

@@ -799,7 +799,8 @@ __global__ void __launch_bounds__(1024) paged_topk_kernel(const __grid_constant_
   const int n = bad || len == 0 ? 0 : (len - 1) / a.page + 1;
   const int keep = min(n, a.select);
   int32_t* sel = a.sel + static_cast<size_t>(bh) * a.select;
-  for (int i = keep + tid; i < a.select; i += threads) sel[i] = -1;
+  // (unsigned: i passes the largest int where select is near it)
+  for (unsigned i = keep + tid; i < static_cast<unsigned>(a.select); i += threads) sel[i] = -1;
   if (n <= keep) {
     for (int i = tid; i < n; i += threads) sel[i] = i;
     return;
