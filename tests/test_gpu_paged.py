@@ -956,3 +956,37 @@ def test_select_rows_as_long_as_a_call_takes(select):
     assert row[:7].tolist() == list(range(7)) and (row[select:] == 7).all()
     assert int(row[7:select].max()) == -1 and int(row[7:select].min()) == -1
     c.check(*c.run(row[:select].view(1, 1, select)))
+
+
+@pytest.mark.parametrize("e4m3,means", [(False, True), (True, True), (False, False)])
+@pytest.mark.parametrize("over", [-1, 0, 1])
+def test_write_at_the_change_of_window(over, e4m3, means):
+    """Tokens around the count from which windows are four times as wide: eight blocks for every SM
+    that this device has.  The caches get the same rows either way, as the older tests check."""
+    Hkv, D, page = 16, 128, 64
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T = 8 * sms * 4 * (256 // (D // 8)) // Hkv + over
+    num = -(-T // page) + 1
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn(T, Hkv, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    order = torch.randperm(num, generator=g, device="cuda")
+    t = torch.arange(T, device="cuda")
+    slots = (order[t // page] * page + t % page).to(torch.int32)
+    p = mcs.paged(1, Hkv, Hkv, D, page, num, num, kv=int(e4m3), k_scale=KS, v_scale=VS)
+    caches = torch.zeros(2, num, Hkv, page, D, dtype=torch.uint8 if e4m3 else torch.bfloat16, device="cuda")
+    mean = torch.zeros(num, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    mcs.mcs_paged_write(p, k, v, slots, caches[0], caches[1], mean if means else None)
+    values = None
+    for x, scale, cache in ((k, KS, caches[0]), (v, VS, caches[1])):
+        if e4m3:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+            mcs.mcs_quantize_e4m3(x, scale, codes)
+            x = codes
+        assert torch.equal(cache.transpose(1, 2).reshape(-1, Hkv, D)[slots.long()], x)
+        values = x if values is None else values
+    if means:
+        values = values.view(torch.float8_e4m3fn).double() * KS if e4m3 else values.double()
+        for j in (0, 1, num - 2):
+            rows = values[j * page:(j + 1) * page]
+            tol = 2.0 ** -8 * rows.mean(0).abs() + (page + 2) * U * rows.abs().mean(0)
+            assert ((mean[order[j]].double() - rows.mean(0)).abs() <= tol).all()

@@ -902,10 +902,9 @@ size_t paged_decode_workspace_bytes(int D, int group) {
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int group = a.Hq / a.Hkv, chunks = (group + kHeads - 1) / kHeads;
   const bool wide = group > 8;
   if (a.D == 128) {

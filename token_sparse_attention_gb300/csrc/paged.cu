@@ -974,10 +974,10 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
 }
 
 template <int D, bool E4M3>
-static cudaError_t write_launch(const WriteArgs& a, cudaStream_t stream) {
+static cudaError_t write_launch(const WriteArgs& a, int sms, cudaStream_t stream) {
   constexpr int GROUPS = kWriteThreads / (D / 8);
-  // four rows per thread once that leaves every SM (152) eight blocks
-  const bool many = static_cast<long long>(a.T) * a.Hkv >= 152LL * 8 * 4 * GROUPS;
+  // four rows per thread once that leaves every SM eight blocks
+  const bool many = static_cast<long long>(a.T) * a.Hkv >= 8LL * sms * 4 * GROUPS;
   const int window = GROUPS * (many ? 4 : 1);
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.T) + window - 1) / window * a.Hkv);
   auto kernel = a.k_mean ? (many ? paged_write_kernel<D, E4M3, 4 * GROUPS> : paged_write_kernel<D, E4M3, GROUPS>)
@@ -1000,8 +1000,11 @@ cudaError_t launch_paged_write(const WriteArgs& a, bool e4m3, cudaStream_t strea
   };
   c.k_most = most(a.k_scale);
   c.v_most = most(a.v_scale);
-  if (a.D == 128) return e4m3 ? write_launch<128, true>(c, stream) : write_launch<128, false>(c, stream);
-  return e4m3 ? write_launch<64, true>(c, stream) : write_launch<64, false>(c, stream);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (a.D == 128) return e4m3 ? write_launch<128, true>(c, sms, stream) : write_launch<128, false>(c, sms, stream);
+  return e4m3 ? write_launch<64, true>(c, sms, stream) : write_launch<64, false>(c, sms, stream);
 }
 
 // Keys of a row: whole 16-byte words for every thread's eight.
@@ -1014,18 +1017,21 @@ size_t paged_select_workspace_bytes(int B, int Hkv, int max_pages) {
 cudaError_t launch_paged_select(const SelectArgs& a, cudaStream_t stream) {
   const int rows = 256 / a.D, head_blocks = (a.Hkv + rows - 1) / rows;
   const int stride = key_stride(a.max_pages);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
   // 32 pages per warp; fewer where that would leave SMs idle
   int per_warp = 32;
   while (per_warp > 8 && static_cast<long long>(a.B) * head_blocks *
-                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 152 * 2)
+                                 ((a.max_pages + 8 * per_warp - 1) / (8 * per_warp)) < 2 * sms)
     per_warp /= 2;
   // and no more blocks than a few rounds of all SMs: a table is often far longer than its sequences
   const long long pairs = static_cast<long long>(a.B) * head_blocks;
   const int page_blocks = static_cast<int>(
-      std::min<long long>((a.max_pages + 8 * per_warp - 1) / (8 * per_warp), std::max<long long>(1, 152 * 16 / pairs)));
+      std::min<long long>((a.max_pages + 8 * per_warp - 1) / (8 * per_warp), std::max<long long>(1, 16 * sms / pairs)));
   const unsigned blocks = static_cast<unsigned>(static_cast<long long>(a.B) * head_blocks * page_blocks);
-  cudaError_t e = launch_dependent(a.D == 128 ? paged_score_kernel<128> : paged_score_kernel<64>, blocks,
-                                   kScoreThreads, 0, stream, a, head_blocks, page_blocks, per_warp, stride);
+  e = launch_dependent(a.D == 128 ? paged_score_kernel<128> : paged_score_kernel<64>, blocks, kScoreThreads, 0, stream, a,
+                       head_blocks, page_blocks, per_warp, stride);
   if (e != cudaSuccess) return e;
   // as many threads as the longest list keeps busy; of the counters, four per thread
   const int threads = std::min((stride / kTopkKeys + 127) / 128 * 128, 1024), bins = std::min(4 * threads, 2048);

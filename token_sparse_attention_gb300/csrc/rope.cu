@@ -689,18 +689,16 @@ size_t norm_rope_backward_workspace_bytes(int D) {
 }
 
 cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   return a.D == 128 ? forward<128>(a, sms, stream) : forward<64>(a, sms, stream);
 }
 
 cudaError_t launch_norm_rope_backward(const RopeArgs& a, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   return a.D == 128 ? backward<128>(a, sms, stream) : backward<64>(a, sms, stream);
 }
 
