@@ -675,7 +675,10 @@ cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
   if (rest_q + rest_k > 0) {
     RopeArgs c = a;
     c.ws = a.ws + static_cast<size_t>(few_q ? bq : 0) * D;  // k's rows follow q's
-    e = steps == 4 ? backward_rows<D, 4>(c, rest_q, rest_k, stream) : backward_rows<D, 2>(c, rest_q, rest_k, stream);
+    if constexpr (D == 128)
+      e = steps == 4 ? backward_rows<D, 4>(c, rest_q, rest_k, stream) : backward_rows<D, 2>(c, rest_q, rest_k, stream);
+    else
+      e = backward_rows<D, 2>(c, rest_q, rest_k, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.dwq == nullptr && a.dwk == nullptr) return e;
