@@ -309,3 +309,24 @@ def test_gradients_without_eps(case):
         got = _f64(dx[i])
         assert (np.abs(got - want) <= tol)[live].all() and (got[~live] == 9).all()
         assert (np.abs(_f64(dw[i]) - want_w) <= (c.D / 2 + 410) * U * (g_ * xh).sum((0, 1, 2))).all()
+
+
+@pytest.mark.parametrize("case", [(1, 4999, 8, 16, 128, 96, False, 0, True, False, True),
+                                  (2, 301, 40, 8, 128, 128, True, 1, False, False, True),
+                                  (1, 700, 16, 32, 64, 64, False, 1, False, False, True)],
+                         ids=lambda c: "-".join(str(int(x)) for x in c))
+def test_gradients_with_and_without_positions(case):
+    """Positions given as each token's place are the positions without any, whichever form takes them:
+    dx is the same bits, dw the same sum in another order."""
+    c = Case(*case)
+    dx, dw = c.backward()
+    c.pos = torch.arange(c.N, device="cuda", dtype=torch.int32).expand(c.B, c.N).contiguous()
+    dx2, dw2 = c.backward()
+    assert all(torch.equal(a, b) for a, b in zip(dx, dx2))
+    for i in range(2):
+        x, w, *rest = c.oracle(i)
+        dy = c.token_major(c.dy[i])
+        want, want_w, _ = po.norm_rope_backward(dy, x, w, *rest)
+        size = (_mix(dy, c.rot, c.inter) * np.abs(x) / np.sqrt((x * x).mean(-1, keepdims=True) + c.eps)).sum((0, 1, 2))
+        for got in (dw[i], dw2[i]):
+            assert (np.abs(_f64(got) - want_w) <= (c.D / 2 + 410) * U * size).all()

@@ -30,9 +30,12 @@ constexpr int kRopeThreads = 32 * kRopeWarps;
 // Loads in flight per thread and blocks per SM, measured: forward 4 at D = 128 and 8 at
 // D = 64, whose rows are half as long (75600 tokens, 64 heads of D = 64: 84 -> 90 % of
 // copy bandwidth).  The gradients have two forms, 2 rows of x and dy per thread and 3 blocks, or
-// 4 and 2, which has less to find out per row, but takes twice the heads at a time: 32760 tokens,
-// 12 + 12 heads of D = 128: 97 us and 103; 40000 tokens, 40 + 8 heads: 244 and 214; 75600 tokens,
-// 32 + 32 heads of D = 64: 300 and 325 (D = 128, 2 rows and 4 blocks: spills, 40 + 8 heads 410).
+// 4 and 2, which takes twice the heads at a time.  At D = 128 and with heads that fill the warps, 4
+// rows are faster where the tokens' positions are given and slower where they are not (why, is not
+// known): 40000 tokens, 40 + 8 heads, 217 us and 236 with 2 rows, without positions 261 and 234;
+// 75600 tokens, 40 + 40 heads 697 and 768, without positions 804 and 732; below 3000 tokens they are
+// within 3 %.  Heads that do not fill them: 32760 tokens, 12 + 12 heads 103 us and 97.  D = 64: 75600
+// tokens, 32 + 32 heads 325 and 300.  (D = 128, 2 rows and 4 blocks: spills, 40 + 8 heads 410.)
 template <int D> struct Tune {
   static constexpr int STEPS = 512 / D, BLOCKS = D == 128 ? 4 : 3, FEW_BLOCKS = BLOCKS;
 };
@@ -642,10 +645,11 @@ cudaError_t backward(const RopeArgs& a, int sms, cudaStream_t stream) {
   constexpr int few = heads_per_warp(D, kFewSteps);
   const long long tokens = static_cast<long long>(a.B) * a.N, tiles = (tokens + kRopeWarps - 1) / kRopeWarps;
   const bool few_q = few_heads(a.Hq, few, tokens, sms), few_k = few_heads(a.Hkv, few, tokens, sms);
-  // four rows per thread at D = 128 where that leaves few lanes without a head
+  // four rows per thread at D = 128 for given positions where that leaves few lanes without a head
   const int hq = few_q ? 0 : a.Hq, hk = few_k ? 0 : a.Hkv;
   auto chunks = [](int H, int steps) { return (H + heads_per_warp(D, steps) - 1) / heads_per_warp(D, steps); };
-  const int steps = 20LL * (chunks(hq, 4) + chunks(hk, 4)) * heads_per_warp(D, 4) <= 23LL * (hq + hk) && D == 128 ? 4 : 2;
+  const bool fill = 20LL * (chunks(hq, 4) + chunks(hk, 4)) * heads_per_warp(D, 4) <= 23LL * (hq + hk);
+  const int steps = D == 128 && a.positions != nullptr && fill ? 4 : 2;
   const int cq = chunks(hq, steps), ck = chunks(hk, steps);
   // the blocks that are resident at a time, shared between q and k by their work where
   // they run together
