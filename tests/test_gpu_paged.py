@@ -990,3 +990,64 @@ def test_write_at_the_change_of_window(over, e4m3, means):
             rows = values[j * page:(j + 1) * page]
             tol = 2.0 ** -8 * rows.mean(0).abs() + (page + 2) * U * rows.abs().mean(0)
             assert ((mean[order[j]].double() - rows.mean(0)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_steps_one_behind_another_see_their_own_rows(e4m3):
+    """Keys normalised in place, written, averaged, scored and attended to, many steps with nothing
+    between the launches (each kernel is set up while the one in front still writes what it reads),
+    against the same steps one at a time."""
+    B, Hq, Hkv, D, page, P, steps, most = 6, 16, 8, 128, 16, 40, 14, 45
+    num = B * P
+    r = np.random.default_rng(5)
+    p = mcs.paged(B, Hq, Hkv, D, page, num, P, kv=int(e4m3), k_scale=KS, v_scale=VS)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    new = r.integers(0, most, (steps, B))
+    new[:, 0] = 1
+    T = int(new.sum(1).max()) + 2
+    ks, vs, qs = rand(steps, T, 1, Hkv, D), rand(steps, T, Hkv, D), rand(steps, B, Hq, D)
+    angle = torch.rand(steps * most, D // 2, generator=g, device="cuda") * 6
+    cos, sin = angle.cos(), angle.sin()
+    rp = mcs.rope_params(T, 1, Hkv, 0, D, D, steps * most, layout=mcs.LAYOUT_BNHD)
+    new, free = _i32(new), _i32(r.permutation(num))
+    ws = mcs.empty_workspace(max(mcs.mcs_paged_decode_workspace(p), mcs.mcs_paged_select_workspace(p)))
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    caches = torch.zeros(2, num, Hkv, page, D, dtype=dt, device="cuda")
+    mean = torch.zeros(num, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    lens, head, table, cu = _i32([0] * B), _i32([0]), _i32(np.zeros((B, P))), _i32([0] * (B + 1))
+    slots, pos, k = _i32([0] * T), _i32([0] * T), torch.empty_like(ks[0])
+    sels = torch.zeros(steps, B, Hkv, 4, dtype=torch.int32, device="cuda")
+    outs = torch.zeros(steps, B, Hq, D, dtype=torch.bfloat16, device="cuda")
+
+    def go(between):
+        for x in (caches, mean, lens, head, table):
+            x.zero_()
+        for i in range(steps):
+            k.copy_(ks[i])
+            calls = [lambda: mcs.mcs_paged_plan(p, new[i], lens, free, head, table, lens, head, cu, slots, pos),
+                     lambda: mcs.mcs_qk_norm_rope(rp, k, None, None, None, cos, sin, pos.view(T, 1), k, None),
+                     lambda: mcs.mcs_paged_write(p, k.view(T, Hkv, D), vs[i], slots, caches[0], caches[1], mean),
+                     lambda: mcs.mcs_paged_select(p, qs[i], mean, table, lens, sels[i], ws),
+                     lambda: mcs.mcs_paged_decode_sparse(p, qs[i], caches[0], caches[1], table, lens, sels[i], outs[i], ws)]
+            for call in calls:
+                call()
+                between()
+
+    state = (caches, mean, lens, head, table, sels, outs)
+    go(torch.cuda.synchronize)
+    want = [x.clone() for x in state]
+    assert mcs.mcs_device_status() == 0 and want[6].isfinite().all()
+    same = lambda: all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(state, want))
+    go(lambda: None)
+    torch.cuda.synchronize()
+    assert same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(lambda: None)
+    for _ in range(4):
+        sels.zero_(), outs.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same()
+    assert mcs.mcs_device_status() == 0

@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kWriteThreads) paged_copy_kernel(const WriteAr
     const long long t = t0 + i * GROUPS;
     slot[i] = -1;
     if (t < a.T) {
-      k[i] = ld_global_nc16(a.k + t * a.stride + col);
-      v[i] = ld_global_nc16(a.v + t * a.stride + col);
+      k[i] = ld_global16(a.k + t * a.stride + col);
+      v[i] = ld_global16(a.v + t * a.stride + col);
       slot[i] = a.slots[t];
     }
   }
@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kWriteThreads, write_by_warps(D, kE4M3Cache, W
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
           if (r + i * size < run) {
-            k[i] = ld_global_nc16(src_k + static_cast<size_t>(r + i * size) * a.stride);
-            v[i] = ld_global_nc16(src_v + static_cast<size_t>(r + i * size) * a.stride);
+            k[i] = ld_global16(src_k + static_cast<size_t>(r + i * size) * a.stride);
+            v[i] = ld_global16(src_v + static_cast<size_t>(r + i * size) * a.stride);
           }
         }
 #pragma unroll
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kScoreThreads, 3)
     auto fetch = [&](int set, int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        x[set][i] = ld_global_nc16(mean + __shfl_sync(0xffffffffu, pid, j - start + i) * page_step);
+        x[set][i] = ld_global16(mean + __shfl_sync(0xffffffffu, pid, j - start + i) * page_step);
     };
     fetch(0, start);
     fetch(1, start + 4);

@@ -163,6 +163,17 @@ __device__ __forceinline__ uint4 ld_global_nc16(const void* src) {
   return v;
 }
 
+// The same of data that the kernel in front may still write when this one begins (a dependent
+// launch), where the promise of .nc, data that no one writes while the kernel lives, does not hold.
+__device__ __forceinline__ uint4 ld_global16(const void* src) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(src)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint4 ld_shared16(const void* src) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
