@@ -1051,3 +1051,38 @@ def test_steps_one_behind_another_see_their_own_rows(e4m3):
         torch.cuda.synchronize()
         assert same()
     assert mcs.mcs_device_status() == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,e4m3,page,select", [(20, 8, 8, 128, False, 128, 80), (48, 32, 16, 64, True, 64, 120)])
+def test_sparse_lists_long_enough_for_the_last_blocks(B, Hq, Hkv, D, e4m3, page, select):
+    # as the dense test above: pages stand in many tables; lists of every head are their own, some
+    # with holes, some sequences short or empty
+    r = np.random.default_rng(select)
+    most = select * page * 5 // 4
+    c = Cache([30 * page] + [0] * (B - 1), Hq, Hkv, D, page, e4m3, seed=B, extra=-(-most // page) - 30)
+    live = c.table[0, :30].copy()
+    c.lens = [int(x) for x in r.integers(most * 9 // 10, most, B)]
+    for i, x in ((2, 0), (B // 2, 1), (B - 3, 17), (B - 1, page + 1)):
+        c.lens[i] = x
+    c.table = live[r.integers(0, 30, c.table.shape)]
+    c.dtable, c.dlens = _i32(c.table), _i32(c.lens)
+    sel = _sel(c, select, 3)
+    sel[1, 0, ::3] = -1
+    tiles = sum(Hkv * (min(-(-x // page), select) * page // (4096 // (D * (1 if e4m3 else 2)))) for x in c.lens)
+    assert tiles >= 2 * torch.cuda.get_device_properties(0).multi_processor_count * 4 * 64
+    first = c.run(_i32(sel))
+    c.check(*first, sel, terms=2048)
+    again = c.run(_i32(sel))
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_join_of_more_segments_than_its_blocks_take_at_once(e4m3):
+    # 20480 segments, 32 to a block of the join and more blocks than are resident; long sequences
+    # among short ones, so that some segments have parts
+    r = np.random.default_rng(2)
+    lens = [int(x) for x in r.integers(0, 4, 4096)]
+    for i in (5, 6, 1999, 4095):
+        lens[i] = 1900 + i % 7
+    c = Cache(lens, 5, 5, 64, 16, e4m3, seed=3, extra=0)
+    c.check(*c.run())
