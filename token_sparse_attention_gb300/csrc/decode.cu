@@ -32,8 +32,7 @@
 // Which CTA does a share changes no result.  Handing shares out by a counter (a launch to
 // clear it, three times the parts) had given all of this back.
 //
-// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 284 us (282 with weights in
-// one part and one running sum in the tensor cores);
+// Measured: 12 x 75600 tokens of 8 KV heads, D = 128, E4M3 (1.86 GB) 283 us;
 // 1 x 1023 (4.2 MB) 8.3 us, all of it latency (shares 1.3 us, page numbers and first
 // tile 1.2, its products and the CTA's join 1.9, the launch behind it 0.7 and its join 2).
 #include <cuda_fp16.h>
@@ -490,10 +489,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // weights in two parts (bf16: 2^-16 off; f16: 2^-22, and 2^-37 of the largest weight), so that
       // their rounding stays below fp32 sums' or the output's; one f16 part, 2^-11 off, showed
-      // wherever values cancel
+      // wherever values cancel.  The low f16 parts of up to 8 heads are rows 8 to 15 of the high
+      // parts' product and cost nothing; those of more heads take products of their own (16 x 65536
+      // tokens of 4 KV heads with 16 query heads each: 179 -> 198 us; in products of their own
+      // with 8 heads: 167 -> 175).
       const float off0 = kShift - (m[0] == -INFINITY ? 0.f : m[0] * a.scale_log2);
       const float off1 = kShift - (m[1] == -INFINITY ? 0.f : m[1] * a.scale_log2);
-      constexpr int GS = E4M3 ? 2 : 1;  // slabs at a time
+      constexpr int GS = E4M3 ? (WIDE ? NS : 2) : 1;  // slabs at a time
 #pragma unroll
       for (int i0 = 0; i0 < NS; i0 += GS) {
         uint32_t p[GS][4], pl[GS][4];
@@ -510,12 +512,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               if (r == 1 && !WIDE) {
-                p[i][2 * j + 1] = pl[i][2 * j + 1] = 0;
+                if (!E4M3) p[i][2 * j + 1] = 0;
+                pl[i][2 * j + 1] = 0;
               } else if (E4M3) {
                 uint32_t hw = pack_f16(x[2 * r], x[2 * r + 1]);
                 const float2 hf = __half22float2(*reinterpret_cast<__half2*>(&hw));
                 p[i][2 * j + r] = hw;
-                pl[i][2 * j + r] = pack_f16(x[2 * r] - hf.x, x[2 * r + 1] - hf.y);
+                (WIDE ? pl[i][2 * j + r] : p[i][2 * j + 1]) = pack_f16(x[2 * r] - hf.x, x[2 * r + 1] - hf.y);
               } else {
                 const uint32_t hb = pack_bf16(x[2 * r], x[2 * r + 1]);
                 p[i][2 * j + r] = hb;
@@ -546,8 +549,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t odd0 = __byte_perm(a0, a1, 0x7632), odd1 = __byte_perm(b0, b1, 0x7632);
                 mma<true>(sums[2 * u], p[i], even0, even1);
                 mma<true>(sums[2 * u + 1], p[i], odd0, odd1);
-                mma<true>(sums[2 * u], pl[i], even0, even1);
-                mma<true>(sums[2 * u + 1], pl[i], odd0, odd1);
+                if (WIDE) {
+                  mma<true>(sums[2 * u], pl[i], even0, even1);
+                  mma<true>(sums[2 * u + 1], pl[i], odd0, odd1);
+                }
               }
             } else {
               mma<false>(o[c], p[i], f[0], f[1]);
@@ -558,9 +563,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (E4M3) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-              for (int e = 0; e < (WIDE ? 4 : 2); ++e) o[2 * c + u][e] += sums[u][e];
+            for (int u = 0; u < 4; ++u) {
+              float* to = o[2 * c + u];
+              if (WIDE) {
+                f2_unpack(f2_add(f2_pack(to[0], to[1]), f2_pack(sums[u][0], sums[u][1])), to[0], to[1]);
+                f2_unpack(f2_add(f2_pack(to[2], to[3]), f2_pack(sums[u][2], sums[u][3])), to[2], to[3]);
+              } else {
+                to[0] += sums[u][0] + sums[u][2];
+                to[1] += sums[u][1] + sums[u][3];
+              }
+            }
           }
         }
       }
