@@ -485,7 +485,9 @@ mcs_status mcs_paged_plan(const mcs_paged* p, const int32_t* new_lens, const int
  * values of rows 0 .. its last new row, summed in fp32 and rounded once; the
  * rows in front of the first new one are read from the cache.  The slots of
  * one call are distinct, and the tokens of one page stand one behind another
- * in ascending order, as mcs_paged_plan lays them out.
+ * with ascending slots that leave none out, as mcs_paged_plan lays them out:
+ * of a page that a call fills with a gap, or with skipped tokens in between,
+ * the mean is undefined (the rows are stored all the same).
  */
 mcs_status mcs_paged_write(const mcs_paged* p, int T, const void* k, const void* v,
                            const int32_t* slots, void* k_cache, void* v_cache, void* k_mean,
@@ -496,7 +498,8 @@ mcs_status mcs_paged_write(const mcs_paged* p, int T, const void* k, const void*
  * * q[b, h] . k) v over the lens[b] tokens of sequence b, q [B, Hq, D] (rows
  * q_stride apart), out [B, Hq, D] bf16; lse [B, Hq] fp32 (natural log,
  * nullable).  lens counts the new token itself, once mcs_paged_write has stored
- * it.  A sequence of no tokens gets zeros, and -inf as its lse.
+ * it.  A sequence of no tokens gets zeros, and -inf as its lse.  An infinite
+ * value in a row that holds a token makes its column NaN or infinite.
  * E4M3: q is converted to f16 as in mcs_sparse_attn_e4m3 (values below 2^-14
  * to multiples of 2^-24).  The weights enter the product with v as two parts,
  * off by 2^-16 of a weight (bf16 cache) or 2^-22 (E4M3, and 2^-37 of the

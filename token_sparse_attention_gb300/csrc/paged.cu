@@ -266,6 +266,8 @@ __device__ __forceinline__ void store8(const WriteArgs& a, const Scale& ks, cons
 
 // Without means.  A block takes one KV head and a window of consecutive tokens, D/8
 // threads per row and ROWS rows per thread, all loaded before the first slot is needed.
+// Bound: HBM (28 005 tokens of 8 heads, bf16 40 us, 94 % of a copy; E4M3 31 us, 92 %), latency for a
+// step (128 tokens 1.9 us).
 template <int D, bool kE4M3Cache, int ROWS>
 __global__ void __launch_bounds__(kWriteThreads) paged_copy_kernel(const WriteArgs a) {
   constexpr int LANES = D / 8, GROUPS = kWriteThreads / LANES, WINDOW = GROUPS * ROWS;
@@ -782,7 +784,10 @@ __device__ __noinline__ uint2 by_digits(const SelectArgs& a, TopkShared& sh, int
 // below them are not (a step is wider than 2E); of the few in between the select-th is found by
 // rank, and what lies within 2E of it is ranked by the exact scores.  Where that does not
 // separate few pages (infinite scores, a range as narrow as the bound, ties en masse), the
-// threshold is found digit by digit (which for all lists took 1 to 2 us more than steps).
+// threshold is found digit by digit (which for all lists took 1 to 2 us more than steps).  Ties en
+// masse, more than 256 pages within the bound, cost an exact score each, 0.13 us a page of a list: 4725
+// pages of 40 heads take 21 us as they come, 106 us where there are 8 different means, 335 us where half
+// of the means are equal and 620 us where all are.
 __global__ void __launch_bounds__(1024) paged_topk_kernel(const __grid_constant__ SelectArgs a, int stride, int bins) {
   extern __shared__ __align__(16) uint32_t hist[];  // [bins], then the places of a list that fits
   __shared__ TopkShared sh;

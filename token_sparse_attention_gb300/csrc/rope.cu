@@ -9,7 +9,7 @@
 // values of each half, so that no value crosses threads and only the mean is a
 // shuffle sum.  Values that are not rotated are pairs of angle 0.  The weights
 // are multiplied into a token's cosines and sines once for the heads a warp
-// takes (8, or 16 at D = 64): y_a' = r (x_a (w_a cos) - x_b (w_b sin)).  Pairs of values go through
+// takes (8, or 32 at D = 64; gradients 4 or 8, and 8 at D = 64): y_a' = r (x_a (w_a cos) - x_b (w_b sin)).  Pairs of values go through
 // the packed fp32 instructions.
 //
 // Bound: HBM, 4 bytes per value (6 for the gradients), at about 45 (85)
@@ -263,8 +263,8 @@ __device__ __forceinline__ void normed(const Row& x, float eps, uint64_t* u, uin
   }
 }
 
-// A tensor with fewer heads than half of what a warp takes of one token: the warp
-// takes the heads of several consecutive tokens, with angles for each row.  One
+// A tensor with at most half of the heads that a warp takes of one token (4, or 16 at D = 64;
+// gradients 2 and 4): the warp takes the heads of several consecutive tokens, with angles for each row.  One
 // tensor per launch.
 struct One {
   int H, tokens;  // heads; tokens per warp
@@ -603,7 +603,7 @@ One one_of(const RopeArgs& a, bool q, int heads) {
   o.w = q ? a.wq : a.wk;
   return o;
 }
-// Whether a tensor gets a launch of its own with several tokens per warp: below half of
+// Whether a tensor gets a launch of its own with several tokens per warp: at most half of
 // the heads a warp takes, and enough tokens to fill the SMs several times, where the
 // second launch pays (62598 tokens of 2 + 1 heads, D = 128: 61 us in one, 32 in two).
 bool few_heads(int H, int heads, long long tokens, int sms) {
