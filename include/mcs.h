@@ -544,6 +544,31 @@ mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void
                                    float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Attention of a step's new tokens, any number per sequence, over the pages
+ * (prompts, pieces of them, proposed tokens to be checked).  cu_new [B + 1] as
+ * mcs_paged_plan leaves it: rows cu_new[b] .. cu_new[b + 1] of q [T, Hq, D] (rows
+ * q_stride apart) are the last tokens of sequence b, in order; lens counts them,
+ * and mcs_paged_write has stored their keys and values.  A token attends to the
+ * tokens in front of it and to itself (causal): out [T, Hq, D] bf16, lse [T, Hq]
+ * fp32 (natural log, nullable).  Rows that are no sequence's stay as they were.  A
+ * token all of whose pages are bad gets zeros, and -inf as its lse.  A sequence
+ * whose rows do not lie in [0, T), or with more new tokens than lens[b], or whose
+ * length is negative or above max_pages * page, sets MCS_ERR_BOUNDS and its rows
+ * stay as they were.  Values behind a token, infinite or NaN, do not reach it;
+ * an infinite or NaN value that it attends to makes its column NaN or infinite.
+ * E4M3: q is converted to f16 as in mcs_paged_decode.  The weights are rounded to
+ * bf16 (bf16 cache) or f16 (E4M3) for the product with v and normalised by the sum of the
+ * rounded ones; scores, maxima and sums are fp32.  Results do not depend on timing.
+ * ws: at least mcs_paged_attn_workspace(p) bytes, as for mcs_paged_decode.
+ * 0 <= T <= 2^30, T * Hq below 2^31.
+ */
+size_t mcs_paged_attn_workspace(const mcs_paged* p);
+mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* k_cache,
+                          const void* v_cache, const int32_t* block_table, const int32_t* lens,
+                          const int32_t* cu_new, void* out, float* lse, void* ws, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/*
  * What stands between a block's projections and its attention: RMS norm of
  * each head of q and k, then the rotation of its first `rot` values by the
  * token's angles, in one pass (for mcs_group, mcs_dense_attn and the sparse

@@ -99,6 +99,43 @@ def decode(q, k_cache, v_cache, table, lens, scale, sel=None):
     return out, lse, absv, size
 
 
+def attn(q, k_cache, v_cache, table, lens, cu, scale, num_pages=None):
+    """Causal attention of the last cu[b + 1] - cu[b] tokens of each sequence, caches in fp64.
+
+    Returns out [T, Hq, D], lse [T, Hq] (NaN in rows that are no sequence's), the mean of |v| under
+    the weights and the largest sum of |q k| scale, as decode() does.  Pages outside
+    [0, num_pages) are skipped."""
+    T, Hq, D = q.shape
+    Hkv, page = k_cache.shape[1:3]
+    num_pages = num_pages or k_cache.shape[0]
+    group = Hq // Hkv
+    out, absv = np.full((T, Hq, D), np.nan), np.zeros((T, Hq, D))
+    lse, size = np.full((T, Hq), np.nan), np.zeros((T, Hq))
+    for b in range(len(lens)):
+        n, new = int(lens[b]), int(cu[b + 1] - cu[b])
+        if new <= 0:
+            continue
+        rows = [(j * page + r, table[b, j], r) for j in range(-(-n // page)) for r in range(page)
+                if j * page + r < n and 0 <= table[b, j] < num_pages]
+        at = np.array(rows).reshape(-1, 3)
+        for h in range(Hkv):
+            k, v = k_cache[at[:, 1], h, at[:, 2]], v_cache[at[:, 1], h, at[:, 2]]
+            for t in range(new):
+                sees = at[:, 0] <= n - new + t
+                ks, vs, r, hs = k[sees], v[sees], int(cu[b]) + t, slice(h * group, (h + 1) * group)
+                if not len(ks):
+                    out[r, hs], lse[r, hs] = 0, -math.inf
+                    continue
+                z = q[r, hs] @ ks.T * scale
+                top = z.max(1, keepdims=True)
+                e = np.exp(z - top)
+                total = e.sum(1, keepdims=True)
+                out[r, hs], absv[r, hs] = e @ vs / total, e @ np.abs(vs) / total
+                lse[r, hs] = (top + np.log(total))[:, 0]
+                size[r, hs] = (np.abs(q[r, hs]) @ np.abs(ks).T).max(1) * scale
+    return out, lse, absv, size
+
+
 def _pairs(D, rot, interleaved):
     one = np.arange(0, rot, 2) if interleaved else np.arange(rot // 2)
     return one, one + (1 if interleaved else rot // 2)

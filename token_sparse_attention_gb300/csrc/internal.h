@@ -224,6 +224,48 @@ struct DecodeArgs {
 cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream);
 size_t paged_decode_workspace_bytes(int D, int group);
 
+// Attention of many query rows per KV head over pages (see paged_attn.cu).
+struct PagedAttnArgs {
+  int G;                     // sequences, or groups of them with a common beginning
+  int Hq, Hkv, D, page, num_pages, max_pages;
+  int T;                     // rows of q
+  int heads, chunks;         // query heads of a unit's token; such chunks of a KV head's heads
+  int tokens;                // tokens of a unit: 128 / heads
+  int causal;
+  int rows;                  // num_pages * Hkv * page
+  int fault;                 // test-only: 1 = loads stop after the first tiles
+  long long q_stride;
+  float scale_log2;          // softmax scale * log2(e) (* k_scale for E4M3)
+  float v_scale;             // 1 for bf16
+  const __nv_bfloat16* q;    // [T, Hq, D]
+  const void* k;             // [num_pages, Hkv, page, D]
+  const void* v;
+  const int32_t* table;      // rows of max_pages
+  const int32_t* row_of;     // [G] table row of each; null: its own number
+  const int32_t* cu;         // [G + 1] rows of q
+  const int32_t* keys;       // [G] keys
+  __nv_bfloat16* out;        // [T, Hq, D]
+  float* lse;                // [T, Hq], nullable
+  float* whole;              // null, or where rows go unjoined: (log2 max, sums) [T * Hq] float4, values
+  float* parts;              // paged_attn_parts_bytes
+  int4* ends;                // paged_attn_ends_bytes
+  long long* places;         // [G + 1] first positions, nullable
+  unsigned* status;
+};
+// tq: 3-D map over q, box {64, heads, tokens}; tk, tv: 2-D maps over the caches' rows, box {64, page}
+// (bf16 only).
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                              const CUtensorMap* tv, bool e4m3, cudaStream_t stream);
+size_t paged_attn_parts_bytes(int D);
+size_t paged_attn_ends_bytes();
+
+// Tiled bf16 maps with 128-byte swizzle: rows [rows][D] in boxes of box_rows x 64, and q [T][H][D]
+// with tokens `stride` elements apart in boxes of tokens x heads x 64.
+bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows);
+bool make_query_map(CUtensorMap* m, const void* base, int T, int H, int D, long long stride, int heads, int tokens);
+// MCS_TEST_FAULT (see mcs_api.cu).
+int test_fault();
+
 // ---------------------------------------------------------------- norm and rotation
 
 struct RopeArgs {

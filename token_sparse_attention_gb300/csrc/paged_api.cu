@@ -3,6 +3,8 @@
 // in include/mcs.h.
 #include <math.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "mcs.h"
 
@@ -95,6 +97,38 @@ mcs_status run_decode(const mcs_paged* p, const void* q, const void* k_cache, co
   if (s != MCS_OK) return s;
   return finish(mcs::launch_paged_decode(a, e4m3, stream), what);
 }
+
+// What the attention of many rows takes from the params; the maps are made for bf16 caches.
+mcs_status many_rows(const mcs_paged* p, int T, const void* q, const void* k_cache, const void* v_cache,
+                     mcs::PagedAttnArgs* a, CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
+  const int group = p->Hq / p->Hkv;
+  a->Hq = p->Hq;
+  a->Hkv = p->Hkv;
+  a->D = p->D;
+  a->page = p->page;
+  a->num_pages = p->num_pages;
+  a->max_pages = p->max_pages;
+  a->T = T;
+  a->heads = std::min(group, 128);
+  a->chunks = (group + a->heads - 1) / a->heads;
+  a->tokens = 128 / a->heads;
+  a->rows = p->num_pages * p->Hkv * p->page;
+  a->q_stride = q_stride_of(p);
+  a->scale_log2 = scale_log2_of(p);
+  a->v_scale = p->kv == MCS_KV_E4M3 ? p->v_scale : 1.f;
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k = k_cache;
+  a->v = v_cache;
+  a->fault = mcs::test_fault();
+  if (p->kv == MCS_KV_BF16 &&
+      (!mcs::make_query_map(tq, q, T, p->Hq, p->D, a->q_stride, a->heads, a->tokens) ||
+       !mcs::make_rows_map(tk, k_cache, a->rows, p->D, p->page) ||
+       !mcs::make_rows_map(tv, v_cache, a->rows, p->D, p->page)))
+    return mcs::record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled(paged)");
+  return status_word(&a->status);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 mcs_status check_rope(const mcs_rope* p) {
   if (p == nullptr) return MCS_ERR_INVALID_ARG;
@@ -278,6 +312,41 @@ mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void
   if (select < 1 || !good_ints(sel)) return MCS_ERR_INVALID_ARG;
   return run_decode(p, q, k_cache, v_cache, block_table, lens, sel, select, out, lse, ws, ws_bytes,
                     stream, "paged sparse decode launch");
+}
+
+size_t mcs_paged_attn_workspace(const mcs_paged* p) {
+  return check_paged(p) == MCS_OK
+             ? round256(mcs::paged_attn_ends_bytes()) + mcs::paged_attn_parts_bytes(p->D)
+             : 0;
+}
+
+mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* k_cache,
+                          const void* v_cache, const int32_t* block_table, const int32_t* lens,
+                          const int32_t* cu_new, void* out, float* lse, void* ws, size_t ws_bytes,
+                          cudaStream_t stream) {
+  mcs_status s = check_paged(p);
+  if (s != MCS_OK) return s;
+  if (T < 0) return MCS_ERR_INVALID_ARG;
+  if (T > (1 << 30) || static_cast<long long>(T) * p->Hq > kIntMax) return MCS_ERR_UNSUPPORTED;
+  if (T == 0) return MCS_OK;
+  if (!good(q) || !good(k_cache) || !good(v_cache) || !good(out) || !good_ints(block_table) ||
+      !good_ints(lens) || !good_ints(cu_new) || !aligned(lse, 4))
+    return MCS_ERR_INVALID_ARG;
+  if (!good(ws) || ws_bytes < mcs_paged_attn_workspace(p)) return MCS_ERR_WORKSPACE;
+  mcs::PagedAttnArgs a{};
+  CUtensorMap tq{}, tk{}, tv{};
+  if ((s = many_rows(p, T, q, k_cache, v_cache, &a, &tq, &tk, &tv)) != MCS_OK) return s;
+  a.G = p->B;
+  a.causal = 1;
+  a.table = block_table;
+  a.cu = cu_new;
+  a.keys = lens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.ends = static_cast<int4*>(ws);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(mcs::paged_attn_ends_bytes()));
+  return finish(mcs::launch_paged_attn(a, &tq, &tk, &tv, p->kv == MCS_KV_E4M3, stream),
+                "paged attention launch");
 }
 
 mcs_status mcs_qk_norm_rope(const mcs_rope* p, const void* q, const void* k, const float* wq,

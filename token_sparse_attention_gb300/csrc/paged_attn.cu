@@ -1,0 +1,1132 @@
+// Attention of many query rows over a paged cache on tcgen05 tensor cores: the new tokens
+// of a step, several per sequence (causal), and the common beginning of sequences that
+// decode together.
+//
+// o_i = sum_j exp(s_ij - m_i) v_j / l_i with s_ij = scale q_i . k_j over the keys j that row
+// i sees: the query heads of a KV head and the tokens of a sequence (or the sequences of a
+// group) are rows of one product with the same keys.  4 D flops per visible (row, key) pair
+// against 4 D bytes (bf16) per key: from about 290 rows on the tensor cores bound it,
+// below that HBM does, as long as each key is read once for all rows.
+//
+// A unit is 128 rows (MMA M): tokens * heads, a token's heads next to each other, as they lie
+// in q.  A segment is a pair of units (a, b) of one sequence and KV head, which share every
+// K and V tile of 128 keys, or its last odd unit, whose tiles the two softmax chains take in
+// turn (a the even, b the odd ones) and join in the CTA.  All segments in a row form one list
+// of steps (a step: one tile for two units, or two tiles for one), and each of the SMs' CTAs
+// takes an equal share of it, whatever the lengths are: few long sequences are so split along
+// their keys, many short ones along the list.  What a share holds whole it writes at once;
+// parts of segments that cross shares go to the workspace and are joined in the order of
+// their keys by a second, programmatically dependent launch.
+//
+// One CTA per SM, 16 warps, as in the dense kernel:
+//   warps 0-3   softmax and epilogue of chain a; thread t owns row t (TMEM lane t)
+//   warps 4-7   the same for chain b
+//   warps 8-14  loads.  bf16: warp 8 issues TMA boxes of a page's rows; warps 9-14 look
+//               through the V tiles in which some row's mask leaves something out (below).
+//               E4M3: all seven copy rows with cp.async and convert them to f16
+//   warp 15     TMEM and MMA issue (one elected lane)
+// TMEM: S_a, S_b (P is written over S), O_a, O_b.  Shared memory: Q_a, Q_b and a ring of K
+// and V tiles that runs on from segment to segment; the next segment's queries are loaded
+// once its last scores are there, while softmax, products and epilogue are still at work.
+//
+// A weight of zero does not hide an infinite or NaN value from a matrix product: 0 * inf =
+// NaN.  So V tiles that hold keys behind a row's last one are looked through before the
+// product: rows that hold no token become zeros, and values of tokens that are not finite
+// become zeros, too, with the first such key of each column kept; a row that sees that key
+// gets NaN in the column.  One or two tiles per segment are concerned.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace mcs {
+namespace {
+
+constexpr int BM = 128;   // rows per unit
+constexpr int BN = 128;   // keys per tile
+constexpr int kLoaders = 7;
+constexpr int kFirstLoader = 8;
+constexpr int kMmaWarp = kFirstLoader + kLoaders;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMaxSms = 160;
+constexpr int kSegCost = 2;  // what changing the segment costs, in steps
+constexpr int kSlab = 16;    // keys that surely lie in one page
+constexpr int kSlabs = BN / kSlab;
+constexpr int kWindow = 32 / kSlabs;  // tiles whose pages a warp looks up at once
+constexpr int kBadSlots = 16;         // steps ahead of the softmax that loads may be: ring depth
+
+// Rescaled only when a row's maximum grows by more than 2^16 (f16 weights: 2^15 < 65504).
+template <bool E4M3>
+constexpr float kThreshold = E4M3 ? 15.f : 16.f;
+
+template <int D>
+struct Layout {
+  static constexpr int kSub = D / 64;                 // 128-byte column sub-tiles of a row
+  static constexpr int kSubBytes = BN * 128;
+  static constexpr int kTileBytes = kSub * kSubBytes;
+  static constexpr int kStages = D == 128 ? 5 : 12;
+  static constexpr int kRing = 2 * kTileBytes;
+  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kNumBars = 3 * kStages + 16;
+  static constexpr int kBadKey = kBars + kNumBars * 8;           // [2][D] words
+  static constexpr int kMl = kBadKey + 2 * D * 4;                // [3][128] floats
+  static constexpr int kMisc = kMl + 3 * BM * 4;                 // Misc
+  static constexpr int kSmem = kMisc + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kStages <= kBadSlots, "bad slots");
+};
+
+// ------------------------------------------------------------------ the list
+
+// sum of floor((a i + b) / m) over i < n: Euclid's algorithm on (m, a), a and m small.
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y - n * m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// A sequence of the list (shared beginnings: a group): n tokens, rows cu .. cu + n of q, keys
+// [0, keys), of which token t sees keys - n + t + 1 (causal) or all.
+struct Seq {
+  int cu, n, keys;
+};
+__device__ __forceinline__ int tiles_until(const PagedAttnArgs& a, const Seq& s, int e) {
+  return static_cast<int>((static_cast<long long>(a.causal ? s.keys - s.n + e : s.keys) + BN - 1) / BN);
+}
+__device__ __forceinline__ bool load_seq(const PagedAttnArgs& a, int g, Seq& s, bool report) {
+  const int lo = a.cu[g], hi = a.cu[g + 1];
+  s.keys = a.keys[g];
+  s.cu = lo;
+  s.n = 0;
+  if (hi == lo) return false;
+  if (lo < 0 || hi < lo || hi > a.T || s.keys < 0 ||
+      static_cast<long long>(s.keys) > static_cast<long long>(a.max_pages) * a.page ||
+      (a.causal && hi - lo > s.keys)) {
+    if (report) atomicOr(a.status, DEV_BOUNDS);
+    return false;
+  }
+  s.n = s.keys > 0 ? hi - lo : 0;
+  return s.n > 0;
+}
+__device__ __forceinline__ int units_of(const PagedAttnArgs& a, const Seq& s) {
+  return (s.n + a.tokens - 1) / a.tokens;
+}
+// Positions of the first k pairs of a sequence's KV head.
+__device__ __forceinline__ long long pairs_upto(const PagedAttnArgs& a, const Seq& s, int k) {
+  if (k <= 0) return 0;
+  if (!a.causal) return static_cast<long long>(k) * (tiles_until(a, s, s.n) + kSegCost);
+  const int w = 2 * a.tokens;
+  // the last pair may end with the sequence, inside its second unit
+  const bool cut = static_cast<long long>(k) * w > s.n;
+  const int whole = cut ? k - 1 : k;
+  return floor_sum(whole, BN, w, static_cast<long long>(s.keys) - s.n + w + BN - 1) +
+         (cut ? tiles_until(a, s, s.n) : 0) + static_cast<long long>(k) * kSegCost;
+}
+__device__ __forceinline__ long long positions_of(const PagedAttnArgs& a, const Seq& s) {
+  const int units = units_of(a, s);
+  return pairs_upto(a, s, units / 2) +
+         ((units & 1) ? (tiles_until(a, s, s.n) + 1) / 2 + kSegCost : 0);
+}
+
+// A walk over a CTA's share, segment by segment; every role makes it by itself.
+struct Walk {
+  Seq s;
+  int g, head, i;  // sequence, KV head and its chunk of query heads, pair (the last odd unit behind them)
+  bool single;     // an odd unit, whose tiles the chains take in turn
+  int tiles, tiles_a;  // of the segment; of a pair's first unit
+  int steps;       // of the segment
+  int t0, count;   // the share's steps of it: [t0, t0 + count)
+  long long left;  // positions from t0 to the share's end
+  int index;       // segments of the share in front of this one
+};
+__device__ __forceinline__ void set_segment(const PagedAttnArgs& a, Walk& w) {
+  const int pairs = units_of(a, w.s) / 2;
+  w.single = w.i >= pairs;
+  if (w.single) {
+    w.tiles = w.tiles_a = tiles_until(a, w.s, w.s.n);
+    w.steps = (w.tiles + 1) / 2;
+  } else {
+    const long long e = (2LL * w.i + 2) * a.tokens;
+    w.tiles = tiles_until(a, w.s, static_cast<int>(min(e, static_cast<long long>(w.s.n))));
+    w.tiles_a = tiles_until(a, w.s, static_cast<int>(e - a.tokens));
+    w.steps = w.tiles;
+  }
+}
+__device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Walk& w) {
+  w.left -= w.steps + kSegCost - w.t0;
+  if (w.left <= 0) return false;
+  const int units = units_of(a, w.s);
+  if (++w.i >= units / 2 + (units & 1)) {
+    w.i = 0;
+    if (++w.head >= a.Hkv * a.chunks) {
+      w.head = 0;
+      do {  // (there is one, unless the lengths change under the kernel)
+        if (++w.g >= a.G) return false;
+      } while (!load_seq(a, w.g, w.s, false));
+    }
+  }
+  set_segment(a, w);
+  w.t0 = 0;
+  w.count = static_cast<int>(min(static_cast<long long>(w.steps), w.left));
+  ++w.index;
+  return true;
+}
+// Whether chain x has a tile in step j of the share's part of the segment, and which.
+__device__ __forceinline__ int tile_of(const Walk& w, int x, int j) {
+  return w.single ? 2 * (w.t0 + j) + x : w.t0 + j;
+}
+__device__ __forceinline__ bool has_tile(const Walk& w, int x, int j) {
+  return tile_of(w, x, j) < (!w.single && x == 0 ? w.tiles_a : w.tiles);
+}
+// Keys that every row of the segment sees: tiles behind it are looked through.
+__device__ __forceinline__ int seen_by_all(const PagedAttnArgs& a, const Walk& w) {
+  return a.causal ? w.s.keys - w.s.n + 2 * w.i * a.tokens + 1 : w.s.keys;
+}
+__device__ __forceinline__ int last_tile(const Walk& w) { return min(tile_of(w, w.single ? 1 : 0, w.count - 1), w.tiles - 1); }
+__device__ __forceinline__ bool look_through(int seen, int tile) { return (tile + 1) * static_cast<long long>(BN) > seen; }
+
+// ------------------------------------------------------------------ small pieces
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+// Used only while tearing down: bounded by time alone.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitLimitCycles) return;
+  }
+}
+__device__ __forceinline__ float sum8(const uint64_t* acc) {
+  float a0, a1, a2, a3, a4, a5, a6, a7;
+  f2_unpack(acc[0], a0, a1);
+  f2_unpack(acc[1], a2, a3);
+  f2_unpack(acc[2], a4, a5);
+  f2_unpack(acc[3], a6, a7);
+  return ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
+}
+__device__ __forceinline__ float max64(const float* s) {
+  float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+  for (int c = 4; c < 60; c += 8) {
+    m0 = fmax3(m0, s[c + 0], s[c + 1]);
+    m1 = fmax3(m1, s[c + 2], s[c + 3]);
+    m2 = fmax3(m2, s[c + 4], s[c + 5]);
+    m3 = fmax3(m3, s[c + 6], s[c + 7]);
+  }
+  m0 = fmax3(m0, s[60], s[61]);
+  m1 = fmax3(m1, s[62], s[63]);
+  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+}
+// Byte offset of 16-byte chunk `seg` of row r in a 128-row tile of 128-byte-swizzled sub-tiles.
+__device__ __forceinline__ int swz_offset(int r, int seg) {
+  return (seg >> 3) * (BN * 128) + r * 128 + (((seg & 7) ^ (r & 7)) << 4);
+}
+// Columns of 64 scores, from column c0 of the tile, that the row does not see become -inf.
+__device__ __forceinline__ void mask64(float* s, int c0, int valid, uint32_t bad) {
+#pragma unroll
+  for (int c = 0; c < 64; ++c)
+    if (c + c0 >= valid || ((bad >> ((c + c0) / kSlab)) & 1u)) s[c] = -INFINITY;
+}
+
+// Values that are not finite in tiles that are looked through: per column the first key, as
+// segment (its number in the share, plus one) << 10 | 1023 - (key - first such tile's first key), so
+// that a later segment's entries are larger than what is left of an earlier one's.  Two
+// segments' records stand side by side; a third waits until the first one's rows are written.
+// The tiles of a segment that are looked through hold fewer than 128 + 256 + 128 keys.
+__device__ __forceinline__ uint32_t bad_mark(int index) { return (static_cast<uint32_t>(index + 1) & 0x3FFFFFu) << 10; }
+__device__ __forceinline__ void note_bad(uint32_t* record, volatile uint32_t* any, const Walk& w, int seen, int col, long long key) {
+  const int first = seen / BN * BN;
+  atomicMax(record + col, bad_mark(w.index) | (1023u - static_cast<uint32_t>(key - first)));
+  *any = bad_mark(w.index);
+}
+// The first key of the column that is not finite (none: beyond every key).
+__device__ __forceinline__ int first_bad(const uint32_t* record, const Walk& w, int seen, int col) {
+  const uint32_t x = record[col];
+  return (x & ~1023u) == bad_mark(w.index) ? seen / BN * BN + static_cast<int>(1023u - (x & 1023u)) : 0x7fffffff;
+}
+
+struct Misc {
+  uint8_t bad[kBadSlots][2];  // slabs of each step's tiles whose pages lie outside the cache
+  uint32_t tmem;
+  int abort;
+  uint32_t any_bad[2];
+  long long sums[kThreads / 32];
+  struct {
+    long long offset;
+    int g, head, i;
+  } start;
+};
+static_assert(sizeof(Misc) <= 256, "misc");
+
+// Parts of segments that cross shares: slot 2 c of share c for a segment that ends there, 2 c + 1
+// for one that goes on.  (log2 maximum, sum of the weights as multiplied, their fp32 sum, 0) of
+// the 256 rows, then the rows' D sums.
+constexpr int kPartRows = 2 * BM;
+__host__ __device__ constexpr size_t part_floats(int D) { return static_cast<size_t>(kPartRows) * (4 + D); }
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const PagedAttnArgs a) {
+  using L = Layout<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];  // (swizzled tiles; there is no other shared memory)
+  uint8_t* qs = smem;
+  uint8_t* ring = smem + L::kRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [NS] stage loaded
+  uint64_t* empty = full + NS;                                   // [NS] stage read
+  uint64_t* looked = empty + NS;                                 // [NS] V tile looked through (bf16)
+  uint64_t* q_full = looked + NS;                                // queries loaded
+  uint64_t* q_empty = q_full + 1;                                // the segment's last scores written
+  uint64_t* s_full = q_empty + 1;                                // [2] S_x written
+  uint64_t* p_full = s_full + 2;                                 // [2] P_x written
+  uint64_t* o_full = p_full + 2;                                 // [2] O_x of the segment final
+  uint64_t* joined = o_full + 2;                                 // [4] chain b's maxima and sums there
+  uint64_t* written = joined + 4;                                // [2] epilogue of segment i done: written[i & 1]
+  uint64_t* fin = written + 2;                                   // every MMA done
+  uint32_t* records = reinterpret_cast<uint32_t*>(smem + L::kBadKey);  // [2][D]
+  float* s_ml = reinterpret_cast<float*>(smem + L::kMl);         // chain b's maxima and sums
+  Misc& misc = *reinterpret_cast<Misc*>(smem + L::kMisc);
+  volatile int* abort_flag = &misc.abort;
+
+  const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full + s, E4M3 ? 32 * kLoaders : 1);
+      mbar_init(empty + s, 1);
+      mbar_init(looked + s, kLoaders - 1);
+    }
+    mbar_init(q_full, E4M3 ? 32 * kLoaders : 1);
+    mbar_init(q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full + x, 1);
+      mbar_init(p_full + x, 4);
+      mbar_init(o_full + x, 1);
+      mbar_init(written + x, 8);
+      misc.any_bad[x] = 0;
+    }
+    for (int x = 0; x < 4; ++x) mbar_init(joined + x, 1);
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    misc.start.g = -1;
+    fence_mbar_init();
+  }
+  if (tid < 2 * D) records[tid] = 0;
+  pdl_begin();
+
+  // ---- this CTA's share: thread t sums sequences [t * per, (t + 1) * per)
+  const int per = (a.G + kThreads - 1) / kThreads, segs = a.Hkv * a.chunks;
+  long long own = 0;
+  for (int k = 0; k < per; ++k) {
+    Seq s;
+    const int g = tid * per + k;
+    if (g < a.G && load_seq(a, g, s, blockIdx.x == 0)) own += positions_of(a, s);
+  }
+  long long upto = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
+  }
+  if (lane == 31) misc.sums[warp] = upto;
+  __syncthreads();
+  long long all = 0;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) {
+    if (k < warp) upto += misc.sums[k];
+    all += misc.sums[k];
+  }
+  if (blockIdx.x == 0 && a.places != nullptr) {  // where each sequence begins, for the join
+    long long at = upto - own;
+    for (int k = 0; k < per; ++k) {
+      Seq s;
+      const int g = tid * per + k;
+      if (g >= a.G) break;
+      a.places[g] = at;
+      if (load_seq(a, g, s, false)) at += positions_of(a, s);
+    }
+    if (tid == 0) a.places[a.G] = all;
+  }
+  all *= segs;
+  const int shares = static_cast<int>(min(all, static_cast<long long>(gridDim.x)));
+  const bool busy = static_cast<int>(blockIdx.x) < shares;
+  const long long lo = busy ? all * blockIdx.x / shares : 0, hi = busy ? all * (blockIdx.x + 1) / shares : 0;
+  if (busy && lo >= (upto - own) * segs && lo < upto * segs) {
+    long long base = (upto - own) * segs;
+    for (int k = 0; k < per; ++k) {
+      Seq s;
+      const int g = tid * per + k;
+      if (g >= a.G || !load_seq(a, g, s, false)) continue;
+      const long long size = positions_of(a, s);
+      if (lo < base + size * segs) {
+        const long long in = lo - base;
+        misc.start.g = g;
+        misc.start.head = static_cast<int>(in / size);
+        misc.start.offset = in - misc.start.head * size;
+        break;
+      }
+      base += size * segs;
+    }
+  }
+  if (warp == kMmaWarp && busy) {
+    tmem_alloc(&misc.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  Walk w = {};
+  bool more = busy && misc.start.g >= 0;
+  if (more && warp == 0) {  // the pair, 32 places at a time
+    Seq s;
+    load_seq(a, misc.start.g, s, false);
+    const int pairs = units_of(a, s) / 2;
+    int first = 0, n = pairs + 1;  // the last k in [first, first + n) with pairs_upto(k) <= offset
+    while (n > 1) {
+      const int step = (n + 31) / 32, k = first + lane * step;
+      const bool in = lane * step < n && pairs_upto(a, s, k) <= misc.start.offset;
+      const int at = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0 is in)
+      n = min(step, n - at * step);
+      first += at * step;
+    }
+    if (lane == 0) {
+      misc.start.i = first;
+      misc.start.offset -= pairs_upto(a, s, first);
+    }
+  }
+  __syncthreads();
+  int part_from = -1;  // the share in which the first segment begins, if that is not this one
+  if (more) {
+    w.g = misc.start.g;
+    w.head = misc.start.head;
+    w.i = misc.start.i;
+    load_seq(a, w.g, w.s, false);
+    const int units = units_of(a, w.s);
+    w.i = min(w.i, units / 2 + (units & 1) - 1);
+    set_segment(a, w);
+    w.t0 = static_cast<int>(misc.start.offset);
+    w.left = hi - lo;
+    w.count = static_cast<int>(min(static_cast<long long>(w.steps - w.t0), w.left));
+    if (w.t0 > 0 && w.count > 0 && w.t0 + w.count == w.steps) {
+      // the largest share that begins at or in front of the segment's first position
+      const long long x = lo - w.t0;
+      int c = static_cast<int>(x * shares / all);
+      while (c + 1 < shares && all * (c + 1) / shares <= x) ++c;
+      while (c > 0 && all * c / shares > x) --c;
+      part_from = c;
+    }
+    if (tid == 0) {
+      a.ends[blockIdx.x] = make_int4(part_from >= 0 ? w.g : -1, w.head, w.i, part_from);
+    }
+    if (w.count <= 0) more = next_segment(a, w);
+    w.index = 0;
+  } else if (tid == 0) {
+    a.ends[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
+  if (!busy) return;
+  const uint32_t tmem = misc.tmem;  // S_a +0, S_b +128, O_a +256, O_b +256+D
+  const int group = a.Hq / a.Hkv;
+
+  if (warp >= kFirstLoader && warp < kMmaWarp) {
+    // ------------------------------------------------------------ loads
+    // pages of a window's tiles: lane i has the row in the caches of the i-th slab, -1 where
+    // there is nothing; the window behind it is asked for when one is begun
+    const int slabs_per_page = a.page / kSlab, shift = 31 - __clz(slabs_per_page);
+    int found[3] = {-1, -1, -1}, window = -1;
+    uint32_t outside[3] = {0, 0, 0};  // slabs inside the sequence whose page is none
+    auto look_up = [&](int win, int& row, bool& out) {
+      const long long slab = static_cast<long long>(win) * 32 + lane;
+      row = -1;
+      out = false;
+      if (slab * kSlab >= w.s.keys) return;
+      const int j = static_cast<int>(slab >> shift);
+      const int at = a.row_of != nullptr ? a.row_of[w.g] : w.g;
+      const int pid = a.table[static_cast<size_t>(at) * a.max_pages + j];
+      if (pid < 0 || pid >= a.num_pages) {
+        out = true;
+        return;
+      }
+      row = (pid * a.Hkv + w.head / a.chunks) * a.page + (static_cast<int>(slab) & (slabs_per_page - 1)) * kSlab;
+    };
+    auto begin_windows = [&](int tile) {
+      window = tile / kWindow;
+      bool out;
+      found[0] = -1;
+      outside[0] = 0;
+      look_up(window, found[1], out);
+      outside[1] = __ballot_sync(0xffffffffu, out);
+      look_up(window + 1, found[2], out);
+      outside[2] = __ballot_sync(0xffffffffu, out);
+    };
+    // (tiles come in order; a V tile is at most two behind the last K tile)
+    auto to_window = [&](int tile) {
+      if (tile / kWindow > window) {
+        ++window;
+        found[0] = found[1], found[1] = found[2];
+        outside[0] = outside[1], outside[1] = outside[2];
+        bool out;
+        look_up(window + 1, found[2], out);
+        outside[2] = __ballot_sync(0xffffffffu, out);
+      }
+    };
+    int it = 0, step = 0;  // ring items and steps so far
+    if (!E4M3 && warp == kFirstLoader) {
+      // ---------------------------------------------------------- bf16: TMA
+      if (elect_one()) {
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+      }
+      __syncwarp();
+      const int boxes = BN / a.page;  // 1 to 8 pages of a tile, kSub boxes each
+      const int box = lane / L::kSub, sub = lane % L::kSub;
+      auto load = [&](int tile, bool is_k, int x, int at_step) -> bool {
+        const int st = it % NS;
+        if (it >= NS && !warp_wait(empty + st, (it / NS - 1) & 1, abort_flag, a.status)) return false;
+        if (is_k) to_window(tile);
+        const int behind = window - tile / kWindow;  // 0 or 1
+        const int slab0 = (tile % kWindow) * kSlabs;
+        const int row = __shfl_sync(0xffffffffu, behind ? found[0] : found[1], slab0 + (box < boxes ? box : 0) * slabs_per_page);
+        if (is_k) {
+          const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu;
+          if (lane == 0) {
+            misc.bad[at_step % kBadSlots][x] = static_cast<uint8_t>(out);
+            if (!w.single) misc.bad[at_step % kBadSlots][1 - x] = static_cast<uint8_t>(out);
+            if (out) atomicOr(a.status, DEV_BOUNDS);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(full + st, L::kTileBytes);
+        __syncwarp();
+        if (box < boxes)  // (a row past the tensor's end reads zeros)
+          tma_load_2d(ring + st * L::kTileBytes + sub * L::kSubBytes + box * a.page * 128, is_k ? &tk : &tv, sub * 64,
+                      row < 0 ? a.rows : row, full + st);
+        __syncwarp();
+        ++it;
+        return true;
+      };
+      bool ok = true;
+      for (; ok && more; more = next_segment(a, w)) {
+        begin_windows(tile_of(w, 0, 0));
+        if (w.index > 0) ok = warp_wait(q_empty, (w.index - 1) & 1, abort_flag, a.status);
+        if (!ok) break;
+        if (elect_one()) {
+          // a box is tokens x heads rows; tokens behind the sequence's are other ones' or zeros
+          const int units = w.single ? 1 : 2;
+          mbar_expect_tx(q_full, units * L::kSub * 128 * a.heads * a.tokens);
+          const int head = w.head / a.chunks * group + w.head % a.chunks * a.heads;
+          for (int u = 0; u < units; ++u)
+            for (int s = 0; s < L::kSub; ++s)
+              tma_load_3d(qs + u * L::kTileBytes + s * L::kSubBytes, &tq, s * 64, head, w.s.cu + (2 * w.i + u) * a.tokens, q_full);
+        }
+        __syncwarp();
+        if (w.single) {
+          ok = load(tile_of(w, 0, 0), true, 0, step);
+          if (ok && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step);
+        } else {
+          ok = load(tile_of(w, 0, 0), true, 0, step);
+        }
+        for (int j = 0; ok && j < w.count; ++j, ++step) {
+          if (a.fault && j >= 1) { ok = false; break; }  // test only: starve the MMA warp
+          for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
+            if (w.single ? has_tile(w, x, j) : true) ok = load(tile_of(w, x, j), false, x, step);
+            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ok = load(tile_of(w, x, j + 1), true, x, step + 1);
+          }
+        }
+      }
+      if (*abort_flag)
+        for (int i = max(it - NS, 0); i < it; ++i) drain_wait(full + i % NS, (i / NS) & 1);
+    } else if (!E4M3) {
+      // ---------------------------------------------------------- bf16: V tiles that masks cut
+      const int me = tid - 32 * (kFirstLoader + 1);
+      constexpr int kLook = 32 * (kLoaders - 1), kSegsRow = D / 8;
+      bool ok = true;
+      for (; ok && more; more = next_segment(a, w)) {
+        const int seen = seen_by_all(a, w);
+        bool begun = false;
+        it += w.single && has_tile(w, 1, 0) ? 2 : 1;
+        for (int j = 0; ok && j < w.count; ++j) {
+          for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
+            if (w.single ? has_tile(w, x, j) : true) {
+              const int tile = tile_of(w, x, j), st = it % NS;
+              if (look_through(seen, tile)) {
+                if (!begun && w.index >= 2)  // the record's last segment has been read
+                  ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
+                begun = true;
+                ok = ok && warp_wait(full + st, (it / NS) & 1, abort_flag, a.status);
+                if (!ok) break;
+                uint8_t* v = ring + st * L::kTileBytes;
+                for (int c = me; c < BN * kSegsRow; c += kLook) {
+                  const int r = c / kSegsRow, sg = c % kSegsRow;
+                  const long long key = static_cast<long long>(tile) * BN + r;
+                  uint8_t* at = v + swz_offset(r, sg);
+                  if (key >= w.s.keys) {
+                    st_shared16(at, make_uint4(0u, 0u, 0u, 0u));
+                    continue;
+                  }
+                  uint4 q = ld_shared16(at);
+                  uint32_t* u = reinterpret_cast<uint32_t*>(&q);
+                  uint32_t hit = 0;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                  if (hit == 0) continue;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const uint32_t m = (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+                    if ((u[e / 2] & m & 0x7F807F80u) == (m & 0x7F807F80u)) {
+                      u[e / 2] &= ~m;
+                      note_bad(records + (w.index & 1) * D, misc.any_bad + (w.index & 1), w, seen, sg * 8 + e, key);
+                    }
+                  }
+                  st_shared16(at, q);
+                }
+                fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
+                __syncwarp();
+                if (lane == 0) mbar_arrive(looked + st);
+              }
+              ++it;
+            }
+            if (j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ++it;
+          }
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- E4M3: cp.async and conversion
+      // Each item's rows are copied as bytes into the upper half of their own f16 lines in the
+      // item's stage; one item later the same lanes read them back, convert them (exact: every
+      // E4M3 value is an f16 value) and store the lines.  Only the lanes of a row touch it, all in
+      // one warp, so a __syncwarp between reads and writes orders them.
+      constexpr int kPT = 32 * kLoaders;
+      constexpr int kSegsRow = D / 8, kChunks = BM * kSegsRow, kPer = (kChunks + kPT - 1) / kPT;
+      constexpr int kCopySegs = D / 16, kRPI = 32 / kCopySegs, kRG = BN / kRPI;
+      constexpr int kGPW = (kRG + kLoaders - 1) / kLoaders;
+      const int pw = warp - kFirstLoader, me = pw * 32 + lane, sub = lane / kCopySegs, seg = lane % kCopySegs;
+      auto raw_at = [&](int i) { return (D == 128 ? BN * 128 : 64) + ((pw + kLoaders * i) * kRPI + sub) * 128 + seg * 16; };
+      int pend = -1, pend_tile = -1;  // item copied, not yet converted; its tile where it is a V tile to be looked through
+      auto convert = [&]() {
+        uint8_t* stage = ring + (pend % NS) * L::kTileBytes;
+        uint4 raw[kGPW];
+#pragma unroll
+        for (int i = 0; i < kGPW; ++i)
+          if (pw + kLoaders * i < kRG) raw[i] = ld_shared16(stage + raw_at(i));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kGPW; ++i) {
+          if (pw + kLoaders * i < kRG) {
+            const int r = (pw + kLoaders * i) * kRPI + sub;
+            if (pend_tile >= 0) {  // NaN codes (there are no infinities)
+              uint32_t* u = reinterpret_cast<uint32_t*>(&raw[i]);
+              uint32_t hit = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              if (hit != 0) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const uint32_t m = 0xFFu << (8 * (e & 3));
+                  if ((u[e / 4] & m & 0x7F7F7F7Fu) == (m & 0x7F7F7F7Fu)) {
+                    u[e / 4] &= ~m;
+                    note_bad(records + (w.index & 1) * D, misc.any_bad + (w.index & 1), w, seen_by_all(a, w), seg * 16 + e,
+                             static_cast<long long>(pend_tile) * BN + r);
+                  }
+                }
+              }
+            }
+            uint4 x, y;
+            e4m3x4_to_f16x4(raw[i].x, x.x, x.y);
+            e4m3x4_to_f16x4(raw[i].y, x.z, x.w);
+            e4m3x4_to_f16x4(raw[i].z, y.x, y.y);
+            e4m3x4_to_f16x4(raw[i].w, y.z, y.w);
+            st_shared16(stage + swz_offset(r, 2 * seg), x);
+            st_shared16(stage + swz_offset(r, 2 * seg + 1), y);
+          }
+        }
+        fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
+        mbar_arrive(full + pend % NS);
+        pend = -1;
+      };
+      auto load = [&](int tile, bool is_k, int x, int at_step, bool look) -> bool {
+        const int st = it % NS;
+        if (it >= NS && !warp_wait(empty + st, (it / NS - 1) & 1, abort_flag, a.status)) return false;
+        if (is_k) to_window(tile);
+        const int behind = window - tile / kWindow, slab0 = (tile % kWindow) * kSlabs;
+        const int rows = behind ? found[0] : found[1];
+        if (is_k && warp == kFirstLoader) {
+          const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu;
+          if (lane == 0) {
+            misc.bad[at_step % kBadSlots][x] = static_cast<uint8_t>(out);
+            if (!w.single) misc.bad[at_step % kBadSlots][1 - x] = static_cast<uint8_t>(out);
+            if (out) atomicOr(a.status, DEV_BOUNDS);
+          }
+        }
+        uint8_t* stage = ring + st * L::kTileBytes;
+        const uint8_t* src = static_cast<const uint8_t*>(is_k ? a.k : a.v);
+#pragma unroll
+        for (int i = 0; i < kGPW; ++i) {
+          const int rg = pw + kLoaders * i, r = rg * kRPI + sub;
+          const int base = __shfl_sync(0xffffffffu, rows, slab0 + (rg < kRG ? r / kSlab : 0));
+          if (rg < kRG) {  // rows that hold no token become zeros
+            const bool there = base >= 0 && static_cast<long long>(tile) * BN + r < w.s.keys;
+            cp_async16_zfill(stage + raw_at(i), src + static_cast<size_t>(there ? base + (r & (kSlab - 1)) : 0) * D + seg * 16, there);
+          }
+        }
+        cp_async_commit();
+        if (pend >= 0) {
+          cp_async_wait_group<1>();
+          convert();
+        }
+        pend = it++;
+        pend_tile = look ? tile : -1;
+        return true;
+      };
+      bool ok = true;
+      for (; ok && more; more = next_segment(a, w)) {
+        begin_windows(tile_of(w, 0, 0));
+        const int seen = seen_by_all(a, w);
+        if (w.index > 0) ok = warp_wait(q_empty, (w.index - 1) & 1, abort_flag, a.status);
+        if (ok && w.index >= 2 && look_through(seen, last_tile(w)))  // the record's last segment has been read
+          ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
+        if (!ok) break;
+        // queries: bf16 to f16 through registers, all loads of a unit first
+        const int chunk0 = w.head % a.chunks * a.heads, head = w.head / a.chunks * group + chunk0;
+        for (int u = 0; u < (w.single ? 1 : 2); ++u) {
+          uint4 qw[kPer];
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int c = me + kPT * k, r = c / kSegsRow, sg = c % kSegsRow;
+            const int t = r / a.heads, h = r - t * a.heads, tok = (2 * w.i + u) * a.tokens + t;
+            qw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < kChunks && t < a.tokens && tok < w.s.n && chunk0 + h < group)
+              qw[k] = ld_global16(a.q + static_cast<size_t>(w.s.cu + tok) * a.q_stride + static_cast<size_t>(head + h) * D + sg * 8);
+          }
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int c = me + kPT * k;
+            if (c < kChunks)
+              st_shared16(qs + u * L::kTileBytes + swz_offset(c / kSegsRow, c % kSegsRow),
+                          make_uint4(bf16x2_to_f16x2(qw[k].x), bf16x2_to_f16x2(qw[k].y), bf16x2_to_f16x2(qw[k].z),
+                                     bf16x2_to_f16x2(qw[k].w)));
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+        ok = load(tile_of(w, 0, 0), true, 0, step, false);
+        if (ok && w.single && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step, false);
+        for (int j = 0; ok && j < w.count; ++j, ++step) {
+          if (a.fault && j >= 1) { ok = false; break; }  // test only: starve the MMA warp
+          for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
+            if (w.single ? has_tile(w, x, j) : true)
+              ok = load(tile_of(w, x, j), false, x, step, look_through(seen, tile_of(w, x, j)));
+            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1)))
+              ok = load(tile_of(w, x, j + 1), true, x, step + 1, false);
+          }
+        }
+        // nothing of this segment waits for the next one's queries
+        cp_async_wait_group<0>();
+        if (ok && pend >= 0) convert();
+      }
+      cp_async_wait_group<0>();
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc_qk = E4M3 ? idesc_f16(BM, BN, false, false) : idesc_bf16(BM, BN, false, false);
+    constexpr uint32_t idesc_pv = E4M3 ? idesc_f16(BM, D, false, true) : idesc_bf16(BM, D, false, true);
+    const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(qs);
+    uint32_t look_parity = 0;  // of each stage's `looked`
+    int it = 0, step = 0;
+    auto stage_addr = [&](int item) { return ring_addr + (item % NS) * L::kTileBytes; };
+    auto wait_full = [&](int item) { return warp_wait(full + item % NS, (item / NS) & 1, abort_flag, a.status); };
+    auto wait_v = [&](int item, bool look) {
+      if (E4M3 || !look) return wait_full(item);
+      const int st = item % NS;
+      const bool ok = warp_wait(looked + st, (look_parity >> st) & 1, abort_flag, a.status);
+      look_parity ^= 1u << st;
+      return ok;
+    };
+    auto issue_qk = [&](int x, int item) {
+      const uint32_t kb = stage_addr(item), qb = q_addr + (w.single ? 0 : x) * L::kTileBytes;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * L::kSubBytes + (kk & 3) * 32;
+        umma_ss(tmem + x * 128, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int x, int item, bool first) {
+      const uint32_t vb = stage_addr(item);
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+        umma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 16 * 128, L::kSubBytes, 1024), idesc_pv,
+                (!first || kk > 0) ? 1u : 0u);
+    };
+    bool ok = true;
+    for (; ok && more; more = next_segment(a, w)) {
+      const int seen = seen_by_all(a, w);
+      int k_item[2];  // of the chains' next scores
+      ok = warp_wait(q_full, w.index & 1, abort_flag, a.status);
+      for (int x = 0; ok && x < 2; ++x) {
+        const bool mine = has_tile(w, x, 0);
+        if (x == 0 || w.single) {
+          if (x == 0 || mine) {
+            k_item[x] = it++;
+            ok = wait_full(k_item[x]);
+          }
+        } else {
+          k_item[1] = k_item[0];
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (mine) issue_qk(x, k_item[x]);
+          umma_commit(s_full + x);
+          if (w.single ? mine : x == 1) umma_commit(empty + k_item[x] % NS);
+          if (x == 1 && w.count == 1) umma_commit(q_empty);
+        }
+        __syncwarp();
+      }
+      int v_item = 0;
+      for (int j = 0; ok && j < w.count; ++j, ++step) {
+        const bool last = j + 1 == w.count;
+        for (int x = 0; ok && x < 2; ++x) {
+          const bool mine = has_tile(w, x, j), next = !last && has_tile(w, x, j + 1);
+          const bool loads_v = w.single ? mine : x == 0, loads_k = !last && (w.single ? next : x == 0);
+          if (loads_v) {
+            v_item = it++;
+            ok = wait_v(v_item, look_through(seen, tile_of(w, x, j)));
+          }
+          if (loads_k) {
+            k_item[x] = it++;
+            ok = ok && wait_full(k_item[x]);
+          } else if (!w.single) {
+            k_item[x] = k_item[0];
+          }
+          ok = ok && warp_wait(p_full + x, step & 1, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (mine) issue_pv(x, v_item, j == 0);
+            if (w.single ? mine : x == 1) umma_commit(empty + v_item % NS);
+            if (last) umma_commit(o_full + x);
+            if (!last) {
+              if (next) issue_qk(x, k_item[x]);
+              umma_commit(s_full + x);
+              if (w.single ? next : x == 1) umma_commit(empty + k_item[x] % NS);
+              if (x == 1 && j + 2 == w.count) umma_commit(q_empty);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (elect_one()) umma_commit(fin);
+    __syncwarp();
+    drain_wait(fin, 0);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + x * 128 + lane_off;
+    const uint32_t tO = tmem + 256 + x * D + lane_off;
+    const float sl2 = a.scale_log2;
+    const int row_t = row / a.heads, row_h = row - row_t * a.heads;
+    int step = 0;
+    uint32_t join_parity = 0;
+    bool ok = true;
+    for (; ok && more; more = next_segment(a, w)) {
+      // this thread's row: token, head, keys it sees
+      const int unit = 2 * w.i + (w.single ? 0 : x);
+      const long long tok = static_cast<long long>(unit) * a.tokens + row_t;
+      const int hh = w.head % a.chunks * a.heads + row_h;
+      const bool live = row_t < a.tokens && tok < w.s.n && hh < group;
+      const int limit = !live ? 0 : a.causal ? w.s.keys - w.s.n + static_cast<int>(tok) + 1 : w.s.keys;
+      const bool idle = __all_sync(0xffffffffu, !live);
+      float m_run = -INFINITY, l_f32 = 0.f, l_mul = 0.f;
+      for (int j = 0; j < w.count; ++j, ++step) {
+        if (!warp_wait(s_full + x, step & 1, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (idle || !has_tile(w, x, j)) {  // P of these rows is never read, or not used
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + x);
+          continue;
+        }
+        const long long ahead = limit - static_cast<long long>(tile_of(w, x, j)) * BN;
+        const int valid = static_cast<int>(max(min(ahead, static_cast<long long>(BN)), 0LL));
+        const uint32_t bad = misc.bad[step % kBadSlots][x];
+        const bool masked = bad != 0 || !__all_sync(0xffffffffu, valid == BN);
+        float s[64];
+        uint32_t* su = reinterpret_cast<uint32_t*>(s);
+        tmem_ld32(tS + 64, su);
+        tmem_ld32(tS + 96, su + 32);
+        tmem_ld_wait();
+        if (masked) mask64(s, 64, valid, bad);
+        const float mx_hi = max64(s);
+        tmem_ld32(tS + 0, su);
+        tmem_ld32(tS + 32, su + 32);
+        tmem_ld_wait();
+        if (masked) mask64(s, 0, valid, bad);
+        const float m_new = fmaxf(max64(s), mx_hi) * sl2;
+        // The reference maximum moves only when the tile's exceeds it by more than the
+        // threshold; TMEM loads and stores are the whole warp's, so all rows enter when one does.
+        const bool need = m_new > m_run + kThreshold<E4M3>;  // (the first maximum of a row, too)
+        if (__any_sync(0xffffffffu, need)) {
+          if (j > 0) {
+            const float f = need ? ex2(m_run - m_new) : 1.f;
+            l_f32 *= f;
+            l_mul *= f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + c * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f * __uint_as_float(o[i]));
+              tmem_st16(tO + c * 16, o);
+            }
+          }
+          if (need) m_run = m_new;
+        }
+        // p = 2^(s c - m).  Two row sums: the fp32 weights (lse) and the rounded ones the product
+        // multiplies by (the output is normalised by those, which keeps its error smaller).
+        const float m_ref = m_run == -INFINITY ? 0.f : m_run;
+        const uint64_t c2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_ref, -m_ref);
+        uint64_t accf[4] = {0ull, 0ull, 0ull, 0ull}, accb[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            tmem_ld32(tS + 64, su);
+            tmem_ld32(tS + 96, su + 32);
+            tmem_ld_wait();
+            if (masked) mask64(s, 64, valid, bad);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), c2, nm2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              pk[i] = E4M3 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+              accf[i & 3] = f2_add(accf[i & 3], f2_pack(p0, p1));
+              if constexpr (E4M3) {
+                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pk[i]));
+                accb[i & 3] = f2_add(accb[i & 3], f2_pack(r.x, r.y));
+              } else {
+                accb[i & 3] = f2_add(accb[i & 3], f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
+              }
+            }
+            tmem_st16(tS + h * 32 + c * 16, pk);
+          }
+        }
+        l_f32 += sum8(accf);
+        l_mul += sum8(accb);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + x);
+      }
+      // ---------------------------------------------------------- epilogue
+      if (ok) ok = warp_wait(o_full + x, w.index & 1, abort_flag, a.status);
+      if (!ok) break;
+      const bool had = has_tile(w, x, 0);  // this chain wrote O
+      float fa = 1.f, fb = 0.f;
+      if (w.single) {  // chain a joins the two
+        if (x == 1) {
+          s_ml[row] = m_run;
+          s_ml[BM + row] = l_mul;
+          s_ml[2 * BM + row] = l_f32;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(joined + (warp & 3));
+        } else {
+          ok = warp_wait(o_full + 1, w.index & 1, abort_flag, a.status) &&
+               warp_wait(joined + (warp & 3), join_parity, abort_flag, a.status);
+          if (!ok) break;
+          join_parity ^= 1;
+          const float m_b = s_ml[row], top = fmaxf(m_run, m_b);
+          fa = m_run == -INFINITY ? 0.f : ex2(m_run - top);
+          fb = m_b == -INFINITY ? 0.f : ex2(m_b - top);
+          // (sums of scores that are NaN stay NaN)
+          l_mul = fmaf(l_mul, fa, s_ml[BM + row] * fb);
+          l_f32 = fmaf(l_f32, fa, s_ml[2 * BM + row] * fb);
+          m_run = top;
+        }
+      }
+      tc_fence_after();
+      if (!idle && !(w.single && x == 1)) {
+        const bool b_too = w.single && has_tile(w, 1, 0);
+        const uint32_t tOb = tmem + 256 + D + lane_off;
+        const bool goes_on = w.t0 + w.count < w.steps, whole = w.t0 == 0 && !goes_on;
+        const size_t out_row = static_cast<size_t>(w.s.cu + static_cast<int>(tok)) * a.Hq + w.head / a.chunks * group + hh;
+        const bool finals = whole && a.whole == nullptr;
+        // (the value scale by itself: its quotient by the sum may be too small for a normal float)
+        const float inv = !finals ? 1.f : l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
+        float* part = nullptr;
+        if (!whole) {
+          part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (goes_on ? 1 : 0)) * part_floats(D);
+          const int r = x * BM + row;
+          if (live) reinterpret_cast<float4*>(part)[r] = make_float4(m_run, l_mul, l_f32, 0.f);
+          part += 4 * kPartRows + static_cast<size_t>(r) * D;
+        } else if (!finals) {
+          part = a.whole + 4 * static_cast<size_t>(a.T) * a.Hq + out_row * D;
+          if (live) reinterpret_cast<float4*>(a.whole)[out_row] = make_float4(m_run, l_mul, l_f32, 0.f);
+        }
+        const int seen = seen_by_all(a, w);
+        const bool spoiled = *static_cast<volatile uint32_t*>(misc.any_bad + (w.index & 1)) == bad_mark(w.index);
+        const uint32_t* record = records + (w.index & 1) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          float v[32];
+          if (had) {
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * fa;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+          if (b_too) {
+            tmem_ld32(tOb + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), fb, v[i]);
+          }
+          if (live) {
+            if (spoiled) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (first_bad(record, w, seen, c * 32 + i) < limit) v[i] = NAN;
+            }
+            if (finals) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c * 32);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = E4M3 ? v[i] * inv * a.v_scale : v[i] * inv;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                                    pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + c * 32);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+          }
+          __syncwarp();  // TMEM loads are the whole warp's
+        }
+        if (finals && live && a.lse != nullptr)
+          a.lse[out_row] = l_f32 == 0.f ? -INFINITY : (m_run + log2f(l_f32)) * 0.6931471805599453f;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(written + (w.index & 1));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the segment that ends in share blockIdx.x / kJoinBlocks and begins in an
+// earlier one, in the order of the shares: kJoinRows rows per block, 8 threads to a row.
+constexpr int kJoinRows = 32;
+constexpr int kJoinBlocks = kPartRows / kJoinRows;
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(8 * kJoinRows) paged_attn_join_kernel(const PagedAttnArgs a) {
+  pdl_begin();
+  const int c1 = blockIdx.x / kJoinBlocks, r = blockIdx.x % kJoinBlocks * kJoinRows + threadIdx.x / 8, t = threadIdx.x % 8;
+  const int4 end = a.ends[c1];
+  if (end.x < 0) return;
+  Seq s;
+  load_seq(a, end.x, s, false);
+  const int group = a.Hq / a.Hkv, pairs = units_of(a, s) / 2;
+  const int row = r % BM, row_t = row / a.heads, hh = end.y % a.chunks * a.heads + row - row_t * a.heads;
+  const long long tok = static_cast<long long>(2 * end.z + r / BM) * a.tokens + row_t;
+  if (row_t >= a.tokens || tok >= s.n || hh >= group || (end.z >= pairs && r >= BM)) return;
+  const int c0 = end.w;
+  auto part = [&](int c) { return a.parts + (2 * static_cast<size_t>(c) + (c < c1 ? 1 : 0)) * part_floats(D); };
+  float top = -INFINITY;
+  for (int c = c0; c <= c1; ++c) top = fmaxf(top, reinterpret_cast<const float4*>(part(c))[r].x);
+  float l_mul = 0.f, l_f32 = 0.f;
+  float4 acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    const float* p = part(c);
+    const float4 ml = reinterpret_cast<const float4*>(p)[r];
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);  // (sums of scores that are NaN stay NaN)
+    l_mul = fmaf(ml.y, f, l_mul);
+    l_f32 = fmaf(ml.z, f, l_f32);
+    const float4* o = reinterpret_cast<const float4*>(p + 4 * kPartRows + static_cast<size_t>(r) * D);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const float4 v = o[t + 8 * i];
+      acc[i].x = fmaf(v.x, f, acc[i].x);
+      acc[i].y = fmaf(v.y, f, acc[i].y);
+      acc[i].z = fmaf(v.z, f, acc[i].z);
+      acc[i].w = fmaf(v.w, f, acc[i].w);
+    }
+  }
+  const size_t out_row = static_cast<size_t>(s.cu + static_cast<int>(tok)) * a.Hq + end.y / a.chunks * group + hh;
+  const float inv = l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    float4 y = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+    if (E4M3) y.x *= a.v_scale, y.y *= a.v_scale, y.z *= a.v_scale, y.w *= a.v_scale;
+    *reinterpret_cast<uint2*>(a.out + out_row * D + 4 * (t + 8 * i)) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+  }
+  if (t == 0 && a.lse != nullptr)
+    a.lse[out_row] = l_f32 == 0.f ? -INFINITY : (top + log2f(l_f32)) * 0.6931471805599453f;
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, int grid,
+                   cudaStream_t stream) {
+  auto kernel = paged_attn_kernel<D, E4M3>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_dependent(kernel, grid, kThreads, Layout<D>::kSmem, stream, *tq, *tk, *tv, a)) != cudaSuccess) return e;
+  if (a.whole != nullptr) return cudaSuccess;  // joined with what the caller adds
+  return launch_dependent(paged_attn_join_kernel<D, E4M3>, grid * kJoinBlocks, 8 * kJoinRows, 0, stream, a);
+}
+
+}  // namespace
+
+size_t paged_attn_parts_bytes(int D) { return 2 * kMaxSms * part_floats(D) * sizeof(float); }
+size_t paged_attn_ends_bytes() { return kMaxSms * sizeof(int4); }
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
+                              bool e4m3, cudaStream_t stream) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(sms, kMaxSms);
+  if (a.D == 128)
+    return e4m3 ? launch<128, true>(a, tq, tk, tv, grid, stream) : launch<128, false>(a, tq, tk, tv, grid, stream);
+  return e4m3 ? launch<64, true>(a, tq, tk, tv, grid, stream) : launch<64, false>(a, tq, tk, tv, grid, stream);
+}
+
+}  // namespace mcs

@@ -27,7 +27,8 @@ __all__ = [
     "mcs_sparse_attn_pairs", "mcs_sparse_attn_pairs_record", "mcs_quantize_e4m3",
     "mcs_sparse_attn_e4m3", "Paged", "paged", "KV_BF16", "KV_E4M3", "mcs_paged_plan",
     "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
-    "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse", "Rope",
+    "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
+    "mcs_paged_attn_workspace", "mcs_paged_attn", "Rope",
     "rope_params", "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace",
     "mcs_qk_norm_rope_backward",
 ]
@@ -45,6 +46,7 @@ EXPORTED = (
     "mcs_quantize_e4m3", "mcs_sparse_attn_e4m3",
     "mcs_paged_plan", "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
     "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
+    "mcs_paged_attn_workspace", "mcs_paged_attn",
     "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace", "mcs_qk_norm_rope_backward",
 )
 
@@ -171,6 +173,8 @@ _SIGS = {
     "mcs_paged_select": ([_gp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp], _st),
     "mcs_paged_decode_sparse": ([_gp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp],
                                 _st),
+    "mcs_paged_attn_workspace": ([_gp], _sz),
+    "mcs_paged_attn": ([_gp, _i] + [_vp] * 9 + [_sz, _vp], _st),
     "mcs_qk_norm_rope": ([_rp] + [_vp] * 10, _st),
     "mcs_qk_norm_rope_backward_workspace": ([_rp], _sz),
     "mcs_qk_norm_rope_backward": ([_rp] + [_vp] * 14 + [_sz, _vp], _st),
@@ -720,6 +724,29 @@ def mcs_paged_decode_sparse(p: Paged, q, k_cache, v_cache, block_table, lens, se
         _at(dev, lens, _I32, (B,), "lens"), _at(dev, sel, _I32, (B, Hkv, keep), "sel"), keep,
         _at(dev, out, _BF, rows, "out"), None if lse is None else _at(dev, lse, _F32, (B, Hq), "lse"),
         *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_paged_decode_sparse")
+
+
+def mcs_paged_attn_workspace(p: Paged) -> int:
+    return lib().mcs_paged_attn_workspace(ctypes.byref(p))
+
+
+def mcs_paged_attn(p: Paged, q, k_cache, v_cache, block_table, lens, cu_new, out, ws, lse=None,
+                   stream=None):
+    """q, out [T, Hq, D]: the new tokens of all sequences, one behind another."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, Hq, D] tensor")
+    T = _count(q.shape[0], "q")
+    dev, B, Hq, D, kv = _device(stream), p.B, p.Hq, p.D, p.kv
+    cache, rows = (p.num_pages, p.Hkv, p.page, D), (T, Hq, D)
+    _check(lib().mcs_paged_attn(
+        ctypes.byref(p), T, _rows_at(dev, q, _BF, rows, p.q_stride, "q"),
+        _cache_at(dev, k_cache, kv, cache, "k_cache"),
+        _cache_at(dev, v_cache, kv, cache, "v_cache"),
+        _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
+        _at(dev, lens, _I32, (B,), "lens"), _at(dev, cu_new, _I32, (B + 1,), "cu_new"),
+        _at(dev, out, _BF, rows, "out"),
+        None if lse is None else _at(dev, lse, _F32, (T, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
+        _queue(stream, dev)), "mcs_paged_attn")
 
 
 # ---------------------------------------------------------------- norm and rotation
