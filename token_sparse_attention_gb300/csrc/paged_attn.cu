@@ -70,11 +70,11 @@ struct Layout {
   static constexpr int kStages = D == 128 ? 5 : 12;
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kBars = kRing + kStages * kTileBytes;
-  static constexpr int kNumBars = 3 * kStages + 16;
+  static constexpr int kNumBars = 4 * kStages + 16;
   static constexpr int kBadKey = kBars + kNumBars * 8;           // [2][D] words
   static constexpr int kMl = kBadKey + 2 * D * 4;                // [3][128] floats
   static constexpr int kMisc = kMl + 3 * BM * 4;                 // Misc
-  static constexpr int kSmem = kMisc + 256;
+  static constexpr int kSmem = kMisc + 208;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages <= kBadSlots, "bad slots");
 };
@@ -196,6 +196,11 @@ __device__ __forceinline__ bool has_tile(const Walk& w, int x, int j) {
 __device__ __forceinline__ int seen_by_all(const PagedAttnArgs& a, const Walk& w) {
   return a.causal ? w.s.keys - w.s.n + 2 * w.i * a.tokens + 1 : w.s.keys;
 }
+// In how many steps of the share's part chain x has a tile (the first ones).
+__device__ __forceinline__ int steps_of(const Walk& w, int x) {
+  const int all = w.single ? (w.tiles - x + 1) / 2 : x == 0 ? w.tiles_a : w.tiles;
+  return max(0, min(w.count, all - w.t0));
+}
 __device__ __forceinline__ int last_tile(const Walk& w) { return min(tile_of(w, w.single ? 1 : 0, w.count - 1), w.tiles - 1); }
 __device__ __forceinline__ bool look_through(int seen, int tile) { return (tile + 1) * static_cast<long long>(BN) > seen; }
 
@@ -236,11 +241,20 @@ __device__ __forceinline__ float max64(const float* s) {
 __device__ __forceinline__ int swz_offset(int r, int seg) {
   return (seg >> 3) * (BN * 128) + r * 128 + (((seg & 7) ^ (r & 7)) << 4);
 }
-// Columns of 64 scores, from column c0 of the tile, that the row does not see become -inf.
-__device__ __forceinline__ void mask64(float* s, int c0, int valid, uint32_t bad) {
+// Scores that the row does not see become -inf where they stand (TMEM): keys from `valid` on and
+// slabs of pages outside the cache.  Few tiles have any; the others' path holds no mask.
+__device__ __noinline__ void mask_scores(uint32_t tS, int valid, uint32_t bad) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < BN; c0 += 32) {
+    uint32_t s[32];
+    tmem_ld32(tS + c0, s);
+    tmem_ld_wait();
 #pragma unroll
-  for (int c = 0; c < 64; ++c)
-    if (c + c0 >= valid || ((bad >> ((c + c0) / kSlab)) & 1u)) s[c] = -INFINITY;
+    for (int c = 0; c < 32; ++c)
+      if (c0 + c >= valid || ((bad >> ((c0 + c) / kSlab)) & 1u)) s[c] = 0xFF800000u;
+    tmem_st32(tS + c0, s);
+  }
+  tmem_st_wait();
 }
 
 // Values that are not finite in tiles that are looked through: per column the first key, as
@@ -249,10 +263,30 @@ __device__ __forceinline__ void mask64(float* s, int c0, int valid, uint32_t bad
 // segments' records stand side by side; a third waits until the first one's rows are written.
 // The tiles of a segment that are looked through hold fewer than 128 + 256 + 128 keys.
 __device__ __forceinline__ uint32_t bad_mark(int index) { return (static_cast<uint32_t>(index + 1) & 0x3FFFFFu) << 10; }
-__device__ __forceinline__ void note_bad(uint32_t* record, volatile uint32_t* any, const Walk& w, int seen, int col, long long key) {
-  const int first = seen / BN * BN;
-  atomicMax(record + col, bad_mark(w.index) | (1023u - static_cast<uint32_t>(key - first)));
-  *any = bad_mark(w.index);
+// Notes the bf16 (or E4M3) values of 16 bytes that are not finite, of key `rel` from the first such
+// tile's first on, and makes them zero.
+template <bool E4M3>
+__device__ __noinline__ uint4 note_bad(uint4 v, uint32_t* record, volatile uint32_t* any, uint32_t mark, int rel) {
+  constexpr int kPerWord = E4M3 ? 4 : 2, kBits = 32 / kPerWord;
+  constexpr uint32_t kValue = E4M3 ? 0xFFu : 0xFFFFu, kNot = E4M3 ? 0x7Fu : 0x7F80u;
+  uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll 1
+    for (int k = 0; k < kPerWord; ++k) {
+      if (((u[e] >> (k * kBits)) & kNot) != kNot) continue;
+      u[e] &= ~(kValue << (k * kBits));
+      atomicMax(record + e * kPerWord + k, mark | (1023u - static_cast<uint32_t>(rel)));
+      *any = mark;
+    }
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+template <bool E4M3>
+__device__ __forceinline__ bool has_bad(uint4 v) {
+  constexpr uint32_t kNot = E4M3 ? 0x7F7F7F7Fu : 0x7F807F80u, kOne = E4M3 ? 0x01010101u : 0x00800080u;
+  constexpr uint32_t kTop = E4M3 ? 0x80808080u : 0x80008000u;
+  return ((((v.x & kNot) + kOne) | ((v.y & kNot) + kOne) | ((v.z & kNot) + kOne) | ((v.w & kNot) + kOne)) & kTop) != 0;
 }
 // The first key of the column that is not finite (none: beyond every key).
 __device__ __forceinline__ int first_bad(const uint32_t* record, const Walk& w, int seen, int col) {
@@ -271,7 +305,7 @@ struct Misc {
     int g, head, i;
   } start;
 };
-static_assert(sizeof(Misc) <= 256, "misc");
+static_assert(sizeof(Misc) <= 208, "misc");
 
 // Parts of segments that cross shares: slot 2 c of share c for a segment that ends there, 2 c + 1
 // for one that goes on.  (log2 maximum, sum of the weights as multiplied, their fp32 sum, 0) of
@@ -292,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + L::kRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [NS] stage loaded
   uint64_t* empty = full + NS;                                   // [NS] stage read
-  uint64_t* looked = empty + NS;                                 // [NS] V tile looked through (bf16)
+  uint64_t* raw = empty + NS;                                    // [NS] V tile to be looked through loaded (bf16)
+  uint64_t* looked = raw + NS;                                   // [NS] and looked through
   uint64_t* q_full = looked + NS;                                // queries loaded
   uint64_t* q_empty = q_full + 1;                                // the segment's last scores written
   uint64_t* s_full = q_empty + 1;                                // [2] S_x written
@@ -311,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < NS; ++s) {
       mbar_init(full + s, E4M3 ? 32 * kLoaders : 1);
       mbar_init(empty + s, 1);
+      mbar_init(raw + s, 1);
       mbar_init(looked + s, kLoaders - 1);
     }
     mbar_init(q_full, E4M3 ? 32 * kLoaders : 1);
@@ -329,6 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (tid < 2 * D) records[tid] = 0;
+  if (!E4M3 && a.heads * a.tokens < BM) {  // rows of the query tiles that no load fills
+    for (int i = tid; i < 2 * L::kTileBytes / 16; i += kThreads) st_shared16(qs + 16 * i, make_uint4(0u, 0u, 0u, 0u));
+    fence_proxy_async_smem();
+  }
   pdl_begin();
 
   // ---- this CTA's share: thread t sums sequences [t * per, (t + 1) * per)
@@ -497,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       const int boxes = BN / a.page;  // 1 to 8 pages of a tile, kSub boxes each
       const int box = lane / L::kSub, sub = lane % L::kSub;
-      auto load = [&](int tile, bool is_k, int x, int at_step) -> bool {
+      uint32_t raw_used = 0, raw_parity = 0;  // of each stage: a tile went to `raw`; the last one's parity
+      auto load = [&](int tile, bool is_k, int x, int at_step, bool look) -> bool {
         const int st = it % NS;
         if (it >= NS && !warp_wait(empty + st, (it / NS - 1) & 1, abort_flag, a.status)) return false;
         if (is_k) to_window(tile);
@@ -513,17 +554,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(full + st, L::kTileBytes);
+        // `full` keeps its turn: tiles to be looked through complete it empty
+        if (lane == 0) {
+          mbar_expect_tx((look ? raw : full) + st, L::kTileBytes);
+          if (look) mbar_arrive(full + st);
+        }
+        if (look) {
+          raw_parity ^= ((raw_used >> st) & 1u) << st;
+          raw_used |= 1u << st;
+        }
         __syncwarp();
         if (box < boxes)  // (a row past the tensor's end reads zeros)
           tma_load_2d(ring + st * L::kTileBytes + sub * L::kSubBytes + box * a.page * 128, is_k ? &tk : &tv, sub * 64,
-                      row < 0 ? a.rows : row, full + st);
+                      row < 0 ? a.rows : row, (look ? raw : full) + st);
         __syncwarp();
         ++it;
         return true;
       };
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
+        const int seen = seen_by_all(a, w);
         begin_windows(tile_of(w, 0, 0));
         if (w.index > 0) ok = warp_wait(q_empty, (w.index - 1) & 1, abort_flag, a.status);
         if (!ok) break;
@@ -538,25 +588,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (w.single) {
-          ok = load(tile_of(w, 0, 0), true, 0, step);
-          if (ok && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step);
+          ok = load(tile_of(w, 0, 0), true, 0, step, false);
+          if (ok && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step, false);
         } else {
-          ok = load(tile_of(w, 0, 0), true, 0, step);
+          ok = load(tile_of(w, 0, 0), true, 0, step, false);
         }
         for (int j = 0; ok && j < w.count; ++j, ++step) {
           if (a.fault && j >= 1) { ok = false; break; }  // test only: starve the MMA warp
           for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
-            if (w.single ? has_tile(w, x, j) : true) ok = load(tile_of(w, x, j), false, x, step);
-            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ok = load(tile_of(w, x, j + 1), true, x, step + 1);
+            if (w.single ? has_tile(w, x, j) : true)
+              ok = load(tile_of(w, x, j), false, x, step, look_through(seen, tile_of(w, x, j)));
+            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1)))
+              ok = load(tile_of(w, x, j + 1), true, x, step + 1, false);
           }
         }
       }
       if (*abort_flag)
-        for (int i = max(it - NS, 0); i < it; ++i) drain_wait(full + i % NS, (i / NS) & 1);
+        for (int i = max(it - NS, 0); i < it; ++i) {
+          drain_wait(full + i % NS, (i / NS) & 1);
+          if ((raw_used >> (i % NS)) & 1u) drain_wait(raw + i % NS, (raw_parity >> (i % NS)) & 1u);
+        }
     } else if (!E4M3) {
       // ---------------------------------------------------------- bf16: V tiles that masks cut
       const int me = tid - 32 * (kFirstLoader + 1);
       constexpr int kLook = 32 * (kLoaders - 1), kSegsRow = D / 8;
+      uint32_t raw_parity = 0;  // of each stage
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
         const int seen = seen_by_all(a, w);
@@ -570,8 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!begun && w.index >= 2)  // the record's last segment has been read
                   ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
                 begun = true;
-                ok = ok && warp_wait(full + st, (it / NS) & 1, abort_flag, a.status);
+                ok = ok && warp_wait(raw + st, (raw_parity >> st) & 1u, abort_flag, a.status);
                 if (!ok) break;
+                raw_parity ^= 1u << st;
                 uint8_t* v = ring + st * L::kTileBytes;
                 for (int c = me; c < BN * kSegsRow; c += kLook) {
                   const int r = c / kSegsRow, sg = c % kSegsRow;
@@ -582,19 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                   }
                   uint4 q = ld_shared16(at);
-                  uint32_t* u = reinterpret_cast<uint32_t*>(&q);
-                  uint32_t hit = 0;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                  if (hit == 0) continue;
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const uint32_t m = (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-                    if ((u[e / 2] & m & 0x7F807F80u) == (m & 0x7F807F80u)) {
-                      u[e / 2] &= ~m;
-                      note_bad(records + (w.index & 1) * D, misc.any_bad + (w.index & 1), w, seen, sg * 8 + e, key);
-                    }
-                  }
+                  if (!has_bad<false>(q)) continue;
+                  q = note_bad<false>(q, records + (w.index & 1) * D + sg * 8, misc.any_bad + (w.index & 1), bad_mark(w.index),
+                                      static_cast<int>(key - seen / BN * BN));
                   st_shared16(at, q);
                 }
                 fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
@@ -619,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kGPW = (kRG + kLoaders - 1) / kLoaders;
       const int pw = warp - kFirstLoader, me = pw * 32 + lane, sub = lane / kCopySegs, seg = lane % kCopySegs;
       auto raw_at = [&](int i) { return (D == 128 ? BN * 128 : 64) + ((pw + kLoaders * i) * kRPI + sub) * 128 + seg * 16; };
-      int pend = -1, pend_tile = -1;  // item copied, not yet converted; its tile where it is a V tile to be looked through
+      // item copied, not yet converted; where it is a V tile to be looked through its first key (see note_bad)
+      int pend = -1, pend_rel = -1;
       auto convert = [&]() {
         uint8_t* stage = ring + (pend % NS) * L::kTileBytes;
         uint4 raw[kGPW];
@@ -631,23 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kGPW; ++i) {
           if (pw + kLoaders * i < kRG) {
             const int r = (pw + kLoaders * i) * kRPI + sub;
-            if (pend_tile >= 0) {  // NaN codes (there are no infinities)
-              uint32_t* u = reinterpret_cast<uint32_t*>(&raw[i]);
-              uint32_t hit = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-              if (hit != 0) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const uint32_t m = 0xFFu << (8 * (e & 3));
-                  if ((u[e / 4] & m & 0x7F7F7F7Fu) == (m & 0x7F7F7F7Fu)) {
-                    u[e / 4] &= ~m;
-                    note_bad(records + (w.index & 1) * D, misc.any_bad + (w.index & 1), w, seen_by_all(a, w), seg * 16 + e,
-                             static_cast<long long>(pend_tile) * BN + r);
-                  }
-                }
-              }
-            }
+            if (pend_rel >= 0 && has_bad<true>(raw[i]))  // NaN codes (there are no infinities)
+              raw[i] = note_bad<true>(raw[i], records + (w.index & 1) * D + seg * 16, misc.any_bad + (w.index & 1),
+                                      bad_mark(w.index), pend_rel + r);
             uint4 x, y;
             e4m3x4_to_f16x4(raw[i].x, x.x, x.y);
             e4m3x4_to_f16x4(raw[i].y, x.z, x.w);
@@ -661,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(full + pend % NS);
         pend = -1;
       };
-      auto load = [&](int tile, bool is_k, int x, int at_step, bool look) -> bool {
+      auto load = [&](int tile, bool is_k, int x, int at_step, int rel) -> bool {
         const int st = it % NS;
         if (it >= NS && !warp_wait(empty + st, (it / NS - 1) & 1, abort_flag, a.status)) return false;
         if (is_k) to_window(tile);
@@ -692,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           convert();
         }
         pend = it++;
-        pend_tile = look ? tile : -1;
+        pend_rel = rel;
         return true;
       };
       bool ok = true;
@@ -726,15 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         mbar_arrive(q_full);
-        ok = load(tile_of(w, 0, 0), true, 0, step, false);
-        if (ok && w.single && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step, false);
+        ok = load(tile_of(w, 0, 0), true, 0, step, -1);
+        if (ok && w.single && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step, -1);
         for (int j = 0; ok && j < w.count; ++j, ++step) {
           if (a.fault && j >= 1) { ok = false; break; }  // test only: starve the MMA warp
           for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
             if (w.single ? has_tile(w, x, j) : true)
-              ok = load(tile_of(w, x, j), false, x, step, look_through(seen, tile_of(w, x, j)));
+              ok = load(tile_of(w, x, j), false, x, step, look_through(seen, tile_of(w, x, j)) ? tile_of(w, x, j) * BN - seen / BN * BN : -1);
             if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1)))
-              ok = load(tile_of(w, x, j + 1), true, x, step + 1, false);
+              ok = load(tile_of(w, x, j + 1), true, x, step + 1, -1);
           }
         }
         // nothing of this segment waits for the next one's queries
@@ -752,8 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0, step = 0;
     auto stage_addr = [&](int item) { return ring_addr + (item % NS) * L::kTileBytes; };
     auto wait_full = [&](int item) { return warp_wait(full + item % NS, (item / NS) & 1, abort_flag, a.status); };
-    auto wait_v = [&](int item, bool look) {
-      if (E4M3 || !look) return wait_full(item);
+    auto wait_looked = [&](int item) {
       const int st = item % NS;
       const bool ok = warp_wait(looked + st, (look_parity >> st) & 1, abort_flag, a.status);
       look_parity ^= 1u << st;
@@ -805,17 +838,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; ok && x < 2; ++x) {
           const bool mine = has_tile(w, x, j), next = !last && has_tile(w, x, j + 1);
           const bool loads_v = w.single ? mine : x == 0, loads_k = !last && (w.single ? next : x == 0);
-          if (loads_v) {
-            v_item = it++;
-            ok = wait_v(v_item, look_through(seen, tile_of(w, x, j)));
-          }
-          if (loads_k) {
+          // the batch's barriers are looked at together; only if one is not complete, each in turn
+          const bool look = loads_v && look_through(seen, tile_of(w, x, j));
+          if (loads_v) v_item = it++;
+          if (loads_k)
             k_item[x] = it++;
-            ok = ok && wait_full(k_item[x]);
-          } else if (!w.single) {
+          else if (!w.single)
             k_item[x] = k_item[0];
+          bool ready = mbar_try_wait(p_full + x, step & 1);
+          if (loads_v && (E4M3 || !look)) ready &= mbar_try_wait(full + v_item % NS, (v_item / NS) & 1);
+          if (loads_k) ready &= mbar_try_wait(full + k_item[x] % NS, (k_item[x] / NS) & 1);
+          if (!__all_sync(0xffffffffu, ready)) {
+            if (loads_v && (E4M3 || !look)) ok = wait_full(v_item);
+            if (loads_k) ok = ok && wait_full(k_item[x]);
+            ok = ok && warp_wait(p_full + x, step & 1, abort_flag, a.status);
           }
-          ok = ok && warp_wait(p_full + x, step & 1, abort_flag, a.status);
+          if (!E4M3 && look) ok = ok && wait_looked(v_item);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -854,36 +892,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long tok = static_cast<long long>(unit) * a.tokens + row_t;
       const int hh = w.head % a.chunks * a.heads + row_h;
       const bool live = row_t < a.tokens && tok < w.s.n && hh < group;
-      const int limit = !live ? 0 : a.causal ? w.s.keys - w.s.n + static_cast<int>(tok) + 1 : w.s.keys;
+      // (rows that are none see what every row sees: they cost no masks)
+      const int limit = live && a.causal ? w.s.keys - w.s.n + static_cast<int>(tok) + 1 : w.s.keys;
       const bool idle = __all_sync(0xffffffffu, !live);
+      const int mine = idle ? 0 : steps_of(w, x), count = w.count;
+      int ahead = limit - tile_of(w, x, 0) * BN;  // keys that the row sees from the tile's first on
+      const int stride = w.single ? 2 * BN : BN;
       float m_run = -INFINITY, l_f32 = 0.f, l_mul = 0.f;
-      for (int j = 0; j < w.count; ++j, ++step) {
+      for (int j = 0; j < count; ++j, ++step, ahead -= stride) {
         if (!warp_wait(s_full + x, step & 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (idle || !has_tile(w, x, j)) {  // P of these rows is never read, or not used
+        if (j >= mine) {  // P of these rows is never read, or not used
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full + x);
           continue;
         }
-        const long long ahead = limit - static_cast<long long>(tile_of(w, x, j)) * BN;
-        const int valid = static_cast<int>(max(min(ahead, static_cast<long long>(BN)), 0LL));
+        const int valid = ahead;
         const uint32_t bad = misc.bad[step % kBadSlots][x];
-        const bool masked = bad != 0 || !__all_sync(0xffffffffu, valid == BN);
+        if (bad != 0 || !__all_sync(0xffffffffu, valid >= BN)) mask_scores(tS, valid, bad);
         float s[64];
         uint32_t* su = reinterpret_cast<uint32_t*>(s);
         tmem_ld32(tS + 64, su);
         tmem_ld32(tS + 96, su + 32);
         tmem_ld_wait();
-        if (masked) mask64(s, 64, valid, bad);
         const float mx_hi = max64(s);
         tmem_ld32(tS + 0, su);
         tmem_ld32(tS + 32, su + 32);
         tmem_ld_wait();
-        if (masked) mask64(s, 0, valid, bad);
         const float m_new = fmaxf(max64(s), mx_hi) * sl2;
         // The reference maximum moves only when the tile's exceeds it by more than the
         // threshold; TMEM loads and stores are the whole warp's, so all rows enter when one does.
@@ -916,7 +955,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tS + 64, su);
             tmem_ld32(tS + 96, su + 32);
             tmem_ld_wait();
-            if (masked) mask64(s, 64, valid, bad);
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
