@@ -70,11 +70,17 @@ struct Layout {
   static constexpr int kStages = D == 128 ? 5 : 12;
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kBars = kRing + kStages * kTileBytes;
-  static constexpr int kNumBars = 4 * kStages + 16;
+  // MMA batches done, round robin.  A waiter reads the phase of batch n's barrier, which is
+  // unambiguous as long as batch n + kDone cannot be done yet.  Loads lag furthest: they wait for the
+  // last reader of the item kStages back, and what the kStages - 1 items behind it feed is at most
+  // three batches for every two (segments of one step), and three more.
+  static constexpr int kDone = D == 128 ? 16 : 32;
+  static_assert(kDone >= (kStages - 1) / 2 * 3 + 5, "batch barriers must outnumber the lag");
+  static constexpr int kNumBars = 3 * kStages + kDone + 10;
   static constexpr int kBadKey = kBars + kNumBars * 8;           // [2][D] words
   static constexpr int kMl = kBadKey + 2 * D * 4;                // [3][128] floats
   static constexpr int kMisc = kMl + 3 * BM * 4;                 // Misc
-  static constexpr int kSmem = kMisc + 208;
+  static constexpr int kSmem = kMisc + 80;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kStages <= kBadSlots, "bad slots");
 };
@@ -299,13 +305,12 @@ struct Misc {
   uint32_t tmem;
   int abort;
   uint32_t any_bad[2];
-  long long sums[kThreads / 32];
   struct {
     long long offset;
     int g, head, i;
   } start;
 };
-static_assert(sizeof(Misc) <= 208, "misc");
+static_assert(sizeof(Misc) <= 80, "misc");
 
 // Parts of segments that cross shares: slot 2 c of share c for a segment that ends there, 2 c + 1
 // for one that goes on.  (log2 maximum, sum of the weights as multiplied, their fp32 sum, 0) of
@@ -325,17 +330,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* qs = smem;
   uint8_t* ring = smem + L::kRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [NS] stage loaded
-  uint64_t* empty = full + NS;                                   // [NS] stage read
-  uint64_t* raw = empty + NS;                                    // [NS] V tile to be looked through loaded (bf16)
+  uint64_t* raw = full + NS;                                     // [NS] V tile to be looked through loaded (bf16)
   uint64_t* looked = raw + NS;                                   // [NS] and looked through
   uint64_t* q_full = looked + NS;                                // queries loaded
-  uint64_t* q_empty = q_full + 1;                                // the segment's last scores written
-  uint64_t* s_full = q_empty + 1;                                // [2] S_x written
-  uint64_t* p_full = s_full + 2;                                 // [2] P_x written
-  uint64_t* o_full = p_full + 2;                                 // [2] O_x of the segment final
-  uint64_t* joined = o_full + 2;                                 // [4] chain b's maxima and sums there
+  uint64_t* p_full = q_full + 1;                                 // [2] P_x written
+  uint64_t* joined = p_full + 2;                                 // [4] chain b's maxima and sums there
   uint64_t* written = joined + 4;                                // [2] epilogue of segment i done: written[i & 1]
   uint64_t* fin = written + 2;                                   // every MMA done
+  uint64_t* done = fin + 1;                                      // [kDone] MMA batch n done: done[n % kDone]
   uint32_t* records = reinterpret_cast<uint32_t*>(smem + L::kBadKey);  // [2][D]
   float* s_ml = reinterpret_cast<float*>(smem + L::kMl);         // chain b's maxima and sums
   Misc& misc = *reinterpret_cast<Misc*>(smem + L::kMisc);
@@ -345,21 +347,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full + s, E4M3 ? 32 * kLoaders : 1);
-      mbar_init(empty + s, 1);
       mbar_init(raw + s, 1);
       mbar_init(looked + s, kLoaders - 1);
     }
     mbar_init(q_full, E4M3 ? 32 * kLoaders : 1);
-    mbar_init(q_empty, 1);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(s_full + x, 1);
       mbar_init(p_full + x, 4);
-      mbar_init(o_full + x, 1);
       mbar_init(written + x, 8);
       misc.any_bad[x] = 0;
     }
     for (int x = 0; x < 4; ++x) mbar_init(joined + x, 1);
     mbar_init(fin, 1);
+    for (int n = 0; n < L::kDone; ++n) mbar_init(done + n, 1);
     *abort_flag = 0;
     misc.start.g = -1;
     fence_mbar_init();
@@ -380,18 +379,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (g < a.G && load_seq(a, g, s, blockIdx.x == 0)) own += positions_of(a, s);
   }
   long long upto = own;
+  long long* sums = reinterpret_cast<long long*>(s_ml);  // (not in use yet)
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += y;
   }
-  if (lane == 31) misc.sums[warp] = upto;
+  if (lane == 31) sums[warp] = upto;
   __syncthreads();
   long long all = 0;
 #pragma unroll
   for (int k = 0; k < kThreads / 32; ++k) {
-    if (k < warp) upto += misc.sums[k];
-    all += misc.sums[k];
+    if (k < warp) upto += sums[k];
+    all += sums[k];
   }
   if (blockIdx.x == 0 && a.places != nullptr) {  // where each sequence begins, for the join
     long long at = upto - own;
@@ -483,6 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!busy) return;
   const uint32_t tmem = misc.tmem;  // S_a +0, S_b +128, O_a +256, O_b +256+D
   const int group = a.Hq / a.Hkv;
+  // MMA batches of a segment, from number `base` on: base QK_a(0) QK_b(0); base + 2 j + x + 1
+  // PV_x(j) QK_x(j + 1).  Each ends in one commit, which signals every earlier MMA, too: it tells
+  // the softmax that S_x is there, the epilogue that O_x is final, the loads that tiles are read.
+  int base = 0;
+  auto wait_batch = [&](int n) { return warp_wait(done + n % L::kDone, (n / L::kDone) & 1, abort_flag, a.status); };
+  auto read_by = [&](bool is_k, int x, int j) {  // the last batch that reads the chain's tile of step j
+    return w.single ? (is_k ? (j == 0 ? base : base + 2 * j + x - 1) : base + 2 * j + x + 1) : base + 2 * j + (is_k ? 0 : 2);
+  };
 
   if (warp >= kFirstLoader && warp < kMmaWarp) {
     // ------------------------------------------------------------ loads
@@ -527,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     int it = 0, step = 0;  // ring items and steps so far
+    int reader = 0;        // lane i: the last batch that reads stage i
+    int q_reader = 0;      // the last batch that reads the queries
     if (!E4M3 && warp == kFirstLoader) {
       // ---------------------------------------------------------- bf16: TMA
       if (elect_one()) {
@@ -538,9 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int boxes = BN / a.page;  // 1 to 8 pages of a tile, kSub boxes each
       const int box = lane / L::kSub, sub = lane % L::kSub;
       uint32_t raw_used = 0, raw_parity = 0;  // of each stage: a tile went to `raw`; the last one's parity
-      auto load = [&](int tile, bool is_k, int x, int at_step, bool look) -> bool {
-        const int st = it % NS;
-        if (it >= NS && !warp_wait(empty + st, (it / NS - 1) & 1, abort_flag, a.status)) return false;
+      auto load = [&](bool is_k, int x, int j, bool look) -> bool {
+        const int st = it % NS, tile = tile_of(w, x, j);
+        if (it >= NS && !wait_batch(__shfl_sync(0xffffffffu, reader, st))) return false;
+        if (lane == st) reader = read_by(is_k, x, j);
         if (is_k) to_window(tile);
         const int behind = window - tile / kWindow;  // 0 or 1
         const int slab0 = (tile % kWindow) * kSlabs;
@@ -548,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_k) {
           const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu;
           if (lane == 0) {
-            misc.bad[at_step % kBadSlots][x] = static_cast<uint8_t>(out);
-            if (!w.single) misc.bad[at_step % kBadSlots][1 - x] = static_cast<uint8_t>(out);
+            misc.bad[(step + j) % kBadSlots][x] = static_cast<uint8_t>(out);
+            if (!w.single) misc.bad[(step + j) % kBadSlots][1 - x] = static_cast<uint8_t>(out);
             if (out) atomicOr(a.status, DEV_BOUNDS);
           }
         }
@@ -575,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && more; more = next_segment(a, w)) {
         const int seen = seen_by_all(a, w);
         begin_windows(tile_of(w, 0, 0));
-        if (w.index > 0) ok = warp_wait(q_empty, (w.index - 1) & 1, abort_flag, a.status);
+        if (w.index > 0) ok = wait_batch(q_reader);
         if (!ok) break;
         if (elect_one()) {
           // a box is tokens x heads rows; tokens behind the sequence's are other ones' or zeros
@@ -587,21 +598,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(qs + u * L::kTileBytes + s * L::kSubBytes, &tq, s * 64, head, w.s.cu + (2 * w.i + u) * a.tokens, q_full);
         }
         __syncwarp();
-        if (w.single) {
-          ok = load(tile_of(w, 0, 0), true, 0, step, false);
-          if (ok && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step, false);
-        } else {
-          ok = load(tile_of(w, 0, 0), true, 0, step, false);
-        }
-        for (int j = 0; ok && j < w.count; ++j, ++step) {
-          if (a.fault && j >= 1) { ok = false; break; }  // test only: starve the MMA warp
-          for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
-            if (w.single ? has_tile(w, x, j) : true)
-              ok = load(tile_of(w, x, j), false, x, step, look_through(seen, tile_of(w, x, j)));
-            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1)))
-              ok = load(tile_of(w, x, j + 1), true, x, step + 1, false);
+        const int xs = w.single ? 2 : 1;  // (a pair's tiles come with chain a)
+        for (int x = 0; ok && x < xs; ++x)
+          if (x == 0 || has_tile(w, x, 0)) ok = load(true, x, 0, false);
+        for (int j = 0; ok && j < w.count; ++j) {
+          if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
+          for (int x = 0; ok && x < xs; ++x) {
+            if (!w.single || has_tile(w, x, j)) ok = load(false, x, j, look_through(seen, tile_of(w, x, j)));
+            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ok = load(true, x, j + 1, false);
           }
         }
+        step += w.count;
+        q_reader = base + 2 * (w.count - 1);
+        base += 2 * w.count + 1;
       }
       if (*abort_flag)
         for (int i = max(it - NS, 0); i < it; ++i) {
@@ -666,74 +675,101 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kGPW = (kRG + kLoaders - 1) / kLoaders;
       const int pw = warp - kFirstLoader, me = pw * 32 + lane, sub = lane / kCopySegs, seg = lane % kCopySegs;
       auto raw_at = [&](int i) { return (D == 128 ? BN * 128 : 64) + ((pw + kLoaders * i) * kRPI + sub) * 128 + seg * 16; };
-      // item copied, not yet converted; where it is a V tile to be looked through its first key (see note_bad)
-      int pend = -1, pend_rel = -1;
+      // Items copied, not yet converted: the `pend` ones in front of `it`; of each, oldest first, where it is
+      // a V tile to be looked through, its first key (see note_bad), -1 otherwise.  Copies run as far
+      // ahead as stages are free: the oldest is converted once nothing else can be begun.
+      constexpr int kAhead = 3;
+      static_assert(kAhead <= NS - 2, "conversions must not wait on the batches they feed");
+      int pend = 0, rel[kAhead] = {-1, -1, -1};
       auto convert = [&]() {
-        uint8_t* stage = ring + (pend % NS) * L::kTileBytes;
-        uint4 raw[kGPW];
+        if (pend == 3)
+          cp_async_wait_group<2>();
+        else if (pend == 2)
+          cp_async_wait_group<1>();
+        else
+          cp_async_wait_group<0>();
+        const int st = (it - pend) % NS;
+        uint8_t* stage = ring + st * L::kTileBytes;
+        if (rel[0] >= 0) {
+#pragma unroll 1
+          for (int i = 0; i < kGPW; ++i) {
+            if (pw + kLoaders * i >= kRG) break;
+            const uint4 v = ld_shared16(stage + raw_at(i));
+            if (has_bad<true>(v))  // NaN codes (there are no infinities)
+              st_shared16(stage + raw_at(i), note_bad<true>(v, records + (w.index & 1) * D + seg * 16, misc.any_bad + (w.index & 1),
+                                                            bad_mark(w.index), rel[0] + (pw + kLoaders * i) * kRPI + sub));
+          }
+          __syncwarp();
+        }
+        uint4 v[kGPW];
 #pragma unroll
         for (int i = 0; i < kGPW; ++i)
-          if (pw + kLoaders * i < kRG) raw[i] = ld_shared16(stage + raw_at(i));
+          if (pw + kLoaders * i < kRG) v[i] = ld_shared16(stage + raw_at(i));
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < kGPW; ++i) {
           if (pw + kLoaders * i < kRG) {
             const int r = (pw + kLoaders * i) * kRPI + sub;
-            if (pend_rel >= 0 && has_bad<true>(raw[i]))  // NaN codes (there are no infinities)
-              raw[i] = note_bad<true>(raw[i], records + (w.index & 1) * D + seg * 16, misc.any_bad + (w.index & 1),
-                                      bad_mark(w.index), pend_rel + r);
             uint4 x, y;
-            e4m3x4_to_f16x4(raw[i].x, x.x, x.y);
-            e4m3x4_to_f16x4(raw[i].y, x.z, x.w);
-            e4m3x4_to_f16x4(raw[i].z, y.x, y.y);
-            e4m3x4_to_f16x4(raw[i].w, y.z, y.w);
+            e4m3x4_to_f16x4(v[i].x, x.x, x.y);
+            e4m3x4_to_f16x4(v[i].y, x.z, x.w);
+            e4m3x4_to_f16x4(v[i].z, y.x, y.y);
+            e4m3x4_to_f16x4(v[i].w, y.z, y.w);
             st_shared16(stage + swz_offset(r, 2 * seg), x);
             st_shared16(stage + swz_offset(r, 2 * seg + 1), y);
           }
         }
         fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
-        mbar_arrive(full + pend % NS);
-        pend = -1;
+        mbar_arrive(full + st);
+        --pend;
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) rel[i] = rel[i + 1];
       };
-      auto load = [&](int tile, bool is_k, int x, int at_step, int rel) -> bool {
-        const int st = it % NS;
-        if (it >= NS && !warp_wait(empty + st, (it / NS - 1) & 1, abort_flag, a.status)) return false;
+      auto load = [&](bool is_k, int x, int j, int look) -> bool {
+        const int st = it % NS, tile = tile_of(w, x, j);
+        if (pend == kAhead) convert();
+        if (it >= NS) {
+          const int n = __shfl_sync(0xffffffffu, reader, st);
+          while (pend > 0 && !__all_sync(0xffffffffu, mbar_try_wait(done + n % L::kDone, (n / L::kDone) & 1))) convert();
+          if (!wait_batch(n)) return false;
+        }
+        if (lane == st) reader = read_by(is_k, x, j);
         if (is_k) to_window(tile);
         const int behind = window - tile / kWindow, slab0 = (tile % kWindow) * kSlabs;
         const int rows = behind ? found[0] : found[1];
         if (is_k && warp == kFirstLoader) {
           const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu;
           if (lane == 0) {
-            misc.bad[at_step % kBadSlots][x] = static_cast<uint8_t>(out);
-            if (!w.single) misc.bad[at_step % kBadSlots][1 - x] = static_cast<uint8_t>(out);
+            misc.bad[(step + j) % kBadSlots][x] = static_cast<uint8_t>(out);
+            if (!w.single) misc.bad[(step + j) % kBadSlots][1 - x] = static_cast<uint8_t>(out);
             if (out) atomicOr(a.status, DEV_BOUNDS);
           }
         }
         uint8_t* stage = ring + st * L::kTileBytes;
         const uint8_t* src = static_cast<const uint8_t*>(is_k ? a.k : a.v);
+        const long long left = w.s.keys - static_cast<long long>(tile) * BN;
 #pragma unroll
         for (int i = 0; i < kGPW; ++i) {
           const int rg = pw + kLoaders * i, r = rg * kRPI + sub;
-          const int base = __shfl_sync(0xffffffffu, rows, slab0 + (rg < kRG ? r / kSlab : 0));
+          const int from = __shfl_sync(0xffffffffu, rows, slab0 + (rg < kRG ? r / kSlab : 0));
           if (rg < kRG) {  // rows that hold no token become zeros
-            const bool there = base >= 0 && static_cast<long long>(tile) * BN + r < w.s.keys;
-            cp_async16_zfill(stage + raw_at(i), src + static_cast<size_t>(there ? base + (r & (kSlab - 1)) : 0) * D + seg * 16, there);
+            const bool there = from >= 0 && r < left;
+            cp_async16_zfill(stage + raw_at(i), src + static_cast<size_t>(there ? from + (r & (kSlab - 1)) : 0) * D + seg * 16, there);
           }
         }
         cp_async_commit();
-        if (pend >= 0) {
-          cp_async_wait_group<1>();
-          convert();
-        }
-        pend = it++;
-        pend_rel = rel;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (i == pend) rel[i] = look;
+        ++pend;
+        ++it;
         return true;
       };
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
         begin_windows(tile_of(w, 0, 0));
         const int seen = seen_by_all(a, w);
-        if (w.index > 0) ok = warp_wait(q_empty, (w.index - 1) & 1, abort_flag, a.status);
+        if (w.index > 0) ok = wait_batch(q_reader);
         if (ok && w.index >= 2 && look_through(seen, last_tile(w)))  // the record's last segment has been read
           ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
         if (!ok) break;
@@ -760,20 +796,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         mbar_arrive(q_full);
-        ok = load(tile_of(w, 0, 0), true, 0, step, -1);
-        if (ok && w.single && has_tile(w, 1, 0)) ok = load(tile_of(w, 1, 0), true, 1, step, -1);
-        for (int j = 0; ok && j < w.count; ++j, ++step) {
-          if (a.fault && j >= 1) { ok = false; break; }  // test only: starve the MMA warp
-          for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
-            if (w.single ? has_tile(w, x, j) : true)
-              ok = load(tile_of(w, x, j), false, x, step, look_through(seen, tile_of(w, x, j)) ? tile_of(w, x, j) * BN - seen / BN * BN : -1);
-            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1)))
-              ok = load(tile_of(w, x, j + 1), true, x, step + 1, -1);
+        const int xs = w.single ? 2 : 1;  // (a pair's tiles come with chain a)
+        for (int x = 0; ok && x < xs; ++x)
+          if (x == 0 || has_tile(w, x, 0)) ok = load(true, x, 0, -1);
+        for (int j = 0; ok && j < w.count; ++j) {
+          if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
+          for (int x = 0; ok && x < xs; ++x) {
+            const int tile = tile_of(w, x, j);
+            if (!w.single || has_tile(w, x, j)) ok = load(false, x, j, look_through(seen, tile) ? (tile - seen / BN) * BN : -1);
+            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ok = load(true, x, j + 1, -1);
           }
         }
         // nothing of this segment waits for the next one's queries
-        cp_async_wait_group<0>();
-        if (ok && pend >= 0) convert();
+        while (ok && pend > 0) convert();
+        step += w.count;
+        q_reader = base + 2 * (w.count - 1);
+        base += 2 * w.count + 1;
       }
       cp_async_wait_group<0>();
     }
@@ -781,27 +819,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idesc_qk = E4M3 ? idesc_f16(BM, BN, false, false) : idesc_bf16(BM, BN, false, false);
     constexpr uint32_t idesc_pv = E4M3 ? idesc_f16(BM, D, false, true) : idesc_bf16(BM, D, false, true);
+    // The tensor core holds one or two MMAs ahead and the issue of a batch ends as its last ones
+    // begin: whatever stands between that and the next batch's issue leaves it idle.  So stages,
+    // parities and barriers of the next batch are worked out in front of the present one's issue.
     const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(qs);
-    uint32_t look_parity = 0;  // of each stage's `looked`
-    int it = 0, step = 0;
-    auto stage_addr = [&](int item) { return ring_addr + (item % NS) * L::kTileBytes; };
-    auto wait_full = [&](int item) { return warp_wait(full + item % NS, (item / NS) & 1, abort_flag, a.status); };
-    auto wait_looked = [&](int item) {
-      const int st = item % NS;
-      const bool ok = warp_wait(looked + st, (look_parity >> st) & 1, abort_flag, a.status);
-      look_parity ^= 1u << st;
-      return ok;
+    uint32_t look_parity = 0;       // of each stage's `looked`
+    int next_st = 0, dn = 0;        // the next ring item's stage; the next batch's barrier
+    uint32_t next_ph = 0, step = 0;
+    struct Item {
+      int st;
+      uint32_t ph;
+      bool look;  // a V tile that is looked through
     };
-    auto issue_qk = [&](int x, int item) {
-      const uint32_t kb = stage_addr(item), qb = q_addr + (w.single ? 0 : x) * L::kTileBytes;
+    auto take = [&](bool look) {
+      const Item i = {next_st, next_ph, look};
+      if (++next_st == NS) next_st = 0, next_ph ^= 1;
+      return i;
+    };
+    auto try_item = [&](const Item& i) {
+      return i.look ? mbar_try_wait(looked + i.st, (look_parity >> i.st) & 1) : mbar_try_wait(full + i.st, i.ph);
+    };
+    auto wait_item = [&](const Item& i) {
+      return i.look ? warp_wait(looked + i.st, (look_parity >> i.st) & 1, abort_flag, a.status)
+                    : warp_wait(full + i.st, i.ph, abort_flag, a.status);
+    };
+    auto issue_qk = [&](int x, int st) {
+      const uint32_t kb = ring_addr + st * L::kTileBytes, qb = q_addr + (w.single ? 0 : x) * L::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * L::kSubBytes + (kk & 3) * 32;
         umma_ss(tmem + x * 128, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0);
       }
     };
-    auto issue_pv = [&](int x, int item, bool first) {
-      const uint32_t vb = stage_addr(item);
+    auto issue_pv = [&](int x, int st, bool first) {
+      const uint32_t vb = ring_addr + st * L::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
         umma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 16 * 128, L::kSubBytes, 1024), idesc_pv,
@@ -809,63 +860,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     for (; ok && more; more = next_segment(a, w)) {
-      const int seen = seen_by_all(a, w);
-      int k_item[2];  // of the chains' next scores
-      ok = warp_wait(q_full, w.index & 1, abort_flag, a.status);
-      for (int x = 0; ok && x < 2; ++x) {
-        const bool mine = has_tile(w, x, 0);
-        if (x == 0 || w.single) {
-          if (x == 0 || mine) {
-            k_item[x] = it++;
-            ok = wait_full(k_item[x]);
-          }
-        } else {
-          k_item[1] = k_item[0];
-        }
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          if (mine) issue_qk(x, k_item[x]);
-          umma_commit(s_full + x);
-          if (w.single ? mine : x == 1) umma_commit(empty + k_item[x] % NS);
-          if (x == 1 && w.count == 1) umma_commit(q_empty);
-        }
-        __syncwarp();
+      const bool single = w.single;
+      const int count = w.count, n0 = steps_of(w, 0), n1 = steps_of(w, 1);
+      // steps from look[x] on have a V tile that is looked through
+      const int seen = seen_by_all(a, w), first = seen / BN - tile_of(w, 0, 0);
+      const int look0 = E4M3 ? count : single ? (first + 1) >> 1 : first, look1 = E4M3 ? count : first >> 1;
+      Item k0 = take(false), k1 = single && n1 > 0 ? take(false) : k0;
+      ok = warp_wait(q_full, w.index & 1, abort_flag, a.status) && wait_item(k0) && wait_item(k1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        if (n0 > 0) issue_qk(0, k0.st);
+        if (n1 > 0) issue_qk(1, k1.st);
+        umma_commit(done + dn);
       }
-      int v_item = 0;
-      for (int j = 0; ok && j < w.count; ++j, ++step) {
-        const bool last = j + 1 == w.count;
-        for (int x = 0; ok && x < 2; ++x) {
-          const bool mine = has_tile(w, x, j), next = !last && has_tile(w, x, j + 1);
-          const bool loads_v = w.single ? mine : x == 0, loads_k = !last && (w.single ? next : x == 0);
-          // the batch's barriers are looked at together; only if one is not complete, each in turn
-          const bool look = loads_v && look_through(seen, tile_of(w, x, j));
-          if (loads_v) v_item = it++;
-          if (loads_k)
-            k_item[x] = it++;
-          else if (!w.single)
-            k_item[x] = k_item[0];
-          bool ready = mbar_try_wait(p_full + x, step & 1);
-          if (loads_v && (E4M3 || !look)) ready &= mbar_try_wait(full + v_item % NS, (v_item / NS) & 1);
-          if (loads_k) ready &= mbar_try_wait(full + k_item[x] % NS, (k_item[x] / NS) & 1);
-          if (!__all_sync(0xffffffffu, ready)) {
-            if (loads_v && (E4M3 || !look)) ok = wait_full(v_item);
-            if (loads_k) ok = ok && wait_full(k_item[x]);
-            ok = ok && warp_wait(p_full + x, step & 1, abort_flag, a.status);
-          }
-          if (!E4M3 && look) ok = ok && wait_looked(v_item);
+      __syncwarp();
+      dn = dn + 1 == L::kDone ? 0 : dn + 1;
+      Item v0 = k0, v1 = k0;
+      // the chains' items of step j: chain a's V, next K, and (an odd unit's) chain b's
+      auto take0 = [&](int j) {
+        if (!single || j < n0) v0 = take(j >= look0);
+        if (j + 1 < (single ? n0 : count)) k0 = take(false);
+      };
+      auto take1 = [&](int j) {
+        if (single) {
+          if (j < n1) v1 = take(j >= look1);
+          if (j + 1 < n1) k1 = take(false);
+        } else {
+          v1 = v0, k1 = k0;
+        }
+      };
+      take0(0);
+#pragma unroll 1
+      for (int j = 0; ok && j < count; ++j, ++step) {
+        {
+          const bool mine = j < n0, next = j + 1 < n0, loads_v = !single || mine, loads_k = j + 1 < (single ? n0 : count);
+          bool ready = mbar_try_wait(p_full, step & 1);
+          if (loads_v) ready &= try_item(v0);
+          if (loads_k) ready &= mbar_try_wait(full + k0.st, k0.ph);
+          if (!__all_sync(0xffffffffu, ready))
+            ok = (!loads_v || wait_item(v0)) && (!loads_k || wait_item(k0)) && warp_wait(p_full, step & 1, abort_flag, a.status);
           if (!ok) break;
+          if (loads_v && v0.look) look_parity ^= 1u << v0.st;
+          uint64_t* bar = done + dn;
+          dn = dn + 1 == L::kDone ? 0 : dn + 1;
+          take1(j);
+          const int vs = v0.st, ks = k0.st;
           tc_fence_after();
           if (elect_one()) {
-            if (mine) issue_pv(x, v_item, j == 0);
-            if (w.single ? mine : x == 1) umma_commit(empty + v_item % NS);
-            if (last) umma_commit(o_full + x);
-            if (!last) {
-              if (next) issue_qk(x, k_item[x]);
-              umma_commit(s_full + x);
-              if (w.single ? next : x == 1) umma_commit(empty + k_item[x] % NS);
-              if (x == 1 && j + 2 == w.count) umma_commit(q_empty);
-            }
+            if (mine) issue_pv(0, vs, j == 0);
+            if (next) issue_qk(0, ks);
+            umma_commit(bar);
+          }
+          __syncwarp();
+        }
+        {
+          const bool mine = j < n1, next = j + 1 < n1;
+          bool ready = mbar_try_wait(p_full + 1, step & 1);
+          if (single && mine) ready &= try_item(v1);
+          if (single && next) ready &= mbar_try_wait(full + k1.st, k1.ph);
+          if (!__all_sync(0xffffffffu, ready))
+            ok = (!single || !mine || wait_item(v1)) && (!single || !next || wait_item(k1)) &&
+                 warp_wait(p_full + 1, step & 1, abort_flag, a.status);
+          if (!ok) break;
+          if (single && mine && v1.look) look_parity ^= 1u << v1.st;
+          uint64_t* bar = done + dn;
+          dn = dn + 1 == L::kDone ? 0 : dn + 1;
+          const int vs = v1.st, ks = k1.st;
+          if (j + 1 < count) take0(j + 1);
+          tc_fence_after();
+          if (elect_one()) {
+            if (mine) issue_pv(1, vs, j == 0);
+            if (next) issue_qk(1, ks);
+            umma_commit(bar);
           }
           __syncwarp();
         }
@@ -900,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stride = w.single ? 2 * BN : BN;
       float m_run = -INFINITY, l_f32 = 0.f, l_mul = 0.f;
       for (int j = 0; j < count; ++j, ++step, ahead -= stride) {
-        if (!warp_wait(s_full + x, step & 1, abort_flag, a.status)) {
+        if (!wait_batch(j == 0 ? base : base + 2 * j + x - 1)) {
           ok = false;
           break;
         }
@@ -984,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(p_full + x);
       }
       // ---------------------------------------------------------- epilogue
-      if (ok) ok = warp_wait(o_full + x, w.index & 1, abort_flag, a.status);
+      if (ok) ok = wait_batch(base + 2 * count - 1 + x);
       if (!ok) break;
       const bool had = has_tile(w, x, 0);  // this chain wrote O
       float fa = 1.f, fb = 0.f;
@@ -996,8 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(joined + (warp & 3));
         } else {
-          ok = warp_wait(o_full + 1, w.index & 1, abort_flag, a.status) &&
-               warp_wait(joined + (warp & 3), join_parity, abort_flag, a.status);
+          ok = wait_batch(base + 2 * count) && warp_wait(joined + (warp & 3), join_parity, abort_flag, a.status);
           if (!ok) break;
           join_parity ^= 1;
           const float m_b = s_ml[row], top = fmaxf(m_run, m_b);
@@ -1078,6 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(written + (w.index & 1));
+      base += 2 * count + 1;
     }
   }
 
