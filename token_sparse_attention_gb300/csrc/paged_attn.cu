@@ -202,6 +202,24 @@ __device__ __forceinline__ bool has_tile(const Walk& w, int x, int j) {
 __device__ __forceinline__ int seen_by_all(const PagedAttnArgs& a, const Walk& w) {
   return a.causal ? w.s.keys - w.s.n + 2 * w.i * a.tokens + 1 : w.s.keys;
 }
+// A walk in one register of a warp's lanes, while the softmax needs the registers.
+__device__ __forceinline__ int fold(const Walk& w, int lane) {
+  const int f[14] = {w.s.cu, w.s.n, w.s.keys, w.g, w.head, w.i, w.single, w.tiles, w.tiles_a, w.steps, w.t0, w.index,
+                     static_cast<int>(w.left), static_cast<int>(w.left >> 32)};
+  int x = w.count;
+#pragma unroll
+  for (int k = 0; k < 14; ++k)
+    if (lane == k) x = f[k];
+  return x;
+}
+__device__ __forceinline__ Walk unfold(int x) {
+  int f[15];
+#pragma unroll
+  for (int k = 0; k < 15; ++k) f[k] = __shfl_sync(0xffffffffu, x, k);
+  return {{f[0], f[1], f[2]}, f[3], f[4], f[5], f[6] != 0, f[7], f[8], f[9], f[10], f[14],
+          static_cast<long long>(static_cast<uint32_t>(f[12])) | (static_cast<long long>(f[13]) << 32), f[11]};
+}
+
 // In how many steps of the share's part chain x has a tile (the first ones).
 __device__ __forceinline__ int steps_of(const Walk& w, int x) {
   const int all = w.single ? (w.tiles - x + 1) / 2 : x == 0 ? w.tiles_a : w.tiles;
@@ -670,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // E4M3 value is an f16 value) and store the lines.  Only the lanes of a row touch it, all in
       // one warp, so a __syncwarp between reads and writes orders them.
       constexpr int kPT = 32 * kLoaders;
-      constexpr int kSegsRow = D / 8, kChunks = BM * kSegsRow, kPer = (kChunks + kPT - 1) / kPT;
+      constexpr int kSegsRow = D / 8, kChunks = BM * kSegsRow;
       constexpr int kCopySegs = D / 16, kRPI = 32 / kCopySegs, kRG = BN / kRPI;
       constexpr int kGPW = (kRG + kLoaders - 1) / kLoaders;
       const int pw = warp - kFirstLoader, me = pw * 32 + lane, sub = lane / kCopySegs, seg = lane % kCopySegs;
@@ -773,23 +791,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && w.index >= 2 && look_through(seen, last_tile(w)))  // the record's last segment has been read
           ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
         if (!ok) break;
-        // queries: bf16 to f16 through registers, all loads of a unit first
+        // queries: bf16 to f16 through registers, kAtOnce chunks side by side
         const int chunk0 = w.head % a.chunks * a.heads, head = w.head / a.chunks * group + chunk0;
-        for (int u = 0; u < (w.single ? 1 : 2); ++u) {
-          uint4 qw[kPer];
+        constexpr int kAtOnce = 5;
+#pragma unroll 1
+        for (int c0 = me; c0 < (w.single ? 1 : 2) * kChunks; c0 += kAtOnce * kPT) {
+          uint4 qw[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int c = me + kPT * k, r = c / kSegsRow, sg = c % kSegsRow;
-            const int t = r / a.heads, h = r - t * a.heads, tok = (2 * w.i + u) * a.tokens + t;
+          for (int k = 0; k < kAtOnce; ++k) {
+            const int c = c0 + kPT * k, r = c % kChunks / kSegsRow, sg = c % kSegsRow;
+            const int t = r / a.heads, h = r - t * a.heads, tok = (2 * w.i + c / kChunks) * a.tokens + t;
             qw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < kChunks && t < a.tokens && tok < w.s.n && chunk0 + h < group)
+            if (c < 2 * kChunks && t < a.tokens && tok < w.s.n && chunk0 + h < group)
               qw[k] = ld_global16(a.q + static_cast<size_t>(w.s.cu + tok) * a.q_stride + static_cast<size_t>(head + h) * D + sg * 8);
           }
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int c = me + kPT * k;
-            if (c < kChunks)
-              st_shared16(qs + u * L::kTileBytes + swz_offset(c / kSegsRow, c % kSegsRow),
+          for (int k = 0; k < kAtOnce; ++k) {
+            const int c = c0 + kPT * k;
+            if (c < 2 * kChunks)
+              st_shared16(qs + c / kChunks * L::kTileBytes + swz_offset(c % kChunks / kSegsRow, c % kSegsRow),
                           make_uint4(bf16x2_to_f16x2(qw[k].x), bf16x2_to_f16x2(qw[k].y), bf16x2_to_f16x2(qw[k].z),
                                      bf16x2_to_f16x2(qw[k].w)));
           }
@@ -949,22 +969,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + x * 128 + lane_off;
     const uint32_t tO = tmem + 256 + x * D + lane_off;
     const float sl2 = a.scale_log2;
-    const int row_t = row / a.heads, row_h = row - row_t * a.heads;
+    // this thread's row of a segment: its token, the head inside the KV head, whether it exists, and
+    // the keys it sees (a row that does not exist sees what every row sees and costs no masks)
+    struct Row {
+      int tok, head, limit;
+      bool live;
+    };
+    auto row_of = [&](const Walk& w) {
+      const int t = row / a.heads;
+      Row r;
+      r.tok = static_cast<int>(min((2LL * w.i + (w.single ? 0 : x)) * a.tokens + t, 0x7fffffffLL));
+      r.head = w.head % a.chunks * a.heads + row - t * a.heads;
+      r.live = t < a.tokens && r.tok < w.s.n && r.head < group;
+      r.limit = r.live && a.causal ? w.s.keys - w.s.n + r.tok + 1 : w.s.keys;
+      return r;
+    };
     int step = 0;
     uint32_t join_parity = 0;
     bool ok = true;
     for (; ok && more; more = next_segment(a, w)) {
-      // this thread's row: token, head, keys it sees
-      const int unit = 2 * w.i + (w.single ? 0 : x);
-      const long long tok = static_cast<long long>(unit) * a.tokens + row_t;
-      const int hh = w.head % a.chunks * a.heads + row_h;
-      const bool live = row_t < a.tokens && tok < w.s.n && hh < group;
-      // (rows that are none see what every row sees: they cost no masks)
-      const int limit = live && a.causal ? w.s.keys - w.s.n + static_cast<int>(tok) + 1 : w.s.keys;
-      const bool idle = __all_sync(0xffffffffu, !live);
-      const int mine = idle ? 0 : steps_of(w, x), count = w.count;
+      const Row mine_row = row_of(w);
+      const int limit = mine_row.limit;
+      const int mine = __all_sync(0xffffffffu, !mine_row.live) ? 0 : steps_of(w, x), count = w.count;
       int ahead = limit - tile_of(w, x, 0) * BN;  // keys that the row sees from the tile's first on
       const int stride = w.single ? 2 * BN : BN;
+      const int folded = fold(w, lane);
       float m_run = -INFINITY, l_f32 = 0.f, l_mul = 0.f;
       for (int j = 0; j < count; ++j, ++step, ahead -= stride) {
         if (!wait_batch(j == 0 ? base : base + 2 * j + x - 1)) {
@@ -1053,6 +1082,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- epilogue
       if (ok) ok = wait_batch(base + 2 * count - 1 + x);
       if (!ok) break;
+      w = unfold(folded);
+      const Row r = row_of(w);
+      const bool idle = __all_sync(0xffffffffu, !r.live), live = r.live;
       const bool had = has_tile(w, x, 0);  // this chain wrote O
       float fa = 1.f, fb = 0.f;
       if (w.single) {  // chain a joins the two
@@ -1080,16 +1112,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool b_too = w.single && has_tile(w, 1, 0);
         const uint32_t tOb = tmem + 256 + D + lane_off;
         const bool goes_on = w.t0 + w.count < w.steps, whole = w.t0 == 0 && !goes_on;
-        const size_t out_row = static_cast<size_t>(w.s.cu + static_cast<int>(tok)) * a.Hq + w.head / a.chunks * group + hh;
+        const size_t out_row = static_cast<size_t>(w.s.cu + r.tok) * a.Hq + w.head / a.chunks * group + r.head;
         const bool finals = whole && a.whole == nullptr;
         // (the value scale by itself: its quotient by the sum may be too small for a normal float)
         const float inv = !finals ? 1.f : l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
         float* part = nullptr;
         if (!whole) {
           part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (goes_on ? 1 : 0)) * part_floats(D);
-          const int r = x * BM + row;
-          if (live) reinterpret_cast<float4*>(part)[r] = make_float4(m_run, l_mul, l_f32, 0.f);
-          part += 4 * kPartRows + static_cast<size_t>(r) * D;
+          const int at = x * BM + row;
+          if (live) reinterpret_cast<float4*>(part)[at] = make_float4(m_run, l_mul, l_f32, 0.f);
+          part += 4 * kPartRows + static_cast<size_t>(at) * D;
         } else if (!finals) {
           part = a.whole + 4 * static_cast<size_t>(a.T) * a.Hq + out_row * D;
           if (live) reinterpret_cast<float4*>(a.whole)[out_row] = make_float4(m_run, l_mul, l_f32, 0.f);
@@ -1120,7 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (spoiled) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (first_bad(record, w, seen, c * 32 + i) < limit) v[i] = NAN;
+                if (first_bad(record, w, seen, c * 32 + i) < r.limit) v[i] = NAN;
             }
             if (finals) {
               uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c * 32);
