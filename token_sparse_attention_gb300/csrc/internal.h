@@ -253,15 +253,16 @@ struct PagedAttnArgs {
   unsigned* status;
 };
 // tq: 3-D map over q, box {64, heads, tokens}; tk, tv: 2-D maps over the caches' rows, box {64, page}
-// (bf16 only).
+// (E4M3: {D, page} bytes; no tq).
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
                               const CUtensorMap* tv, bool e4m3, cudaStream_t stream);
 size_t paged_attn_parts_bytes(int D);
 size_t paged_attn_ends_bytes();
 
-// Tiled bf16 maps with 128-byte swizzle: rows [rows][D] in boxes of box_rows x 64, and q [T][H][D]
-// with tokens `stride` elements apart in boxes of tokens x heads x 64.
-bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows);
+// Tiled maps: rows [rows][D] of bf16 in boxes of box_rows x 64 with 128-byte swizzle, or of bytes in
+// boxes of box_rows x D without; and q [T][H][D] bf16 with tokens `stride` elements apart in boxes of
+// tokens x heads x 64 with 128-byte swizzle.
+bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows, bool bytes);
 bool make_query_map(CUtensorMap* m, const void* base, int T, int H, int D, long long stride, int heads, int tokens);
 // MCS_TEST_FAULT (see mcs_api.cu).
 int test_fault();

@@ -239,15 +239,16 @@ cudaError_t device_status_word(unsigned** out) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_mcs_status);
 }
 
-bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows) {
+bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows, bool bytes) {
   EncodeTiledFn f = encode_fn();
   if (!f) return false;
   cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D * (bytes ? 1 : 2)};
+  cuuint32_t box[2] = {bytes ? (cuuint32_t)D : 64, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return f(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+           const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -98,7 +98,7 @@ mcs_status run_decode(const mcs_paged* p, const void* q, const void* k_cache, co
   return finish(mcs::launch_paged_decode(a, e4m3, stream), what);
 }
 
-// What the attention of many rows takes from the params; the maps are made for bf16 caches.
+// What the attention of many rows takes from the params; and its tensor maps.
 mcs_status many_rows(const mcs_paged* p, int T, const void* q, const void* k_cache, const void* v_cache,
                      mcs::PagedAttnArgs* a, CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
   const int group = p->Hq / p->Hkv;
@@ -120,10 +120,10 @@ mcs_status many_rows(const mcs_paged* p, int T, const void* q, const void* k_cac
   a->k = k_cache;
   a->v = v_cache;
   a->fault = mcs::test_fault();
-  if (p->kv == MCS_KV_BF16 &&
-      (!mcs::make_query_map(tq, q, T, p->Hq, p->D, a->q_stride, a->heads, a->tokens) ||
-       !mcs::make_rows_map(tk, k_cache, a->rows, p->D, p->page) ||
-       !mcs::make_rows_map(tv, v_cache, a->rows, p->D, p->page)))
+  const bool e4m3 = p->kv == MCS_KV_E4M3;
+  if ((!e4m3 && !mcs::make_query_map(tq, q, T, p->Hq, p->D, a->q_stride, a->heads, a->tokens)) ||
+      !mcs::make_rows_map(tk, k_cache, a->rows, p->D, p->page, e4m3) ||
+      !mcs::make_rows_map(tv, v_cache, a->rows, p->D, p->page, e4m3))
     return mcs::record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled(paged)");
   return status_word(&a->status);
 }

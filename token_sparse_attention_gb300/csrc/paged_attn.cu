@@ -21,9 +21,9 @@
 // One CTA per SM, 16 warps, as in the dense kernel:
 //   warps 0-3   softmax and epilogue of chain a; thread t owns row t (TMEM lane t)
 //   warps 4-7   the same for chain b
-//   warps 8-14  loads.  bf16: warp 8 issues TMA boxes of a page's rows; warps 9-14 look
-//               through the V tiles in which some row's mask leaves something out (below).
-//               E4M3: all seven copy rows with cp.async and convert them to f16
+//   warp 8      loads: TMA boxes of a page's rows
+//   warps 9-14  bf16: look through the V tiles in which some row's mask leaves something out
+//               (below).  E4M3: convert every tile to f16
 //   warp 15     TMEM and MMA issue (one elected lane)
 // TMEM: S_a, S_b (P is written over S), O_a, O_b.  Shared memory: Q_a, Q_b and a ring of K
 // and V tiles that runs on from segment to segment; the next segment's queries are loaded
@@ -62,14 +62,18 @@ constexpr int kBadSlots = 16;         // steps ahead of the softmax that loads m
 template <bool E4M3>
 constexpr float kThreshold = E4M3 ? 15.f : 16.f;
 
-template <int D>
+template <int D, bool E4M3>
 struct Layout {
   static constexpr int kSub = D / 64;                 // 128-byte column sub-tiles of a row
   static constexpr int kSubBytes = BN * 128;
   static constexpr int kTileBytes = kSub * kSubBytes;
-  static constexpr int kStages = D == 128 ? 5 : 12;
+  // E4M3 bytes on their way to f16: in the tile's second half, whose lines they are converted to
+  // (D = 128), or behind the tile (D = 64: a row's bytes are not as long as a line)
+  static constexpr int kRaw = D == 128 ? kSubBytes : kTileBytes;
+  static constexpr int kStageBytes = kTileBytes + (E4M3 && D == 64 ? BN * D : 0);
+  static constexpr int kStages = D == 128 ? 5 : E4M3 ? 8 : 12;
   static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kBars = kRing + kStages * kStageBytes;
   // MMA batches done, round robin.  A waiter reads the phase of batch n's barrier, which is
   // unambiguous as long as batch n + kDone cannot be done yet.  Loads lag furthest: they wait for the
   // last reader of the item kStages back, and what the kStages - 1 items behind it feed is at most
@@ -226,7 +230,6 @@ __device__ __forceinline__ int steps_of(const Walk& w, int x) {
   return max(0, min(w.count, all - w.t0));
 }
 __device__ __forceinline__ int last_tile(const Walk& w) { return min(tile_of(w, w.single ? 1 : 0, w.count - 1), w.tiles - 1); }
-__device__ __forceinline__ bool look_through(int seen, int tile) { return (tile + 1) * static_cast<long long>(BN) > seen; }
 
 // ------------------------------------------------------------------ small pieces
 
@@ -342,13 +345,13 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const PagedAttnArgs a) {
-  using L = Layout<D>;
+  using L = Layout<D, E4M3>;
   constexpr int NS = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];  // (swizzled tiles; there is no other shared memory)
   uint8_t* qs = smem;
   uint8_t* ring = smem + L::kRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [NS] stage loaded
-  uint64_t* raw = full + NS;                                     // [NS] V tile to be looked through loaded (bf16)
+  uint64_t* raw = full + NS;                                     // [NS] loaded, to be looked through (bf16) or converted (E4M3)
   uint64_t* looked = raw + NS;                                   // [NS] and looked through
   uint64_t* q_full = looked + NS;                                // queries loaded
   uint64_t* p_full = q_full + 1;                                 // [2] P_x written
@@ -364,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full + s, E4M3 ? 32 * kLoaders : 1);
+      mbar_init(full + s, E4M3 ? kLoaders - 1 : 1);
       mbar_init(raw + s, 1);
       mbar_init(looked + s, kLoaders - 1);
     }
-    mbar_init(q_full, E4M3 ? 32 * kLoaders : 1);
+    mbar_init(q_full, E4M3 ? kLoaders - 1 : 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(p_full + x, 4);
       mbar_init(written + x, 8);
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (tid < 2 * D) records[tid] = 0;
+  if (tid < 2 * kBadSlots) (&misc.bad[0][0])[tid] = 0;
   if (!E4M3 && a.heads * a.tokens < BM) {  // rows of the query tiles that no load fills
     for (int i = tid; i < 2 * L::kTileBytes / 16; i += kThreads) st_shared16(qs + 16 * i, make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_smem();
@@ -506,9 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the softmax that S_x is there, the epilogue that O_x is final, the loads that tiles are read.
   int base = 0;
   auto wait_batch = [&](int n) { return warp_wait(done + n % L::kDone, (n / L::kDone) & 1, abort_flag, a.status); };
-  auto read_by = [&](bool is_k, int x, int j) {  // the last batch that reads the chain's tile of step j
-    return w.single ? (is_k ? (j == 0 ? base : base + 2 * j + x - 1) : base + 2 * j + x + 1) : base + 2 * j + (is_k ? 0 : 2);
-  };
 
   if (warp >= kFirstLoader && warp < kMmaWarp) {
     // ------------------------------------------------------------ loads
@@ -552,63 +553,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         outside[2] = __ballot_sync(0xffffffffu, out);
       }
     };
-    int it = 0, step = 0;  // ring items and steps so far
-    int reader = 0;        // lane i: the last batch that reads stage i
-    int q_reader = 0;      // the last batch that reads the queries
-    if (!E4M3 && warp == kFirstLoader) {
-      // ---------------------------------------------------------- bf16: TMA
+    // Ring items of a segment, in the order in which the MMA warp asks for them: the chains' first K,
+    // then for every step and chain its V and its next K (a pair's tiles come with chain a).
+    int it = 0;  // items so far
+    if (warp == kFirstLoader) {
+      // ---------------------------------------------------------- TMA
       if (elect_one()) {
-        tma_prefetch_desc(&tq);
+        if (!E4M3) tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
       }
       __syncwarp();
-      const int boxes = BN / a.page;  // 1 to 8 pages of a tile, kSub boxes each
-      const int box = lane / L::kSub, sub = lane % L::kSub;
-      uint32_t raw_used = 0, raw_parity = 0;  // of each stage: a tile went to `raw`; the last one's parity
-      auto load = [&](bool is_k, int x, int j, bool look) -> bool {
-        const int st = it % NS, tile = tile_of(w, x, j);
-        if (it >= NS && !wait_batch(__shfl_sync(0xffffffffu, reader, st))) return false;
-        if (lane == st) reader = read_by(is_k, x, j);
-        if (is_k) to_window(tile);
-        const int behind = window - tile / kWindow;  // 0 or 1
-        const int slab0 = (tile % kWindow) * kSlabs;
-        const int row = __shfl_sync(0xffffffffu, behind ? found[0] : found[1], slab0 + (box < boxes ? box : 0) * slabs_per_page);
-        if (is_k) {
-          const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu;
-          if (lane == 0) {
-            misc.bad[(step + j) % kBadSlots][x] = static_cast<uint8_t>(out);
-            if (!w.single) misc.bad[(step + j) % kBadSlots][1 - x] = static_cast<uint8_t>(out);
-            if (out) atomicOr(a.status, DEV_BOUNDS);
-          }
+      // Two items at a time, as the MMA warp takes them: lanes 0-15 load the first one's boxes (a
+      // page's rows, 128 bytes wide), lanes 16-31 the second's.
+      constexpr int kBoxSubs = E4M3 ? 1 : L::kSub, kBoxBytes = E4M3 ? D : 128;
+      const int half = lane >> 4, box = (lane & 15) / kBoxSubs, sub = (lane & 15) % kBoxSubs, boxes = BN / a.page;
+      const uint32_t to = smem_u32(ring) + (E4M3 ? L::kRaw : sub * L::kSubBytes) + box * a.page * kBoxBytes;
+      int reader = 0, q_reader = 0;  // lane i: the last batch that reads stage i; the last that reads the queries
+      int next_st = 0, step = 0;
+      uint32_t raw_used = 0, raw_parity = 0;  // bf16, of each stage: a tile went to `raw`; the last one's parity
+      uint32_t dirty = 0;                     // steps (and chains) whose `bad` is not zero
+      auto issue = [&](bool first, bool first_k, int first_tile, int first_read, bool look, bool second, int second_tile,
+                       int second_read) -> bool {
+        const int st0 = next_st, st1 = first ? (st0 + 1 == NS ? 0 : st0 + 1) : st0;
+        const int st = half ? st1 : st0;
+        const bool mine = half ? second : first;
+        const int n = __shfl_sync(0xffffffffu, reader, st);
+        const bool used = it + (half && first ? 1 : 0) >= NS;
+        bool ok = !mine || !used || mbar_try_wait(done + n % L::kDone, (n / L::kDone) & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = !mine || !used || mbar_wait(done + n % L::kDone, (n / L::kDone) & 1, abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+        }
+        if (second) to_window(second_tile);
+        const int tile = half ? second_tile : first_tile;
+        const bool behind = tile / kWindow != window;
+        const int from = (tile % kWindow) * kSlabs + (box < boxes ? box : 0) * slabs_per_page;
+        const int r0 = __shfl_sync(0xffffffffu, found[0], from), r1 = __shfl_sync(0xffffffffu, found[1], from);
+        const int row = behind ? r0 : r1;
+        const bool to_raw = E4M3 || (look && half == 0);
+        uint64_t* bar = (to_raw ? raw : full) + st;
+        if (mine && (lane & 15) == 0) {
+          mbar_expect_tx(bar, E4M3 ? BN * D : L::kTileBytes);
+          if (!E4M3 && to_raw) mbar_arrive(full + st);  // `full` keeps its turn: such tiles complete it empty
         }
         __syncwarp();
-        // `full` keeps its turn: tiles to be looked through complete it empty
-        if (lane == 0) {
-          mbar_expect_tx((look ? raw : full) + st, L::kTileBytes);
-          if (look) mbar_arrive(full + st);
-        }
-        if (look) {
-          raw_parity ^= ((raw_used >> st) & 1u) << st;
-          raw_used |= 1u << st;
+        if (mine && box < boxes) {  // (a row past the tensor's end reads zeros)
+          const bool is_k = half || first_k;
+          tma_load_2d_at(to + st * L::kStageBytes, is_k ? &tk : &tv, sub * 64, row < 0 ? a.rows : row, bar);
         }
         __syncwarp();
-        if (box < boxes)  // (a row past the tensor's end reads zeros)
-          tma_load_2d(ring + st * L::kTileBytes + sub * L::kSubBytes + box * a.page * 128, is_k ? &tk : &tv, sub * 64,
-                      row < 0 ? a.rows : row, (look ? raw : full) + st);
-        __syncwarp();
-        ++it;
+        if (!E4M3 && look) {
+          raw_parity ^= ((raw_used >> st0) & 1u) << st0;
+          raw_used |= 1u << st0;
+        }
+        if (first && lane == st0) reader = first_read;
+        if (second && lane == st1) reader = second_read;
+        it += (first ? 1 : 0) + (second ? 1 : 0);
+        next_st = second ? (st1 + 1 == NS ? 0 : st1 + 1) : st1;
         return true;
+      };
+      // slabs of the tile whose pages are none, for the softmax; in front of the load that it goes with
+      auto tell = [&](int tile, int at, int x) {
+        to_window(tile);
+        const uint32_t out = ((tile / kWindow != window ? outside[0] : outside[1]) >> ((tile % kWindow) * kSlabs)) & 0xffu;
+        const int slot = (at % kBadSlots) * 2 + x;
+        if (out == 0 && ((dirty >> slot) & 1u) == 0) return;
+        dirty = (dirty & ~(1u << slot)) | (out ? 1u << slot : 0u);
+        if (lane == 0) {
+          (&misc.bad[0][0])[slot] = static_cast<uint8_t>(out);
+          if (out) atomicOr(a.status, DEV_BOUNDS);
+        }
+        __syncwarp();
       };
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
-        const int seen = seen_by_all(a, w);
-        begin_windows(tile_of(w, 0, 0));
+        const bool single = w.single;
+        const int count = w.count, n0 = steps_of(w, 0), n1 = steps_of(w, 1), tile0 = tile_of(w, 0, 0);
+        const int kn0 = single ? n0 : count, first_look = seen_by_all(a, w) / BN;
+        begin_windows(tile0);
         if (w.index > 0) ok = wait_batch(q_reader);
         if (!ok) break;
-        if (elect_one()) {
+        if (!E4M3 && elect_one()) {
           // a box is tokens x heads rows; tokens behind the sequence's are other ones' or zeros
-          const int units = w.single ? 1 : 2;
+          const int units = single ? 1 : 2;
           mbar_expect_tx(q_full, units * L::kSub * 128 * a.heads * a.tokens);
           const int head = w.head / a.chunks * group + w.head % a.chunks * a.heads;
           for (int u = 0; u < units; ++u)
@@ -616,224 +644,178 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(qs + u * L::kTileBytes + s * L::kSubBytes, &tq, s * 64, head, w.s.cu + (2 * w.i + u) * a.tokens, q_full);
         }
         __syncwarp();
-        const int xs = w.single ? 2 : 1;  // (a pair's tiles come with chain a)
-        for (int x = 0; ok && x < xs; ++x)
-          if (x == 0 || has_tile(w, x, 0)) ok = load(true, x, 0, false);
-        for (int j = 0; ok && j < w.count; ++j) {
+        tell(tile0, step, 0);
+        if (!single) tell(tile0, step, 1);
+        if (single && n1 > 0) tell(tile0 + 1, step, 1);
+        ok = issue(true, true, tile0, base, false, single && n1 > 0, tile0 + 1, base);
+        // (one call of `issue` in the loop: its code is long)
+        const int turns = single ? 2 * count : count;
+#pragma unroll 1
+        for (int i = 0; ok && i < turns; ++i) {
+          const int j = single ? i >> 1 : i, x = single ? i & 1 : 0;
           if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
-          for (int x = 0; ok && x < xs; ++x) {
-            if (!w.single || has_tile(w, x, j)) ok = load(false, x, j, look_through(seen, tile_of(w, x, j)));
-            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ok = load(true, x, j + 1, false);
+          const bool v = !single || j < (x ? n1 : n0), k = j + 1 < (x ? n1 : kn0);
+          const int v_tile = tile0 + i, k_tile = v_tile + (single ? 2 : 1);
+          if (k) {
+            tell(k_tile, step + j + 1, x);
+            if (!single) tell(k_tile, step + j + 1, 1);
           }
+          // V_x(j) is read by batch base + 2 j + x + 1, K_x(j + 1) too (a pair's by chain b's)
+          const int read = base + 2 * j + (single ? x + 1 : 2);
+          if (ok && v) ok = issue(true, false, v_tile, read, v_tile >= first_look, k, k_tile, read);
         }
-        step += w.count;
-        q_reader = base + 2 * (w.count - 1);
-        base += 2 * w.count + 1;
+        step += count;
+        q_reader = base + 2 * (count - 1);
+        base += 2 * count + 1;
       }
       if (*abort_flag)
         for (int i = max(it - NS, 0); i < it; ++i) {
-          drain_wait(full + i % NS, (i / NS) & 1);
-          if ((raw_used >> (i % NS)) & 1u) drain_wait(raw + i % NS, (raw_parity >> (i % NS)) & 1u);
+          if (!E4M3) drain_wait(full + i % NS, (i / NS) & 1);
+          if (E4M3) drain_wait(raw + i % NS, (i / NS) & 1);
+          if (!E4M3 && ((raw_used >> (i % NS)) & 1u)) drain_wait(raw + i % NS, (raw_parity >> (i % NS)) & 1u);
         }
-    } else if (!E4M3) {
-      // ---------------------------------------------------------- bf16: V tiles that masks cut
-      const int me = tid - 32 * (kFirstLoader + 1);
-      constexpr int kLook = 32 * (kLoaders - 1), kSegsRow = D / 8;
-      uint32_t raw_parity = 0;  // of each stage
-      bool ok = true;
-      for (; ok && more; more = next_segment(a, w)) {
-        const int seen = seen_by_all(a, w);
-        bool begun = false;
-        it += w.single && has_tile(w, 1, 0) ? 2 : 1;
-        for (int j = 0; ok && j < w.count; ++j) {
-          for (int x = 0; ok && x < (w.single ? 2 : 1); ++x) {
-            if (w.single ? has_tile(w, x, j) : true) {
-              const int tile = tile_of(w, x, j), st = it % NS;
-              if (look_through(seen, tile)) {
-                if (!begun && w.index >= 2)  // the record's last segment has been read
-                  ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
-                begun = true;
-                ok = ok && warp_wait(raw + st, (raw_parity >> st) & 1u, abort_flag, a.status);
-                if (!ok) break;
-                raw_parity ^= 1u << st;
-                uint8_t* v = ring + st * L::kTileBytes;
-                for (int c = me; c < BN * kSegsRow; c += kLook) {
-                  const int r = c / kSegsRow, sg = c % kSegsRow;
-                  const long long key = static_cast<long long>(tile) * BN + r;
-                  uint8_t* at = v + swz_offset(r, sg);
-                  if (key >= w.s.keys) {
-                    st_shared16(at, make_uint4(0u, 0u, 0u, 0u));
-                    continue;
-                  }
-                  uint4 q = ld_shared16(at);
-                  if (!has_bad<false>(q)) continue;
-                  q = note_bad<false>(q, records + (w.index & 1) * D + sg * 8, misc.any_bad + (w.index & 1), bad_mark(w.index),
-                                      static_cast<int>(key - seen / BN * BN));
-                  st_shared16(at, q);
-                }
-                fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
-                __syncwarp();
-                if (lane == 0) mbar_arrive(looked + st);
-              }
-              ++it;
-            }
-            if (j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ++it;
-          }
-        }
-      }
     } else {
-      // ---------------------------------------------------------- E4M3: cp.async and conversion
-      // Each item's rows are copied as bytes into the upper half of their own f16 lines in the
-      // item's stage; one item later the same lanes read them back, convert them (exact: every
-      // E4M3 value is an f16 value) and store the lines.  Only the lanes of a row touch it, all in
-      // one warp, so a __syncwarp between reads and writes orders them.
-      constexpr int kPT = 32 * kLoaders;
-      constexpr int kSegsRow = D / 8, kChunks = BM * kSegsRow;
-      constexpr int kCopySegs = D / 16, kRPI = 32 / kCopySegs, kRG = BN / kRPI;
-      constexpr int kGPW = (kRG + kLoaders - 1) / kLoaders;
-      const int pw = warp - kFirstLoader, me = pw * 32 + lane, sub = lane / kCopySegs, seg = lane % kCopySegs;
-      auto raw_at = [&](int i) { return (D == 128 ? BN * 128 : 64) + ((pw + kLoaders * i) * kRPI + sub) * 128 + seg * 16; };
-      // Items copied, not yet converted: the `pend` ones in front of `it`; of each, oldest first, where it is
-      // a V tile to be looked through, its first key (see note_bad), -1 otherwise.  Copies run as far
-      // ahead as stages are free: the oldest is converted once nothing else can be begun.
-      constexpr int kAhead = 3;
-      static_assert(kAhead <= NS - 2, "conversions must not wait on the batches they feed");
-      int pend = 0, rel[kAhead] = {-1, -1, -1};
-      auto convert = [&]() {
-        if (pend == 3)
-          cp_async_wait_group<2>();
-        else if (pend == 2)
-          cp_async_wait_group<1>();
-        else
-          cp_async_wait_group<0>();
-        const int st = (it - pend) % NS;
-        uint8_t* stage = ring + st * L::kTileBytes;
-        if (rel[0] >= 0) {
-#pragma unroll 1
-          for (int i = 0; i < kGPW; ++i) {
-            if (pw + kLoaders * i >= kRG) break;
-            const uint4 v = ld_shared16(stage + raw_at(i));
-            if (has_bad<true>(v))  // NaN codes (there are no infinities)
-              st_shared16(stage + raw_at(i), note_bad<true>(v, records + (w.index & 1) * D + seg * 16, misc.any_bad + (w.index & 1),
-                                                            bad_mark(w.index), rel[0] + (pw + kLoaders * i) * kRPI + sub));
-          }
-          __syncwarp();
-        }
-        uint4 v[kGPW];
-#pragma unroll
-        for (int i = 0; i < kGPW; ++i)
-          if (pw + kLoaders * i < kRG) v[i] = ld_shared16(stage + raw_at(i));
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kGPW; ++i) {
-          if (pw + kLoaders * i < kRG) {
-            const int r = (pw + kLoaders * i) * kRPI + sub;
-            uint4 x, y;
-            e4m3x4_to_f16x4(v[i].x, x.x, x.y);
-            e4m3x4_to_f16x4(v[i].y, x.z, x.w);
-            e4m3x4_to_f16x4(v[i].z, y.x, y.y);
-            e4m3x4_to_f16x4(v[i].w, y.z, y.w);
-            st_shared16(stage + swz_offset(r, 2 * seg), x);
-            st_shared16(stage + swz_offset(r, 2 * seg + 1), y);
-          }
-        }
-        fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
-        mbar_arrive(full + st);
-        --pend;
-#pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) rel[i] = rel[i + 1];
-      };
-      auto load = [&](bool is_k, int x, int j, int look) -> bool {
-        const int st = it % NS, tile = tile_of(w, x, j);
-        if (pend == kAhead) convert();
-        if (it >= NS) {
-          const int n = __shfl_sync(0xffffffffu, reader, st);
-          while (pend > 0 && !__all_sync(0xffffffffu, mbar_try_wait(done + n % L::kDone, (n / L::kDone) & 1))) convert();
-          if (!wait_batch(n)) return false;
-        }
-        if (lane == st) reader = read_by(is_k, x, j);
-        if (is_k) to_window(tile);
-        const int behind = window - tile / kWindow, slab0 = (tile % kWindow) * kSlabs;
-        const int rows = behind ? found[0] : found[1];
-        if (is_k && warp == kFirstLoader) {
-          const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu;
-          if (lane == 0) {
-            misc.bad[(step + j) % kBadSlots][x] = static_cast<uint8_t>(out);
-            if (!w.single) misc.bad[(step + j) % kBadSlots][1 - x] = static_cast<uint8_t>(out);
-            if (out) atomicOr(a.status, DEV_BOUNDS);
-          }
-        }
-        uint8_t* stage = ring + st * L::kTileBytes;
-        const uint8_t* src = static_cast<const uint8_t*>(is_k ? a.k : a.v);
-        const long long left = w.s.keys - static_cast<long long>(tile) * BN;
-#pragma unroll
-        for (int i = 0; i < kGPW; ++i) {
-          const int rg = pw + kLoaders * i, r = rg * kRPI + sub;
-          const int from = __shfl_sync(0xffffffffu, rows, slab0 + (rg < kRG ? r / kSlab : 0));
-          if (rg < kRG) {  // rows that hold no token become zeros
-            const bool there = from >= 0 && r < left;
-            cp_async16_zfill(stage + raw_at(i), src + static_cast<size_t>(there ? from + (r & (kSlab - 1)) : 0) * D + seg * 16, there);
-          }
-        }
-        cp_async_commit();
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (i == pend) rel[i] = look;
-        ++pend;
-        ++it;
-        return true;
-      };
+      // ---------------------------------------------------------- tiles on their way to the MMA
+      // bf16: V tiles that masks cut are looked through.  E4M3: every tile is converted to f16
+      // (exact: every E4M3 value is an f16 value), looked through where that is asked for, and
+      // the queries, too.
+      constexpr int kHelp = 32 * (kLoaders - 1), kSegsRow = D / 8;
+      const int hw = warp - kFirstLoader - 1, me = 32 * hw + lane;
+      uint32_t raw_parity = 0;  // of each stage
+      int q_reader = 0;
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
-        begin_windows(tile_of(w, 0, 0));
-        const int seen = seen_by_all(a, w);
-        if (w.index > 0) ok = wait_batch(q_reader);
-        if (ok && w.index >= 2 && look_through(seen, last_tile(w)))  // the record's last segment has been read
-          ok = warp_wait(written + (w.index & 1), ((w.index - 2) / 2) & 1, abort_flag, a.status);
+        const bool single = w.single;
+        const int count = w.count, n0 = steps_of(w, 0), n1 = steps_of(w, 1), tile0 = tile_of(w, 0, 0);
+        const int first_look = seen_by_all(a, w) / BN, mark = w.index & 1, keys = w.s.keys;
+        // a record's last segment, two back, has been read when this one's is begun
+        const bool looks = first_look <= last_tile(w);
+        if (looks && w.index >= 2) ok = warp_wait(written + mark, ((w.index - 2) / 2) & 1, abort_flag, a.status);
         if (!ok) break;
-        // queries: bf16 to f16 through registers, kAtOnce chunks side by side
-        const int chunk0 = w.head % a.chunks * a.heads, head = w.head / a.chunks * group + chunk0;
-        constexpr int kAtOnce = 5;
+        if constexpr (!E4M3) {
+          // items in front of step j
+          auto items_until = [&](int j) {
+            return single ? 2 * j + 1 + (n1 > 0 ? 1 + min(j, n1) + min(j, n1 - 1) : 0) : 2 * j + 1;
+          };
+          const int jl = looks ? max(0, single ? (first_look - tile0) >> 1 : first_look - tile0) : count;
+          int i = it + items_until(jl);
+          for (int j = jl; ok && j < count; ++j) {
+            for (int x = 0; x < (single ? 2 : 1); ++x) {
+              const int tile = tile0 + (single ? 2 * j + x : j), st = i % NS;
+              if (single && j >= (x ? n1 : n0)) continue;
+              i += j + 1 < (single ? (x ? n1 : n0) : count) ? 2 : 1;
+              if (tile < first_look) continue;
+              ok = warp_wait(raw + st, (raw_parity >> st) & 1u, abort_flag, a.status);
+              if (!ok) break;
+              raw_parity ^= 1u << st;
+              uint8_t* v = ring + st * L::kStageBytes;
+              for (int c = me; c < BN * kSegsRow; c += kHelp) {
+                const int r = c / kSegsRow, sg = c % kSegsRow;
+                uint8_t* at = v + swz_offset(r, sg);
+                if (r >= keys - tile * BN) {
+                  st_shared16(at, make_uint4(0u, 0u, 0u, 0u));
+                  continue;
+                }
+                const uint4 q = ld_shared16(at);
+                if (has_bad<false>(q))
+                  st_shared16(at, note_bad<false>(q, records + mark * D + sg * 8, misc.any_bad + mark, bad_mark(w.index),
+                                                  (tile - first_look) * BN + r));
+              }
+              fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
+              __syncwarp();
+              if (lane == 0) mbar_arrive(looked + st);
+            }
+          }
+          it += single ? 2 * n0 + (n1 > 0 ? 2 * n1 : 0) : 2 * count;
+        } else {
+          if (w.index > 0) ok = wait_batch(q_reader);
+          if (!ok) break;
+          // queries: bf16 to f16 through registers, kAtOnce chunks side by side
+          constexpr int kChunks = BM * kSegsRow, kAtOnce = 6;
+          const int chunk0 = w.head % a.chunks * a.heads, head = w.head / a.chunks * group + chunk0;
 #pragma unroll 1
-        for (int c0 = me; c0 < (w.single ? 1 : 2) * kChunks; c0 += kAtOnce * kPT) {
-          uint4 qw[kAtOnce];
+          for (int c0 = me; c0 < (single ? 1 : 2) * kChunks; c0 += kAtOnce * kHelp) {
+            uint4 qw[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            const int c = c0 + kPT * k, r = c % kChunks / kSegsRow, sg = c % kSegsRow;
-            const int t = r / a.heads, h = r - t * a.heads, tok = (2 * w.i + c / kChunks) * a.tokens + t;
-            qw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < 2 * kChunks && t < a.tokens && tok < w.s.n && chunk0 + h < group)
-              qw[k] = ld_global16(a.q + static_cast<size_t>(w.s.cu + tok) * a.q_stride + static_cast<size_t>(head + h) * D + sg * 8);
-          }
+            for (int k = 0; k < kAtOnce; ++k) {
+              const int c = c0 + kHelp * k, r = c % kChunks / kSegsRow, sg = c % kSegsRow;
+              const int t = r / a.heads, h = r - t * a.heads, tok = (2 * w.i + c / kChunks) * a.tokens + t;
+              qw[k] = make_uint4(0u, 0u, 0u, 0u);
+              if (c < 2 * kChunks && t < a.tokens && tok < w.s.n && chunk0 + h < group)
+                qw[k] = ld_global16(a.q + static_cast<size_t>(w.s.cu + tok) * a.q_stride + static_cast<size_t>(head + h) * D + sg * 8);
+            }
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            const int c = c0 + kPT * k;
-            if (c < 2 * kChunks)
-              st_shared16(qs + c / kChunks * L::kTileBytes + swz_offset(c % kChunks / kSegsRow, c % kSegsRow),
-                          make_uint4(bf16x2_to_f16x2(qw[k].x), bf16x2_to_f16x2(qw[k].y), bf16x2_to_f16x2(qw[k].z),
-                                     bf16x2_to_f16x2(qw[k].w)));
+            for (int k = 0; k < kAtOnce; ++k) {
+              const int c = c0 + kHelp * k;
+              if (c < 2 * kChunks)
+                st_shared16(qs + c / kChunks * L::kTileBytes + swz_offset(c % kChunks / kSegsRow, c % kSegsRow),
+                            make_uint4(bf16x2_to_f16x2(qw[k].x), bf16x2_to_f16x2(qw[k].y), bf16x2_to_f16x2(qw[k].z),
+                                       bf16x2_to_f16x2(qw[k].w)));
+            }
           }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full);
-        const int xs = w.single ? 2 : 1;  // (a pair's tiles come with chain a)
-        for (int x = 0; ok && x < xs; ++x)
-          if (x == 0 || has_tile(w, x, 0)) ok = load(true, x, 0, -1);
-        for (int j = 0; ok && j < w.count; ++j) {
-          if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
-          for (int x = 0; ok && x < xs; ++x) {
-            const int tile = tile_of(w, x, j);
-            if (!w.single || has_tile(w, x, j)) ok = load(false, x, j, look_through(seen, tile) ? (tile - seen / BN) * BN : -1);
-            if (ok && j + 1 < w.count && (!w.single || has_tile(w, x, j + 1))) ok = load(true, x, j + 1, -1);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+          // One row of 16-byte chunks per kSegs lanes.  Only these lanes touch a row's bytes and its f16
+          // line; where both share memory (D = 128) a __syncwarp between reads and writes orders them.
+          constexpr int kSegs = D / 16, kRows = 32 / kSegs, kGroups = BN / kRows, kTurns = (kGroups + kLoaders - 2) / (kLoaders - 1);
+          const int sub = lane / kSegs, seg = lane % kSegs;
+          const int heads_of = single ? 1 + (n1 > 0 ? 1 : 0) : 1;
+          const int turns = heads_of + (single ? 4 : 2) * count;
+#pragma unroll 1
+          for (int i = 0; ok && i < turns; ++i) {
+            // item i: the first K, then (V, next K) of each step and chain
+            const int m = i - heads_of, u = m >> 1, j = single ? u >> 1 : u, x = single ? u & 1 : 0;
+            const bool is_k = m < 0 || (m & 1);
+            if (m >= 0 && j + (is_k ? 1 : 0) >= (single ? (x ? n1 : n0) : count)) continue;
+            const int tile = tile0 + u, st = it % NS;  // (of a V tile)
+            const bool look = !is_k && tile >= first_look;
+            ok = warp_wait(raw + st, (it / NS) & 1, abort_flag, a.status);
+            if (!ok) break;
+            ++it;
+            uint8_t* stage = ring + st * L::kStageBytes;
+            uint8_t* from = stage + L::kRaw;
+            if (look) {
+#pragma unroll 1
+              for (int k = 0; k < kTurns; ++k) {
+                const int r = (hw + (kLoaders - 1) * k) * kRows + sub;
+                if (r >= BN) continue;
+                uint4 q = ld_shared16(from + r * D + seg * 16);
+                if (r >= keys - tile * BN)
+                  q = make_uint4(0u, 0u, 0u, 0u);
+                else if (has_bad<true>(q))  // NaN codes (there are no infinities)
+                  q = note_bad<true>(q, records + mark * D + seg * 16, misc.any_bad + mark, bad_mark(w.index),
+                                     (tile - first_look) * BN + r);
+                st_shared16(from + r * D + seg * 16, q);
+              }
+              __syncwarp();
+            }
+            uint4 v[kTurns];
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k)
+              if (hw + (kLoaders - 1) * k < kGroups) v[k] = ld_shared16(from + ((hw + (kLoaders - 1) * k) * kRows + sub) * D + seg * 16);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+              if (hw + (kLoaders - 1) * k < kGroups) {
+                const int r = (hw + (kLoaders - 1) * k) * kRows + sub;
+                uint4 p, q;
+                e4m3x4_to_f16x4(v[k].x, p.x, p.y);
+                e4m3x4_to_f16x4(v[k].y, p.z, p.w);
+                e4m3x4_to_f16x4(v[k].z, q.x, q.y);
+                e4m3x4_to_f16x4(v[k].w, q.z, q.w);
+                st_shared16(stage + swz_offset(r, 2 * seg), p);
+                st_shared16(stage + swz_offset(r, 2 * seg + 1), q);
+              }
+            }
+            fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + st);
           }
+          q_reader = base + 2 * (count - 1);
+          base += 2 * count + 1;
         }
-        // nothing of this segment waits for the next one's queries
-        while (ok && pend > 0) convert();
-        step += w.count;
-        q_reader = base + 2 * (w.count - 1);
-        base += 2 * w.count + 1;
       }
-      cp_async_wait_group<0>();
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
@@ -864,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     : warp_wait(full + i.st, i.ph, abort_flag, a.status);
     };
     auto issue_qk = [&](int x, int st) {
-      const uint32_t kb = ring_addr + st * L::kTileBytes, qb = q_addr + (w.single ? 0 : x) * L::kTileBytes;
+      const uint32_t kb = ring_addr + st * L::kStageBytes, qb = q_addr + (w.single ? 0 : x) * L::kTileBytes;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * L::kSubBytes + (kk & 3) * 32;
@@ -872,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     auto issue_pv = [&](int x, int st, bool first) {
-      const uint32_t vb = ring_addr + st * L::kTileBytes;
+      const uint32_t vb = ring_addr + st * L::kStageBytes;
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
         umma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 16 * 128, L::kSubBytes, 1024), idesc_pv,
@@ -1243,9 +1225,9 @@ template <int D, bool E4M3>
 cudaError_t launch(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, int grid,
                    cudaStream_t stream) {
   auto kernel = paged_attn_kernel<D, E4M3>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, E4M3>::kSmem);
   if (e != cudaSuccess) return e;
-  if ((e = launch_dependent(kernel, grid, kThreads, Layout<D>::kSmem, stream, *tq, *tk, *tv, a)) != cudaSuccess) return e;
+  if ((e = launch_dependent(kernel, grid, kThreads, Layout<D, E4M3>::kSmem, stream, *tq, *tk, *tv, a)) != cudaSuccess) return e;
   if (a.whole != nullptr) return cudaSuccess;  // joined with what the caller adds
   return launch_dependent(paged_attn_join_kernel<D, E4M3>, grid * kJoinBlocks, 8 * kJoinRows, 0, stream, a);
 }
