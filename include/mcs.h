@@ -569,6 +569,28 @@ mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* 
                           cudaStream_t stream);
 
 /*
+ * mcs_paged_decode for sequences that begin alike: answers to one prompt, beams,
+ * requests behind the same instructions.  Sequences group_start[g] ..
+ * group_start[g + 1] - 1 of the batch form group g (group_start [groups + 1]
+ * ascends from 0 to B; 1 <= groups <= B), and the first shared_pages[g] entries of
+ * their table rows are the same pages, full ones, as mcs_paged_fork leaves them:
+ * these are read once for the whole group, from the table row of its first
+ * sequence that holds them.  Same results as mcs_paged_decode, with the weights of
+ * the common beginning rounded as in mcs_paged_attn.  Groups may have one
+ * sequence, or nothing in common (0).  group_start that does not ascend so sets
+ * MCS_ERR_BOUNDS in the device status and shares nothing; a sequence that is
+ * neither empty nor as long as its group's beginning, or a negative or too large
+ * shared_pages, sets it, too, and that sequence (group) is read by itself.
+ * ws: at least mcs_paged_decode_shared_workspace(p) bytes, as above.
+ */
+size_t mcs_paged_decode_shared_workspace(const mcs_paged* p);
+mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_table,
+                                   const int32_t* lens, const int32_t* group_start,
+                                   const int32_t* shared_pages, void* out, float* lse, void* ws,
+                                   size_t ws_bytes, cudaStream_t stream);
+
+/*
  * What stands between a block's projections and its attention: RMS norm of
  * each head of q and k, then the rotation of its first `rot` values by the
  * token's angles, in one pass (for mcs_group, mcs_dense_attn and the sparse

@@ -93,3 +93,62 @@ def test_attn_matches_oracle(lens, new, Hq, Hkv, D, page, e4m3):
     got = c.attn()
     assert mcs.mcs_device_status() == 0
     c.check_attn(*got)
+
+
+# ------------------------------------------------------------------ common beginnings
+
+class Family(tp.Cache):
+    """Groups of sequences: (pages in common, [tokens of each behind them; None: an empty sequence])."""
+
+    def __init__(self, groups, Hq, Hkv, D, page, e4m3=False, seed=0, **kw):
+        lens, self.starts, self.shared = [], [0], []
+        for pages, own in groups:
+            lens += [0 if x is None else pages * page + x for x in own]
+            self.starts.append(len(lens))
+            self.shared.append(pages)
+        super().__init__(lens, Hq, Hkv, D, page, e4m3, seed=seed, **kw)
+        for (pages, own), a in zip(groups, self.starts):
+            first = next((b for b in range(a, a + len(own)) if lens[b]), a)
+            for b in range(a, a + len(own)):
+                if lens[b]:
+                    self.table[b, :pages] = self.table[first, :pages]
+        self.dtable = _i32(self.table)
+        self.dstarts, self.dshared = _i32(self.starts), _i32(self.shared)
+        self.ws = mcs.empty_workspace(mcs.mcs_paged_decode_shared_workspace(self.p))
+
+    def run(self, lse=True, stream=None):
+        B, Hq, D = self.q.shape
+        out = torch.full((B + 1, Hq, D), 77.0, dtype=torch.bfloat16, device="cuda")
+        ls = torch.full((B + 1, Hq), 77.0, device="cuda")
+        mcs.mcs_paged_decode_shared(self.p, self.q, self.k, self.v, self.dtable, self.dlens, self.dstarts, self.dshared,
+                                    out[:B], self.ws, lse=ls[:B] if lse else None, stream=stream)
+        return out, ls
+
+    def check(self, out, ls):
+        B, Hq, D = self.q.shape
+        k, v = (_f64(x) * s for x, s in zip((self.k, self.v), self.scales))
+        want, lse, absv, size = po.decode(_f64(self.q), k, v, self.table, self.lens, self.scale)
+        assert (_f64(out[B]) == 77).all() and (_f64(ls[B]) == 77).all()
+        out, ls = _f64(out[:B]), _f64(ls[:B])
+        tol, tol_lse = tolerance(want, lse, absv, size, D, max(self.lens), self.e4m3)
+        bad = ~(np.abs(out - want) <= tol)
+        assert not bad.any(), (len(np.argwhere(bad)), np.argwhere(bad)[:5], out[bad][:5], want[bad][:5])
+        live = np.isfinite(lse)
+        assert (ls[~live] == -np.inf).all()
+        assert (np.abs(ls[live] - lse[live]) <= tol_lse[live]).all()
+
+
+FAMILIES = [  # groups, Hq, Hkv, D, page
+    ([(1, [1, 1])], 1, 1, 128, 16), ([(9, [0, 5, 40])], 8, 2, 128, 16), ([(3, [7, 1, None, 300])], 4, 4, 64, 64),
+    ([(5, [3] * 9), (0, [17, 40]), (2, [None, 9, 0]), (4, [None, None]), (3, [11])], 5, 1, 128, 32),
+    ([(20, list(range(1, 41)))], 8, 2, 128, 16), ([(2, [5] * 70), (1, [200] * 3)], 20, 2, 64, 128),
+    ([(60, [1, 90, 3, 4])], 34, 2, 128, 16), ([(0, [0 + 5, 9])], 4, 2, 128, 16), ([(130, [33, 2])], 260, 2, 64, 16)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("groups,Hq,Hkv,D,page", FAMILIES)
+def test_shared_decode_matches_oracle(groups, Hq, Hkv, D, page, e4m3):
+    c = Family(groups, Hq, Hkv, D, page, e4m3, seed=Hq + page)
+    got = c.run()
+    assert mcs.mcs_device_status() == 0
+    c.check(*got)

@@ -43,6 +43,7 @@
 
 #include "internal.h"
 #include "launch.cuh"
+#include "paged_list.cuh"
 #include "ptx.cuh"
 
 namespace mcs {
@@ -216,8 +217,10 @@ __device__ __forceinline__ void store_rows(float* to, const float (*o)[4], int r
   }
 }
 
-// WIDE: more than 8 query heads in a segment.
-template <int D, bool E4M3, bool WIDE>
+// WIDE: more than 8 query heads in a segment.  SHARED: the sequences' own tails behind a common
+// beginning of skip[b] pages (lens are the tails'), whose rows are joined with the beginning's
+// afterwards: what a warp holds whole it leaves unnormalised.
+template <int D, bool E4M3, bool WIDE, bool SHARED = false>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(const DecodeArgs a, int chunks, int tail) {
   using G = Geo<D, E4M3>;
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
       }
     }
-    const int pid = a.table[static_cast<size_t>(ahead.b) * a.max_pages + j];
+    const int pid = a.table[static_cast<size_t>(ahead.b) * a.max_pages + j + (SHARED ? a.skip[ahead.b] : 0)];
     if (pid < 0 || pid >= a.num_pages) {
       atomicOr(a.status, DEV_BOUNDS);
       return;
@@ -597,7 +600,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
       const int head = g + 8 * r;
       if (head >= heads) continue;
-      if (here.t0 == 0) {
+      if (SHARED && here.t0 == 0) {
+        const size_t at = static_cast<size_t>(here.b) * a.Hq + h * group + q0 + head;
+        if (t == 0) reinterpret_cast<float2*>(a.own + static_cast<size_t>(a.B) * a.Hq * D)[at] = make_float2(m[r], l[r]);
+        store_rows<D, E4M3>(a.own + at * D, o, r, 1.f, t);
+      } else if (here.t0 == 0) {
         // (the value scale by itself: its quotient by l may be too small for a normal float)
         const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
         const size_t at = static_cast<size_t>(here.b) * a.Hq + h * group + q0 + head;
@@ -881,10 +888,77 @@ __global__ void __launch_bounds__(THREADS, THREADS == kJoinFew ? 2 : WIDE && D =
   }
 }
 
+// Joins, for every sequence and query head, what the tail's shares left with what the common
+// beginning's did (PagedAttnArgs): parts in the order of the keys, the beginning's first.  A warp per
+// row, a lane per D / 32 values.
 template <int D, bool E4M3, bool WIDE>
-cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) paged_shared_join_kernel(const DecodeArgs a, const SharedArgs p, int chunks, int grid, int tail) {
+  constexpr int TK = Geo<D, E4M3>::TK, ROWS = WIDE ? 16 : 8, V = D / 32;
+  constexpr float kShift = E4M3 ? 12.f : 0.f;
+  pdl_begin();
+  const int lane = lane_id();
+  const int row = blockIdx.x * 8 + warp_id();
+  if (row >= a.B * a.Hq) return;
+  const int b = row / a.Hq, head = row - b * a.Hq, group = a.Hq / a.Hkv, h = head / group, hh = head - h * group;
+  float top = -INFINITY, l_mul = 0.f, l_f32 = 0.f, acc[V] = {};
+  // a part: log2 maximum, sum of the weights as multiplied, their fp32 sum, the row's values
+  auto add = [&](float m, float mul, float f32, const float* o) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = o[V * lane + i];
+    const float up = fmaxf(top, m), f = m == -INFINITY ? 0.f : ex2(m - up), g = top == -INFINITY ? 0.f : ex2(top - up);
+    l_mul = fmaf(l_mul, g, mul * f);
+    l_f32 = fmaf(l_f32, g, f32 * f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(acc[i], g, v[i] * f);
+    top = up;
+  };
+  const int own = a.lens[b];
+  if (a.skip[b] > 0) {
+    const PagedAttnPlace at = paged_attn_place(p, b, h, hh);
+    for (int c = at.c0; c <= at.c1; ++c) {
+      const float* part = at.c0 == at.c1 ? p.whole : p.parts + (2 * static_cast<size_t>(c) + (c < at.c1 ? 1 : 0)) * paged_attn_part_floats(D);
+      const size_t r = at.c0 == at.c1 ? row : at.row, rows = at.c0 == at.c1 ? static_cast<size_t>(a.B) * a.Hq : kPagedAttnPartRows;
+      const float4 ml = reinterpret_cast<const float4*>(part)[r];
+      add(ml.x, ml.y, ml.z, part + 4 * rows + r * D);
+    }
+  }
+  if (own > 0) {
+    const int segs = a.Hkv * chunks, seg = h * chunks + hh / kHeads, r = hh % kHeads;
+    const long long* prefix = static_cast<const long long*>(a.ws);
+    const Shares shares = shares_of(prefix[a.B] * segs, grid, tail);
+    const long long size = positions_of<TK>(a, own), first = prefix[b] * segs + seg * size;
+    const int c0 = shares.of(first), c1 = shares.of(first + size - kSegCost - 1);
+    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
+    if (c0 == c1) {
+      const float2 ml = reinterpret_cast<const float2*>(a.own + static_cast<size_t>(a.B) * a.Hq * D)[row];
+      add(ml.x - kShift, ml.y, ml.y, a.own + static_cast<size_t>(row) * D);
+    } else {
+      const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
+      for (int i = 0; i < n; ++i) {
+        const int c = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
+        const float* part = parts + (2 * static_cast<size_t>(c) + (i < n - 1)) * part_floats(D, WIDE);
+        const float2 ml = reinterpret_cast<const float2*>(part)[r];
+        add(ml.x - kShift, ml.y, ml.y, part + 2 * ROWS + r * D);
+      }
+    }
+  }
+  const float inv = l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
+  float y[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) y[i] = E4M3 ? acc[i] * inv * a.v_scale : acc[i] * inv;
+  __nv_bfloat16* out = a.out + static_cast<size_t>(row) * D + V * lane;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(y[0], y[1]);
+  if (a.lse != nullptr && lane == 0) a.lse[row] = l_f32 == 0.f ? -INFINITY : (top + log2f(l_f32)) * 0.6931471805599453f;
+}
+
+template <int D, bool E4M3, bool WIDE>
+cudaError_t launch(const DecodeArgs& a, int chunks, int sms, const SharedArgs* shared, cudaStream_t stream) {
   constexpr int kSmem = kWarps * kStages * kStageBytes;
-  auto kernel = paged_decode_kernel<D, E4M3, WIDE>;
+  auto kernel = shared ? paged_decode_kernel<D, E4M3, WIDE, true> : paged_decode_kernel<D, E4M3, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   // two CTAs per SM, no more than the longest lists could give a tile to, and the last
@@ -898,6 +972,8 @@ cudaError_t launch(const DecodeArgs& a, int chunks, int sms, cudaStream_t stream
   const int tail = most >= 2LL * n * kWarps * kTailMin ? kTailPerSm * n : 0;
   const int grid = static_cast<int>(std::min<long long>(2 * n, most)) + tail;
   if ((e = launch_dependent(kernel, grid, kThreads, kSmem, stream, a, chunks, tail)) != cudaSuccess) return e;
+  if (shared)
+    return launch_dependent(paged_shared_join_kernel<D, E4M3, WIDE>, (a.B * a.Hq + 7) / 8, 256, 0, stream, a, *shared, chunks, grid, tail);
   const int segments = a.B * a.Hkv * chunks;
   if (segments <= sms / 8) {
     constexpr int kBlocks = (WIDE ? 16 : 8) / join_rows(WIDE, kJoinFew);
@@ -915,18 +991,24 @@ size_t paged_decode_workspace_bytes(int D, int group) {
   return parts_offset() + 2 * kMaxCtas * kWarps * part_floats(D, group > 8) * sizeof(float);
 }
 
-cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream) {
+cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, const SharedArgs* shared, cudaStream_t stream) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int group = a.Hq / a.Hkv, chunks = (group + kHeads - 1) / kHeads;
   const bool wide = group > 8;
-  if (a.D == 128) {
-    if (e4m3) return wide ? launch<128, true, true>(a, chunks, sms, stream) : launch<128, true, false>(a, chunks, sms, stream);
-    return wide ? launch<128, false, true>(a, chunks, sms, stream) : launch<128, false, false>(a, chunks, sms, stream);
-  }
-  if (e4m3) return wide ? launch<64, true, true>(a, chunks, sms, stream) : launch<64, true, false>(a, chunks, sms, stream);
-  return wide ? launch<64, false, true>(a, chunks, sms, stream) : launch<64, false, false>(a, chunks, sms, stream);
+#define MCS_DECODE_CASE(DD, EE, WW) \
+  if (a.D == (DD) && e4m3 == (EE) && wide == (WW)) return launch<DD, EE, WW>(a, chunks, sms, shared, stream);
+  MCS_DECODE_CASE(128, false, false)
+  MCS_DECODE_CASE(128, false, true)
+  MCS_DECODE_CASE(128, true, false)
+  MCS_DECODE_CASE(128, true, true)
+  MCS_DECODE_CASE(64, false, false)
+  MCS_DECODE_CASE(64, false, true)
+  MCS_DECODE_CASE(64, true, false)
+  MCS_DECODE_CASE(64, true, true)
+#undef MCS_DECODE_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace mcs

@@ -220,8 +220,23 @@ struct DecodeArgs {
   float* lse;                // [B, Hq], nullable
   void* ws;
   unsigned* status;
+  // behind a common beginning (lens are the tails'): its pages, and where whole rows go: their values
+  // [B * Hq, D], then (log2 maximum, sum) [B * Hq] float2
+  const int32_t* skip;       // [B]
+  float* own;
 };
-cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream);
+// A common beginning's result, for the join with the tails (see paged_list.cuh).
+struct SharedArgs {
+  int G, tokens, heads, chunks, segs, grid;
+  const int32_t* group_of;   // [B]
+  const int32_t* cu;         // [G + 1]
+  const int32_t* keys;       // [G]
+  const long long* places;   // [G + 1]
+  const float* whole;        // as PagedAttnArgs'
+  const float* parts;
+};
+// shared: null, or what the tails are joined with.
+cudaError_t launch_paged_decode(const DecodeArgs& a, bool e4m3, const SharedArgs* shared, cudaStream_t stream);
 size_t paged_decode_workspace_bytes(int D, int group);
 
 // Attention of many query rows per KV head over pages (see paged_attn.cu).
@@ -258,6 +273,25 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, const CUtensorMap* tq, con
                               const CUtensorMap* tv, bool e4m3, cudaStream_t stream);
 size_t paged_attn_parts_bytes(int D);
 size_t paged_attn_ends_bytes();
+// CTAs of the launch: shares of the list.
+cudaError_t paged_attn_grid(int* grid);
+
+// Groups of sequences with a common beginning: what the attention over the beginnings and over the
+// tails take (see mcs_paged_decode_shared).
+struct SharedPlanArgs {
+  int B, G, page, max_pages;
+  const int32_t* lens;       // [B]
+  const int32_t* starts;     // [G + 1]
+  const int32_t* shared;     // [G] pages
+  int32_t* tail;             // [B] tokens behind the beginning
+  int32_t* skip;             // [B] pages of the beginning
+  int32_t* group_of;         // [B]
+  int32_t* cu;               // [G + 1]
+  int32_t* keys;             // [G] tokens of the beginning
+  int32_t* leader;           // [G] the sequence whose table row is read for it
+  unsigned* status;
+};
+cudaError_t launch_shared_plan(const SharedPlanArgs& a, cudaStream_t stream);
 
 // Tiled maps: rows [rows][D] of bf16 in boxes of box_rows x 64 with 128-byte swizzle, or of bytes in
 // boxes of box_rows x D without; and q [T][H][D] bf16 with tokens `stride` elements apart in boxes of

@@ -95,7 +95,7 @@ mcs_status run_decode(const mcs_paged* p, const void* q, const void* k_cache, co
   a.ws = ws;
   mcs_status s = status_word(&a.status);
   if (s != MCS_OK) return s;
-  return finish(mcs::launch_paged_decode(a, e4m3, stream), what);
+  return finish(mcs::launch_paged_decode(a, e4m3, nullptr, stream), what);
 }
 
 // What the attention of many rows takes from the params; and its tensor maps.
@@ -129,6 +129,30 @@ mcs_status many_rows(const mcs_paged* p, int T, const void* q, const void* k_cac
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace of the decode behind common beginnings.
+struct SharedWs {
+  size_t decode, ends, parts, places, whole, own, ints, total;
+};
+SharedWs shared_ws(const mcs_paged* p) {
+  const size_t rows = static_cast<size_t>(p->B) * p->Hq;
+  SharedWs w;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t x = at;
+    at += round256(n);
+    return x;
+  };
+  w.decode = take(mcs::paged_decode_workspace_bytes(p->D, p->Hq / p->Hkv));
+  w.ends = take(mcs::paged_attn_ends_bytes());
+  w.parts = take(mcs::paged_attn_parts_bytes(p->D));
+  w.places = take((p->B + 1) * sizeof(long long));
+  w.whole = take(rows * (4 + p->D) * sizeof(float));
+  w.own = take(rows * (2 + p->D) * sizeof(float));
+  w.ints = take((6 * static_cast<size_t>(p->B) + 1) * sizeof(int32_t));
+  w.total = at;
+  return w;
+}
 
 mcs_status check_rope(const mcs_rope* p) {
   if (p == nullptr) return MCS_ERR_INVALID_ARG;
@@ -347,6 +371,94 @@ mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* 
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(mcs::paged_attn_ends_bytes()));
   return finish(mcs::launch_paged_attn(a, &tq, &tk, &tv, p->kv == MCS_KV_E4M3, stream),
                 "paged attention launch");
+}
+
+size_t mcs_paged_decode_shared_workspace(const mcs_paged* p) {
+  return check_paged(p) == MCS_OK ? shared_ws(p).total : 0;
+}
+
+mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_table,
+                                   const int32_t* lens, const int32_t* group_start,
+                                   const int32_t* shared_pages, void* out, float* lse, void* ws,
+                                   size_t ws_bytes, cudaStream_t stream) {
+  mcs_status s = check_paged(p);
+  if (s != MCS_OK) return s;
+  if (groups < 1 || groups > p->B) return MCS_ERR_INVALID_ARG;
+  if (!good(q) || !good(k_cache) || !good(v_cache) || !good(out) || !good_ints(block_table) ||
+      !good_ints(lens) || !good_ints(group_start) || !good_ints(shared_pages) || !aligned(lse, 4))
+    return MCS_ERR_INVALID_ARG;
+  if (!good(ws) || ws_bytes < mcs_paged_decode_shared_workspace(p)) return MCS_ERR_WORKSPACE;
+  const SharedWs w = shared_ws(p);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int32_t* ints = reinterpret_cast<int32_t*>(base + w.ints);
+  mcs::SharedPlanArgs plan{};
+  plan.B = p->B;
+  plan.G = groups;
+  plan.page = p->page;
+  plan.max_pages = p->max_pages;
+  plan.lens = lens;
+  plan.starts = group_start;
+  plan.shared = shared_pages;
+  plan.tail = ints;
+  plan.skip = ints + p->B;
+  plan.group_of = ints + 2 * p->B;
+  plan.keys = ints + 3 * p->B;
+  plan.leader = ints + 4 * p->B;
+  plan.cu = ints + 5 * p->B;
+  mcs::PagedAttnArgs a{};
+  CUtensorMap tq{}, tk{}, tv{};
+  if ((s = many_rows(p, p->B, q, k_cache, v_cache, &a, &tq, &tk, &tv)) != MCS_OK) return s;
+  a.G = groups;
+  a.table = block_table;
+  a.row_of = plan.leader;
+  a.cu = plan.cu;
+  a.keys = plan.keys;
+  a.whole = reinterpret_cast<float*>(base + w.whole);
+  a.parts = reinterpret_cast<float*>(base + w.parts);
+  a.ends = reinterpret_cast<int4*>(base + w.ends);
+  a.places = reinterpret_cast<long long*>(base + w.places);
+  plan.status = a.status;
+  mcs::SharedArgs join{};
+  join.G = groups;
+  join.tokens = a.tokens;
+  join.heads = a.heads;
+  join.chunks = a.chunks;
+  join.segs = p->Hkv * a.chunks;
+  join.group_of = plan.group_of;
+  join.cu = plan.cu;
+  join.keys = plan.keys;
+  join.places = a.places;
+  join.whole = a.whole;
+  join.parts = a.parts;
+  mcs::DecodeArgs d{};
+  d.B = p->B;
+  d.Hq = p->Hq;
+  d.Hkv = p->Hkv;
+  d.D = p->D;
+  d.page = p->page;
+  d.num_pages = p->num_pages;
+  d.max_pages = p->max_pages;
+  d.q_stride = a.q_stride;
+  d.scale_log2 = a.scale_log2;
+  d.v_scale = a.v_scale;
+  d.q = a.q;
+  d.k = k_cache;
+  d.v = v_cache;
+  d.table = block_table;
+  d.lens = plan.tail;
+  d.out = static_cast<__nv_bfloat16*>(out);
+  d.lse = lse;
+  d.ws = base + w.decode;
+  d.status = a.status;
+  d.skip = plan.skip;
+  d.own = reinterpret_cast<float*>(base + w.own);
+  cudaError_t e = mcs::paged_attn_grid(&join.grid);
+  const bool e4m3 = p->kv == MCS_KV_E4M3;
+  if (e == cudaSuccess) e = mcs::launch_shared_plan(plan, stream);
+  if (e == cudaSuccess) e = mcs::launch_paged_attn(a, &tq, &tk, &tv, e4m3, stream);
+  if (e == cudaSuccess) e = mcs::launch_paged_decode(d, e4m3, &join, stream);
+  return finish(e, "paged shared decode launch");
 }
 
 mcs_status mcs_qk_norm_rope(const mcs_rope* p, const void* q, const void* k, const float* wq,

@@ -40,19 +40,20 @@
 
 #include "internal.h"
 #include "launch.cuh"
+#include "paged_list.cuh"
 #include "ptx.cuh"
 
 namespace mcs {
 namespace {
 
-constexpr int BM = 128;   // rows per unit
-constexpr int BN = 128;   // keys per tile
+constexpr int BM = kPagedAttnRows;  // rows per unit
+constexpr int BN = kPagedAttnKeys;  // keys per tile
+constexpr int kSegCost = kPagedAttnSegCost;
 constexpr int kLoaders = 7;
 constexpr int kFirstLoader = 8;
 constexpr int kMmaWarp = kFirstLoader + kLoaders;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxSms = 160;
-constexpr int kSegCost = 2;  // what changing the segment costs, in steps
 constexpr int kSlab = 16;    // keys that surely lie in one page
 constexpr int kSlabs = BN / kSlab;
 constexpr int kWindow = 32 / kSlabs;  // tiles whose pages a warp looks up at once
@@ -90,67 +91,6 @@ struct Layout {
 };
 
 // ------------------------------------------------------------------ the list
-
-// sum of floor((a i + b) / m) over i < n: Euclid's algorithm on (m, a), a and m small.
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long sum = 0;
-  while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y - n * m;
-    const long long t = m;
-    m = a;
-    a = t;
-  }
-  return sum;
-}
-
-// A sequence of the list (shared beginnings: a group): n tokens, rows cu .. cu + n of q, keys
-// [0, keys), of which token t sees keys - n + t + 1 (causal) or all.
-struct Seq {
-  int cu, n, keys;
-};
-__device__ __forceinline__ int tiles_until(const PagedAttnArgs& a, const Seq& s, int e) {
-  return static_cast<int>((static_cast<long long>(a.causal ? s.keys - s.n + e : s.keys) + BN - 1) / BN);
-}
-__device__ __forceinline__ bool load_seq(const PagedAttnArgs& a, int g, Seq& s, bool report) {
-  const int lo = a.cu[g], hi = a.cu[g + 1];
-  s.keys = a.keys[g];
-  s.cu = lo;
-  s.n = 0;
-  if (hi == lo) return false;
-  if (lo < 0 || hi < lo || hi > a.T || s.keys < 0 ||
-      static_cast<long long>(s.keys) > static_cast<long long>(a.max_pages) * a.page ||
-      (a.causal && hi - lo > s.keys)) {
-    if (report) atomicOr(a.status, DEV_BOUNDS);
-    return false;
-  }
-  s.n = s.keys > 0 ? hi - lo : 0;
-  return s.n > 0;
-}
-__device__ __forceinline__ int units_of(const PagedAttnArgs& a, const Seq& s) {
-  return (s.n + a.tokens - 1) / a.tokens;
-}
-// Positions of the first k pairs of a sequence's KV head.
-__device__ __forceinline__ long long pairs_upto(const PagedAttnArgs& a, const Seq& s, int k) {
-  if (k <= 0) return 0;
-  if (!a.causal) return static_cast<long long>(k) * (tiles_until(a, s, s.n) + kSegCost);
-  const int w = 2 * a.tokens;
-  // the last pair may end with the sequence, inside its second unit
-  const bool cut = static_cast<long long>(k) * w > s.n;
-  const int whole = cut ? k - 1 : k;
-  return floor_sum(whole, BN, w, static_cast<long long>(s.keys) - s.n + w + BN - 1) +
-         (cut ? tiles_until(a, s, s.n) : 0) + static_cast<long long>(k) * kSegCost;
-}
-__device__ __forceinline__ long long positions_of(const PagedAttnArgs& a, const Seq& s) {
-  const int units = units_of(a, s);
-  return pairs_upto(a, s, units / 2) +
-         ((units & 1) ? (tiles_until(a, s, s.n) + 1) / 2 + kSegCost : 0);
-}
 
 // A walk over a CTA's share, segment by segment; every role makes it by itself.
 struct Walk {
@@ -333,11 +273,8 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 80, "misc");
 
-// Parts of segments that cross shares: slot 2 c of share c for a segment that ends there, 2 c + 1
-// for one that goes on.  (log2 maximum, sum of the weights as multiplied, their fp32 sum, 0) of
-// the 256 rows, then the rows' D sums.
-constexpr int kPartRows = 2 * BM;
-__host__ __device__ constexpr size_t part_floats(int D) { return static_cast<size_t>(kPartRows) * (4 + D); }
+constexpr int kPartRows = kPagedAttnPartRows;
+__host__ __device__ constexpr size_t part_floats(int D) { return paged_attn_part_floats(D); }
 
 // ------------------------------------------------------------------ the kernel
 
@@ -487,12 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.left = hi - lo;
     w.count = static_cast<int>(min(static_cast<long long>(w.steps - w.t0), w.left));
     if (w.t0 > 0 && w.count > 0 && w.t0 + w.count == w.steps) {
-      // the largest share that begins at or in front of the segment's first position
-      const long long x = lo - w.t0;
-      int c = static_cast<int>(x * shares / all);
-      while (c + 1 < shares && all * (c + 1) / shares <= x) ++c;
-      while (c > 0 && all * c / shares > x) --c;
-      part_from = c;
+      part_from = share_of(lo - w.t0, all, shares);
     }
     if (tid == 0) {
       a.ends[blockIdx.x] = make_int4(part_from >= 0 ? w.g : -1, w.head, w.i, part_from);
@@ -1168,6 +1100,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
+// Which sequences a common beginning serves.  One CTA: it is a few reads and writes per sequence.
+// Bounds that do not ascend from 0 to B leave every sequence by itself; a group of which fewer than
+// two sequences reach the beginning's end, too.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlanArgs a) {
+  pdl_begin();
+  const int tid = threadIdx.x, lane = lane_id();
+  const long long room = static_cast<long long>(a.max_pages) * a.page;
+  bool bad = tid == 0 && (a.starts[0] != 0 || a.starts[a.G] != a.B);
+  for (int g = tid; g < a.G; g += kPlanThreads) bad = bad || a.starts[g] > a.starts[g + 1];
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    const int len = a.lens[b];
+    const bool good = len >= 0 && len <= room;
+    if (!good) atomicOr(a.status, DEV_BOUNDS);
+    a.tail[b] = good ? len : 0;
+    a.skip[b] = 0;
+    a.group_of[b] = -1;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
+  for (int g = tid; g <= a.G; g += kPlanThreads) a.cu[g] = bad ? 0 : a.starts[g];
+  for (int g = warp_id(); g < a.G; g += kPlanThreads / 32) {
+    const int lo = bad ? 0 : a.starts[g], hi = bad ? 0 : a.starts[g + 1], pages = a.shared[g];
+    const bool good = pages >= 0 && pages <= a.max_pages;
+    const int keys = good ? pages * a.page : 0;
+    bool wrong = !good;
+    int live = 0, leader = 0x7fffffff;
+    for (int b = lo + lane; b < hi; b += 32) {
+      const int len = a.tail[b];
+      wrong = wrong || (len > 0 && len < keys);
+      if (len > 0 && len >= keys) {
+        ++live;
+        leader = min(leader, b);
+      }
+    }
+    live = __reduce_add_sync(0xffffffffu, live);
+    leader = __reduce_min_sync(0xffffffffu, leader);
+    if (wrong) atomicOr(a.status, DEV_BOUNDS);
+    const bool use = live > 1 && keys > 0;
+    if (lane == 0) {
+      a.keys[g] = use ? keys : 0;
+      a.leader[g] = use ? leader : 0;
+    }
+    for (int b = lo + lane; use && b < hi; b += 32) {
+      const int len = a.tail[b];
+      if (len == 0 || len < keys) continue;
+      a.tail[b] = len - keys;
+      a.skip[b] = pages;
+      a.group_of[b] = g;
+    }
+  }
+}
+
 // Joins the parts of the segment that ends in share blockIdx.x / kJoinBlocks and begins in an
 // earlier one, in the order of the shares: kJoinRows rows per block, 8 threads to a row.
 constexpr int kJoinRows = 32;
@@ -1234,15 +1219,24 @@ cudaError_t launch(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensor
 
 }  // namespace
 
+cudaError_t launch_shared_plan(const SharedPlanArgs& a, cudaStream_t stream) {
+  return launch_dependent(shared_plan_kernel, 1, kPlanThreads, 0, stream, a);
+}
+
 size_t paged_attn_parts_bytes(int D) { return 2 * kMaxSms * part_floats(D) * sizeof(float); }
 size_t paged_attn_ends_bytes() { return kMaxSms * sizeof(int4); }
 
+cudaError_t paged_attn_grid(int* grid) {
+  const cudaError_t e = sm_count(grid);
+  *grid = std::min(*grid, kMaxSms);
+  return e;
+}
+
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
                               bool e4m3, cudaStream_t stream) {
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  int grid = 0;
+  const cudaError_t e = paged_attn_grid(&grid);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(sms, kMaxSms);
   if (a.D == 128)
     return e4m3 ? launch<128, true>(a, tq, tk, tv, grid, stream) : launch<128, false>(a, tq, tk, tv, grid, stream);
   return e4m3 ? launch<64, true>(a, tq, tk, tv, grid, stream) : launch<64, false>(a, tq, tk, tv, grid, stream);

@@ -28,7 +28,8 @@ __all__ = [
     "mcs_sparse_attn_e4m3", "Paged", "paged", "KV_BF16", "KV_E4M3", "mcs_paged_plan",
     "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
     "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
-    "mcs_paged_attn_workspace", "mcs_paged_attn", "Rope",
+    "mcs_paged_attn_workspace", "mcs_paged_attn", "mcs_paged_decode_shared_workspace",
+    "mcs_paged_decode_shared", "Rope",
     "rope_params", "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace",
     "mcs_qk_norm_rope_backward",
 ]
@@ -46,7 +47,8 @@ EXPORTED = (
     "mcs_quantize_e4m3", "mcs_sparse_attn_e4m3",
     "mcs_paged_plan", "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
     "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
-    "mcs_paged_attn_workspace", "mcs_paged_attn",
+    "mcs_paged_attn_workspace", "mcs_paged_attn", "mcs_paged_decode_shared_workspace",
+    "mcs_paged_decode_shared",
     "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace", "mcs_qk_norm_rope_backward",
 )
 
@@ -175,6 +177,8 @@ _SIGS = {
                                 _st),
     "mcs_paged_attn_workspace": ([_gp], _sz),
     "mcs_paged_attn": ([_gp, _i] + [_vp] * 9 + [_sz, _vp], _st),
+    "mcs_paged_decode_shared_workspace": ([_gp], _sz),
+    "mcs_paged_decode_shared": ([_gp, _i] + [_vp] * 10 + [_sz, _vp], _st),
     "mcs_qk_norm_rope": ([_rp] + [_vp] * 10, _st),
     "mcs_qk_norm_rope_backward_workspace": ([_rp], _sz),
     "mcs_qk_norm_rope_backward": ([_rp] + [_vp] * 14 + [_sz, _vp], _st),
@@ -747,6 +751,30 @@ def mcs_paged_attn(p: Paged, q, k_cache, v_cache, block_table, lens, cu_new, out
         _at(dev, out, _BF, rows, "out"),
         None if lse is None else _at(dev, lse, _F32, (T, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
         _queue(stream, dev)), "mcs_paged_attn")
+
+
+def mcs_paged_decode_shared_workspace(p: Paged) -> int:
+    return lib().mcs_paged_decode_shared_workspace(ctypes.byref(p))
+
+
+def mcs_paged_decode_shared(p: Paged, q, k_cache, v_cache, block_table, lens, group_start,
+                            shared_pages, out, ws, lse=None, stream=None):
+    """Sequences group_start[g] .. group_start[g + 1] - 1 have their first shared_pages[g] pages in
+    common."""
+    if not isinstance(shared_pages, torch.Tensor) or shared_pages.dim() != 1:
+        raise ValueError("shared_pages must be a [groups] tensor")
+    G = _count(shared_pages.shape[0], "shared_pages")
+    dev, B, Hq, D, kv = _device(stream), p.B, p.Hq, p.D, p.kv
+    cache, rows = (p.num_pages, p.Hkv, p.page, D), (B, Hq, D)
+    _check(lib().mcs_paged_decode_shared(
+        ctypes.byref(p), G, _rows_at(dev, q, _BF, rows, p.q_stride, "q"),
+        _cache_at(dev, k_cache, kv, cache, "k_cache"),
+        _cache_at(dev, v_cache, kv, cache, "v_cache"),
+        _at(dev, block_table, _I32, (B, p.max_pages), "block_table"),
+        _at(dev, lens, _I32, (B,), "lens"), _at(dev, group_start, _I32, (G + 1,), "group_start"),
+        _at(dev, shared_pages, _I32, (G,), "shared_pages"), _at(dev, out, _BF, rows, "out"),
+        None if lse is None else _at(dev, lse, _F32, (B, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
+        _queue(stream, dev)), "mcs_paged_decode_shared")
 
 
 # ---------------------------------------------------------------- norm and rotation
