@@ -591,6 +591,73 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
                                    size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Pages that several sequences hold.  extra [num_pages] int32 counts the holders
+ * of a page beyond the first: 0 for a page of one sequence, and for a free one, so
+ * that mcs_paged_plan needs not know of it (start with zeros).  One call renews the
+ * tables, which all layers share; what it asks to be copied it lists in `moves`, and
+ * mcs_paged_copy does that for each layer's caches:
+ *   moves [., 3] int32: (from, to, rows), the first `rows` rows of page `from`
+ *   to page `to`; (-1, -1, 0) where there is nothing to copy.
+ *
+ * mcs_paged_fork: n sequences (1 <= n <= 4096) take the place of the B old ones.  New
+ * sequence i continues parents[i], an old sequence's number; or is empty (-1).  An
+ * old sequence may have any number of children (several answers, beams) or none
+ * (it ends).  lens_out [n] and table_out [n, max_pages] (-1 past a sequence's last
+ * page) are the new ones'.  Full pages are shared.  The last page, if it is
+ * not full, stays with the first child when nobody else holds it; every
+ * other child gets a fresh one from free_pages [n_free], from position free_head[0] on
+ * in the order of the children, and a row of `moves` [n, 3], in its own
+ * place.  Pages that nobody holds any more are free again: in ascending order
+ * they are put in front of what is left, so that free_out from head_out[0] =
+ * free_head[0] + fresh pages - freed pages on is the free list (what stands in
+ * front is not touched); a page freed and one taken by the same call are
+ * never the same.  Apart from the outputs that may be inputs (extra_out: extra,
+ * free_out: free_pages, head_out: free_head) no output overlaps an input.  A
+ * request that cannot be met (parents outside [-1, B), too few free pages, a length or
+ * a page outside the cache, holders below zero, a free list without room) sets
+ * MCS_ERR_BOUNDS in the device status and takes nothing: all rows of `moves` are
+ * (-1, -1, 0) and no other output is written.
+ * Copies of a call belong in front of the next mcs_paged_write.
+ */
+size_t mcs_paged_fork_workspace(const mcs_paged* p);
+mcs_status mcs_paged_fork(const mcs_paged* p, int n, const int32_t* parents, const int32_t* lens,
+                          const int32_t* block_table, const int32_t* extra,
+                          const int32_t* free_pages, int n_free, const int32_t* free_head,
+                          int32_t* lens_out, int32_t* table_out, int32_t* extra_out,
+                          int32_t* free_out, int32_t* head_out, int32_t* moves, void* ws,
+                          size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Moves pages to the front of the cache, so that its end is free: the last page
+ * in use goes to the first free one, the last but one to the second, and so
+ * on, while that lies in front of it, at most `most` pages (moves [most, 3], filled
+ * from the front).  In use is every page that holds a token of one of the B
+ * sequences; ALL others are free afterwards, and extra_out is 0 for them.  table_out
+ * [B, max_pages] has the new numbers (entries past a sequence's last page as in
+ * block_table), extra_out the holders of the pages where they are now,
+ * and free_out [n_free] from head_out[0] on all free pages, ascending.
+ * table_out may be block_table and extra_out may be extra.  n_free smaller than the
+ * number of free pages, or a length or a page outside the cache, sets
+ * MCS_ERR_BOUNDS and changes nothing, as above.  0 <= most.
+ */
+size_t mcs_paged_compact_workspace(const mcs_paged* p);
+mcs_status mcs_paged_compact(const mcs_paged* p, const int32_t* lens, const int32_t* block_table,
+                             const int32_t* extra, int32_t* table_out, int32_t* extra_out,
+                             int32_t* free_out, int n_free, int32_t* head_out, int32_t* moves,
+                             int most, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Copies what the n rows of `moves` say, in both caches (all KV heads) and, when
+ * given, the pages' means in k_mean (nullable).  Rows past the copied ones
+ * stay as they were in page `to`.  No page is written by two rows, or read by
+ * one and written by another.  A row with from < 0 is skipped; one that names a page
+ * outside the cache or more rows than a page has sets MCS_ERR_BOUNDS and is
+ * skipped.
+ */
+mcs_status mcs_paged_copy(const mcs_paged* p, int n, const int32_t* moves, void* k_cache,
+                          void* v_cache, void* k_mean, cudaStream_t stream);
+
+/*
  * What stands between a block's projections and its attention: RMS norm of
  * each head of q and k, then the rotation of its first `rot` values by the
  * token's angles, in one pass (for mcs_group, mcs_dense_attn and the sparse

@@ -136,6 +136,94 @@ def attn(q, k_cache, v_cache, table, lens, cu, scale, num_pages=None):
     return out, lse, absv, size
 
 
+def fork(parents, lens, table, extra, free, head, page, num_pages):
+    """(lens, table, extra, free list from its head on, head, moves) of the new sequences, or None
+    for a request that cannot be met.  Walks over the old sequences' pages with a dictionary of
+    holders."""
+    B, P = table.shape
+    if any(not 0 <= n <= P * page for n in lens) or any(not -1 <= p < B for p in parents):
+        return None
+    holders = {}
+    for b in range(B):
+        for j in range(-(-int(lens[b]) // page)):
+            if not 0 <= table[b, j] < num_pages:
+                return None
+            holders[int(table[b, j])] = int(extra[table[b, j]]) + 1
+    before = dict(holders)
+    if not 0 <= head <= len(free):
+        return None
+    n = len(parents)
+    lens_out, table_out, moves = np.zeros(n, int), np.full((n, P), -1), np.tile([-1, -1, 0], (n, 1))
+    for b in range(B):  # the old sequences let go
+        for j in range(-(-int(lens[b]) // page)):
+            holders[int(table[b, j])] -= 1
+    kept, taken = set(), []
+    for i, p in enumerate(parents):
+        if p < 0:
+            continue
+        lens_out[i] = lens[p]
+        for j in range(-(-int(lens[p]) // page)):
+            pid = int(table[p, j])
+            if (j + 1) * page > lens[p] and (p in kept or before[pid] > 1):  # an open page that is not the child's to keep
+                at = head + len(taken)
+                if at >= len(free) or not 0 <= free[at] < num_pages:
+                    return None
+                moves[i] = pid, free[at], lens[p] % page
+                taken.append(int(free[at]))
+                table_out[i, j] = free[at]
+            else:
+                table_out[i, j] = pid
+                holders[pid] += 1
+        kept.add(p)
+    if any(h < 0 for h in holders.values()):
+        return None
+    freed = sorted(pid for pid, h in holders.items() if h == 0 and before[pid] > 0)
+    head_out = head + len(taken) - len(freed)
+    if head_out < 0:
+        return None
+    extra_out = np.array(extra)
+    for pid, h in holders.items():
+        extra_out[pid] = max(h - 1, 0)
+    return lens_out, table_out, extra_out, freed + [int(x) for x in free[head + len(taken):]], head_out, moves
+
+
+def compact(lens, table, extra, n_free, most, page, num_pages):
+    """(table, extra, free list from its head on, head, moves), or None."""
+    B, P = table.shape
+    if any(not 0 <= n <= P * page for n in lens):
+        return None
+    fill = {}
+    for b in range(B):
+        for j in range(-(-int(lens[b]) // page)):
+            if not 0 <= table[b, j] < num_pages:
+                return None
+            fill[int(table[b, j])] = max(fill.get(int(table[b, j]), 0), min(page, int(lens[b]) - j * page))
+    holes = [p for p in range(num_pages) if p not in fill]
+    if n_free < len(holes):
+        return None
+    to = {p: p for p in fill}
+    moves = np.tile([-1, -1, 0], (most, 1))
+    for i, (src, dst) in enumerate(zip(sorted(fill, reverse=True), holes)):
+        if i < most and src > dst:
+            to[src], moves[i] = dst, (src, dst, fill[src])
+    table_out, extra_out = table.copy(), np.zeros(num_pages, int)
+    for b in range(B):
+        for j in range(-(-int(lens[b]) // page)):
+            table_out[b, j] = to[int(table[b, j])]
+    for src, dst in to.items():
+        extra_out[dst] = extra[src]
+    free = [p for p in range(num_pages) if p not in to.values()]
+    return table_out, extra_out, free, n_free - len(free), moves
+
+
+def copy(moves, k_cache, v_cache, k_mean):
+    for src, dst, rows in moves:
+        if src >= 0:
+            k_cache[dst, :, :rows], v_cache[dst, :, :rows] = k_cache[src, :, :rows].copy(), v_cache[src, :, :rows].copy()
+            if k_mean is not None:
+                k_mean[dst] = k_mean[src]
+
+
 def _pairs(D, rot, interleaved):
     one = np.arange(0, rot, 2) if interleaved else np.arange(rot // 2)
     return one, one + (1 if interleaved else rot // 2)

@@ -301,6 +301,42 @@ bool make_query_map(CUtensorMap* m, const void* base, int T, int H, int D, long 
 // MCS_TEST_FAULT (see mcs_api.cu).
 int test_fault();
 
+// Pages that several sequences hold (see pages.cu).
+struct PagesArgs {
+  int B, page, num_pages, max_pages, n_free;
+  int n;                     // fork: new sequences; compaction: moves at most
+  const int32_t* parents;    // [n] fork
+  const int32_t* lens;       // [B]
+  const int32_t* table;      // [B, max_pages]
+  const int32_t* extra;      // [num_pages] holders beyond the first
+  const int32_t* free_pages; // [n_free] fork
+  const int32_t* free_head;  // [1] fork
+  int32_t* lens_out;         // [n] fork
+  int32_t* table_out;        // [n or B, max_pages]; compaction: may be table
+  int32_t* extra_out;        // [num_pages], may be extra
+  int32_t* free_out;         // [n_free], may be free_pages
+  int32_t* head_out;         // [1], may be free_head
+  int32_t* moves;            // [n, 3]
+  int32_t* ws;
+  unsigned* status;
+};
+cudaError_t launch_paged_fork(const PagesArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_compact(const PagesArgs& a, cudaStream_t stream);
+size_t paged_fork_workspace_bytes(int num_pages);
+size_t paged_compact_workspace_bytes(int num_pages);
+
+struct CopyArgs {
+  int n, Hkv, page, num_pages;
+  int row_words, mean_words; // 16-byte words of a row of the caches, and of a page's mean per head
+  int parts;                 // set by the launcher: pieces of a page
+  const int32_t* moves;      // [n, 3]
+  void* k;
+  void* v;
+  void* mean;                // nullable
+  unsigned* status;
+};
+cudaError_t launch_paged_copy(CopyArgs a, cudaStream_t stream);
+
 // ---------------------------------------------------------------- norm and rotation
 
 struct RopeArgs {

@@ -461,6 +461,111 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
   return finish(e, "paged shared decode launch");
 }
 
+size_t mcs_paged_fork_workspace(const mcs_paged* p) {
+  return check_paged(p) == MCS_OK ? mcs::paged_fork_workspace_bytes(p->num_pages) : 0;
+}
+
+mcs_status mcs_paged_fork(const mcs_paged* p, int n, const int32_t* parents, const int32_t* lens,
+                          const int32_t* block_table, const int32_t* extra,
+                          const int32_t* free_pages, int n_free, const int32_t* free_head,
+                          int32_t* lens_out, int32_t* table_out, int32_t* extra_out,
+                          int32_t* free_out, int32_t* head_out, int32_t* moves, void* ws,
+                          size_t ws_bytes, cudaStream_t stream) {
+  mcs_status s = check_paged(p);
+  if (s != MCS_OK) return s;
+  if (n < 1 || n_free < 0) return MCS_ERR_INVALID_ARG;
+  if (n > 4096 || n_free > (1 << 30)) return MCS_ERR_UNSUPPORTED;
+  if (!good_ints(parents) || !good_ints(lens) || !good_ints(block_table) || !good_ints(extra) ||
+      (n_free > 0 && (!good_ints(free_pages) || !good_ints(free_out))) || !good_ints(free_head) ||
+      !good_ints(lens_out) || !good_ints(table_out) || !good_ints(extra_out) ||
+      !good_ints(head_out) || !good_ints(moves) || table_out == block_table || lens_out == lens)
+    return MCS_ERR_INVALID_ARG;
+  if (!good(ws) || ws_bytes < mcs_paged_fork_workspace(p)) return MCS_ERR_WORKSPACE;
+  mcs::PagesArgs a{};
+  a.B = p->B;
+  a.page = p->page;
+  a.num_pages = p->num_pages;
+  a.max_pages = p->max_pages;
+  a.n_free = n_free;
+  a.n = n;
+  a.parents = parents;
+  a.lens = lens;
+  a.table = block_table;
+  a.extra = extra;
+  a.free_pages = free_pages;
+  a.free_head = free_head;
+  a.lens_out = lens_out;
+  a.table_out = table_out;
+  a.extra_out = extra_out;
+  a.free_out = free_out;
+  a.head_out = head_out;
+  a.moves = moves;
+  a.ws = static_cast<int32_t*>(ws);
+  if ((s = status_word(&a.status)) != MCS_OK) return s;
+  return finish(mcs::launch_paged_fork(a, stream), "paged fork launch");
+}
+
+size_t mcs_paged_compact_workspace(const mcs_paged* p) {
+  return check_paged(p) == MCS_OK ? mcs::paged_compact_workspace_bytes(p->num_pages) : 0;
+}
+
+mcs_status mcs_paged_compact(const mcs_paged* p, const int32_t* lens, const int32_t* block_table,
+                             const int32_t* extra, int32_t* table_out, int32_t* extra_out,
+                             int32_t* free_out, int n_free, int32_t* head_out, int32_t* moves,
+                             int most, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  mcs_status s = check_paged(p);
+  if (s != MCS_OK) return s;
+  if (most < 0 || n_free < 0) return MCS_ERR_INVALID_ARG;
+  if (most > (1 << 28) || n_free > (1 << 30)) return MCS_ERR_UNSUPPORTED;
+  if (!good_ints(lens) || !good_ints(block_table) || !good_ints(extra) || !good_ints(table_out) ||
+      !good_ints(extra_out) || (n_free > 0 && !good_ints(free_out)) || !good_ints(head_out) ||
+      (most > 0 && !good_ints(moves)))
+    return MCS_ERR_INVALID_ARG;
+  if (!good(ws) || ws_bytes < mcs_paged_compact_workspace(p)) return MCS_ERR_WORKSPACE;
+  mcs::PagesArgs a{};
+  a.B = p->B;
+  a.page = p->page;
+  a.num_pages = p->num_pages;
+  a.max_pages = p->max_pages;
+  a.n_free = n_free;
+  a.n = most;
+  a.lens = lens;
+  a.table = block_table;
+  a.extra = extra;
+  a.table_out = table_out;
+  a.extra_out = extra_out;
+  a.free_out = free_out;
+  a.head_out = head_out;
+  a.moves = moves;
+  a.ws = static_cast<int32_t*>(ws);
+  if ((s = status_word(&a.status)) != MCS_OK) return s;
+  return finish(mcs::launch_paged_compact(a, stream), "paged compaction launch");
+}
+
+mcs_status mcs_paged_copy(const mcs_paged* p, int n, const int32_t* moves, void* k_cache,
+                          void* v_cache, void* k_mean, cudaStream_t stream) {
+  mcs_status s = check_paged(p);
+  if (s != MCS_OK) return s;
+  if (n < 0) return MCS_ERR_INVALID_ARG;
+  if (n > (1 << 28)) return MCS_ERR_UNSUPPORTED;
+  if (n == 0) return MCS_OK;
+  if (!good_ints(moves) || !good(k_cache) || !good(v_cache) || !aligned(k_mean, 16))
+    return MCS_ERR_INVALID_ARG;
+  mcs::CopyArgs a{};
+  a.n = n;
+  a.Hkv = p->Hkv;
+  a.page = p->page;
+  a.num_pages = p->num_pages;
+  a.row_words = p->D * (p->kv == MCS_KV_E4M3 ? 1 : 2) / 16;
+  a.mean_words = p->D / 8;
+  a.moves = moves;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.mean = k_mean;
+  if ((s = status_word(&a.status)) != MCS_OK) return s;
+  return finish(mcs::launch_paged_copy(a, stream), "paged copy launch");
+}
+
 mcs_status mcs_qk_norm_rope(const mcs_rope* p, const void* q, const void* k, const float* wq,
                             const float* wk, const float* cos_table, const float* sin_table,
                             const int32_t* positions, void* q_out, void* k_out,

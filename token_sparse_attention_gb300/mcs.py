@@ -29,7 +29,8 @@ __all__ = [
     "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
     "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
     "mcs_paged_attn_workspace", "mcs_paged_attn", "mcs_paged_decode_shared_workspace",
-    "mcs_paged_decode_shared", "Rope",
+    "mcs_paged_decode_shared", "mcs_paged_fork_workspace", "mcs_paged_fork",
+    "mcs_paged_compact_workspace", "mcs_paged_compact", "mcs_paged_copy", "Rope",
     "rope_params", "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace",
     "mcs_qk_norm_rope_backward",
 ]
@@ -48,7 +49,8 @@ EXPORTED = (
     "mcs_paged_plan", "mcs_paged_write", "mcs_paged_decode_workspace", "mcs_paged_decode",
     "mcs_paged_select_workspace", "mcs_paged_select", "mcs_paged_decode_sparse",
     "mcs_paged_attn_workspace", "mcs_paged_attn", "mcs_paged_decode_shared_workspace",
-    "mcs_paged_decode_shared",
+    "mcs_paged_decode_shared", "mcs_paged_fork_workspace", "mcs_paged_fork",
+    "mcs_paged_compact_workspace", "mcs_paged_compact", "mcs_paged_copy",
     "mcs_qk_norm_rope", "mcs_qk_norm_rope_backward_workspace", "mcs_qk_norm_rope_backward",
 )
 
@@ -179,6 +181,11 @@ _SIGS = {
     "mcs_paged_attn": ([_gp, _i] + [_vp] * 9 + [_sz, _vp], _st),
     "mcs_paged_decode_shared_workspace": ([_gp], _sz),
     "mcs_paged_decode_shared": ([_gp, _i] + [_vp] * 10 + [_sz, _vp], _st),
+    "mcs_paged_fork_workspace": ([_gp], _sz),
+    "mcs_paged_fork": ([_gp, _i] + [_vp] * 5 + [_i] + [_vp] * 8 + [_sz, _vp], _st),
+    "mcs_paged_compact_workspace": ([_gp], _sz),
+    "mcs_paged_compact": ([_gp] + [_vp] * 6 + [_i, _vp, _vp, _i, _vp, _sz, _vp], _st),
+    "mcs_paged_copy": ([_gp, _i] + [_vp] * 5, _st),
     "mcs_qk_norm_rope": ([_rp] + [_vp] * 10, _st),
     "mcs_qk_norm_rope_backward_workspace": ([_rp], _sz),
     "mcs_qk_norm_rope_backward": ([_rp] + [_vp] * 14 + [_sz, _vp], _st),
@@ -775,6 +782,68 @@ def mcs_paged_decode_shared(p: Paged, q, k_cache, v_cache, block_table, lens, gr
         _at(dev, shared_pages, _I32, (G,), "shared_pages"), _at(dev, out, _BF, rows, "out"),
         None if lse is None else _at(dev, lse, _F32, (B, Hq), "lse"), *_bytes_at(dev, ws, "ws"),
         _queue(stream, dev)), "mcs_paged_decode_shared")
+
+
+def mcs_paged_fork_workspace(p: Paged) -> int:
+    return lib().mcs_paged_fork_workspace(ctypes.byref(p))
+
+
+def mcs_paged_fork(p: Paged, parents, lens, block_table, extra, free_pages, free_head, lens_out,
+                   table_out, extra_out, free_out, head_out, moves, ws, stream=None):
+    """parents [n]: which of the B sequences each new one continues (-1: an empty one); moves
+    [n, 3] says what mcs_paged_copy has to copy."""
+    n, n_free = _count(parents.numel(), "parents"), _count(free_pages.numel(), "free_pages")
+    dev, B, P, one, pages = _device(stream), p.B, p.max_pages, (1,), (p.num_pages,)
+    _check(lib().mcs_paged_fork(
+        ctypes.byref(p), n, _at(dev, parents, _I32, (n,), "parents"),
+        _at(dev, lens, _I32, (B,), "lens"), _at(dev, block_table, _I32, (B, P), "block_table"),
+        _at(dev, extra, _I32, pages, "extra"), _at(dev, free_pages, _I32, (n_free,), "free_pages"),
+        n_free, _at(dev, free_head, _I32, one, "free_head"),
+        _at(dev, lens_out, _I32, (n,), "lens_out"),
+        _at(dev, table_out, _I32, (n, P), "table_out"),
+        _at(dev, extra_out, _I32, pages, "extra_out"),
+        _at(dev, free_out, _I32, (n_free,), "free_out"),
+        _at(dev, head_out, _I32, one, "head_out"), _at(dev, moves, _I32, (n, 3), "moves"),
+        *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_paged_fork")
+
+
+def mcs_paged_compact_workspace(p: Paged) -> int:
+    return lib().mcs_paged_compact_workspace(ctypes.byref(p))
+
+
+def _moves_of(moves) -> int:
+    if not isinstance(moves, torch.Tensor) or moves.dim() != 2:
+        raise ValueError("moves must be a [n, 3] tensor")
+    return _count(moves.shape[0], "moves")
+
+
+def mcs_paged_compact(p: Paged, lens, block_table, extra, table_out, extra_out, free_out, head_out,
+                      moves, ws, stream=None):
+    """moves [most, 3]: the first dimension says how many pages are moved at most."""
+    most, n_free = _moves_of(moves), _count(free_out.numel(), "free_out")
+    dev, B, pages = _device(stream), p.B, (p.num_pages,)
+    table = (B, p.max_pages)
+    _check(lib().mcs_paged_compact(
+        ctypes.byref(p), _at(dev, lens, _I32, (B,), "lens"),
+        _at(dev, block_table, _I32, table, "block_table"), _at(dev, extra, _I32, pages, "extra"),
+        _at(dev, table_out, _I32, table, "table_out"),
+        _at(dev, extra_out, _I32, pages, "extra_out"),
+        _at(dev, free_out, _I32, (n_free,), "free_out"), n_free,
+        _at(dev, head_out, _I32, (1,), "head_out"), _at(dev, moves, _I32, (most, 3), "moves"), most,
+        *_bytes_at(dev, ws, "ws"), _queue(stream, dev)), "mcs_paged_compact")
+
+
+def mcs_paged_copy(p: Paged, moves, k_cache, v_cache, k_mean=None, stream=None):
+    """The first rows of pages to other pages, in both caches: moves [n, 3] (from, to, rows)."""
+    n = _moves_of(moves)
+    dev, Hkv, pages, kv = _device(stream), p.Hkv, p.num_pages, p.kv
+    cache = (pages, Hkv, p.page, p.D)
+    _check(lib().mcs_paged_copy(
+        ctypes.byref(p), n, _at(dev, moves, _I32, (n, 3), "moves"),
+        _cache_at(dev, k_cache, kv, cache, "k_cache"),
+        _cache_at(dev, v_cache, kv, cache, "v_cache"),
+        None if k_mean is None else _at(dev, k_mean, _BF, (pages, Hkv, p.D), "k_mean"),
+        _queue(stream, dev)), "mcs_paged_copy")
 
 
 # ---------------------------------------------------------------- norm and rotation
