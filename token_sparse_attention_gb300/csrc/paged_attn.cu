@@ -10,11 +10,10 @@
 //
 // A unit is 128 rows (MMA M): tokens * heads, a token's heads next to each other, as they lie
 // in q.  A segment is a pair of units (a, b) of one sequence and KV head, which share every
-// K and V tile of 128 keys, or its last odd unit, whose tiles the two softmax chains take in
-// turn (a the even, b the odd ones) and join in the CTA.  All segments in a row form one list
-// of steps (a step: one tile for two units, or two tiles for one), and each of the SMs' CTAs
-// takes an equal share of it, whatever the lengths are: few long sequences are so split along
-// their keys, many short ones along the list.  What a share holds whole it writes at once;
+// K and V tile of 128 keys, or its last odd unit, of whose tiles the two softmax chains take 64
+// keys each, joined in the CTA.  All segments in a row form one list of tiles, and each of the
+// SMs' CTAs takes an equal share of it, whatever the lengths are: few long sequences are so split
+// along their keys, many short ones along the list.  What a share holds whole it writes at once;
 // parts of segments that cross shares go to the workspace and are joined in the order of
 // their keys by a second, programmatically dependent launch.
 //
@@ -68,26 +67,26 @@ struct Layout {
   static constexpr int kSub = D / 64;                 // 128-byte column sub-tiles of a row
   static constexpr int kSubBytes = BN * 128;
   static constexpr int kTileBytes = kSub * kSubBytes;
-  // E4M3 bytes on their way to f16: in the tile's second half, whose lines they are converted to
-  // (D = 128), or behind the tile (D = 64: a row's bytes are not as long as a line)
-  static constexpr int kRaw = D == 128 ? kSubBytes : kTileBytes;
-  static constexpr int kStageBytes = kTileBytes + (E4M3 && D == 64 ? BN * D : 0);
-  static constexpr int kStages = D == 128 ? 5 : E4M3 ? 8 : 12;
+  // ring of K and V tiles; E4M3: behind it a ring of tiles as they are in the cache
+  static constexpr int kStages = E4M3 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 12;
+  static constexpr int kRawStages = E4M3 ? (D == 128 ? 4 : 12) : 0, kRawBytes = BN * D;
   static constexpr int kRing = 2 * kTileBytes;
-  static constexpr int kBars = kRing + kStages * kStageBytes;
+  static constexpr int kRaw = kRing + kStages * kTileBytes;
+  static constexpr int kBars = kRaw + kRawStages * kRawBytes;
   // MMA batches done, round robin.  A waiter reads the phase of batch n's barrier, which is
-  // unambiguous as long as batch n + kDone cannot be done yet.  Loads lag furthest: they wait for the
-  // last reader of the item kStages back, and what the kStages - 1 items behind it feed is at most
-  // three batches for every two (segments of one step), and three more.
+  // unambiguous as long as batch n + kDone cannot be done yet.  Loads (and conversions) lag furthest:
+  // they wait for the last reader of the item kStages back, and what the kStages - 1 items behind it
+  // feed is at most three batches for every two (segments of one step), and three more.
   static constexpr int kDone = D == 128 ? 16 : 32;
   static_assert(kDone >= (kStages - 1) / 2 * 3 + 5, "batch barriers must outnumber the lag");
-  static constexpr int kNumBars = 3 * kStages + kDone + 10;
+  static constexpr int kAside = E4M3 ? kRawStages : kStages;
+  static constexpr int kNumBars = kStages + 2 * kAside + kDone + 10;
   static constexpr int kBadKey = kBars + kNumBars * 8;           // [2][D] words
   static constexpr int kMl = kBadKey + 2 * D * 4;                // [3][128] floats
   static constexpr int kMisc = kMl + 3 * BM * 4;                 // Misc
   static constexpr int kSmem = kMisc + 80;
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(kStages <= kBadSlots, "bad slots");
+  static_assert((kStages + kRawStages) / 2 + 2 <= kBadSlots, "bad slots");
 };
 
 // ------------------------------------------------------------------ the list
@@ -96,24 +95,20 @@ struct Layout {
 struct Walk {
   Seq s;
   int g, head, i;  // sequence, KV head and its chunk of query heads, pair (the last odd unit behind them)
-  bool single;     // an odd unit, whose tiles the chains take in turn
-  int tiles, tiles_a;  // of the segment; of a pair's first unit
-  int steps;       // of the segment
-  int t0, count;   // the share's steps of it: [t0, t0 + count)
+  bool single;     // an odd unit, whose tiles the chains halve
+  int steps, steps_a;  // tiles of the segment; of a pair's first unit
+  int t0, count;   // the share's tiles of it: [t0, t0 + count)
   long long left;  // positions from t0 to the share's end
   int index;       // segments of the share in front of this one
 };
 __device__ __forceinline__ void set_segment(const PagedAttnArgs& a, Walk& w) {
-  const int pairs = units_of(a, w.s) / 2;
-  w.single = w.i >= pairs;
+  w.single = w.i >= units_of(a, w.s) / 2;
   if (w.single) {
-    w.tiles = w.tiles_a = tiles_until(a, w.s, w.s.n);
-    w.steps = (w.tiles + 1) / 2;
+    w.steps = w.steps_a = tiles_until(a, w.s, w.s.n);
   } else {
     const long long e = (2LL * w.i + 2) * a.tokens;
-    w.tiles = tiles_until(a, w.s, static_cast<int>(min(e, static_cast<long long>(w.s.n))));
-    w.tiles_a = tiles_until(a, w.s, static_cast<int>(e - a.tokens));
-    w.steps = w.tiles;
+    w.steps = tiles_until(a, w.s, static_cast<int>(min(e, static_cast<long long>(w.s.n))));
+    w.steps_a = tiles_until(a, w.s, static_cast<int>(e - a.tokens));
   }
 }
 __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Walk& w) {
@@ -135,41 +130,34 @@ __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Walk& w) {
   ++w.index;
   return true;
 }
-// Whether chain x has a tile in step j of the share's part of the segment, and which.
-__device__ __forceinline__ int tile_of(const Walk& w, int x, int j) {
-  return w.single ? 2 * (w.t0 + j) + x : w.t0 + j;
-}
-__device__ __forceinline__ bool has_tile(const Walk& w, int x, int j) {
-  return tile_of(w, x, j) < (!w.single && x == 0 ? w.tiles_a : w.tiles);
-}
-// Keys that every row of the segment sees: tiles behind it are looked through.
-__device__ __forceinline__ int seen_by_all(const PagedAttnArgs& a, const Walk& w) {
-  return a.causal ? w.s.keys - w.s.n + 2 * w.i * a.tokens + 1 : w.s.keys;
-}
+
 // A walk in one register of a warp's lanes, while the softmax needs the registers.
 __device__ __forceinline__ int fold(const Walk& w, int lane) {
-  const int f[14] = {w.s.cu, w.s.n, w.s.keys, w.g, w.head, w.i, w.single, w.tiles, w.tiles_a, w.steps, w.t0, w.index,
+  const int f[13] = {w.s.cu, w.s.n, w.s.keys, w.g, w.head, w.i, w.single, w.steps, w.steps_a, w.t0, w.index,
                      static_cast<int>(w.left), static_cast<int>(w.left >> 32)};
   int x = w.count;
 #pragma unroll
-  for (int k = 0; k < 14; ++k)
+  for (int k = 0; k < 13; ++k)
     if (lane == k) x = f[k];
   return x;
 }
 __device__ __forceinline__ Walk unfold(int x) {
-  int f[15];
+  int f[14];
 #pragma unroll
-  for (int k = 0; k < 15; ++k) f[k] = __shfl_sync(0xffffffffu, x, k);
-  return {{f[0], f[1], f[2]}, f[3], f[4], f[5], f[6] != 0, f[7], f[8], f[9], f[10], f[14],
-          static_cast<long long>(static_cast<uint32_t>(f[12])) | (static_cast<long long>(f[13]) << 32), f[11]};
+  for (int k = 0; k < 14; ++k) f[k] = __shfl_sync(0xffffffffu, x, k);
+  return {{f[0], f[1], f[2]}, f[3], f[4], f[5], f[6] != 0, f[7], f[8], f[9], f[13],
+          static_cast<long long>(static_cast<uint32_t>(f[11])) | (static_cast<long long>(f[12]) << 32), f[10]};
 }
 
-// In how many steps of the share's part chain x has a tile (the first ones).
+// How many of the share's tiles chain x works on: the first ones (a pair's first unit ends earlier).
 __device__ __forceinline__ int steps_of(const Walk& w, int x) {
-  const int all = w.single ? (w.tiles - x + 1) / 2 : x == 0 ? w.tiles_a : w.tiles;
-  return max(0, min(w.count, all - w.t0));
+  return max(0, min(w.count, (x == 0 ? w.steps_a : w.steps) - w.t0));
 }
-__device__ __forceinline__ int last_tile(const Walk& w) { return min(tile_of(w, w.single ? 1 : 0, w.count - 1), w.tiles - 1); }
+
+// Keys that every row of the segment sees: tiles behind it are looked through.
+__device__ __forceinline__ int seen_by_all(const PagedAttnArgs& a, const Walk& w) {
+  return a.causal ? w.s.keys - w.s.n + 2 * w.i * a.tokens + 1 : w.s.keys;
+}
 
 // ------------------------------------------------------------------ small pieces
 
@@ -210,9 +198,9 @@ __device__ __forceinline__ int swz_offset(int r, int seg) {
 }
 // Scores that the row does not see become -inf where they stand (TMEM): keys from `valid` on and
 // slabs of pages outside the cache.  Few tiles have any; the others' path holds no mask.
-__device__ __noinline__ void mask_scores(uint32_t tS, int valid, uint32_t bad) {
+__device__ __noinline__ void mask_scores(uint32_t tS, int keys, int valid, uint32_t bad) {
 #pragma unroll 1
-  for (int c0 = 0; c0 < BN; c0 += 32) {
+  for (int c0 = 0; c0 < keys; c0 += 32) {
     uint32_t s[32];
     tmem_ld32(tS + c0, s);
     tmem_ld_wait();
@@ -262,7 +250,7 @@ __device__ __forceinline__ int first_bad(const uint32_t* record, const Walk& w, 
 }
 
 struct Misc {
-  uint8_t bad[kBadSlots][2];  // slabs of each step's tiles whose pages lie outside the cache
+  uint8_t bad[kBadSlots];  // slabs of each step's tile whose pages lie outside the cache
   uint32_t tmem;
   int abort;
   uint32_t any_bad[2];
@@ -288,9 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* qs = smem;
   uint8_t* ring = smem + L::kRing;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // [NS] stage loaded
-  uint64_t* raw = full + NS;                                     // [NS] loaded, to be looked through (bf16) or converted (E4M3)
-  uint64_t* looked = raw + NS;                                   // [NS] and looked through
-  uint64_t* q_full = looked + NS;                                // queries loaded
+  // bf16: [NS] V tile loaded that is to be looked through, and looked through; E4M3: [kRawStages] tile
+  // loaded, and converted
+  uint64_t* raw = full + NS;
+  uint64_t* past = raw + L::kAside;
+  uint64_t* q_full = past + L::kAside;                           // queries loaded
   uint64_t* p_full = q_full + 1;                                 // [2] P_x written
   uint64_t* joined = p_full + 2;                                 // [4] chain b's maxima and sums there
   uint64_t* written = joined + 4;                                // [2] epilogue of segment i done: written[i & 1]
@@ -303,10 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   if (tid == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(full + s, E4M3 ? kLoaders - 1 : 1);
+    for (int s = 0; s < NS; ++s) mbar_init(full + s, E4M3 ? kLoaders - 1 : 1);
+    for (int s = 0; s < L::kAside; ++s) {
       mbar_init(raw + s, 1);
-      mbar_init(looked + s, kLoaders - 1);
+      mbar_init(past + s, kLoaders - 1);
     }
     mbar_init(q_full, E4M3 ? kLoaders - 1 : 1);
     for (int x = 0; x < 2; ++x) {
@@ -322,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (tid < 2 * D) records[tid] = 0;
-  if (tid < 2 * kBadSlots) (&misc.bad[0][0])[tid] = 0;
+  if (tid < kBadSlots) misc.bad[tid] = 0;
   if (!E4M3 && a.heads * a.tokens < BM) {  // rows of the query tiles that no load fills
     for (int i = tid; i < 2 * L::kTileBytes / 16; i += kThreads) st_shared16(qs + 16 * i, make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_smem();
@@ -474,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       look_up(window + 1, found[2], out);
       outside[2] = __ballot_sync(0xffffffffu, out);
     };
-    // (tiles come in order; a V tile is at most two behind the last K tile)
+    // (tiles come in order; a V tile is one behind the last K tile)
     auto to_window = [&](int tile) {
       if (tile / kWindow > window) {
         ++window;
@@ -485,9 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         outside[2] = __ballot_sync(0xffffffffu, out);
       }
     };
-    // Ring items of a segment, in the order in which the MMA warp asks for them: the chains' first K,
-    // then for every step and chain its V and its next K (a pair's tiles come with chain a).
+    // Ring items of a segment, in the order in which the MMA warp asks for them: K(0), then V(j) and
+    // K(j + 1) of every step.  K(j) and, of the step in front, V(j - 1) are read last by batch base + 2 j.
     int it = 0;  // items so far
+    int reader = 0, q_reader = 0;  // lane i: the last batch that reads stage i; the last that reads the queries
     if (warp == kFirstLoader) {
       // ---------------------------------------------------------- TMA
       if (elect_one()) {
@@ -496,79 +487,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tv);
       }
       __syncwarp();
-      // Two items at a time, as the MMA warp takes them: lanes 0-15 load the first one's boxes (a
-      // page's rows, 128 bytes wide), lanes 16-31 the second's.
+      // a lane per box: a page's rows, 128 bytes wide (E4M3: all of a row's)
       constexpr int kBoxSubs = E4M3 ? 1 : L::kSub, kBoxBytes = E4M3 ? D : 128;
-      const int half = lane >> 4, box = (lane & 15) / kBoxSubs, sub = (lane & 15) % kBoxSubs, boxes = BN / a.page;
-      const uint32_t to = smem_u32(ring) + (E4M3 ? L::kRaw : sub * L::kSubBytes) + box * a.page * kBoxBytes;
-      int reader = 0, q_reader = 0;  // lane i: the last batch that reads stage i; the last that reads the queries
-      int next_st = 0, step = 0;
+      constexpr int kSlots = E4M3 ? L::kRawStages : NS, kSlotBytes = E4M3 ? L::kRawBytes : L::kTileBytes;
+      const int box = lane / kBoxSubs, sub = lane % kBoxSubs, boxes = BN / a.page;
+      const uint32_t to = smem_u32(E4M3 ? smem + L::kRaw : ring) + sub * L::kSubBytes + box * a.page * kBoxBytes;
+      int st = 0, step = 0;
+      uint32_t turn = 0;  // of the slots, parity
       uint32_t raw_used = 0, raw_parity = 0;  // bf16, of each stage: a tile went to `raw`; the last one's parity
-      uint32_t dirty = 0;                     // steps (and chains) whose `bad` is not zero
-      auto issue = [&](bool first, bool first_k, int first_tile, int first_read, bool look, bool second, int second_tile,
-                       int second_read) -> bool {
-        const int st0 = next_st, st1 = first ? (st0 + 1 == NS ? 0 : st0 + 1) : st0;
-        const int st = half ? st1 : st0;
-        const bool mine = half ? second : first;
-        const int n = __shfl_sync(0xffffffffu, reader, st);
-        const bool used = it + (half && first ? 1 : 0) >= NS;
-        bool ok = !mine || !used || mbar_try_wait(done + n % L::kDone, (n / L::kDone) & 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = !mine || !used || mbar_wait(done + n % L::kDone, (n / L::kDone) & 1, abort_flag, a.status);
-          if (!__all_sync(0xffffffffu, ok)) return false;
-        }
-        if (second) to_window(second_tile);
-        const int tile = half ? second_tile : first_tile;
-        const bool behind = tile / kWindow != window;
-        const int from = (tile % kWindow) * kSlabs + (box < boxes ? box : 0) * slabs_per_page;
-        const int r0 = __shfl_sync(0xffffffffu, found[0], from), r1 = __shfl_sync(0xffffffffu, found[1], from);
-        const int row = behind ? r0 : r1;
-        const bool to_raw = E4M3 || (look && half == 0);
-        uint64_t* bar = (to_raw ? raw : full) + st;
-        if (mine && (lane & 15) == 0) {
-          mbar_expect_tx(bar, E4M3 ? BN * D : L::kTileBytes);
-          if (!E4M3 && to_raw) mbar_arrive(full + st);  // `full` keeps its turn: such tiles complete it empty
-        }
-        __syncwarp();
-        if (mine && box < boxes) {  // (a row past the tensor's end reads zeros)
-          const bool is_k = half || first_k;
-          tma_load_2d_at(to + st * L::kStageBytes, is_k ? &tk : &tv, sub * 64, row < 0 ? a.rows : row, bar);
-        }
-        __syncwarp();
-        if (!E4M3 && look) {
-          raw_parity ^= ((raw_used >> st0) & 1u) << st0;
-          raw_used |= 1u << st0;
-        }
-        if (first && lane == st0) reader = first_read;
-        if (second && lane == st1) reader = second_read;
-        it += (first ? 1 : 0) + (second ? 1 : 0);
-        next_st = second ? (st1 + 1 == NS ? 0 : st1 + 1) : st1;
-        return true;
-      };
-      // slabs of the tile whose pages are none, for the softmax; in front of the load that it goes with
-      auto tell = [&](int tile, int at, int x) {
-        to_window(tile);
-        const uint32_t out = ((tile / kWindow != window ? outside[0] : outside[1]) >> ((tile % kWindow) * kSlabs)) & 0xffu;
-        const int slot = (at % kBadSlots) * 2 + x;
-        if (out == 0 && ((dirty >> slot) & 1u) == 0) return;
-        dirty = (dirty & ~(1u << slot)) | (out ? 1u << slot : 0u);
-        if (lane == 0) {
-          (&misc.bad[0][0])[slot] = static_cast<uint8_t>(out);
-          if (out) atomicOr(a.status, DEV_BOUNDS);
-        }
-        __syncwarp();
-      };
+      uint32_t dirty = 0;                     // steps whose `bad` is not zero
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
-        const bool single = w.single;
-        const int count = w.count, n0 = steps_of(w, 0), n1 = steps_of(w, 1), tile0 = tile_of(w, 0, 0);
-        const int kn0 = single ? n0 : count, first_look = seen_by_all(a, w) / BN;
-        begin_windows(tile0);
-        if (w.index > 0) ok = wait_batch(q_reader);
+        const int count = w.count, t0 = w.t0, first_look = seen_by_all(a, w) / BN;
+        begin_windows(t0);
+        if (w.index > 0 && !E4M3) ok = wait_batch(q_reader);
         if (!ok) break;
         if (!E4M3 && elect_one()) {
           // a box is tokens x heads rows; tokens behind the sequence's are other ones' or zeros
-          const int units = single ? 1 : 2;
+          const int units = w.single ? 1 : 2;
           mbar_expect_tx(q_full, units * L::kSub * 128 * a.heads * a.tokens);
           const int head = w.head / a.chunks * group + w.head % a.chunks * a.heads;
           for (int u = 0; u < units; ++u)
@@ -576,34 +512,54 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(qs + u * L::kTileBytes + s * L::kSubBytes, &tq, s * 64, head, w.s.cu + (2 * w.i + u) * a.tokens, q_full);
         }
         __syncwarp();
-        tell(tile0, step, 0);
-        if (!single) tell(tile0, step, 1);
-        if (single && n1 > 0) tell(tile0 + 1, step, 1);
-        ok = issue(true, true, tile0, base, false, single && n1 > 0, tile0 + 1, base);
-        // (one call of `issue` in the loop: its code is long)
-        const int turns = single ? 2 * count : count;
 #pragma unroll 1
-        for (int i = 0; ok && i < turns; ++i) {
-          const int j = single ? i >> 1 : i, x = single ? i & 1 : 0;
-          if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
-          const bool v = !single || j < (x ? n1 : n0), k = j + 1 < (x ? n1 : kn0);
-          const int v_tile = tile0 + i, k_tile = v_tile + (single ? 2 : 1);
-          if (k) {
-            tell(k_tile, step + j + 1, x);
-            if (!single) tell(k_tile, step + j + 1, 1);
+        for (int i = 0; i < 2 * count; ++i) {  // K of step i / 2, or V of step (i - 1) / 2
+          const int j = i >> 1, tile = t0 + j;
+          const bool is_k = !(i & 1);
+          if (a.fault && i >= 3) ok = false;  // test only: starve the MMA warp
+          if (ok && it >= kSlots)
+            ok = E4M3 ? warp_wait(past + st, turn ^ 1, abort_flag, a.status) : wait_batch(__shfl_sync(0xffffffffu, reader, st));
+          if (!ok) break;
+          to_window(tile);
+          const bool behind = tile / kWindow != window;
+          const int slab0 = (tile % kWindow) * kSlabs;
+          if (is_k) {  // slabs whose pages are none, for the softmax; in front of the load that they go with
+            const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu, bit = 1u << ((step + j) % kBadSlots);
+            if (out != 0 || (dirty & bit) != 0) {
+              dirty = out ? dirty | bit : dirty & ~bit;
+              if (lane == 0) {
+                misc.bad[(step + j) % kBadSlots] = static_cast<uint8_t>(out);
+                if (out) atomicOr(a.status, DEV_BOUNDS);
+              }
+              __syncwarp();
+            }
           }
-          // V_x(j) is read by batch base + 2 j + x + 1, K_x(j + 1) too (a pair's by chain b's)
-          const int read = base + 2 * j + (single ? x + 1 : 2);
-          if (ok && v) ok = issue(true, false, v_tile, read, v_tile >= first_look, k, k_tile, read);
+          const int row = __shfl_sync(0xffffffffu, behind ? found[0] : found[1], slab0 + (box < boxes ? box : 0) * slabs_per_page);
+          const bool look = !E4M3 && !is_k && tile >= first_look;
+          uint64_t* bar = (E4M3 || look ? raw : full) + st;
+          if (lane == 0) {
+            mbar_expect_tx(bar, kSlotBytes);
+            if (look) mbar_arrive(full + st);  // `full` keeps its turn: such tiles complete it empty
+          }
+          __syncwarp();
+          if (box < boxes)  // (a row past the tensor's end reads zeros)
+            tma_load_2d_at(to + st * kSlotBytes, is_k ? &tk : &tv, sub * 64, row < 0 ? a.rows : row, bar);
+          __syncwarp();
+          if (look) {
+            raw_parity ^= ((raw_used >> st) & 1u) << st;
+            raw_used |= 1u << st;
+          }
+          if (lane == st) reader = base + 2 * j + (is_k ? 0 : 2);
+          ++it;
+          if (++st == kSlots) st = 0, turn ^= 1;
         }
         step += count;
         q_reader = base + 2 * (count - 1);
         base += 2 * count + 1;
       }
       if (*abort_flag)
-        for (int i = max(it - NS, 0); i < it; ++i) {
-          if (!E4M3) drain_wait(full + i % NS, (i / NS) & 1);
-          if (E4M3) drain_wait(raw + i % NS, (i / NS) & 1);
+        for (int i = max(it - kSlots, 0); i < it; ++i) {
+          drain_wait((E4M3 ? raw : full) + i % kSlots, (i / kSlots) & 1);
           if (!E4M3 && ((raw_used >> (i % NS)) & 1u)) drain_wait(raw + i % NS, (raw_parity >> (i % NS)) & 1u);
         }
     } else {
@@ -614,51 +570,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kHelp = 32 * (kLoaders - 1), kSegsRow = D / 8;
       const int hw = warp - kFirstLoader - 1, me = 32 * hw + lane;
       uint32_t raw_parity = 0;  // of each stage
-      int q_reader = 0;
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
-        const bool single = w.single;
-        const int count = w.count, n0 = steps_of(w, 0), n1 = steps_of(w, 1), tile0 = tile_of(w, 0, 0);
-        const int first_look = seen_by_all(a, w) / BN, mark = w.index & 1, keys = w.s.keys;
+        const int count = w.count, t0 = w.t0, keys = w.s.keys, first_look = seen_by_all(a, w) / BN, mark = w.index & 1;
         // a record's last segment, two back, has been read when this one's is begun
-        const bool looks = first_look <= last_tile(w);
-        if (looks && w.index >= 2) ok = warp_wait(written + mark, ((w.index - 2) / 2) & 1, abort_flag, a.status);
+        if (first_look < t0 + count && w.index >= 2) ok = warp_wait(written + mark, ((w.index - 2) / 2) & 1, abort_flag, a.status);
         if (!ok) break;
         if constexpr (!E4M3) {
-          // items in front of step j
-          auto items_until = [&](int j) {
-            return single ? 2 * j + 1 + (n1 > 0 ? 1 + min(j, n1) + min(j, n1 - 1) : 0) : 2 * j + 1;
-          };
-          const int jl = looks ? max(0, single ? (first_look - tile0) >> 1 : first_look - tile0) : count;
-          int i = it + items_until(jl);
-          for (int j = jl; ok && j < count; ++j) {
-            for (int x = 0; x < (single ? 2 : 1); ++x) {
-              const int tile = tile0 + (single ? 2 * j + x : j), st = i % NS;
-              if (single && j >= (x ? n1 : n0)) continue;
-              i += j + 1 < (single ? (x ? n1 : n0) : count) ? 2 : 1;
-              if (tile < first_look) continue;
-              ok = warp_wait(raw + st, (raw_parity >> st) & 1u, abort_flag, a.status);
-              if (!ok) break;
-              raw_parity ^= 1u << st;
-              uint8_t* v = ring + st * L::kStageBytes;
-              for (int c = me; c < BN * kSegsRow; c += kHelp) {
-                const int r = c / kSegsRow, sg = c % kSegsRow;
-                uint8_t* at = v + swz_offset(r, sg);
-                if (r >= keys - tile * BN) {
-                  st_shared16(at, make_uint4(0u, 0u, 0u, 0u));
-                  continue;
-                }
-                const uint4 q = ld_shared16(at);
-                if (has_bad<false>(q))
-                  st_shared16(at, note_bad<false>(q, records + mark * D + sg * 8, misc.any_bad + mark, bad_mark(w.index),
-                                                  (tile - first_look) * BN + r));
+          for (int j = max(0, first_look - t0); ok && j < count; ++j) {
+            const int tile = t0 + j, st = (it + 2 * j + 1) % NS;
+            ok = warp_wait(raw + st, (raw_parity >> st) & 1u, abort_flag, a.status);
+            if (!ok) break;
+            raw_parity ^= 1u << st;
+            uint8_t* v = ring + st * L::kTileBytes;
+            for (int c = me; c < BN * kSegsRow; c += kHelp) {
+              const int r = c / kSegsRow, sg = c % kSegsRow;
+              uint8_t* at = v + swz_offset(r, sg);
+              if (r >= keys - tile * BN) {
+                st_shared16(at, make_uint4(0u, 0u, 0u, 0u));
+                continue;
               }
-              fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
-              __syncwarp();
-              if (lane == 0) mbar_arrive(looked + st);
+              const uint4 q = ld_shared16(at);
+              if (has_bad<false>(q))
+                st_shared16(at, note_bad<false>(q, records + mark * D + sg * 8, misc.any_bad + mark, bad_mark(w.index),
+                                                (tile - first_look) * BN + r));
             }
+            fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
+            __syncwarp();
+            if (lane == 0) mbar_arrive(past + st);
           }
-          it += single ? 2 * n0 + (n1 > 0 ? 2 * n1 : 0) : 2 * count;
+          it += 2 * count;
         } else {
           if (w.index > 0) ok = wait_batch(q_reader);
           if (!ok) break;
@@ -666,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kChunks = BM * kSegsRow, kAtOnce = 6;
           const int chunk0 = w.head % a.chunks * a.heads, head = w.head / a.chunks * group + chunk0;
 #pragma unroll 1
-          for (int c0 = me; c0 < (single ? 1 : 2) * kChunks; c0 += kAtOnce * kHelp) {
+          for (int c0 = me; c0 < (w.single ? 1 : 2) * kChunks; c0 += kAtOnce * kHelp) {
             uint4 qw[kAtOnce];
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
@@ -688,26 +629,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(q_full);
-          // One row of 16-byte chunks per kSegs lanes.  Only these lanes touch a row's bytes and its f16
-          // line; where both share memory (D = 128) a __syncwarp between reads and writes orders them.
+          // rows in 16-byte pieces, a row per kSegs lanes
           constexpr int kSegs = D / 16, kRows = 32 / kSegs, kGroups = BN / kRows, kTurns = (kGroups + kLoaders - 2) / (kLoaders - 1);
           const int sub = lane / kSegs, seg = lane % kSegs;
-          const int heads_of = single ? 1 + (n1 > 0 ? 1 : 0) : 1;
-          const int turns = heads_of + (single ? 4 : 2) * count;
 #pragma unroll 1
-          for (int i = 0; ok && i < turns; ++i) {
-            // item i: the first K, then (V, next K) of each step and chain
-            const int m = i - heads_of, u = m >> 1, j = single ? u >> 1 : u, x = single ? u & 1 : 0;
-            const bool is_k = m < 0 || (m & 1);
-            if (m >= 0 && j + (is_k ? 1 : 0) >= (single ? (x ? n1 : n0) : count)) continue;
-            const int tile = tile0 + u, st = it % NS;  // (of a V tile)
-            const bool look = !is_k && tile >= first_look;
-            ok = warp_wait(raw + st, (it / NS) & 1, abort_flag, a.status);
+          for (int i = 0; ok && i < 2 * count; ++i) {
+            const int j = i >> 1, tile = t0 + j, st = it % NS, slot = it % L::kRawStages;
+            const bool is_k = !(i & 1);
+            ok = (it < NS || wait_batch(__shfl_sync(0xffffffffu, reader, st))) &&
+                 warp_wait(raw + slot, (it / L::kRawStages) & 1, abort_flag, a.status);
             if (!ok) break;
+            if (lane == st) reader = base + 2 * j + (is_k ? 0 : 2);
             ++it;
-            uint8_t* stage = ring + st * L::kStageBytes;
-            uint8_t* from = stage + L::kRaw;
-            if (look) {
+            uint8_t* from = smem + L::kRaw + slot * L::kRawBytes;
+            uint8_t* stage = ring + st * L::kTileBytes;
+            if (!is_k && tile >= first_look) {
 #pragma unroll 1
               for (int k = 0; k < kTurns; ++k) {
                 const int r = (hw + (kLoaders - 1) * k) * kRows + sub;
@@ -720,13 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      (tile - first_look) * BN + r);
                 st_shared16(from + r * D + seg * 16, q);
               }
-              __syncwarp();
             }
             uint4 v[kTurns];
 #pragma unroll
             for (int k = 0; k < kTurns; ++k)
               if (hw + (kLoaders - 1) * k < kGroups) v[k] = ld_shared16(from + ((hw + (kLoaders - 1) * k) * kRows + sub) * D + seg * 16);
-            __syncwarp();
 #pragma unroll
             for (int k = 0; k < kTurns; ++k) {
               if (hw + (kLoaders - 1) * k < kGroups) {
@@ -742,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
             __syncwarp();
-            if (lane == 0) mbar_arrive(full + st);
+            if (lane == 0) {
+              mbar_arrive(full + st);
+              mbar_arrive(past + slot);
+            }
           }
           q_reader = base + 2 * (count - 1);
           base += 2 * count + 1;
@@ -752,12 +689,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idesc_qk = E4M3 ? idesc_f16(BM, BN, false, false) : idesc_bf16(BM, BN, false, false);
+    constexpr uint32_t idesc_half = E4M3 ? idesc_f16(BM, BN / 2, false, false) : idesc_bf16(BM, BN / 2, false, false);
     constexpr uint32_t idesc_pv = E4M3 ? idesc_f16(BM, D, false, true) : idesc_bf16(BM, D, false, true);
     // The tensor core holds one or two MMAs ahead and the issue of a batch ends as its last ones
     // begin: whatever stands between that and the next batch's issue leaves it idle.  So stages,
     // parities and barriers of the next batch are worked out in front of the present one's issue.
     const uint32_t ring_addr = smem_u32(ring), q_addr = smem_u32(qs);
-    uint32_t look_parity = 0;       // of each stage's `looked`
+    uint32_t look_parity = 0;       // of each stage's `past` (bf16)
     int next_st = 0, dn = 0;        // the next ring item's stage; the next batch's barrier
     uint32_t next_ph = 0, step = 0;
     struct Item {
@@ -771,105 +709,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       return i;
     };
     auto try_item = [&](const Item& i) {
-      return i.look ? mbar_try_wait(looked + i.st, (look_parity >> i.st) & 1) : mbar_try_wait(full + i.st, i.ph);
+      return i.look ? mbar_try_wait(past + i.st, (look_parity >> i.st) & 1) : mbar_try_wait(full + i.st, i.ph);
     };
     auto wait_item = [&](const Item& i) {
-      return i.look ? warp_wait(looked + i.st, (look_parity >> i.st) & 1, abort_flag, a.status)
+      return i.look ? warp_wait(past + i.st, (look_parity >> i.st) & 1, abort_flag, a.status)
                     : warp_wait(full + i.st, i.ph, abort_flag, a.status);
     };
-    auto issue_qk = [&](int x, int st) {
-      const uint32_t kb = ring_addr + st * L::kStageBytes, qb = q_addr + (w.single ? 0 : x) * L::kTileBytes;
+    // S_x = Q_x K^T; an odd unit's chains take the tile's first and last 64 keys
+    auto issue_qk = [&](int x, int st, bool single) {
+      const uint32_t kb = ring_addr + st * L::kTileBytes + (single ? x * (BN / 2) * 128 : 0);
+      const uint32_t qb = q_addr + (single ? 0 : x) * L::kTileBytes, idesc = single ? idesc_half : idesc_qk;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * L::kSubBytes + (kk & 3) * 32;
-        umma_ss(tmem + x * 128, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0);
+        umma_ss(tmem + x * 128, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), idesc, kk > 0);
       }
     };
-    auto issue_pv = [&](int x, int st, bool first) {
-      const uint32_t vb = ring_addr + st * L::kStageBytes;
+    // O_x (+)= P_x V
+    auto issue_pv = [&](int x, int st, bool first, bool single) {
+      const uint32_t vb = ring_addr + st * L::kTileBytes + (single ? x * (BN / 2) * 128 : 0);
 #pragma unroll
       for (int kk = 0; kk < BN / 16; ++kk)
-        umma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 16 * 128, L::kSubBytes, 1024), idesc_pv,
-                (!first || kk > 0) ? 1u : 0u);
+        if (kk < BN / 32 || !single)
+          umma_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 16 * 128, L::kSubBytes, 1024), idesc_pv,
+                  (!first || kk > 0) ? 1u : 0u);
     };
     bool ok = true;
     for (; ok && more; more = next_segment(a, w)) {
       const bool single = w.single;
-      const int count = w.count, n0 = steps_of(w, 0), n1 = steps_of(w, 1);
-      // steps from look[x] on have a V tile that is looked through
-      const int seen = seen_by_all(a, w), first = seen / BN - tile_of(w, 0, 0);
-      const int look0 = E4M3 ? count : single ? (first + 1) >> 1 : first, look1 = E4M3 ? count : first >> 1;
-      Item k0 = take(false), k1 = single && n1 > 0 ? take(false) : k0;
-      ok = warp_wait(q_full, w.index & 1, abort_flag, a.status) && wait_item(k0) && wait_item(k1);
+      const int count = w.count, n0 = steps_of(w, 0);  // (chain b works on every tile)
+      const int look_from = E4M3 ? count : seen_by_all(a, w) / BN - w.t0;
+      Item k = take(false), v = take(0 >= look_from);
+      ok = warp_wait(q_full, w.index & 1, abort_flag, a.status) && wait_item(k);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        if (n0 > 0) issue_qk(0, k0.st);
-        if (n1 > 0) issue_qk(1, k1.st);
+        if (n0 > 0) issue_qk(0, k.st, single);
+        issue_qk(1, k.st, single);
         umma_commit(done + dn);
       }
       __syncwarp();
-      dn = dn + 1 == L::kDone ? 0 : dn + 1;
-      Item v0 = k0, v1 = k0;
-      // the chains' items of step j: chain a's V, next K, and (an odd unit's) chain b's
-      auto take0 = [&](int j) {
-        if (!single || j < n0) v0 = take(j >= look0);
-        if (j + 1 < (single ? n0 : count)) k0 = take(false);
-      };
-      auto take1 = [&](int j) {
-        if (single) {
-          if (j < n1) v1 = take(j >= look1);
-          if (j + 1 < n1) k1 = take(false);
-        } else {
-          v1 = v0, k1 = k0;
-        }
-      };
-      take0(0);
+      dn = (dn + 1) % L::kDone;
+      if (count > 1) k = take(false);
 #pragma unroll 1
       for (int j = 0; ok && j < count; ++j, ++step) {
+        const bool last = j + 1 == count;
         {
-          const bool mine = j < n0, next = j + 1 < n0, loads_v = !single || mine, loads_k = j + 1 < (single ? n0 : count);
+          const bool mine = j < n0, next = j + 1 < n0;
           bool ready = mbar_try_wait(p_full, step & 1);
-          if (loads_v) ready &= try_item(v0);
-          if (loads_k) ready &= mbar_try_wait(full + k0.st, k0.ph);
+          ready &= try_item(v);
+          if (!last) ready &= mbar_try_wait(full + k.st, k.ph);
           if (!__all_sync(0xffffffffu, ready))
-            ok = (!loads_v || wait_item(v0)) && (!loads_k || wait_item(k0)) && warp_wait(p_full, step & 1, abort_flag, a.status);
+            ok = wait_item(v) && (last || wait_item(k)) && warp_wait(p_full, step & 1, abort_flag, a.status);
           if (!ok) break;
-          if (loads_v && v0.look) look_parity ^= 1u << v0.st;
+          if (v.look) look_parity ^= 1u << v.st;
           uint64_t* bar = done + dn;
-          dn = dn + 1 == L::kDone ? 0 : dn + 1;
-          take1(j);
-          const int vs = v0.st, ks = k0.st;
+          dn = (dn + 1) % L::kDone;
           tc_fence_after();
           if (elect_one()) {
-            if (mine) issue_pv(0, vs, j == 0);
-            if (next) issue_qk(0, ks);
+            if (mine) issue_pv(0, v.st, j == 0, single);
+            if (next) issue_qk(0, k.st, single);
             umma_commit(bar);
           }
           __syncwarp();
         }
-        {
-          const bool mine = j < n1, next = j + 1 < n1;
-          bool ready = mbar_try_wait(p_full + 1, step & 1);
-          if (single && mine) ready &= try_item(v1);
-          if (single && next) ready &= mbar_try_wait(full + k1.st, k1.ph);
-          if (!__all_sync(0xffffffffu, ready))
-            ok = (!single || !mine || wait_item(v1)) && (!single || !next || wait_item(k1)) &&
-                 warp_wait(p_full + 1, step & 1, abort_flag, a.status);
-          if (!ok) break;
-          if (single && mine && v1.look) look_parity ^= 1u << v1.st;
-          uint64_t* bar = done + dn;
-          dn = dn + 1 == L::kDone ? 0 : dn + 1;
-          const int vs = v1.st, ks = k1.st;
-          if (j + 1 < count) take0(j + 1);
-          tc_fence_after();
-          if (elect_one()) {
-            if (mine) issue_pv(1, vs, j == 0);
-            if (next) issue_qk(1, ks);
-            umma_commit(bar);
-          }
-          __syncwarp();
+        const bool ready = mbar_try_wait(p_full + 1, step & 1);
+        if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(p_full + 1, step & 1, abort_flag, a.status);
+        if (!ok) break;
+        uint64_t* bar = done + dn;
+        dn = (dn + 1) % L::kDone;
+        const int vs = v.st, ks = k.st;
+        if (!last) v = take(j + 1 >= look_from);
+        if (j + 2 < count) k = take(false);
+        tc_fence_after();
+        if (elect_one()) {
+          issue_pv(1, vs, j == 0, single);
+          if (!last) issue_qk(1, ks, single);
+          umma_commit(bar);
         }
+        __syncwarp();
       }
     }
     if (elect_one()) umma_commit(fin);
@@ -905,11 +823,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Row mine_row = row_of(w);
       const int limit = mine_row.limit;
       const int mine = __all_sync(0xffffffffu, !mine_row.live) ? 0 : steps_of(w, x), count = w.count;
-      int ahead = limit - tile_of(w, x, 0) * BN;  // keys that the row sees from the tile's first on
-      const int stride = w.single ? 2 * BN : BN;
+      // an odd unit's chains see half a tile each: its first, its last 64 keys
+      const bool single = w.single;
+      int ahead = limit - w.t0 * BN - (single ? x * (BN / 2) : 0);  // keys that the row sees from the chain's first on
       const int folded = fold(w, lane);
       float m_run = -INFINITY, l_f32 = 0.f, l_mul = 0.f;
-      for (int j = 0; j < count; ++j, ++step, ahead -= stride) {
+      for (int j = 0; j < count; ++j, ++step, ahead -= BN) {
         if (!wait_batch(j == 0 ? base : base + 2 * j + x - 1)) {
           ok = false;
           break;
@@ -921,15 +840,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(p_full + x);
           continue;
         }
-        const int valid = ahead;
-        const uint32_t bad = misc.bad[step % kBadSlots][x];
-        if (bad != 0 || !__all_sync(0xffffffffu, valid >= BN)) mask_scores(tS, valid, bad);
+        const uint32_t bad = misc.bad[step % kBadSlots] >> (single ? x * (kSlabs / 2) : 0);
+        const int keys = single ? BN / 2 : BN;
+        if (bad != 0 || !__all_sync(0xffffffffu, ahead >= keys)) mask_scores(tS, keys, ahead, bad);
         float s[64];
         uint32_t* su = reinterpret_cast<uint32_t*>(s);
-        tmem_ld32(tS + 64, su);
-        tmem_ld32(tS + 96, su + 32);
-        tmem_ld_wait();
-        const float mx_hi = max64(s);
+        float mx_hi = -INFINITY;
+        if (!single) {
+          tmem_ld32(tS + 64, su);
+          tmem_ld32(tS + 96, su + 32);
+          tmem_ld_wait();
+          mx_hi = max64(s);
+        }
         tmem_ld32(tS + 0, su);
         tmem_ld32(tS + 32, su + 32);
         tmem_ld_wait();
@@ -962,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1) {
+            if (single) break;
             tmem_ld32(tS + 64, su);
             tmem_ld32(tS + 96, su + 32);
             tmem_ld_wait();
@@ -999,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w = unfold(folded);
       const Row r = row_of(w);
       const bool idle = __all_sync(0xffffffffu, !r.live), live = r.live;
-      const bool had = has_tile(w, x, 0);  // this chain wrote O
+      const bool had = steps_of(w, x) > 0;  // this chain wrote O
       float fa = 1.f, fb = 0.f;
       if (w.single) {  // chain a joins the two
         if (x == 1) {
@@ -1023,7 +946,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       if (!idle && !(w.single && x == 1)) {
-        const bool b_too = w.single && has_tile(w, 1, 0);
         const uint32_t tOb = tmem + 256 + D + lane_off;
         const bool goes_on = w.t0 + w.count < w.steps, whole = w.t0 == 0 && !goes_on;
         const size_t out_row = static_cast<size_t>(w.s.cu + r.tok) * a.Hq + w.head / a.chunks * group + r.head;
@@ -1043,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seen = seen_by_all(a, w);
         const bool spoiled = *static_cast<volatile uint32_t*>(misc.any_bad + (w.index & 1)) == bad_mark(w.index);
         const uint32_t* record = records + (w.index & 1) * D;
-#pragma unroll
+#pragma unroll 1  // (once per segment: short code is there sooner)
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           float v[32];
@@ -1056,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
           }
-          if (b_too) {
+          if (w.single) {
             tmem_ld32(tOb + c * 32, o);
             tmem_ld_wait();
 #pragma unroll

@@ -2,8 +2,7 @@
 // kernels, and the join of a common beginning with the sequences' tails (decode.cu), agree on.
 //
 // A unit is 128 query rows: tokens * heads.  A segment is a pair of units of one sequence (or group
-// of sequences) and KV head, or its last odd unit; a step is one tile of 128 keys for both units of a
-// pair, or two tiles for an odd one.  Each segment has steps + kPagedAttnSegCost positions; segments
+// of sequences) and KV head, or its last odd unit; a step is one tile of 128 keys.  Each segment has steps + kPagedAttnSegCost positions; segments
 // stand in the order (sequence, KV head and chunk of its query heads, pair).
 #pragma once
 
@@ -80,8 +79,7 @@ __device__ __forceinline__ long long pairs_upto(const PagedAttnArgs& a, const Se
 }
 __device__ __forceinline__ long long positions_of(const PagedAttnArgs& a, const Seq& s) {
   const int units = units_of(a, s);
-  return pairs_upto(a, s, units / 2) +
-         ((units & 1) ? (tiles_until(a, s, s.n) + 1) / 2 + kPagedAttnSegCost : 0);
+  return pairs_upto(a, s, units / 2) + ((units & 1) ? tiles_until(a, s, s.n) + kPagedAttnSegCost : 0);
 }
 
 // The shares of a list of `all` positions: share c begins at all * c / shares.
@@ -100,10 +98,8 @@ struct PagedAttnPlace {
 __device__ __forceinline__ PagedAttnPlace paged_attn_place(const SharedArgs& p, int b, int h, int hh) {
   const int g = p.group_of[b], n = p.cu[g + 1] - p.cu[g], t = b - p.cu[g];
   const int units = (n + p.tokens - 1) / p.tokens, pairs = units / 2, u = t / p.tokens;
-  const int tiles = (p.keys[g] + kPagedAttnKeys - 1) / kPagedAttnKeys, odd = (tiles + 1) / 2;
-  const long long pair_size = tiles + kPagedAttnSegCost;
-  const long long size = pairs * pair_size + ((units & 1) ? odd + kPagedAttnSegCost : 0);
-  const int segs = p.segs, i = u / 2, steps = i < pairs ? tiles : odd;
+  const int segs = p.segs, i = u / 2, steps = (p.keys[g] + kPagedAttnKeys - 1) / kPagedAttnKeys;
+  const long long pair_size = steps + kPagedAttnSegCost, size = (pairs + (units & 1)) * pair_size;
   const long long all = p.places[p.G] * segs;
   const long long at = p.places[g] * segs + (h * p.chunks + hh / p.heads) * size + i * pair_size;
   const int shares = static_cast<int>(min(all, static_cast<long long>(p.grid)));
