@@ -435,46 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kFirstLoader && warp < kMmaWarp) {
     // ------------------------------------------------------------ loads
-    // pages of a window's tiles: lane i has the row in the caches of the i-th slab, -1 where
-    // there is nothing; the window behind it is asked for when one is begun
-    const int slabs_per_page = a.page / kSlab, shift = 31 - __clz(slabs_per_page);
-    int found[3] = {-1, -1, -1}, window = -1;
-    uint32_t outside[3] = {0, 0, 0};  // slabs inside the sequence whose page is none
-    auto look_up = [&](int win, int& row, bool& out) {
-      const long long slab = static_cast<long long>(win) * 32 + lane;
-      row = -1;
-      out = false;
-      if (slab * kSlab >= w.s.keys) return;
-      const int j = static_cast<int>(slab >> shift);
-      const int at = a.row_of != nullptr ? a.row_of[w.g] : w.g;
-      const int pid = a.table[static_cast<size_t>(at) * a.max_pages + j];
-      if (pid < 0 || pid >= a.num_pages) {
-        out = true;
-        return;
-      }
-      row = (pid * a.Hkv + w.head / a.chunks) * a.page + (static_cast<int>(slab) & (slabs_per_page - 1)) * kSlab;
-    };
-    auto begin_windows = [&](int tile) {
-      window = tile / kWindow;
-      bool out;
-      found[0] = -1;
-      outside[0] = 0;
-      look_up(window, found[1], out);
-      outside[1] = __ballot_sync(0xffffffffu, out);
-      look_up(window + 1, found[2], out);
-      outside[2] = __ballot_sync(0xffffffffu, out);
-    };
-    // (tiles come in order; a V tile is one behind the last K tile)
-    auto to_window = [&](int tile) {
-      if (tile / kWindow > window) {
-        ++window;
-        found[0] = found[1], found[1] = found[2];
-        outside[0] = outside[1], outside[1] = outside[2];
-        bool out;
-        look_up(window + 1, found[2], out);
-        outside[2] = __ballot_sync(0xffffffffu, out);
-      }
-    };
     // Ring items of a segment, in the order in which the MMA warp asks for them: K(0), then V(j) and
     // K(j + 1) of every step.  K(j) and, of the step in front, V(j - 1) are read last by batch base + 2 j.
     int it = 0;  // items so far
@@ -487,19 +447,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tv);
       }
       __syncwarp();
+      // Pages of kWindow tiles at a time: lane i has the row in the caches of the i-th slab, -1 where
+      // there is nothing; those of the next ones are asked for when a window is begun.
+      const int slabs_per_page = a.page / kSlab, shift = 31 - __clz(slabs_per_page);
+      auto look_up = [&](int window, int& row, uint32_t& outside) {
+        const long long slab = static_cast<long long>(window) * 32 + lane;
+        row = -1;
+        bool out = false;
+        if (slab * kSlab < w.s.keys) {
+          const int at = a.row_of != nullptr ? a.row_of[w.g] : w.g;
+          const int pid = a.table[static_cast<size_t>(at) * a.max_pages + static_cast<int>(slab >> shift)];
+          out = pid < 0 || pid >= a.num_pages;
+          if (!out) row = (pid * a.Hkv + w.head / a.chunks) * a.page + (static_cast<int>(slab) & (slabs_per_page - 1)) * kSlab;
+        }
+        outside = __ballot_sync(0xffffffffu, out);  // slabs inside the sequence whose page is none
+      };
       // a lane per box: a page's rows, 128 bytes wide (E4M3: all of a row's)
       constexpr int kBoxSubs = E4M3 ? 1 : L::kSub, kBoxBytes = E4M3 ? D : 128;
       constexpr int kSlots = E4M3 ? L::kRawStages : NS, kSlotBytes = E4M3 ? L::kRawBytes : L::kTileBytes;
       const int box = lane / kBoxSubs, sub = lane % kBoxSubs, boxes = BN / a.page;
+      const int box_slab = box < boxes ? box * slabs_per_page : 0;
       const uint32_t to = smem_u32(E4M3 ? smem + L::kRaw : ring) + sub * L::kSubBytes + box * a.page * kBoxBytes;
       int st = 0, step = 0;
       uint32_t turn = 0;  // of the slots, parity
       uint32_t raw_used = 0, raw_parity = 0;  // bf16, of each stage: a tile went to `raw`; the last one's parity
       uint32_t dirty = 0;                     // steps whose `bad` is not zero
+      // Bytes may arrive in front of their announcement: the phase waits for the arrival.
+      auto load = [&](const CUtensorMap* tm, int row, bool look, int read_by) -> bool {
+        if (it >= kSlots) {
+          const bool ok = E4M3 ? warp_wait(past + st, turn ^ 1, abort_flag, a.status) : wait_batch(__shfl_sync(0xffffffffu, reader, st));
+          if (!ok) return false;
+        }
+        uint64_t* bar = (E4M3 || look ? raw : full) + st;
+        if (box < boxes)  // (a row past the tensor's end reads zeros)
+          tma_load_2d_at(to + st * kSlotBytes, tm, sub * 64, row < 0 ? a.rows : row, bar);
+        if (lane == 0) {
+          mbar_expect_tx(bar, kSlotBytes);
+          if (look) mbar_arrive(full + st);  // `full` keeps its turn: such tiles complete it empty
+        }
+        if (look) {
+          raw_parity ^= ((raw_used >> st) & 1u) << st;
+          raw_used |= 1u << st;
+        }
+        if (lane == st) reader = read_by;
+        ++it;
+        if (++st == kSlots) st = 0, turn ^= 1;
+        return true;
+      };
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
-        const int count = w.count, t0 = w.t0, first_look = seen_by_all(a, w) / BN;
-        begin_windows(t0);
+        const int count = w.count, t0 = w.t0, look_from = E4M3 ? count : seen_by_all(a, w) / BN - t0;
+        int window = t0 / kWindow, slab0 = t0 % kWindow * kSlabs, rows, next_rows;
+        uint32_t outside, next_outside;
+        look_up(window, rows, outside);
+        look_up(window + 1, next_rows, next_outside);
         if (w.index > 0 && !E4M3) ok = wait_batch(q_reader);
         if (!ok) break;
         if (!E4M3 && elect_one()) {
@@ -513,45 +514,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
 #pragma unroll 1
-        for (int i = 0; i < 2 * count; ++i) {  // K of step i / 2, or V of step (i - 1) / 2
-          const int j = i >> 1, tile = t0 + j;
-          const bool is_k = !(i & 1);
-          if (a.fault && i >= 3) ok = false;  // test only: starve the MMA warp
-          if (ok && it >= kSlots)
-            ok = E4M3 ? warp_wait(past + st, turn ^ 1, abort_flag, a.status) : wait_batch(__shfl_sync(0xffffffffu, reader, st));
-          if (!ok) break;
-          to_window(tile);
-          const bool behind = tile / kWindow != window;
-          const int slab0 = (tile % kWindow) * kSlabs;
-          if (is_k) {  // slabs whose pages are none, for the softmax; in front of the load that they go with
-            const uint32_t out = ((behind ? outside[0] : outside[1]) >> slab0) & 0xffu, bit = 1u << ((step + j) % kBadSlots);
-            if (out != 0 || (dirty & bit) != 0) {
-              dirty = out ? dirty | bit : dirty & ~bit;
-              if (lane == 0) {
-                misc.bad[(step + j) % kBadSlots] = static_cast<uint8_t>(out);
-                if (out) atomicOr(a.status, DEV_BOUNDS);
-              }
-              __syncwarp();
+        for (int j = 0; ok && j < count; ++j) {
+          if (slab0 == 32) {
+            slab0 = 0;
+            rows = next_rows, outside = next_outside;
+            look_up(++window + 1, next_rows, next_outside);
+          }
+          const int row = __shfl_sync(0xffffffffu, rows, slab0 + box_slab);
+          const uint32_t out = (outside >> slab0) & 0xffu, bit = 1u << ((step + j) % kBadSlots);
+          slab0 += kSlabs;
+          if (out != 0 || (dirty & bit) != 0) {  // for the softmax; in front of the load that it goes with
+            dirty = out ? dirty | bit : dirty & ~bit;
+            if (lane == 0) {
+              misc.bad[(step + j) % kBadSlots] = static_cast<uint8_t>(out);
+              if (out) atomicOr(a.status, DEV_BOUNDS);
             }
+            __syncwarp();
           }
-          const int row = __shfl_sync(0xffffffffu, behind ? found[0] : found[1], slab0 + (box < boxes ? box : 0) * slabs_per_page);
-          const bool look = !E4M3 && !is_k && tile >= first_look;
-          uint64_t* bar = (E4M3 || look ? raw : full) + st;
-          if (lane == 0) {
-            mbar_expect_tx(bar, kSlotBytes);
-            if (look) mbar_arrive(full + st);  // `full` keeps its turn: such tiles complete it empty
-          }
-          __syncwarp();
-          if (box < boxes)  // (a row past the tensor's end reads zeros)
-            tma_load_2d_at(to + st * kSlotBytes, is_k ? &tk : &tv, sub * 64, row < 0 ? a.rows : row, bar);
-          __syncwarp();
-          if (look) {
-            raw_parity ^= ((raw_used >> st) & 1u) << st;
-            raw_used |= 1u << st;
-          }
-          if (lane == st) reader = base + 2 * j + (is_k ? 0 : 2);
-          ++it;
-          if (++st == kSlots) st = 0, turn ^= 1;
+          ok = load(&tk, row, false, base + 2 * j);
+          if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
+          ok = ok && load(&tv, row, j >= look_from, base + 2 * j + 2);
         }
         step += count;
         q_reader = base + 2 * (count - 1);
