@@ -68,8 +68,8 @@ struct Layout {
   static constexpr int kSubBytes = BN * 128;
   static constexpr int kTileBytes = kSub * kSubBytes;
   // ring of K and V tiles; E4M3: behind it a ring of tiles as they are in the cache
-  static constexpr int kStages = E4M3 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 12;
-  static constexpr int kRawStages = E4M3 ? (D == 128 ? 4 : 12) : 0, kRawBytes = BN * D;
+  static constexpr int kStages = E4M3 ? (D == 128 ? 4 : 8) : D == 128 ? 5 : 12;
+  static constexpr int kRawStages = E4M3 ? (D == 128 ? 2 : 8) : 0, kRawBytes = BN * D;
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kRaw = kRing + kStages * kTileBytes;
   static constexpr int kBars = kRaw + kRawStages * kRawBytes;
@@ -618,11 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; ok && i < 2 * count; ++i) {
             const int j = i >> 1, tile = t0 + j, st = it % NS, slot = it % L::kRawStages;
             const bool is_k = !(i & 1);
-            ok = (it < NS || wait_batch(__shfl_sync(0xffffffffu, reader, st))) &&
-                 warp_wait(raw + slot, (it / L::kRawStages) & 1, abort_flag, a.status);
+            ok = warp_wait(raw + slot, (it / L::kRawStages) & 1, abort_flag, a.status);
             if (!ok) break;
-            if (lane == st) reader = base + 2 * j + (is_k ? 0 : 2);
-            ++it;
             uint8_t* from = smem + L::kRaw + slot * L::kRawBytes;
             uint8_t* stage = ring + st * L::kTileBytes;
             if (!is_k && tile >= first_look) {
@@ -643,6 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < kTurns; ++k)
               if (hw + (kLoaders - 1) * k < kGroups) v[k] = ld_shared16(from + ((hw + (kLoaders - 1) * k) * kRows + sub) * D + seg * 16);
+            if (it >= NS) ok = wait_batch(__shfl_sync(0xffffffffu, reader, st));
+            if (!ok) break;
+            if (lane == st) reader = base + 2 * j + (is_k ? 0 : 2);
+            ++it;
+            __syncwarp();  // every lane has its pieces
+            if (lane == 0) mbar_arrive(past + slot);
 #pragma unroll
             for (int k = 0; k < kTurns; ++k) {
               if (hw + (kLoaders - 1) * k < kGroups) {
@@ -658,10 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();  // generic writes -> tensor-core operand reads
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(full + st);
-              mbar_arrive(past + slot);
-            }
+            if (lane == 0) mbar_arrive(full + st);
           }
           q_reader = base + 2 * (count - 1);
           base += 2 * count + 1;
@@ -858,8 +858,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (need) m_run = m_new;
         }
-        // p = 2^(s c - m).  Two row sums: the fp32 weights (lse) and the rounded ones the product
-        // multiplies by (the output is normalised by those, which keeps its error smaller).
+        // p = 2^(s c - m).  Two row sums: the fp32 weights (lse) and, where they are rounded to bf16, the
+        // rounded ones the product multiplies by (the output is normalised by those, which keeps its
+        // error smaller; f16's 2^-11 stays below the output's rounding without, and its second sum cost a
+        // fifth of the softmax).
         const float m_ref = m_run == -INFINITY ? 0.f : m_run;
         const uint64_t c2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_ref, -m_ref);
         uint64_t accf[4] = {0ull, 0ull, 0ull, 0ull}, accb[4] = {0ull, 0ull, 0ull, 0ull};
@@ -881,18 +883,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float p0 = ex2(x0), p1 = ex2(x1);
               pk[i] = E4M3 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
               accf[i & 3] = f2_add(accf[i & 3], f2_pack(p0, p1));
-              if constexpr (E4M3) {
-                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pk[i]));
-                accb[i & 3] = f2_add(accb[i & 3], f2_pack(r.x, r.y));
-              } else {
+              if constexpr (!E4M3)
                 accb[i & 3] = f2_add(accb[i & 3], f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
-              }
             }
             tmem_st16(tS + h * 32 + c * 16, pk);
           }
         }
         l_f32 += sum8(accf);
-        l_mul += sum8(accb);
+        l_mul += sum8(E4M3 ? accf : accb);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
