@@ -184,8 +184,12 @@ struct Walk {
   int t0, count;    // the warp's tiles of this segment: [t0, t0 + count)
   long long left;   // positions from t0 to the end of the share
 };
+// What a kernel reads that may begin before the one in front has ended (see paged_decode_kernel): from L2.
+template <bool SHARED>
+__device__ __forceinline__ int load(const int32_t* p) { return SHARED ? __ldcg(p) : *p; }
+
 // To the next segment; false at the end of the share.
-template <int TK>
+template <int TK, bool SHARED>
 __device__ __forceinline__ bool next_segment(Walk& w, const DecodeArgs& a, int segs) {
   w.left -= w.tb + kSegCost - w.t0;
   if (w.left <= 0) return false;
@@ -193,7 +197,7 @@ __device__ __forceinline__ bool next_segment(Walk& w, const DecodeArgs& a, int s
     w.seg = 0;
     do {  // (there is one, unless the lengths change under the kernel)
       if (++w.b >= a.B) return false;
-      w.tb = tiles_of<TK>(a, a.lens[w.b]);
+      w.tb = tiles_of<TK>(a, load<SHARED>(a.lens + w.b));
     } while (w.tb == 0);
   }
   w.t0 = 0;
@@ -237,7 +241,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   long long* prefix = static_cast<long long*>(a.ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + parts_offset());
 
-  pdl_begin();
+  // (SHARED: the kernel in front, over the beginnings, has nothing that this one reads and writes
+  // nothing that it does; what this one reads was there when that one began.  So they run side by
+  // side, this one on the SMs that are free or become so, and it waits before it ends.  Its loads are
+  // from L2: an L1 may hold older lines.)
+  if (SHARED)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else
+    pdl_begin();
 
   // ---- this warp's share, found by itself: lane i sums sequences [i * per, (i + 1) * per),
   // one scan over the lanes, and one over the sequences of the lane that holds the start
@@ -245,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   long long own = 0;
 #pragma unroll 4
   for (int i = 0; i < per; ++i)
-    if (b_lane + i < a.B) own += positions_of<TK>(a, a.lens[b_lane + i]);
+    if (b_lane + i < a.B) own += positions_of<TK>(a, load<SHARED>(a.lens + b_lane + i));
   auto scan = [&](long long x) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -258,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (blockIdx.x == 0 && w == 0) {
     long long sum = upto - own;
     for (int b = b_lane; b < min(a.B, b_lane + per); ++b) {
-      const int x = positions_of<TK>(a, a.lens[b]);
-      if (x == 0 && a.lens[b] != 0) atomicOr(a.status, DEV_BOUNDS);
+      const int len = load<SHARED>(a.lens + b), x = positions_of<TK>(a, len);
+      if (x == 0 && len != 0) atomicOr(a.status, DEV_BOUNDS);
       prefix[b] = sum;
       sum += x;
     }
@@ -267,7 +278,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const Shares shares = shares_of(all, gridDim.x, tail);
   const int warps = shares.big + shares.small, me = blockIdx.x * kWarps + w;
-  if (static_cast<int>(blockIdx.x) * kWarps >= warps) return;  // a CTA without a share
+  if (static_cast<int>(blockIdx.x) * kWarps >= warps) {  // a CTA without a share
+    if (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   Walk here = {};
   bool busy = me < warps;
   if (busy) {
@@ -281,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int b = b0 + lane;
       long long x = own, y = upto;  // (a sequence per lane: known already)
       if (per > 1) {
-        x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, a.lens[b]) : 0;
+        x = b < a.B && b < (from + 1) * per ? positions_of<TK>(a, load<SHARED>(a.lens + b)) : 0;
         y = scan(x);
       }
       const uint32_t hit = __ballot_sync(0xffffffffu, lo < (base + y) * segs);
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     here.left = hi - lo;
     here.count = static_cast<int>(min(static_cast<long long>(here.tb - here.t0), here.left));
-    if (busy && here.count <= 0) busy = next_segment<TK>(here, a, segs);
+    if (busy && here.count <= 0) busy = next_segment<TK, SHARED>(here, a, segs);
   }
 
   // ---- the warp's ring: its tiles, three ahead
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const long long row0 = static_cast<long long>(ahead.t0 + k) * TK + lane * 16;
     found = 0;
     if (k + lane / NS >= ahead.count) return;
-    const int len = a.lens[ahead.b];
+    const int len = load<SHARED>(a.lens + ahead.b);
     if (row0 >= list_rows(a, len)) return;
     const int h = ahead.seg / chunks;
     const int at = static_cast<int>(row0 >> page_log2(a)), inner = static_cast<int>(row0) & (a.page - 1);
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
       }
     }
-    const int pid = a.table[static_cast<size_t>(ahead.b) * a.max_pages + j + (SHARED ? a.skip[ahead.b] : 0)];
+    const int pid = load<SHARED>(a.table + static_cast<size_t>(ahead.b) * a.max_pages + j + (SHARED ? __ldcg(a.skip + ahead.b) : 0));
     if (pid < 0 || pid >= a.num_pages) {
       atomicOr(a.status, DEV_BOUNDS);
       return;
@@ -340,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   auto load_next = [&](int stage) {
     if (more && k_next >= ahead.count) {
-      more = next_segment<TK>(ahead, a, segs);
+      more = next_segment<TK, SHARED>(ahead, a, segs);
       k_next = 0;
     }
     if (more) {
@@ -406,12 +420,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         if ((WIDE || r == 0) && g + 8 * r < heads) {
           const __nv_bfloat16* p = q + (g + 8 * r) * D + 16 * i;
           if (E4M3) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * t);
+            const uint2 v = SHARED ? __ldcg(reinterpret_cast<const uint2*>(p + 4 * t)) : *reinterpret_cast<const uint2*>(p + 4 * t);
             x = bf16x2_to_f16x2(v.x);
             y = bf16x2_to_f16x2(v.y);
           } else {
-            x = *reinterpret_cast<const uint32_t*>(p + 2 * t);
-            y = *reinterpret_cast<const uint32_t*>(p + 8 + 2 * t);
+            x = load<SHARED>(reinterpret_cast<const int32_t*>(p + 2 * t));
+            y = load<SHARED>(reinterpret_cast<const int32_t*>(p + 8 + 2 * t));
           }
         }
         qa[i][r] = x;
@@ -628,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         store_rows<D, E4M3>(part + 2 * (WIDE ? 16 : 8) + head * D, o, r, 1.f, t);
       }
     }
-    busy = next_segment<TK>(here, a, segs);
+    busy = next_segment<TK, SHARED>(here, a, segs);
   }
 
   // ---- join the warps whose last segment is the same and goes on
@@ -681,6 +695,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       *reinterpret_cast<float4*>(part + 2 * ROWS + row * D + col) = acc;
     }
   }
+  if (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins the parts of a segment if several shares hold tiles of it, in
@@ -900,47 +915,85 @@ __global__ void __launch_bounds__(256) paged_shared_join_kernel(const DecodeArgs
   const int row = blockIdx.x * 8 + warp_id();
   if (row >= a.B * a.Hq) return;
   const int b = row / a.Hq, head = row - b * a.Hq, group = a.Hq / a.Hkv, h = head / group, hh = head - h * group;
-  float top = -INFINITY, l_mul = 0.f, l_f32 = 0.f, acc[V] = {};
-  // a part: log2 maximum, sum of the weights as multiplied, their fp32 sum, the row's values
-  auto add = [&](float m, float mul, float f32, const float* o) {
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = o[V * lane + i];
-    const float up = fmaxf(top, m), f = m == -INFINITY ? 0.f : ex2(m - up), g = top == -INFINITY ? 0.f : ex2(top - up);
-    l_mul = fmaf(l_mul, g, mul * f);
-    l_f32 = fmaf(l_f32, g, f32 * f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(acc[i], g, v[i] * f);
-    top = up;
-  };
+  // the row's parts: those of the beginning, then those of the tail
   const int own = a.lens[b];
-  if (a.skip[b] > 0) {
-    const PagedAttnPlace at = paged_attn_place(p, b, h, hh);
-    for (int c = at.c0; c <= at.c1; ++c) {
-      const float* part = at.c0 == at.c1 ? p.whole : p.parts + (2 * static_cast<size_t>(c) + (c < at.c1 ? 1 : 0)) * paged_attn_part_floats(D);
-      const size_t r = at.c0 == at.c1 ? row : at.row, rows = at.c0 == at.c1 ? static_cast<size_t>(a.B) * a.Hq : kPagedAttnPartRows;
-      const float4 ml = reinterpret_cast<const float4*>(part)[r];
-      add(ml.x, ml.y, ml.z, part + 4 * rows + r * D);
-    }
-  }
+  PagedAttnPlace at = {0, -1, 0};
+  if (a.skip[b] > 0) at = paged_attn_place(p, b, h, hh);
+  int c0 = 0, c1 = -1, k0 = 0, tails = 0;
   if (own > 0) {
-    const int segs = a.Hkv * chunks, seg = h * chunks + hh / kHeads, r = hh % kHeads;
+    const int segs = a.Hkv * chunks, seg = h * chunks + hh / kHeads;
     const long long* prefix = static_cast<const long long*>(a.ws);
     const Shares shares = shares_of(prefix[a.B] * segs, grid, tail);
     const long long size = positions_of<TK>(a, own), first = prefix[b] * segs + seg * size;
-    const int c0 = shares.of(first), c1 = shares.of(first + size - kSegCost - 1);
-    const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
-    if (c0 == c1) {
-      const float2 ml = reinterpret_cast<const float2*>(a.own + static_cast<size_t>(a.B) * a.Hq * D)[row];
-      add(ml.x - kShift, ml.y, ml.y, a.own + static_cast<size_t>(row) * D);
-    } else {
-      const int k0 = c0 / kWarps, n = (c1 - 1) / kWarps - k0 + 2;
-      for (int i = 0; i < n; ++i) {
-        const int c = i == n - 1 ? c1 : max(c0, (k0 + i) * kWarps);
-        const float* part = parts + (2 * static_cast<size_t>(c) + (i < n - 1)) * part_floats(D, WIDE);
-        const float2 ml = reinterpret_cast<const float2*>(part)[r];
-        add(ml.x - kShift, ml.y, ml.y, part + 2 * ROWS + r * D);
+    c0 = shares.of(first);
+    c1 = shares.of(first + size - kSegCost - 1);
+    k0 = c0 / kWarps;
+    tails = c0 == c1 ? 1 : (c1 - 1) / kWarps - k0 + 2;
+  }
+  const int heads = at.c1 - at.c0 + 1, n = heads + tails, r = hh % kHeads;
+  const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
+  const size_t rows = static_cast<size_t>(a.B) * a.Hq;
+  float top = -INFINITY, l_mul = 0.f, l_f32 = 0.f, acc[V] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    // lane i: the i-th part's log2 maximum, sum of the weights as multiplied, their fp32 sum, and values
+    const int i = i0 + lane;
+    float m = -INFINITY, mul = 0.f, f32 = 0.f;
+    const float* o = nullptr;
+    if (i < heads) {
+      const bool whole = heads == 1;
+      const int c = at.c0 + i;
+      const float* part = whole ? p.whole : p.parts + (2 * static_cast<size_t>(c) + (c < at.c1 ? 1 : 0)) * paged_attn_part_floats(D);
+      const size_t at_row = whole ? row : at.row;
+      const float4 ml = reinterpret_cast<const float4*>(part)[at_row];
+      m = ml.x, mul = ml.y, f32 = ml.z;
+      o = part + 4 * (whole ? rows : kPagedAttnPartRows) + at_row * D;
+    } else if (i < n) {
+      float2 ml;
+      if (c0 == c1) {
+        ml = reinterpret_cast<const float2*>(a.own + rows * D)[row];
+        o = a.own + static_cast<size_t>(row) * D;
+      } else {
+        const int k = i - heads, c = k == tails - 1 ? c1 : max(c0, (k0 + k) * kWarps);
+        const float* part = parts + (2 * static_cast<size_t>(c) + (k < tails - 1)) * part_floats(D, WIDE);
+        ml = reinterpret_cast<const float2*>(part)[r];
+        o = part + 2 * ROWS + r * D;
       }
+      m = ml.x - kShift, mul = f32 = ml.y;
+    }
+    float up = fmaxf(top, m);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+    const float g = top == -INFINITY ? 0.f : ex2(top - up), f = m == -INFINITY ? 0.f : ex2(m - up);
+    mul *= f, f32 *= f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      mul += __shfl_xor_sync(0xffffffffu, mul, d);
+      f32 += __shfl_xor_sync(0xffffffffu, f32, d);
+    }
+    l_mul = fmaf(l_mul, g, mul);
+    l_f32 = fmaf(l_f32, g, f32);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= g;
+    top = up;
+    const int count = min(32, n - i0);
+    constexpr int kAtOnce = 8;
+    for (int k0 = 0; k0 < count; k0 += kAtOnce) {
+      float x[kAtOnce][V], fk[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int src = min(k0 + k, count - 1);
+        const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), src));
+        fk[k] = __shfl_sync(0xffffffffu, f, src);
+        if (k0 + k < count) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[k][v] = from[V * lane + v];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (k0 + k < count)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = fmaf(x[k][v], fk[k], acc[v]);
     }
   }
   const float inv = l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;

@@ -283,6 +283,7 @@ struct SharedPlanArgs {
   const int32_t* lens;       // [B]
   const int32_t* starts;     // [G + 1]
   const int32_t* shared;     // [G] pages
+  unsigned long long row_bytes;  // of a token, keys and values of all heads
   int32_t* tail;             // [B] tokens behind the beginning
   int32_t* skip;             // [B] pages of the beginning
   int32_t* group_of;         // [B]

@@ -400,6 +400,7 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
   plan.lens = lens;
   plan.starts = group_start;
   plan.shared = shared_pages;
+  plan.row_bytes = static_cast<unsigned long long>(p->Hkv) * p->D * (p->kv == MCS_KV_E4M3 ? 2 : 4);
   plan.tail = ints;
   plan.skip = ints + p->B;
   plan.group_of = ints + 2 * p->B;

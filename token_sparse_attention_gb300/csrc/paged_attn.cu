@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   all *= segs;
   const int shares = static_cast<int>(min(all, static_cast<long long>(gridDim.x)));
   const bool busy = static_cast<int>(blockIdx.x) < shares;
-  const long long lo = busy ? all * blockIdx.x / shares : 0, hi = busy ? all * (blockIdx.x + 1) / shares : 0;
+  const long long lo = busy ? share_begin(blockIdx.x, all, shares) : 0, hi = busy ? share_begin(blockIdx.x + 1, all, shares) : 0;
   if (busy && lo >= (upto - own) * segs && lo < upto * segs) {
     long long base = (upto - own) * segs;
     for (int k = 0; k < per; ++k) {
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lo < base + size * segs) {
         const long long in = lo - base;
         misc.start.g = g;
-        misc.start.head = static_cast<int>(in / size);
+        misc.start.head = static_cast<int>(quotient(in, size));
         misc.start.offset = in - misc.start.head * size;
         break;
       }
@@ -1004,11 +1004,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Which sequences a common beginning serves.  One CTA: it is a few reads and writes per sequence.
 // Bounds that do not ascend from 0 to B leave every sequence by itself; a group of which fewer than
-// two sequences reach the beginning's end, too.
+// two sequences reach the beginning's end, too; and so does a batch in which reading the beginnings
+// once saves less than kWorth bytes: the attention over them and the join take about 15 us more than
+// reading so much again from L2.
 constexpr int kPlanThreads = 1024;
+constexpr unsigned long long kWorth = 128ull << 20;
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlanArgs a) {
-  pdl_begin();
+  __shared__ unsigned long long s_saved;
   const int tid = threadIdx.x, lane = lane_id();
+  if (tid == 0) s_saved = 0;
+  pdl_begin();
   const long long room = static_cast<long long>(a.max_pages) * a.page;
   bool bad = tid == 0 && (a.starts[0] != 0 || a.starts[a.G] != a.B);
   for (int g = tid; g < a.G; g += kPlanThreads) bad = bad || a.starts[g] > a.starts[g + 1];
@@ -1040,16 +1045,28 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     live = __reduce_add_sync(0xffffffffu, live);
     leader = __reduce_min_sync(0xffffffffu, leader);
     if (wrong) atomicOr(a.status, DEV_BOUNDS);
-    const bool use = live > 1 && keys > 0;
     if (lane == 0) {
+      const bool use = live > 1 && keys > 0;
       a.keys[g] = use ? keys : 0;
       a.leader[g] = use ? leader : 0;
+      if (use) atomicAdd(&s_saved, (live - 1ull) * keys * a.row_bytes);
     }
-    for (int b = lo + lane; use && b < hi; b += 32) {
+  }
+  __syncthreads();
+  const bool worth = s_saved >= kWorth;
+  for (int g = warp_id(); g < a.G; g += kPlanThreads / 32) {
+    const int keys = a.keys[g];
+    __syncwarp();
+    if (keys == 0) continue;
+    if (!worth) {
+      if (lane == 0) a.keys[g] = 0;
+      continue;
+    }
+    for (int b = a.starts[g] + lane; b < a.starts[g + 1]; b += 32) {
       const int len = a.tail[b];
-      if (len == 0 || len < keys) continue;
+      if (len < keys) continue;
       a.tail[b] = len - keys;
-      a.skip[b] = pages;
+      a.skip[b] = a.shared[g];
       a.group_of[b] = g;
     }
   }

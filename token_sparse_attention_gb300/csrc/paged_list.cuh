@@ -22,18 +22,25 @@ __host__ __device__ constexpr size_t paged_attn_part_floats(int D) { return stat
 
 #ifdef __CUDACC__
 
-// sum of floor((a i + b) / m) over i < n: Euclid's algorithm on (m, a), a and m small.
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// x / y, in 32 bits where that is enough (a fifth of the time).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
+}
+
+// sum of floor((a i + b) / m) over i < n: Euclid's algorithm on (m, a), both below 2^16; b below 2^32.
+__device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t a, long long b) {
   long long sum = 0;
   while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
+    const uint32_t qa = a / m;
+    const long long qb = quotient(b, m);
+    sum += (n - 1) * n / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
     const long long y = a * n + b;
     if (y < m) break;
-    n = y / m;
+    n = quotient(y, m);
     b = y - n * m;
-    const long long t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -82,11 +89,17 @@ __device__ __forceinline__ long long positions_of(const PagedAttnArgs& a, const 
   return pairs_upto(a, s, units / 2) + ((units & 1) ? tiles_until(a, s, s.n) + kPagedAttnSegCost : 0);
 }
 
-// The shares of a list of `all` positions: share c begins at all * c / shares.
+// The shares of a list of `all` positions: share c begins at floor(all * c / shares).
+__device__ __forceinline__ long long share_begin(int c, long long all, int shares) {
+  const long long q = quotient(all, shares);
+  return c * q + static_cast<uint32_t>(c) * static_cast<uint32_t>(all - q * shares) / static_cast<uint32_t>(shares);
+}
+// The share that holds position x: an estimate that is off by one at most, then exact products.
 __device__ __forceinline__ int share_of(long long x, long long all, int shares) {
-  int c = static_cast<int>(x * shares / all);
-  while (c + 1 < shares && all * (c + 1) / shares <= x) ++c;
-  while (c > 0 && all * c / shares > x) --c;
+  const long long y = (x + 1) * shares;
+  int c = static_cast<int>(static_cast<float>(x) * (static_cast<float>(shares) / static_cast<float>(all)));
+  while (c > 0 && c * all >= y) --c;
+  while ((c + 1) * all < y) ++c;
   return c;
 }
 
