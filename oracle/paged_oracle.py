@@ -117,7 +117,7 @@ def attn(q, k_cache, v_cache, table, lens, cu, scale, num_pages=None):
             continue
         rows = [(j * page + r, table[b, j], r) for j in range(-(-n // page)) for r in range(page)
                 if j * page + r < n and 0 <= table[b, j] < num_pages]
-        at = np.array(rows).reshape(-1, 3)
+        at = np.array(rows, int).reshape(-1, 3)
         for h in range(Hkv):
             k, v = k_cache[at[:, 1], h, at[:, 2]], v_cache[at[:, 1], h, at[:, 2]]
             for t in range(new):

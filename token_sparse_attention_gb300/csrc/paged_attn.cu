@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           ok = load(&tk, row, false, base + 2 * j);
-          if (a.fault && j >= 1) ok = false;  // test only: starve the MMA warp
+          if (a.fault) ok = false;  // test only: starve the MMA warp
           ok = ok && load(&tv, row, j >= look_from, base + 2 * j + 2);
         }
         step += count;
