@@ -329,14 +329,13 @@ size_t paged_compact_workspace_bytes(int num_pages);
 struct CopyArgs {
   int n, Hkv, page, num_pages;
   int row_words, mean_words; // 16-byte words of a row of the caches, and of a page's mean per head
-  int parts;                 // set by the launcher: pieces of a page
   const int32_t* moves;      // [n, 3]
   void* k;
   void* v;
   void* mean;                // nullable
   unsigned* status;
 };
-cudaError_t launch_paged_copy(CopyArgs a, cudaStream_t stream);
+cudaError_t launch_paged_copy(const CopyArgs& a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- norm and rotation
 

@@ -30,10 +30,16 @@ constexpr int kAll = kCluster * kThreads;
 constexpr int kWarps = kThreads / 32;
 constexpr long long kTableHere = 1 << 16;  // entries of a table that the cluster writes itself
 
-// What one CTA tells the others, in the workspace.
+// What the CTAs tell each other: two words of each in everyone's shared memory.
 struct Told {
-  int bad, a, b, c;
+  int2 of[kCluster];
 };
+__device__ __forceinline__ void tell(Told& told, int2 x) {
+  if (threadIdx.x >= kCluster) return;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&told.of[blockIdx.x])), "r"(threadIdx.x));
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x.x), "r"(x.y) : "memory");
+}
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -109,49 +115,82 @@ __device__ __forceinline__ void write_rows(const PagesArgs& a, const int32_t* fr
   }
 }
 
-// Workspace: Told [kCluster], holders' changes [num_pages], the children's fresh pages [n] (-1: none).
+// Workspace: a word for the launch behind this one, holders' changes [num_pages], the children's
+// fresh pages [n] (-1: none).
+constexpr int kWsHead = 4;  // words
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_fork_kernel(const PagesArgs a, bool here) {
   extern __shared__ int32_t sm[];
   int32_t* s_count = sm;             // [B] children
   int32_t* s_first = s_count + a.B;  // [B] the first of them
+  int32_t* s_open = s_first + a.B;   // [B] the page that is not full, -1: none; -2 - it: which others hold, too
   __shared__ int s_sums[33];
-  Told* told = reinterpret_cast<Told*>(a.ws);
-  int32_t* change = a.ws + sizeof(Told) * kCluster / 4;
+  __shared__ Told s_told;
+  int32_t* change = a.ws + kWsHead;
   int32_t* fresh = change + a.num_pages;
   const int tid = threadIdx.x, me = blockIdx.x * kThreads + tid;
   const int shift = 31 - __clz(a.page), mask = a.page - 1;
   const long long room = static_cast<long long>(a.max_pages) << shift;
   pdl_begin();
-  for (int b = tid; b < a.B; b += kThreads) s_count[b] = 0, s_first[b] = 0x7fffffff;
+  const int head = a.free_head[0], parent0 = tid < a.n ? a.parents[tid] : -1;
+  bool bad = false;
+  for (int b = tid; b < a.B; b += kThreads) {
+    const int len = a.lens[b];
+    int open = -1;
+    s_count[b] = 0, s_first[b] = 0x7fffffff;
+    if (len < 0 || len > room) {
+      bad = true;
+    } else if ((len & mask) != 0) {
+      open = a.table[static_cast<size_t>(b) * a.max_pages + (len >> shift)];
+      if (open < 0 || open >= a.num_pages)
+        bad = true;
+      else if (a.extra[open] != 0)
+        open = -2 - open;
+    }
+    s_open[b] = open;
+  }
   for (int p = me; p < a.num_pages; p += kAll) change[p] = 0;
   __syncthreads();
-  bool bad = false;
+#pragma unroll 1
   for (int i = tid; i < a.n; i += kThreads) {
-    const int p = a.parents[i];
+    const int p = i == tid ? parent0 : a.parents[i];
     bad = bad || p < -1 || p >= a.B;
     if (p >= 0 && p < a.B) {
       atomicAdd(s_count + p, 1);
       atomicMin(s_first + p, i);
     }
   }
-  for (int b = tid; b < a.B; b += kThreads) bad = bad || a.lens[b] < 0 || a.lens[b] > room;
+  cluster_sync();  // the changes are zero
   bad = __syncthreads_or(bad);
-  const int head = a.free_head[0];
-  int need = 0;
-  if (!bad) {  // every CTA for itself: the children that copy, and their places in the free list
-    for (int i0 = 0; i0 < a.n; i0 += kThreads) {
-      const int i = i0 + tid, p = i < a.n ? a.parents[i] : -1, len = p < 0 ? 0 : a.lens[p];
-      bool copies = false;
-      if ((len & mask) != 0) {
-        const int pid = a.table[static_cast<size_t>(p) * a.max_pages + (len >> shift)];
-        if (pid < 0 || pid >= a.num_pages)
-          bad = true;
-        else
-          copies = s_first[p] != i || a.extra[pid] != 0;
+  if (!bad) {
+    for_pages(a, [&](int b, int j, int pid, int len) {
+      if (pid < 0 || pid >= a.num_pages) {
+        bad = true;
+        return;
       }
-      int total;
-      const int at = head + need + block_scan(copies ? 1 : 0, s_sums, total);
-      if (i < a.n && blockIdx.x == 0) {
+      const int c = s_count[b], d = j < (len >> shift) ? c - 1 : c > 0 && s_open[b] >= 0 ? 0 : -1;
+      if (d != 0) atomicAdd(change + pid, d);
+    });
+  }
+  // children that copy, and their places in the free list: every CTA counts, the last one writes
+  int need = 0;
+  bad = __syncthreads_or(bad);
+  if (!bad) {
+    bad = head < 0 || head > a.n_free;
+#pragma unroll 1
+    for (int i0 = 0; i0 < a.n; i0 += kThreads) {
+      const int i = i0 + tid, p = i >= a.n ? -1 : i == tid ? parent0 : a.parents[i], open = p < 0 ? -1 : s_open[p];
+      const bool copies = open < -1 || (open >= 0 && s_first[p] != i);
+      const uint32_t votes = __ballot_sync(0xffffffffu, copies);
+      if (lane_id() == 0) s_sums[warp_id()] = __popc(votes);
+      __syncthreads();
+      int at = head + need + __popc(votes & ((1u << lane_id()) - 1u)), total = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int x = s_sums[w];
+        at += w < warp_id() ? x : 0;
+        total += x;
+      }
+      if (i < a.n && blockIdx.x == kCluster - 1) {
         int pid = -1;
         if (copies && at >= 0 && at < a.n_free) {
           pid = a.free_pages[at];
@@ -160,22 +199,11 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_for
         fresh[i] = pid;
       }
       need += total;
+      __syncthreads();
     }
-    bad = __syncthreads_or(bad) || head < 0 || head > a.n_free || need > a.n_free - head;
+    bad = bad || need > a.n_free - head;
   }
-  cluster_sync();  // the changes are zero
-  if (!bad) {
-    for_pages(a, [&](int b, int j, int pid, int len) {
-      if (pid < 0 || pid >= a.num_pages) {
-        bad = true;
-        return;
-      }
-      const int c = s_count[b], d = j < (len >> shift) ? c - 1 : c > 0 && a.extra[pid] == 0 ? 0 : -1;
-      if (d != 0) atomicAdd(change + pid, d);
-    });
-  }
-  bad = __syncthreads_or(bad);
-  cluster_sync();
+  cluster_sync();  // the changes are there
   // pages without holders: each CTA looks at its part of the cache
   const int part = (a.num_pages + kCluster - 1) / kCluster;
   const int p0 = min(a.num_pages, part * static_cast<int>(blockIdx.x)), p1 = min(a.num_pages, p0 + part);
@@ -188,35 +216,38 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_for
   bad = __syncthreads_or(bad);
   int freed_here;
   block_scan(mine, s_sums, freed_here);
-  if (tid == 0) told[blockIdx.x] = {bad ? 1 : 0, freed_here, 0, 0};
+  tell(s_told, make_int2(bad, freed_here));
   cluster_sync();
   int freed = 0, before = 0;
 #pragma unroll
   for (int c = 0; c < kCluster; ++c) {
-    const int x = __ldcg(&told[c].a);
-    bad = bad || __ldcg(&told[c].bad) != 0;
-    if (c < static_cast<int>(blockIdx.x)) before += x;
-    freed += x;
+    const int2 x = s_told.of[c];
+    bad = bad || x.x != 0;
+    if (c < static_cast<int>(blockIdx.x)) before += x.y;
+    freed += x.y;
   }
   const int head_out = head + need - freed;
   bad = bad || head_out < 0;
   if (me == 0) {
-    told[0].b = bad;  // for the launch behind this one
+    a.ws[0] = bad;
     if (bad)
       atomicOr(a.status, DEV_BOUNDS);
     else
       a.head_out[0] = head_out;
   }
+#pragma unroll 1
   for (int i = me; i < a.n; i += kAll) {
     const int p = bad ? -1 : a.parents[i], len = p < 0 ? 0 : a.lens[p], to = bad ? -1 : __ldcg(fresh + i);
+    const int open = p < 0 ? -1 : s_open[p];
     if (!bad) a.lens_out[i] = len;
-    a.moves[3 * i] = to < 0 ? -1 : a.table[static_cast<size_t>(p) * a.max_pages + (len >> shift)];
+    a.moves[3 * i] = to < 0 ? -1 : open < 0 ? -2 - open : open;
     a.moves[3 * i + 1] = to;
     a.moves[3 * i + 2] = to < 0 ? 0 : len & mask;
   }
   if (bad) return;  // nothing is taken
   if (here) write_rows(a, fresh, blockIdx.x * kWarps + warp_id(), kCluster * kWarps);
   // the free list: what is freed, ascending, in front of what was free
+#pragma unroll 1
   for (int q0 = p0; q0 < p1; q0 += kThreads) {
     const int p = q0 + tid;
     const int d = p < p1 ? __ldcg(change + p) : 0, extra = p < p1 ? a.extra[p] : 0;
@@ -233,8 +264,8 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_for
 
 __global__ void __launch_bounds__(256) paged_fork_rows_kernel(const PagesArgs a) {
   pdl_begin();
-  if (reinterpret_cast<const Told*>(a.ws)[0].b) return;
-  write_rows(a, a.ws + sizeof(Told) * kCluster / 4 + a.num_pages, blockIdx.x * 8 + warp_id(), gridDim.x * 8);
+  if (a.ws[0]) return;
+  write_rows(a, a.ws + kWsHead + a.num_pages, blockIdx.x * 8 + warp_id(), gridDim.x * 8);
 }
 
 // ------------------------------------------------------------------ compaction
@@ -254,11 +285,11 @@ __device__ __forceinline__ void renumber_rows(const PagesArgs& a, const int32_t*
   }
 }
 
-// Workspace: Told [kCluster], tokens in each page [num_pages], the pages' new numbers [num_pages].
+// Workspace: a word for the launch behind this one, tokens in each page [num_pages], the pages' new numbers [num_pages].
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_compact_kernel(const PagesArgs a, bool here) {
   __shared__ int s_sums[33];
-  Told* told = reinterpret_cast<Told*>(a.ws);
-  int32_t* fill = a.ws + sizeof(Told) * kCluster / 4;
+  __shared__ Told s_told, s_front;
+  int32_t* fill = a.ws + kWsHead;
   int32_t* to = fill + a.num_pages;
   const int tid = threadIdx.x, me = blockIdx.x * kThreads + tid;
   const long long room = static_cast<long long>(a.max_pages) * a.page;
@@ -285,27 +316,26 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_com
     return total;
   };
   const int own = count(a.num_pages);
-  if (tid == 0) told[blockIdx.x] = {bad ? 1 : 0, own, 0, 0};
+  tell(s_told, make_int2(bad, own));
   cluster_sync();
   int used = 0, before = 0;  // U, and of these in front of this CTA's part
 #pragma unroll
   for (int c = 0; c < kCluster; ++c) {
-    const int x = __ldcg(&told[c].a);
-    bad = bad || __ldcg(&told[c].bad) != 0;
-    if (c < static_cast<int>(blockIdx.x)) before += x;
-    used += x;
+    const int2 x = s_told.of[c];
+    bad = bad || x.x != 0;
+    if (c < static_cast<int>(blockIdx.x)) before += x.y;
+    used += x.y;
   }
   const int head_out = a.n_free - (a.num_pages - used);
   bad = bad || head_out < 0;
-  const int in_front = count(used);
-  if (tid == 0) told[blockIdx.x].b = in_front;
+  tell(s_front, make_int2(0, count(used)));
   cluster_sync();
   int moves = used;  // M: the free pages among the first U
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) moves -= __ldcg(&told[c].b);
+  for (int c = 0; c < kCluster; ++c) moves -= s_front.of[c].y;
   moves = bad ? 0 : min(moves, a.n);
   if (me == 0) {
-    told[0].c = bad;  // for the launch behind this one
+    a.ws[0] = bad;
     if (bad)
       atomicOr(a.status, DEV_BOUNDS);
     else
@@ -344,68 +374,50 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_com
 
 __global__ void __launch_bounds__(256) paged_renumber_kernel(const PagesArgs a) {
   pdl_begin();
-  if (reinterpret_cast<const Told*>(a.ws)[0].c) return;
-  renumber_rows(a, a.ws + sizeof(Told) * kCluster / 4 + a.num_pages, blockIdx.x * 8 + warp_id(), gridDim.x * 8);
+  if (a.ws[0]) return;
+  renumber_rows(a, a.ws + kWsHead + a.num_pages, blockIdx.x * 8 + warp_id(), gridDim.x * 8);
 }
 
 // ------------------------------------------------------------------ copies
 
-// A unit is one of the two caches of a move (and its page's mean, with the first); a block looks
-// kCopyThreads of its units over at once, since most moves of a call may be none.  Bound: HBM.
-constexpr int kCopyThreads = 256;
-__global__ void __launch_bounds__(kCopyThreads) paged_page_copy_kernel(const CopyArgs a) {
-  __shared__ int s_todo[kCopyThreads];
-  __shared__ int s_count;
+// A unit is one KV head's rows of one of the two caches (and, with the first, its mean), which lie one
+// behind another: at most 32 KB.  A warp per unit, the next one's entry on its way; every warp by
+// itself, so that one's first loads cover the other's last stores.  Bound: HBM.
+constexpr int kCopyWarps = 8;
+__global__ void __launch_bounds__(32 * kCopyWarps) paged_page_copy_kernel(const CopyArgs a) {
   pdl_begin();
-  const int tid = threadIdx.x;
-  const long long units = 2LL * a.parts * a.n;
-  for (long long u0 = blockIdx.x; u0 < units; u0 += static_cast<long long>(kCopyThreads) * gridDim.x) {
-    __syncthreads();
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    const long long mine = u0 + static_cast<long long>(tid) * gridDim.x;
-    if (mine < units) {
-      const int32_t* m = a.moves + 3 * (mine / (2 * a.parts));
-      if (m[0] >= 0) s_todo[atomicAdd(&s_count, 1)] = tid;
+  const int lane = lane_id();
+  const long long units = 2LL * a.Hkv * a.n, step = static_cast<long long>(gridDim.x) * kCopyWarps;
+  long long u = static_cast<long long>(blockIdx.x) * kCopyWarps + warp_id();
+  auto entry = [&](long long x, int k) { return x < units ? a.moves[3 * (x / (2 * a.Hkv)) + k] : -1; };
+  int from = entry(u, 0), to = entry(u, 1), rows = entry(u, 2);
+  for (; u < units; u += step) {
+    const int src_page = from, dst_page = to, n = rows;
+    from = entry(u + step, 0), to = entry(u + step, 1), rows = entry(u + step, 2);
+    if (src_page < 0 || src_page == dst_page) continue;
+    const int which = static_cast<int>(u % (2 * a.Hkv)), h = which % a.Hkv;
+    if (src_page >= a.num_pages || dst_page < 0 || dst_page >= a.num_pages || n < 0 || n > a.page) {
+      if (lane == 0) atomicOr(a.status, DEV_BOUNDS);
+      continue;
     }
-    __syncthreads();
-    for (int k = 0; k < s_count; ++k) {
-      const long long unit = u0 + static_cast<long long>(s_todo[k]) * gridDim.x;
-      const int32_t* m = a.moves + 3 * (unit / (2 * a.parts));
-      const int which = static_cast<int>(unit % (2 * a.parts)), cache = which / a.parts, piece = which % a.parts;
-      const int from = m[0], to = m[1], rows = m[2];
-      if (from >= a.num_pages || to < 0 || to >= a.num_pages || rows < 0 || rows > a.page) {
-        if (tid == 0) atomicOr(a.status, DEV_BOUNDS);
-        continue;
-      }
-      if (from == to) continue;
-      // words of 16 bytes: a head's rows one behind another, heads page * row apart
-      const int h0 = static_cast<int>(static_cast<long long>(a.Hkv) * piece / a.parts);
-      const int h1 = static_cast<int>(static_cast<long long>(a.Hkv) * (piece + 1) / a.parts);
-      const int row = a.row_words, run = rows * row, words = (h1 - h0) * run;
-      uint4* base = static_cast<uint4*>(cache ? a.v : a.k);
-      const size_t pitch = static_cast<size_t>(a.page) * row;
-      const uint4* src = base + (static_cast<size_t>(from) * a.Hkv + h0) * pitch;
-      uint4* dst = base + (static_cast<size_t>(to) * a.Hkv + h0) * pitch;
-      constexpr int kAtOnce = 8;
-      for (int w0 = tid; w0 < words; w0 += kAtOnce * kCopyThreads) {
-        uint4 x[kAtOnce];
-        int at[kAtOnce];
+    const int words = n * a.row_words;
+    const size_t pitch = static_cast<size_t>(a.page) * a.row_words;
+    uint4* base = static_cast<uint4*>(which >= a.Hkv ? a.v : a.k);
+    const uint4* src = base + (static_cast<size_t>(src_page) * a.Hkv + h) * pitch;
+    uint4* dst = base + (static_cast<size_t>(dst_page) * a.Hkv + h) * pitch;
+    if (a.mean != nullptr && which < a.Hkv && lane < a.mean_words) {
+      uint4* mean = static_cast<uint4*>(a.mean) + static_cast<size_t>(h) * a.mean_words + lane;
+      mean[static_cast<size_t>(dst_page) * a.Hkv * a.mean_words] = ld_global16(mean + static_cast<size_t>(src_page) * a.Hkv * a.mean_words);
+    }
+    constexpr int kAtOnce = 8;
+    for (int w = lane; w < words; w += 32 * kAtOnce) {
+      uint4 x[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int w = w0 + i * kCopyThreads, h = run == static_cast<int>(pitch) ? 0 : w / max(run, 1);
-          at[i] = w + h * (static_cast<int>(pitch) - run);
-          if (w < words) x[i] = ld_global16(src + at[i]);
-        }
+      for (int i = 0; i < kAtOnce; ++i)
+        if (w + 32 * i < words) x[i] = ld_global16(src + w + 32 * i);
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-          if (w0 + i * kCopyThreads < words) dst[at[i]] = x[i];
-      }
-      if (a.mean != nullptr && which == 0) {
-        const int n = a.Hkv * a.mean_words;
-        uint4* mean = static_cast<uint4*>(a.mean);
-        for (int w = tid; w < n; w += kCopyThreads) mean[static_cast<size_t>(to) * n + w] = ld_global16(mean + static_cast<size_t>(from) * n + w);
-      }
+      for (int i = 0; i < kAtOnce; ++i)
+        if (w + 32 * i < words) dst[w + 32 * i] = x[i];
     }
   }
 }
@@ -413,15 +425,18 @@ __global__ void __launch_bounds__(kCopyThreads) paged_page_copy_kernel(const Cop
 }  // namespace
 
 size_t paged_fork_workspace_bytes(int num_pages) {
-  return sizeof(Told) * kCluster + (static_cast<size_t>(num_pages) + 4096) * sizeof(int32_t);
+  return (kWsHead + static_cast<size_t>(num_pages) + 4096) * sizeof(int32_t);
 }
 size_t paged_compact_workspace_bytes(int num_pages) {
-  return sizeof(Told) * kCluster + 2 * static_cast<size_t>(num_pages) * sizeof(int32_t);
+  return (kWsHead + 2 * static_cast<size_t>(num_pages)) * sizeof(int32_t);
 }
 
 cudaError_t launch_paged_fork(const PagesArgs& a, cudaStream_t stream) {
   const bool here = static_cast<long long>(a.n) * a.max_pages <= kTableHere;
-  cudaError_t e = launch_dependent(paged_fork_kernel, kCluster, kThreads, 2 * a.B * sizeof(int32_t), stream, a, here);
+  constexpr int kMost = 3 * 4096 * sizeof(int32_t);
+  cudaError_t e = cudaFuncSetAttribute(paged_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(paged_fork_kernel, kCluster, kThreads, 3 * a.B * sizeof(int32_t), stream, a, here);
   if (e != cudaSuccess || here) return e;
   int sms = 0;
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
@@ -437,15 +452,12 @@ cudaError_t launch_paged_compact(const PagesArgs& a, cudaStream_t stream) {
   return launch_dependent(paged_renumber_kernel, 4 * sms, 256, 0, stream, a);
 }
 
-cudaError_t launch_paged_copy(CopyArgs a, cudaStream_t stream) {
+cudaError_t launch_paged_copy(const CopyArgs& a, cudaStream_t stream) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  // pieces of at most about 16 KB, whole heads
-  const long long bytes = 16LL * a.Hkv * a.page * a.row_words;
-  a.parts = static_cast<int>(std::max(1LL, std::min<long long>(a.Hkv, bytes >> 14)));
-  const long long units = 2LL * a.parts * a.n;
-  return launch_dependent(paged_page_copy_kernel, static_cast<unsigned>(std::min<long long>(units, 6LL * sms)), kCopyThreads, 0, stream, a);
+  const long long blocks = (2LL * a.Hkv * a.n + kCopyWarps - 1) / kCopyWarps;
+  return launch_dependent(paged_page_copy_kernel, static_cast<unsigned>(std::min<long long>(blocks, 8LL * sms)), 32 * kCopyWarps, 0, stream, a);
 }
 
 }  // namespace mcs
