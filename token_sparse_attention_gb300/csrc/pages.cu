@@ -387,15 +387,19 @@ constexpr int kCopyWarps = 8;
 __global__ void __launch_bounds__(32 * kCopyWarps) paged_page_copy_kernel(const CopyArgs a) {
   pdl_begin();
   const int lane = lane_id();
-  const long long units = 2LL * a.Hkv * a.n, step = static_cast<long long>(gridDim.x) * kCopyWarps;
-  long long u = static_cast<long long>(blockIdx.x) * kCopyWarps + warp_id();
-  auto entry = [&](long long x, int k) { return x < units ? a.moves[3 * (x / (2 * a.Hkv)) + k] : -1; };
-  int from = entry(u, 0), to = entry(u, 1), rows = entry(u, 2);
-  for (; u < units; u += step) {
-    const int src_page = from, dst_page = to, n = rows;
-    from = entry(u + step, 0), to = entry(u + step, 1), rows = entry(u + step, 2);
+  // unit: entry * per + which; from one of a warp's units to its next
+  const int per = 2 * a.Hkv, step = gridDim.x * kCopyWarps, step_entry = step / per, step_which = step - step_entry * per;
+  const int first = blockIdx.x * kCopyWarps + warp_id();
+  int at = first / per, next_which = first - at * per;
+  auto entry = [&](int k) { return at < a.n ? a.moves[3 * static_cast<size_t>(at) + k] : -1; };
+  int from = entry(0), to = entry(1), rows = entry(2);
+  while (at < a.n) {
+    const int src_page = from, dst_page = to, n = rows, which = next_which, h = which >= a.Hkv ? which - a.Hkv : which;
+    at += step_entry;
+    next_which += step_which;
+    if (next_which >= per) next_which -= per, ++at;
+    from = entry(0), to = entry(1), rows = entry(2);
     if (src_page < 0 || src_page == dst_page) continue;
-    const int which = static_cast<int>(u % (2 * a.Hkv)), h = which % a.Hkv;
     if (src_page >= a.num_pages || dst_page < 0 || dst_page >= a.num_pages || n < 0 || n > a.page) {
       if (lane == 0) atomicOr(a.status, DEV_BOUNDS);
       continue;
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(32 * kCopyWarps) paged_page_copy_kernel(const 
       uint4* mean = static_cast<uint4*>(a.mean) + static_cast<size_t>(h) * a.mean_words + lane;
       mean[static_cast<size_t>(dst_page) * a.Hkv * a.mean_words] = ld_global16(mean + static_cast<size_t>(src_page) * a.Hkv * a.mean_words);
     }
-    constexpr int kAtOnce = 8;
+    constexpr int kAtOnce = 16;
     for (int w = lane; w < words; w += 32 * kAtOnce) {
       uint4 x[kAtOnce];
 #pragma unroll
