@@ -557,8 +557,8 @@ mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void
  * stay as they were.  Values behind a token, infinite or NaN, do not reach it;
  * an infinite or NaN value that it attends to makes its column NaN or infinite.
  * E4M3: q is converted to f16 as in mcs_paged_decode.  The weights are rounded to
- * bf16 (bf16 cache) or f16 (E4M3) for the product with v and normalised by the sum of the
- * rounded ones; scores, maxima and sums are fp32.  Results do not depend on timing.
+ * bf16 (bf16 cache) or f16 (E4M3) for the product with v; scores, maxima and the sums
+ * that normalise it are fp32.  Results do not depend on timing.
  * ws: at least mcs_paged_attn_workspace(p) bytes, as for mcs_paged_decode.
  * 0 <= T <= 2^30, T * Hq below 2^31.
  */
@@ -575,8 +575,9 @@ mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* 
  * ascends from 0 to B; 1 <= groups <= B), and the first shared_pages[g] entries of
  * their table rows are the same pages, full ones, as mcs_paged_fork leaves them:
  * these are read once for the whole group, from the table row of its first
- * sequence that holds them.  Same results as mcs_paged_decode, with the weights of
- * the common beginning rounded as in mcs_paged_attn.  Groups may have one
+ * sequence that holds them, unless that saves the batch less than 128 MB of reads,
+ * where every sequence is read by itself.  Same results as mcs_paged_decode, with the
+ * weights of the common beginning rounded as in mcs_paged_attn.  Groups may have one
  * sequence, or nothing in common (0).  group_start that does not ascend so sets
  * MCS_ERR_BOUNDS in the device status and shares nothing; a sequence that is
  * neither empty nor as long as its group's beginning, or a negative or too large

@@ -933,20 +933,20 @@ __global__ void __launch_bounds__(256) paged_shared_join_kernel(const DecodeArgs
   const int heads = at.c1 - at.c0 + 1, n = heads + tails, r = hh % kHeads;
   const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + parts_offset());
   const size_t rows = static_cast<size_t>(a.B) * a.Hq;
-  float top = -INFINITY, l_mul = 0.f, l_f32 = 0.f, acc[V] = {};
+  float top = -INFINITY, sum = 0.f, acc[V] = {};
   for (int i0 = 0; i0 < n; i0 += 32) {
-    // lane i: the i-th part's log2 maximum, sum of the weights as multiplied, their fp32 sum, and values
+    // lane i: the i-th part's log2 maximum, sum of weights, and values
     const int i = i0 + lane;
-    float m = -INFINITY, mul = 0.f, f32 = 0.f;
+    float m = -INFINITY, l = 0.f;
     const float* o = nullptr;
     if (i < heads) {
       const bool whole = heads == 1;
       const int c = at.c0 + i;
       const float* part = whole ? p.whole : p.parts + (2 * static_cast<size_t>(c) + (c < at.c1 ? 1 : 0)) * paged_attn_part_floats(D);
       const size_t at_row = whole ? row : at.row;
-      const float4 ml = reinterpret_cast<const float4*>(part)[at_row];
-      m = ml.x, mul = ml.y, f32 = ml.z;
-      o = part + 4 * (whole ? rows : kPagedAttnPartRows) + at_row * D;
+      const float2 ml = reinterpret_cast<const float2*>(whole ? part + rows * D : part)[at_row];
+      m = ml.x, l = ml.y;
+      o = part + (whole ? 0 : 2 * kPagedAttnPartRows) + at_row * D;
     } else if (i < n) {
       float2 ml;
       if (c0 == c1) {
@@ -958,20 +958,16 @@ __global__ void __launch_bounds__(256) paged_shared_join_kernel(const DecodeArgs
         ml = reinterpret_cast<const float2*>(part)[r];
         o = part + 2 * ROWS + r * D;
       }
-      m = ml.x - kShift, mul = f32 = ml.y;
+      m = ml.x - kShift, l = ml.y;
     }
     float up = fmaxf(top, m);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
     const float g = top == -INFINITY ? 0.f : ex2(top - up), f = m == -INFINITY ? 0.f : ex2(m - up);
-    mul *= f, f32 *= f;
+    l *= f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      mul += __shfl_xor_sync(0xffffffffu, mul, d);
-      f32 += __shfl_xor_sync(0xffffffffu, f32, d);
-    }
-    l_mul = fmaf(l_mul, g, mul);
-    l_f32 = fmaf(l_f32, g, f32);
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    sum = fmaf(sum, g, l);
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= g;
     top = up;
@@ -996,7 +992,7 @@ __global__ void __launch_bounds__(256) paged_shared_join_kernel(const DecodeArgs
           for (int v = 0; v < V; ++v) acc[v] = fmaf(x[k][v], fk[k], acc[v]);
     }
   }
-  const float inv = l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
   float y[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) y[i] = E4M3 ? acc[i] * inv * a.v_scale : acc[i] * inv;
@@ -1005,7 +1001,7 @@ __global__ void __launch_bounds__(256) paged_shared_join_kernel(const DecodeArgs
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
   else
     *reinterpret_cast<uint32_t*>(out) = pack_bf16(y[0], y[1]);
-  if (a.lse != nullptr && lane == 0) a.lse[row] = l_f32 == 0.f ? -INFINITY : (top + log2f(l_f32)) * 0.6931471805599453f;
+  if (a.lse != nullptr && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, bool E4M3, bool WIDE>

@@ -261,7 +261,7 @@ struct PagedAttnArgs {
   const int32_t* keys;       // [G] keys
   __nv_bfloat16* out;        // [T, Hq, D]
   float* lse;                // [T, Hq], nullable
-  float* whole;              // null, or where rows go unjoined: (log2 max, sums) [T * Hq] float4, values
+  float* whole;              // null, or where rows go unjoined: values [T * Hq, D], (log2 maximum, sum) [T * Hq]
   float* parts;              // paged_attn_parts_bytes
   int4* ends;                // paged_attn_ends_bytes
   long long* places;         // [G + 1] first positions, nullable

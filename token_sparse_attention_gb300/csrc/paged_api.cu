@@ -147,7 +147,7 @@ SharedWs shared_ws(const mcs_paged* p) {
   w.ends = take(mcs::paged_attn_ends_bytes());
   w.parts = take(mcs::paged_attn_parts_bytes(p->D));
   w.places = take((p->B + 1) * sizeof(long long));
-  w.whole = take(rows * (4 + p->D) * sizeof(float));
+  w.whole = take(rows * (2 + p->D) * sizeof(float));
   w.own = take(rows * (2 + p->D) * sizeof(float));
   w.ints = take((6 * static_cast<size_t>(p->B) + 1) * sizeof(int32_t));
   w.total = at;

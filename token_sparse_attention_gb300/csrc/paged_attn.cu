@@ -82,8 +82,8 @@ struct Layout {
   static constexpr int kAside = E4M3 ? kRawStages : kStages;
   static constexpr int kNumBars = kStages + 2 * kAside + kDone + 10;
   static constexpr int kBadKey = kBars + kNumBars * 8;           // [2][D] words
-  static constexpr int kMl = kBadKey + 2 * D * 4;                // [3][128] floats
-  static constexpr int kMisc = kMl + 3 * BM * 4;                 // Misc
+  static constexpr int kMl = kBadKey + 2 * D * 4;                // [2][128] floats
+  static constexpr int kMisc = kMl + 2 * BM * 4;                 // Misc
   static constexpr int kSmem = kMisc + 80;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert((kStages + kRawStages) / 2 + 2 <= kBadSlots, "bad slots");
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool single = w.single;
       int ahead = limit - w.t0 * BN - (single ? x * (BN / 2) : 0);  // keys that the row sees from the chain's first on
       const int folded = fold(w, lane);
-      float m_run = -INFINITY, l_f32 = 0.f, l_mul = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < count; ++j, ++step, ahead -= BN) {
         if (!wait_batch(j == 0 ? base : base + 2 * j + x - 1)) {
           ok = false;
@@ -844,8 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, need)) {
           if (j > 0) {
             const float f = need ? ex2(m_run - m_new) : 1.f;
-            l_f32 *= f;
-            l_mul *= f;
+            l_run *= f;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -858,13 +857,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (need) m_run = m_new;
         }
-        // p = 2^(s c - m).  Two row sums: the fp32 weights (lse) and, where they are rounded to bf16, the
-        // rounded ones the product multiplies by (the output is normalised by those, which keeps its
-        // error smaller; f16's 2^-11 stays below the output's rounding without, and its second sum cost a
-        // fifth of the softmax).
+        // p = 2^(s c - m), rounded to bf16 or f16 for the product and summed in fp32 as they were, for lse
+        // and output: a weight's rounding then counts once in the output, by at most 2^-8 of the weight
+        // times its value.  (A second sum of the rounded weights makes equal values come out unrounded,
+        // but no bound smaller, and cost 4 to 9 % of a prompt's time.)
         const float m_ref = m_run == -INFINITY ? 0.f : m_run;
         const uint64_t c2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_ref, -m_ref);
-        uint64_t accf[4] = {0ull, 0ull, 0ull, 0ull}, accb[4] = {0ull, 0ull, 0ull, 0ull};
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1) {
@@ -882,15 +881,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               f2_unpack(f2_fma(f2_pack(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), c2, nm2), x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               pk[i] = E4M3 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-              accf[i & 3] = f2_add(accf[i & 3], f2_pack(p0, p1));
-              if constexpr (!E4M3)
-                accb[i & 3] = f2_add(accb[i & 3], f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xFFFF0000u)));
+              acc[i & 3] = f2_add(acc[i & 3], f2_pack(p0, p1));
             }
             tmem_st16(tS + h * 32 + c * 16, pk);
           }
         }
-        l_f32 += sum8(accf);
-        l_mul += sum8(E4M3 ? accf : accb);
+        l_run += sum8(acc);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -907,8 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.single) {  // chain a joins the two
         if (x == 1) {
           s_ml[row] = m_run;
-          s_ml[BM + row] = l_mul;
-          s_ml[2 * BM + row] = l_f32;
+          s_ml[BM + row] = l_run;
           __syncwarp();
           if (lane == 0) mbar_arrive(joined + (warp & 3));
         } else {
@@ -919,8 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fa = m_run == -INFINITY ? 0.f : ex2(m_run - top);
           fb = m_b == -INFINITY ? 0.f : ex2(m_b - top);
           // (sums of scores that are NaN stay NaN)
-          l_mul = fmaf(l_mul, fa, s_ml[BM + row] * fb);
-          l_f32 = fmaf(l_f32, fa, s_ml[2 * BM + row] * fb);
+          l_run = fmaf(l_run, fa, s_ml[BM + row] * fb);
           m_run = top;
         }
       }
@@ -931,16 +925,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t out_row = static_cast<size_t>(w.s.cu + r.tok) * a.Hq + w.head / a.chunks * group + r.head;
         const bool finals = whole && a.whole == nullptr;
         // (the value scale by itself: its quotient by the sum may be too small for a normal float)
-        const float inv = !finals ? 1.f : l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
+        const float inv = !finals ? 1.f : l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
         float* part = nullptr;
         if (!whole) {
           part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (goes_on ? 1 : 0)) * part_floats(D);
           const int at = x * BM + row;
-          if (live) reinterpret_cast<float4*>(part)[at] = make_float4(m_run, l_mul, l_f32, 0.f);
-          part += 4 * kPartRows + static_cast<size_t>(at) * D;
+          if (live) reinterpret_cast<float2*>(part)[at] = make_float2(m_run, l_run);
+          part += 2 * kPartRows + static_cast<size_t>(at) * D;
         } else if (!finals) {
-          part = a.whole + 4 * static_cast<size_t>(a.T) * a.Hq + out_row * D;
-          if (live) reinterpret_cast<float4*>(a.whole)[out_row] = make_float4(m_run, l_mul, l_f32, 0.f);
+          part = a.whole + out_row * D;
+          if (live) reinterpret_cast<float2*>(a.whole + static_cast<size_t>(a.T) * a.Hq * D)[out_row] = make_float2(m_run, l_run);
         }
         const int seen = seen_by_all(a, w);
         const bool spoiled = *static_cast<volatile uint32_t*>(misc.any_bad + (w.index & 1)) == bad_mark(w.index);
@@ -987,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();  // TMEM loads are the whole warp's
         }
         if (finals && live && a.lse != nullptr)
-          a.lse[out_row] = l_f32 == 0.f ? -INFINITY : (m_run + log2f(l_f32)) * 0.6931471805599453f;
+          a.lse[out_row] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
       }
       tc_fence_before();
       __syncwarp();
@@ -1091,19 +1085,18 @@ __global__ void __launch_bounds__(8 * kJoinRows) paged_attn_join_kernel(const Pa
   const int c0 = end.w;
   auto part = [&](int c) { return a.parts + (2 * static_cast<size_t>(c) + (c < c1 ? 1 : 0)) * part_floats(D); };
   float top = -INFINITY;
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, reinterpret_cast<const float4*>(part(c))[r].x);
-  float l_mul = 0.f, l_f32 = 0.f;
+  for (int c = c0; c <= c1; ++c) top = fmaxf(top, reinterpret_cast<const float2*>(part(c))[r].x);
+  float sum = 0.f;
   float4 acc[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int c = c0; c <= c1; ++c) {
     const float* p = part(c);
-    const float4 ml = reinterpret_cast<const float4*>(p)[r];
+    const float2 ml = reinterpret_cast<const float2*>(p)[r];
     const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);  // (sums of scores that are NaN stay NaN)
-    l_mul = fmaf(ml.y, f, l_mul);
-    l_f32 = fmaf(ml.z, f, l_f32);
-    const float4* o = reinterpret_cast<const float4*>(p + 4 * kPartRows + static_cast<size_t>(r) * D);
+    sum = fmaf(ml.y, f, sum);
+    const float4* o = reinterpret_cast<const float4*>(p + 2 * kPartRows + static_cast<size_t>(r) * D);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const float4 v = o[t + 8 * i];
@@ -1114,7 +1107,7 @@ __global__ void __launch_bounds__(8 * kJoinRows) paged_attn_join_kernel(const Pa
     }
   }
   const size_t out_row = static_cast<size_t>(s.cu + static_cast<int>(tok)) * a.Hq + end.y / a.chunks * group + hh;
-  const float inv = l_mul > 0.f || l_mul != l_mul ? 1.f / l_mul : 0.f;
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     float4 y = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
@@ -1122,7 +1115,7 @@ __global__ void __launch_bounds__(8 * kJoinRows) paged_attn_join_kernel(const Pa
     *reinterpret_cast<uint2*>(a.out + out_row * D + 4 * (t + 8 * i)) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
   }
   if (t == 0 && a.lse != nullptr)
-    a.lse[out_row] = l_f32 == 0.f ? -INFINITY : (top + log2f(l_f32)) * 0.6931471805599453f;
+    a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, bool E4M3>

@@ -15,10 +15,9 @@ constexpr int kPagedAttnKeys = 128;
 constexpr int kPagedAttnSegCost = 2;  // what changing the segment costs, in steps
 
 // Parts of segments that cross shares: slot 2 c of share c for a segment that ends there, 2 c + 1
-// for one that goes on.  (log2 maximum, sum of the weights as multiplied, their fp32 sum, 0) of
-// the 256 rows, then the rows' D sums.
+// for one that goes on.  (log2 maximum, sum of weights) of the 256 rows, then the rows' D sums.
 constexpr int kPagedAttnPartRows = 2 * kPagedAttnRows;
-__host__ __device__ constexpr size_t paged_attn_part_floats(int D) { return static_cast<size_t>(kPagedAttnPartRows) * (4 + D); }
+__host__ __device__ constexpr size_t paged_attn_part_floats(int D) { return static_cast<size_t>(kPagedAttnPartRows) * (2 + D); }
 
 #ifdef __CUDACC__
 
