@@ -2,8 +2,8 @@
 beginning, against the fp64 oracle.
 
 Tolerances, taken before the first run (u = 2^-24): those of test_gpu_paged.py, with the weights
-rounded once to bf16 (2^-8 of a weight) or f16 (2^-11) and the output normalised by the sum of the
-rounded ones: numerator and denominator are each off by that times A = sum p |v|.  A weight's
+rounded once to bf16 (2^-8 of a weight) or f16 (2^-11) for the product: numerator and, where rounded
+weights are summed, denominator are each off by that times A = sum p |v|.  A weight's
 smallest part: weights below 2^-24 of 2^15 times the row's reference maximum round in f16 by at most
 2^-25, and the reference may lie 2^15 below the true maximum: 2^-25 per key of a sum of at least 1.
 """
@@ -203,6 +203,33 @@ def test_shared_decode_reports_and_reads_by_itself(what):
     got = c.run()
     assert mcs.mcs_device_status() == 6
     c.check(*got)
+
+
+@pytest.mark.parametrize("extra", [2, 70000], ids=["small table", "wide table"])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_little_in_common_is_read_by_itself(e4m3, extra):
+    """Beginnings too small to be worth it, in tables that cannot name larger ones and in tables that can:
+    the same bits, which are those of a decode, and the same reports."""
+    c = Family([(9, [0, 5, 40]), (0, [17, None]), (3, [7, 1])], 8, 2, 128, 16, e4m3, seed=5, extra=extra)
+    out, ls = c.run()
+    assert mcs.mcs_device_status() == 0
+    c.check(out, ls)
+    plain, plain_ls = torch.empty_like(out[:c.B]), torch.empty_like(ls[:c.B])
+    mcs.mcs_paged_decode(c.p, c.q, c.k, c.v, c.dtable, c.dlens, plain, c.ws, lse=plain_ls)
+    assert extra > 2 or (torch.equal(plain, out[:c.B]) and torch.equal(plain_ls, ls[:c.B]))
+    for starts, shared, change in (([0, 3, 2, 7], c.shared, {}), ([1, 3, 5, 7], c.shared, {}), ([0, 3, 5, 6], c.shared, {}),
+                                   (c.starts, [9, -1, 3], {}), (c.starts, [9, c.p.max_pages + 1, 3], {}),
+                                   (c.starts, c.shared, {1: 30}), (c.starts, c.shared, {5: -2}),
+                                   (c.starts, c.shared, {5: c.p.max_pages * 16 + 1})):
+        lens = list(c.lens)
+        for b, n in change.items():
+            lens[b] = n
+        d = Family([(9, [0, 5, 40]), (0, [17, None]), (3, [7, 1])], 8, 2, 128, 16, e4m3, seed=5, extra=extra)
+        d.dstarts, d.dshared, d.dlens = _i32(starts), _i32(shared), _i32(lens)
+        d.lens = [x if 0 <= x <= d.p.max_pages * 16 else 0 for x in lens]
+        got = d.run()
+        assert mcs.mcs_device_status() == 6
+        d.check(*got)
 
 
 # ------------------------------------------------------------------ what masks hide, and what they do not

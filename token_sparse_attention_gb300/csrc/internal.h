@@ -278,13 +278,19 @@ cudaError_t paged_attn_grid(int* grid);
 
 // Groups of sequences with a common beginning: what the attention over the beginnings and over the
 // tails take (see mcs_paged_decode_shared).
+// Bytes that reading common beginnings once has to save: the attention over them, which starts anew on every
+// SM, and the join take about 15 us more than one decode, which reads so much again from L2 in that time (4
+// sequences behind 8192 tokens of 8 heads, bf16, 101 MB: 31 us shared, 23 by themselves; 8 of them, 235 MB: 36
+// and 33; 32 behind 4096, 520 MB: 39 and 54).
+constexpr unsigned long long kSharedWorth = 128ull << 20;
+
 struct SharedPlanArgs {
   int B, G, page, max_pages;
   const int32_t* lens;       // [B]
   const int32_t* starts;     // [G + 1]
   const int32_t* shared;     // [G] pages
   unsigned long long row_bytes;  // of a token, keys and values of all heads
-  int32_t* tail;             // [B] tokens behind the beginning
+  int32_t* tail;             // [B] tokens behind the beginning; null: check only
   int32_t* skip;             // [B] pages of the beginning
   int32_t* group_of;         // [B]
   int32_t* cu;               // [G + 1]

@@ -999,10 +999,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Which sequences a common beginning serves.  One CTA: it is a few reads and writes per sequence.
 // Bounds that do not ascend from 0 to B leave every sequence by itself; a group of which fewer than
 // two sequences reach the beginning's end, too; and so does a batch in which reading the beginnings
-// once saves less than kWorth bytes: the attention over them and the join take about 15 us more than
-// reading so much again from L2.
+// once saves less than kSharedWorth bytes.  Without `tail` it only checks.
 constexpr int kPlanThreads = 1024;
-constexpr unsigned long long kWorth = 128ull << 20;
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlanArgs a) {
   __shared__ unsigned long long s_saved;
   const int tid = threadIdx.x, lane = lane_id();
@@ -1011,17 +1009,19 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   const long long room = static_cast<long long>(a.max_pages) * a.page;
   bool bad = tid == 0 && (a.starts[0] != 0 || a.starts[a.G] != a.B);
   for (int g = tid; g < a.G; g += kPlanThreads) bad = bad || a.starts[g] > a.starts[g + 1];
+  const bool writes = a.tail != nullptr;
   for (int b = tid; b < a.B; b += kPlanThreads) {
     const int len = a.lens[b];
     const bool good = len >= 0 && len <= room;
     if (!good) atomicOr(a.status, DEV_BOUNDS);
+    if (!writes) continue;
     a.tail[b] = good ? len : 0;
     a.skip[b] = 0;
     a.group_of[b] = -1;
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(a.status, DEV_BOUNDS);
-  for (int g = tid; g <= a.G; g += kPlanThreads) a.cu[g] = bad ? 0 : a.starts[g];
+  for (int g = tid; writes && g <= a.G; g += kPlanThreads) a.cu[g] = bad ? 0 : a.starts[g];
   for (int g = warp_id(); g < a.G; g += kPlanThreads / 32) {
     const int lo = bad ? 0 : a.starts[g], hi = bad ? 0 : a.starts[g + 1], pages = a.shared[g];
     const bool good = pages >= 0 && pages <= a.max_pages;
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     bool wrong = !good;
     int live = 0, leader = 0x7fffffff;
     for (int b = lo + lane; b < hi; b += 32) {
-      const int len = a.tail[b];
+      const int len = a.lens[b] <= room ? a.lens[b] : 0;
       wrong = wrong || (len > 0 && len < keys);
       if (len > 0 && len >= keys) {
         ++live;
@@ -1039,15 +1039,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     live = __reduce_add_sync(0xffffffffu, live);
     leader = __reduce_min_sync(0xffffffffu, leader);
     if (wrong) atomicOr(a.status, DEV_BOUNDS);
-    if (lane == 0) {
+    if (writes && lane == 0) {
       const bool use = live > 1 && keys > 0;
       a.keys[g] = use ? keys : 0;
       a.leader[g] = use ? leader : 0;
       if (use) atomicAdd(&s_saved, (live - 1ull) * keys * a.row_bytes);
     }
   }
+  if (!writes) return;
   __syncthreads();
-  const bool worth = s_saved >= kWorth;
+  const bool worth = s_saved >= kSharedWorth;
   for (int g = warp_id(); g < a.G; g += kPlanThreads / 32) {
     const int keys = a.keys[g];
     __syncwarp();
