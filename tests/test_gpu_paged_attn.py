@@ -406,6 +406,55 @@ def test_another_stream_and_graphs_of_new_lengths(e4m3):
     assert mcs.mcs_device_status() == 0
 
 
+def test_groups_without_sequences():
+    groups = [(0, []), (40, [5, 0, 40, None, 9, 100] * 3), (3, []), (20, [7] * 20), (1, [])]
+    for c in (Family(groups, 16, 8, 128, 128, seed=4), Family([(0, []), (9, [0, 5]), (4, [3])], 8, 2, 64, 16, seed=4)):
+        got = c.run()
+        assert mcs.mcs_device_status() == 0
+        c.check(*got)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_calls_at_once_on_two_streams(e4m3):
+    c = Step([300, 9000, 700, 40], [10, 90, 300, 3], 8, 2, 128, 16, e4m3, seed=6)
+    f = big_family(e4m3)
+    want, wantf = c.attn(), f.run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(6):
+        got += [(c.attn(stream=streams[0]), want), (f.run(stream=streams[1]), wantf)]
+    for s in streams:
+        s.synchronize()
+    assert mcs.mcs_device_status() == 0
+    assert all(torch.equal(x, y) for pair in got for x, y in zip(*pair))
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_pages_whose_offsets_pass_32_bits(e4m3):
+    """The same pages at the end of caches of 4.3 GB: the same bits, and copies between both ends."""
+    for c in (Step([300, 90, 700, 40], [10, 90, 90, 3], 16, 8, 128, 128, e4m3, seed=6), big_family(e4m3)):
+        run = c.attn if isinstance(c, Step) else c.run
+        want, n = run(), c.k.shape[0]
+        N = 2 ** 32 // c.k[0].nbytes + n
+        far = [torch.empty((N,) + x.shape[1:], dtype=x.dtype, device="cuda") for x in (c.k, c.v)]
+        for x, y in zip(far, (c.k, c.v)):
+            x[N - n:] = y
+        held = (c.table >= 0) & (c.table < n)
+        c.dtable = _i32(np.where(held, c.table + (N - n), c.table))
+        c.k, c.v, c.p.num_pages = *far, N
+        got = run()
+        assert mcs.mcs_device_status() == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        moves = _i32([[N - 1 - i, i, c.page] for i in range(n)])
+        mcs.mcs_paged_copy(c.p, moves, c.k, c.v)
+        assert mcs.mcs_device_status() == 0
+        for x in far:
+            assert torch.equal(x[:n].flip(0).view(torch.uint8), x[N - n:].view(torch.uint8))
+        del far, c
+
+
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 def test_withheld_loads_time_out_and_the_context_survives(e4m3, monkeypatch):
     c = Step([700, 300], [90, 300], 4, 2, 128, 16, e4m3, seed=6)
