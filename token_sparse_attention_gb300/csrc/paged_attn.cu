@@ -166,6 +166,25 @@ __device__ __forceinline__ int steps_of(const Walk& w, int x) {
   return max(0, min(w.count, (x == 0 ? w.steps_a : w.steps) - w.t0));
 }
 
+// Lane q of four holds r[i]: piece i of its row.  Then it holds piece q of the rows of lanes i, and stores of
+// r[i] fill 64 bytes of a row instead of 16 of four (which took a third of an epilogue).
+__device__ __forceinline__ void turn(uint4 (&r)[4], int lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    const bool odd = (lane & d) != 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = d == 1 ? 2 * k : k;
+      uint4 x = odd ? r[i] : r[i + d];
+      x.x = __shfl_xor_sync(0xffffffffu, x.x, d);
+      x.y = __shfl_xor_sync(0xffffffffu, x.y, d);
+      x.z = __shfl_xor_sync(0xffffffffu, x.z, d);
+      x.w = __shfl_xor_sync(0xffffffffu, x.w, d);
+      (odd ? r[i] : r[i + d]) = x;
+    }
+  }
+}
+
 // Keys that every row of the segment sees: tiles behind it are looked through.
 __device__ __forceinline__ int seen_by_all(const PagedAttnArgs& a, const Walk& w) {
   return a.causal ? w.s.keys - w.s.n + 2 * w.i * a.tokens + 1 : w.s.keys;
@@ -934,20 +953,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!idle && !(w.single && x == 1)) {
         const uint32_t tOb = tmem + 256 + D + lane_off;
         const bool goes_on = w.t0 + w.count < w.steps, whole = w.t0 == 0 && !goes_on;
-        const size_t out_row = static_cast<size_t>(w.s.cu + r.tok) * a.Hq + w.head / a.chunks * group + r.head;
+        const int out_row = live ? (w.s.cu + r.tok) * a.Hq + w.head / a.chunks * group + r.head : 0;
         const bool finals = whole && a.whole == nullptr;
         // (the value scale by itself: its quotient by the sum may be too small for a normal float)
         const float inv = !finals ? 1.f : l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
-        float* part = nullptr;
-        if (!whole) {
-          part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (goes_on ? 1 : 0)) * part_floats(D);
-          const int at = x * BM + row;
-          if (live) reinterpret_cast<float2*>(part)[at] = make_float2(m_run, l_run);
-          part += 2 * kPartRows + static_cast<size_t>(at) * D;
-        } else if (!finals) {
-          part = a.whole + out_row * D;
-          if (live) reinterpret_cast<float2*>(a.whole + static_cast<size_t>(a.T) * a.Hq * D)[out_row] = make_float2(m_run, l_run);
-        }
+        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (goes_on ? 1 : 0)) * part_floats(D);
+        float* const sums = whole ? a.whole + static_cast<size_t>(a.T) * a.Hq * D : part;
+        const int at = whole ? out_row : x * BM + row;
+        if (live && !finals) reinterpret_cast<float2*>(sums)[at] = make_float2(m_run, l_run);
+        part = whole ? a.whole : part + 2 * kPartRows;
+        int ats[4];  // of this lane's four, -1: none
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ats[i] = __shfl_sync(0xffffffffu, live ? at : -1, (lane & 28) + i);
         const int seen = seen_by_all(a, w);
         const bool spoiled = *static_cast<volatile uint32_t*>(misc.any_bad + (w.index & 1)) == bad_mark(w.index);
         const uint32_t* record = records + (w.index & 1) * D;
@@ -970,24 +987,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), fb, v[i]);
           }
-          if (live) {
-            if (spoiled) {
+          if (spoiled) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (first_bad(record, w, seen, c * 32 + i) < r.limit) v[i] = NAN;
-            }
-            if (finals) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + c * 32);
+            for (int i = 0; i < 32; ++i)
+              if (first_bad(record, w, seen, c * 32 + i) < r.limit) v[i] = NAN;
+          }
+          const size_t col = c * 32 + (lane & 3) * (finals ? 8 : 4);
+          uint4 p[4];
+          if (finals) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = E4M3 ? v[i] * inv * a.v_scale : v[i] * inv;
+            for (int i = 0; i < 32; ++i) v[i] = E4M3 ? v[i] * inv * a.v_scale : v[i] * inv;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                                    pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(part + c * 32);
+            for (int e = 0; e < 4; ++e)
+              p[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                                pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+            turn(p, lane);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int i = 0; i < 4; ++i)
+              if (ats[i] >= 0) *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(ats[i]) * D + col) = p[i];
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float* f = v + 16 * h + 4 * e;
+                p[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+              }
+              turn(p, lane);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (ats[i] >= 0) *reinterpret_cast<uint4*>(part + static_cast<size_t>(ats[i]) * D + col + 16 * h) = p[i];
             }
           }
           __syncwarp();  // TMEM loads are the whole warp's
