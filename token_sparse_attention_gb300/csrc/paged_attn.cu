@@ -106,7 +106,8 @@ struct Layout {
 // A walk over a CTA's share, segment by segment; every role makes it by itself.
 struct Walk {
   Seq s;
-  int g, head, i;  // sequence, KV head and its chunk of query heads, pair (the last odd unit behind them)
+  int units;
+  int g, kv, chunk, i;  // sequence, KV head and its chunk of query heads, pair (the last odd unit behind them)
   bool single;     // an odd unit, whose tiles the chains halve
   int steps, steps_a;  // tiles of the segment; of a pair's first unit
   int t0, count;   // the share's tiles of it: [t0, t0 + count)
@@ -114,7 +115,7 @@ struct Walk {
   int index;       // segments of the share in front of this one
 };
 __device__ __forceinline__ void set_segment(const PagedAttnArgs& a, Walk& w) {
-  w.single = w.i >= units_of(a, w.s) / 2;
+  w.single = w.i >= w.units / 2;
   if (w.single) {
     w.steps = w.steps_a = tiles_until(a, w.s, w.s.n);
   } else {
@@ -126,14 +127,17 @@ __device__ __forceinline__ void set_segment(const PagedAttnArgs& a, Walk& w) {
 __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Walk& w) {
   w.left -= w.steps + kSegCost - w.t0;
   if (w.left <= 0) return false;
-  const int units = units_of(a, w.s);
-  if (++w.i >= units / 2 + (units & 1)) {
+  if (++w.i >= w.units / 2 + (w.units & 1)) {
     w.i = 0;
-    if (++w.head >= a.Hkv * a.chunks) {
-      w.head = 0;
-      do {  // (there is one, unless the lengths change under the kernel)
-        if (++w.g >= a.G) return false;
-      } while (!load_seq(a, w.g, w.s, false));
+    if (++w.chunk == a.chunks) {
+      w.chunk = 0;
+      if (++w.kv == a.Hkv) {
+        w.kv = 0;
+        do {  // (there is one, unless the lengths change under the kernel)
+          if (++w.g >= a.G) return false;
+        } while (!load_seq(a, w.g, w.s, false));
+        w.units = units_of(a, w.s);
+      }
     }
   }
   set_segment(a, w);
@@ -145,20 +149,20 @@ __device__ __forceinline__ bool next_segment(const PagedAttnArgs& a, Walk& w) {
 
 // A walk in one register of a warp's lanes, while the softmax needs the registers.
 __device__ __forceinline__ int fold(const Walk& w, int lane) {
-  const int f[13] = {w.s.cu, w.s.n, w.s.keys, w.g, w.head, w.i, w.single, w.steps, w.steps_a, w.t0, w.index,
+  const int f[15] = {w.s.cu, w.s.n, w.s.keys, w.units, w.g, w.kv, w.chunk, w.i, w.single, w.steps, w.steps_a, w.t0, w.index,
                      static_cast<int>(w.left), static_cast<int>(w.left >> 32)};
   int x = w.count;
 #pragma unroll
-  for (int k = 0; k < 13; ++k)
+  for (int k = 0; k < 15; ++k)
     if (lane == k) x = f[k];
   return x;
 }
 __device__ __forceinline__ Walk unfold(int x) {
-  int f[14];
+  int f[16];
 #pragma unroll
-  for (int k = 0; k < 14; ++k) f[k] = __shfl_sync(0xffffffffu, x, k);
-  return {{f[0], f[1], f[2]}, f[3], f[4], f[5], f[6] != 0, f[7], f[8], f[9], f[13],
-          static_cast<long long>(static_cast<uint32_t>(f[11])) | (static_cast<long long>(f[12]) << 32), f[10]};
+  for (int k = 0; k < 16; ++k) f[k] = __shfl_sync(0xffffffffu, x, k);
+  return {{f[0], f[1], f[2]}, f[3], f[4], f[5], f[6], f[7], f[8] != 0, f[9], f[10], f[11], f[15],
+          static_cast<long long>(static_cast<uint32_t>(f[13])) | (static_cast<long long>(f[14]) << 32), f[12]};
 }
 
 // How many of the share's tiles chain x works on: the first ones (a pair's first unit ends earlier).
@@ -435,11 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int part_from = -1;  // the share in which the first segment begins, if that is not this one
   if (more) {
     w.g = misc.start.g;
-    w.head = misc.start.head;
+    w.kv = misc.start.head / a.chunks;
+    w.chunk = misc.start.head - w.kv * a.chunks;
     w.i = misc.start.i;
     load_seq(a, w.g, w.s, false);
-    const int units = units_of(a, w.s);
-    w.i = min(w.i, units / 2 + (units & 1) - 1);
+    w.units = units_of(a, w.s);
+    w.i = min(w.i, w.units / 2 + (w.units & 1) - 1);
     set_segment(a, w);
     w.t0 = static_cast<int>(misc.start.offset);
     w.left = hi - lo;
@@ -448,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       part_from = share_of(lo - w.t0, all, shares);
     }
     if (tid == 0) {
-      a.ends[blockIdx.x] = make_int4(part_from >= 0 ? w.g : -1, w.head, w.i, part_from);
+      a.ends[blockIdx.x] = make_int4(part_from >= 0 ? w.g : -1, w.kv * a.chunks + w.chunk, w.i, part_from);
     }
     if (w.count <= 0) more = next_segment(a, w);
     w.index = 0;
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int at = a.row_of != nullptr ? a.row_of[w.g] : w.g;
           const int pid = a.table[static_cast<size_t>(at) * a.max_pages + static_cast<int>(slab >> shift)];
           out = pid < 0 || pid >= a.num_pages;
-          if (!out) row = (pid * a.Hkv + w.head / a.chunks) * a.page + (static_cast<int>(slab) & (slabs_per_page - 1)) * kSlab;
+          if (!out) row = (pid * a.Hkv + w.kv) * a.page + (static_cast<int>(slab) & (slabs_per_page - 1)) * kSlab;
         }
         outside = __ballot_sync(0xffffffffu, out);  // slabs inside the sequence whose page is none
       };
@@ -538,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a box is tokens x heads rows; tokens behind the sequence's are other ones' or zeros
           const int units = w.single ? 1 : 2;
           mbar_expect_tx(q_full, units * L::kSub * 128 * a.heads * a.tokens);
-          const int head = w.head / a.chunks * group + w.head % a.chunks * a.heads;
+          const int head = w.kv * group + w.chunk * a.heads;
           for (int u = 0; u < units; ++u)
             for (int s = 0; s < L::kSub; ++s)
               tma_load_3d(qs + u * L::kTileBytes + s * L::kSubBytes, &tq, s * 64, head, w.s.cu + (2 * w.i + u) * a.tokens, q_full);
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           // queries: bf16 to f16 through registers, kAtOnce chunks side by side
           constexpr int kChunks = BM * kSegsRow, kAtOnce = 6;
-          const int chunk0 = w.head % a.chunks * a.heads, head = w.head / a.chunks * group + chunk0;
+          const int chunk0 = w.chunk * a.heads, head = w.kv * group + chunk0;
 #pragma unroll 1
           for (int c0 = me; c0 < (w.single ? 1 : 2) * kChunks; c0 += kAtOnce * kHelp) {
             uint4 qw[kAtOnce];
@@ -820,11 +825,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tok, head, limit;
       bool live;
     };
+    const int row_t = row / a.heads;
     auto row_of = [&](const Walk& w) {
-      const int t = row / a.heads;
+      const int t = row_t;
       Row r;
       r.tok = static_cast<int>(min((2LL * w.i + (w.single ? 0 : x)) * a.tokens + t, 0x7fffffffLL));
-      r.head = w.head % a.chunks * a.heads + row - t * a.heads;
+      r.head = w.chunk * a.heads + row - t * a.heads;
       r.live = t < a.tokens && r.tok < w.s.n && r.head < group;
       r.limit = r.live && a.causal ? w.s.keys - w.s.n + r.tok + 1 : w.s.keys;
       return r;
@@ -953,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!idle && !(w.single && x == 1)) {
         const uint32_t tOb = tmem + 256 + D + lane_off;
         const bool goes_on = w.t0 + w.count < w.steps, whole = w.t0 == 0 && !goes_on;
-        const int out_row = live ? (w.s.cu + r.tok) * a.Hq + w.head / a.chunks * group + r.head : 0;
+        const int out_row = live ? (w.s.cu + r.tok) * a.Hq + w.kv * group + r.head : 0;
         const bool finals = whole && a.whole == nullptr;
         // (the value scale by itself: its quotient by the sum may be too small for a normal float)
         const float inv = !finals ? 1.f : l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
