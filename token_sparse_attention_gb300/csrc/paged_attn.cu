@@ -962,7 +962,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int out_row = live ? (w.s.cu + r.tok) * a.Hq + w.kv * group + r.head : 0;
         const bool finals = whole && a.whole == nullptr;
         // (the value scale by itself: its quotient by the sum may be too small for a normal float)
-        const float inv = !finals ? 1.f : l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+        if (finals) {
+          const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+          fa *= inv;
+          fb *= inv;
+        }
         float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (goes_on ? 1 : 0)) * part_floats(D);
         float* const sums = whole ? a.whole + static_cast<size_t>(a.T) * a.Hq * D : part;
         const int at = whole ? out_row : x * BM + row;
@@ -993,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), fb, v[i]);
           }
-          if (spoiled) {
+          if (__builtin_expect(spoiled, 0)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (first_bad(record, w, seen, c * 32 + i) < r.limit) v[i] = NAN;
@@ -1002,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 p[4];
           if (finals) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = E4M3 ? v[i] * inv * a.v_scale : v[i] * inv;
+            for (int i = 0; i < 32; ++i) v[i] = E4M3 ? v[i] * a.v_scale : v[i];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               p[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
