@@ -98,9 +98,9 @@ mcs_status run_decode(const mcs_paged* p, const void* q, const void* k_cache, co
   return finish(mcs::launch_paged_decode(a, e4m3, nullptr, stream), what);
 }
 
-// What the attention of many rows takes from the params; and its tensor maps.
+// What the attention of many rows takes from the params.
 mcs_status many_rows(const mcs_paged* p, int T, const void* q, const void* k_cache, const void* v_cache,
-                     mcs::PagedAttnArgs* a, CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
+                     mcs::PagedAttnArgs* a) {
   const int group = p->Hq / p->Hkv;
   a->Hq = p->Hq;
   a->Hkv = p->Hkv;
@@ -120,12 +120,15 @@ mcs_status many_rows(const mcs_paged* p, int T, const void* q, const void* k_cac
   a->k = k_cache;
   a->v = v_cache;
   a->fault = mcs::test_fault();
-  const bool e4m3 = p->kv == MCS_KV_E4M3;
-  if ((!e4m3 && !mcs::make_query_map(tq, q, T, p->Hq, p->D, a->q_stride, a->heads, a->tokens)) ||
-      !mcs::make_rows_map(tk, k_cache, a->rows, p->D, p->page, e4m3) ||
-      !mcs::make_rows_map(tv, v_cache, a->rows, p->D, p->page, e4m3))
-    return mcs::record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled(paged)");
   return status_word(&a->status);
+}
+
+mcs_status launch_many_rows(const mcs::PagedAttnArgs& a, bool e4m3, cudaStream_t stream) {
+  CUtensorMap tq{}, tk{}, tv{};
+  if ((!e4m3 && !mcs::make_query_map(&tq, a.q, a.T, a.Hq, a.D, a.q_stride, a.heads, a.tokens)) ||
+      !mcs::make_rows_map(&tk, a.k, a.rows, a.D, a.page, e4m3) || !mcs::make_rows_map(&tv, a.v, a.rows, a.D, a.page, e4m3))
+    return mcs::record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled(paged)");
+  return finish(mcs::launch_paged_attn(a, &tq, &tk, &tv, e4m3, stream), "paged attention launch");
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -358,8 +361,7 @@ mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* 
     return MCS_ERR_INVALID_ARG;
   if (!good(ws) || ws_bytes < mcs_paged_attn_workspace(p)) return MCS_ERR_WORKSPACE;
   mcs::PagedAttnArgs a{};
-  CUtensorMap tq{}, tk{}, tv{};
-  if ((s = many_rows(p, T, q, k_cache, v_cache, &a, &tq, &tk, &tv)) != MCS_OK) return s;
+  if ((s = many_rows(p, T, q, k_cache, v_cache, &a)) != MCS_OK) return s;
   a.G = p->B;
   a.causal = 1;
   a.table = block_table;
@@ -369,8 +371,7 @@ mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* 
   a.lse = lse;
   a.ends = static_cast<int4*>(ws);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(mcs::paged_attn_ends_bytes()));
-  return finish(mcs::launch_paged_attn(a, &tq, &tk, &tv, p->kv == MCS_KV_E4M3, stream),
-                "paged attention launch");
+  return launch_many_rows(a, p->kv == MCS_KV_E4M3, stream);
 }
 
 size_t mcs_paged_decode_shared_workspace(const mcs_paged* p) {
@@ -411,8 +412,7 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
   plan.leader = ints + 4 * p->B;
   plan.cu = ints + 5 * p->B;
   mcs::PagedAttnArgs a{};
-  CUtensorMap tq{}, tk{}, tv{};
-  if ((s = many_rows(p, p->B, q, k_cache, v_cache, &a, &tq, &tk, &tv)) != MCS_OK) return s;
+  if ((s = many_rows(p, p->B, q, k_cache, v_cache, &a)) != MCS_OK) return s;
   a.G = groups;
   a.table = block_table;
   a.row_of = plan.leader;
@@ -469,9 +469,9 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
   }
   cudaError_t e = mcs::paged_attn_grid(&join.grid);
   if (e == cudaSuccess) e = mcs::launch_shared_plan(plan, stream);
-  if (e == cudaSuccess) e = mcs::launch_paged_attn(a, &tq, &tk, &tv, e4m3, stream);
-  if (e == cudaSuccess) e = mcs::launch_paged_decode(d, e4m3, &join, stream);
-  return finish(e, "paged shared decode launch");
+  if (e != cudaSuccess) return finish(e, "paged shared decode launch");
+  if ((s = launch_many_rows(a, e4m3, stream)) != MCS_OK) return s;
+  return finish(mcs::launch_paged_decode(d, e4m3, &join, stream), "paged shared decode launch");
 }
 
 size_t mcs_paged_fork_workspace(const mcs_paged* p) {
