@@ -35,11 +35,13 @@
 // gets NaN in the column.  One or two tiles per segment are concerned.
 //
 // Measured, and what bounds it:
-//   a prompt of 16384 tokens, 32 / 8 heads, D = 128: bf16 1443 us, 1524 TFLOP/s, 78 % of a
+//   a prompt of 16384 tokens, 32 / 8 heads, D = 128: bf16 1363 us, 1613 TFLOP/s, 82 % of a
 //     matrix product's rate; with the softmax left out it would be 94 %, so the chains' softmax bounds
 //     it (two warps per scheduler: maxima, exponentials, sums, rounding, and TMEM on both sides).
-//     E4M3 1757 us: the conversions take issue slots from it
-//   1024 tokens behind 73552, 40 / 8 heads: bf16 1125 us, E4M3 1120, 71 %, the same
+//     E4M3 1661 us: the conversions take issue slots from it
+//   8192 tokens, 40 heads: bf16 515 us, E4M3 565, 67 and 62 %: shorter segments, of which each change takes
+//     about 4 us: last softmax, product, epilogue, first scores and softmax one after another
+//   1024 tokens behind 73552, 40 / 8 heads: bf16 1065 us, E4M3 1076, 74 and 73 %, as the first
 //   32 x 5 tokens behind 8000, 32 / 8 heads, bf16 (1.05 GB): 177 us, 5.9 TB/s, 87 % of a copy
 //   the same in E4M3 (0.52 GB): 165 us, 3.2 TB/s.  A step of an odd unit is a chain of waits (tile there,
 //     stage free, converted, scores, weights) of 1.4 us; without the conversions' work it takes 1.1.  Two more
