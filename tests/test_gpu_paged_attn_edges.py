@@ -1,0 +1,50 @@
+"""GPU parity of paged attention and shared decode where their kernels' bookkeeping is at its edges:
+many short segments of which only some are looked through, keys that outweigh all others, batches on
+either side of what is worth sharing, lengths and moves that cannot be."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import test_gpu_paged as tp
+from tests import test_gpu_paged_attn as ta
+from token_sparse_attention_gb300 import build as mcs_build
+from token_sparse_attention_gb300 import mcs
+
+pytestmark = pytest.mark.gpu
+
+_i32, _f64 = tp._i32, tp._f64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    mcs_build.build()
+    mcs.lib()
+    yield
+    assert mcs.mcs_device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D,gap", [(64, 1), (64, 3), (128, 1), (128, 2)])
+def test_infinite_values_of_many_short_segments(D, gap, e4m3):
+    """One token each of thousands of sequences, a dozen and more to a block: those that end with a tile of
+    128 keys have nothing to look through, those between them do, and hold infinite values there."""
+    r = np.random.default_rng(D + gap)
+    B = 2500
+    lens = [int(r.integers(1, 4)) * 128 - (0 if b % (gap + 1) else int(r.integers(1, 100))) for b in range(B)]
+    c = ta.Step(lens, [1] * B, 2, 1, D, 128, e4m3, seed=D)
+    want, want_ls = c.attn()
+    hit = torch.zeros(c.q.shape, dtype=torch.bool, device="cuda")
+    at = [b for b in range(0, B, gap + 1) if r.random() < 0.6]
+    cols = r.integers(0, D, (len(at), 3))
+    for i in range(3):
+        pos = np.array([int(r.integers(lens[b] // 128 * 128, lens[b])) for b in at])
+        pid = torch.from_numpy(c.table[at, pos // 128]).cuda()
+        col = torch.from_numpy(cols[:, i]).cuda()
+        c.v[pid, 0, torch.from_numpy(pos % 128).cuda(), col] = 0x7F if e4m3 else [np.inf, -np.inf, np.nan][i]
+        hit[torch.tensor(at, device="cuda"), :, col] = True
+    for _ in range(5):
+        out, ls = c.attn()
+        assert not torch.isfinite(out.float()[hit]).any()
+        assert torch.equal(out[~hit], want[~hit]) and torch.equal(ls, want_ls)
+    assert mcs.mcs_device_status() == 0

@@ -593,8 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; ok && more; more = next_segment(a, w)) {
         const int count = w.count, t0 = w.t0, keys = w.s.keys, first_look = seen_by_all(a, w) / BN, mark = w.index & 1;
-        // a record's last segment, two back, has been read when this one's is begun
-        if (first_look < t0 + count && w.index >= 2) ok = warp_wait(written + mark, ((w.index - 2) / 2) & 1, abort_flag, a.status);
+        // A record's last segment, two back, has been read when this one's is begun.  Waited for whether or not
+        // there are tiles to look through: a wait left out would put the next one two phases behind, where the
+        // barrier's parity says the opposite.
+        if (w.index >= 2) ok = warp_wait(written + mark, ((w.index - 2) / 2) & 1, abort_flag, a.status);
         if (!ok) break;
         if constexpr (!E4M3) {
           for (int j = max(0, first_look - t0); ok && j < count; ++j) {
