@@ -48,3 +48,24 @@ def test_infinite_values_of_many_short_segments(D, gap, e4m3):
         assert not torch.isfinite(out.float()[hit]).any()
         assert torch.equal(out[~hit], want[~hit]) and torch.equal(ls, want_ls)
     assert mcs.mcs_device_status() == 0
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
+def test_nan_values_in_every_tile_that_masks_cut(D, page):
+    """E4M3 prompts of many tiles whose values hold NaN codes here and there, and nothing but NaN behind the
+    sequences: slots in which tiles are looked through are loaded again and again."""
+    lens, new = [1500, 1130, 70, 2049], [1500, 1000, 70, 300]
+    r = np.random.default_rng(D)
+    c = ta.Step(lens, new, 8, 4, D, page, True, seed=D)
+    want, want_ls = c.attn()
+    hit = torch.zeros(c.q.shape, dtype=torch.bool, device="cuda")
+    for b, (n, m) in enumerate(zip(lens, new)):
+        for t in range(int(r.integers(0, 60)), n, 61):
+            h, col = int(r.integers(0, 4)), int(r.integers(0, D))
+            c.v[int(c.table[b, t // page]), h, t % page, col] = 0x7F if t % 2 else 0xFF
+            hit[int(c.cu[b]) + max(0, t - (n - m)):int(c.cu[b + 1]), 2 * h:2 * h + 2, col] = True
+    for _ in range(3):
+        out, ls = c.attn()
+        assert torch.isnan(out.float()[hit]).all()
+        assert torch.equal(out[~hit], want[~hit]) and torch.equal(ls, want_ls)
+    assert mcs.mcs_device_status() == 0

@@ -662,24 +662,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             uint8_t* from = smem + L::kRaw + slot * L::kRawBytes;
             uint8_t* stage = ring + st * L::kTileBytes;
-            if (!is_k && tile >= first_look) {
-#pragma unroll 1
-              for (int k = 0; k < kTurns; ++k) {
-                const int r = (hw + (kLoaders - 1) * k) * kRows + sub;
-                if (r >= BN) continue;
-                uint4 q = ld_shared16(from + r * D + seg * 16);
-                if (r >= keys - tile * BN)
-                  q = make_uint4(0u, 0u, 0u, 0u);
-                else if (has_bad<true>(q))  // NaN codes (there are no infinities)
-                  q = note_bad<true>(q, records + mark * D + seg * 16, misc.any_bad + mark, bad_mark(w.index),
-                                     (tile - first_look) * BN + r);
-                st_shared16(from + r * D + seg * 16, q);
-              }
-            }
             uint4 v[kTurns];
 #pragma unroll
             for (int k = 0; k < kTurns; ++k)
               if (hw + (kLoaders - 1) * k < kGroups) v[k] = ld_shared16(from + ((hw + (kLoaders - 1) * k) * kRows + sub) * D + seg * 16);
+            // (looked through in registers: nothing is written to memory that the next copy overwrites)
+            if (!is_k && tile >= first_look) {
+#pragma unroll
+              for (int k = 0; k < kTurns; ++k) {
+                if (hw + (kLoaders - 1) * k >= kGroups) continue;
+                const int r = (hw + (kLoaders - 1) * k) * kRows + sub;
+                if (r >= keys - tile * BN)
+                  v[k] = make_uint4(0u, 0u, 0u, 0u);
+                else if (has_bad<true>(v[k]))  // NaN codes (there are no infinities)
+                  v[k] = note_bad<true>(v[k], records + mark * D + seg * 16, misc.any_bad + mark, bad_mark(w.index),
+                                        (tile - first_look) * BN + r);
+              }
+            }
             if (it >= NS) ok = wait_batch(__shfl_sync(0xffffffffu, reader, st));
             if (!ok) break;
             if (lane == st) reader = base + 2 * j + (is_k ? 0 : 2);
