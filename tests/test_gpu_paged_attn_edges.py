@@ -69,3 +69,73 @@ def test_nan_values_in_every_tile_that_masks_cut(D, page):
         assert torch.isnan(out.float()[hit]).all()
         assert torch.equal(out[~hit], want[~hit]) and torch.equal(ls, want_ls)
     assert mcs.mcs_device_status() == 0
+
+
+# ------------------------------------------------------------------ beginnings read once, whatever they save
+
+LARGER = [  # groups, Hq, Hkv, D, page: odd numbers of rows, more than 16 and more than 128 heads per KV head
+    ([(17, [1, None, 300, 0, 45])], 9, 1, 128, 16), ([(33, [5, 0, 7]), (70, [90] * 4)], 34, 2, 64, 16),
+    ([(9, [130, 3, 40]), (0, [7]), (2, [1, 1])], 129, 1, 128, 32), ([(12, [0, 17, None, 9, 64])], 261, 1, 64, 64),
+    ([(4, [55] * 33), (3, [1, 2])], 15, 3, 128, 128)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("groups,Hq,Hkv,D,page", ta.FAMILIES + LARGER)
+def test_small_beginnings_read_once(groups, Hq, Hkv, D, page, e4m3, monkeypatch):
+    monkeypatch.setenv("MCS_TEST_SHARED_WORTH", "0")
+    c = ta.Family(groups, Hq, Hkv, D, page, e4m3, seed=Hq + page)
+    first = c.run()
+    assert mcs.mcs_device_status() == 0
+    c.check(*first)
+    again = c.run()
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert torch.equal(c.run(lse=False)[0], first[0])
+    # the same read by themselves: another order of the sums, other roundings of the weights
+    monkeypatch.setenv("MCS_TEST_SHARED_WORTH", str(1 << 60))
+    c.check(*c.run())
+
+
+def test_the_larger_families_are_read_by_themselves_too():
+    for groups, Hq, Hkv, D, page in LARGER:
+        for e4m3 in (False, True):
+            c = ta.Family(groups, Hq, Hkv, D, page, e4m3, seed=Hq + page)
+            c.check(*c.run())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 128, 16), (18, 1, 64, 32)])
+def test_infinite_values_in_a_common_beginning(Hq, Hkv, D, page, monkeypatch):
+    """Beginnings that end inside a tile of 128 keys, and with one: columns with an infinite value or a NaN
+    code come out so in the sequences that have it, and nowhere else."""
+    monkeypatch.setenv("MCS_TEST_SHARED_WORTH", "0")
+    tile = 128 // page
+    groups = [(2 * tile + 1, [3, 0, 200]), (3 * tile, [1, 40, 0]), (3 * tile - 1, [9, 8])]
+    for e4m3 in (False, True):
+        clean = ta.Family(groups, Hq, Hkv, D, page, e4m3, seed=7)
+        want, want_ls = clean.run()
+        c = ta.Family(groups, Hq, Hkv, D, page, e4m3, seed=7)
+        hit = torch.zeros(want.shape, dtype=torch.bool, device="cuda")
+        group = Hq // Hkv
+        for g, (t, h, col) in enumerate([((2 * tile + 1) * page - 1, 0, 5), (17, Hkv - 1, D - 1), ((3 * tile - 1) * page - 2, 0, 0)]):
+            b = c.starts[g]
+            c.v[int(c.table[b, t // page]), h, t % page, col] = 0x7F if e4m3 else [np.inf, -np.inf, np.nan][g]
+            hit[c.starts[g]:c.starts[g + 1], h * group:(h + 1) * group, col] = True
+        out, ls = c.run()
+        assert mcs.mcs_device_status() == 0
+        assert not torch.isfinite(out.float()[hit]).any()
+        assert torch.equal(out[~hit], want[~hit]) and torch.equal(ls, want_ls)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_read_once_of_random_shapes(seed, monkeypatch):
+    monkeypatch.setenv("MCS_TEST_SHARED_WORTH", "0")
+    r = np.random.default_rng(7000 + seed)
+    Hkv = int(r.choice([1, 2, 3, 4]))
+    Hq, D, page = Hkv * int(r.choice([1, 3, 4, 8, 9, 16, 17, 20, 33, 140])), int(r.choice([64, 128])), int(r.choice([16, 32, 64, 128]))
+    groups = [(int(int(r.choice([1, 30, 400])) * r.random() * 16 / page) + int(r.integers(0, 2)),
+               [int(200 ** r.random()) - 1 if r.random() > 0.1 else None for _ in range(int(r.integers(1, int(r.choice([2, 9, 40])))))])
+              for _ in range(int(r.integers(1, 5)))]
+    e4m3 = bool(seed // 2 % 2)
+    c = ta.Family(groups, Hq, Hkv, D, page, e4m3, seed=seed, q_stride=int(r.choice([0, (Hq + 2 * Hkv) * D])))
+    c.check(*c.run())
+    # groups of empty sequences may name more pages than a table row has, which is reported
+    assert mcs.mcs_device_status() == (6 if max(c.shared) > c.p.max_pages else 0)

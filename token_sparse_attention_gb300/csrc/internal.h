@@ -290,6 +290,7 @@ struct SharedPlanArgs {
   const int32_t* starts;     // [G + 1]
   const int32_t* shared;     // [G] pages
   unsigned long long row_bytes;  // of a token, keys and values of all heads
+  unsigned long long worth;      // bytes that reading beginnings once has to save
   int32_t* tail;             // [B] tokens behind the beginning; null: check only
   int32_t* skip;             // [B] pages of the beginning
   int32_t* group_of;         // [B]
@@ -305,8 +306,9 @@ cudaError_t launch_shared_plan(const SharedPlanArgs& a, cudaStream_t stream);
 // tokens x heads x 64 with 128-byte swizzle.
 bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int box_rows, bool bytes);
 bool make_query_map(CUtensorMap* m, const void* base, int T, int H, int D, long long stride, int heads, int tokens);
-// MCS_TEST_FAULT (see mcs_api.cu).
+// MCS_TEST_FAULT and MCS_TEST_SHARED_WORTH (see mcs_api.cu).
 int test_fault();
+unsigned long long shared_worth();
 
 // Pages that several sequences hold (see pages.cu).
 struct PagesArgs {

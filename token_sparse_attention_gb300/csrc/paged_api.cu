@@ -401,10 +401,11 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
   plan.lens = lens;
   plan.starts = group_start;
   plan.shared = shared_pages;
+  plan.worth = mcs::shared_worth();
   plan.row_bytes = static_cast<unsigned long long>(p->Hkv) * p->D * (p->kv == MCS_KV_E4M3 ? 2 : 4);
   // Where tables of this size cannot name beginnings worth sharing, arguments are checked and sequences read by
   // themselves, without the launches that find that out (4 beams behind 1008 tokens 21 -> 16 us).
-  const bool never = static_cast<double>(p->B - 1) * p->max_pages * p->page * plan.row_bytes < mcs::kSharedWorth;
+  const bool never = static_cast<double>(p->B - 1) * p->max_pages * p->page * plan.row_bytes < plan.worth;
   plan.tail = ints;
   plan.skip = ints + p->B;
   plan.group_of = ints + 2 * p->B;

@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Which sequences a common beginning serves.  One CTA: it is a few reads and writes per sequence.
 // Bounds that do not ascend from 0 to B leave every sequence by itself; a group of which fewer than
 // two sequences reach the beginning's end, too; and so does a batch in which reading the beginnings
-// once saves less than kSharedWorth bytes.  Without `tail` it only checks.
+// once saves less than `worth` bytes.  Without `tail` it only checks.
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlanArgs a) {
   __shared__ unsigned long long s_saved;
@@ -1102,7 +1102,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
   }
   if (!writes) return;
   __syncthreads();
-  const bool worth = s_saved >= kSharedWorth;
+  const bool worth = s_saved >= a.worth;
   for (int g = warp_id(); g < a.G; g += kPlanThreads / 32) {
     const int keys = a.keys[g];
     __syncwarp();
