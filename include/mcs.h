@@ -575,10 +575,12 @@ mcs_status mcs_paged_attn(const mcs_paged* p, int T, const void* q, const void* 
  * ascends from 0 to B; 1 <= groups <= B), and the first shared_pages[g] entries of
  * their table rows are the same pages, full ones, as mcs_paged_fork leaves them:
  * these are read once for the whole group, from the table row of its first
- * sequence that holds them, unless that saves the batch less than 128 MB of reads,
- * where every sequence is read by itself.  Same results as mcs_paged_decode, with the
- * weights of the common beginning rounded as in mcs_paged_attn.  Groups may have one
- * sequence, or nothing in common (0).  group_start that does not ascend so sets
+ * sequence that holds them, where that saves the batch enough: 200 MB of reads, and
+ * as many as the beginnings hold themselves up to 128 MB (over E4M3 with 128 / D
+ * times what they hold beyond).  Otherwise every sequence is read by itself.  Same
+ * results as mcs_paged_decode, with the weights of a beginning that is read once
+ * rounded as in mcs_paged_attn.  Groups may have one sequence, or nothing in
+ * common (0).  group_start that does not ascend so sets
  * MCS_ERR_BOUNDS in the device status and shares nothing; a sequence that is
  * neither empty nor as long as its group's beginning, or a negative or too large
  * shared_pages, sets it, too, and that sequence (group) is read by itself.

@@ -8,6 +8,7 @@ import torch
 
 from tests import test_gpu_paged as tp
 from tests import test_gpu_paged_attn as ta
+from tests import test_gpu_paged_sharing as ts
 from token_sparse_attention_gb300 import build as mcs_build
 from token_sparse_attention_gb300 import mcs
 
@@ -139,3 +140,33 @@ def test_read_once_of_random_shapes(seed, monkeypatch):
     c.check(*c.run())
     # groups of empty sequences may name more pages than a table row has, which is reported
     assert mcs.mcs_device_status() == (6 if max(c.shared) > c.p.max_pages else 0)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_batches_on_either_side_of_what_is_worth_it(e4m3):
+    """Beginnings that save just enough to be read once and just too little: both as a decode says, and the
+    bits are those of beginnings read once for the former alone."""
+    Hq, Hkv, D, page, es = 8, 8, 128, 128, 2 if e4m3 else 4
+    for n in (4, 12):
+        unit = page * Hkv * D * es  # bytes of a page
+        need = next(x for x in range(1, 10 ** 6) if (n - 1) * x * unit >= 200000000 + min(x * unit, 2 ** 27) +
+                    (e4m3 * max(0, x * unit - 2 ** 27)))
+        for pages in (need, need - 1):
+            c = ta.Family([(pages, [5] * (n - 1) + [140])], Hq, Hkv, D, page, e4m3, seed=n)
+            got = c.run()
+            assert mcs.mcs_device_status() == 0
+            c.check(*got)
+            with pytest.MonkeyPatch.context() as m:
+                m.setenv("MCS_TEST_SHARED_WORTH", "0")
+                once = c.run()
+            if pages == need:
+                assert torch.equal(got[0], once[0]) and torch.equal(got[1], once[1])
+            else:  # (joined by the same kernel as if something were shared, so not a decode's bits)
+                assert not torch.equal(got[1], once[1])
+
+
+@pytest.mark.parametrize("e4m3,Hq,Hkv,D,page,long", [(False, 8, 2, 128, 16, 0), (True, 4, 4, 64, 32, 0), (False, 16, 16, 128, 64, 1100),
+                                                     (True, 9, 1, 128, 16, 300)])
+def test_beams_together_with_their_beginnings_read_once(e4m3, Hq, Hkv, D, page, long, monkeypatch):
+    monkeypatch.setenv("MCS_TEST_SHARED_WORTH", "0")
+    ts.test_beams_of_two_requests_together(e4m3, Hq, Hkv, D, page, long)

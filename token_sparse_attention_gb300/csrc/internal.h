@@ -278,11 +278,18 @@ cudaError_t paged_attn_grid(int* grid);
 
 // Groups of sequences with a common beginning: what the attention over the beginnings and over the
 // tails take (see mcs_paged_decode_shared).
-// Bytes that reading common beginnings once has to save: the attention over them, which starts anew on every
-// SM, and the join take about 15 us more than one decode, which reads so much again from L2 in that time (4
-// sequences behind 8192 tokens of 8 heads, bf16, 101 MB: 31 us shared, 23 by themselves; 8 of them, 235 MB: 36
-// and 33; 32 behind 4096, 520 MB: 39 and 54).
-constexpr unsigned long long kSharedWorth = 128ull << 20;
+// Whether common beginnings are read once: the bytes that this saves are at least kSharedWorth and what the
+// beginnings hold themselves, as far as that fits L2 (beyond it, over E4M3: 128 / D times).  The attention over
+// them, which starts anew on every SM, and the join take 15 to 25 us more than a decode, which reads beginnings that
+// fit L2 again from there, at twice HBM's rate; E4M3's steps over them take as long whatever a tile holds, so that
+// beginnings of two sequences gain nothing.  us read once / by themselves (after the same check), between cold and
+// warm L2, 32 / 8 heads, D = 128; bf16: 16 sequences behind 3248 tokens (saves 200 MB, holds 13) 41 / 38, behind
+// 4880 (300, 20) 44 / 48; 4 behind 24416 (300, 100) 62 / 56, behind 48832 (600, 200) 81 / 118; 16 pairs behind 3904 (256,
+// 256) 90 / 73, behind 6096 (400, 400) 110 / 143.  E4M3: 96 behind 1024 (200, 2) 44 / 50; 4 behind 48832 (300, 100) 78
+// / 73, behind 97664 (600, 200) 110 / 138; 16 pairs behind 12208 (400, 400) 157 / 152, behind 48832 (1600, 1600) 496 / 487.
+// Of 307 measured batches the rule reads 12 once that were 4 us or more faster by themselves (at most 14 of 78), and 3
+// by themselves that were more than 12 us faster read once (at most 18 of 74).
+constexpr unsigned long long kSharedWorth = 200000000ull, kSharedNear = 128ull << 20;
 
 struct SharedPlanArgs {
   int B, G, page, max_pages;
@@ -290,7 +297,9 @@ struct SharedPlanArgs {
   const int32_t* starts;     // [G + 1]
   const int32_t* shared;     // [G] pages
   unsigned long long row_bytes;  // of a token, keys and values of all heads
-  unsigned long long worth;      // bytes that reading beginnings once has to save
+  // bytes that reading beginnings once has to save: `worth`, their own up to `near`, and of the others so many times as much
+  unsigned long long worth, near;
+  int beyond;
   int32_t* tail;             // [B] tokens behind the beginning; null: check only
   int32_t* skip;             // [B] pages of the beginning
   int32_t* group_of;         // [B]
@@ -308,7 +317,7 @@ bool make_rows_map(CUtensorMap* m, const void* base, long long rows, int D, int 
 bool make_query_map(CUtensorMap* m, const void* base, int T, int H, int D, long long stride, int heads, int tokens);
 // MCS_TEST_FAULT and MCS_TEST_SHARED_WORTH (see mcs_api.cu).
 int test_fault();
-unsigned long long shared_worth();
+bool shared_worth(unsigned long long* worth);
 
 // Pages that several sequences hold (see pages.cu).
 struct PagesArgs {

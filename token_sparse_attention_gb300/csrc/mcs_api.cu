@@ -267,12 +267,14 @@ bool make_query_map(CUtensorMap* m, const void* base, int T, int H, int D, long 
 
 int test_fault() { return fault_from_env(); }
 
-// MCS_TEST_SHARED_WORTH=bytes (test-only): from how many bytes saved on beginnings are read once, so that
+// MCS_TEST_SHARED_WORTH=bytes (test-only): from how many bytes saved on beginnings are read once, whatever they hold, so that
 // small batches take the path of large ones, or large ones that of small ones.  Read at every call; unset in
 // normal use.
-unsigned long long shared_worth() {
+bool shared_worth(unsigned long long* worth) {
   const char* f = getenv("MCS_TEST_SHARED_WORTH");
-  return f != nullptr && *f != '\0' ? strtoull(f, nullptr, 10) : kSharedWorth;
+  if (f == nullptr || *f == '\0') return false;
+  *worth = strtoull(f, nullptr, 10);
+  return true;
 }
 }  // namespace mcs
 

@@ -401,7 +401,10 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
   plan.lens = lens;
   plan.starts = group_start;
   plan.shared = shared_pages;
-  plan.worth = mcs::shared_worth();
+  plan.worth = mcs::kSharedWorth;
+  plan.near = mcs::kSharedNear;
+  plan.beyond = p->kv == MCS_KV_E4M3 ? 128 / p->D : 0;
+  if (mcs::shared_worth(&plan.worth)) plan.near = 0, plan.beyond = 0;
   plan.row_bytes = static_cast<unsigned long long>(p->Hkv) * p->D * (p->kv == MCS_KV_E4M3 ? 2 : 4);
   // Where tables of this size cannot name beginnings worth sharing, arguments are checked and sequences read by
   // themselves, without the launches that find that out (4 beams behind 1008 tokens 21 -> 16 us).

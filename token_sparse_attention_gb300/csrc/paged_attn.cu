@@ -1053,12 +1053,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Which sequences a common beginning serves.  One CTA: it is a few reads and writes per sequence.
 // Bounds that do not ascend from 0 to B leave every sequence by itself; a group of which fewer than
 // two sequences reach the beginning's end, too; and so does a batch in which reading the beginnings
-// once saves less than `worth` bytes.  Without `tail` it only checks.
+// once saves too few bytes (see SharedPlanArgs).  Without `tail` it only checks.
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlanArgs a) {
-  __shared__ unsigned long long s_saved;
+  __shared__ unsigned long long s_saved, s_once;
   const int tid = threadIdx.x, lane = lane_id();
-  if (tid == 0) s_saved = 0;
+  if (tid == 0) s_saved = s_once = 0;
   pdl_begin();
   const long long room = static_cast<long long>(a.max_pages) * a.page;
   bool bad = tid == 0 && (a.starts[0] != 0 || a.starts[a.G] != a.B);
@@ -1097,12 +1097,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
       const bool use = live > 1 && keys > 0;
       a.keys[g] = use ? keys : 0;
       a.leader[g] = use ? leader : 0;
-      if (use) atomicAdd(&s_saved, (live - 1ull) * keys * a.row_bytes);
+      if (use) {
+        atomicAdd(&s_saved, (live - 1ull) * keys * a.row_bytes);
+        atomicAdd(&s_once, keys * a.row_bytes);
+      }
     }
   }
   if (!writes) return;
   __syncthreads();
-  const bool worth = s_saved >= a.worth;
+  const unsigned long long close = min(s_once, a.near);
+  const bool worth = s_saved >= a.worth + close + a.beyond * (s_once - close);
   for (int g = warp_id(); g < a.G; g += kPlanThreads / 32) {
     const int keys = a.keys[g];
     __syncwarp();
