@@ -556,9 +556,10 @@ mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void
  * length is negative or above max_pages * page, sets MCS_ERR_BOUNDS and its rows
  * stay as they were.  Values behind a token, infinite or NaN, do not reach it;
  * an infinite or NaN value that it attends to makes its column NaN or infinite.
- * E4M3: q is converted to f16 as in mcs_paged_decode.  The weights are rounded to
- * bf16 (bf16 cache) or f16 (E4M3) for the product with v; scores, maxima and the sums
- * that normalise it are fp32.  Results do not depend on timing.
+ * E4M3: q is converted to f16 as in mcs_paged_decode.  The weights are rounded once
+ * for the product with v, to bf16 (bf16 cache: off by at most 2^-8 of a weight) or
+ * f16 (E4M3: 2^-11, and 2^-37 of the row's largest); scores, maxima and the sums that
+ * normalise it are fp32.  Results do not depend on timing.
  * ws: at least mcs_paged_attn_workspace(p) bytes, as for mcs_paged_decode.
  * 0 <= T <= 2^30, T * Hq below 2^31.
  */

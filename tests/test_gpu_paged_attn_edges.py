@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged_oracle as po
 from tests import test_gpu_paged as tp
 from tests import test_gpu_paged_attn as ta
 from tests import test_gpu_paged_sharing as ts
@@ -170,3 +171,78 @@ def test_batches_on_either_side_of_what_is_worth_it(e4m3):
 def test_beams_together_with_their_beginnings_read_once(e4m3, Hq, Hkv, D, page, long, monkeypatch):
     monkeypatch.setenv("MCS_TEST_SHARED_WORTH", "0")
     ts.test_beams_of_two_requests_together(e4m3, Hq, Hkv, D, page, long)
+
+
+# ------------------------------------------------------------------ one key that outweighs all others
+
+def _with_a_sink(c, rows, seed):
+    """Scores of log2 weight p in front of all others' 0 for the first key, p from 20 to 34 over the rows; the
+    first value is zero in even columns, small in odd ones, the others are about 1."""
+    r = np.random.default_rng(seed)
+    pid = int(c.table[0, 0])
+    value = torch.from_numpy(r.uniform(60, 120, c.v.shape[-1])).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    hole = c.k == 0x7F
+    c.k.masked_fill_(~hole, 0)
+    c.v.copy_(torch.where(c.v == 0x7F, c.v, value))
+    c.k[pid, :, 0, 0] = 0x7E  # 448
+    c.v[pid, :, 0, 0::2] = 0
+    c.v[pid, :, 0, 1::2] = 0x58  # 16
+    c.q.zero_()
+    c.q[..., 0] = torch.linspace(20, 34, rows).to(torch.bfloat16).cuda().view(c.q.shape[0], c.q.shape[1])
+
+
+SINK_SCALE = float(np.float32(np.log(2) / (448 * tp.KS)))
+
+
+def _check_sink(out, ls, q, c, oracle):
+    """Rounding to bf16; scores and exponentials as in test_gpu_paged_attn; a weight as f16: 2^-11 of it, and where
+    it is small 2^-37 of the row's largest: the reference lies 2^12 below the maximum when it is set, f16
+    rounds to multiples of 2^-24, and what the maximum grows by makes the sum that divides larger."""
+    k, v = (_f64(x) * s for x, s in zip((c.k, c.v), c.scales))
+    want, lse, absv, size = oracle(_f64(q), k, v)
+    n, D = max(c.lens), c.D
+    tol, tol_lse = ta.tolerance(want, lse, absv, size, D, n, True, weight=2.0 ** -11)
+    tol = tol + 2.0 ** -37 * n * np.nanmax(np.abs(v))
+    assert not np.isnan(want).any()
+    off = np.abs(_f64(out) - want)
+    assert (off <= tol).all(), (off / tol).max()
+    assert (np.abs(_f64(ls) - lse) <= tol_lse).all()
+    # the many others are what even columns consist of
+    assert (want[..., 0::2] > 2 * tol[..., 0::2]).all()
+
+
+def _params(c, B, kv=1):
+    return mcs.paged(B, c.p.Hq, c.p.Hkv, c.D, c.page, c.p.num_pages, c.p.max_pages, kv=kv, scale=c.p.scale,
+                     k_scale=c.p.k_scale, v_scale=c.p.v_scale)
+
+
+@pytest.mark.parametrize("D,new,tokens,times", [(128, 3, 75600, 1), (64, 40, 75600, 1), (128, 17, 300000, 1),
+                                                (128, 2, 75600, 170), (64, 3, 20000, 400)])
+def test_many_small_weights_behind_a_large_one(D, new, tokens, times):
+    """`times`: the same sequence so many times over, so that a block reads most of it for its rows."""
+    c = ta.Step([tokens], [new], 8, 1, D, 128, True, behind=0, scale=SINK_SCALE)
+    _with_a_sink(c, new * 8, D)
+    q, table = c.q, c.table
+    c.q, c.dtable, c.dlens = c.q.repeat(times, 1, 1), _i32(np.repeat(table, times, 0)), _i32([tokens] * times)
+    c.p, c.dcu = _params(c, times), _i32(np.arange(times + 1) * new)
+    out, ls = (x.view((times, new) + x.shape[1:]) for x in c.attn())
+    assert mcs.mcs_device_status() == 0
+    assert times == 1 or ls.shape == (times, new, 8)
+    _check_sink(out, ls, q, c, lambda q, k, v: po.attn(q, k, v, table, c.lens, c.cu, c.scale))
+
+
+@pytest.mark.parametrize("Hq,D,tokens,times", [(8, 128, 75648, 1), (20, 64, 75648, 1), (4, 128, 299904, 1),
+                                               (8, 128, 75648, 160), (20, 64, 30080, 200)])
+def test_many_small_weights_in_a_common_beginning(Hq, D, tokens, times, monkeypatch):
+    """`times`: so many groups of two sequences behind the same pages."""
+    for worth in ("0", str(1 << 60)):
+        monkeypatch.setenv("MCS_TEST_SHARED_WORTH", worth)
+        c = ta.Family([(tokens // 128, [1, 40])], Hq, 1, D, 128, True, scale=SINK_SCALE)
+        _with_a_sink(c, 2 * Hq, D)
+        q, table, lens = c.q, c.table, c.lens
+        c.q, c.dtable, c.dlens = q.repeat(times, 1, 1), _i32(np.tile(table, (times, 1))), _i32(lens * times)
+        c.p, c.dstarts, c.dshared = _params(c, 2 * times), _i32(np.arange(times + 1) * 2), _i32([tokens // 128] * times)
+        c.ws = mcs.empty_workspace(mcs.mcs_paged_decode_shared_workspace(c.p))
+        out, ls = (x[:-1].view((times, 2) + x.shape[1:]) for x in c.run())
+        assert mcs.mcs_device_status() == 0
+        _check_sink(out, ls, q, c, lambda q, k, v: po.decode(q, k, v, table, lens, c.scale))

@@ -72,9 +72,17 @@ constexpr int kSlabs = BN / kSlab;
 constexpr int kWindow = 32 / kSlabs;  // tiles whose pages a warp looks up at once
 constexpr int kBadSlots = 16;         // steps ahead of the softmax that loads may be: ring depth
 
-// Rescaled only when a row's maximum grows by more than 2^16 (f16 weights: 2^15 < 65504).
+// Weights are 2^(x - r), x the score in powers of two and r the row's reference: its maximum when that was
+// last set, for f16 weights 2^12 below it, since f16 keeps nothing below 2^-25: weights down to 2^-37 of the
+// maximum then count, as in the decode, where keys of next to no weight each make up a visible part of the
+// output by their number.  (Scores so large that a float cannot tell 12 apart keep the maximum.)
+// The reference moves only when the maximum has come to lie 2^16 above it (f16 weights: 2^15 < 65504).
 template <bool E4M3>
 constexpr float kThreshold = E4M3 ? 15.f : 16.f;
+template <bool E4M3>
+__device__ __forceinline__ float reference_of(float maximum) {
+  return E4M3 && fabsf(maximum) < 0x1p24f ? maximum - 12.f : maximum;
+}
 
 template <int D, bool E4M3>
 struct Layout {
@@ -878,12 +886,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tS + 32, su + 32);
         tmem_ld_wait();
         const float m_new = fmaxf(max64(s), mx_hi) * sl2;
-        // The reference maximum moves only when the tile's exceeds it by more than the
+        // The reference moves only when the tile's maximum exceeds it by more than the
         // threshold; TMEM loads and stores are the whole warp's, so all rows enter when one does.
         const bool need = m_new > m_run + kThreshold<E4M3>;  // (the first maximum of a row, too)
         if (__any_sync(0xffffffffu, need)) {
+          const float ref = reference_of<E4M3>(m_new);
           if (j > 0) {
-            const float f = need ? ex2(m_run - m_new) : 1.f;
+            const float f = need ? ex2(m_run - ref) : 1.f;
             l_run *= f;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -895,11 +904,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(tO + c * 16, o);
             }
           }
-          if (need) m_run = m_new;
+          if (need) m_run = ref;
         }
         // p = 2^(s c - m), rounded to bf16 or f16 for the product and summed in fp32 as they were, for lse
-        // and output: a weight's rounding then counts once in the output, by at most 2^-8 of the weight
-        // times its value.  (A second sum of the rounded weights makes equal values come out unrounded,
+        // and output: a weight's rounding then counts once in the output, by at most 2^-8 (f16: 2^-11, and
+        // 2^-37 of the largest weight) of the weight times its value.  (A second sum of the rounded weights makes equal values come out unrounded,
         // but no bound smaller, and cost 4 to 9 % of a prompt's time.)
         const float m_ref = m_run == -INFINITY ? 0.f : m_run;
         const uint64_t c2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_ref, -m_ref);
