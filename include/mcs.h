@@ -553,8 +553,8 @@ mcs_status mcs_paged_decode_sparse(const mcs_paged* p, const void* q, const void
  * fp32 (natural log, nullable).  Rows that are no sequence's stay as they were.  A
  * token all of whose pages are bad gets zeros, and -inf as its lse.  A sequence
  * whose rows do not lie in [0, T), or with more new tokens than lens[b], or whose
- * length is negative or above max_pages * page, sets MCS_ERR_BOUNDS and its rows
- * stay as they were.  Values behind a token, infinite or NaN, do not reach it;
+ * length is negative or above max_pages * page (whether or not it has new tokens),
+ * sets MCS_ERR_BOUNDS and its rows stay as they were.  T = 0 does nothing.  Values behind a token, infinite or NaN, do not reach it;
  * an infinite or NaN value that it attends to makes its column NaN or infinite.
  * E4M3: q is converted to f16 as in mcs_paged_decode.  The weights are rounded once
  * for the product with v, to bf16 (bf16 cache: off by at most 2^-8 of a weight) or

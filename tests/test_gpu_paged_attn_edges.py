@@ -246,3 +246,20 @@ def test_many_small_weights_in_a_common_beginning(Hq, D, tokens, times, monkeypa
         out, ls = (x[:-1].view((times, 2) + x.shape[1:]) for x in c.run())
         assert mcs.mcs_device_status() == 0
         _check_sink(out, ls, q, c, lambda q, k, v: po.decode(q, k, v, table, lens, c.scale))
+
+
+# ------------------------------------------------------------------ what cannot be
+
+@pytest.mark.parametrize("length", [-1, -2 ** 31, "too long", 2 ** 31 - 1])
+def test_attn_reports_lengths_of_sequences_without_new_tokens(length):
+    c = ta.Step([300, 90, 70, 40], [10, 0, 9, 0], 4, 2, 64, 16, seed=6)
+    for b in (1, 3):
+        lens = list(c.lens)
+        lens[b] = c.p.max_pages * 16 + 1 if length == "too long" else length
+        c.dlens = _i32(lens)
+        got = c.attn()
+        assert mcs.mcs_device_status() == 6
+        c.check_attn(*got)
+    c.dlens = _i32([300, 0, 70, c.p.max_pages * 16])
+    c.check_attn(*c.attn())
+    assert mcs.mcs_device_status() == 0

@@ -59,10 +59,8 @@ __device__ __forceinline__ bool load_seq(const PagedAttnArgs& a, int g, Seq& s, 
   s.keys = a.keys[g];
   s.cu = lo;
   s.n = 0;
-  if (hi == lo) return false;
-  if (lo < 0 || hi < lo || hi > a.T || s.keys < 0 ||
-      static_cast<long long>(s.keys) > static_cast<long long>(a.max_pages) * a.page ||
-      (a.causal && hi - lo > s.keys)) {
+  if (s.keys < 0 || static_cast<long long>(s.keys) > static_cast<long long>(a.max_pages) * a.page ||
+      (hi != lo && (lo < 0 || hi < lo || hi > a.T || (a.causal && hi - lo > s.keys)))) {
     if (report) atomicOr(a.status, DEV_BOUNDS);
     return false;
   }
