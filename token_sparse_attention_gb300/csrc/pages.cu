@@ -403,11 +403,12 @@ __global__ void __launch_bounds__(32 * kCopyWarps) paged_page_copy_kernel(const 
     next_which += step_which;
     if (next_which >= per) next_which -= per, ++at;
     from = entry(0), to = entry(1), rows = entry(2);
-    if (src_page < 0 || src_page == dst_page) continue;
+    if (src_page < 0) continue;
     if (src_page >= a.num_pages || dst_page < 0 || dst_page >= a.num_pages || n < 0 || n > a.page) {
       if (lane == 0) atomicOr(a.status, DEV_BOUNDS);
       continue;
     }
+    if (src_page == dst_page) continue;
     const int words = n * a.row_words;
     const size_t pitch = static_cast<size_t>(a.page) * a.row_words;
     uint4* base = static_cast<uint4*>(which >= a.Hkv ? a.v : a.k);
