@@ -618,7 +618,8 @@ mcs_status mcs_paged_decode_shared(const mcs_paged* p, int groups, const void* q
  * never the same.  Apart from the outputs that may be inputs (extra_out: extra,
  * free_out: free_pages, head_out: free_head) no output overlaps an input.  A
  * request that cannot be met (parents outside [-1, B), too few free pages, a length or
- * a page outside the cache, holders below zero, a free list without room) sets
+ * a page outside the cache, a count in extra below zero, more sequences that let go
+ * of a page than hold it, a free list without room) sets
  * MCS_ERR_BOUNDS in the device status and takes nothing: all rows of `moves` are
  * (-1, -1, 0) and no other output is written.
  * Copies of a call belong in front of the next mcs_paged_write.

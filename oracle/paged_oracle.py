@@ -141,7 +141,7 @@ def fork(parents, lens, table, extra, free, head, page, num_pages):
     for a request that cannot be met.  Walks over the old sequences' pages with a dictionary of
     holders."""
     B, P = table.shape
-    if any(not 0 <= n <= P * page for n in lens) or any(not -1 <= p < B for p in parents):
+    if any(not 0 <= n <= P * page for n in lens) or any(not -1 <= p < B for p in parents) or min(extra) < 0:
         return None
     holders = {}
     for b in range(B):

@@ -32,3 +32,20 @@ def test_copy_of_a_page_to_itself_is_checked_like_any_other():
         mcs.mcs_paged_copy(p, _i32([row, [-1, -1, 0]]), k, v, mean)
         assert mcs.mcs_device_status() == status, row
         assert all(torch.equal(x, y) for x, y in zip((k, v, mean), before))
+
+
+@pytest.mark.parametrize("count", [-1, -2, -2 ** 31])
+@pytest.mark.parametrize("what", ["gains", "keeps", "loses", "free"])
+def test_fork_refuses_counts_below_zero(what, count):
+    """Of a page that gets more holders, one that keeps its holder, one that loses it, a free one."""
+    s = tg.State(3, 2, 100, 90, 16, 9, seed=5, empty=0)
+    b = next(b for b in range(6) if s.lens[b] >= 32)
+    parents = {"gains": [b, b, b], "keeps": list(range(6)), "loses": [x for x in range(6) if x != b], "free": list(range(6))}[what]
+    s.check_fork(parents, s.fork(parents), False)
+    s.extra[s.free[-1] if what == "free" else s.table[b, 0]] = count
+    for in_place in (False, True):
+        lens, table, extra, free, head, moves = s.fork(parents, in_place)
+        assert mcs.mcs_device_status() == 6
+        assert (lens == -77).all() and (table == -77).all() and (moves == [-1, -1, 0]).all()
+        assert (extra == (s.extra if in_place else -77)).all() and (free == (s.free if in_place else -77)).all()
+        assert head.tolist() == [s.head if in_place else -77]

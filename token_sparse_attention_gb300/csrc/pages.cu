@@ -213,8 +213,8 @@ __global__ void __cluster_dims__(kCluster) __launch_bounds__(kThreads) paged_for
   const int p0 = min(a.num_pages, part * static_cast<int>(blockIdx.x)), p1 = min(a.num_pages, p0 + part);
   int mine = 0;
   for (int p = p0 + tid; p < p1; p += kThreads) {
-    const int d = __ldcg(change + p), holders = a.extra[p] + 1 + d;
-    bad = bad || (d < 0 && holders < 0);
+    const int d = __ldcg(change + p), extra = a.extra[p], holders = extra + 1 + d;
+    bad = bad || extra < 0 || (d < 0 && holders < 0);
     mine += d < 0 && holders == 0;
   }
   bad = __syncthreads_or(bad);
