@@ -14,9 +14,11 @@ def test_counts_below_zero_are_refused_wherever_they_stand(page, parents):
     for head in (0, 3):  # without room in front of the free list, and with it
         free = np.array([9] * head + [3, 4, 5])
         extra[page] = int(page == 0)
-        # a page that is freed finds no place in front of a list that begins at 0
-        ended = not {0, 1} <= set(parents)
-        assert (po.fork(parents, *args, extra, free, head, 16, 6) is None) == (ended and head == 0)
+        # an ended sequence frees its last page, both free the common one; a second child takes a page
+        live = [x for x in parents if x >= 0]
+        ended = 2 - len(set(live))
+        room = head + len(live) - len(set(live)) - ended - (ended == 2)
+        assert (po.fork(parents, *args, extra, free, head, 16, 6) is None) == (room < 0)
         for n in (-1, -5):
             extra[page] = n
             assert po.fork(parents, *args, extra, free, head, 16, 6) is None
