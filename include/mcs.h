@@ -641,8 +641,15 @@ mcs_status mcs_paged_fork(const mcs_paged* p, int n, const int32_t* parents, con
  * [B, max_pages] has the new numbers (entries past a sequence's last page as in
  * block_table), extra_out the holders of the pages where they are now,
  * and free_out [n_free] from head_out[0] on all free pages, ascending.
- * table_out may be block_table and extra_out may be extra.  n_free smaller than the
- * number of free pages, or a length or a page outside the cache, sets
+ * table_out may be block_table and extra_out may be extra.
+ * With most = 0 nothing moves and the free list is made anew from lens and
+ * block_table.  So tokens are taken back (proposed ones that were not accepted): lower
+ * lens, and call this with most = 0 and all sequences of the cache before the next
+ * mcs_paged_plan or mcs_paged_fork; without it, pages that no length reaches any more
+ * stay out of the free list.  A sequence gives back only what it alone holds, tokens
+ * it got after its last fork (extra is not lowered), and a page that keeps some of
+ * its tokens has their mean again once a token is written to it.
+ * n_free smaller than the number of free pages, or a length or a page outside the cache, sets
  * MCS_ERR_BOUNDS and changes nothing, as above.  0 <= most.
  */
 size_t mcs_paged_compact_workspace(const mcs_paged* p);
