@@ -34,16 +34,16 @@
 // become zeros, too, with the first such key of each column kept; a row that sees that key
 // gets NaN in the column.  One or two tiles per segment are concerned.
 //
-// Measured, and what bounds it:
-//   a prompt of 16384 tokens, 32 / 8 heads, D = 128: bf16 1363 us, 1613 TFLOP/s, 82 % of a
+// Measured (graph replays; two figures: different GPUs), and what bounds it:
+//   a prompt of 16384 tokens, 32 / 8 heads, D = 128: bf16 1372 to 1386 us, 1600 TFLOP/s, 81 % of a
 //     matrix product's rate; with the softmax left out it would be 94 %, so the chains' softmax bounds
 //     it (two warps per scheduler: maxima, exponentials, sums, rounding, and TMEM on both sides).
-//     E4M3 1661 us: the conversions take issue slots from it
-//   8192 tokens, 40 heads: bf16 515 us, E4M3 565, 67 and 62 %: shorter segments, of which each change takes
-//     about 4 us: last softmax, product, epilogue, first scores and softmax one after another
-//   1024 tokens behind 73552, 40 / 8 heads: bf16 1065 us, E4M3 1076, 74 and 73 %, as the first
-//   32 x 5 tokens behind 8000, 32 / 8 heads, bf16 (1.05 GB): 177 us, 5.9 TB/s, 87 % of a copy
-//   the same in E4M3 (0.52 GB): 165 us, 3.2 TB/s.  A step of an odd unit is a chain of waits (tile there,
+//     E4M3 1696 to 1844 us: the conversions take issue slots from it
+//   8192 tokens, 40 heads: bf16 512 us, E4M3 577 to 655, 67 and 54 to 61 %: shorter segments, of which each change
+//     takes about 4 us: last softmax, product, epilogue, first scores and softmax one after another
+//   1024 tokens behind 73552, 40 / 8 heads: bf16 1050 to 1102 us, E4M3 1106 to 1175, 72 to 75 and 67 to 71 %, as the first
+//   32 x 5 tokens behind 8000, 32 / 8 heads, bf16 (1.05 GB): 174 to 178 us, 5.9 TB/s, 87 % of a copy
+//   the same in E4M3 (0.52 GB): 164 to 173 us, 3.2 TB/s.  A step of an odd unit is a chain of waits (tile there,
 //     stage free, converted, scores, weights) of 1.4 us; without the conversions' work it takes 1.1.  Two more
 //     tiles ahead, one more f16 stage, and scores a step ahead in S's other half changed nothing each
 //   77 tokens, 16 heads, D = 64: 14.6 us, latency: the first use of each role's code and data
