@@ -819,7 +819,8 @@ def _moves_of(moves) -> int:
 
 def mcs_paged_compact(p: Paged, lens, block_table, extra, table_out, extra_out, free_out, head_out,
                       moves, ws, stream=None):
-    """moves [most, 3]: the first dimension says how many pages are moved at most."""
+    """moves [most, 3]: the first dimension says how many pages are moved at most; none: the free list is
+    made anew, as after tokens that were taken back by lowering lens."""
     most, n_free = _moves_of(moves), _count(free_out.numel(), "free_out")
     dev, B, pages = _device(stream), p.B, (p.num_pages,)
     table = (B, p.max_pages)
